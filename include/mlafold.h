@@ -335,10 +335,102 @@ int32_t mla_folded_decode_noalloc(const mla_shape *shape, const void *q, const v
                                   int32_t *work, int32_t list_len, void *out, float *lse,
                                   int32_t *status, mla_stream_t stream);
 
-/* Bits the decode kernel ORs into *status. */
+/* ---------------------------------------------------------------------------
+ * Around the decode: what fills its cache and what makes its queries. The pages
+ * take the cache and the absorbed FP8 queries as given; these calls are
+ * additions of this library.
+ *
+ * Rope table: `rope` [rope_rows, 64] FP32, device: row p holds the cosines of
+ * the 32 plane angles of position p, then their sines (whatever scaling of the
+ * angles the model uses is in the table). Planes: interleaved = 1 pairs rope
+ * dims (2i, 2i + 1), interleaved = 0 pairs (i, i + 32); plane (a, b) becomes
+ * (a cos - b sin, b cos + a sin).
+ * E4M3 rounding: to nearest even from FP32, magnitudes above 448 to 448, NaN
+ * to the NaN code. */
+
+/* Shape of mla_kv_append. All fields are host values. */
+typedef struct {
+  int32_t R;            /* requests, 1 .. 2^20                                          */
+  int32_t tokens;       /* rows of kv_new, >= 0 (0 launches nothing)                    */
+  int32_t page_size;    /* tokens per cache page; must be 64                            */
+  int32_t max_pages;    /* entries per block_table row (row pitch), 1 .. 2^25 - 1       */
+  int32_t num_pages;    /* pages in the cache, 1 .. 2^25 - 1                            */
+  int32_t rope_rows;    /* rows of the rope table, >= 1                                 */
+  int32_t interleaved;  /* 1 or 0: how the rope dims pair up (above)                    */
+  int64_t row_stride;   /* elements between rows of kv_new, >= 576, a multiple of 8     */
+} mla_append_shape;
+
+/* New tokens into the paged latent cache: RMS norm of the 512 latent dims,
+ * rotation of the 64 rope dims, E4M3 codes through the block table:
+ *   y = (x[0:512] * rsqrt(mean(x[0:512]^2) + norm_eps) * norm_weight,
+ *        rotate(x[512:576], rope[p]))
+ *   kv[block_table[r][j / 64]][j % 64] = e4m3(y / kv_scale)
+ * for token i of request r, j = starts[r] + i, p = rope_starts[r] + i.
+ *   kv_new       [tokens, 576] BF16 rows of row_stride elements, device,
+ *                16-byte aligned: latent, then rope dims.
+ *   norm_weight  [512] BF16, device, 16-byte aligned; NULL: no norm.
+ *   norm_eps     finite, >= 0.
+ *   rope         the rope table, device.
+ *   cu_tokens    [R + 1] int32, device: request r's rows are cu_tokens[r] ..
+ *                cu_tokens[r + 1] - 1 (ascending from 0; rows from
+ *                cu_tokens[R] on belong to no request and are skipped).
+ *                NULL: tokens / R rows for each request, in order.
+ *   starts       [R] int32, device: the request's cached tokens before the
+ *                call; negative: a padding request, its rows are skipped.
+ *   rope_starts  [R] int32, device: the position of the request's first new
+ *                token (e.g. starts + a shared prefix's length); NULL: starts.
+ *   block_table  [R, max_pages] int32, device; read at the pages written.
+ *   kv_scale     finite, > 0, with a finite reciprocal.
+ *   kv           [num_pages, 64, 576] E4M3, device, 16-byte aligned; only the
+ *                new tokens' rows are written.
+ *   status       optional int32 device word: MLA_FAULT_PAGE_RANGE (a token past
+ *                the block-table row or on a page outside the cache),
+ *                MLA_FAULT_ROPE_RANGE (a position outside the table); such
+ *                tokens are skipped.
+ * Two tokens of one call must not have the same cache row: its content is then
+ * unspecified. FP32 from load to the one rounding. */
+int32_t mla_kv_append(const mla_append_shape *shape, const void *kv_new, const void *norm_weight,
+                      float norm_eps, const float *rope, const int32_t *cu_tokens,
+                      const int32_t *starts, const int32_t *rope_starts,
+                      const int32_t *block_table, float kv_scale, void *kv, int32_t *status,
+                      mla_stream_t stream);
+
+/* Shape of mla_query_absorb. All fields are host values. */
+typedef struct {
+  int32_t R;             /* requests, >= 1                                               */
+  int32_t k;             /* query tokens per request, >= 1; R*k <= 2^24                  */
+  int32_t H;             /* heads, 1 .. 2^16; ceil(R*k / 128) * H <= 2^24                */
+  int32_t rope_rows;     /* rows of the rope table, >= 1                                 */
+  int32_t interleaved;   /* 1 or 0: how the rope dims pair up (above)                    */
+  int64_t token_stride;  /* elements between tokens of q, >= 192, a multiple of 8        */
+  int64_t head_stride;   /* elements between heads of q, >= 192, a multiple of 8         */
+} mla_query_shape;
+
+/* Absorbed decode queries: the nope part times W_UK, the rope part rotated,
+ * E4M3 codes in the layout the decode reads:
+ *   out[t, h] = e4m3((q[t, h, 0:128] . W_UK[h], rotate(q[t, h, 128:192], rope[p])) / q_scale)
+ * for token t = r*k + i at position p = rope_starts[r] + i.
+ *   q            [R*k, H, 192] BF16 with the shape's strides, device, 16-byte
+ *                aligned: 128 nope dims, then 64 rope dims.
+ *   w_uk         [H, 128, 512] BF16, device, 16-byte aligned, latent-contiguous.
+ *                May be read before the preceding call of this library on the
+ *                stream has finished: none of them writes it.
+ *   rope         the rope table, device, 16-byte aligned.
+ *   rope_starts  [R] int32, device; negative: a padding request (rope dims 0).
+ *   q_scale      finite, > 0, with a finite reciprocal.
+ *   out          [R*k, H, 576] E4M3, device, 16-byte aligned, written.
+ *   status       optional int32 device word: MLA_FAULT_ROPE_RANGE (a position
+ *                past the table; its rope dims are 0), MLA_FAULT_WAIT_TIMEOUT.
+ * BF16 products, FP32 accumulation, one rounding. */
+int32_t mla_query_absorb(const mla_query_shape *shape, const void *q, const void *w_uk,
+                         const float *rope, const int32_t *rope_starts, float q_scale, void *out,
+                         int32_t *status, mla_stream_t stream);
+
+/* Bits the kernels OR into *status. */
 #define MLA_FAULT_WAIT_TIMEOUT 0x1 /* a pipeline wait gave up; the CTA stopped early */
 #define MLA_FAULT_PAGE_RANGE 0x2   /* a block-table entry was outside [0, num_pages) */
 #define MLA_FAULT_WORK_ITEM 0x4    /* a work item named a request or split out of range */
+#define MLA_FAULT_ROPE_RANGE 0x8   /* a token's position was outside the rope table */
 
 #ifdef __cplusplus
 }

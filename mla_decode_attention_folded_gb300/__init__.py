@@ -15,6 +15,11 @@ balanced-MLA page, ``BalancedMla.require`` / ``plan`` / ``decode``):
 * ``.decode(q, kv, block_table, seq_lens, bmm1_scale, bmm2_scale)`` runs the
   split-KV decode and the LSE reduction: BF16 ``out [R, k*H, 512]`` and the
   base-2 ``lse [R, k*H]``, in the stock token-major-then-head order.
+
+Around the decode (additions of this library): ``kv_append(...)`` writes new
+tokens into the paged cache (RMS norm, rotation, E4M3), ``query_absorb(...)``
+makes the decode's queries (W_UK, rotation, E4M3), ``rope_table(rows)`` makes the
+table of angles both read.
 """
 from __future__ import annotations
 
@@ -23,15 +28,17 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import (FAULT_PAGE_RANGE, FAULT_WAIT_TIMEOUT, FAULT_WORK_ITEM, MlaError, MlaShape,
-                   POLICY_BALANCED, POLICY_UNIFORM)
+from ._lib import (AppendShape, FAULT_PAGE_RANGE, FAULT_ROPE_RANGE, FAULT_WAIT_TIMEOUT,
+                   FAULT_WORK_ITEM, MlaError, MlaShape, POLICY_BALANCED, POLICY_UNIFORM,
+                   QueryShape)
 
 __all__ = ["MlaShape", "MlaError", "POLICY_BALANCED", "POLICY_UNIFORM", "make_shape",
            "plan_list_len", "workspace_bytes", "plan_splits", "folded_decode",
            "split_combine", "uv_combine", "lse_merge", "folded_decode_noalloc",
            "folded_decode_wait_test", "tier_plan", "row_copy", "balanced_tiers", "TIERS", "MOVE",
            "FoldedMla", "TieredMla", "fold_factor", "FAULT_WAIT_TIMEOUT", "FAULT_PAGE_RANGE",
-           "FAULT_WORK_ITEM", "library_path"]
+           "FAULT_WORK_ITEM", "FAULT_ROPE_RANGE", "library_path", "rope_table", "kv_append",
+           "query_absorb"]
 
 PAGE = 64
 
@@ -344,3 +351,123 @@ class TieredMla:
             if lse is not None:
                 row_copy(self.lse_s, lse, self.tier_rows, n, R, False, main)
         return out, lse
+
+
+# ---------------------------------------------------------------- around the decode
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+_BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
+
+
+def _check(dev: int, name: str, t, dtypes, *shape) -> None:
+    """`t` is a contiguous tensor of this shape (-1: any size) and one of these
+    types on CUDA device `dev`; the library sees only its pointer."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} is not a tensor on cuda:{dev}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has type {t.dtype}, not {dtypes[0]}")
+    if t.dim() != len(shape) or any(w >= 0 and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+
+
+def _device(name: str, t) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} is not a CUDA tensor")
+    return t.get_device()
+
+
+def _empty(size, dtype, device, stream):
+    """An output for a launch on `stream`, from that stream's memory pool."""
+    if stream is None:
+        return torch.empty(size, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=dtype, device=device)
+
+
+def rope_table(rows: int, base: float = 10000.0, device=None) -> torch.Tensor:
+    """[rows, 64] FP32: the cosines, then the sines, of position * base^(-2i/64)
+    for the 32 planes of the 64 rope dims (angles in 64 bits). Models that scale
+    their angles fill a table of this layout themselves."""
+    device = torch.device("cuda" if device is None else device)
+    inv = base ** (-torch.arange(0, 64, 2, dtype=torch.float64, device=device) / 64)
+    angle = torch.arange(rows, dtype=torch.float64, device=device)[:, None] * inv
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def kv_append(kv_new, kv, block_table, starts, rope, kv_scale: float, norm_weight=None,
+              norm_eps: float = 1e-6, cu_tokens=None, rope_starts=None, interleaved: bool = True,
+              status=None, stream=None) -> None:
+    """Append new tokens to the paged cache kv [pages, 64, 576] (E4M3 codes,
+    written in place): kv_new [tokens, 576] BF16 (rows may be strided), latent
+    dims normed with norm_weight [512] BF16 (None: no norm), rope dims rotated
+    at position rope_starts[r] + i (None: starts), divided by kv_scale. Token i
+    of request r goes to cache index starts[r] + i through block_table[r]; a
+    request with a negative start is skipped. cu_tokens [R + 1] gives ragged
+    requests their rows; without it each has tokens / R. See mla_kv_append in
+    include/mlafold.h."""
+    dev = _device("kv", kv)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return kv_append(kv_new, kv, block_table, starts, rope, kv_scale, norm_weight,
+                             norm_eps, cu_tokens, rope_starts, interleaved, status, stream)
+    _check(dev, "kv", kv, _E4M3, -1, PAGE, 576)
+    _check(dev, "block_table", block_table, _I32, -1, -1)
+    R = block_table.shape[0]
+    _check(dev, "starts", starts, _I32, R)
+    _check(dev, "rope", rope, _F32, -1, 64)
+    if _device("kv_new", kv_new) != dev or kv_new.dim() != 2 or kv_new.shape[1] != 576 or \
+            kv_new.dtype != torch.bfloat16 or kv_new.stride(1) != 1:
+        raise ValueError("kv_new is not [tokens, 576] BF16 with contiguous rows on kv's device")
+    if norm_weight is not None:
+        _check(dev, "norm_weight", norm_weight, _BF16, 512)
+    if cu_tokens is not None:
+        _check(dev, "cu_tokens", cu_tokens, _I32, R + 1)
+    if rope_starts is not None:
+        _check(dev, "rope_starts", rope_starts, _I32, R)
+    if status is not None:
+        _check(dev, "status", status, _I32, 1)
+    tokens = kv_new.shape[0]
+    shape = AppendShape(R, tokens, PAGE, block_table.shape[1], kv.shape[0], rope.shape[0],
+                        1 if interleaved else 0, kv_new.stride(0) if tokens > 1 else 576)
+    _lib.check("mla_kv_append", _lib.load().mla_kv_append(
+        ctypes.byref(shape), _ptr(kv_new), _ptr(norm_weight), float(norm_eps), _ptr(rope),
+        _ptr(cu_tokens), _ptr(starts), _ptr(rope_starts), _ptr(block_table), float(kv_scale),
+        _ptr(kv), _ptr(status), _stream(stream)))
+
+
+def query_absorb(q, w_uk, rope, rope_starts, q_scale: float, out=None, interleaved: bool = True,
+                 status=None, stream=None):
+    """The decode's queries [R*k, H, 576] (E4M3 codes): q [R*k, H, 192] BF16
+    (128 nope, 64 rope dims; tokens and heads may be strided), the nope part
+    times w_uk [H, 128, 512] BF16 per head, the rope part rotated at position
+    rope_starts[r] + i of token i of request r, divided by q_scale. See
+    mla_query_absorb in include/mlafold.h."""
+    dev = _device("q", q)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return query_absorb(q, w_uk, rope, rope_starts, q_scale, out, interleaved, status,
+                                stream)
+    if q.dim() != 3 or q.shape[2] != 192 or q.dtype != torch.bfloat16 or q.stride(2) != 1:
+        raise ValueError("q is not [R*k, H, 192] BF16 with contiguous dims")
+    T, H = q.shape[0], q.shape[1]
+    _check(dev, "rope_starts", rope_starts, _I32, -1)
+    R = rope_starts.shape[0]
+    if R < 1 or T < R or T % R:
+        raise ValueError(f"{T} tokens are not a positive multiple of {R} requests")
+    _check(dev, "w_uk", w_uk, _BF16, H, 128, 512)
+    _check(dev, "rope", rope, _F32, -1, 64)
+    if status is not None:
+        _check(dev, "status", status, _I32, 1)
+    if out is None:
+        out = _empty((T, H, 576), torch.uint8, q.device, stream)
+    else:
+        _check(dev, "out", out, _E4M3, T, H, 576)
+    shape = QueryShape(R, T // R, H, rope.shape[0], 1 if interleaved else 0,
+                       q.stride(0) if T > 1 else H * 192, q.stride(1) if H > 1 else 192)
+    _lib.check("mla_query_absorb", _lib.load().mla_query_absorb(
+        ctypes.byref(shape), _ptr(q), _ptr(w_uk), _ptr(rope), _ptr(rope_starts), float(q_scale),
+        _ptr(out), _ptr(status), _stream(stream)))
+    return out

@@ -16,13 +16,13 @@ STATUS_NAMES = {0: "MLA_OK", -1: "MLA_ERR_NULL", -2: "MLA_ERR_SHAPE", -3: "MLA_E
                 -4: "MLA_ERR_LIST", -5: "MLA_ERR_UNSUPPORTED", -6: "MLA_ERR_CUDA",
                 -7: "MLA_ERR_ALIGN", -8: "MLA_ERR_SCRATCH_LIMIT"}
 POLICY_BALANCED, POLICY_UNIFORM = 0, 1
-FAULT_WAIT_TIMEOUT, FAULT_PAGE_RANGE, FAULT_WORK_ITEM = 0x1, 0x2, 0x4
+FAULT_WAIT_TIMEOUT, FAULT_PAGE_RANGE, FAULT_WORK_ITEM, FAULT_ROPE_RANGE = 0x1, 0x2, 0x4, 0x8
 
 # Every symbol include/mlafold.h declares.
 EXPORTS = ("mla_plan_list_len", "mla_workspace_bytes", "mla_plan_splits",
            "mla_folded_decode", "mla_split_combine", "mla_lse_merge",
            "mla_folded_decode_noalloc", "mla_uv_combine", "mla_folded_decode_wait_test",
-           "mla_tier_plan", "mla_row_copy")
+           "mla_tier_plan", "mla_row_copy", "mla_kv_append", "mla_query_absorb")
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -32,6 +32,19 @@ class MlaShape(ctypes.Structure):
                 ("num_pages", ctypes.c_int32), ("num_ctas", ctypes.c_int32),
                 ("min_split_tokens", ctypes.c_int32), ("max_splits", ctypes.c_int32),
                 ("policy", ctypes.c_int32), ("groups", ctypes.c_int32)]
+
+
+class AppendShape(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int32), ("tokens", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("rope_rows", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("row_stride", ctypes.c_int64)]
+
+
+class QueryShape(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int32), ("k", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("rope_rows", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 class MlaError(RuntimeError):
@@ -76,6 +89,10 @@ def load() -> ctypes.CDLL:
     lib.mla_folded_decode_noalloc.restype = I32
     lib.mla_uv_combine.argtypes = [SP, P, P, I32, P, SZ, F, P, P, P, P, P]
     lib.mla_uv_combine.restype = I32
+    lib.mla_kv_append.argtypes = [ctypes.POINTER(AppendShape), P, P, F, P, P, P, P, P, F, P, P, P]
+    lib.mla_kv_append.restype = I32
+    lib.mla_query_absorb.argtypes = [ctypes.POINTER(QueryShape), P, P, P, P, F, P, P, P]
+    lib.mla_query_absorb.restype = I32
     _lib = lib
     return lib
 

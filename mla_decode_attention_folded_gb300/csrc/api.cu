@@ -8,9 +8,7 @@
 
 using namespace mlafold;
 
-namespace {
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+namespace mlafold {
 
 int check_shape(const mla_shape* s) {
   if (!s) return MLA_ERR_NULL;
@@ -41,7 +39,7 @@ int check_device() {
   return MLA_OK;
 }
 
-}  // namespace
+}  // namespace mlafold
 
 extern "C" {
 

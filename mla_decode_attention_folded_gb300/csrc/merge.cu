@@ -16,15 +16,6 @@ namespace {
 
 constexpr int kWarps = 8;
 
-__device__ __forceinline__ void bf16x8_to_f32(const uint4& v, float* f) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
-
 __global__ void __launch_bounds__(kWarps * 32)
 lse_merge_kernel(int S, int rows, const uint16_t* __restrict__ parts_out,
                  const float* __restrict__ parts_lse, uint16_t* __restrict__ out,

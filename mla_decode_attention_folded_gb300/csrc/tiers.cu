@@ -80,8 +80,6 @@ __global__ void row_copy_kernel(const uint8_t* __restrict__ src, uint8_t* __rest
   }
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 }  // namespace
 }  // namespace mlafold
 

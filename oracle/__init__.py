@@ -20,6 +20,9 @@ What it computes, from the pages' problem statement:
                    float64 here).
 * ``uv``        -- the W_UV up-projection of each head's merged latent row
                    (drafter-attention page, ``DraftDcp`` and ``latent_major``).
+* ``step``      -- what surrounds the decode in a step: cache rows of new tokens,
+                   absorbed queries, the decode behind a shared prefix (this
+                   library's additions; the pages take their results as given).
 * ``planner``   -- the integer split planner (balanced and uniform) that the
                    device planner must reproduce bit for bit. The pages name
                    the idea (balanced-MLA page, module overview; rank rule of
