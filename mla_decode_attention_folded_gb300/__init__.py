@@ -19,7 +19,8 @@ balanced-MLA page, ``BalancedMla.require`` / ``plan`` / ``decode``):
 Around the decode (additions of this library): ``kv_append(...)`` writes new
 tokens into the paged cache (RMS norm, rotation, E4M3), ``query_absorb(...)``
 makes the decode's queries (W_UK, rotation, E4M3), ``rope_table(rows)`` makes the
-table of angles both read.
+table of angles both read; ``PrefixMla(...)`` decodes a batch whose requests
+share a prefix, reading the prefix's keys once for all of them.
 """
 from __future__ import annotations
 
@@ -38,7 +39,7 @@ __all__ = ["MlaShape", "MlaError", "POLICY_BALANCED", "POLICY_UNIFORM", "make_sh
            "folded_decode_wait_test", "tier_plan", "row_copy", "balanced_tiers", "TIERS", "MOVE",
            "FoldedMla", "TieredMla", "fold_factor", "FAULT_WAIT_TIMEOUT", "FAULT_PAGE_RANGE",
            "FAULT_WORK_ITEM", "FAULT_ROPE_RANGE", "library_path", "rope_table", "kv_append",
-           "query_absorb"]
+           "query_absorb", "prefix_workspace_bytes", "prefix_decode", "PrefixMla"]
 
 PAGE = 64
 
@@ -52,8 +53,8 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream) -> int | None:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:      # the current stream's handle, without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -358,22 +359,27 @@ _E4M3 = (torch.uint8, torch.float8_e4m3fn)
 _BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
 
 
-def _check(dev: int, name: str, t, dtypes, *shape) -> None:
-    """`t` is a contiguous tensor of this shape (-1: any size) and one of these
-    types on CUDA device `dev`; the library sees only its pointer."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != dev:
+def _check(dev: int, name: str, t, dtypes, shape) -> None:
+    """`t` is a contiguous tensor of this shape and one of these types on CUDA
+    device `dev`; the library sees only its pointer."""
+    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype in dtypes and \
+            t.shape == shape and t.is_contiguous():
+        return
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
         raise ValueError(f"{name} is not a tensor on cuda:{dev}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has type {t.dtype}, not {dtypes[0]}")
-    if t.dim() != len(shape) or any(w >= 0 and n != w for n, w in zip(t.shape, shape)):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} is not contiguous")
+    raise ValueError(f"{name} is not contiguous")
 
 
-def _device(name: str, t) -> int:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _device(name: str, t, dims: int) -> int:
+    """The CUDA device of `t`, a tensor of so many dims."""
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
         raise ValueError(f"{name} is not a CUDA tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {dims} dims")
     return t.get_device()
 
 
@@ -408,30 +414,33 @@ def kv_append(kv_new, kv, block_table, starts, rope, kv_scale: float, norm_weigh
     request with a negative start is skipped. cu_tokens [R + 1] gives ragged
     requests their rows; without it each has tokens / R. See mla_kv_append in
     include/mlafold.h."""
-    dev = _device("kv", kv)
+    dev = _device("kv", kv, 3)
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return kv_append(kv_new, kv, block_table, starts, rope, kv_scale, norm_weight,
                              norm_eps, cu_tokens, rope_starts, interleaved, status, stream)
-    _check(dev, "kv", kv, _E4M3, -1, PAGE, 576)
-    _check(dev, "block_table", block_table, _I32, -1, -1)
-    R = block_table.shape[0]
-    _check(dev, "starts", starts, _I32, R)
-    _check(dev, "rope", rope, _F32, -1, 64)
-    if _device("kv_new", kv_new) != dev or kv_new.dim() != 2 or kv_new.shape[1] != 576 or \
+    _device("block_table", block_table, 2)
+    _device("rope", rope, 2)
+    R, max_pages = block_table.shape
+    pages, rope_rows = kv.shape[0], rope.shape[0]
+    _check(dev, "kv", kv, _E4M3, (pages, PAGE, 576))
+    _check(dev, "block_table", block_table, _I32, (R, max_pages))
+    _check(dev, "starts", starts, _I32, (R,))
+    _check(dev, "rope", rope, _F32, (rope_rows, 64))
+    if _device("kv_new", kv_new, 2) != dev or kv_new.shape[1] != 576 or \
             kv_new.dtype != torch.bfloat16 or kv_new.stride(1) != 1:
         raise ValueError("kv_new is not [tokens, 576] BF16 with contiguous rows on kv's device")
     if norm_weight is not None:
-        _check(dev, "norm_weight", norm_weight, _BF16, 512)
+        _check(dev, "norm_weight", norm_weight, _BF16, (512,))
     if cu_tokens is not None:
-        _check(dev, "cu_tokens", cu_tokens, _I32, R + 1)
+        _check(dev, "cu_tokens", cu_tokens, _I32, (R + 1,))
     if rope_starts is not None:
-        _check(dev, "rope_starts", rope_starts, _I32, R)
+        _check(dev, "rope_starts", rope_starts, _I32, (R,))
     if status is not None:
-        _check(dev, "status", status, _I32, 1)
+        _check(dev, "status", status, _I32, (1,))
     tokens = kv_new.shape[0]
-    shape = AppendShape(R, tokens, PAGE, block_table.shape[1], kv.shape[0], rope.shape[0],
-                        1 if interleaved else 0, kv_new.stride(0) if tokens > 1 else 576)
+    shape = AppendShape(R, tokens, PAGE, max_pages, pages, rope_rows, 1 if interleaved else 0,
+                        kv_new.stride(0) if tokens > 1 else 576)
     _lib.check("mla_kv_append", _lib.load().mla_kv_append(
         ctypes.byref(shape), _ptr(kv_new), _ptr(norm_weight), float(norm_eps), _ptr(rope),
         _ptr(cu_tokens), _ptr(starts), _ptr(rope_starts), _ptr(block_table), float(kv_scale),
@@ -445,29 +454,118 @@ def query_absorb(q, w_uk, rope, rope_starts, q_scale: float, out=None, interleav
     times w_uk [H, 128, 512] BF16 per head, the rope part rotated at position
     rope_starts[r] + i of token i of request r, divided by q_scale. See
     mla_query_absorb in include/mlafold.h."""
-    dev = _device("q", q)
+    dev = _device("q", q, 3)
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return query_absorb(q, w_uk, rope, rope_starts, q_scale, out, interleaved, status,
                                 stream)
-    if q.dim() != 3 or q.shape[2] != 192 or q.dtype != torch.bfloat16 or q.stride(2) != 1:
+    if q.shape[2] != 192 or q.dtype != torch.bfloat16 or q.stride(2) != 1:
         raise ValueError("q is not [R*k, H, 192] BF16 with contiguous dims")
-    T, H = q.shape[0], q.shape[1]
-    _check(dev, "rope_starts", rope_starts, _I32, -1)
-    R = rope_starts.shape[0]
+    _device("rope", rope, 2)
+    _device("rope_starts", rope_starts, 1)
+    T, H, _ = q.shape
+    R, rope_rows = rope_starts.shape[0], rope.shape[0]
     if R < 1 or T < R or T % R:
         raise ValueError(f"{T} tokens are not a positive multiple of {R} requests")
-    _check(dev, "w_uk", w_uk, _BF16, H, 128, 512)
-    _check(dev, "rope", rope, _F32, -1, 64)
+    _check(dev, "rope_starts", rope_starts, _I32, (R,))
+    _check(dev, "w_uk", w_uk, _BF16, (H, 128, 512))
+    _check(dev, "rope", rope, _F32, (rope_rows, 64))
     if status is not None:
-        _check(dev, "status", status, _I32, 1)
+        _check(dev, "status", status, _I32, (1,))
     if out is None:
         out = _empty((T, H, 576), torch.uint8, q.device, stream)
     else:
-        _check(dev, "out", out, _E4M3, T, H, 576)
-    shape = QueryShape(R, T // R, H, rope.shape[0], 1 if interleaved else 0,
+        _check(dev, "out", out, _E4M3, (T, H, 576))
+    shape = QueryShape(R, T // R, H, rope_rows, 1 if interleaved else 0,
                        q.stride(0) if T > 1 else H * 192, q.stride(1) if H > 1 else 192)
     _lib.check("mla_query_absorb", _lib.load().mla_query_absorb(
         ctypes.byref(shape), _ptr(q), _ptr(w_uk), _ptr(rope), _ptr(rope_starts), float(q_scale),
         _ptr(out), _ptr(status), _stream(stream)))
     return out
+
+
+def prefix_workspace_bytes(shape: MlaShape, prefix_pages: int) -> int:
+    out = ctypes.c_size_t(0)
+    _lib.check("mla_prefix_workspace_bytes", _lib.load().mla_prefix_workspace_bytes(
+        ctypes.byref(shape), int(prefix_pages), ctypes.byref(out)))
+    return out.value
+
+
+def prefix_decode(shape: MlaShape, q, kv, prefix_table, prefix_len, block_table, seq_lens,
+                  bmm1_scale: float, bmm2_scale: float, counts, work, workspace, out, lse,
+                  status=None, stream=None) -> None:
+    """The shared-prefix decode over the plan of plan_splits for the requests'
+    own lengths (see mla_prefix_decode in include/mlafold.h)."""
+    _lib.check("mla_prefix_decode", _lib.load().mla_prefix_decode(
+        ctypes.byref(shape), prefix_table.numel(), _ptr(q), _ptr(kv), _ptr(prefix_table),
+        _ptr(prefix_len), _ptr(block_table), _ptr(seq_lens), float(bmm1_scale), float(bmm2_scale),
+        _ptr(counts), _ptr(work), work.numel(), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse), _ptr(status),
+        _stream(stream)))
+
+
+class PrefixMla:
+    """Decode of a batch of R requests that share a prefix of up to
+    prefix_pages pages: plan buffers and workspace of one shape, allocated here
+    and reused by every call. ``plan(seq_lens)`` plans the requests' own keys
+    once per step; ``decode`` attends over the prefix and them. Calls on one
+    object share its buffers: they must run in stream order."""
+
+    def __init__(self, R: int, k: int, H: int, max_pages: int, prefix_pages: int, num_pages: int,
+                 device=None, num_ctas: int | None = None, min_split_tokens: int = 256,
+                 max_splits: int = 64, policy: int = POLICY_BALANCED):
+        self.device = torch.device(device if device is not None else "cuda")
+        if num_ctas is None:
+            num_ctas = torch.cuda.get_device_properties(self.device).multi_processor_count
+        self.shape = make_shape(R, k, H, max_pages, num_pages, num_ctas, min_split_tokens,
+                                max_splits, policy)
+        self.R, self.k, self.H, self.M = R, k, H, k * H
+        self.max_pages, self.prefix_pages, self.num_pages = max_pages, prefix_pages, num_pages
+        i32 = dict(dtype=torch.int32, device=self.device)
+        self.workspace = torch.empty(prefix_workspace_bytes(self.shape, prefix_pages),
+                                     dtype=torch.uint8, device=self.device)
+        self.counts = torch.zeros(R, **i32)
+        self.work = torch.full((plan_list_len(self.shape),), -1, **i32)
+        self.status = torch.zeros(1, **i32)
+
+    def plan(self, seq_lens, stream=None) -> None:
+        """Plan the splits of the requests' own keys: seq_lens [R] int32."""
+        dev = self.work.get_device()
+        _check(dev, "seq_lens", seq_lens, _I32, (self.R,))
+        if dev != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return plan_splits(self.shape, seq_lens, self.counts, self.work, stream)
+        plan_splits(self.shape, seq_lens, self.counts, self.work, stream)
+
+    def decode(self, q, kv, prefix_table, prefix_len, block_table, seq_lens, bmm1_scale: float,
+               bmm2_scale: float, out=None, lse=None, stream=None, return_lse: bool = True):
+        """out [R, k*H, 512] BF16 and the base-2 lse [R, k*H] (None without
+        return_lse) of queries q [R*k, H, 576] over the prefix (prefix_table
+        [prefix_pages] and prefix_len [1], int32) and each request's own keys
+        (block_table [R, max_pages], seq_lens [R], the planned lengths)."""
+        dev = self.work.get_device()
+        if dev != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return self.decode(q, kv, prefix_table, prefix_len, block_table, seq_lens,
+                                   bmm1_scale, bmm2_scale, out, lse, stream, return_lse)
+        R, M = self.R, self.M
+        _check(dev, "q", q, _E4M3, (R * self.k, self.H, 576))
+        _check(dev, "kv", kv, _E4M3, (self.num_pages, PAGE, 576))
+        _check(dev, "prefix_table", prefix_table, _I32, (self.prefix_pages,))
+        _check(dev, "prefix_len", prefix_len, _I32, (1,))
+        _check(dev, "block_table", block_table, _I32, (R, self.max_pages))
+        _check(dev, "seq_lens", seq_lens, _I32, (R,))
+        if out is None:
+            out = _empty((R, M, 512), torch.bfloat16, q.device, stream)
+        else:
+            _check(dev, "out", out, _BF16, (R, M, 512))
+        if not return_lse:
+            lse = None
+        elif lse is None:
+            lse = _empty((R, M), torch.float32, q.device, stream)
+        else:
+            _check(dev, "lse", lse, _F32, (R, M))
+        prefix_decode(self.shape, q, kv, prefix_table, prefix_len, block_table, seq_lens,
+                      bmm1_scale, bmm2_scale, self.counts, self.work, self.workspace, out, lse,
+                      self.status, stream)
+        return out, lse

@@ -115,7 +115,7 @@ __device__ __forceinline__ Job read_job(const DecodeArgs& a, int item, int blk, 
     jb.j0 = min(max(pa, 0) * kPage, jb.j1);
   }
   jb.ntiles = (int)cdiv(jb.j1 - jb.j0, kTileKeys);
-  jb.direct = n == 1;
+  jb.direct = n == 1 && !a.all_partial;
   if (!jb.direct && item >= a.slots) {
     if (report && a.status) atomicOr(a.status, MLA_FAULT_WORK_ITEM);
     jb.skip = true;

@@ -1,0 +1,113 @@
+"""Refusals of the calls around the decode, on the host: nothing here launches a
+kernel. The C entries get aligned pointers that are never read; the binding's
+checks refuse CPU tensors before anything else."""
+import ctypes
+
+import pytest
+import torch
+
+import mla_decode_attention_folded_gb300 as mla
+from mla_decode_attention_folded_gb300 import _lib
+
+P = ctypes.c_void_p(1 << 20)                       # aligned, never dereferenced
+ODD = ctypes.c_void_p((1 << 20) + 8)
+NULL, SHAPE, UNSUPPORTED, ALIGN = -1, -2, -5, -7
+
+
+def _append(shape=None, *, ptr=None, eps=1e-6, scale=0.1, **fields):
+    s = _lib.AppendShape(2, 8, 64, 4, 10, 100, 1, 576)
+    for name, value in fields.items():
+        setattr(s, name, value)
+    at = dict(x=P, w=None, rope=P, cu=None, starts=P, rope_starts=None, table=P, kv=P, status=None)
+    at.update(ptr or {})
+    return _lib.load().mla_kv_append(
+        ctypes.byref(s) if shape is None else shape, at["x"], at["w"], eps, at["rope"], at["cu"],
+        at["starts"], at["rope_starts"], at["table"], scale, at["kv"], at["status"], None)
+
+
+@pytest.mark.parametrize("fields,code", [
+    (dict(page_size=32), UNSUPPORTED), (dict(R=0), SHAPE), (dict(R=(1 << 20) + 1), SHAPE),
+    (dict(tokens=-1), SHAPE), (dict(tokens=7), SHAPE), (dict(max_pages=0), SHAPE),
+    (dict(max_pages=1 << 25), SHAPE), (dict(num_pages=0), SHAPE), (dict(num_pages=1 << 25), SHAPE),
+    (dict(rope_rows=0), SHAPE), (dict(interleaved=2), SHAPE), (dict(row_stride=568), SHAPE),
+    (dict(row_stride=580), ALIGN)])
+def test_append_shapes_refused(fields, code):
+    assert _append(**fields) == code
+
+
+@pytest.mark.parametrize("name", ["x", "rope", "starts", "table", "kv"])
+def test_append_null_pointers_refused(name):
+    assert _append(ptr={name: None}) == NULL
+
+
+@pytest.mark.parametrize("name", ["x", "w", "kv"])
+def test_append_alignment_refused(name):
+    assert _append(ptr={name: ODD}) == ALIGN
+
+
+@pytest.mark.parametrize("kw", [dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
+                                dict(scale=float("inf")), dict(scale=1e-45), dict(eps=-1e-6),
+                                dict(eps=float("nan")), dict(eps=float("inf"))])
+def test_append_numbers_refused(kw):
+    assert _append(**kw) == SHAPE
+
+
+def test_append_without_tokens_needs_no_pointers():
+    assert _append(tokens=0, ptr=dict(x=None, kv=None)) == 0
+    assert _lib.load().mla_kv_append(None, P, None, 1e-6, P, None, P, None, P, 1.0, P, None,
+                                     None) == NULL
+
+
+def _absorb(*, ptr=None, scale=0.1, **fields):
+    s = _lib.QueryShape(2, 4, 8, 100, 1, 8 * 192, 192)
+    for name, value in fields.items():
+        setattr(s, name, value)
+    at = dict(q=P, w=P, rope=P, starts=P, out=P, status=None)
+    at.update(ptr or {})
+    return _lib.load().mla_query_absorb(ctypes.byref(s), at["q"], at["w"], at["rope"],
+                                        at["starts"], scale, at["out"], at["status"], None)
+
+
+@pytest.mark.parametrize("fields,code", [
+    (dict(R=0), SHAPE), (dict(k=0), SHAPE), (dict(H=0), SHAPE), (dict(H=(1 << 16) + 1), SHAPE),
+    (dict(R=1 << 23, k=4), SHAPE), (dict(R=1 << 22, k=1, H=1 << 12), SHAPE),
+    (dict(rope_rows=0), SHAPE), (dict(interleaved=-1), SHAPE), (dict(token_stride=184), SHAPE),
+    (dict(head_stride=184), SHAPE), (dict(token_stride=1540), ALIGN), (dict(head_stride=196), ALIGN)])
+def test_absorb_shapes_refused(fields, code):
+    assert _absorb(**fields) == code
+
+
+@pytest.mark.parametrize("name", ["q", "w", "rope", "starts", "out"])
+def test_absorb_pointers_refused(name):
+    assert _absorb(ptr={name: None}) == NULL
+    if name != "starts":
+        assert _absorb(ptr={name: ODD}) == ALIGN
+
+
+@pytest.mark.parametrize("scale", [0.0, -1.0, float("nan"), float("inf"), 1e-45])
+def test_absorb_scales_refused(scale):
+    assert _absorb(scale=scale) == SHAPE
+
+
+def test_binding_refuses_cpu_tensors():
+    x = torch.zeros(2, 576, dtype=torch.bfloat16)
+    kv = torch.zeros(1, 64, 576, dtype=torch.uint8)
+    i32 = torch.zeros(1, dtype=torch.int32)
+    rope = mla.rope_table(4, device="cpu")
+    with pytest.raises(ValueError, match="kv is not a CUDA tensor"):
+        mla.kv_append(x, kv, i32[None], i32, rope, 1.0)
+    with pytest.raises(ValueError, match="q is not a CUDA tensor"):
+        mla.query_absorb(torch.zeros(2, 1, 192, dtype=torch.bfloat16), x, rope, i32, 1.0)
+
+
+@pytest.mark.parametrize("base", [10000.0, 500000.0])
+def test_rope_table(base):
+    t = mla.rope_table(131072, base, device="cpu")
+    assert t.shape == (131072, 64) and t.dtype == torch.float32
+    import math
+    for p in (0, 1, 777, 131071):
+        for i in (0, 7, 31):
+            a = p * base ** (-i / 32)
+            # 64-bit angles: their error is below 2^-53 * 2^17 * a few steps, FP32 rounding 2^-25.
+            assert abs(float(t[p, i]) - math.cos(a)) < 2.0 ** -24
+            assert abs(float(t[p, 32 + i]) - math.sin(a)) < 2.0 ** -24
