@@ -438,7 +438,7 @@ int32_t mla_prefix_workspace_bytes(const mla_shape *shape, int32_t prefix_pages,
  *   j < seq_lens[r] of the request's own keys, as in mla_folded_decode.
  *   shape, counts, work, list_len  the plan of mla_plan_splits for seq_lens, the
  *                requests' own lengths, with groups 0 or 1.
- *   prefix_pages 1 .. 2^25 - 1: entries of prefix_table.
+ *   prefix_pages 1 .. 2^24: entries of prefix_table.
  *   prefix_table [prefix_pages] int32, device: the prefix's pages; only the
  *                first ceil(prefix_len / 64) are read.
  *   prefix_len   [1] int32, device: its keys (negative is read as 0; more than

@@ -5,15 +5,16 @@
 //   s[n][j] = bmm1 * q[n] . kv[key j],  j over the prefix's keys, then the request's own
 //   out[n]  = bmm2 * sum_j softmax_j(s[n]) kv[key j][0:512],  lse[n] = log2 sum_j 2^(s log2 e)
 //
-// The softmax splits over key sets by their LSEs: the prefix is decoded as one
-// wide request of N = R*k*H rows, the requests' own keys by the planned
-// decode, both into FP32 partials; the merge below joins all of a row's
-// partials and rounds once to BF16.
+// The softmax splits over key sets by their LSEs: the prefix against all R*k*H
+// rows (prefix_wide.cu), the requests' own keys by the planned decode, both into
+// FP32 partials; the merge below joins all of a row's partials and rounds once
+// to BF16.
 //
 // The merge is bound by memory: per row, the partials of its prefix pieces and
 // of its own splits (2 KB each) in, 1 KB out. One warp per row; the lanes hold
 // the partials' LSEs and share weights by shuffles, as the split reducer does.
 #include "internal.h"
+#include "prefix.h"
 #include "ptx.cuh"
 
 namespace mlafold {
@@ -24,15 +25,15 @@ constexpr int kWarps = 8;                  // rows per CTA
 struct MergeArgs {
   const int32_t* counts;                   // [R] splits of each request's own keys
   const int32_t* work;                     // their work list
-  const int32_t* prefix_counts;            // [1] pieces of the prefix
-  const float* prefix_o;                   // [prefix_slots][N][512]
-  const float* prefix_lse;                 // [prefix_slots][N]
+  const int32_t* prefix_len;               // [1]
+  const float* prefix_o;                   // [units + blocks - 1][128][512]
+  const float* prefix_lse;                 // [units + blocks - 1][128]
   const float* own_o;                      // [slots][M][512]
   const float* own_lse;                    // [slots][M]
   uint16_t* out;                           // [N][512]
   float* lse;                              // [N], may be null
   float bmm2;
-  int R, M, slots, prefix_slots;
+  int R, M, slots, prefix_pages, units, blocks;
 };
 
 __global__ void __launch_bounds__(kWarps * 32) prefix_merge_kernel(const MergeArgs a) {
@@ -51,19 +52,29 @@ __global__ void __launch_bounds__(kWarps * 32) prefix_merge_kernel(const MergeAr
   const int start = s_start;
   int n_own = a.counts[r];
   if (start < 0 || n_own < 1 || start + n_own > a.slots) n_own = 0;   // not a plan of this shape
-  const int n_pre = min(max(a.prefix_counts[0], 0), a.prefix_slots);
-  const int n = n_pre + n_own;
-  const size_t N = (size_t)a.R * a.M;
+  const int tiles = (int)cdiv(wide_len(a.prefix_len, a.prefix_pages, nullptr, false), kWideKeys);
+  const long long total = (long long)tiles * a.blocks;
+  const long long used = total < a.units ? total : a.units;
   for (int m = blockIdx.x * kWarps + (threadIdx.x >> 5); m < a.M; m += gridDim.x * kWarps) {
     const size_t row = (size_t)r * a.M + m;
+    // The prefix's pieces of this row's block, in consecutive slots.
+    const long long block = row / kWideRows;
+    int n_pre = 0;
+    size_t pre = 0;
+    if (tiles > 0) {
+      const int u0 = wide_unit_of(block * tiles, total, used);
+      n_pre = wide_unit_of((block + 1) * tiles - 1, total, used) - u0 + 1;
+      pre = (size_t)(u0 + block) * kWideRows + row % kWideRows;
+    }
+    const int n = n_pre + n_own;
     // Partial s of this row: first the prefix's pieces, then the request's splits.
     auto lse_of = [&](int s) {
-      return s < n_pre ? a.prefix_lse[(size_t)s * N + row]
+      return s < n_pre ? a.prefix_lse[pre + (size_t)s * kWideRows]
                        : a.own_lse[(size_t)(start + s - n_pre) * a.M + m];
     };
     auto row_of = [&](int s) {
       return reinterpret_cast<const float4*>(
-          s < n_pre ? a.prefix_o + ((size_t)s * N + row) * kDv
+          s < n_pre ? a.prefix_o + (pre + (size_t)s * kWideRows) * kDv
                     : a.own_o + ((size_t)(start + s - n_pre) * a.M + m) * kDv);
     };
     float mx = -INFINITY;
@@ -99,7 +110,7 @@ __global__ void __launch_bounds__(kWarps * 32) prefix_merge_kernel(const MergeAr
                          ((uint32_t)f32_to_bf16_bits(acc[v].y * scale) << 16),
                      (uint32_t)f32_to_bf16_bits(acc[v].z * scale) |
                          ((uint32_t)f32_to_bf16_bits(acc[v].w * scale) << 16));
-    if (a.lse && lane == 0) a.lse[row] = z > 0.f ? mx + __log2f(z) : -INFINITY;
+    if (a.lse && lane == 0) a.lse[row] = z == 0.f ? -INFINITY : mx + __log2f(z);
   }
 }
 
@@ -116,41 +127,31 @@ cudaError_t launch_merge(const MergeArgs& a, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, prefix_merge_kernel, a);
 }
 
-// The prefix as one wide request of N rows, on the shape's decode and planner.
-mla_shape wide_shape(const mla_shape& s, int prefix_pages) {
-  mla_shape p = s;
-  p.R = 1;
-  p.k = s.R * s.k;
-  p.max_pages = prefix_pages;
-  p.policy = MLA_POLICY_BALANCED;
-  p.groups = 1;
-  return p;
-}
+// Row blocks of the batch and CTA pairs of the wide kernel.
+int wide_blocks(const mla_shape& s) { return (int)cdiv((long long)s.R * s.k * s.H, kWideRows); }
+int wide_units(const mla_shape& s) { return s.num_ctas / 2 > 0 ? s.num_ctas / 2 : 1; }
 
 // Workspace offsets. Every split of a request's own keys has a partial, so
 // that one-split rows too reach the merge unrounded.
 struct Layout {
-  size_t prefix_o, prefix_lse, own_o, own_lse, prefix_counts, prefix_work, bytes;
+  size_t prefix_o, prefix_lse, own_o, own_lse, bytes;
 };
-Layout layout(const mla_shape& s, int prefix_pages) {
-  const mla_shape p = wide_shape(s, prefix_pages);
-  const size_t N = (size_t)s.R * s.k * s.H, M = (size_t)s.k * s.H;
-  const size_t ps = plan_items(p), os = plan_items(s);
+Layout layout(const mla_shape& s) {
+  const size_t ps = (size_t)(wide_units(s) + wide_blocks(s) - 1) * kWideRows;
+  const size_t os = (size_t)plan_items(s) * s.k * s.H;
   Layout l;
   l.prefix_o = 0;
-  l.prefix_lse = l.prefix_o + align256(ps * N * kDv * 4);
-  l.own_o = l.prefix_lse + align256(ps * N * 4);
-  l.own_lse = l.own_o + align256(os * M * kDv * 4);
-  l.prefix_counts = l.own_lse + align256(os * M * 4);
-  l.prefix_work = l.prefix_counts + 256;
-  l.bytes = l.prefix_work + align256((size_t)plan_list_len(p) * 4);
+  l.prefix_lse = l.prefix_o + align256(ps * kDv * 4);
+  l.own_o = l.prefix_lse + align256(ps * 4);
+  l.own_lse = l.own_o + align256(os * kDv * 4);
+  l.bytes = l.own_lse + align256(os * 4);
   return l;
 }
 
 int check_prefix_shape(const mla_shape* s, int prefix_pages) {
   const int st = check_shape(s);
   if (st != MLA_OK) return st;
-  if (shape_groups(*s) != 1 || prefix_pages < 1 || prefix_pages >= (1 << 25)) return MLA_ERR_SHAPE;
+  if (shape_groups(*s) != 1 || prefix_pages < 1 || prefix_pages > (1 << 24)) return MLA_ERR_SHAPE;
   return MLA_OK;
 }
 
@@ -164,7 +165,7 @@ extern "C" int32_t mla_prefix_workspace_bytes(const mla_shape* shape, int32_t pr
   const int st = check_prefix_shape(shape, prefix_pages);
   if (st != MLA_OK) return st;
   if (!bytes) return MLA_ERR_NULL;
-  *bytes = layout(*shape, prefix_pages).bytes;
+  *bytes = layout(*shape).bytes;
   return MLA_OK;
 }
 
@@ -186,24 +187,28 @@ extern "C" int32_t mla_prefix_decode(const mla_shape* shape, int32_t prefix_page
       !aligned(workspace, 256) || !aligned(status, 4))
     return MLA_ERR_ALIGN;
   if (list_len < plan_list_len(*shape)) return MLA_ERR_LIST;
-  const Layout l = layout(*shape, prefix_pages);
+  const Layout l = layout(*shape);
   if (workspace_bytes_given < l.bytes) return MLA_ERR_WORKSPACE;
   if (!scales_ok(bmm1_scale, bmm2_scale)) return MLA_ERR_SHAPE;
   if ((st = check_device()) != MLA_OK) return st;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const mla_shape p = wide_shape(*shape, prefix_pages);
-  int32_t* pc = reinterpret_cast<int32_t*>(ws + l.prefix_counts);
-  int32_t* pw = reinterpret_cast<int32_t*>(ws + l.prefix_work);
-  if (launch_plan(p, prefix_len, pc, pw, plan_list_len(p), cs) != cudaSuccess) return MLA_ERR_CUDA;
-  DecodeArgs a = decode_args(p, q, kv, prefix_table, prefix_len, bmm1_scale, 1.f, pc, pw, out,
-                             nullptr, status);
-  a.part_o = reinterpret_cast<float*>(ws + l.prefix_o);
-  a.part_lse = reinterpret_cast<float*>(ws + l.prefix_lse);
-  a.slots = plan_items(p);
-  a.all_partial = 1;
-  if (launch_decode(p, a, cs) != cudaSuccess) return MLA_ERR_CUDA;
-  a = decode_args(*shape, q, kv, block_table, seq_lens, bmm1_scale, 1.f, counts, work, out, nullptr,
+  WideArgs w;
+  w.prefix_table = prefix_table;
+  w.prefix_len = prefix_len;
+  w.part_o = reinterpret_cast<float*>(ws + l.prefix_o);
+  w.part_lse = reinterpret_cast<float*>(ws + l.prefix_lse);
+  w.status = status;
+  w.bmm1_log2 = (float)((double)bmm1_scale * 1.4426950408889634);
+  w.N = (long long)shape->R * shape->k * shape->H;
+  w.prefix_pages = prefix_pages;
+  w.num_pages = shape->num_pages;
+  w.units = wide_units(*shape);
+  w.blocks = wide_blocks(*shape);
+  if (launch_wide(w, static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(kv), cs) !=
+      cudaSuccess)
+    return MLA_ERR_CUDA;
+  DecodeArgs a = decode_args(*shape, q, kv, block_table, seq_lens, bmm1_scale, 1.f, counts, work, out, nullptr,
                   status);
   a.part_o = reinterpret_cast<float*>(ws + l.own_o);
   a.part_lse = reinterpret_cast<float*>(ws + l.own_lse);
@@ -213,9 +218,9 @@ extern "C" int32_t mla_prefix_decode(const mla_shape* shape, int32_t prefix_page
   MergeArgs m;
   m.counts = counts;
   m.work = work;
-  m.prefix_counts = pc;
-  m.prefix_o = reinterpret_cast<const float*>(ws + l.prefix_o);
-  m.prefix_lse = reinterpret_cast<const float*>(ws + l.prefix_lse);
+  m.prefix_len = prefix_len;
+  m.prefix_o = w.part_o;
+  m.prefix_lse = w.part_lse;
   m.own_o = reinterpret_cast<const float*>(ws + l.own_o);
   m.own_lse = reinterpret_cast<const float*>(ws + l.own_lse);
   m.out = static_cast<uint16_t*>(out);
@@ -224,6 +229,8 @@ extern "C" int32_t mla_prefix_decode(const mla_shape* shape, int32_t prefix_page
   m.R = shape->R;
   m.M = shape->k * shape->H;
   m.slots = plan_items(*shape);
-  m.prefix_slots = plan_items(p);
+  m.prefix_pages = prefix_pages;
+  m.units = w.units;
+  m.blocks = w.blocks;
   return launch_merge(m, cs) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
