@@ -55,7 +55,9 @@ constexpr int kPRow = 128;                    // a key's 64 hi codes, then its 6
 constexpr int kPBytes = kKeys * kPRow;
 constexpr int kOffQ = 2 * kStageBytes;
 constexpr int kOffP = kOffQ + kQBytes;
-constexpr int kOffCtl = kOffP + kPBytes;
+constexpr int kOffStage = kOffP + kPBytes;    // P of keys 64 .. 127 on its way to the other CTA
+constexpr int kOffCtl = kOffStage + 64 * kPRow;
+static_assert(64 * kPRow <= kRopeBytes, "the first 64 keys' P waits in the rope's place");
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSCol = 256;                    // S buffers after O's two blocks of 128 columns
 constexpr unsigned long long kTimeoutNs = 2000000000ull;
@@ -67,10 +69,11 @@ static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms need 1 KB a
 struct WideCtl {
   uint64_t k_full[2];      // TMA -> MMA (rank 0), relay (rank 1): own keys landed
   uint64_t k_peer[2];      // rank 0: the other CTA's keys landed
-  uint64_t v_full[2];      // TMA -> softmax: the other CTA's keys of the own dims landed
+  uint64_t v_full[2];      // TMA -> MMA, relay: the other CTA's keys of the own dims landed
   uint64_t s_full[2];      // MMA -> softmax, TMA: S of a tile done
-  uint64_t s_empty[2];     // rank 0: S read by the softmax of both CTAs
-  uint64_t p_full;         // rank 0: P written by both CTAs, V complete in both
+  uint64_t p_full;         // softmax of both CTAs -> MMA (rank 0), relay (rank 1): this CTA's
+                           // rows of P written
+  uint64_t p_peer;         // rank 0: P and V complete in the other CTA
   uint64_t pv_done[2];     // MMA -> softmax, TMA: O holds the tile; P and the stage are free
   uint64_t q_full, q_peer, q_empty;
   uint64_t vote_bar[2];    // the other CTA's flag is in vote_peer
@@ -93,10 +96,10 @@ constexpr uint32_t kMoved = 1, kFailed = 2;
 
 __device__ __forceinline__ bool w_wait(uint64_t* bar, uint32_t parity, WideCtl* ctl,
                                        int32_t* status) {
-  if (tc::mbar_try_wait_cluster(bar, parity)) return true;
+  if (tc::mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = tc::globaltimer_ns();
   while (true) {
-    if (tc::mbar_try_wait_cluster(bar, parity)) return true;
+    if (tc::mbar_try_wait(bar, parity)) return true;
     if (*reinterpret_cast<volatile int*>(&ctl->abort_flag)) return false;
     if (tc::globaltimer_ns() - t0 > kTimeoutNs) {
       *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
@@ -118,45 +121,41 @@ __device__ void producer(const WideArgs& a, const WidePart& w, uint8_t* smem, Wi
   const int lane = threadIdx.x & 31;
   const long long n = w.end - w.begin;             // tiles of this pair
   const int pages_all = (int)cdiv(w.len, kPage);
-  auto page_id = [&](long long i) {                // lane l: page l of the pair's tile i
-    const int p = (int)((w.begin + i) % w.tiles) * (kKeys / kPage) + lane;
-    int id = -1;
-    if (lane < kKeys / kPage && i < n && p < pages_all) {
-      id = a.prefix_table[p];
-      if (id < 0 || id >= a.num_pages) {
-        if (a.status) atomicOr(a.status, MLA_FAULT_PAGE_RANGE);
-        id = -1;
-      }
-    }
-    return id;
+  int tile = (int)(w.begin % w.tiles);             // within its block, of the next page_ids()
+  int block = (int)(w.begin / w.tiles);            // of the next Q
+  auto page_ids = [&]() {                          // lane l: page l of the next tile
+    const int p = tile * (kKeys / kPage) + lane;
+    if (++tile == w.tiles) tile = 0;
+    return lane < kKeys / kPage && p < pages_all ? a.prefix_table[p] : -1;
   };
   long long nk = 0, nv = 0;                        // next tile: own keys, other keys' values
-  long long q_at = 0;                              // first tile of the next block
+  long long q_at = 0, q_step = w.tiles - tile;     // first tile of the next block
   uint32_t x = 0;                                  // blocks whose Q was requested
-  int ids[2] = {-1, -1}, next = page_id(0);
+  int ids[2] = {-1, -1}, next = page_ids();
   unsigned long long t0 = 0;
   bool ok = true;
   while (nv < n) {
     uint32_t can = 0;                              // lane 0 looks, all lanes act
     if (lane == 0) {
-      if (q_at <= nk && q_at < n && (x == 0 || tc::mbar_test_wait_cluster(&ctl->q_empty, (x - 1) & 1)))
+      if (q_at <= nk && q_at < n && (x == 0 || tc::mbar_test_wait(&ctl->q_empty, (x - 1) & 1)))
         can |= 1;
-      if (nk < n && (nk < 2 || tc::mbar_test_wait_cluster(&ctl->pv_done[nk & 1], (uint32_t)((nk >> 1) - 1) & 1)))
+      if (nk < n && (nk < 2 || tc::mbar_test_wait(&ctl->pv_done[nk & 1], (uint32_t)((nk >> 1) - 1) & 1)))
         can |= 2;
-      if (nv < nk && tc::mbar_test_wait_cluster(&ctl->s_full[nv & 1], (uint32_t)(nv >> 1) & 1)) can |= 4;
+      if (nv < nk && tc::mbar_test_wait(&ctl->s_full[nv & 1], (uint32_t)(nv >> 1) & 1)) can |= 4;
     }
     can = __shfl_sync(0xffffffffu, can, 0);
     if (can & 1) {
-      const long long f = w.begin + q_at;
       if (lane == 0) {
         uint8_t* q = smem + kOffQ;
-        const int row = (int)(f / w.tiles) * kRows + (int)rank * 64;
+        const int row = block * kRows + (int)rank * 64;
         tc::mbar_arrive_expect_tx(&ctl->q_full, kQBytes);
         for (int c = 0; c < 4; ++c)
           tc::tma_load_2d(q + c * kQChunk, tm_q, &ctl->q_full, c * 128, row);
         tc::tma_load_2d(q + 4 * kQChunk, tm_qr, &ctl->q_full, 512, row);
       }
-      q_at += w.tiles - f % w.tiles;               // the next block starts there
+      q_at += q_step;
+      q_step = w.tiles;
+      ++block;
       ++x;
     }
     if (can & 4) {
@@ -179,9 +178,13 @@ __device__ void producer(const WideArgs& a, const WidePart& w, uint8_t* smem, Wi
     }
     if (can & 2) {
       const int st = nk & 1;
-      if (st) ids[1] = next; else ids[0] = next;
-      const int cur = next;
-      next = page_id(nk + 1);
+      int cur = next;
+      if (cur >= a.num_pages || (cur < 0 && lane < kKeys / kPage &&
+                                 ((tile ? tile : w.tiles) - 1) * (kKeys / kPage) + lane < pages_all)) {
+        if (a.status) atomicOr(a.status, MLA_FAULT_PAGE_RANGE);
+        cur = -1;
+      }
+      if (st) ids[1] = cur; else ids[0] = cur;
       const int p0 = __shfl_sync(0xffffffffu, cur, 2 * rank);
       const int p1 = __shfl_sync(0xffffffffu, cur, 2 * rank + 1);
       if (lane == 0) {
@@ -197,6 +200,7 @@ __device__ void producer(const WideArgs& a, const WidePart& w, uint8_t* smem, Wi
                           512, id * kPage);
         }
       }
+      next = nk + 1 < n ? page_ids() : -1;         // in flight until the next tile
       ++nk;
     }
     if (can) {
@@ -234,17 +238,47 @@ __device__ void producer(const WideArgs& a, const WidePart& w, uint8_t* smem, Wi
 }
 
 // ---------------------------------------------------------------- relay (rank 1)
-// Tells rank 0's MMA thread what landed here.
+// Tells rank 0's MMA thread what is complete here.
 __device__ void relay(const WideArgs& a, const WidePart& w, WideCtl* ctl) {
+  const long long n = w.end - w.begin;
+  long long nk = 0, np = 0;                        // next tile: keys, P
   uint32_t x = 0;
-  for (long long i = 0; i < w.end - w.begin; ++i) {
-    if (i == 0 || (w.begin + i) % w.tiles == 0) {
-      if (!w_wait(&ctl->q_full, x & 1, ctl, a.status)) return;
-      tc::remote_arrive(tc::map_rank(&ctl->q_peer, 0));
-      ++x;
+  unsigned long long t0 = 0;
+  while (np < n) {
+    bool progress = false;
+    if (np < nk && tc::mbar_test_wait(&ctl->p_full, (uint32_t)np & 1) &&
+        tc::mbar_test_wait(&ctl->v_full[np & 1], (uint32_t)(np >> 1) & 1)) {
+      tc::remote_arrive(tc::map_rank(&ctl->p_peer, 0));
+      ++np;
+      progress = true;
     }
-    if (!w_wait(&ctl->k_full[i & 1], (uint32_t)(i >> 1) & 1, ctl, a.status)) return;
-    tc::remote_arrive(tc::map_rank(&ctl->k_peer[i & 1], 0));
+    if (nk < n && nk <= np + 1 && tc::mbar_test_wait(&ctl->k_full[nk & 1], (uint32_t)(nk >> 1) & 1)) {
+      bool q = true;
+      if (nk == 0 || (w.begin + nk) % w.tiles == 0) {
+        q = tc::mbar_test_wait(&ctl->q_full, x & 1);
+        if (q) {
+          tc::remote_arrive(tc::map_rank(&ctl->q_peer, 0));
+          ++x;
+        }
+      }
+      if (q) {
+        tc::remote_arrive(tc::map_rank(&ctl->k_peer[nk & 1], 0));
+        ++nk;
+        progress = true;
+      }
+    }
+    if (progress) {
+      t0 = 0;
+      continue;
+    }
+    const unsigned long long now = tc::globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    const bool expired = now - t0 > kTimeoutNs;
+    if (*reinterpret_cast<volatile int*>(&ctl->abort_flag) || expired) {
+      *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
+      if (expired && a.status) atomicOr(a.status, MLA_FAULT_WAIT_TIMEOUT);
+      return;
+    }
   }
 }
 
@@ -260,7 +294,9 @@ __device__ void mma_issuer(const WideArgs& a, const WidePart& w, uint8_t* smem, 
   unsigned long long t0 = 0;
   while (npv < n) {
     bool progress = false;
-    if (npv < ns && tc::mbar_test_wait_cluster(&ctl->p_full, (uint32_t)npv & 1)) {
+    if (npv < ns && tc::mbar_test_wait(&ctl->p_full, (uint32_t)npv & 1) &&
+        tc::mbar_test_wait(&ctl->p_peer, (uint32_t)npv & 1) &&
+        tc::mbar_test_wait(&ctl->v_full[npv & 1], (uint32_t)(npv >> 1) & 1)) {
       tc::fence_after_sync();
       const uint32_t kv = s_kv + (npv & 1) * kStageBytes;
       const bool first = npv == 0 || (w.begin + npv) % w.tiles == 0;
@@ -287,12 +323,13 @@ __device__ void mma_issuer(const WideArgs& a, const WidePart& w, uint8_t* smem, 
       const uint32_t ph = (uint32_t)(ns >> 1) & 1;
       if (ns == block_end) {                       // a new block: its Q in both CTAs
         if (!q_ready)
-          q_ready = tc::mbar_test_wait_cluster(&ctl->q_full, x & 1) &&
-                    tc::mbar_test_wait_cluster(&ctl->q_peer, x & 1);
+          q_ready = tc::mbar_test_wait(&ctl->q_full, x & 1) &&
+                    tc::mbar_test_wait(&ctl->q_peer, x & 1);
       }
-      if ((ns != block_end || q_ready) && tc::mbar_test_wait_cluster(&ctl->k_full[st], ph) &&
-          tc::mbar_test_wait_cluster(&ctl->k_peer[st], ph) &&
-          (ns < 2 || tc::mbar_test_wait_cluster(&ctl->s_empty[st], ph ^ 1))) {
+      if ((ns != block_end || q_ready) && tc::mbar_test_wait(&ctl->k_full[st], ph) &&
+          tc::mbar_test_wait(&ctl->k_peer[st], ph)) {
+        // The S buffer of tile ns - 2 is free: its stage was refilled after its
+        // PV, whose P the softmax wrote after it had read that S.
         tc::fence_after_sync();
         if (ns == block_end) {
           block_end += w.tiles - (w.begin + ns) % w.tiles;
@@ -362,10 +399,6 @@ struct Soft {
     const bool got = ok && w_wait(bar, parity, ctl, a.status);
     ok = __all_sync(0xffffffffu, got);
   }
-  __device__ void arrive(uint64_t* bar, uint32_t to) {      // one arrival per warp
-    __syncwarp();
-    if (lane == 0) tc::remote_arrive(tc::map_rank(bar, to));
-  }
   // Scores of 32 rows of this thread's key, in base 2 (-inf for keys past the end).
   __device__ void scores(int st, int c, bool valid, float (&v)[32]) const {
     uint32_t raw[32];
@@ -382,8 +415,9 @@ struct Soft {
     ++swaps;
     float got = v;
     if (gt < kRows) {
-      tc::remote_st(tc::map_rank(&ctl->swap[b][gt], 1 - rank), __float_as_uint(v));
-      arrive(&ctl->swap_bar[b], 1 - rank);
+      if (gt == 0) tc::mbar_arrive_expect_tx(&ctl->swap_bar[b], kRows * 4);
+      tc::remote_st_async(tc::map_rank(&ctl->swap[b][gt], 1 - rank), __float_as_uint(v),
+                          tc::map_rank(&ctl->swap_bar[b], 1 - rank));
       wait(&ctl->swap_bar[b], ph);
       got = *reinterpret_cast<volatile float*>(&ctl->swap[b][gt]);
     }
@@ -508,8 +542,9 @@ struct Soft {
       uint32_t mine = *reinterpret_cast<volatile uint32_t*>(&ctl->vote[b]);
       if (lane == 0) {
         ctl->vote[b ^ 1] = 0;                      // read by all before this barrier
-        tc::remote_st(tc::map_rank(&ctl->vote_peer[b], 1 - rank), mine & kMoved);
-        tc::remote_arrive(tc::map_rank(&ctl->vote_bar[b], 1 - rank));
+        tc::mbar_arrive_expect_tx(&ctl->vote_bar[b], 4);
+        tc::remote_st_async(tc::map_rank(&ctl->vote_peer[b], 1 - rank), mine & kMoved,
+                            tc::map_rank(&ctl->vote_bar[b], 1 - rank));
       }
       wait(&ctl->vote_bar[b], ph);
       if (!ok) mine |= kFailed;
@@ -560,24 +595,27 @@ __device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
           s.weigh(st, valid, lp, hi, lo);
         }
       }
-      tc::fence_before_sync();
-      s.arrive(&ctl->s_empty[st], 0);
       // P is free once PV of the previous tile is done with it.
       if (g > 0) s.wait(&ctl->pv_done[(g - 1) & 1], (uint32_t)((g - 1) >> 1) & 1);
-      s.wait(&ctl->v_full[st], ph);
       // This key's 64 rows: the P half of CTA `half`, rows of 128 bytes in 16-byte
-      // pieces, piece j of key k at j ^ (k & 7).
+      // pieces, piece j of key k at j ^ (k & 7). Rows for the other CTA wait here
+      // for a bulk copy: 64 keys in the stage's rope slot, which S is done with,
+      // 64 behind P; both are free again once PV of this tile is done.
       const int key = (int)rank * 128 + tl;
-      const uint32_t row = tc::map_rank(smem + kOffP + key * kPRow, (uint32_t)s.half);
+      const bool away = s.half != (int)rank;
+      uint8_t* put = smem + (!away ? kOffP + key * kPRow
+                             : tl < 64 ? st * kStageBytes + 4 * kChunkBytes + tl * kPRow
+                                       : kOffStage + (tl - 64) * kPRow);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        tc::remote_st(row + ((j ^ (key & 7)) << 4),
-                      make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]));
-        tc::remote_st(row + (((4 + j) ^ (key & 7)) << 4),
-                      make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]));
+        *reinterpret_cast<uint4*>(put + ((j ^ (key & 7)) << 4)) =
+            make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
+        *reinterpret_cast<uint4*>(put + (((4 + j) ^ (key & 7)) << 4)) =
+            make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]);
       }
       // Keys past the end: their V must be finite (0), in both halves' slots.
       if (key0 + kKeys > w.len) {
+        s.wait(&ctl->v_full[st], ph);
 #pragma unroll
         for (int kh = 0; kh < 2; ++kh)
           if (key0 + kh * 128 + tl >= w.len) {
@@ -587,9 +625,19 @@ __device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
             for (int u = 0; u < 8; ++u) v[u] = make_uint4(0, 0, 0, 0);
           }
       }
-      tc::fence_proxy_async();
+      tc::fence_proxy_async_smem();
       tc::fence_before_sync();
-      s.arrive(&ctl->p_full, 0);
+      __syncwarp();
+      if (s.lane == 0) {
+        if (away)                                  // this warp's 32 keys
+          tc::bulk_copy_to(tc::map_rank(smem + kOffP + key * kPRow, 1 - rank), put, 32 * kPRow,
+                           tc::map_rank(&ctl->p_full, 1 - rank));
+        // One warp also announces what the other CTA's 128 keys bring.
+        if (s.gt == 0)
+          tc::mbar_arrive_expect_tx(&ctl->p_full, 128 * kPRow);
+        else
+          tc::mbar_arrive(&ctl->p_full);
+      }
     }
     // Row sums over both CTAs' keys, 1 / l and the LSE, then this CTA's dims.
 #pragma unroll
@@ -646,13 +694,13 @@ wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
       tc::mbar_init(&ctl->k_peer[b], 1);
       tc::mbar_init(&ctl->v_full[b], 1);
       tc::mbar_init(&ctl->s_full[b], 1);
-      tc::mbar_init(&ctl->s_empty[b], 2 * kSoft / 32);
       tc::mbar_init(&ctl->pv_done[b], 1);
       tc::mbar_init(&ctl->vote_bar[b], 1);
-      tc::mbar_init(&ctl->swap_bar[b], kRows / 32);
+      tc::mbar_init(&ctl->swap_bar[b], 1);
       ctl->vote[b] = 0;
     }
-    tc::mbar_init(&ctl->p_full, 2 * kSoft / 32);
+    tc::mbar_init(&ctl->p_full, kSoft / 32);
+    tc::mbar_init(&ctl->p_peer, 1);
     tc::mbar_init(&ctl->q_full, 1);
     tc::mbar_init(&ctl->q_peer, 1);
     tc::mbar_init(&ctl->q_empty, 1);
@@ -695,6 +743,9 @@ wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
   }
   tc::fence_before_sync();
   __syncthreads();
+  if (ctl->abort_flag)     // let stores in flight to the other CTA land before it may leave
+    for (const unsigned long long t0 = tc::globaltimer_ns(); tc::globaltimer_ns() - t0 < 100000;) {
+    }
   tc::cluster_sync();      // no CTA leaves while the other's MMAs or stores may reach it
   tc::fence_after_sync();
   if (warp == 1) tc::tmem_dealloc_pair(tmem, kTmemCols);
