@@ -48,8 +48,8 @@ using dec::kStageBytes;
 
 constexpr int kRows = kWideRows;              // query rows per block: the MMA's N
 constexpr int kKeys = kWideKeys;              // keys per tile, half of them per CTA
-// Four warpgroups: the TMA warp, the MMA (or relay) warp and two idle ones; four
-// scout warps; two groups of softmax warps. The softmax threads hold 64 row
+// Four warpgroups: two TMA warps and two MMA (or relay) warps; four scout warps;
+// two groups of softmax warps. The softmax threads hold 64 row
 // sums and 32 words of codes: registers move to them from the others (the
 // launch's 4 x 128 a thread: 64 + 64 + 2 x 192).
 constexpr int kScout = 128;                   // scouts: a key and all 128 rows each
@@ -75,20 +75,21 @@ constexpr uint32_t kIdescLo = kIdescHi | (1u << 10);      // B in E5M2
 static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms need 1 KB alignment");
 
 struct WideCtl {
-  uint64_t k_full[2];      // TMA -> MMA (rank 0), relay (rank 1): own keys landed
-  uint64_t k_peer[2];      // rank 0: the other CTA's keys landed
-  uint64_t v_full[2];      // TMA -> MMA, relay: the other CTA's keys of the own dims landed
+  uint64_t k_full[2];      // rank 0: TMA of both CTAs -> S: both CTAs' keys landed
+  uint64_t v_full[2];      // TMA -> PV, relay: the other CTA's keys of the own dims landed
   uint64_t s_full[2];      // MMA -> softmax, scouts, TMA: S of a tile done
-  uint64_t p_own;          // softmax -> MMA, relay: P of the own keys written or under way
-  uint64_t p_in;           // softmax of the other CTA -> MMA, relay: P of its keys landed
-  uint64_t p_peer[2];      // rank 0: P of CTA i's keys (and V for it) complete in rank 1
+  uint64_t p_own;          // rank 0: softmax -> PV: P of CTA 0's keys written or under way
+  uint64_t p_in;           // bulk copies of the other CTA -> PV, relay: P of its keys landed
+  uint64_t p_peer[2];      // rank 0: P of CTA 0's keys (and V for it) complete in rank 1; its
+                           // softmax: P of CTA 1's keys written or under way
   uint64_t pv_half[2];     // MMA -> softmax of rank 0, TMA: O holds CTA 0's keys of the tile
   uint64_t pv_done[2];     // MMA -> softmax, TMA: O holds the tile; P and the stage are free
-  uint64_t q_full, q_peer, q_empty;
+  uint64_t q_full;         // rank 0: TMA of both CTAs -> S
+  uint64_t q_empty;        // MMA -> TMA
   uint64_t vote_bar[2];    // the other CTA's flag is in vote_peer
   uint64_t told[2];        // scouts -> softmax: verdict
   uint64_t swap_bar[2];    // the other CTA's row values are in swap
-  uint64_t drain;
+  uint64_t drain[2];
   uint32_t vote_peer[2];
   uint32_t vote[2];        // bits of this CTA's scouts: kMoved, kFailed
   uint32_t verdict[2];     // of the pair's scouts
@@ -144,324 +145,234 @@ __device__ __forceinline__ uint32_t peek(const uint32_t* p) {
   return *reinterpret_cast<const volatile uint32_t*>(p);
 }
 
-// ---------------------------------------------------------------- producer
-// One warp; lane l < 4 holds the id of page l of a tile. Three kinds of load,
-// each issued as soon as what it overwrites is free.
-__device__ void producer(const WideArgs& a, const WidePart& w, uint8_t* smem, WideCtl* ctl,
-                         uint32_t rank, const CUtensorMap* tm_kv, const CUtensorMap* tm_kvr,
-                         const CUtensorMap* tm_q, const CUtensorMap* tm_qr) {
-  const int lane = threadIdx.x & 31;
-  const long long n = w.end - w.begin;             // tiles of this pair
-  const int pages_all = (int)cdiv(w.len, kPage);
-  int tile = (int)(w.begin % w.tiles);             // within its block, of the next page_ids()
-  int block = (int)(w.begin / w.tiles);            // of the next Q
-  auto page_ids = [&]() {                          // lane l: page l of the next tile
+// ---------------------------------------------------------------- loads
+// The page ids of a tile, in lanes 0-3 of a warp: asked for a tile ahead, checked
+// when used.
+struct Pages {
+  const WideArgs& a;
+  int tile, tiles, all, lane;                      // tile: within its block, the next one to ask for
+  int next;
+  bool report;
+  __device__ Pages(const WideArgs& a_, const WidePart& w, bool report_)
+      : a(a_), tile((int)(w.begin % w.tiles)), tiles(w.tiles), all((int)cdiv(w.len, kPage)),
+        lane(threadIdx.x & 31), report(report_) {
+    next = ask();
+  }
+  __device__ int ask() {
     const int p = tile * (kKeys / kPage) + lane;
-    if (++tile == w.tiles) tile = 0;
-    return lane < kKeys / kPage && p < pages_all ? a.prefix_table[p] : -1;
-  };
-  // Next tile: own keys' bands 0-1, their bands 2-3 and rope, other keys' values.
-  long long nk = 0, nk2 = 0, nv = 0;
-  long long q_at = 0, q_step = w.tiles - tile;     // first tile of the next block
+    if (++tile == tiles) tile = 0;
+    return lane < kKeys / kPage && p < all ? a.prefix_table[p] : -2;      // -2: no such page
+  }
+  __device__ int take(bool more) {
+    int cur = next;
+    next = more ? ask() : -2;
+    if (cur != -2 && (cur < 0 || cur >= a.num_pages)) {
+      if (report && a.status) atomicOr(a.status, MLA_FAULT_PAGE_RANGE);
+      cur = -1;
+    }
+    return cur;
+  }
+};
+
+// Own keys (and Q at each block's start), counted on rank 0's barriers. A
+// stage's bands 0-1 hold V of CTA 0's keys, which PV is done with first, bands
+// 2-3 that of CTA 1's; the rope's place holds P on its way until the end.
+__device__ void load_keys(const WideArgs& a, const WidePart& w, uint8_t* smem, WideCtl* ctl,
+                          uint32_t rank, const CUtensorMap* tm_kv, const CUtensorMap* tm_kvr,
+                          const CUtensorMap* tm_q, const CUtensorMap* tm_qr) {
+  const int lane = threadIdx.x & 31;
+  const long long n = w.end - w.begin;
+  Pages pages(a, w, true);
+  int block = (int)(w.begin / w.tiles), tile = (int)(w.begin % w.tiles);
+  const uint32_t q_bar = tc::map_rank(&ctl->q_full, 0);
   uint32_t x = 0;                                  // blocks whose Q was requested
-  int ids[2] = {-1, -1}, next = page_ids();
-  unsigned long long t0 = 0;
   bool ok = true;
-  while (nv < n) {
-    uint32_t can = 0;                              // lane 0 looks, all lanes act
+  for (long long i = 0; ok && i < n; ++i) {
+    const int st = i & 1;
+    const uint32_t ph = (uint32_t)((i >> 1) - 1) & 1;
+    const int cur = pages.take(i + 1 < n);
+    const int p0 = __shfl_sync(0xffffffffu, cur, 2 * rank);
+    const int p1 = __shfl_sync(0xffffffffu, cur, 2 * rank + 1);
     if (lane == 0) {
-      if (q_at <= nk && q_at < n && (x == 0 || tc::mbar_test_wait(&ctl->q_empty, (x - 1) & 1)))
-        can |= 1;
-      // A stage's bands 0-1 hold V of CTA 0's keys, which PV is done with first;
-      // bands 2-3 that of CTA 1's. The rope's place holds P until the end.
-      if (nk < n && nk <= nk2 + 1 && nk < nv + 2 &&
-          (nk < 2 || tc::mbar_test_wait(&ctl->pv_half[nk & 1], (uint32_t)((nk >> 1) - 1) & 1)))
-        can |= 2;
-      if (nv < nk2 && tc::mbar_test_wait(&ctl->s_full[nv & 1], (uint32_t)(nv >> 1) & 1)) can |= 4;
-      if (nk2 < nk &&
-          (nk2 < 2 || tc::mbar_test_wait(&ctl->pv_done[nk2 & 1], (uint32_t)((nk2 >> 1) - 1) & 1)))
-        can |= 8;
-    }
-    can = __shfl_sync(0xffffffffu, can, 0);
-    if (can & 1) {
-      if (lane == 0) {
-        uint8_t* q = smem + kOffQ;
-        const int row = block * kRows + (int)rank * 64;
-        tc::mbar_arrive_expect_tx(&ctl->q_full, kQBytes);
-        for (int c = 0; c < 4; ++c)
-          tc::tma_load_2d(q + c * kQChunk, tm_q, &ctl->q_full, c * 128, row);
-        tc::tma_load_2d(q + 4 * kQChunk, tm_qr, &ctl->q_full, 512, row);
+      const uint32_t bar = tc::map_rank(&ctl->k_full[st], 0);
+      uint8_t* stage = smem + st * kStageBytes;
+      if (i >= 2) ok = w_wait(&ctl->pv_half[st], ph, ctl, a.status);
+      if (ok) {
+        tc::remote_arrive_expect_tx(bar, ((p0 >= 0) + (p1 >= 0)) * dec::kPageBytes);
+        for (int h = 0; h < 2; ++h)
+          for (int c = 0; c < 2; ++c)
+            if ((h ? p1 : p0) >= 0)
+              tc::tma_load_2d_pair(stage + c * kChunkBytes + h * (kChunkBytes / 2), tm_kv, bar,
+                                   c * 128, (h ? p1 : p0) * kPage);
       }
-      q_at += q_step;
-      q_step = w.tiles;
-      ++block;
-      ++x;
-    }
-    if (can & 8) {
-      const int st = nk2 & 1, cur = st ? ids[1] : ids[0];
-      const int p0 = __shfl_sync(0xffffffffu, cur, 2 * rank);
-      const int p1 = __shfl_sync(0xffffffffu, cur, 2 * rank + 1);
-      if (lane == 0) {
-        uint8_t* stage = smem + st * kStageBytes;
+      if (ok && (i == 0 || tile == 0)) {           // a new block
+        if (x > 0) ok = w_wait(&ctl->q_empty, (x - 1) & 1, ctl, a.status);
+        if (ok) {
+          uint8_t* q = smem + kOffQ;
+          const int row = block * kRows + (int)rank * 64;
+          tc::remote_arrive_expect_tx(q_bar, kQBytes);
+          for (int c = 0; c < 4; ++c)
+            tc::tma_load_2d_pair(q + c * kQChunk, tm_q, q_bar, c * 128, row);
+          tc::tma_load_2d_pair(q + 4 * kQChunk, tm_qr, q_bar, 512, row);
+        }
+        ++block;
+        ++x;
+      }
+      if (ok && i >= 2) ok = w_wait(&ctl->pv_done[st], ph, ctl, a.status);
+      if (ok) {
         for (int h = 0; h < 2; ++h) {
           const int id = h ? p1 : p0;
           if (id < 0) continue;
           for (int c = 2; c < 4; ++c)
-            tc::tma_load_2d(stage + c * kChunkBytes + h * (kChunkBytes / 2), tm_kv,
-                            &ctl->k_full[st], c * 128, id * kPage);
-          tc::tma_load_2d(stage + 4 * kChunkBytes + h * (kRopeBytes / 2), tm_kvr, &ctl->k_full[st],
-                          512, id * kPage);
+            tc::tma_load_2d_pair(stage + c * kChunkBytes + h * (kChunkBytes / 2), tm_kv, bar,
+                                 c * 128, id * kPage);
+          tc::tma_load_2d_pair(stage + 4 * kChunkBytes + h * (kRopeBytes / 2), tm_kvr, bar, 512,
+                               id * kPage);
         }
       }
-      ++nk2;
     }
-    if (can & 4) {
-      const int st = nv & 1, cur = st ? ids[1] : ids[0];
-      const uint32_t other = 1 - rank;
-      const int p0 = __shfl_sync(0xffffffffu, cur, 2 * other);
-      const int p1 = __shfl_sync(0xffffffffu, cur, 2 * other + 1);
-      if (lane == 0) {
-        uint8_t* stage = smem + st * kStageBytes;
-        tc::mbar_arrive_expect_tx(&ctl->v_full[st], ((p0 >= 0) + (p1 >= 0)) * 2 * kPage * 128);
-        for (int h = 0; h < 2; ++h) {
-          const int id = h ? p1 : p0;
-          if (id < 0) continue;
-          for (int i = 0; i < 2; ++i)              // own dims of the other CTA's keys
-            tc::tma_load_2d(stage + (2 * other + i) * kChunkBytes + h * (kChunkBytes / 2), tm_kv,
-                            &ctl->v_full[st], (2 * rank + i) * 128, id * kPage);
-        }
-      }
-      ++nv;
-    }
-    if (can & 2) {
-      const int st = nk & 1;
-      int cur = next;
-      if (cur >= a.num_pages || (cur < 0 && lane < kKeys / kPage &&
-                                 ((tile ? tile : w.tiles) - 1) * (kKeys / kPage) + lane < pages_all)) {
-        if (a.status) atomicOr(a.status, MLA_FAULT_PAGE_RANGE);
-        cur = -1;
-      }
-      if (st) ids[1] = cur; else ids[0] = cur;
-      const int p0 = __shfl_sync(0xffffffffu, cur, 2 * rank);
-      const int p1 = __shfl_sync(0xffffffffu, cur, 2 * rank + 1);
-      if (lane == 0) {
-        uint8_t* stage = smem + st * kStageBytes;
-        tc::mbar_arrive_expect_tx(&ctl->k_full[st], ((p0 >= 0) + (p1 >= 0)) * dec::kPageBytes);
-        for (int h = 0; h < 2; ++h) {
-          const int id = h ? p1 : p0;
-          if (id < 0) continue;
-          for (int c = 0; c < 2; ++c)
-            tc::tma_load_2d(stage + c * kChunkBytes + h * (kChunkBytes / 2), tm_kv,
-                            &ctl->k_full[st], c * 128, id * kPage);
-        }
-      }
-      next = nk + 1 < n ? page_ids() : -1;         // in flight until the next tile
-      ++nk;
-    }
-    if (can) {
-      t0 = 0;
-      continue;
-    }
-    const unsigned long long now = tc::globaltimer_ns();
-    if (t0 == 0) t0 = now;
-    bool stop = false;
-    if (lane == 0) {
-      const bool expired = now - t0 > kTimeoutNs;
-      if (expired) {
-        *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
-        if (a.status) atomicOr(a.status, MLA_FAULT_WAIT_TIMEOUT);
-      }
-      stop = *reinterpret_cast<volatile int*>(&ctl->abort_flag) != 0;
-    }
-    if (__shfl_sync(0xffffffffu, (int)stop, 0)) {
-      ok = false;
-      break;
-    }
-  }
-  if (lane == 0 && !ok) {                          // never leave with copies in flight
-    const unsigned long long t1 = tc::globaltimer_ns();
-    auto drain = [&](uint64_t* bar, uint32_t parity) {
-      while (!tc::mbar_try_wait(bar, parity) && tc::globaltimer_ns() - t1 < kTimeoutNs) {
-      }
-    };
-    // A tile whose second part was never requested does not complete: its first
-    // part has landed well before the wait below gives up.
-    for (long long i = nk2 < 2 ? 0 : nk2 - 2; i < nk; ++i)
-      drain(&ctl->k_full[i & 1], (uint32_t)(i >> 1) & 1);
-    for (long long i = nv < 2 ? 0 : nv - 2; i < nv; ++i)
-      drain(&ctl->v_full[i & 1], (uint32_t)(i >> 1) & 1);
-    if (x > 0) drain(&ctl->q_full, (x - 1) & 1);
+    if (++tile == w.tiles) tile = 0;
+    ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
   }
 }
 
-// ---------------------------------------------------------------- relay (rank 1)
-// Tells rank 0's MMA thread what is complete here.
+// The other CTA's keys of the own value dims, over the bands S is done with.
+__device__ void load_values(const WideArgs& a, const WidePart& w, uint8_t* smem, WideCtl* ctl,
+                            uint32_t rank, const CUtensorMap* tm_kv) {
+  const int lane = threadIdx.x & 31;
+  const long long n = w.end - w.begin;
+  const uint32_t other = 1 - rank;
+  Pages pages(a, w, false);
+  bool ok = true;
+  for (long long i = 0; ok && i < n; ++i) {
+    const int st = i & 1;
+    const int cur = pages.take(i + 1 < n);
+    const int p0 = __shfl_sync(0xffffffffu, cur, 2 * other);
+    const int p1 = __shfl_sync(0xffffffffu, cur, 2 * other + 1);
+    if (lane == 0 && (ok = w_wait(&ctl->s_full[st], (uint32_t)(i >> 1) & 1, ctl, a.status))) {
+      uint8_t* stage = smem + st * kStageBytes;
+      tc::mbar_arrive_expect_tx(&ctl->v_full[st], ((p0 >= 0) + (p1 >= 0)) * 2 * kPage * 128);
+      for (int h = 0; h < 2; ++h)
+        for (int d = 0; d < 2; ++d)
+          if ((h ? p1 : p0) >= 0)
+            tc::tma_load_2d(stage + (2 * other + d) * kChunkBytes + h * (kChunkBytes / 2), tm_kv,
+                            &ctl->v_full[st], (2 * rank + d) * 128, (h ? p1 : p0) * kPage);
+    }
+    ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+  }
+}
+
+// Rank 1: tells rank 0's PV issuer that P of CTA 0's keys and V for it are here.
 __device__ void relay(const WideArgs& a, const WidePart& w, WideCtl* ctl) {
   const long long n = w.end - w.begin;
-  long long nk = 0, np0 = 0, np1 = 0;              // next tile: keys, P of CTA 0's and CTA 1's keys
-  uint32_t x = 0;
-  unsigned long long t0 = 0;
-  int tile = (int)(w.begin % w.tiles);             // of the next keys, within its block
-  tc::mbar_arrive_expect_tx(&ctl->p_in, 128 * kPRow);
-  while (np0 < n || np1 < n) {
-    bool progress = false;
-    if (np0 < nk && tc::mbar_test_wait(&ctl->p_in, (uint32_t)np0 & 1) &&
-        tc::mbar_test_wait(&ctl->v_full[np0 & 1], (uint32_t)(np0 >> 1) & 1)) {
-      tc::remote_arrive(tc::map_rank(&ctl->p_peer[0], 0));
-      if (++np0 < n) tc::mbar_arrive_expect_tx(&ctl->p_in, 128 * kPRow);
-      progress = true;
-    }
-    if (np1 < nk && tc::mbar_test_wait(&ctl->p_own, (uint32_t)np1 & 1)) {
-      tc::remote_arrive(tc::map_rank(&ctl->p_peer[1], 0));
-      ++np1;
-      progress = true;
-    }
-    if (nk < n && nk <= np1 + 1 && tc::mbar_test_wait(&ctl->k_full[nk & 1], (uint32_t)(nk >> 1) & 1)) {
-      bool q = true;
-      if (nk == 0 || tile == 0) {
-        q = tc::mbar_test_wait(&ctl->q_full, x & 1);
-        if (q) {
-          tc::remote_arrive(tc::map_rank(&ctl->q_peer, 0));
-          ++x;
-        }
-      }
-      if (q) {
-        tc::remote_arrive(tc::map_rank(&ctl->k_peer[nk & 1], 0));
-        if (++tile == w.tiles) tile = 0;
-        ++nk;
-        progress = true;
-      }
-    }
-    if (progress) {
-      t0 = 0;
-      continue;
-    }
-    const unsigned long long now = tc::globaltimer_ns();
-    if (t0 == 0) t0 = now;
-    const bool expired = now - t0 > kTimeoutNs;
-    if (*reinterpret_cast<volatile int*>(&ctl->abort_flag) || expired) {
-      *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
-      if (expired && a.status) atomicOr(a.status, MLA_FAULT_WAIT_TIMEOUT);
+  const uint32_t to = tc::map_rank(&ctl->p_peer[0], 0);
+  for (long long i = 0; i < n; ++i) {
+    tc::mbar_arrive_expect_tx(&ctl->p_in, 128 * kPRow);
+    if (!w_wait(&ctl->v_full[i & 1], (uint32_t)(i >> 1) & 1, ctl, a.status) ||
+        !w_wait(&ctl->p_in, (uint32_t)i & 1, ctl, a.status))
       return;
-    }
+    tc::remote_arrive(to);
   }
 }
 
-// ---------------------------------------------------------------- MMA issuer (rank 0)
-__device__ void mma_issuer(const WideArgs& a, const WidePart& w, uint8_t* smem, WideCtl* ctl,
-                           uint32_t tmem) {
+// ---------------------------------------------------------------- MMAs (rank 0)
+// S and PV are issued by a thread each: neither waits on the other's inputs.
+__device__ __forceinline__ void mma_drain(uint64_t* bar) {
+  tc::mma_commit_pair(bar);                        // every MMA done before TMEM is released
+  const unsigned long long t0 = tc::globaltimer_ns();
+  while (!tc::mbar_try_wait(bar, 0) && tc::globaltimer_ns() - t0 < kTimeoutNs) {
+  }
+}
+
+__device__ void issue_s(const WideArgs& a, const WidePart& w, uint8_t* smem, WideCtl* ctl,
+                        uint32_t tmem) {
   const uint32_t s_kv = tc::smem_u32(smem), s_q = tc::smem_u32(smem + kOffQ);
-  const uint32_t s_p = tc::smem_u32(smem + kOffP);
   const long long n = w.end - w.begin;
-  long long ns = 0, block_end = 0;                 // next S; tile at which the next block begins
-  long long npv = 0;                               // next PV: half tiles, CTA 0's keys first
-  int pv_tile = (int)(w.begin % w.tiles);          // PV's tile within its block
-  bool pv_first = true;                            // the pair's first of the block
-  uint32_t votes = 0;                              // verdicts the scouts gave before it
+  int tile = (int)(w.begin % w.tiles);
   uint32_t x = 0;
-  bool q_ready = false;
-  unsigned long long t0 = 0;
-  tc::mbar_arrive_expect_tx(&ctl->p_in, 128 * kPRow);
-  while (npv < 2 * n) {
-    bool progress = false;
-    const long long tp = npv >> 1;
-    const int kh = (int)(npv & 1);
-    const uint32_t pp = (uint32_t)tp & 1;
-    if (tp < ns) {
-      // P of CTA kh's keys and V for it, in both CTAs. The first half waits for
-      // CTA 1's softmax too (and with it the second half's P) where that touches
-      // what the half writes or reads: O (read out before a block's first tile,
-      // scaled where the maxima moved) or V (keys past a block's end are cleared).
-      bool ready = tc::mbar_test_wait(&ctl->p_peer[kh], pp);
-      if (kh == 0) {
-        ready = ready && tc::mbar_test_wait(&ctl->p_own, pp);
-        if (ready && (pv_first || pv_tile == w.tiles - 1 || (peek(&ctl->verdict[votes & 1]) & kMoved)))
-          ready = tc::mbar_test_wait(&ctl->p_peer[1], pp) && tc::mbar_test_wait(&ctl->p_in, pp) &&
-                  tc::mbar_test_wait(&ctl->v_full[tp & 1], (uint32_t)(tp >> 1) & 1);
-      } else {
-        ready = ready && tc::mbar_test_wait(&ctl->p_in, pp) &&
-                tc::mbar_test_wait(&ctl->v_full[tp & 1], (uint32_t)(tp >> 1) & 1);
-      }
-      if (ready) {
-        tc::fence_after_sync();
-        const uint32_t kv = s_kv + (tp & 1) * kStageBytes;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t va = tc::smem_desc(kv + (kh * 2 + i) * kChunkBytes + kk * 32 * 128,
-                                              kChunkBytes, 1024, tc::kSw128);
-            const uint32_t pk = s_p + (kh * 128 + kk * 32) * kPRow;
-            tc::mma_f8_pair(tmem + i * kRows, va, tc::smem_desc(pk, kPBytes, 1024, tc::kSw128),
-                            kIdescHi, !(pv_first && kh == 0 && kk == 0));
-            tc::mma_f8_pair(tmem + i * kRows, va, tc::smem_desc(pk + 64, kPBytes, 1024, tc::kSw128),
-                            kIdescLo, true);
-          }
-        tc::mma_commit_pair(kh == 0 ? &ctl->pv_half[tp & 1] : &ctl->pv_done[tp & 1]);
-        if (kh == 1) {
-          if (tp + 1 < n) tc::mbar_arrive_expect_tx(&ctl->p_in, 128 * kPRow);
-          if (!pv_first) ++votes;
-          if (++pv_tile == w.tiles) pv_tile = 0;
-          pv_first = pv_tile == 0;
-        }
-        ++npv;
-        progress = true;
-      }
+  for (long long i = 0; i < n; ++i) {
+    const int st = i & 1;
+    if (i == 0 || tile == 0) {                     // a new block: its Q in both CTAs
+      if (!w_wait(&ctl->q_full, x & 1, ctl, a.status)) break;
+      ++x;
     }
-    if (ns < n && ns <= (npv >> 1) + 1) {
-      const int st = ns & 1;
-      const uint32_t ph = (uint32_t)(ns >> 1) & 1;
-      if (ns == block_end) {                       // a new block: its Q in both CTAs
-        if (!q_ready)
-          q_ready = tc::mbar_test_wait(&ctl->q_full, x & 1) &&
-                    tc::mbar_test_wait(&ctl->q_peer, x & 1);
-      }
-      if ((ns != block_end || q_ready) && tc::mbar_test_wait(&ctl->k_full[st], ph) &&
-          tc::mbar_test_wait(&ctl->k_peer[st], ph)) {
-        // The S buffer of tile ns - 2 is free: its stage was refilled after its
-        // PV, whose P the softmax wrote after it had read that S.
-        tc::fence_after_sync();
-        if (ns == block_end) {
-          block_end += w.tiles - (w.begin + ns) % w.tiles;
-          q_ready = false;
-          ++x;
-        }
-        const uint32_t kv = s_kv + st * kStageBytes, d = tmem + kSCol + st * kRows;
+    // The S buffer of tile i - 2 is free: its stage was refilled after its PV,
+    // whose P the softmax wrote after it (and the scouts) had read that S.
+    if (!w_wait(&ctl->k_full[st], (uint32_t)(i >> 1) & 1, ctl, a.status)) break;
+    tc::fence_after_sync();
+    const uint32_t kv = s_kv + st * kStageBytes, d = tmem + kSCol + st * kRows;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+    for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc::mma_f8_pair(d, tc::smem_desc(kv + c * kChunkBytes + kk * 32, 16, 1024, tc::kSw128),
-                            tc::smem_desc(s_q + c * kQChunk + kk * 32, 16, 1024, tc::kSw128),
-                            kIdescS, (c | kk) != 0);
+      for (int kk = 0; kk < 4; ++kk)
+        tc::mma_f8_pair(d, tc::smem_desc(kv + c * kChunkBytes + kk * 32, 16, 1024, tc::kSw128),
+                        tc::smem_desc(s_q + c * kQChunk + kk * 32, 16, 1024, tc::kSw128), kIdescS,
+                        (c | kk) != 0);
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
-          tc::mma_f8_pair(d, tc::smem_desc(kv + 4 * kChunkBytes + kk * 32, 16, 512, tc::kSw64),
-                          tc::smem_desc(s_q + 4 * kQChunk + kk * 32, 16, 512, tc::kSw64), kIdescS,
-                          true);
-        tc::mma_commit_pair(&ctl->s_full[st]);
-        ++ns;
-        if (ns == block_end || ns == n) tc::mma_commit_pair(&ctl->q_empty);
-        progress = true;
-      }
-    }
-    if (progress) {
-      t0 = 0;
-    } else {
-      const unsigned long long now = tc::globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      const bool expired = now - t0 > kTimeoutNs;
-      if (*reinterpret_cast<volatile int*>(&ctl->abort_flag) || expired) {
-        *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
-        if (expired && a.status) atomicOr(a.status, MLA_FAULT_WAIT_TIMEOUT);
-        break;
-      }
-    }
+    for (int kk = 0; kk < 2; ++kk)
+      tc::mma_f8_pair(d, tc::smem_desc(kv + 4 * kChunkBytes + kk * 32, 16, 512, tc::kSw64),
+                      tc::smem_desc(s_q + 4 * kQChunk + kk * 32, 16, 512, tc::kSw64), kIdescS, true);
+    tc::mma_commit_pair(&ctl->s_full[st]);
+    if (++tile == w.tiles) tile = 0;
+    if (tile == 0) tc::mma_commit_pair(&ctl->q_empty);
   }
-  tc::mma_commit_pair(&ctl->drain);                // every MMA done before TMEM is released
-  const unsigned long long t1 = tc::globaltimer_ns();
-  while (!tc::mbar_try_wait(&ctl->drain, 0) && tc::globaltimer_ns() - t1 < kTimeoutNs) {
+  mma_drain(&ctl->drain[0]);
+}
+
+__device__ void issue_pv(const WideArgs& a, const WidePart& w, uint8_t* smem, WideCtl* ctl,
+                         uint32_t tmem) {
+  const uint32_t s_kv = tc::smem_u32(smem), s_p = tc::smem_u32(smem + kOffP);
+  const long long n = w.end - w.begin;
+  int tile = (int)(w.begin % w.tiles);
+  bool first = true;                               // the pair's first tile of the block
+  uint32_t votes = 0;                              // verdicts the scouts gave before it
+  bool ok = true;
+  for (long long i = 0; ok && i < n; ++i) {
+    const int st = i & 1;
+    const uint32_t pp = (uint32_t)i & 1, ph = (uint32_t)(i >> 1) & 1;
+    tc::mbar_arrive_expect_tx(&ctl->p_in, 128 * kPRow);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      ok = ok && w_wait(bar, parity, ctl, a.status);
+    };
+    auto half = [&](int kh, bool fresh) {
+      tc::fence_after_sync();
+      const uint32_t kv = s_kv + st * kStageBytes;
+#pragma unroll
+      for (int d = 0; d < 2; ++d)
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t va = tc::smem_desc(kv + (kh * 2 + d) * kChunkBytes + kk * 32 * 128,
+                                            kChunkBytes, 1024, tc::kSw128);
+          const uint32_t pk = s_p + (kh * 128 + kk * 32) * kPRow;
+          tc::mma_f8_pair(tmem + d * kRows, va, tc::smem_desc(pk, kPBytes, 1024, tc::kSw128), kIdescHi,
+                          !(fresh && kk == 0));
+          tc::mma_f8_pair(tmem + d * kRows, va, tc::smem_desc(pk + 64, kPBytes, 1024, tc::kSw128),
+                          kIdescLo, true);
+        }
+    };
+    // P of CTA 0's keys and V for it, in both CTAs. The first half waits for CTA
+    // 1's softmax too (and with it the second half's P) where that touches what
+    // the half writes or reads: O (read out before a block's first tile, scaled
+    // where the maxima moved) or V (keys past a block's end are cleared).
+    wait(&ctl->p_own, pp);
+    wait(&ctl->p_peer[0], pp);
+    const bool both =
+        first || tile == w.tiles - 1 || (ok && (peek(&ctl->verdict[votes & 1]) & kMoved));
+    if (both) wait(&ctl->p_peer[1], pp);
+    if (!ok) break;
+    half(0, first);
+    tc::mma_commit_pair(&ctl->pv_half[st]);
+    wait(&ctl->v_full[st], ph);
+    wait(&ctl->p_in, pp);
+    if (!both) wait(&ctl->p_peer[1], pp);
+    if (!ok) break;
+    half(1, false);
+    tc::mma_commit_pair(&ctl->pv_done[st]);
+    if (!first) ++votes;
+    if (++tile == w.tiles) tile = 0;
+    first = tile == 0;
   }
+  mma_drain(&ctl->drain[1]);
 }
 
 // ---------------------------------------------------------------- scouts
@@ -779,7 +690,10 @@ __device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
         if (away)                                  // this warp's 32 keys
           tc::bulk_copy_to(tc::map_rank(smem + kOffP + key * kPRow, 1 - rank), put, 32 * kPRow,
                            tc::map_rank(&ctl->p_in, 1 - rank));
-        tc::mbar_arrive(&ctl->p_own);
+        if (rank == 0)
+          tc::mbar_arrive(&ctl->p_own);
+        else
+          tc::remote_arrive(tc::map_rank(&ctl->p_peer[1], 0));
       }
     }
     // Row sums over both CTAs' keys, 1 / l and the LSE, then this CTA's dims.
@@ -835,26 +749,25 @@ wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
   const uint32_t rank = tc::cluster_rank();
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
-      tc::mbar_init(&ctl->k_full[b], 1);
-      tc::mbar_init(&ctl->k_peer[b], 1);
+      tc::mbar_init(&ctl->k_full[b], 2);
       tc::mbar_init(&ctl->v_full[b], 1);
       tc::mbar_init(&ctl->s_full[b], 1);
-      tc::mbar_init(&ctl->p_peer[b], 1);
       tc::mbar_init(&ctl->pv_half[b], 1);
       tc::mbar_init(&ctl->pv_done[b], 1);
       tc::mbar_init(&ctl->vote_bar[b], 1);
       tc::mbar_init(&ctl->told[b], 1);
       tc::mbar_init(&ctl->swap_bar[b], 1);
+      tc::mbar_init(&ctl->drain[b], 1);
       ctl->vote[b] = 0;
       ctl->soft_word[b] = 0;
     }
     tc::mbar_init(&ctl->p_own, kSoft / 32);
     tc::mbar_init(&ctl->p_in, 1);
     ctl->moves = 0;
-    tc::mbar_init(&ctl->q_full, 1);
-    tc::mbar_init(&ctl->q_peer, 1);
+    tc::mbar_init(&ctl->p_peer[0], 1);
+    tc::mbar_init(&ctl->p_peer[1], kSoft / 32);
+    tc::mbar_init(&ctl->q_full, 2);
     tc::mbar_init(&ctl->q_empty, 1);
-    tc::mbar_init(&ctl->drain, 1);
     ctl->abort_flag = 0;
     tc::fence_barrier_init();
   }
@@ -882,11 +795,15 @@ wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
   } else if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     if (warp == 0) {
-      producer(a, w, smem, ctl, rank, &tm_kv, &tm_kvr, &tm_q, &tm_qr);
-    } else if (warp == 1 && lane == 0) {
-      if (rank == 0)
-        mma_issuer(a, w, smem, ctl, tmem);
-      else
+      load_keys(a, w, smem, ctl, rank, &tm_kv, &tm_kvr, &tm_q, &tm_qr);
+    } else if (warp == 3) {
+      load_values(a, w, smem, ctl, rank, &tm_kv);
+    } else if (lane == 0) {
+      if (rank == 0 && warp == 1)
+        issue_s(a, w, smem, ctl, tmem);
+      else if (rank == 0)
+        issue_pv(a, w, smem, ctl, tmem);
+      else if (warp == 2)
         relay(a, w, ctl);
     }
   } else if (warp < 8) {
@@ -898,8 +815,8 @@ wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (ctl->abort_flag)     // let stores in flight to the other CTA land before it may leave
-    for (const unsigned long long t0 = tc::globaltimer_ns(); tc::globaltimer_ns() - t0 < 100000;) {
+  if (ctl->abort_flag)     // a wait ran out: what is still in flight here or to the other CTA lands
+    for (const unsigned long long t0 = tc::globaltimer_ns(); tc::globaltimer_ns() - t0 < 1000000;) {
     }
   tc::cluster_sync();      // no CTA leaves while the other's MMAs or stores may reach it
   tc::fence_after_sync();
