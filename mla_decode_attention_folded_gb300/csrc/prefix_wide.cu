@@ -48,15 +48,15 @@ using dec::kStageBytes;
 
 constexpr int kRows = kWideRows;              // query rows per block: the MMA's N
 constexpr int kKeys = kWideKeys;              // keys per tile, half of them per CTA
-// Four warpgroups: two TMA warps and two MMA (or relay) warps; four scout warps;
-// two groups of softmax warps. The softmax threads hold 64 row
-// sums and 32 words of codes: registers move to them from the others (the
-// launch's 4 x 128 a thread: 64 + 64 + 2 x 192).
+// Six warpgroups: two TMA warps and two MMA (or relay) warps; four scout warps;
+// four groups of softmax warps. Registers move to the softmax (32 row sums and
+// 16 words of codes a thread) from the others: the launch's 6 x 80 a thread go
+// 56 + 40 + 4 x 96.
 constexpr int kScout = 128;                   // scouts: a key and all 128 rows each
-constexpr int kSoft = 256;                    // softmax threads: a key and 64 rows each
+constexpr int kSoft = 512;                    // softmax threads: a key and 32 rows each
 constexpr int kThreads = 128 + kScout + kSoft;
-constexpr int kRegsIssue = 64, kRegsScout = 64, kRegsSoft = 192;
-static_assert(kRegsIssue + kRegsScout + 2 * kRegsSoft <= 4 * (65536 / kThreads), "register pool");
+constexpr int kRegsIssue = 56, kRegsScout = 40, kRegsSoft = 96;
+static_assert(kRegsIssue + kRegsScout + 4 * kRegsSoft <= 6 * (65536 / kThreads / 8 * 8), "register pool");
 constexpr int kQChunk = 64 * 128;             // this CTA's 64 rows x 128 dims
 constexpr int kQBytes = 64 * kDqk;
 constexpr int kPRow = 128;                    // a key's 64 hi codes, then its 64 lo codes
@@ -94,15 +94,15 @@ struct WideCtl {
   uint32_t vote[2];        // bits of this CTA's scouts: kMoved, kFailed
   uint32_t verdict[2];     // of the pair's scouts
   uint32_t soft_word[2];   // kFailed of softmax threads; kMoved, kFailed of the verdict
-  uint32_t moves;          // how often new maxima came into m_run
+  uint32_t moves;          // how often new maxima came into neg_max
   uint32_t tmem_base;
   int abort_flag;
-  alignas(16) float m_run[kRows];   // running row max (base-2 scores), read four at a time
-  float vec[kRows];        // rescale factors, then 1 / l
+  alignas(16) float neg_max[kRows]; // minus the running row max (base-2 scores), read four at a time
+  alignas(16) float vec[kRows];     // rescale factors, then 1 / l
   float red[4][kRows];
   float swap[2][kRows];
 };
-static_assert(offsetof(WideCtl, m_run) % 16 == 0, "float4 reads");
+static_assert(offsetof(WideCtl, neg_max) % 16 == 0, "16-byte reads");
 constexpr int kSmemBytes = kOffCtl + (int)sizeof(WideCtl) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 constexpr uint32_t kMoved = 1, kFailed = 2;
@@ -403,18 +403,18 @@ __device__ void scout(const WideArgs& a, const WidePart& w, WideCtl* ctl, uint32
     const bool valid = key0 + (int)rank * 128 + tl < w.len;
     float most = -INFINITY;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      uint32_t raw[32];
-      tc::tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + kSCol + st * kRows + c * 32, raw);
+    for (int c = 0; c < kRows; c += 16) {
+      uint32_t raw[16];
+      tc::tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + kSCol + st * kRows + c, raw);
       tc::tmem_wait_ld();
-      const float4* m4 = reinterpret_cast<const float4*>(&ctl->m_run[c * 32]);
+      const float4* m4 = reinterpret_cast<const float4*>(&ctl->neg_max[c]);
 #pragma unroll
-      for (int i = 0; i < 32; i += 4) {
+      for (int i = 0; i < 16; i += 4) {
         const float4 m = m4[i / 4];
-        most = fmaxf(most, fmaf(__uint_as_float(raw[i]), a.bmm1_log2, -m.x));
-        most = fmaxf(most, fmaf(__uint_as_float(raw[i + 1]), a.bmm1_log2, -m.y));
-        most = fmaxf(most, fmaf(__uint_as_float(raw[i + 2]), a.bmm1_log2, -m.z));
-        most = fmaxf(most, fmaf(__uint_as_float(raw[i + 3]), a.bmm1_log2, -m.w));
+        most = fmaxf(most, fmaf(__uint_as_float(raw[i]), a.bmm1_log2, m.x));
+        most = fmaxf(most, fmaf(__uint_as_float(raw[i + 1]), a.bmm1_log2, m.y));
+        most = fmaxf(most, fmaf(__uint_as_float(raw[i + 2]), a.bmm1_log2, m.z));
+        most = fmaxf(most, fmaf(__uint_as_float(raw[i + 3]), a.bmm1_log2, m.w));
       }
     }
     tc::fence_before_sync();
@@ -450,7 +450,7 @@ struct Soft {
   const WideArgs& a;
   WideCtl* ctl;
   uint32_t tmem, rank;
-  int quarter, half, lane, gt;
+  int quarter, part, lane, gt;                     // rows 32 part .. 32 part + 31
   uint32_t swaps = 0, votes = 0, words = 0;
   bool ok = true;                                  // warp-uniform
 
@@ -459,7 +459,7 @@ struct Soft {
     const int warp = threadIdx.x >> 5;
     quarter = warp & 3;
     gt = threadIdx.x - 128 - kScout;
-    half = gt >> 7;
+    part = gt >> 7;
     lane = threadIdx.x & 31;
   }
   __device__ uint32_t lanes() const { return (uint32_t)(quarter * 32) << 16; }
@@ -494,28 +494,31 @@ struct Soft {
     asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
     return r;
   }
-  // P of the tile: codes of this thread's key in 64 rows; lp gathers the row
+  // The weights of two rows of this thread's key.
+  __device__ __forceinline__ void pair(uint64_t raw, uint64_t neg_max, bool valid, float& p0,
+                                       float& p1) const {
+    float d0, d1;
+    unpack_f32x2(fma_f32x2(raw, pack_f32x2(a.bmm1_log2, a.bmm1_log2), neg_max), d0, d1);
+    p0 = valid ? ex2(at_most_9(d0)) : 0.f;
+    p1 = valid ? ex2(at_most_9(d1)) : 0.f;
+  }
+  // P of the tile: codes of this thread's key in its 32 rows; lp gathers the row
   // sums. Scores more than 9 above a row's max count as 9: the scouts' verdict
   // has such a tile done again.
-  __device__ void weigh(int st, bool valid, float (&lp)[64], uint32_t (&hi)[16],
-                        uint32_t (&lo)[16]) const {
-    uint32_t raw[2][32];
-    const uint32_t at = tmem + lanes() + kSCol + st * kRows + half * 64;
-    tc::tmem_ld32(at, raw[0]);
-    tc::tmem_ld32(at + 32, raw[1]);
+  __device__ void weigh(int st, bool valid, uint64_t (&lp)[16], uint32_t (&hi)[8],
+                        uint32_t (&lo)[8]) const {
+    uint32_t raw[32];
+    tc::tmem_ld32(tmem + lanes() + kSCol + st * kRows + part * 32, raw);
     tc::tmem_wait_ld();
-    const float4* m4 = reinterpret_cast<const float4*>(&ctl->m_run[half * 64]);
+    const ulonglong2* m4 = reinterpret_cast<const ulonglong2*>(&ctl->neg_max[part * 32]);
 #pragma unroll
-    for (int i = 0; i < 64; i += 4) {
-      const float4 mm = m4[i / 4];
-      const float m[4] = {mm.x, mm.y, mm.z, mm.w};
+    for (int i = 0; i < 32; i += 4) {
+      const ulonglong2 m = m4[i / 4];
       float p[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float s = __uint_as_float(raw[i >> 5][(i & 31) + u]);
-        p[u] = valid ? ex2(at_most_9(fmaf(s, a.bmm1_log2, -m[u]))) : 0.f;
-        lp[i + u] += p[u];
-      }
+      pair(pack_f32x2(__uint_as_float(raw[i]), __uint_as_float(raw[i + 1])), m.x, valid, p[0], p[1]);
+      pair(pack_f32x2(__uint_as_float(raw[i + 2]), __uint_as_float(raw[i + 3])), m.y, valid, p[2], p[3]);
+      lp[i / 2] = add_f32x2(lp[i / 2], pack_f32x2(p[0], p[1]));
+      lp[i / 2 + 1] = add_f32x2(lp[i / 2 + 1], pack_f32x2(p[2], p[3]));
       const uint32_t h01 = dec::f32x2_to_f16x2(p[0], p[1]), h23 = dec::f32x2_to_f16x2(p[2], p[3]);
       const uint16_t e01 = dec::f16x2_to_e4m3x2(h01), e23 = dec::f16x2_to_e4m3x2(h23);
       const uint16_t l01 = f16x2_to_e5m2x2(dec::f16x2_sub(h01, e4m3x2_to_f16x2(e01)));
@@ -525,45 +528,42 @@ struct Soft {
     }
   }
   // Takes back what weigh added (the same values bit for bit).
-  __device__ void unweigh(int st, bool valid, float (&lp)[64]) const {
+  __device__ void unweigh(int st, bool valid, uint64_t (&lp)[16]) const {
+    uint32_t raw[32];
+    tc::tmem_ld32(tmem + lanes() + kSCol + st * kRows + part * 32, raw);
+    tc::tmem_wait_ld();
+    const uint64_t* m2 = reinterpret_cast<const uint64_t*>(&ctl->neg_max[part * 32]);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      uint32_t raw[32];
-      tc::tmem_ld32(tmem + lanes() + kSCol + st * kRows + half * 64 + c * 32, raw);
-      tc::tmem_wait_ld();
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float d =
-            fmaf(__uint_as_float(raw[i]), a.bmm1_log2, -ctl->m_run[half * 64 + c * 32 + i]);
-        lp[c * 32 + i] -= valid ? ex2(at_most_9(d)) : 0.f;
-      }
+    for (int i = 0; i < 32; i += 2) {
+      float p0, p1;
+      pair(pack_f32x2(__uint_as_float(raw[i]), __uint_as_float(raw[i + 1])), m2[i / 2], valid, p0, p1);
+      lp[i / 2] = add_f32x2(lp[i / 2], pack_f32x2(-p0, -p1));
     }
   }
   // Rows whose max grew by more than 8: the new max, 2 below the tile's, agreed
   // with the other CTA; row sums and O follow. `last`: the pair's previous tile
   // if O holds something of this block, else -1.
-  __device__ void move(int st, bool valid, float (&lp)[64], long long last) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
+  __device__ void move(int st, bool valid, uint64_t (&lp)[16], long long last) {
+    {
       uint32_t raw[32];
       float v[32];
-      tc::tmem_ld32(tmem + lanes() + kSCol + st * kRows + half * 64 + c * 32, raw);
+      tc::tmem_ld32(tmem + lanes() + kSCol + st * kRows + part * 32, raw);
       tc::tmem_wait_ld();
 #pragma unroll
       for (int i = 0; i < 32; ++i)
         v[i] = valid ? __uint_as_float(raw[i]) * a.bmm1_log2 : -INFINITY;
       dec::transpose_reduce32<true>(v, lane);
-      ctl->red[quarter][half * 64 + c * 32 + lane] = v[0];
+      ctl->red[quarter][part * 32 + lane] = v[0];
     }
     soft_sync();
     if (gt < kRows) {
       const float own = fmaxf(fmaxf(ctl->red[0][gt], ctl->red[1][gt]),
                               fmaxf(ctl->red[2][gt], ctl->red[3][gt]));
       const float tm = fmaxf(own, swap(own));
-      const float mo = ctl->m_run[gt];
+      const float mo = -ctl->neg_max[gt];
       const float mn = tm > mo + 8.f ? tm - dec::kMaxLead : mo;
       ctl->vec[gt] = mo == -INFINITY ? 0.f : ex2(mo - mn);
-      ctl->m_run[gt] = mn;
+      ctl->neg_max[gt] = -mn;
     } else {
       ++swaps;
     }
@@ -573,20 +573,21 @@ struct Soft {
       *reinterpret_cast<volatile uint32_t*>(&ctl->moves) += 1;
     }
 #pragma unroll
-    for (int i = 0; i < 64; ++i) lp[i] *= ctl->vec[half * 64 + i];
+    for (int i = 0; i < 16; ++i)
+      lp[i] = fma_f32x2(lp[i], *reinterpret_cast<const uint64_t*>(&ctl->vec[part * 32 + 2 * i]),
+                        pack_f32x2(0.f, 0.f));
     if (last >= 0) {
       wait(&ctl->pv_done[last & 1], (uint32_t)(last >> 1) & 1);
       tc::fence_after_sync();
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i) {                // two blocks of dims, 32 rows at a time
+      for (int d = 0; d < 2; ++d) {                // the two blocks of dims
         uint32_t raw[32];
-        const int row = half * 64 + (i & 1) * 32;
-        const uint32_t at = tmem + lanes() + (i >> 1) * kRows + row;
+        const uint32_t at = tmem + lanes() + d * kRows + part * 32;
         tc::tmem_ld32(at, raw);
         tc::tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 32; ++e)
-          raw[e] = __float_as_uint(__uint_as_float(raw[e]) * ctl->vec[row + e]);
+          raw[e] = __float_as_uint(__uint_as_float(raw[e]) * ctl->vec[part * 32 + e]);
         tc::tmem_st32(at, raw);
       }
       tc::tmem_wait_st();
@@ -619,27 +620,27 @@ __device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
   const int tl = s.quarter * 32 + s.lane;          // key of this CTA's half tile / dim of a block
   const long long n = w.end - w.begin;
   int block = (int)(w.begin / w.tiles), first_tile = (int)(w.begin % w.tiles);
-  float lp[64];                                    // this key's share of its rows' sums
-  // Where this key's 64 rows go, the P half of CTA `half`: rows of 128 bytes in
+  uint64_t lp[16];                                 // this key's share of its rows' sums, in pairs
+  // Where this key's rows go, the P half of CTA part / 2: rows of 128 bytes in
   // 16-byte pieces, piece j of key k at j ^ (k & 7). Rows for the other CTA wait
   // here for a bulk copy: 64 keys in the stage's rope slot, which S is done with,
   // 64 behind P; both are free again once PV of the tile is done.
   const int key = (int)rank * 128 + tl;
-  const bool away = s.half != (int)rank;
+  const bool away = (s.part >> 1) != (int)rank;
   long long g = 0;
   while (g < n) {
     const int nt = (int)min((long long)(w.tiles - first_tile), n - g);
     soft_sync();                                   // the previous block's readers are done
-    if (s.gt < kRows) ctl->m_run[s.gt] = -INFINITY;
+    if (s.gt < kRows) ctl->neg_max[s.gt] = INFINITY;
 #pragma unroll
-    for (int i = 0; i < 64; ++i) lp[i] = 0.f;
+    for (int i = 0; i < 16; ++i) lp[i] = 0;
     soft_sync();
     for (int t = 0; t < nt; ++t, ++g) {
       const int st = g & 1;
       const uint32_t ph = (uint32_t)(g >> 1) & 1;
       const int key0 = (first_tile + t) * kKeys;
       const bool valid = key0 + key < w.len;
-      uint32_t hi[16], lo[16];
+      uint32_t hi[8], lo[8];
       s.wait(&ctl->s_full[st], ph);
       tc::fence_after_sync();
       if (t == 0) {
@@ -665,31 +666,33 @@ __device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
                              : tl < 64 ? st * kStageBytes + 4 * kChunkBytes + tl * kPRow
                                        : kOffStage + (tl - 64) * kPRow);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        *reinterpret_cast<uint4*>(put + ((j ^ (key & 7)) << 4)) =
+      for (int j = 0; j < 2; ++j) {
+        const int at = (s.part & 1) * 2 + j;
+        *reinterpret_cast<uint4*>(put + ((at ^ (key & 7)) << 4)) =
             make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
-        *reinterpret_cast<uint4*>(put + (((4 + j) ^ (key & 7)) << 4)) =
+        *reinterpret_cast<uint4*>(put + (((4 + at) ^ (key & 7)) << 4)) =
             make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]);
       }
-      // Keys past the end: their V must be finite (0), in both halves' slots.
+      // Keys past the end: their V must be finite (0), a slot of each part.
       if (key0 + kKeys > w.len) {
         s.wait(&ctl->v_full[st], ph);
+        if (key0 + (s.part >> 1) * 128 + tl >= w.len) {
+          uint4* v =
+              reinterpret_cast<uint4*>(smem + st * kStageBytes + s.part * kChunkBytes + tl * 128);
 #pragma unroll
-        for (int kh = 0; kh < 2; ++kh)
-          if (key0 + kh * 128 + tl >= w.len) {
-            uint4* v = reinterpret_cast<uint4*>(smem + st * kStageBytes +
-                                                (kh * 2 + s.half) * kChunkBytes + tl * 128);
-#pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] = make_uint4(0, 0, 0, 0);
-          }
+          for (int u = 0; u < 8; ++u) v[u] = make_uint4(0, 0, 0, 0);
+        }
       }
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
-      __syncwarp();
-      if (s.lane == 0) {
-        if (away)                                  // this warp's 32 keys
+      if (away) {                                  // both warps of these 32 keys' rows
+        asm volatile("bar.sync %0, 64;" ::"r"(3 + s.quarter) : "memory");
+        if (s.lane == 0 && (s.part & 1) == 0)
           tc::bulk_copy_to(tc::map_rank(smem + kOffP + key * kPRow, 1 - rank), put, 32 * kPRow,
                            tc::map_rank(&ctl->p_in, 1 - rank));
+      }
+      __syncwarp();
+      if (s.lane == 0) {
         if (rank == 0)
           tc::mbar_arrive(&ctl->p_own);
         else
@@ -697,13 +700,12 @@ __device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
       }
     }
     // Row sums over both CTAs' keys, 1 / l and the LSE, then this CTA's dims.
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    {
       float v[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = lp[c * 32 + i];
+      for (int i = 0; i < 16; ++i) unpack_f32x2(lp[i], v[2 * i], v[2 * i + 1]);
       dec::transpose_reduce32<false>(v, s.lane);
-      ctl->red[s.quarter][s.half * 64 + c * 32 + s.lane] = v[0];
+      ctl->red[s.quarter][s.part * 32 + s.lane] = v[0];
     }
     soft_sync();
     const size_t slot = (size_t)(w.unit + block) * kRows;
@@ -713,7 +715,7 @@ __device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
       const float l = own + s.swap(own);
       ctl->vec[s.gt] = l > 0.f ? 1.f / l : 0.f;
       if (rank == 0 && s.gt < rows)
-        a.part_lse[slot + s.gt] = l == 0.f ? -INFINITY : ctl->m_run[s.gt] + __log2f(l);
+        a.part_lse[slot + s.gt] = l == 0.f ? -INFINITY : __log2f(l) - ctl->neg_max[s.gt];
     } else {
       ++s.swaps;
     }
@@ -721,15 +723,15 @@ __device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
     s.wait(&ctl->pv_done[(g - 1) & 1], (uint32_t)((g - 1) >> 1) & 1);
     tc::fence_after_sync();
 #pragma unroll 1
-    for (int i = 0; i < 4; ++i) {                  // two blocks of dims, 32 rows at a time
+    for (int d = 0; d < 2; ++d) {                  // the two blocks of dims
       uint32_t raw[32];
-      const int row0 = s.half * 64 + (i & 1) * 32;
-      tc::tmem_ld32(tmem + s.lanes() + (i >> 1) * kRows + row0, raw);
+      tc::tmem_ld32(tmem + s.lanes() + d * kRows + s.part * 32, raw);
       tc::tmem_wait_ld();
-      float* dst = a.part_o + (slot + row0) * kDv + rank * 256 + (i >> 1) * 128 + tl;
+      float* dst = a.part_o + (slot + s.part * 32) * kDv + rank * 256 + d * 128 + tl;
 #pragma unroll
       for (int e = 0; e < 32; ++e)
-        if (row0 + e < rows) dst[(size_t)e * kDv] = __uint_as_float(raw[e]) * ctl->vec[row0 + e];
+        if (s.part * 32 + e < rows)
+          dst[(size_t)e * kDv] = __uint_as_float(raw[e]) * ctl->vec[s.part * 32 + e];
     }
     tc::fence_before_sync();
     ++block;
