@@ -51,12 +51,13 @@ constexpr int kKeys = kWideKeys;              // keys per tile, half of them per
 // Six warpgroups: two TMA warps and two MMA (or relay) warps; four scout warps;
 // four groups of softmax warps. Registers move to the softmax (32 row sums and
 // 16 words of codes a thread) from the others: the launch's 6 x 80 a thread go
-// 56 + 40 + 4 x 96.
+// 64 + 64 + 4 x 88.
 constexpr int kScout = 128;                   // scouts: a key and all 128 rows each
 constexpr int kSoft = 512;                    // softmax threads: a key and 32 rows each
 constexpr int kThreads = 128 + kScout + kSoft;
-constexpr int kRegsIssue = 56, kRegsScout = 40, kRegsSoft = 96;
-static_assert(kRegsIssue + kRegsScout + 4 * kRegsSoft <= 6 * (65536 / kThreads / 8 * 8), "register pool");
+constexpr int kRegsIssue = 64, kRegsScout = 64, kRegsSoft = 88;
+static_assert(kRegsIssue + kRegsScout + 4 * kRegsSoft <= 6 * (65536 / kThreads / 8 * 8),
+              "register pool");
 constexpr int kQChunk = 64 * 128;             // this CTA's 64 rows x 128 dims
 constexpr int kQBytes = 64 * kDqk;
 constexpr int kPRow = 128;                    // a key's 64 hi codes, then its 64 lo codes
@@ -403,13 +404,13 @@ __device__ void scout(const WideArgs& a, const WidePart& w, WideCtl* ctl, uint32
     const bool valid = key0 + (int)rank * 128 + tl < w.len;
     float most = -INFINITY;
 #pragma unroll 1
-    for (int c = 0; c < kRows; c += 16) {
-      uint32_t raw[16];
-      tc::tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + kSCol + st * kRows + c, raw);
+    for (int c = 0; c < kRows; c += 32) {
+      uint32_t raw[32];
+      tc::tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + kSCol + st * kRows + c, raw);
       tc::tmem_wait_ld();
       const float4* m4 = reinterpret_cast<const float4*>(&ctl->neg_max[c]);
 #pragma unroll
-      for (int i = 0; i < 16; i += 4) {
+      for (int i = 0; i < 32; i += 4) {
         const float4 m = m4[i / 4];
         most = fmaxf(most, fmaf(__uint_as_float(raw[i]), a.bmm1_log2, m.x));
         most = fmaxf(most, fmaf(__uint_as_float(raw[i + 1]), a.bmm1_log2, m.y));
@@ -421,7 +422,7 @@ __device__ void scout(const WideArgs& a, const WidePart& w, WideCtl* ctl, uint32
     const bool any = __any_sync(0xffffffffu, valid && most > 8.f);
     if (lane == 0 && (any || !ok)) atomicOr(&ctl->vote[b], (any ? kMoved : 0) | (ok ? 0 : kFailed));
     scout_sync();
-    if (quarter == 0) {
+    if (warp == 4) {
       uint32_t mine = peek(&ctl->vote[b]);
       __syncwarp();
       if (lane == 0) {
@@ -507,24 +508,29 @@ struct Soft {
   // has such a tile done again.
   __device__ void weigh(int st, bool valid, uint64_t (&lp)[16], uint32_t (&hi)[8],
                         uint32_t (&lo)[8]) const {
-    uint32_t raw[32];
-    tc::tmem_ld32(tmem + lanes() + kSCol + st * kRows + part * 32, raw);
-    tc::tmem_wait_ld();
     const ulonglong2* m4 = reinterpret_cast<const ulonglong2*>(&ctl->neg_max[part * 32]);
 #pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-      const ulonglong2 m = m4[i / 4];
-      float p[4];
-      pair(pack_f32x2(__uint_as_float(raw[i]), __uint_as_float(raw[i + 1])), m.x, valid, p[0], p[1]);
-      pair(pack_f32x2(__uint_as_float(raw[i + 2]), __uint_as_float(raw[i + 3])), m.y, valid, p[2], p[3]);
-      lp[i / 2] = add_f32x2(lp[i / 2], pack_f32x2(p[0], p[1]));
-      lp[i / 2 + 1] = add_f32x2(lp[i / 2 + 1], pack_f32x2(p[2], p[3]));
-      const uint32_t h01 = dec::f32x2_to_f16x2(p[0], p[1]), h23 = dec::f32x2_to_f16x2(p[2], p[3]);
-      const uint16_t e01 = dec::f16x2_to_e4m3x2(h01), e23 = dec::f16x2_to_e4m3x2(h23);
-      const uint16_t l01 = f16x2_to_e5m2x2(dec::f16x2_sub(h01, e4m3x2_to_f16x2(e01)));
-      const uint16_t l23 = f16x2_to_e5m2x2(dec::f16x2_sub(h23, e4m3x2_to_f16x2(e23)));
-      hi[i / 4] = (uint32_t)e01 | ((uint32_t)e23 << 16);
-      lo[i / 4] = (uint32_t)l01 | ((uint32_t)l23 << 16);
+    for (int c = 0; c < 32; c += 16) {
+      uint32_t raw[16];
+      tc::tmem_ld16(tmem + lanes() + kSCol + st * kRows + part * 32 + c, raw);
+      tc::tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        const int i = c + e;
+        const ulonglong2 m = m4[i / 4];
+        float p[4];
+        pair(pack_f32x2(__uint_as_float(raw[e]), __uint_as_float(raw[e + 1])), m.x, valid, p[0], p[1]);
+        pair(pack_f32x2(__uint_as_float(raw[e + 2]), __uint_as_float(raw[e + 3])), m.y, valid, p[2],
+             p[3]);
+        lp[i / 2] = add_f32x2(lp[i / 2], pack_f32x2(p[0], p[1]));
+        lp[i / 2 + 1] = add_f32x2(lp[i / 2 + 1], pack_f32x2(p[2], p[3]));
+        const uint32_t h01 = dec::f32x2_to_f16x2(p[0], p[1]), h23 = dec::f32x2_to_f16x2(p[2], p[3]);
+        const uint16_t e01 = dec::f16x2_to_e4m3x2(h01), e23 = dec::f16x2_to_e4m3x2(h23);
+        const uint16_t l01 = f16x2_to_e5m2x2(dec::f16x2_sub(h01, e4m3x2_to_f16x2(e01)));
+        const uint16_t l23 = f16x2_to_e5m2x2(dec::f16x2_sub(h23, e4m3x2_to_f16x2(e23)));
+        hi[i / 4] = (uint32_t)e01 | ((uint32_t)e23 << 16);
+        lo[i / 4] = (uint32_t)l01 | ((uint32_t)l23 << 16);
+      }
     }
   }
   // Takes back what weigh added (the same values bit for bit).
