@@ -26,9 +26,9 @@
 // down to 2^-13 of absolute error. The running max is lazy as in decode_tc.cu
 // (moved when a score exceeds it by more than 8, to 2 below the new one) and
 // agreed between the CTAs of a pair, whose scores share accumulators: P is
-// computed on the assumption that no row moves, scout warps meanwhile look
-// for a row that moves and exchange a flag, and only then is the tile done again
-// with new maxima.
+// computed and written as if no row moved; a vote of both CTAs follows it, which
+// only the PV of the tile waits for; where a row did move the softmax takes the
+// tile back and writes its P again with new maxima.
 //
 // Work: the tiles of all row blocks, block after block, are one sequence cut
 // into equal parts, one per pair; a part's piece of a block goes to partial
@@ -48,15 +48,15 @@ using dec::kStageBytes;
 
 constexpr int kRows = kWideRows;              // query rows per block: the MMA's N
 constexpr int kKeys = kWideKeys;              // keys per tile, half of them per CTA
-// Six warpgroups: two TMA warps and two MMA (or relay) warps; four scout warps;
-// four groups of softmax warps. Registers move to the softmax (32 row sums and
-// 16 words of codes a thread) from the others: the launch's 6 x 80 a thread go
-// 64 + 64 + 4 x 88.
-constexpr int kScout = 128;                   // scouts: a key and all 128 rows each
+// Six warpgroups: two TMA warps, the S and PV (or relay) warps; the vote warp and
+// three idle ones; four groups of softmax warps. Registers move to the softmax
+// (32 row sums and 16 words of codes a thread) from the others: the launch's
+// 6 x 80 a thread go 64 + 32 + 4 x 96.
 constexpr int kSoft = 512;                    // softmax threads: a key and 32 rows each
-constexpr int kThreads = 128 + kScout + kSoft;
-constexpr int kRegsIssue = 64, kRegsScout = 64, kRegsSoft = 88;
-static_assert(kRegsIssue + kRegsScout + 4 * kRegsSoft <= 6 * (65536 / kThreads / 8 * 8),
+constexpr int kSoftWarps = kSoft / 32;
+constexpr int kThreads = 256 + kSoft;
+constexpr int kRegsIssue = 64, kRegsVote = 32, kRegsSoft = 96;
+static_assert(kRegsIssue + kRegsVote + 4 * kRegsSoft <= 6 * (65536 / kThreads / 8 * 8),
               "register pool");
 constexpr int kQChunk = 64 * 128;             // this CTA's 64 rows x 128 dims
 constexpr int kQBytes = 64 * kDqk;
@@ -78,7 +78,7 @@ static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms need 1 KB a
 struct WideCtl {
   uint64_t k_full[2];      // rank 0: TMA of both CTAs -> S: both CTAs' keys landed
   uint64_t v_full[2];      // TMA -> PV, relay: the other CTA's keys of the own dims landed
-  uint64_t s_full[2];      // MMA -> softmax, scouts, TMA: S of a tile done
+  uint64_t s_full[2];      // MMA -> softmax, TMA: S of a tile done
   uint64_t p_own;          // rank 0: softmax -> PV: P of CTA 0's keys written or under way
   uint64_t p_in;           // bulk copies of the other CTA -> PV, relay: P of its keys landed
   uint64_t p_peer[2];      // rank 0: P of CTA 0's keys (and V for it) complete in rank 1; its
@@ -87,15 +87,16 @@ struct WideCtl {
   uint64_t pv_done[2];     // MMA -> softmax, TMA: O holds the tile; P and the stage are free
   uint64_t q_full;         // rank 0: TMA of both CTAs -> S
   uint64_t q_empty;        // MMA -> TMA
+  uint64_t vote_in;        // softmax -> vote warp: this CTA's votes on a tile
   uint64_t vote_bar[2];    // the other CTA's flag is in vote_peer
-  uint64_t told[2];        // scouts -> softmax: verdict
+  uint64_t told[2];        // vote warp -> PV, relay, softmax: verdict
+  uint64_t sync;           // softmax among themselves (a bounded barrier)
+  uint64_t pair[4];        // the two warps that send a quarter's P to the other CTA
   uint64_t swap_bar[2];    // the other CTA's row values are in swap
   uint64_t drain[2];
   uint32_t vote_peer[2];
-  uint32_t vote[2];        // bits of this CTA's scouts: kMoved, kFailed
-  uint32_t verdict[2];     // of the pair's scouts
-  uint32_t soft_word[2];   // kFailed of softmax threads; kMoved, kFailed of the verdict
-  uint32_t moves;          // how often new maxima came into neg_max
+  uint32_t vote[2];        // kMoved of this CTA's softmax
+  uint32_t verdict[2];     // of the pair: whether a row moved
   uint32_t tmem_base;
   int abort_flag;
   alignas(16) float neg_max[kRows]; // minus the running row max (base-2 scores), read four at a time
@@ -106,7 +107,7 @@ struct WideCtl {
 static_assert(offsetof(WideCtl, neg_max) % 16 == 0, "16-byte reads");
 constexpr int kSmemBytes = kOffCtl + (int)sizeof(WideCtl) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-constexpr uint32_t kMoved = 1, kFailed = 2;
+constexpr uint32_t kMoved = 1;
 
 __device__ __forceinline__ bool w_wait(uint64_t* bar, uint32_t parity, WideCtl* ctl,
                                        int32_t* status) {
@@ -121,26 +122,6 @@ __device__ __forceinline__ bool w_wait(uint64_t* bar, uint32_t parity, WideCtl* 
       return false;
     }
   }
-}
-__device__ __forceinline__ void soft_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kSoft) : "memory");
-}
-__device__ __forceinline__ void scout_sync() {
-  asm volatile("bar.sync 2, %0;" ::"n"(kScout) : "memory");
-}
-// Waits, as bounded as w_wait, until the maxima have moved `count` times.
-__device__ __forceinline__ bool wait_moves(uint32_t count, WideCtl* ctl, int32_t* status) {
-  const unsigned long long t0 = tc::globaltimer_ns();
-  while (*reinterpret_cast<volatile uint32_t*>(&ctl->moves) < count) {
-    if (*reinterpret_cast<volatile int*>(&ctl->abort_flag)) return false;
-    if (tc::globaltimer_ns() - t0 > kTimeoutNs) {
-      *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
-      if (status) atomicOr(status, MLA_FAULT_WAIT_TIMEOUT);
-      return false;
-    }
-  }
-  __threadfence_block();
-  return true;
 }
 __device__ __forceinline__ uint32_t peek(const uint32_t* p) {
   return *reinterpret_cast<const volatile uint32_t*>(p);
@@ -263,16 +244,35 @@ __device__ void load_values(const WideArgs& a, const WidePart& w, uint8_t* smem,
   }
 }
 
-// Rank 1: tells rank 0's PV issuer that P of CTA 0's keys and V for it are here.
+// Waits for the verdict on a tile: -1 if the wait ran out, else whether a row moved.
+__device__ __forceinline__ int wait_verdict(uint32_t vote, WideCtl* ctl, int32_t* status) {
+  if (!w_wait(&ctl->told[vote & 1], (vote >> 1) & 1, ctl, status)) return -1;
+  return (int)(peek(&ctl->verdict[vote & 1]) & kMoved);
+}
+
+// Rank 1: tells rank 0's PV issuer that P of CTA 0's keys and V for it are here;
+// twice for a tile whose P is written again.
 __device__ void relay(const WideArgs& a, const WidePart& w, WideCtl* ctl) {
   const long long n = w.end - w.begin;
   const uint32_t to = tc::map_rank(&ctl->p_peer[0], 0);
+  int tile = (int)(w.begin % w.tiles);
+  bool first = true;
+  uint32_t votes = 0, ps = 0;
   for (long long i = 0; i < n; ++i) {
     tc::mbar_arrive_expect_tx(&ctl->p_in, 128 * kPRow);
     if (!w_wait(&ctl->v_full[i & 1], (uint32_t)(i >> 1) & 1, ctl, a.status) ||
-        !w_wait(&ctl->p_in, (uint32_t)i & 1, ctl, a.status))
+        !w_wait(&ctl->p_in, ps++ & 1, ctl, a.status))
       return;
+    const int moved = first ? 0 : wait_verdict(votes++, ctl, a.status);
+    if (moved < 0) return;
+    if (moved) tc::mbar_arrive_expect_tx(&ctl->p_in, 128 * kPRow);
     tc::remote_arrive(to);
+    if (moved) {
+      if (!w_wait(&ctl->p_in, ps++ & 1, ctl, a.status)) return;
+      tc::remote_arrive(to);
+    }
+    if (++tile == w.tiles) tile = 0;
+    first = tile == 0;
   }
 }
 
@@ -298,7 +298,7 @@ __device__ void issue_s(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
       ++x;
     }
     // The S buffer of tile i - 2 is free: its stage was refilled after its PV,
-    // whose P the softmax wrote after it (and the scouts) had read that S.
+    // whose P the softmax wrote after it had read that S.
     if (!w_wait(&ctl->k_full[st], (uint32_t)(i >> 1) & 1, ctl, a.status)) break;
     tc::fence_after_sync();
     const uint32_t kv = s_kv + st * kStageBytes, d = tmem + kSCol + st * kRows;
@@ -326,11 +326,11 @@ __device__ void issue_pv(const WideArgs& a, const WidePart& w, uint8_t* smem, Wi
   const long long n = w.end - w.begin;
   int tile = (int)(w.begin % w.tiles);
   bool first = true;                               // the pair's first tile of the block
-  uint32_t votes = 0;                              // verdicts the scouts gave before it
+  uint32_t votes = 0, ps = 0;                      // verdicts before this tile, writes of P
   bool ok = true;
   for (long long i = 0; ok && i < n; ++i) {
     const int st = i & 1;
-    const uint32_t pp = (uint32_t)i & 1, ph = (uint32_t)(i >> 1) & 1;
+    const uint32_t ph = (uint32_t)(i >> 1) & 1;
     tc::mbar_arrive_expect_tx(&ctl->p_in, 128 * kPRow);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       ok = ok && w_wait(bar, parity, ctl, a.status);
@@ -355,121 +355,99 @@ __device__ void issue_pv(const WideArgs& a, const WidePart& w, uint8_t* smem, Wi
     // 1's softmax too (and with it the second half's P) where that touches what
     // the half writes or reads: O (read out before a block's first tile, scaled
     // where the maxima moved) or V (keys past a block's end are cleared).
-    wait(&ctl->p_own, pp);
-    wait(&ctl->p_peer[0], pp);
-    const bool both =
-        first || tile == w.tiles - 1 || (ok && (peek(&ctl->verdict[votes & 1]) & kMoved));
-    if (both) wait(&ctl->p_peer[1], pp);
+    bool both = first || tile == w.tiles - 1;
+    wait(&ctl->p_own, ps & 1);
+    wait(&ctl->p_peer[0], ps & 1);
+    if (!first && ok) {
+      const int moved = wait_verdict(votes++, ctl, a.status);
+      if (moved < 0) break;
+      if (moved) {                                 // that P is void: another follows
+        wait(&ctl->p_peer[1], ps & 1);
+        wait(&ctl->p_in, ps & 1);
+        if (!ok) break;
+        ++ps;
+        tc::mbar_arrive_expect_tx(&ctl->p_in, 128 * kPRow);
+        wait(&ctl->p_own, ps & 1);
+        wait(&ctl->p_peer[0], ps & 1);
+        both = true;
+      }
+    }
+    if (both) wait(&ctl->p_peer[1], ps & 1);
     if (!ok) break;
     half(0, first);
     tc::mma_commit_pair(&ctl->pv_half[st]);
     wait(&ctl->v_full[st], ph);
-    wait(&ctl->p_in, pp);
-    if (!both) wait(&ctl->p_peer[1], pp);
+    wait(&ctl->p_in, ps & 1);
+    if (!both) wait(&ctl->p_peer[1], ps & 1);
     if (!ok) break;
     half(1, false);
     tc::mma_commit_pair(&ctl->pv_done[st]);
-    if (!first) ++votes;
+    ++ps;
     if (++tile == w.tiles) tile = 0;
     first = tile == 0;
   }
   mma_drain(&ctl->drain[1]);
 }
 
-// ---------------------------------------------------------------- scouts
-// Whether a score exceeds its row's max by more than 8, tile by tile, agreed
-// between the pair's CTAs while the softmax computes P as if none did.
-__device__ void scout(const WideArgs& a, const WidePart& w, WideCtl* ctl, uint32_t tmem,
-                      uint32_t rank) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int quarter = warp & 3, tl = quarter * 32 + lane;
+// ---------------------------------------------------------------- votes
+// One thread: after this CTA's softmax has cast its votes on a tile, exchanges
+// them with the other CTA and tells the verdict.
+__device__ void vote(const WideArgs& a, const WidePart& w, WideCtl* ctl, uint32_t rank) {
   const long long n = w.end - w.begin;
   int tile = (int)(w.begin % w.tiles);
-  uint32_t votes = 0, moves = 0;
-  bool ok = true, fresh = true;                    // fresh: the block's first tile
-  for (long long g = 0; g < n; ++g) {
-    const int st = g & 1, key0 = tile * kKeys;
-    if (++tile == w.tiles) tile = 0;
-    if (fresh) {                                   // its maxima come from the tile itself
-      fresh = tile == 0;
-      ok = __all_sync(0xffffffffu, ok && wait_moves(++moves, ctl, a.status));
-      continue;
-    }
-    const int b = votes & 1;
-    const uint32_t ph = (votes >> 1) & 1;
-    ++votes;
-    if (ok) ok = w_wait(&ctl->s_full[st], (uint32_t)(g >> 1) & 1, ctl, a.status);
-    ok = __all_sync(0xffffffffu, ok);
-    tc::fence_after_sync();
-    const bool valid = key0 + (int)rank * 128 + tl < w.len;
-    float most = -INFINITY;
-#pragma unroll 1
-    for (int c = 0; c < kRows; c += 32) {
-      uint32_t raw[32];
-      tc::tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + kSCol + st * kRows + c, raw);
-      tc::tmem_wait_ld();
-      const float4* m4 = reinterpret_cast<const float4*>(&ctl->neg_max[c]);
-#pragma unroll
-      for (int i = 0; i < 32; i += 4) {
-        const float4 m = m4[i / 4];
-        most = fmaxf(most, fmaf(__uint_as_float(raw[i]), a.bmm1_log2, m.x));
-        most = fmaxf(most, fmaf(__uint_as_float(raw[i + 1]), a.bmm1_log2, m.y));
-        most = fmaxf(most, fmaf(__uint_as_float(raw[i + 2]), a.bmm1_log2, m.z));
-        most = fmaxf(most, fmaf(__uint_as_float(raw[i + 3]), a.bmm1_log2, m.w));
-      }
-    }
-    tc::fence_before_sync();
-    const bool any = __any_sync(0xffffffffu, valid && most > 8.f);
-    if (lane == 0 && (any || !ok)) atomicOr(&ctl->vote[b], (any ? kMoved : 0) | (ok ? 0 : kFailed));
-    scout_sync();
-    if (warp == 4) {
+  bool first = true;
+  uint32_t votes = 0;
+  for (long long i = 0; i < n; ++i) {
+    if (!first) {
+      const int b = votes & 1;
+      if (!w_wait(&ctl->vote_in, votes & 1, ctl, a.status)) return;
       uint32_t mine = peek(&ctl->vote[b]);
-      __syncwarp();
-      if (lane == 0) {
-        ctl->vote[b] = 0;
-        tc::mbar_arrive_expect_tx(&ctl->vote_bar[b], 4);
-        tc::remote_st_async(tc::map_rank(&ctl->vote_peer[b], 1 - rank), mine & kMoved,
-                            tc::map_rank(&ctl->vote_bar[b], 1 - rank));
-        if (!w_wait(&ctl->vote_bar[b], ph, ctl, a.status)) mine |= kFailed;
-        mine |= peek(&ctl->vote_peer[b]);
-        *reinterpret_cast<volatile uint32_t*>(&ctl->verdict[b]) = mine;
-        tc::mbar_arrive(&ctl->told[b]);
-      }
+      *reinterpret_cast<volatile uint32_t*>(&ctl->vote[b]) = 0;
+      tc::mbar_arrive_expect_tx(&ctl->vote_bar[b], 4);
+      tc::remote_st_async(tc::map_rank(&ctl->vote_peer[b], 1 - rank), mine,
+                          tc::map_rank(&ctl->vote_bar[b], 1 - rank));
+      if (!w_wait(&ctl->vote_bar[b], (votes >> 1) & 1, ctl, a.status)) return;
+      *reinterpret_cast<volatile uint32_t*>(&ctl->verdict[b]) = mine | peek(&ctl->vote_peer[b]);
+      tc::mbar_arrive(&ctl->told[b]);
+      ++votes;
     }
-    scout_sync();
-    const uint32_t verdict = peek(&ctl->verdict[b]);
-    if (verdict & kFailed) return;                 // all of them
-    if (verdict & kMoved) {
-      ok = __all_sync(0xffffffffu, ok && wait_moves(++moves, ctl, a.status));
-    }
-    fresh = tile == 0;
+    if (++tile == w.tiles) tile = 0;
+    first = tile == 0;
   }
 }
 
 // ---------------------------------------------------------------- softmax
+// Every wait here is bounded, barriers among the softmax warps included: a
+// thread whose wait runs out leaves, and the others' next one ends by the abort
+// flag.
 struct Soft {
   const WideArgs& a;
   WideCtl* ctl;
   uint32_t tmem, rank;
   int quarter, part, lane, gt;                     // rows 32 part .. 32 part + 31
-  uint32_t swaps = 0, votes = 0, words = 0;
+  uint32_t swaps = 0, votes = 0, syncs = 0, sends = 0;
   bool ok = true;                                  // warp-uniform
 
   __device__ Soft(const WideArgs& a_, WideCtl* c, uint32_t t, uint32_t r)
       : a(a_), ctl(c), tmem(t), rank(r) {
     const int warp = threadIdx.x >> 5;
     quarter = warp & 3;
-    gt = threadIdx.x - 128 - kScout;
+    gt = threadIdx.x - 256;
     part = gt >> 7;
     lane = threadIdx.x & 31;
   }
   __device__ uint32_t lanes() const { return (uint32_t)(quarter * 32) << 16; }
-  // A thread that gave up a wait goes on through the barriers, so that every
-  // thread reaches each of them, until verdict() makes all of them leave.
   __device__ void wait(uint64_t* bar, uint32_t parity) {
     const bool got = ok && w_wait(bar, parity, ctl, a.status);
     ok = __all_sync(0xffffffffu, got);
   }
+  // Barrier of `warps` warps on `bar`, its `count`-th use.
+  __device__ void meet(uint64_t* bar, uint32_t count) {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bar);
+    wait(bar, count & 1);
+  }
+  __device__ void sync() { meet(&ctl->sync, syncs++); }
   // Row value `v` of threads gt < 128 (row gt) to the other CTA; returns its value.
   __device__ float swap(float v) {
     const int b = swaps & 1;
@@ -496,18 +474,20 @@ struct Soft {
     return r;
   }
   // The weights of two rows of this thread's key.
-  __device__ __forceinline__ void pair(uint64_t raw, uint64_t neg_max, bool valid, float& p0,
-                                       float& p1) const {
+  __device__ __forceinline__ void pair(uint64_t raw, uint64_t neg_max, bool valid, float& most,
+                                       float& p0, float& p1) const {
     float d0, d1;
     unpack_f32x2(fma_f32x2(raw, pack_f32x2(a.bmm1_log2, a.bmm1_log2), neg_max), d0, d1);
+    most = fmaxf(most, fmaxf(d0, d1));
     p0 = valid ? ex2(at_most_9(d0)) : 0.f;
     p1 = valid ? ex2(at_most_9(d1)) : 0.f;
   }
   // P of the tile: codes of this thread's key in its 32 rows; lp gathers the row
-  // sums. Scores more than 9 above a row's max count as 9: the scouts' verdict
-  // has such a tile done again.
-  __device__ void weigh(int st, bool valid, uint64_t (&lp)[16], uint32_t (&hi)[8],
-                        uint32_t (&lo)[8]) const {
+  // sums. Returns the largest score above its row's max; more than 9 count as 9
+  // (more than 8 has the tile done again).
+  __device__ float weigh(int st, bool valid, uint64_t (&lp)[16], uint32_t (&hi)[8],
+                         uint32_t (&lo)[8]) const {
+    float most = -INFINITY;
     const ulonglong2* m4 = reinterpret_cast<const ulonglong2*>(&ctl->neg_max[part * 32]);
 #pragma unroll
     for (int c = 0; c < 32; c += 16) {
@@ -519,8 +499,9 @@ struct Soft {
         const int i = c + e;
         const ulonglong2 m = m4[i / 4];
         float p[4];
-        pair(pack_f32x2(__uint_as_float(raw[e]), __uint_as_float(raw[e + 1])), m.x, valid, p[0], p[1]);
-        pair(pack_f32x2(__uint_as_float(raw[e + 2]), __uint_as_float(raw[e + 3])), m.y, valid, p[2],
+        pair(pack_f32x2(__uint_as_float(raw[e]), __uint_as_float(raw[e + 1])), m.x, valid, most, p[0],
+             p[1]);
+        pair(pack_f32x2(__uint_as_float(raw[e + 2]), __uint_as_float(raw[e + 3])), m.y, valid, most, p[2],
              p[3]);
         lp[i / 2] = add_f32x2(lp[i / 2], pack_f32x2(p[0], p[1]));
         lp[i / 2 + 1] = add_f32x2(lp[i / 2 + 1], pack_f32x2(p[2], p[3]));
@@ -532,6 +513,7 @@ struct Soft {
         lo[i / 4] = (uint32_t)l01 | ((uint32_t)l23 << 16);
       }
     }
+    return valid ? most : -INFINITY;
   }
   // Takes back what weigh added (the same values bit for bit).
   __device__ void unweigh(int st, bool valid, uint64_t (&lp)[16]) const {
@@ -541,8 +523,9 @@ struct Soft {
     const uint64_t* m2 = reinterpret_cast<const uint64_t*>(&ctl->neg_max[part * 32]);
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
-      float p0, p1;
-      pair(pack_f32x2(__uint_as_float(raw[i]), __uint_as_float(raw[i + 1])), m2[i / 2], valid, p0, p1);
+      float most = 0.f, p0, p1;
+      pair(pack_f32x2(__uint_as_float(raw[i]), __uint_as_float(raw[i + 1])), m2[i / 2], valid, most, p0,
+           p1);
       lp[i / 2] = add_f32x2(lp[i / 2], pack_f32x2(-p0, -p1));
     }
   }
@@ -561,7 +544,7 @@ struct Soft {
       dec::transpose_reduce32<true>(v, lane);
       ctl->red[quarter][part * 32 + lane] = v[0];
     }
-    soft_sync();
+    sync();
     if (gt < kRows) {
       const float own = fmaxf(fmaxf(ctl->red[0][gt], ctl->red[1][gt]),
                               fmaxf(ctl->red[2][gt], ctl->red[3][gt]));
@@ -573,11 +556,7 @@ struct Soft {
     } else {
       ++swaps;
     }
-    soft_sync();
-    if (gt == 0) {
-      __threadfence_block();
-      *reinterpret_cast<volatile uint32_t*>(&ctl->moves) += 1;
-    }
+    sync();
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       lp[i] = fma_f32x2(lp[i], *reinterpret_cast<const uint64_t*>(&ctl->vec[part * 32 + 2 * i]),
@@ -599,24 +578,69 @@ struct Soft {
       tc::tmem_wait_st();
     }
   }
-  // The scouts' verdict on the tile, the same for every thread; kFailed also
-  // once any softmax thread gave up a wait.
-  __device__ uint32_t verdict() {
-    const int v = votes & 1, b = words & 1;
-    const uint32_t ph = (votes >> 1) & 1;
-    ++votes;
-    ++words;
-    if (gt < 32) {
-      wait(&ctl->told[v], ph);
-      if (lane == 0) atomicOr(&ctl->soft_word[b], (ok ? peek(&ctl->verdict[v]) : kFailed));
-    } else if (!ok && lane == 0) {
-      atomicOr(&ctl->soft_word[b], kFailed);
+  // The codes of this thread's key to their place; rows for the other CTA by way
+  // of `put`, from which the two warps that hold a key's 64 rows send them.
+  __device__ void write_p(uint8_t* put, int key, bool away, const uint32_t (&hi)[8],
+                          const uint32_t (&lo)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int at = (part & 1) * 2 + j;
+      *reinterpret_cast<uint4*>(put + ((at ^ (key & 7)) << 4)) =
+          make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
+      *reinterpret_cast<uint4*>(put + (((4 + at) ^ (key & 7)) << 4)) =
+          make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]);
     }
-    soft_sync();
-    const uint32_t word = peek(&ctl->soft_word[b]);
-    // The other word was last read before this barrier.
-    if (gt == 0) *reinterpret_cast<volatile uint32_t*>(&ctl->soft_word[b ^ 1]) = 0;
-    return word;
+  }
+  __device__ void send_p(const uint8_t* put, const uint8_t* place, bool away) {
+    tc::fence_proxy_async_smem();
+    tc::fence_before_sync();
+    if (away) {
+      meet(&ctl->pair[quarter], sends++);
+      if (lane == 0 && (part & 1) == 0 && ok)
+        tc::bulk_copy_to(tc::map_rank(place, 1 - rank), put, 32 * kPRow,
+                         tc::map_rank(&ctl->p_in, 1 - rank));
+    }
+    __syncwarp();
+    if (lane == 0) {
+      if (rank == 0)
+        tc::mbar_arrive(&ctl->p_own);
+      else
+        tc::remote_arrive(tc::map_rank(&ctl->p_peer[1], 0));
+    }
+  }
+  // Casts this CTA's votes on a tile.
+  __device__ void cast(bool moved) {
+    const bool any = __any_sync(0xffffffffu, moved);
+    if (lane == 0) {
+      if (any) atomicOr(&ctl->vote[votes & 1], kMoved);
+      tc::mbar_arrive(&ctl->vote_in);
+    }
+    ++votes;
+  }
+  // Waits until PV of the tile that was voted on last is done with `bar`'s part,
+  // or the verdict on it says that a row moved (true): PV then has not begun.
+  __device__ bool moved_or(uint64_t* bar, uint32_t parity, bool voted) {
+    bool moved = false;
+    if (ok) {
+      const uint32_t v = votes - 1;
+      const unsigned long long t0 = tc::globaltimer_ns();
+      while (!tc::mbar_try_wait(bar, parity)) {
+        if (voted && tc::mbar_test_wait(&ctl->told[v & 1], (v >> 1) & 1) &&
+            (peek(&ctl->verdict[v & 1]) & kMoved)) {
+          moved = true;
+          break;
+        }
+        const bool expired = tc::globaltimer_ns() - t0 > kTimeoutNs;
+        if (*reinterpret_cast<volatile int*>(&ctl->abort_flag) || expired) {
+          *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
+          if (expired && a.status) atomicOr(a.status, MLA_FAULT_WAIT_TIMEOUT);
+          ok = false;
+          break;
+        }
+      }
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    return __any_sync(0xffffffffu, moved);
   }
 };
 
@@ -633,52 +657,67 @@ __device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
   // 64 behind P; both are free again once PV of the tile is done.
   const int key = (int)rank * 128 + tl;
   const bool away = (s.part >> 1) != (int)rank;
+  uint8_t* const place = smem + kOffP + key * kPRow;
+  auto put_at = [&](int st) {
+    return !away ? place
+                 : smem + (tl < 64 ? st * kStageBytes + 4 * kChunkBytes + tl * kPRow
+                                   : kOffStage + (tl - 64) * kPRow);
+  };
+  uint32_t hi[8], lo[8];
+  uint32_t ps = 0;                                 // writes of P before this tile's
+  // Tile g's P again, with new maxima, agreed after both CTAs' first copies of it
+  // have landed (they wait for p_in before they exchange row maxima).
+  auto again = [&](long long g, bool valid) {
+    s.unweigh(g & 1, valid, lp);
+    s.wait(&ctl->p_in, (ps - 1) & 1);
+    s.sync();                                      // everyone has read the old maxima
+    s.move(g & 1, valid, lp, g - 1);
+    s.weigh(g & 1, valid, lp, hi, lo);
+    uint8_t* put = put_at(g & 1);
+    s.write_p(put, key, away, hi, lo);
+    s.send_p(put, place, away);
+    ++ps;
+  };
   long long g = 0;
   while (g < n) {
     const int nt = (int)min((long long)(w.tiles - first_tile), n - g);
-    soft_sync();                                   // the previous block's readers are done
+    s.sync();                                      // the previous block's readers are done
     if (s.gt < kRows) ctl->neg_max[s.gt] = INFINITY;
 #pragma unroll
     for (int i = 0; i < 16; ++i) lp[i] = 0;
-    soft_sync();
+    s.sync();
+    bool valid = true;
     for (int t = 0; t < nt; ++t, ++g) {
       const int st = g & 1;
       const uint32_t ph = (uint32_t)(g >> 1) & 1;
       const int key0 = (first_tile + t) * kKeys;
-      const bool valid = key0 + key < w.len;
-      uint32_t hi[8], lo[8];
+      valid = key0 + key < w.len;
       s.wait(&ctl->s_full[st], ph);
+      if (!s.ok) return;
       tc::fence_after_sync();
       if (t == 0) {
         s.move(st, valid, lp, -1);
         s.weigh(st, valid, lp, hi, lo);
       } else {
-        s.weigh(st, valid, lp, hi, lo);
-        const uint32_t verdict = s.verdict();
-        if (verdict & kFailed) return;             // all of them
-        if (verdict & kMoved) {
+        float most = s.weigh(st, valid, lp, hi, lo);
+        // The place of P of these keys is free once PV of the previous tile is
+        // done with it; if that tile moved it is done again first.
+        uint64_t* bar = rank == 0 ? &ctl->pv_half[(g - 1) & 1] : &ctl->pv_done[(g - 1) & 1];
+        const uint32_t bph = (uint32_t)((g - 1) >> 1) & 1;
+        if (s.moved_or(bar, bph, t > 1)) {
           s.unweigh(st, valid, lp);
-          soft_sync();                             // everyone has read the old maxima
-          s.move(st, valid, lp, g - 1);
-          s.weigh(st, valid, lp, hi, lo);
+          again(g - 1, true);
+          most = s.weigh(st, valid, lp, hi, lo);
+          s.wait(bar, bph);
         }
+        s.cast(most > 8.f);
       }
-      // The place of P of these keys is free once PV of the previous tile is done
-      // with it.
-      if (g > 0)
+      if (t == 0 && g > 0)
         s.wait(rank == 0 ? &ctl->pv_half[(g - 1) & 1] : &ctl->pv_done[(g - 1) & 1],
                (uint32_t)((g - 1) >> 1) & 1);
-      uint8_t* put = smem + (!away ? kOffP + key * kPRow
-                             : tl < 64 ? st * kStageBytes + 4 * kChunkBytes + tl * kPRow
-                                       : kOffStage + (tl - 64) * kPRow);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int at = (s.part & 1) * 2 + j;
-        *reinterpret_cast<uint4*>(put + ((at ^ (key & 7)) << 4)) =
-            make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
-        *reinterpret_cast<uint4*>(put + (((4 + at) ^ (key & 7)) << 4)) =
-            make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]);
-      }
+      if (!s.ok) return;
+      uint8_t* put = put_at(st);
+      s.write_p(put, key, away, hi, lo);
       // Keys past the end: their V must be finite (0), a slot of each part.
       if (key0 + kKeys > w.len) {
         s.wait(&ctl->v_full[st], ph);
@@ -689,21 +728,14 @@ __device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
           for (int u = 0; u < 8; ++u) v[u] = make_uint4(0, 0, 0, 0);
         }
       }
-      tc::fence_proxy_async_smem();
-      tc::fence_before_sync();
-      if (away) {                                  // both warps of these 32 keys' rows
-        asm volatile("bar.sync %0, 64;" ::"r"(3 + s.quarter) : "memory");
-        if (s.lane == 0 && (s.part & 1) == 0)
-          tc::bulk_copy_to(tc::map_rank(smem + kOffP + key * kPRow, 1 - rank), put, 32 * kPRow,
-                           tc::map_rank(&ctl->p_in, 1 - rank));
-      }
-      __syncwarp();
-      if (s.lane == 0) {
-        if (rank == 0)
-          tc::mbar_arrive(&ctl->p_own);
-        else
-          tc::remote_arrive(tc::map_rank(&ctl->p_peer[1], 0));
-      }
+      s.send_p(put, place, away);
+      ++ps;
+    }
+    const int last = (int)((g - 1) & 1);
+    const uint32_t last_ph = (uint32_t)((g - 1) >> 1) & 1;
+    if (s.moved_or(&ctl->pv_done[last], last_ph, nt > 1)) {
+      again(g - 1, valid);
+      s.wait(&ctl->pv_done[last], last_ph);
     }
     // Row sums over both CTAs' keys, 1 / l and the LSE, then this CTA's dims.
     {
@@ -713,7 +745,7 @@ __device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
       dec::transpose_reduce32<false>(v, s.lane);
       ctl->red[s.quarter][s.part * 32 + s.lane] = v[0];
     }
-    soft_sync();
+    s.sync();
     const size_t slot = (size_t)(w.unit + block) * kRows;
     const int rows = (int)min((long long)kRows, a.N - (long long)block * kRows);
     if (s.gt < kRows) {
@@ -725,8 +757,8 @@ __device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
     } else {
       ++s.swaps;
     }
-    soft_sync();
-    s.wait(&ctl->pv_done[(g - 1) & 1], (uint32_t)((g - 1) >> 1) & 1);
+    s.sync();
+    if (!s.ok) return;
     tc::fence_after_sync();
 #pragma unroll 1
     for (int d = 0; d < 2; ++d) {                  // the two blocks of dims
@@ -767,13 +799,14 @@ wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
       tc::mbar_init(&ctl->swap_bar[b], 1);
       tc::mbar_init(&ctl->drain[b], 1);
       ctl->vote[b] = 0;
-      ctl->soft_word[b] = 0;
     }
-    tc::mbar_init(&ctl->p_own, kSoft / 32);
+    tc::mbar_init(&ctl->vote_in, kSoftWarps);
+    tc::mbar_init(&ctl->sync, kSoftWarps);
+    for (int q = 0; q < 4; ++q) tc::mbar_init(&ctl->pair[q], 2);
+    tc::mbar_init(&ctl->p_own, kSoftWarps);
     tc::mbar_init(&ctl->p_in, 1);
-    ctl->moves = 0;
     tc::mbar_init(&ctl->p_peer[0], 1);
-    tc::mbar_init(&ctl->p_peer[1], kSoft / 32);
+    tc::mbar_init(&ctl->p_peer[1], kSoftWarps);
     tc::mbar_init(&ctl->q_full, 2);
     tc::mbar_init(&ctl->q_empty, 1);
     ctl->abort_flag = 0;
@@ -815,8 +848,8 @@ wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
         relay(a, w, ctl);
     }
   } else if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsScout));
-    scout(a, w, ctl, tmem, rank);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsVote));
+    if (warp == 4 && lane == 0) vote(a, w, ctl, rank);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     softmax(a, w, smem, ctl, tmem, rank);
