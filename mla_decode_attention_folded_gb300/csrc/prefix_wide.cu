@@ -26,9 +26,9 @@
 // down to 2^-13 of absolute error. The running max is lazy as in decode_tc.cu
 // (moved when a score exceeds it by more than 8, to 2 below the new one) and
 // agreed between the CTAs of a pair, whose scores share accumulators: P is
-// computed and written as if no row moved; a vote of both CTAs follows it, which
-// only the PV of the tile waits for; where a row did move the softmax takes the
-// tile back and writes its P again with new maxima.
+// computed and written as if no row moved, and each warp's vote goes to the PV
+// issuer; where a row did move that says so instead of issuing, and the softmax
+// takes the tile back and writes its P again with new maxima.
 //
 // Work: the tiles of all row blocks, block after block, are one sequence cut
 // into equal parts, one per pair; a part's piece of a block goes to partial
@@ -48,16 +48,15 @@ using dec::kStageBytes;
 
 constexpr int kRows = kWideRows;              // query rows per block: the MMA's N
 constexpr int kKeys = kWideKeys;              // keys per tile, half of them per CTA
-// Six warpgroups: two TMA warps, the S and PV (or relay) warps; the vote warp and
-// three idle ones; four groups of softmax warps. Registers move to the softmax
-// (32 row sums and 16 words of codes a thread) from the others: the launch's
-// 6 x 80 a thread go 64 + 32 + 4 x 96.
+// Five warpgroups: two TMA warps and two for S and PV (rank 0) or the relays (rank
+// 1); four of softmax warps. Registers move to the softmax (32 row sums and 16
+// words of codes a thread) from the first: the launch's 5 x 96 a thread go 64 +
+// 4 x 104.
 constexpr int kSoft = 512;                    // softmax threads: a key and 32 rows each
 constexpr int kSoftWarps = kSoft / 32;
-constexpr int kThreads = 256 + kSoft;
-constexpr int kRegsIssue = 64, kRegsVote = 32, kRegsSoft = 96;
-static_assert(kRegsIssue + kRegsVote + 4 * kRegsSoft <= 6 * (65536 / kThreads / 8 * 8),
-              "register pool");
+constexpr int kThreads = 128 + kSoft;
+constexpr int kRegsIssue = 64, kRegsSoft = 104;
+static_assert(kRegsIssue + 4 * kRegsSoft <= 5 * (65536 / kThreads / 8 * 8), "register pool");
 constexpr int kQChunk = 64 * 128;             // this CTA's 64 rows x 128 dims
 constexpr int kQBytes = 64 * kDqk;
 constexpr int kPRow = 128;                    // a key's 64 hi codes, then its 64 lo codes
@@ -81,22 +80,20 @@ struct WideCtl {
   uint64_t s_full[2];      // MMA -> softmax, TMA: S of a tile done
   uint64_t p_own;          // rank 0: softmax -> PV: P of CTA 0's keys written or under way
   uint64_t p_in;           // bulk copies of the other CTA -> PV, relay: P of its keys landed
-  uint64_t p_peer[2];      // rank 0: P of CTA 0's keys (and V for it) complete in rank 1; its
+  uint64_t v_peer[2];      // rank 0: V complete in rank 1
+  uint64_t p_peer[2];      // rank 0: P of CTA 0's keys complete in rank 1; its
                            // softmax: P of CTA 1's keys written or under way
   uint64_t pv_half[2];     // MMA -> softmax of rank 0, TMA: O holds CTA 0's keys of the tile
   uint64_t pv_done[2];     // MMA -> softmax, TMA: O holds the tile; P and the stage are free
   uint64_t q_full;         // rank 0: TMA of both CTAs -> S
   uint64_t q_empty;        // MMA -> TMA
-  uint64_t vote_in;        // softmax -> vote warp: this CTA's votes on a tile
-  uint64_t vote_bar[2];    // the other CTA's flag is in vote_peer
-  uint64_t told[2];        // vote warp -> PV, relay, softmax: verdict
+  uint64_t votes[2];       // rank 0: softmax of rank 1 -> PV: its votes are in vote[1]
   uint64_t sync;           // softmax among themselves (a bounded barrier)
   uint64_t pair[4];        // the two warps that send a quarter's P to the other CTA
   uint64_t swap_bar[2];    // the other CTA's row values are in swap
   uint64_t drain[2];
-  uint32_t vote_peer[2];
-  uint32_t vote[2];        // kMoved of this CTA's softmax
-  uint32_t verdict[2];     // of the pair: whether a row moved
+  uint32_t vote[2][2];     // rank 0: whether CTA i saw a row move, for two votes
+  uint32_t moved;          // how many tiles PV sent back
   uint32_t tmem_base;
   int abort_flag;
   alignas(16) float neg_max[kRows]; // minus the running row max (base-2 scores), read four at a time
@@ -107,7 +104,6 @@ struct WideCtl {
 static_assert(offsetof(WideCtl, neg_max) % 16 == 0, "16-byte reads");
 constexpr int kSmemBytes = kOffCtl + (int)sizeof(WideCtl) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-constexpr uint32_t kMoved = 1;
 
 __device__ __forceinline__ bool w_wait(uint64_t* bar, uint32_t parity, WideCtl* ctl,
                                        int32_t* status) {
@@ -244,35 +240,32 @@ __device__ void load_values(const WideArgs& a, const WidePart& w, uint8_t* smem,
   }
 }
 
-// Waits for the verdict on a tile: -1 if the wait ran out, else whether a row moved.
-__device__ __forceinline__ int wait_verdict(uint32_t vote, WideCtl* ctl, int32_t* status) {
-  if (!w_wait(&ctl->told[vote & 1], (vote >> 1) & 1, ctl, status)) return -1;
-  return (int)(peek(&ctl->verdict[vote & 1]) & kMoved);
+// Rank 1 tells rank 0's PV issuer what is complete here: V of each tile, and P of
+// CTA 0's keys each time it is written (twice for a tile that PV sent back; the
+// last tile's PV ends it).
+__device__ void relay_values(const WideArgs& a, const WidePart& w, WideCtl* ctl) {
+  for (long long i = 0; i < w.end - w.begin; ++i) {
+    if (!w_wait(&ctl->v_full[i & 1], (uint32_t)(i >> 1) & 1, ctl, a.status)) return;
+    tc::remote_arrive(tc::map_rank(&ctl->v_peer[i & 1], 0));
+  }
 }
-
-// Rank 1: tells rank 0's PV issuer that P of CTA 0's keys and V for it are here;
-// twice for a tile whose P is written again.
-__device__ void relay(const WideArgs& a, const WidePart& w, WideCtl* ctl) {
-  const long long n = w.end - w.begin;
+__device__ void relay_p(const WideArgs& a, const WidePart& w, WideCtl* ctl) {
+  const long long n = w.end - w.begin, last = n - 1;
   const uint32_t to = tc::map_rank(&ctl->p_peer[0], 0);
-  int tile = (int)(w.begin % w.tiles);
-  bool first = true;
-  uint32_t votes = 0, ps = 0;
-  for (long long i = 0; i < n; ++i) {
+  for (long long k = 0;; ++k) {
     tc::mbar_arrive_expect_tx(&ctl->p_in, 128 * kPRow);
-    if (!w_wait(&ctl->v_full[i & 1], (uint32_t)(i >> 1) & 1, ctl, a.status) ||
-        !w_wait(&ctl->p_in, ps++ & 1, ctl, a.status))
-      return;
-    const int moved = first ? 0 : wait_verdict(votes++, ctl, a.status);
-    if (moved < 0) return;
-    if (moved) tc::mbar_arrive_expect_tx(&ctl->p_in, 128 * kPRow);
-    tc::remote_arrive(to);
-    if (moved) {
-      if (!w_wait(&ctl->p_in, ps++ & 1, ctl, a.status)) return;
-      tc::remote_arrive(to);
+    const unsigned long long t0 = tc::globaltimer_ns();
+    while (!tc::mbar_try_wait(&ctl->p_in, (uint32_t)k & 1)) {
+      // Every tile's last write has been told of: its PV ends this.
+      if (k - peek(&ctl->moved) >= n && tc::mbar_test_wait(&ctl->pv_done[last & 1], (uint32_t)(last >> 1) & 1)) return;
+      const bool expired = tc::globaltimer_ns() - t0 > kTimeoutNs;
+      if (*reinterpret_cast<volatile int*>(&ctl->abort_flag) || expired) {
+        *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
+        if (expired && a.status) atomicOr(a.status, MLA_FAULT_WAIT_TIMEOUT);
+        return;
+      }
     }
-    if (++tile == w.tiles) tile = 0;
-    first = tile == 0;
+    tc::remote_arrive(to);
   }
 }
 
@@ -326,7 +319,7 @@ __device__ void issue_pv(const WideArgs& a, const WidePart& w, uint8_t* smem, Wi
   const long long n = w.end - w.begin;
   int tile = (int)(w.begin % w.tiles);
   bool first = true;                               // the pair's first tile of the block
-  uint32_t votes = 0, ps = 0;                      // verdicts before this tile, writes of P
+  uint32_t votes = 0, ps = 0;                      // votes before this tile, writes of P
   bool ok = true;
   for (long long i = 0; ok && i < n; ++i) {
     const int st = i & 1;
@@ -357,21 +350,27 @@ __device__ void issue_pv(const WideArgs& a, const WidePart& w, uint8_t* smem, Wi
     // where the maxima moved) or V (keys past a block's end are cleared).
     bool both = first || tile == w.tiles - 1;
     wait(&ctl->p_own, ps & 1);
-    wait(&ctl->p_peer[0], ps & 1);
+    if (!first) wait(&ctl->votes[votes & 1], (votes >> 1) & 1);
     if (!first && ok) {
-      const int moved = wait_verdict(votes++, ctl, a.status);
-      if (moved < 0) break;
-      if (moved) {                                 // that P is void: another follows
+      const int b = votes++ & 1;
+      if (peek(&ctl->vote[0][b]) | peek(&ctl->vote[1][b])) {
+        // A row moved: that P is void, another follows.
+        wait(&ctl->p_peer[0], ps & 1);
         wait(&ctl->p_peer[1], ps & 1);
         wait(&ctl->p_in, ps & 1);
         if (!ok) break;
         ++ps;
         tc::mbar_arrive_expect_tx(&ctl->p_in, 128 * kPRow);
+        for (int c = 0; c < 2; ++c) *reinterpret_cast<volatile uint32_t*>(&ctl->vote[c][b]) = 0;
+        const uint32_t count = peek(&ctl->moved) + 1;
+        tc::remote_st(tc::map_rank(&ctl->moved, 1), count);
+        *reinterpret_cast<volatile uint32_t*>(&ctl->moved) = count;
         wait(&ctl->p_own, ps & 1);
-        wait(&ctl->p_peer[0], ps & 1);
         both = true;
       }
     }
+    wait(&ctl->p_peer[0], ps & 1);
+    wait(&ctl->v_peer[st], ph);
     if (both) wait(&ctl->p_peer[1], ps & 1);
     if (!ok) break;
     half(0, first);
@@ -389,33 +388,6 @@ __device__ void issue_pv(const WideArgs& a, const WidePart& w, uint8_t* smem, Wi
   mma_drain(&ctl->drain[1]);
 }
 
-// ---------------------------------------------------------------- votes
-// One thread: after this CTA's softmax has cast its votes on a tile, exchanges
-// them with the other CTA and tells the verdict.
-__device__ void vote(const WideArgs& a, const WidePart& w, WideCtl* ctl, uint32_t rank) {
-  const long long n = w.end - w.begin;
-  int tile = (int)(w.begin % w.tiles);
-  bool first = true;
-  uint32_t votes = 0;
-  for (long long i = 0; i < n; ++i) {
-    if (!first) {
-      const int b = votes & 1;
-      if (!w_wait(&ctl->vote_in, votes & 1, ctl, a.status)) return;
-      uint32_t mine = peek(&ctl->vote[b]);
-      *reinterpret_cast<volatile uint32_t*>(&ctl->vote[b]) = 0;
-      tc::mbar_arrive_expect_tx(&ctl->vote_bar[b], 4);
-      tc::remote_st_async(tc::map_rank(&ctl->vote_peer[b], 1 - rank), mine,
-                          tc::map_rank(&ctl->vote_bar[b], 1 - rank));
-      if (!w_wait(&ctl->vote_bar[b], (votes >> 1) & 1, ctl, a.status)) return;
-      *reinterpret_cast<volatile uint32_t*>(&ctl->verdict[b]) = mine | peek(&ctl->vote_peer[b]);
-      tc::mbar_arrive(&ctl->told[b]);
-      ++votes;
-    }
-    if (++tile == w.tiles) tile = 0;
-    first = tile == 0;
-  }
-}
-
 // ---------------------------------------------------------------- softmax
 // Every wait here is bounded, barriers among the softmax warps included: a
 // thread whose wait runs out leaves, and the others' next one ends by the abort
@@ -425,14 +397,14 @@ struct Soft {
   WideCtl* ctl;
   uint32_t tmem, rank;
   int quarter, part, lane, gt;                     // rows 32 part .. 32 part + 31
-  uint32_t swaps = 0, votes = 0, syncs = 0, sends = 0;
+  uint32_t swaps = 0, votes = 0, syncs = 0, sends = 0, moves = 0;
   bool ok = true;                                  // warp-uniform
 
   __device__ Soft(const WideArgs& a_, WideCtl* c, uint32_t t, uint32_t r)
       : a(a_), ctl(c), tmem(t), rank(r) {
     const int warp = threadIdx.x >> 5;
     quarter = warp & 3;
-    gt = threadIdx.x - 256;
+    gt = threadIdx.x - 128;
     part = gt >> 7;
     lane = threadIdx.x & 31;
   }
@@ -608,26 +580,32 @@ struct Soft {
         tc::remote_arrive(tc::map_rank(&ctl->p_peer[1], 0));
     }
   }
-  // Casts this CTA's votes on a tile.
+  // This warp's vote on a tile, to the PV issuer: CTA 0's go with its P.
   __device__ void cast(bool moved) {
     const bool any = __any_sync(0xffffffffu, moved);
     if (lane == 0) {
-      if (any) atomicOr(&ctl->vote[votes & 1], kMoved);
-      tc::mbar_arrive(&ctl->vote_in);
+      uint32_t* word = &ctl->vote[rank][votes & 1];
+      if (rank == 0) {
+        if (any) *reinterpret_cast<volatile uint32_t*>(word) = 1;
+      } else {
+        if (any) {
+          tc::remote_st(tc::map_rank(word, 0), 1);
+          tc::fence_cluster();
+        }
+        tc::remote_arrive(tc::map_rank(&ctl->votes[votes & 1], 0));
+      }
     }
     ++votes;
   }
-  // Waits until PV of the tile that was voted on last is done with `bar`'s part,
-  // or the verdict on it says that a row moved (true): PV then has not begun.
-  __device__ bool moved_or(uint64_t* bar, uint32_t parity, bool voted) {
-    bool moved = false;
+  // Waits until PV of the previous tile is done with `bar`'s part, or has sent the
+  // tile back (true) instead of beginning.
+  __device__ bool moved_or(uint64_t* bar, uint32_t parity) {
+    bool back = false;
     if (ok) {
-      const uint32_t v = votes - 1;
       const unsigned long long t0 = tc::globaltimer_ns();
       while (!tc::mbar_try_wait(bar, parity)) {
-        if (voted && tc::mbar_test_wait(&ctl->told[v & 1], (v >> 1) & 1) &&
-            (peek(&ctl->verdict[v & 1]) & kMoved)) {
-          moved = true;
+        if (peek(&ctl->moved) != moves) {
+          back = true;
           break;
         }
         const bool expired = tc::globaltimer_ns() - t0 > kTimeoutNs;
@@ -640,7 +618,9 @@ struct Soft {
       }
     }
     ok = __all_sync(0xffffffffu, ok);
-    return __any_sync(0xffffffffu, moved);
+    back = __any_sync(0xffffffffu, back);
+    moves += back ? 1 : 0;
+    return back;
   }
 };
 
@@ -699,18 +679,19 @@ __device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
         s.move(st, valid, lp, -1);
         s.weigh(st, valid, lp, hi, lo);
       } else {
-        float most = s.weigh(st, valid, lp, hi, lo);
+        s.cast(s.weigh(st, valid, lp, hi, lo) > 8.f);
         // The place of P of these keys is free once PV of the previous tile is
-        // done with it; if that tile moved it is done again first.
+        // done with it; if that tile came back it is done again first. (The votes on
+        // this one were then cast on maxima that only grew since: at worst it comes
+        // back for nothing.)
         uint64_t* bar = rank == 0 ? &ctl->pv_half[(g - 1) & 1] : &ctl->pv_done[(g - 1) & 1];
         const uint32_t bph = (uint32_t)((g - 1) >> 1) & 1;
-        if (s.moved_or(bar, bph, t > 1)) {
+        if (s.moved_or(bar, bph)) {
           s.unweigh(st, valid, lp);
           again(g - 1, true);
-          most = s.weigh(st, valid, lp, hi, lo);
+          s.weigh(st, valid, lp, hi, lo);
           s.wait(bar, bph);
         }
-        s.cast(most > 8.f);
       }
       if (t == 0 && g > 0)
         s.wait(rank == 0 ? &ctl->pv_half[(g - 1) & 1] : &ctl->pv_done[(g - 1) & 1],
@@ -733,7 +714,7 @@ __device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
     }
     const int last = (int)((g - 1) & 1);
     const uint32_t last_ph = (uint32_t)((g - 1) >> 1) & 1;
-    if (s.moved_or(&ctl->pv_done[last], last_ph, nt > 1)) {
+    if (s.moved_or(&ctl->pv_done[last], last_ph)) {
       again(g - 1, valid);
       s.wait(&ctl->pv_done[last], last_ph);
     }
@@ -794,13 +775,13 @@ wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
       tc::mbar_init(&ctl->s_full[b], 1);
       tc::mbar_init(&ctl->pv_half[b], 1);
       tc::mbar_init(&ctl->pv_done[b], 1);
-      tc::mbar_init(&ctl->vote_bar[b], 1);
-      tc::mbar_init(&ctl->told[b], 1);
+      tc::mbar_init(&ctl->v_peer[b], 1);
+      tc::mbar_init(&ctl->votes[b], kSoftWarps);
       tc::mbar_init(&ctl->swap_bar[b], 1);
       tc::mbar_init(&ctl->drain[b], 1);
-      ctl->vote[b] = 0;
+      ctl->vote[0][b] = ctl->vote[1][b] = 0;
     }
-    tc::mbar_init(&ctl->vote_in, kSoftWarps);
+    ctl->moved = 0;
     tc::mbar_init(&ctl->sync, kSoftWarps);
     for (int q = 0; q < 4; ++q) tc::mbar_init(&ctl->pair[q], 2);
     tc::mbar_init(&ctl->p_own, kSoftWarps);
@@ -844,12 +825,11 @@ wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
         issue_s(a, w, smem, ctl, tmem);
       else if (rank == 0)
         issue_pv(a, w, smem, ctl, tmem);
-      else if (warp == 2)
-        relay(a, w, ctl);
+      else if (warp == 1)
+        relay_values(a, w, ctl);
+      else
+        relay_p(a, w, ctl);
     }
-  } else if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsVote));
-    if (warp == 4 && lane == 0) vote(a, w, ctl, rank);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     softmax(a, w, smem, ctl, tmem, rank);

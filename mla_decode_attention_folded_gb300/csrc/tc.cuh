@@ -254,6 +254,12 @@ __device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
+__device__ __forceinline__ void remote_st(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void fence_cluster() {
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
 // Arrival on a barrier of the cluster. It orders this CTA's own shared memory
 // (CTA-scope release); data for another CTA's memory goes by remote_st_async.
 __device__ __forceinline__ void remote_arrive(uint32_t bar) {
