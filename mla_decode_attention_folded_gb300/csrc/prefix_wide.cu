@@ -3,32 +3,30 @@
 //
 // Bound by the FP8 tensor pipe: 2 * 1088 FLOP per (row, key) beside 576 bytes
 // per key. What sets the shape is TMEM: a 512-dim FP32 accumulator of 128 rows
-// fills an SM's 512 columns, and MMAs of fewer than 128 columns run at half
-// the rate. A pair of CTAs (tcgen05 cta_group::2) therefore shares a block of
-// 128 rows and splits the 512 value dims:
+// fills an SM's 512 columns. A pair of CTAs (tcgen05 cta_group::2) therefore
+// shares a block of 128 rows, 64 in each CTA: an MMA of M = 128 over the pair
+// keeps a CTA's 64 rows in all 128 lanes (lanes 0-63 its first N / 2 columns,
+// lanes 64-127 the others), so O takes 256 columns beside two S buffers of 128,
+// and at N = 256 runs at the pipe's full rate (66 cycles per instruction
+// measured; an M = 128, N = 64 MMA of one CTA takes 50 for a quarter of it).
 //
-//   S^T[256 keys, 128 rows]  = K[256, 576] . Q[128, 576]^T    18 MMAs, M = 256, N = 128
-//   O^T[512 dims, 128 rows] += V^T[512, 256] . P^T[256, 128]  2 x 16 MMAs, M = 256, N = 128
+//   S[128 rows, 256 keys]  = Q[128, 576] . K[256, 576]^T      18 MMAs
+//   O[128 rows, 512 dims] += P[128, 256] . V[256, 512]        2 dim halves x 16 MMAs
 //
-// CTA c computes S for keys 128 c .. 128 c + 127 of a 256-key tile (its TMEM
-// lanes) and O for value dims 256 c .. 256 c + 255: 256 columns of O beside two
-// S buffers of 128. Both operands of the second product are in place: a KV
-// stage holds the CTA's own 128 keys for S (four 128-dim bands and the rope);
-// once S is done its two bands of the other CTA's dims are overwritten with
-// the other CTA's keys of its own dims, so the slots (i, key half) of V lie at
-// the same offsets in both CTAs, as the pair's MMA wants. P^T is split by
-// rows: CTA c holds rows 64 c .. 64 c + 63 for all 256 keys, each CTA writing
-// its keys' half of the rows into the other's shared memory.
+// Rows never leave their CTA: softmax, maxima and sums are its own. B is split
+// over the pair: CTA c brings keys 128 c .. 128 c + 127 of a 256-key tile to S,
+// and dims 256 c .. 256 c + 255 of all 256 keys to PV. A KV stage holds the CTA's
+// own keys (four 128-dim bands and the rope); once S is done with them, its two
+// bands of the other CTA's dims are overwritten with the other CTA's keys of its
+// own dims, so that V of (dim half i, keys of CTA h) lies in slot 2 h + i in both
+// CTAs, as the pair's MMA wants, and two stages fit.
 //
 // P enters the product as an E4M3 and an E5M2 term: p16 = fp16(p), hi =
 // e4m3(p16), lo = e5m2(p16 - hi). E5M2's range keeps the second term where hi
 // is subnormal (p < 2^-6, absolute step 2^-9), so hi + lo is p to 2^-7 relative
 // down to 2^-13 of absolute error. The running max is lazy as in decode_tc.cu
-// (moved when a score exceeds it by more than 8, to 2 below the new one) and
-// agreed between the CTAs of a pair, whose scores share accumulators: P is
-// computed and written as if no row moved, and each warp's vote goes to the PV
-// issuer; where a row did move that says so instead of issuing, and the softmax
-// takes the tile back and writes its P again with new maxima.
+// (moved when a score exceeds it by more than 8, to 2 below the new one); P is
+// computed as if no row moved and once more where one did.
 //
 // Work: the tiles of all row blocks, block after block, are one sequence cut
 // into equal parts, one per pair; a part's piece of a block goes to partial
@@ -46,62 +44,39 @@ using dec::kChunkBytes;      // 128 keys x 128 dims
 using dec::kRopeBytes;       // 128 keys x 64 dims
 using dec::kStageBytes;
 
-constexpr int kRows = kWideRows;              // query rows per block: the MMA's N
-constexpr int kKeys = kWideKeys;              // keys per tile, half of them per CTA
-// Five warpgroups: two TMA warps and two for S and PV (rank 0) or the relays (rank
-// 1); four of softmax warps. Registers move to the softmax (32 row sums and 16
-// words of codes a thread) from the first: the launch's 5 x 96 a thread go 64 +
-// 4 x 104.
-constexpr int kSoft = 512;                    // softmax threads: a key and 32 rows each
-constexpr int kSoftWarps = kSoft / 32;
-constexpr int kThreads = 128 + kSoft;
-constexpr int kRegsIssue = 64, kRegsSoft = 104;
-static_assert(kRegsIssue + 4 * kRegsSoft <= 5 * (65536 / kThreads / 8 * 8), "register pool");
+constexpr int kRows = kWideRows;              // query rows per block, half of them per CTA
+constexpr int kKeys = kWideKeys;              // keys per tile
+constexpr int kSoft = 512;                    // softmax threads: a row and 32 keys each
+constexpr int kThreads = 128 + kSoft;         // + two TMA warps, the S and the PV warp
 constexpr int kQChunk = 64 * 128;             // this CTA's 64 rows x 128 dims
 constexpr int kQBytes = 64 * kDqk;
-constexpr int kPRow = 128;                    // a key's 64 hi codes, then its 64 lo codes
-constexpr int kPBytes = kKeys * kPRow;
+constexpr int kPChunk = 64 * 128;             // 64 rows x 128 keys of one term
 constexpr int kOffQ = 2 * kStageBytes;
-constexpr int kOffP = kOffQ + kQBytes;
-constexpr int kOffStage = kOffP + kPBytes;    // P of keys 64 .. 127 on its way to the other CTA
-constexpr int kOffCtl = kOffStage + 64 * kPRow;
-static_assert(64 * kPRow <= kRopeBytes, "the first 64 keys' P waits in the rope's place");
+constexpr int kOffP = kOffQ + kQBytes;        // hi of CTA 0's and CTA 1's keys, then lo
+constexpr int kOffCtl = kOffP + 4 * kPChunk;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kSCol = 256;                    // S buffers after O's two blocks of 128 columns
+constexpr int kSCol = 256;                    // S buffers after O's two halves of 128 columns
 constexpr unsigned long long kTimeoutNs = 2000000000ull;
-constexpr uint32_t kIdescS = tc::idesc_e4m3_f32(256, kRows, false, false);
-constexpr uint32_t kIdescHi = tc::idesc_e4m3_f32(256, kRows, true, true);
-constexpr uint32_t kIdescLo = kIdescHi | (1u << 10);      // B in E5M2
+constexpr uint32_t kIdescS = tc::idesc_e4m3_f32(kRows, kKeys, false, false);
+constexpr uint32_t kIdescHi = tc::idesc_e4m3_f32(kRows, 256, false, true);
+constexpr uint32_t kIdescLo = kIdescHi | (1u << 7);       // A in E5M2
 static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms need 1 KB alignment");
 
 struct WideCtl {
   uint64_t k_full[2];      // rank 0: TMA of both CTAs -> S: both CTAs' keys landed
-  uint64_t v_full[2];      // TMA -> PV, relay: the other CTA's keys of the own dims landed
+  uint64_t v_full[2];      // rank 0: TMA of both CTAs -> PV: V complete in both
+  uint64_t v_tail[2];      // TMA -> softmax, TMA warp: V of a block's last tile landed here
   uint64_t s_full[2];      // MMA -> softmax, TMA: S of a tile done
-  uint64_t p_own;          // rank 0: softmax -> PV: P of CTA 0's keys written or under way
-  uint64_t p_in;           // bulk copies of the other CTA -> PV, relay: P of its keys landed
-  uint64_t v_peer[2];      // rank 0: V complete in rank 1
-  uint64_t p_peer[2];      // rank 0: P of CTA 0's keys complete in rank 1; its
-                           // softmax: P of CTA 1's keys written or under way
-  uint64_t pv_half[2];     // MMA -> softmax of rank 0, TMA: O holds CTA 0's keys of the tile
+  uint64_t p_full[2];      // rank 0: softmax of both CTAs -> PV: P of CTA h's keys written
+  uint64_t pv_half[2];     // MMA -> softmax, TMA: O holds CTA 0's keys of the tile
   uint64_t pv_done[2];     // MMA -> softmax, TMA: O holds the tile; P and the stage are free
   uint64_t q_full;         // rank 0: TMA of both CTAs -> S
   uint64_t q_empty;        // MMA -> TMA
-  uint64_t votes[2];       // rank 0: softmax of rank 1 -> PV: its votes are in vote[1]
-  uint64_t sync;           // softmax among themselves (a bounded barrier)
-  uint64_t pair[4];        // the two warps that send a quarter's P to the other CTA
-  uint64_t swap_bar[2];    // the other CTA's row values are in swap
   uint64_t drain[2];
-  uint32_t vote[2][2];     // rank 0: whether CTA i saw a row move, for two votes
-  uint32_t moved;          // how many tiles PV sent back
   uint32_t tmem_base;
   int abort_flag;
-  alignas(16) float neg_max[kRows]; // minus the running row max (base-2 scores), read four at a time
-  alignas(16) float vec[kRows];     // rescale factors, then 1 / l
-  float red[4][kRows];
-  float swap[2][kRows];
+  float red[8][64];        // row values of the eight threads that share a row
 };
-static_assert(offsetof(WideCtl, neg_max) % 16 == 0, "16-byte reads");
 constexpr int kSmemBytes = kOffCtl + (int)sizeof(WideCtl) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
@@ -119,8 +94,18 @@ __device__ __forceinline__ bool w_wait(uint64_t* bar, uint32_t parity, WideCtl* 
     }
   }
 }
-__device__ __forceinline__ uint32_t peek(const uint32_t* p) {
-  return *reinterpret_cast<const volatile uint32_t*>(p);
+__device__ __forceinline__ void soft_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kSoft) : "memory");
+}
+__device__ __forceinline__ bool soft_any(bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
+      " bar.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)pred), "n"(kSoft)
+      : "memory");
+  return r != 0;
 }
 
 // ---------------------------------------------------------------- loads
@@ -152,9 +137,9 @@ struct Pages {
   }
 };
 
-// Own keys (and Q at each block's start), counted on rank 0's barriers. A
-// stage's bands 0-1 hold V of CTA 0's keys, which PV is done with first, bands
-// 2-3 that of CTA 1's; the rope's place holds P on its way until the end.
+// Own keys (and Q at each block's start). A stage's bands 0-1 hold V of CTA 0's
+// keys, which PV is done with first, bands 2-3 that of CTA 1's: it is refilled in
+// two parts.
 __device__ void load_keys(const WideArgs& a, const WidePart& w, uint8_t* smem, WideCtl* ctl,
                           uint32_t rank, const CUtensorMap* tm_kv, const CUtensorMap* tm_kvr,
                           const CUtensorMap* tm_q, const CUtensorMap* tm_qr) {
@@ -214,58 +199,42 @@ __device__ void load_keys(const WideArgs& a, const WidePart& w, uint8_t* smem, W
   }
 }
 
-// The other CTA's keys of the own value dims, over the bands S is done with.
+// The other CTA's keys of the own value dims, over the bands S is done with. In a
+// block's last tile the softmax clears V behind the last key, so that must have
+// landed here before rank 0 hears of it.
 __device__ void load_values(const WideArgs& a, const WidePart& w, uint8_t* smem, WideCtl* ctl,
                             uint32_t rank, const CUtensorMap* tm_kv) {
   const int lane = threadIdx.x & 31;
   const long long n = w.end - w.begin;
   const uint32_t other = 1 - rank;
   Pages pages(a, w, false);
+  int tile = (int)(w.begin % w.tiles);
+  uint32_t tails = 0;                              // parity of each stage's tails so far
   bool ok = true;
   for (long long i = 0; ok && i < n; ++i) {
     const int st = i & 1;
     const int cur = pages.take(i + 1 < n);
     const int p0 = __shfl_sync(0xffffffffu, cur, 2 * other);
     const int p1 = __shfl_sync(0xffffffffu, cur, 2 * other + 1);
+    const bool tail = tile == w.tiles - 1;
+    if (++tile == w.tiles) tile = 0;
     if (lane == 0 && (ok = w_wait(&ctl->s_full[st], (uint32_t)(i >> 1) & 1, ctl, a.status))) {
       uint8_t* stage = smem + st * kStageBytes;
-      tc::mbar_arrive_expect_tx(&ctl->v_full[st], ((p0 >= 0) + (p1 >= 0)) * 2 * kPage * 128);
+      const uint32_t there = tc::map_rank(&ctl->v_full[st], 0);
+      const uint32_t bar = tail ? tc::map_rank(&ctl->v_tail[st], rank) : there;
+      tc::remote_arrive_expect_tx(bar, ((p0 >= 0) + (p1 >= 0)) * 2 * kPage * 128);
       for (int h = 0; h < 2; ++h)
         for (int d = 0; d < 2; ++d)
           if ((h ? p1 : p0) >= 0)
-            tc::tma_load_2d(stage + (2 * other + d) * kChunkBytes + h * (kChunkBytes / 2), tm_kv,
-                            &ctl->v_full[st], (2 * rank + d) * 128, (h ? p1 : p0) * kPage);
-    }
-    ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-  }
-}
-
-// Rank 1 tells rank 0's PV issuer what is complete here: V of each tile, and P of
-// CTA 0's keys each time it is written (twice for a tile that PV sent back; the
-// last tile's PV ends it).
-__device__ void relay_values(const WideArgs& a, const WidePart& w, WideCtl* ctl) {
-  for (long long i = 0; i < w.end - w.begin; ++i) {
-    if (!w_wait(&ctl->v_full[i & 1], (uint32_t)(i >> 1) & 1, ctl, a.status)) return;
-    tc::remote_arrive(tc::map_rank(&ctl->v_peer[i & 1], 0));
-  }
-}
-__device__ void relay_p(const WideArgs& a, const WidePart& w, WideCtl* ctl) {
-  const long long n = w.end - w.begin, last = n - 1;
-  const uint32_t to = tc::map_rank(&ctl->p_peer[0], 0);
-  for (long long k = 0;; ++k) {
-    tc::mbar_arrive_expect_tx(&ctl->p_in, 128 * kPRow);
-    const unsigned long long t0 = tc::globaltimer_ns();
-    while (!tc::mbar_try_wait(&ctl->p_in, (uint32_t)k & 1)) {
-      // Every tile's last write has been told of: its PV ends this.
-      if (k - peek(&ctl->moved) >= n && tc::mbar_test_wait(&ctl->pv_done[last & 1], (uint32_t)(last >> 1) & 1)) return;
-      const bool expired = tc::globaltimer_ns() - t0 > kTimeoutNs;
-      if (*reinterpret_cast<volatile int*>(&ctl->abort_flag) || expired) {
-        *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
-        if (expired && a.status) atomicOr(a.status, MLA_FAULT_WAIT_TIMEOUT);
-        return;
+            tc::tma_load_2d_pair(stage + (2 * other + d) * kChunkBytes + h * (kChunkBytes / 2), tm_kv,
+                                 bar, (2 * rank + d) * 128, (h ? p1 : p0) * kPage);
+      if (tail) {
+        ok = w_wait(&ctl->v_tail[st], (tails >> st) & 1, ctl, a.status);
+        tc::remote_arrive(there);
       }
     }
-    tc::remote_arrive(to);
+    if (tail) tails ^= 1u << st;
+    ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
   }
 }
 
@@ -294,18 +263,18 @@ __device__ void issue_s(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
     // whose P the softmax wrote after it had read that S.
     if (!w_wait(&ctl->k_full[st], (uint32_t)(i >> 1) & 1, ctl, a.status)) break;
     tc::fence_after_sync();
-    const uint32_t kv = s_kv + st * kStageBytes, d = tmem + kSCol + st * kRows;
+    const uint32_t kv = s_kv + st * kStageBytes, d = tmem + kSCol + st * 128;
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        tc::mma_f8_pair(d, tc::smem_desc(kv + c * kChunkBytes + kk * 32, 16, 1024, tc::kSw128),
-                        tc::smem_desc(s_q + c * kQChunk + kk * 32, 16, 1024, tc::kSw128), kIdescS,
+        tc::mma_f8_pair(d, tc::smem_desc(s_q + c * kQChunk + kk * 32, 16, 1024, tc::kSw128),
+                        tc::smem_desc(kv + c * kChunkBytes + kk * 32, 16, 1024, tc::kSw128), kIdescS,
                         (c | kk) != 0);
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk)
-      tc::mma_f8_pair(d, tc::smem_desc(kv + 4 * kChunkBytes + kk * 32, 16, 512, tc::kSw64),
-                      tc::smem_desc(s_q + 4 * kQChunk + kk * 32, 16, 512, tc::kSw64), kIdescS, true);
+      tc::mma_f8_pair(d, tc::smem_desc(s_q + 4 * kQChunk + kk * 32, 16, 512, tc::kSw64),
+                      tc::smem_desc(kv + 4 * kChunkBytes + kk * 32, 16, 512, tc::kSw64), kIdescS, true);
     tc::mma_commit_pair(&ctl->s_full[st]);
     if (++tile == w.tiles) tile = 0;
     if (tile == 0) tc::mma_commit_pair(&ctl->q_empty);
@@ -319,69 +288,30 @@ __device__ void issue_pv(const WideArgs& a, const WidePart& w, uint8_t* smem, Wi
   const long long n = w.end - w.begin;
   int tile = (int)(w.begin % w.tiles);
   bool first = true;                               // the pair's first tile of the block
-  uint32_t votes = 0, ps = 0;                      // votes before this tile, writes of P
   bool ok = true;
   for (long long i = 0; ok && i < n; ++i) {
     const int st = i & 1;
-    const uint32_t ph = (uint32_t)(i >> 1) & 1;
-    tc::mbar_arrive_expect_tx(&ctl->p_in, 128 * kPRow);
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      ok = ok && w_wait(bar, parity, ctl, a.status);
-    };
-    auto half = [&](int kh, bool fresh) {
+    ok = w_wait(&ctl->v_full[st], (uint32_t)(i >> 1) & 1, ctl, a.status);
+#pragma unroll
+    for (int kh = 0; kh < 2; ++kh) {               // CTA 0's keys, then CTA 1's
+      ok = ok && w_wait(&ctl->p_full[kh], (uint32_t)i & 1, ctl, a.status);
+      if (!ok) break;
       tc::fence_after_sync();
       const uint32_t kv = s_kv + st * kStageBytes;
 #pragma unroll
       for (int d = 0; d < 2; ++d)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          const uint64_t va = tc::smem_desc(kv + (kh * 2 + d) * kChunkBytes + kk * 32 * 128,
-                                            kChunkBytes, 1024, tc::kSw128);
-          const uint32_t pk = s_p + (kh * 128 + kk * 32) * kPRow;
-          tc::mma_f8_pair(tmem + d * kRows, va, tc::smem_desc(pk, kPBytes, 1024, tc::kSw128), kIdescHi,
-                          !(fresh && kk == 0));
-          tc::mma_f8_pair(tmem + d * kRows, va, tc::smem_desc(pk + 64, kPBytes, 1024, tc::kSw128),
+          const uint64_t v = tc::smem_desc(kv + (kh * 2 + d) * kChunkBytes + kk * 32 * 128,
+                                           kChunkBytes, 1024, tc::kSw128);
+          const uint32_t p = s_p + kh * kPChunk + kk * 32;
+          tc::mma_f8_pair(tmem + d * 128, tc::smem_desc(p, 16, 1024, tc::kSw128), v, kIdescHi,
+                          !(first && kh == 0 && kk == 0));
+          tc::mma_f8_pair(tmem + d * 128, tc::smem_desc(p + 2 * kPChunk, 16, 1024, tc::kSw128), v,
                           kIdescLo, true);
         }
-    };
-    // P of CTA 0's keys and V for it, in both CTAs. The first half waits for CTA
-    // 1's softmax too (and with it the second half's P) where that touches what
-    // the half writes or reads: O (read out before a block's first tile, scaled
-    // where the maxima moved) or V (keys past a block's end are cleared).
-    bool both = first || tile == w.tiles - 1;
-    wait(&ctl->p_own, ps & 1);
-    if (!first) wait(&ctl->votes[votes & 1], (votes >> 1) & 1);
-    if (!first && ok) {
-      const int b = votes++ & 1;
-      if (peek(&ctl->vote[0][b]) | peek(&ctl->vote[1][b])) {
-        // A row moved: that P is void, another follows.
-        wait(&ctl->p_peer[0], ps & 1);
-        wait(&ctl->p_peer[1], ps & 1);
-        wait(&ctl->p_in, ps & 1);
-        if (!ok) break;
-        ++ps;
-        tc::mbar_arrive_expect_tx(&ctl->p_in, 128 * kPRow);
-        for (int c = 0; c < 2; ++c) *reinterpret_cast<volatile uint32_t*>(&ctl->vote[c][b]) = 0;
-        const uint32_t count = peek(&ctl->moved) + 1;
-        tc::remote_st(tc::map_rank(&ctl->moved, 1), count);
-        *reinterpret_cast<volatile uint32_t*>(&ctl->moved) = count;
-        wait(&ctl->p_own, ps & 1);
-        both = true;
-      }
+      tc::mma_commit_pair(kh == 0 ? &ctl->pv_half[st] : &ctl->pv_done[st]);
     }
-    wait(&ctl->p_peer[0], ps & 1);
-    wait(&ctl->v_peer[st], ph);
-    if (both) wait(&ctl->p_peer[1], ps & 1);
-    if (!ok) break;
-    half(0, first);
-    tc::mma_commit_pair(&ctl->pv_half[st]);
-    wait(&ctl->v_full[st], ph);
-    wait(&ctl->p_in, ps & 1);
-    if (!both) wait(&ctl->p_peer[1], ps & 1);
-    if (!ok) break;
-    half(1, false);
-    tc::mma_commit_pair(&ctl->pv_done[st]);
-    ++ps;
     if (++tile == w.tiles) tile = 0;
     first = tile == 0;
   }
@@ -389,370 +319,204 @@ __device__ void issue_pv(const WideArgs& a, const WidePart& w, uint8_t* smem, Wi
 }
 
 // ---------------------------------------------------------------- softmax
-// Every wait here is bounded, barriers among the softmax warps included: a
-// thread whose wait runs out leaves, and the others' next one ends by the abort
-// flag.
-struct Soft {
-  const WideArgs& a;
-  WideCtl* ctl;
-  uint32_t tmem, rank;
-  int quarter, part, lane, gt;                     // rows 32 part .. 32 part + 31
-  uint32_t swaps = 0, votes = 0, syncs = 0, sends = 0, moves = 0;
-  bool ok = true;                                  // warp-uniform
+__device__ __forceinline__ float at_most_9(float d) {      // NaN stays
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(d), "f"(9.f));
+  return r;
+}
+__device__ __forceinline__ uint16_t f16x2_to_e5m2x2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+// P of 32 keys of a row from their scores: the codes of both terms, the sum, and
+// the largest score above the row's max. More than 9 above it counts as 9: such
+// a tile is done again.
+__device__ __forceinline__ void weigh(const uint32_t (&raw)[32], float scale, float neg_max,
+                                      float& most, float& sum, uint32_t (&hi)[8],
+                                      uint32_t (&lo)[8]) {
+  const uint64_t scale2 = pack_f32x2(scale, scale), neg2 = pack_f32x2(neg_max, neg_max);
+  uint64_t sums[2] = {0, 0};
+  most = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    uint64_t d01 = pack_f32x2(__uint_as_float(raw[i]), __uint_as_float(raw[i + 1]));
+    uint64_t d23 = pack_f32x2(__uint_as_float(raw[i + 2]), __uint_as_float(raw[i + 3]));
+    d01 = fma_f32x2(d01, scale2, neg2);
+    d23 = fma_f32x2(d23, scale2, neg2);
+    float d[4], p[4];
+    unpack_f32x2(d01, d[0], d[1]);
+    unpack_f32x2(d23, d[2], d[3]);
+    most = fmaxf(most, fmaxf(fmaxf(d[0], d[1]), fmaxf(d[2], d[3])));
+#pragma unroll
+    for (int u = 0; u < 4; ++u) p[u] = ex2(at_most_9(d[u]));
+    sums[0] = add_f32x2(sums[0], pack_f32x2(p[0], p[1]));
+    sums[1] = add_f32x2(sums[1], pack_f32x2(p[2], p[3]));
+    const uint32_t h01 = dec::f32x2_to_f16x2(p[0], p[1]), h23 = dec::f32x2_to_f16x2(p[2], p[3]);
+    const uint16_t e01 = dec::f16x2_to_e4m3x2(h01), e23 = dec::f16x2_to_e4m3x2(h23);
+    const uint16_t l01 = f16x2_to_e5m2x2(dec::f16x2_sub(h01, e4m3x2_to_f16x2(e01)));
+    const uint16_t l23 = f16x2_to_e5m2x2(dec::f16x2_sub(h23, e4m3x2_to_f16x2(e23)));
+    hi[i / 4] = (uint32_t)e01 | ((uint32_t)e23 << 16);
+    lo[i / 4] = (uint32_t)l01 | ((uint32_t)l23 << 16);
+  }
+  float a, b;
+  unpack_f32x2(add_f32x2(sums[0], sums[1]), a, b);
+  sum = a + b;
+}
 
-  __device__ Soft(const WideArgs& a_, WideCtl* c, uint32_t t, uint32_t r)
-      : a(a_), ctl(c), tmem(t), rank(r) {
-    const int warp = threadIdx.x >> 5;
-    quarter = warp & 3;
-    gt = threadIdx.x - 128;
-    part = gt >> 7;
-    lane = threadIdx.x & 31;
-  }
-  __device__ uint32_t lanes() const { return (uint32_t)(quarter * 32) << 16; }
-  __device__ void wait(uint64_t* bar, uint32_t parity) {
-    const bool got = ok && w_wait(bar, parity, ctl, a.status);
-    ok = __all_sync(0xffffffffu, got);
-  }
-  // Barrier of `warps` warps on `bar`, its `count`-th use.
-  __device__ void meet(uint64_t* bar, uint32_t count) {
-    __syncwarp();
-    if (lane == 0) tc::mbar_arrive(bar);
-    wait(bar, count & 1);
-  }
-  __device__ void sync() { meet(&ctl->sync, syncs++); }
-  // Row value `v` of threads gt < 128 (row gt) to the other CTA; returns its value.
-  __device__ float swap(float v) {
-    const int b = swaps & 1;
-    const uint32_t ph = (swaps >> 1) & 1;
-    ++swaps;
-    float got = v;
-    if (gt < kRows) {
-      if (gt == 0) tc::mbar_arrive_expect_tx(&ctl->swap_bar[b], kRows * 4);
-      tc::remote_st_async(tc::map_rank(&ctl->swap[b][gt], 1 - rank), __float_as_uint(v),
-                          tc::map_rank(&ctl->swap_bar[b], 1 - rank));
-      wait(&ctl->swap_bar[b], ph);
-      got = *reinterpret_cast<volatile float*>(&ctl->swap[b][gt]);
-    }
-    return got;
-  }
-  static __device__ __forceinline__ float at_most_9(float d) {    // NaN stays
-    float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(d), "f"(9.f));
-    return r;
-  }
-  static __device__ __forceinline__ uint16_t f16x2_to_e5m2x2(uint32_t h) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
-    return r;
-  }
-  // The weights of two rows of this thread's key.
-  __device__ __forceinline__ void pair(uint64_t raw, uint64_t neg_max, bool valid, float& most,
-                                       float& p0, float& p1) const {
-    float d0, d1;
-    unpack_f32x2(fma_f32x2(raw, pack_f32x2(a.bmm1_log2, a.bmm1_log2), neg_max), d0, d1);
-    most = fmaxf(most, fmaxf(d0, d1));
-    p0 = valid ? ex2(at_most_9(d0)) : 0.f;
-    p1 = valid ? ex2(at_most_9(d1)) : 0.f;
-  }
-  // P of the tile: codes of this thread's key in its 32 rows; lp gathers the row
-  // sums. Returns the largest score above its row's max; more than 9 count as 9
-  // (more than 8 has the tile done again).
-  __device__ float weigh(int st, bool valid, uint64_t (&lp)[16], uint32_t (&hi)[8],
-                         uint32_t (&lo)[8]) const {
-    float most = -INFINITY;
-    const ulonglong2* m4 = reinterpret_cast<const ulonglong2*>(&ctl->neg_max[part * 32]);
-#pragma unroll
-    for (int c = 0; c < 32; c += 16) {
-      uint32_t raw[16];
-      tc::tmem_ld16(tmem + lanes() + kSCol + st * kRows + part * 32 + c, raw);
-      tc::tmem_wait_ld();
-#pragma unroll
-      for (int e = 0; e < 16; e += 4) {
-        const int i = c + e;
-        const ulonglong2 m = m4[i / 4];
-        float p[4];
-        pair(pack_f32x2(__uint_as_float(raw[e]), __uint_as_float(raw[e + 1])), m.x, valid, most, p[0],
-             p[1]);
-        pair(pack_f32x2(__uint_as_float(raw[e + 2]), __uint_as_float(raw[e + 3])), m.y, valid, most, p[2],
-             p[3]);
-        lp[i / 2] = add_f32x2(lp[i / 2], pack_f32x2(p[0], p[1]));
-        lp[i / 2 + 1] = add_f32x2(lp[i / 2 + 1], pack_f32x2(p[2], p[3]));
-        const uint32_t h01 = dec::f32x2_to_f16x2(p[0], p[1]), h23 = dec::f32x2_to_f16x2(p[2], p[3]);
-        const uint16_t e01 = dec::f16x2_to_e4m3x2(h01), e23 = dec::f16x2_to_e4m3x2(h23);
-        const uint16_t l01 = f16x2_to_e5m2x2(dec::f16x2_sub(h01, e4m3x2_to_f16x2(e01)));
-        const uint16_t l23 = f16x2_to_e5m2x2(dec::f16x2_sub(h23, e4m3x2_to_f16x2(e23)));
-        hi[i / 4] = (uint32_t)e01 | ((uint32_t)e23 << 16);
-        lo[i / 4] = (uint32_t)l01 | ((uint32_t)l23 << 16);
-      }
-    }
-    return valid ? most : -INFINITY;
-  }
-  // Takes back what weigh added (the same values bit for bit).
-  __device__ void unweigh(int st, bool valid, uint64_t (&lp)[16]) const {
-    uint32_t raw[32];
-    tc::tmem_ld32(tmem + lanes() + kSCol + st * kRows + part * 32, raw);
-    tc::tmem_wait_ld();
-    const uint64_t* m2 = reinterpret_cast<const uint64_t*>(&ctl->neg_max[part * 32]);
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      float most = 0.f, p0, p1;
-      pair(pack_f32x2(__uint_as_float(raw[i]), __uint_as_float(raw[i + 1])), m2[i / 2], valid, most, p0,
-           p1);
-      lp[i / 2] = add_f32x2(lp[i / 2], pack_f32x2(-p0, -p1));
-    }
-  }
-  // Rows whose max grew by more than 8: the new max, 2 below the tile's, agreed
-  // with the other CTA; row sums and O follow. `last`: the pair's previous tile
-  // if O holds something of this block, else -1.
-  __device__ void move(int st, bool valid, uint64_t (&lp)[16], long long last) {
-    {
-      uint32_t raw[32];
-      float v[32];
-      tc::tmem_ld32(tmem + lanes() + kSCol + st * kRows + part * 32, raw);
-      tc::tmem_wait_ld();
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        v[i] = valid ? __uint_as_float(raw[i]) * a.bmm1_log2 : -INFINITY;
-      dec::transpose_reduce32<true>(v, lane);
-      ctl->red[quarter][part * 32 + lane] = v[0];
-    }
-    sync();
-    if (gt < kRows) {
-      const float own = fmaxf(fmaxf(ctl->red[0][gt], ctl->red[1][gt]),
-                              fmaxf(ctl->red[2][gt], ctl->red[3][gt]));
-      const float tm = fmaxf(own, swap(own));
-      const float mo = -ctl->neg_max[gt];
-      const float mn = tm > mo + 8.f ? tm - dec::kMaxLead : mo;
-      ctl->vec[gt] = mo == -INFINITY ? 0.f : ex2(mo - mn);
-      ctl->neg_max[gt] = -mn;
-    } else {
-      ++swaps;
-    }
-    sync();
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      lp[i] = fma_f32x2(lp[i], *reinterpret_cast<const uint64_t*>(&ctl->vec[part * 32 + 2 * i]),
-                        pack_f32x2(0.f, 0.f));
-    if (last >= 0) {
-      wait(&ctl->pv_done[last & 1], (uint32_t)(last >> 1) & 1);
-      tc::fence_after_sync();
-#pragma unroll 1
-      for (int d = 0; d < 2; ++d) {                // the two blocks of dims
-        uint32_t raw[32];
-        const uint32_t at = tmem + lanes() + d * kRows + part * 32;
-        tc::tmem_ld32(at, raw);
-        tc::tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          raw[e] = __float_as_uint(__uint_as_float(raw[e]) * ctl->vec[part * 32 + e]);
-        tc::tmem_st32(at, raw);
-      }
-      tc::tmem_wait_st();
-    }
-  }
-  // The codes of this thread's key to their place; rows for the other CTA by way
-  // of `put`, from which the two warps that hold a key's 64 rows send them.
-  __device__ void write_p(uint8_t* put, int key, bool away, const uint32_t (&hi)[8],
-                          const uint32_t (&lo)[8]) const {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int at = (part & 1) * 2 + j;
-      *reinterpret_cast<uint4*>(put + ((at ^ (key & 7)) << 4)) =
-          make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
-      *reinterpret_cast<uint4*>(put + (((4 + at) ^ (key & 7)) << 4)) =
-          make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]);
-    }
-  }
-  __device__ void send_p(const uint8_t* put, const uint8_t* place, bool away) {
-    tc::fence_proxy_async_smem();
-    tc::fence_before_sync();
-    if (away) {
-      meet(&ctl->pair[quarter], sends++);
-      if (lane == 0 && (part & 1) == 0 && ok)
-        tc::bulk_copy_to(tc::map_rank(place, 1 - rank), put, 32 * kPRow,
-                         tc::map_rank(&ctl->p_in, 1 - rank));
-    }
-    __syncwarp();
-    if (lane == 0) {
-      if (rank == 0)
-        tc::mbar_arrive(&ctl->p_own);
-      else
-        tc::remote_arrive(tc::map_rank(&ctl->p_peer[1], 0));
-    }
-  }
-  // This warp's vote on a tile, to the PV issuer: CTA 0's go with its P.
-  __device__ void cast(bool moved) {
-    const bool any = __any_sync(0xffffffffu, moved);
-    if (lane == 0) {
-      uint32_t* word = &ctl->vote[rank][votes & 1];
-      if (rank == 0) {
-        if (any) *reinterpret_cast<volatile uint32_t*>(word) = 1;
-      } else {
-        if (any) {
-          tc::remote_st(tc::map_rank(word, 0), 1);
-          tc::fence_cluster();
-        }
-        tc::remote_arrive(tc::map_rank(&ctl->votes[votes & 1], 0));
-      }
-    }
-    ++votes;
-  }
-  // Waits until PV of the previous tile is done with `bar`'s part, or has sent the
-  // tile back (true) instead of beginning.
-  __device__ bool moved_or(uint64_t* bar, uint32_t parity) {
-    bool back = false;
-    if (ok) {
-      const unsigned long long t0 = tc::globaltimer_ns();
-      while (!tc::mbar_try_wait(bar, parity)) {
-        if (peek(&ctl->moved) != moves) {
-          back = true;
-          break;
-        }
-        const bool expired = tc::globaltimer_ns() - t0 > kTimeoutNs;
-        if (*reinterpret_cast<volatile int*>(&ctl->abort_flag) || expired) {
-          *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
-          if (expired && a.status) atomicOr(a.status, MLA_FAULT_WAIT_TIMEOUT);
-          ok = false;
-          break;
-        }
-      }
-    }
-    ok = __all_sync(0xffffffffu, ok);
-    back = __any_sync(0xffffffffu, back);
-    moves += back ? 1 : 0;
-    return back;
-  }
-};
-
+// Thread (row, 32 keys): TMEM lane l holds row l % 64, keys of CTA l / 64; the
+// four warps of a lane quarter take 32 of its columns each. A thread that gave up
+// a wait goes on through the barriers, so that every thread reaches each of
+// them, until the next vote has all of them leave.
 __device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, WideCtl* ctl,
                         uint32_t tmem, uint32_t rank) {
-  Soft s(a, ctl, tmem, rank);
-  const int tl = s.quarter * 32 + s.lane;          // key of this CTA's half tile / dim of a block
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quarter = warp & 3, group = (warp - 4) >> 2;
+  const int row = (quarter & 1) * 32 + lane, kh = quarter >> 1;
+  const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+  const int col0 = group * 32;                     // of S: keys; of a half of O: dims
+  float* const mine = &ctl->red[kh * 4 + group][row];
   const long long n = w.end - w.begin;
   int block = (int)(w.begin / w.tiles), first_tile = (int)(w.begin % w.tiles);
-  uint64_t lp[16];                                 // this key's share of its rows' sums, in pairs
-  // Where this key's rows go, the P half of CTA part / 2: rows of 128 bytes in
-  // 16-byte pieces, piece j of key k at j ^ (k & 7). Rows for the other CTA wait
-  // here for a bulk copy: 64 keys in the stage's rope slot, which S is done with,
-  // 64 behind P; both are free again once PV of the tile is done.
-  const int key = (int)rank * 128 + tl;
-  const bool away = (s.part >> 1) != (int)rank;
-  uint8_t* const place = smem + kOffP + key * kPRow;
-  auto put_at = [&](int st) {
-    return !away ? place
-                 : smem + (tl < 64 ? st * kStageBytes + 4 * kChunkBytes + tl * kPRow
-                                   : kOffStage + (tl - 64) * kPRow);
+  uint32_t tails = 0;                              // parity of each stage's tails so far
+  bool ok = true;                                  // warp-uniform
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool got = ok && w_wait(bar, parity, ctl, a.status);
+    ok = __all_sync(0xffffffffu, got);
   };
-  uint32_t hi[8], lo[8];
-  uint32_t ps = 0;                                 // writes of P before this tile's
-  // Tile g's P again, with new maxima, agreed after both CTAs' first copies of it
-  // have landed (they wait for p_in before they exchange row maxima).
-  auto again = [&](long long g, bool valid) {
-    s.unweigh(g & 1, valid, lp);
-    s.wait(&ctl->p_in, (ps - 1) & 1);
-    s.sync();                                      // everyone has read the old maxima
-    s.move(g & 1, valid, lp, g - 1);
-    s.weigh(g & 1, valid, lp, hi, lo);
-    uint8_t* put = put_at(g & 1);
-    s.write_p(put, key, away, hi, lo);
-    s.send_p(put, place, away);
-    ++ps;
+  // The eight threads' values of this row, joined.
+  auto row_max = [&](float v) {
+    *mine = v;
+    soft_sync();
+    for (int j = 0; j < 8; ++j) v = fmaxf(v, ctl->red[j][row]);
+    return v;
+  };
+  auto row_sum = [&](float v) {
+    *mine = v;
+    soft_sync();
+    v = 0.f;
+    for (int j = 0; j < 8; ++j) v += ctl->red[j][row];
+    return v;
   };
   long long g = 0;
   while (g < n) {
     const int nt = (int)min((long long)(w.tiles - first_tile), n - g);
-    s.sync();                                      // the previous block's readers are done
-    if (s.gt < kRows) ctl->neg_max[s.gt] = INFINITY;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) lp[i] = 0;
-    s.sync();
-    bool valid = true;
+    float m = -INFINITY, l = 0.f;                  // the row's max; this thread's share of its sum
     for (int t = 0; t < nt; ++t, ++g) {
       const int st = g & 1;
       const uint32_t ph = (uint32_t)(g >> 1) & 1;
       const int key0 = (first_tile + t) * kKeys;
-      valid = key0 + key < w.len;
-      s.wait(&ctl->s_full[st], ph);
-      if (!s.ok) return;
+      const bool tail = key0 + kKeys > w.len;
+      wait(&ctl->s_full[st], ph);
       tc::fence_after_sync();
-      if (t == 0) {
-        s.move(st, valid, lp, -1);
-        s.weigh(st, valid, lp, hi, lo);
-      } else {
-        s.cast(s.weigh(st, valid, lp, hi, lo) > 8.f);
-        // The place of P of these keys is free once PV of the previous tile is
-        // done with it; if that tile came back it is done again first. (The votes on
-        // this one were then cast on maxima that only grew since: at worst it comes
-        // back for nothing.)
-        uint64_t* bar = rank == 0 ? &ctl->pv_half[(g - 1) & 1] : &ctl->pv_done[(g - 1) & 1];
-        const uint32_t bph = (uint32_t)((g - 1) >> 1) & 1;
-        if (s.moved_or(bar, bph)) {
-          s.unweigh(st, valid, lp);
-          again(g - 1, true);
-          s.weigh(st, valid, lp, hi, lo);
-          s.wait(bar, bph);
+      uint32_t raw[32], hi[8], lo[8];
+      tc::tmem_ld32(tmem + lanes + kSCol + st * 128 + col0, raw);
+      tc::tmem_wait_ld();
+      if (tail) {                                  // keys past the end
+        const int left = w.len - (key0 + kh * 128 + col0);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i >= left) raw[i] = 0xff800000u;     // -inf
+      }
+      float most, sum;
+      bool moved = t == 0;
+      if (t > 0) {
+        weigh(raw, a.bmm1_log2, -m, most, sum, hi, lo);
+        if (soft_any(most > 8.f || !ok)) {
+          if (soft_any(!ok)) return;               // all of them
+          moved = true;
         }
       }
-      if (t == 0 && g > 0)
-        s.wait(rank == 0 ? &ctl->pv_half[(g - 1) & 1] : &ctl->pv_done[(g - 1) & 1],
-               (uint32_t)((g - 1) >> 1) & 1);
-      if (!s.ok) return;
-      uint8_t* put = put_at(st);
-      s.write_p(put, key, away, hi, lo);
-      // Keys past the end: their V must be finite (0), a slot of each part.
-      if (key0 + kKeys > w.len) {
-        s.wait(&ctl->v_full[st], ph);
-        if (key0 + (s.part >> 1) * 128 + tl >= w.len) {
-          uint4* v =
-              reinterpret_cast<uint4*>(smem + st * kStageBytes + s.part * kChunkBytes + tl * 128);
+      if (moved) {
+        // Rows whose max grew by more than 8 (or begin): the new max is 2 below
+        // the tile's; the sum and O follow.
+        float v = -INFINITY;
 #pragma unroll
-          for (int u = 0; u < 8; ++u) v[u] = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < 32; ++i) v = fmaxf(v, __uint_as_float(raw[i]) * a.bmm1_log2);
+        const float tm = row_max(v);
+        const float mn = tm > m + 8.f ? tm - dec::kMaxLead : m;
+        const float f = m == -INFINITY ? 0.f : ex2(m - mn);
+        m = mn;
+        l *= f;
+        if (t > 0) {
+          wait(&ctl->pv_done[(g - 1) & 1], (uint32_t)((g - 1) >> 1) & 1);
+          tc::fence_after_sync();
+#pragma unroll 1
+          for (int d = 0; d < 2; ++d) {
+            uint32_t o[32];
+            const uint32_t at = tmem + lanes + d * 128 + col0;
+            tc::tmem_ld32(at, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tc::tmem_st32(at, o);
+          }
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+        }
+        soft_sync();                               // O is scaled before any P of this CTA counts
+        weigh(raw, a.bmm1_log2, m == -INFINITY ? 0.f : -m, most, sum, hi, lo);
+      }
+      l += sum;
+      // P of these keys is free once PV of the previous tile is done with it.
+      if (g > 0)
+        wait(kh == 0 ? &ctl->pv_half[(g - 1) & 1] : &ctl->pv_done[(g - 1) & 1],
+             (uint32_t)((g - 1) >> 1) & 1);
+      // Rows of 128 bytes (128 keys) in 16-byte pieces, piece j of row r at j ^ (r & 7).
+      uint8_t* p = smem + kOffP + kh * kPChunk + row * 128;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int at = ((group * 2 + j) ^ (row & 7)) << 4;
+        *reinterpret_cast<uint4*>(p + at) =
+            make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
+        *reinterpret_cast<uint4*>(p + 2 * kPChunk + at) =
+            make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]);
+      }
+      if (tail) {
+        // V behind the last key must be finite (0): 256 keys x this CTA's 256 dims,
+        // half a band row per thread.
+        wait(&ctl->v_tail[st], (tails >> st) & 1);
+        for (int z = threadIdx.x - 128; z < kKeys * 2; z += kSoft) {
+          const int key = z >> 1, slot = (key >> 7) * 2 + (z & 1);
+          if (key0 + key >= w.len) {
+            uint4* v = reinterpret_cast<uint4*>(smem + st * kStageBytes + slot * kChunkBytes +
+                                                (key & 127) * 128);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = make_uint4(0, 0, 0, 0);
+          }
         }
       }
-      s.send_p(put, place, away);
-      ++ps;
+      if (first_tile + t == w.tiles - 1) tails ^= 1u << st;
+      tc::fence_proxy_async_smem();
+      tc::fence_before_sync();
+      if (tail) soft_sync();                       // V is clear before any P of this CTA counts
+      __syncwarp();
+      if (lane == 0) tc::remote_arrive(tc::map_rank(&ctl->p_full[kh], 0));
     }
-    const int last = (int)((g - 1) & 1);
-    const uint32_t last_ph = (uint32_t)((g - 1) >> 1) & 1;
-    if (s.moved_or(&ctl->pv_done[last], last_ph)) {
-      again(g - 1, valid);
-      s.wait(&ctl->pv_done[last], last_ph);
-    }
-    // Row sums over both CTAs' keys, 1 / l and the LSE, then this CTA's dims.
-    {
-      float v[32];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) unpack_f32x2(lp[i], v[2 * i], v[2 * i + 1]);
-      dec::transpose_reduce32<false>(v, s.lane);
-      ctl->red[s.quarter][s.part * 32 + s.lane] = v[0];
-    }
-    s.sync();
-    const size_t slot = (size_t)(w.unit + block) * kRows;
-    const int rows = (int)min((long long)kRows, a.N - (long long)block * kRows);
-    if (s.gt < kRows) {
-      const float own = ctl->red[0][s.gt] + ctl->red[1][s.gt] + ctl->red[2][s.gt] + ctl->red[3][s.gt];
-      const float l = own + s.swap(own);
-      ctl->vec[s.gt] = l > 0.f ? 1.f / l : 0.f;
-      if (rank == 0 && s.gt < rows)
-        a.part_lse[slot + s.gt] = l == 0.f ? -INFINITY : __log2f(l) - ctl->neg_max[s.gt];
-    } else {
-      ++s.swaps;
-    }
-    s.sync();
-    if (!s.ok) return;
+    // The row's sum, its LSE, and the row itself.
+    soft_sync();                                   // red[] is free
+    const float z = row_sum(l);
+    const float inv = z > 0.f ? 1.f / z : 0.f;
+    const size_t at = (size_t)(w.unit + block) * kRows + rank * 64 + row;
+    const bool live = (long long)block * kRows + rank * 64 + row < a.N;
+    if (live && kh == 0 && group == 0) a.part_lse[at] = z == 0.f ? -INFINITY : m + __log2f(z);
+    wait(&ctl->pv_done[(g - 1) & 1], (uint32_t)((g - 1) >> 1) & 1);
     tc::fence_after_sync();
 #pragma unroll 1
-    for (int d = 0; d < 2; ++d) {                  // the two blocks of dims
-      uint32_t raw[32];
-      tc::tmem_ld32(tmem + s.lanes() + d * kRows + s.part * 32, raw);
+    for (int d = 0; d < 2; ++d) {
+      uint32_t o[32];
+      tc::tmem_ld32(tmem + lanes + d * 128 + col0, o);
       tc::tmem_wait_ld();
-      float* dst = a.part_o + (slot + s.part * 32) * kDv + rank * 256 + d * 128 + tl;
+      if (live) {                                  // columns of half d: band d of CTA kh's dims
+        float4* dst = reinterpret_cast<float4*>(a.part_o + at * kDv + kh * 256 + d * 128 + col0);
 #pragma unroll
-      for (int e = 0; e < 32; ++e)
-        if (s.part * 32 + e < rows)
-          dst[(size_t)e * kDv] = __uint_as_float(raw[e]) * ctl->vec[s.part * 32 + e];
+        for (int i = 0; i < 32; i += 4)
+          dst[i / 4] = make_float4(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
+                                   __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
+      }
     }
     tc::fence_before_sync();
+    soft_sync();                                   // O is read before any P of the next block counts
     ++block;
     first_tile = 0;
   }
@@ -771,24 +535,15 @@ wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&ctl->k_full[b], 2);
-      tc::mbar_init(&ctl->v_full[b], 1);
+      tc::mbar_init(&ctl->v_full[b], 2);
+      tc::mbar_init(&ctl->v_tail[b], 1);
       tc::mbar_init(&ctl->s_full[b], 1);
+      tc::mbar_init(&ctl->p_full[b], 2 * kSoft / 64);   // the warps of one key half, both CTAs
       tc::mbar_init(&ctl->pv_half[b], 1);
       tc::mbar_init(&ctl->pv_done[b], 1);
-      tc::mbar_init(&ctl->v_peer[b], 1);
-      tc::mbar_init(&ctl->votes[b], kSoftWarps);
-      tc::mbar_init(&ctl->swap_bar[b], 1);
       tc::mbar_init(&ctl->drain[b], 1);
-      ctl->vote[0][b] = ctl->vote[1][b] = 0;
     }
-    ctl->moved = 0;
-    tc::mbar_init(&ctl->sync, kSoftWarps);
-    for (int q = 0; q < 4; ++q) tc::mbar_init(&ctl->pair[q], 2);
-    tc::mbar_init(&ctl->p_own, kSoftWarps);
-    tc::mbar_init(&ctl->p_in, 1);
-    tc::mbar_init(&ctl->p_peer[0], 1);
-    tc::mbar_init(&ctl->p_peer[1], kSoftWarps);
-    tc::mbar_init(&ctl->q_full, 2);
+        tc::mbar_init(&ctl->q_full, 2);
     tc::mbar_init(&ctl->q_empty, 1);
     ctl->abort_flag = 0;
     tc::fence_barrier_init();
@@ -814,32 +569,24 @@ wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
   const WidePart w = wide_part(a, (int)(blockIdx.x >> 1), threadIdx.x == 0);
   if (w.begin == w.end) {
     // No tiles for this pair.
-  } else if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    if (warp == 0) {
-      load_keys(a, w, smem, ctl, rank, &tm_kv, &tm_kvr, &tm_q, &tm_qr);
-    } else if (warp == 3) {
-      load_values(a, w, smem, ctl, rank, &tm_kv);
-    } else if (lane == 0) {
-      if (rank == 0 && warp == 1)
-        issue_s(a, w, smem, ctl, tmem);
-      else if (rank == 0)
-        issue_pv(a, w, smem, ctl, tmem);
-      else if (warp == 1)
-        relay_values(a, w, ctl);
-      else
-        relay_p(a, w, ctl);
-    }
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+  } else if (warp == 0) {
+    load_keys(a, w, smem, ctl, rank, &tm_kv, &tm_kvr, &tm_q, &tm_qr);
+  } else if (warp == 3) {
+    load_values(a, w, smem, ctl, rank, &tm_kv);
+  } else if (warp >= 4) {
     softmax(a, w, smem, ctl, tmem, rank);
+  } else if (rank == 0 && lane == 0) {
+    if (warp == 1)
+      issue_s(a, w, smem, ctl, tmem);
+    else
+      issue_pv(a, w, smem, ctl, tmem);
   }
   tc::fence_before_sync();
   __syncthreads();
   if (ctl->abort_flag)     // a wait ran out: what is still in flight here or to the other CTA lands
     for (const unsigned long long t0 = tc::globaltimer_ns(); tc::globaltimer_ns() - t0 < 1000000;) {
     }
-  tc::cluster_sync();      // no CTA leaves while the other's MMAs or stores may reach it
+  tc::cluster_sync();      // no CTA leaves while the other's MMAs or arrivals may reach it
   tc::fence_after_sync();
   if (warp == 1) tc::tmem_dealloc_pair(tmem, kTmemCols);
 }
