@@ -426,37 +426,53 @@ int32_t mla_query_absorb(const mla_query_shape *shape, const void *q, const void
                          const float *rope, const int32_t *rope_starts, float q_scale, void *out,
                          int32_t *status, mla_stream_t stream);
 
-/* Bytes of workspace mla_prefix_decode needs for this shape (groups 0 or 1)
- * and a prefix of up to prefix_pages pages. Writes the size to *bytes. Host
- * only. */
-int32_t mla_prefix_workspace_bytes(const mla_shape *shape, int32_t prefix_pages, size_t *bytes);
-
-/* The decode of a batch whose requests all begin with one shared prefix: its
- * keys are read and multiplied once for all R*k*H rows; each request's own keys
- * (block_table, seq_lens; none is fine) follow; one softmax over both:
+/* The decode of a batch whose requests all begin with one shared prefix, for
+ * mla_shape with groups 0 or 1 (its policy, min_split_tokens and max_splits are
+ * not used: the work is cut into equal parts, one per pair of CTAs, num_ctas / 2
+ * pairs).
+ *
+ * mla_prefix_workspace_bytes -- bytes of workspace the decode needs. Writes the
+ * size to *bytes. Host only.
+ *
+ * mla_prefix_plan -- once per step, reused by every layer: where each request's
+ * own keys lie in the line of work (one CTA; integer arithmetic only).
+ *   seq_lens  [R] int32, device: the requests' own keys (negative is read as 0).
+ *   plan      [plan_len] int64, device, plan_len >= R + 1: words 0 .. R written.
+ *
+ * mla_prefix_decode -- the prefix's keys are read and multiplied once for all
+ * R*k*H rows; each request's own keys (none is fine) follow; one softmax over both:
  *   s[n][j] over j < prefix_len of kv[prefix_table[j / 64]][j % 64], then over
  *   j < seq_lens[r] of the request's own keys, as in mla_folded_decode.
- *   shape, counts, work, list_len  the plan of mla_plan_splits for seq_lens, the
- *                requests' own lengths, with groups 0 or 1.
  *   prefix_pages 1 .. 2^24: entries of prefix_table.
  *   prefix_table [prefix_pages] int32, device: the prefix's pages; only the
  *                first ceil(prefix_len / 64) are read.
  *   prefix_len   [1] int32, device: its keys (negative is read as 0; more than
- *                prefix_pages * 64 sets MLA_FAULT_PAGE_RANGE and is cut off).
- *   workspace    >= mla_prefix_workspace_bytes(shape, prefix_pages) bytes,
- *                device, 256-byte aligned; calls that share one must not
- *                overlap. Its contents need not be initialised.
+ *                prefix_pages * 64, as more than max_pages * 64 own keys, sets
+ *                MLA_FAULT_PAGE_RANGE and is cut off). May change between the
+ *                decodes of one plan.
+ *   seq_lens     the planned lengths.
+ *   plan         of mla_prefix_plan for them.
+ *   workspace    >= mla_prefix_workspace_bytes(shape) bytes, device, 256-byte
+ *                aligned; calls that share one must not overlap. Its contents
+ *                need not be initialised.
  *   out          [R, k*H, 512] BF16, device, 16-byte aligned: every row is
  *                written; lse [R, k*H] FP32 base-2 or NULL. A row with no keys
  *                at all gets out = 0, lse = -inf.
+ *   status       as for mla_folded_decode: MLA_FAULT_PAGE_RANGE,
+ *                MLA_FAULT_WAIT_TIMEOUT.
  *   the others   as for mla_folded_decode.
- * All partial results stay FP32 until one rounding to BF16. */
+ * Numerics as there, except that P's second term is E5M2 (hi + lo is p to 2^-7
+ * relative, down to 2^-13 where p is small) and that all partial results stay
+ * FP32 until one rounding to BF16. */
+int32_t mla_prefix_workspace_bytes(const mla_shape *shape, size_t *bytes);
+int32_t mla_prefix_plan(const mla_shape *shape, const int32_t *seq_lens, int64_t *plan,
+                        int32_t plan_len, mla_stream_t stream);
 int32_t mla_prefix_decode(const mla_shape *shape, int32_t prefix_pages, const void *q,
                           const void *kv, const int32_t *prefix_table, const int32_t *prefix_len,
                           const int32_t *block_table, const int32_t *seq_lens, float bmm1_scale,
-                          float bmm2_scale, const int32_t *counts, int32_t *work,
-                          int32_t list_len, void *workspace, size_t workspace_bytes, void *out,
-                          float *lse, int32_t *status, mla_stream_t stream);
+                          float bmm2_scale, const int64_t *plan, int32_t plan_len, void *workspace,
+                          size_t workspace_bytes, void *out, float *lse, int32_t *status,
+                          mla_stream_t stream);
 
 /* Bits the kernels OR into *status. */
 #define MLA_FAULT_WAIT_TIMEOUT 0x1 /* a pipeline wait gave up; the CTA stopped early */

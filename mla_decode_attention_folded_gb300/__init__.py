@@ -39,7 +39,8 @@ __all__ = ["MlaShape", "MlaError", "POLICY_BALANCED", "POLICY_UNIFORM", "make_sh
            "folded_decode_wait_test", "tier_plan", "row_copy", "balanced_tiers", "TIERS", "MOVE",
            "FoldedMla", "TieredMla", "fold_factor", "FAULT_WAIT_TIMEOUT", "FAULT_PAGE_RANGE",
            "FAULT_WORK_ITEM", "FAULT_ROPE_RANGE", "library_path", "rope_table", "kv_append",
-           "query_absorb", "prefix_workspace_bytes", "prefix_decode", "PrefixMla"]
+           "query_absorb", "prefix_workspace_bytes", "prefix_plan", "prefix_decode",
+           "PrefixMla"]
 
 PAGE = 64
 
@@ -484,58 +485,60 @@ def query_absorb(q, w_uk, rope, rope_starts, q_scale: float, out=None, interleav
     return out
 
 
-def prefix_workspace_bytes(shape: MlaShape, prefix_pages: int) -> int:
+def prefix_workspace_bytes(shape: MlaShape) -> int:
     out = ctypes.c_size_t(0)
     _lib.check("mla_prefix_workspace_bytes", _lib.load().mla_prefix_workspace_bytes(
-        ctypes.byref(shape), int(prefix_pages), ctypes.byref(out)))
+        ctypes.byref(shape), ctypes.byref(out)))
     return out.value
 
 
+def prefix_plan(shape: MlaShape, seq_lens, plan, stream=None) -> None:
+    """The line of work of the requests' own keys: plan [R + 1] int64 (see
+    mla_prefix_plan in include/mlafold.h)."""
+    _lib.check("mla_prefix_plan", _lib.load().mla_prefix_plan(
+        ctypes.byref(shape), _ptr(seq_lens), _ptr(plan), plan.numel(), _stream(stream)))
+
+
 def prefix_decode(shape: MlaShape, q, kv, prefix_table, prefix_len, block_table, seq_lens,
-                  bmm1_scale: float, bmm2_scale: float, counts, work, workspace, out, lse,
-                  status=None, stream=None) -> None:
-    """The shared-prefix decode over the plan of plan_splits for the requests'
+                  bmm1_scale: float, bmm2_scale: float, plan, workspace, out, lse, status=None,
+                  stream=None) -> None:
+    """The shared-prefix decode over the plan of prefix_plan for the requests'
     own lengths (see mla_prefix_decode in include/mlafold.h)."""
     _lib.check("mla_prefix_decode", _lib.load().mla_prefix_decode(
         ctypes.byref(shape), prefix_table.numel(), _ptr(q), _ptr(kv), _ptr(prefix_table),
         _ptr(prefix_len), _ptr(block_table), _ptr(seq_lens), float(bmm1_scale), float(bmm2_scale),
-        _ptr(counts), _ptr(work), work.numel(), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse), _ptr(status),
-        _stream(stream)))
+        _ptr(plan), plan.numel(), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _ptr(out), _ptr(lse), _ptr(status), _stream(stream)))
 
 
 class PrefixMla:
     """Decode of a batch of R requests that share a prefix of up to
-    prefix_pages pages: plan buffers and workspace of one shape, allocated here
-    and reused by every call. ``plan(seq_lens)`` plans the requests' own keys
-    once per step; ``decode`` attends over the prefix and them. Calls on one
-    object share its buffers: they must run in stream order."""
+    prefix_pages pages: plan and workspace of one shape, allocated here and
+    reused by every call. ``plan(seq_lens)`` plans the requests' own keys once
+    per step; ``decode`` attends over the prefix and them. Calls on one object
+    share its buffers: they must run in stream order."""
 
     def __init__(self, R: int, k: int, H: int, max_pages: int, prefix_pages: int, num_pages: int,
-                 device=None, num_ctas: int | None = None, min_split_tokens: int = 256,
-                 max_splits: int = 64, policy: int = POLICY_BALANCED):
+                 device=None, num_ctas: int | None = None):
         self.device = torch.device(device if device is not None else "cuda")
         if num_ctas is None:
             num_ctas = torch.cuda.get_device_properties(self.device).multi_processor_count
-        self.shape = make_shape(R, k, H, max_pages, num_pages, num_ctas, min_split_tokens,
-                                max_splits, policy)
+        self.shape = make_shape(R, k, H, max_pages, num_pages, num_ctas)
         self.R, self.k, self.H, self.M = R, k, H, k * H
         self.max_pages, self.prefix_pages, self.num_pages = max_pages, prefix_pages, num_pages
-        i32 = dict(dtype=torch.int32, device=self.device)
-        self.workspace = torch.empty(prefix_workspace_bytes(self.shape, prefix_pages),
-                                     dtype=torch.uint8, device=self.device)
-        self.counts = torch.zeros(R, **i32)
-        self.work = torch.full((plan_list_len(self.shape),), -1, **i32)
-        self.status = torch.zeros(1, **i32)
+        self.workspace = torch.empty(prefix_workspace_bytes(self.shape), dtype=torch.uint8,
+                                     device=self.device)
+        self.places = torch.zeros(R + 1, dtype=torch.int64, device=self.device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
 
     def plan(self, seq_lens, stream=None) -> None:
-        """Plan the splits of the requests' own keys: seq_lens [R] int32."""
-        dev = self.work.get_device()
-        _check(dev, "seq_lens", seq_lens, _I32, (self.R,))
+        """Plan the requests' own keys: seq_lens [R] int32."""
+        dev = self.places.get_device()
         if dev != torch.cuda.current_device():
             with torch.cuda.device(dev):
-                return plan_splits(self.shape, seq_lens, self.counts, self.work, stream)
-        plan_splits(self.shape, seq_lens, self.counts, self.work, stream)
+                return self.plan(seq_lens, stream)
+        _check(dev, "seq_lens", seq_lens, _I32, (self.R,))
+        prefix_plan(self.shape, seq_lens, self.places, stream)
 
     def decode(self, q, kv, prefix_table, prefix_len, block_table, seq_lens, bmm1_scale: float,
                bmm2_scale: float, out=None, lse=None, stream=None, return_lse: bool = True):
@@ -543,7 +546,7 @@ class PrefixMla:
         return_lse) of queries q [R*k, H, 576] over the prefix (prefix_table
         [prefix_pages] and prefix_len [1], int32) and each request's own keys
         (block_table [R, max_pages], seq_lens [R], the planned lengths)."""
-        dev = self.work.get_device()
+        dev = self.places.get_device()
         if dev != torch.cuda.current_device():
             with torch.cuda.device(dev):
                 return self.decode(q, kv, prefix_table, prefix_len, block_table, seq_lens,
@@ -566,6 +569,6 @@ class PrefixMla:
         else:
             _check(dev, "lse", lse, _F32, (R, M))
         prefix_decode(self.shape, q, kv, prefix_table, prefix_len, block_table, seq_lens,
-                      bmm1_scale, bmm2_scale, self.counts, self.work, self.workspace, out, lse,
-                      self.status, stream)
+                      bmm1_scale, bmm2_scale, self.places, self.workspace, out, lse, self.status,
+                      stream)
         return out, lse

@@ -43,36 +43,6 @@ bool scales_ok(float bmm1, float bmm2) {
   return std::isfinite(bmm1) && bmm1 > 0.f && std::isfinite(bmm2);
 }
 
-DecodeArgs decode_args(const mla_shape& s, const void* q, const void* kv,
-                       const int32_t* block_table, const int32_t* seq_lens, float bmm1_scale,
-                       float bmm2_scale, const int32_t* counts, int32_t* work, void* out,
-                       float* lse, int32_t* status) {
-  DecodeArgs a = {};
-  a.q = static_cast<const uint8_t*>(q);
-  a.kv = static_cast<const uint8_t*>(kv);
-  a.block_table = block_table;
-  a.seq_lens = seq_lens;
-  a.counts = counts;
-  a.work = work;
-  a.sched = work + plan_items(s);
-  a.ranges = work + plan_ranges_offset(s);
-  a.units = work + plan_units_offset(s);
-  a.nunits = plan_units(group_rows(s), s.num_ctas);
-  a.out = static_cast<uint16_t*>(out);
-  a.lse = lse;
-  a.status = status;
-  a.bmm1_log2 = (float)((double)bmm1_scale * 1.4426950408889634);
-  a.bmm2 = bmm2_scale;
-  a.R = plan_rows(s);
-  a.M = group_rows(s);
-  a.groups = shape_groups(s);
-  a.max_pages = s.max_pages;
-  a.num_pages = s.num_pages;
-  a.items = plan_items(s);
-  a.wait_limit_ns = kDecodeWaitLimitNs;
-  return a;
-}
-
 }  // namespace mlafold
 
 extern "C" {
@@ -132,18 +102,40 @@ int32_t decode_impl(const mla_shape* shape, const void* q, const void* kv,
   if ((st = check_device()) != MLA_OK) return st;
   const int M = group_rows(*shape);
   const int slots = partial_slots(*shape);
-  DecodeArgs a = decode_args(*shape, q, kv, block_table, seq_lens, bmm1_scale, bmm2_scale, counts,
-                             work, out, lse, status);
+  DecodeArgs a;
+  a.q = static_cast<const uint8_t*>(q);
+  a.kv = static_cast<const uint8_t*>(kv);
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.counts = counts;
+  a.work = work;
+  a.sched = work + plan_items(*shape);
+  a.ranges = work + plan_ranges_offset(*shape);
+  a.units = work + plan_units_offset(*shape);
+  a.nunits = plan_units(M, shape->num_ctas);
   a.part_o = static_cast<float*>(workspace);
   a.part_lse = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                                     partial_out_bytes(slots, M))
                          : nullptr;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.status = status;
+  a.bmm1_log2 = (float)((double)bmm1_scale * 1.4426950408889634);
+  a.bmm2 = bmm2_scale;
+  a.R = plan_rows(*shape);
+  a.M = M;
+  a.groups = shape_groups(*shape);
+  a.max_pages = shape->max_pages;
+  a.num_pages = shape->num_pages;
+  a.items = plan_items(*shape);
   a.slots = slots;
   a.wait_limit_ns = wait_limit_ns;
   a.withhold_first_copy = withhold_first_copy;
   cudaError_t e = launch_decode(*shape, a, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
+
+constexpr unsigned long long kDecodeWaitLimitNs = 2000000000ull;   // 2 s
 
 }  // namespace
 

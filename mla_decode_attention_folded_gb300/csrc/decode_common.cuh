@@ -115,7 +115,7 @@ __device__ __forceinline__ Job read_job(const DecodeArgs& a, int item, int blk, 
     jb.j0 = min(max(pa, 0) * kPage, jb.j1);
   }
   jb.ntiles = (int)cdiv(jb.j1 - jb.j0, kTileKeys);
-  jb.direct = n == 1 && !a.all_partial;
+  jb.direct = n == 1;
   if (!jb.direct && item >= a.slots) {
     if (report && a.status) atomicOr(a.status, MLA_FAULT_WORK_ITEM);
     jb.skip = true;
@@ -404,41 +404,6 @@ __device__ __forceinline__ uint32_t f16x2_sub(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
-}
-
-// ---------------------------------------------------------------- row reductions
-// Reduce v[32] across the 32 lanes by halving exchanges (31 shuffles per
-// lane instead of 160); afterwards lane l holds the reduction of row l in v[0].
-template <int LEN, bool MAX>
-__device__ __forceinline__ void tr_step(float* v, int lane, int o) {
-  const bool upper = (lane & o) != 0;
-#pragma unroll
-  for (int i = 0; i < LEN / 2; ++i) {
-    const float send = upper ? v[i] : v[i + LEN / 2];
-    const float keep = upper ? v[i + LEN / 2] : v[i];
-    const float recv = __shfl_xor_sync(0xffffffffu, send, o);
-    v[i] = MAX ? fmaxf(keep, recv) : keep + recv;
-  }
-}
-// The same for v[16] (16 rows per thread): after four halving steps v[0]
-// holds row (lane >> 1) reduced over the 16 lanes that share bit 0 of the
-// lane index; one more exchange with lane ^ 1 completes it.
-template <bool MAX>
-__device__ __forceinline__ void transpose_reduce16(float* v, int lane) {
-  tr_step<16, MAX>(v, lane, 16);
-  tr_step<8, MAX>(v, lane, 8);
-  tr_step<4, MAX>(v, lane, 4);
-  tr_step<2, MAX>(v, lane, 2);
-  const float r = __shfl_xor_sync(0xffffffffu, v[0], 1);
-  v[0] = MAX ? fmaxf(v[0], r) : v[0] + r;
-}
-template <bool MAX>
-__device__ __forceinline__ void transpose_reduce32(float* v, int lane) {
-  tr_step<32, MAX>(v, lane, 16);
-  tr_step<16, MAX>(v, lane, 8);
-  tr_step<8, MAX>(v, lane, 4);
-  tr_step<4, MAX>(v, lane, 2);
-  tr_step<2, MAX>(v, lane, 1);
 }
 
 // ---------------------------------------------------------------- host side

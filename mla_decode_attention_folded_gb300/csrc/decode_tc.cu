@@ -84,6 +84,40 @@ struct Cfg {
   static_assert(kSCol + kSBufs * NR <= (int)kTmemCols, "TMEM budget");
 };
 
+// Reduce v[32] across the 32 lanes by halving exchanges (31 shuffles per
+// lane instead of 160); afterwards lane l holds the reduction of row l in v[0].
+template <int LEN, bool MAX>
+__device__ __forceinline__ void tr_step(float* v, int lane, int o) {
+  const bool upper = (lane & o) != 0;
+#pragma unroll
+  for (int i = 0; i < LEN / 2; ++i) {
+    const float send = upper ? v[i] : v[i + LEN / 2];
+    const float keep = upper ? v[i + LEN / 2] : v[i];
+    const float recv = __shfl_xor_sync(0xffffffffu, send, o);
+    v[i] = MAX ? fmaxf(keep, recv) : keep + recv;
+  }
+}
+// The same for v[16] (16 rows per thread): after four halving steps v[0]
+// holds row (lane >> 1) reduced over the 16 lanes that share bit 0 of the
+// lane index; one more exchange with lane ^ 1 completes it.
+template <bool MAX>
+__device__ __forceinline__ void transpose_reduce16(float* v, int lane) {
+  tr_step<16, MAX>(v, lane, 16);
+  tr_step<8, MAX>(v, lane, 8);
+  tr_step<4, MAX>(v, lane, 4);
+  tr_step<2, MAX>(v, lane, 2);
+  const float r = __shfl_xor_sync(0xffffffffu, v[0], 1);
+  v[0] = MAX ? fmaxf(v[0], r) : v[0] + r;
+}
+template <bool MAX>
+__device__ __forceinline__ void transpose_reduce32(float* v, int lane) {
+  tr_step<32, MAX>(v, lane, 16);
+  tr_step<16, MAX>(v, lane, 8);
+  tr_step<8, MAX>(v, lane, 4);
+  tr_step<4, MAX>(v, lane, 2);
+  tr_step<2, MAX>(v, lane, 1);
+}
+
 // Reduce this thread's RT row values across the warp's 32 keys and store row
 // results in red[r0 + row] (RT = 32: lane l holds row l; RT = 16: row l >> 1).
 template <int RT, bool MAX>

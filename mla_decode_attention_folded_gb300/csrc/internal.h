@@ -102,6 +102,7 @@ inline size_t workspace_bytes(const mla_shape& s) {
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 int check_shape(const mla_shape* s);
 int check_device();
+bool scales_ok(float bmm1, float bmm2);   // bmm1 finite and positive, bmm2 finite
 
 struct DecodeArgs {
   const uint8_t* q;
@@ -126,18 +127,7 @@ struct DecodeArgs {
   unsigned long long wait_limit_ns;   // bound of every pipeline wait (drains keep their own)
   int withhold_first_copy;            // failure-detection test: CTA 0 never issues its
                                       // first KV tile's copy, so one wait must run out
-  int all_partial;                    // one-split rows go to the partials too (slots covers
-                                      // every item), not to out
 };
-constexpr unsigned long long kDecodeWaitLimitNs = 2000000000ull;   // 2 s
-// Host: bmm1 finite and positive, bmm2 finite.
-bool scales_ok(float bmm1, float bmm2);
-// Host: the arguments of a decode of this shape with the default wait bound;
-// the partials (part_o, part_lse, slots) are the caller's to set.
-DecodeArgs decode_args(const mla_shape& s, const void* q, const void* kv,
-                       const int32_t* block_table, const int32_t* seq_lens, float bmm1_scale,
-                       float bmm2_scale, const int32_t* counts, int32_t* work, void* out,
-                       float* lse, int32_t* status);
 
 // Launchers (return cudaError_t of the launch).
 cudaError_t launch_plan(const mla_shape& s, const int32_t* seq_lens, int32_t* counts,

@@ -1,8 +1,10 @@
-// The shared prefix's keys against every row of the batch (prefix.cu joins the
-// result with the requests' own keys): N = R*k*H query rows, one set of keys.
+// Blocks of 128 query rows against the keys they share: all rows against the
+// prefix's, a request's rows against its own (prefix.h says in which order and by
+// which CTAs; prefix.cu joins the partial results).
 //
 // Bound by the FP8 tensor pipe: 2 * 1088 FLOP per (row, key) beside 576 bytes
-// per key. What sets the shape is TMEM: a 512-dim FP32 accumulator of 128 rows
+// per key; with few rows per request by what two stages of keys per CTA can
+// stream from HBM. What sets the shape is TMEM: a 512-dim FP32 accumulator of 128 rows
 // fills an SM's 512 columns. A pair of CTAs (tcgen05 cta_group::2) therefore
 // shares a block of 128 rows, 64 in each CTA: an MMA of M = 128 over the pair
 // keeps a CTA's 64 rows in all 128 lanes (lanes 0-63 its first N / 2 columns,
@@ -27,10 +29,6 @@
 // down to 2^-13 of absolute error. The running max is lazy as in decode_tc.cu
 // (moved when a score exceeds it by more than 8, to 2 below the new one); P is
 // computed as if no row moved and once more where one did.
-//
-// Work: the tiles of all row blocks, block after block, are one sequence cut
-// into equal parts, one per pair; a part's piece of a block goes to partial
-// slot unit + block. No plan: the cuts follow from the prefix's length.
 #include "decode_common.cuh"
 #include "internal.h"
 #include "prefix.h"
@@ -75,9 +73,11 @@ struct WideCtl {
   uint64_t drain[2];
   uint32_t tmem_base;
   int abort_flag;
-  float red[8][64];        // row values of the eight threads that share a row
+  alignas(16) float red[8][64];     // row values of the eight threads that share a row
 };
-constexpr int kSmemBytes = kOffCtl + (int)sizeof(WideCtl) + 1024;
+// Behind the control block: the plan, R + 1 places.
+constexpr int kOffPlan = kOffCtl + (int)((sizeof(WideCtl) + 15) / 16 * 16);
+constexpr int kSmemBytes = kOffPlan + (kMaxR + 1) * 8 + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ bool w_wait(uint64_t* bar, uint32_t parity, WideCtl* ctl,
@@ -109,24 +109,25 @@ __device__ __forceinline__ bool soft_any(bool pred) {
 }
 
 // ---------------------------------------------------------------- loads
-// The page ids of a tile, in lanes 0-3 of a warp: asked for a tile ahead, checked
-// when used.
+// The page ids of a piece's tiles, in lanes 0-3 of a warp: asked for a tile ahead,
+// checked when used.
 struct Pages {
   const WideArgs& a;
-  int tile, tiles, all, lane;                      // tile: within its block, the next one to ask for
-  int next;
-  bool report;
-  __device__ Pages(const WideArgs& a_, const WidePart& w, bool report_)
-      : a(a_), tile((int)(w.begin % w.tiles)), tiles(w.tiles), all((int)cdiv(w.len, kPage)),
-        lane(threadIdx.x & 31), report(report_) {
+  const int32_t* table = nullptr;
+  int page = 0, end = 0, next = -2, lane;          // page: this lane's of the next tile
+  __device__ explicit Pages(const WideArgs& a_) : a(a_), lane(threadIdx.x & 31) {}
+  __device__ int ask() {
+    const int p = page;
+    page += kKeys / kPage;
+    return lane < kKeys / kPage && p < end ? table[p] : -2;      // -2: no such page
+  }
+  __device__ void begin(const WidePiece& p) {
+    table = p.table;
+    page = p.tile * (kKeys / kPage) + lane;
+    end = (int)cdiv(p.len, kPage);
     next = ask();
   }
-  __device__ int ask() {
-    const int p = tile * (kKeys / kPage) + lane;
-    if (++tile == tiles) tile = 0;
-    return lane < kKeys / kPage && p < all ? a.prefix_table[p] : -2;      // -2: no such page
-  }
-  __device__ int take(bool more) {
+  __device__ int take(bool more, bool report) {
     int cur = next;
     next = more ? ask() : -2;
     if (cur != -2 && (cur < 0 || cur >= a.num_pages)) {
@@ -137,104 +138,110 @@ struct Pages {
   }
 };
 
-// Own keys (and Q at each block's start). A stage's bands 0-1 hold V of CTA 0's
+// Own keys (and Q at each piece's start). A stage's bands 0-1 hold V of CTA 0's
 // keys, which PV is done with first, bands 2-3 that of CTA 1's: it is refilled in
 // two parts.
-__device__ void load_keys(const WideArgs& a, const WidePart& w, uint8_t* smem, WideCtl* ctl,
+__device__ void load_keys(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl* ctl,
                           uint32_t rank, const CUtensorMap* tm_kv, const CUtensorMap* tm_kvr,
                           const CUtensorMap* tm_q, const CUtensorMap* tm_qr) {
   const int lane = threadIdx.x & 31;
-  const long long n = w.end - w.begin;
-  Pages pages(a, w, true);
-  int block = (int)(w.begin / w.tiles), tile = (int)(w.begin % w.tiles);
+  Pages pages(a);
   const uint32_t q_bar = tc::map_rank(&ctl->q_full, 0);
-  uint32_t x = 0;                                  // blocks whose Q was requested
+  uint32_t x = 0, i = 0;                           // pieces, tiles
   bool ok = true;
-  for (long long i = 0; ok && i < n; ++i) {
-    const int st = i & 1;
-    const uint32_t ph = (uint32_t)((i >> 1) - 1) & 1;
-    const int cur = pages.take(i + 1 < n);
-    const int p0 = __shfl_sync(0xffffffffu, cur, 2 * rank);
-    const int p1 = __shfl_sync(0xffffffffu, cur, 2 * rank + 1);
-    if (lane == 0) {
-      const uint32_t bar = tc::map_rank(&ctl->k_full[st], 0);
-      uint8_t* stage = smem + st * kStageBytes;
-      if (i >= 2) ok = w_wait(&ctl->pv_half[st], ph, ctl, a.status);
-      if (ok) {
-        tc::remote_arrive_expect_tx(bar, ((p0 >= 0) + (p1 >= 0)) * dec::kPageBytes);
-        for (int h = 0; h < 2; ++h)
-          for (int c = 0; c < 2; ++c)
-            if ((h ? p1 : p0) >= 0)
-              tc::tma_load_2d_pair(stage + c * kChunkBytes + h * (kChunkBytes / 2), tm_kv, bar,
-                                   c * 128, (h ? p1 : p0) * kPage);
-      }
-      if (ok && (i == 0 || tile == 0)) {           // a new block
-        if (x > 0) ok = w_wait(&ctl->q_empty, (x - 1) & 1, ctl, a.status);
+  WidePiece piece;
+  while (ok && walk.next(piece)) {
+    pages.begin(piece);
+    for (int t = 0; ok && t < piece.count; ++t, ++i) {
+      const int st = i & 1;
+      const uint32_t ph = ((i >> 1) - 1) & 1;
+      const int cur = pages.take(t + 1 < piece.count, true);
+      const int p0 = __shfl_sync(0xffffffffu, cur, 2 * rank);
+      const int p1 = __shfl_sync(0xffffffffu, cur, 2 * rank + 1);
+      if (lane == 0) {
+        const uint32_t bar = tc::map_rank(&ctl->k_full[st], 0);
+        uint8_t* stage = smem + st * kStageBytes;
+        if (i >= 2) ok = w_wait(&ctl->pv_half[st], ph, ctl, a.status);
         if (ok) {
-          uint8_t* q = smem + kOffQ;
-          const int row = block * kRows + (int)rank * 64;
-          tc::remote_arrive_expect_tx(q_bar, kQBytes);
-          for (int c = 0; c < 4; ++c)
-            tc::tma_load_2d_pair(q + c * kQChunk, tm_q, q_bar, c * 128, row);
-          tc::tma_load_2d_pair(q + 4 * kQChunk, tm_qr, q_bar, 512, row);
+          tc::remote_arrive_expect_tx(bar, ((p0 >= 0) + (p1 >= 0)) * dec::kPageBytes);
+          for (int h = 0; h < 2; ++h)
+            for (int c = 0; c < 2; ++c)
+              if ((h ? p1 : p0) >= 0)
+                tc::tma_load_2d_pair(stage + c * kChunkBytes + h * (kChunkBytes / 2), tm_kv, bar,
+                                     c * 128, (h ? p1 : p0) * kPage);
         }
-        ++block;
-        ++x;
-      }
-      if (ok && i >= 2) ok = w_wait(&ctl->pv_done[st], ph, ctl, a.status);
-      if (ok) {
-        for (int h = 0; h < 2; ++h) {
-          const int id = h ? p1 : p0;
-          if (id < 0) continue;
-          for (int c = 2; c < 4; ++c)
-            tc::tma_load_2d_pair(stage + c * kChunkBytes + h * (kChunkBytes / 2), tm_kv, bar,
-                                 c * 128, id * kPage);
-          tc::tma_load_2d_pair(stage + 4 * kChunkBytes + h * (kRopeBytes / 2), tm_kvr, bar, 512,
-                               id * kPage);
+        if (ok && t == 0) {
+          if (x > 0) ok = w_wait(&ctl->q_empty, (x - 1) & 1, ctl, a.status);
+          if (ok) {
+            uint8_t* q = smem + kOffQ;
+            const int row = (int)(piece.row0 + rank * 64);
+            tc::remote_arrive_expect_tx(q_bar, kQBytes);
+            for (int c = 0; c < 4; ++c)
+              tc::tma_load_2d_pair(q + c * kQChunk, tm_q, q_bar, c * 128, row);
+            tc::tma_load_2d_pair(q + 4 * kQChunk, tm_qr, q_bar, 512, row);
+          }
+        }
+        if (ok && i >= 2) ok = w_wait(&ctl->pv_done[st], ph, ctl, a.status);
+        if (ok) {
+          for (int h = 0; h < 2; ++h) {
+            const int id = h ? p1 : p0;
+            if (id < 0) continue;
+            for (int c = 2; c < 4; ++c)
+              tc::tma_load_2d_pair(stage + c * kChunkBytes + h * (kChunkBytes / 2), tm_kv, bar,
+                                   c * 128, id * kPage);
+            tc::tma_load_2d_pair(stage + 4 * kChunkBytes + h * (kRopeBytes / 2), tm_kvr, bar, 512,
+                                 id * kPage);
+          }
         }
       }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
     }
-    if (++tile == w.tiles) tile = 0;
-    ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+    ++x;
   }
 }
 
-// The other CTA's keys of the own value dims, over the bands S is done with. In a
-// block's last tile the softmax clears V behind the last key, so that must have
-// landed here before rank 0 hears of it.
-__device__ void load_values(const WideArgs& a, const WidePart& w, uint8_t* smem, WideCtl* ctl,
+// Whether keys of the piece's tile t lie past the end.
+__device__ __forceinline__ bool ragged(const WidePiece& p, int t) {
+  return (long long)(p.tile + t + 1) * kKeys > p.len;
+}
+
+// The other CTA's keys of the own value dims, over the bands S is done with. Where
+// the softmax clears V behind the last key, that must have landed here before
+// rank 0 hears of it.
+__device__ void load_values(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl* ctl,
                             uint32_t rank, const CUtensorMap* tm_kv) {
   const int lane = threadIdx.x & 31;
-  const long long n = w.end - w.begin;
   const uint32_t other = 1 - rank;
-  Pages pages(a, w, false);
-  int tile = (int)(w.begin % w.tiles);
-  uint32_t tails = 0;                              // parity of each stage's tails so far
+  Pages pages(a);
+  uint32_t tails = 0, i = 0;                       // parity of each stage's tails so far; tiles
   bool ok = true;
-  for (long long i = 0; ok && i < n; ++i) {
-    const int st = i & 1;
-    const int cur = pages.take(i + 1 < n);
-    const int p0 = __shfl_sync(0xffffffffu, cur, 2 * other);
-    const int p1 = __shfl_sync(0xffffffffu, cur, 2 * other + 1);
-    const bool tail = tile == w.tiles - 1;
-    if (++tile == w.tiles) tile = 0;
-    if (lane == 0 && (ok = w_wait(&ctl->s_full[st], (uint32_t)(i >> 1) & 1, ctl, a.status))) {
-      uint8_t* stage = smem + st * kStageBytes;
-      const uint32_t there = tc::map_rank(&ctl->v_full[st], 0);
-      const uint32_t bar = tail ? tc::map_rank(&ctl->v_tail[st], rank) : there;
-      tc::remote_arrive_expect_tx(bar, ((p0 >= 0) + (p1 >= 0)) * 2 * kPage * 128);
-      for (int h = 0; h < 2; ++h)
-        for (int d = 0; d < 2; ++d)
-          if ((h ? p1 : p0) >= 0)
-            tc::tma_load_2d_pair(stage + (2 * other + d) * kChunkBytes + h * (kChunkBytes / 2), tm_kv,
-                                 bar, (2 * rank + d) * 128, (h ? p1 : p0) * kPage);
-      if (tail) {
-        ok = w_wait(&ctl->v_tail[st], (tails >> st) & 1, ctl, a.status);
-        tc::remote_arrive(there);
+  WidePiece piece;
+  while (ok && walk.next(piece)) {
+    pages.begin(piece);
+    for (int t = 0; ok && t < piece.count; ++t, ++i) {
+      const int st = i & 1;
+      const int cur = pages.take(t + 1 < piece.count, false);
+      const int p0 = __shfl_sync(0xffffffffu, cur, 2 * other);
+      const int p1 = __shfl_sync(0xffffffffu, cur, 2 * other + 1);
+      const bool tail = ragged(piece, t);
+      if (lane == 0 && (ok = w_wait(&ctl->s_full[st], (i >> 1) & 1, ctl, a.status))) {
+        uint8_t* stage = smem + st * kStageBytes;
+        const uint32_t there = tc::map_rank(&ctl->v_full[st], 0);
+        const uint32_t bar = tail ? tc::map_rank(&ctl->v_tail[st], rank) : there;
+        tc::remote_arrive_expect_tx(bar, ((p0 >= 0) + (p1 >= 0)) * 2 * kPage * 128);
+        for (int h = 0; h < 2; ++h)
+          for (int d = 0; d < 2; ++d)
+            if ((h ? p1 : p0) >= 0)
+              tc::tma_load_2d_pair(stage + (2 * other + d) * kChunkBytes + h * (kChunkBytes / 2),
+                                   tm_kv, bar, (2 * rank + d) * 128, (h ? p1 : p0) * kPage);
+        if (tail) {
+          ok = w_wait(&ctl->v_tail[st], (tails >> st) & 1, ctl, a.status);
+          tc::remote_arrive(there);
+        }
       }
+      if (tail) tails ^= 1u << st;
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
     }
-    if (tail) tails ^= 1u << st;
-    ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
   }
 }
 
@@ -247,73 +254,72 @@ __device__ __forceinline__ void mma_drain(uint64_t* bar) {
   }
 }
 
-__device__ void issue_s(const WideArgs& a, const WidePart& w, uint8_t* smem, WideCtl* ctl,
+__device__ void issue_s(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl* ctl,
                         uint32_t tmem) {
   const uint32_t s_kv = tc::smem_u32(smem), s_q = tc::smem_u32(smem + kOffQ);
-  const long long n = w.end - w.begin;
-  int tile = (int)(w.begin % w.tiles);
-  uint32_t x = 0;
-  for (long long i = 0; i < n; ++i) {
-    const int st = i & 1;
-    if (i == 0 || tile == 0) {                     // a new block: its Q in both CTAs
-      if (!w_wait(&ctl->q_full, x & 1, ctl, a.status)) break;
-      ++x;
+  uint32_t x = 0, i = 0;                           // pieces, tiles
+  bool ok = true;
+  WidePiece piece;
+  while (ok && walk.next(piece)) {
+    if (!(ok = w_wait(&ctl->q_full, x & 1, ctl, a.status))) break;     // Q in both CTAs
+    ++x;
+    for (int t = 0; t < piece.count; ++t, ++i) {
+      const int st = i & 1;
+      // The S buffer of tile i - 2 is free: its stage was refilled after its PV,
+      // whose P the softmax wrote after it had read that S.
+      if (!(ok = w_wait(&ctl->k_full[st], (i >> 1) & 1, ctl, a.status))) break;
+      tc::fence_after_sync();
+      const uint32_t kv = s_kv + st * kStageBytes, d = tmem + kSCol + st * 128;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          tc::mma_f8_pair(d, tc::smem_desc(s_q + c * kQChunk + kk * 32, 16, 1024, tc::kSw128),
+                          tc::smem_desc(kv + c * kChunkBytes + kk * 32, 16, 1024, tc::kSw128), kIdescS,
+                          (c | kk) != 0);
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+        tc::mma_f8_pair(d, tc::smem_desc(s_q + 4 * kQChunk + kk * 32, 16, 512, tc::kSw64),
+                        tc::smem_desc(kv + 4 * kChunkBytes + kk * 32, 16, 512, tc::kSw64), kIdescS,
+                        true);
+      tc::mma_commit_pair(&ctl->s_full[st]);
     }
-    // The S buffer of tile i - 2 is free: its stage was refilled after its PV,
-    // whose P the softmax wrote after it had read that S.
-    if (!w_wait(&ctl->k_full[st], (uint32_t)(i >> 1) & 1, ctl, a.status)) break;
-    tc::fence_after_sync();
-    const uint32_t kv = s_kv + st * kStageBytes, d = tmem + kSCol + st * 128;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        tc::mma_f8_pair(d, tc::smem_desc(s_q + c * kQChunk + kk * 32, 16, 1024, tc::kSw128),
-                        tc::smem_desc(kv + c * kChunkBytes + kk * 32, 16, 1024, tc::kSw128), kIdescS,
-                        (c | kk) != 0);
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk)
-      tc::mma_f8_pair(d, tc::smem_desc(s_q + 4 * kQChunk + kk * 32, 16, 512, tc::kSw64),
-                      tc::smem_desc(kv + 4 * kChunkBytes + kk * 32, 16, 512, tc::kSw64), kIdescS, true);
-    tc::mma_commit_pair(&ctl->s_full[st]);
-    if (++tile == w.tiles) tile = 0;
-    if (tile == 0) tc::mma_commit_pair(&ctl->q_empty);
+    if (ok) tc::mma_commit_pair(&ctl->q_empty);
   }
   mma_drain(&ctl->drain[0]);
 }
 
-__device__ void issue_pv(const WideArgs& a, const WidePart& w, uint8_t* smem, WideCtl* ctl,
+__device__ void issue_pv(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl* ctl,
                          uint32_t tmem) {
   const uint32_t s_kv = tc::smem_u32(smem), s_p = tc::smem_u32(smem + kOffP);
-  const long long n = w.end - w.begin;
-  int tile = (int)(w.begin % w.tiles);
-  bool first = true;                               // the pair's first tile of the block
+  uint32_t i = 0;
   bool ok = true;
-  for (long long i = 0; ok && i < n; ++i) {
-    const int st = i & 1;
-    ok = w_wait(&ctl->v_full[st], (uint32_t)(i >> 1) & 1, ctl, a.status);
+  WidePiece piece;
+  while (ok && walk.next(piece)) {
+    for (int t = 0; ok && t < piece.count; ++t, ++i) {
+      const int st = i & 1;
+      ok = w_wait(&ctl->v_full[st], (i >> 1) & 1, ctl, a.status);
 #pragma unroll
-    for (int kh = 0; kh < 2; ++kh) {               // CTA 0's keys, then CTA 1's
-      ok = ok && w_wait(&ctl->p_full[kh], (uint32_t)i & 1, ctl, a.status);
-      if (!ok) break;
-      tc::fence_after_sync();
-      const uint32_t kv = s_kv + st * kStageBytes;
+      for (int kh = 0; kh < 2; ++kh) {               // CTA 0's keys, then CTA 1's
+        ok = ok && w_wait(&ctl->p_full[kh], i & 1, ctl, a.status);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint32_t kv = s_kv + st * kStageBytes;
 #pragma unroll
-      for (int d = 0; d < 2; ++d)
+        for (int d = 0; d < 2; ++d)
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const uint64_t v = tc::smem_desc(kv + (kh * 2 + d) * kChunkBytes + kk * 32 * 128,
-                                           kChunkBytes, 1024, tc::kSw128);
-          const uint32_t p = s_p + kh * kPChunk + kk * 32;
-          tc::mma_f8_pair(tmem + d * 128, tc::smem_desc(p, 16, 1024, tc::kSw128), v, kIdescHi,
-                          !(first && kh == 0 && kk == 0));
-          tc::mma_f8_pair(tmem + d * 128, tc::smem_desc(p + 2 * kPChunk, 16, 1024, tc::kSw128), v,
-                          kIdescLo, true);
-        }
-      tc::mma_commit_pair(kh == 0 ? &ctl->pv_half[st] : &ctl->pv_done[st]);
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t v = tc::smem_desc(kv + (kh * 2 + d) * kChunkBytes + kk * 32 * 128,
+                                             kChunkBytes, 1024, tc::kSw128);
+            const uint32_t p = s_p + kh * kPChunk + kk * 32;
+            tc::mma_f8_pair(tmem + d * 128, tc::smem_desc(p, 16, 1024, tc::kSw128), v, kIdescHi,
+                            !(t == 0 && kh == 0 && kk == 0));
+            tc::mma_f8_pair(tmem + d * 128, tc::smem_desc(p + 2 * kPChunk, 16, 1024, tc::kSw128), v,
+                            kIdescLo, true);
+          }
+        tc::mma_commit_pair(kh == 0 ? &ctl->pv_half[st] : &ctl->pv_done[st]);
+      }
     }
-    if (++tile == w.tiles) tile = 0;
-    first = tile == 0;
   }
   mma_drain(&ctl->drain[1]);
 }
@@ -368,7 +374,7 @@ __device__ __forceinline__ void weigh(const uint32_t (&raw)[32], float scale, fl
 // four warps of a lane quarter take 32 of its columns each. A thread that gave up
 // a wait goes on through the barriers, so that every thread reaches each of
 // them, until the next vote has all of them leave.
-__device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, WideCtl* ctl,
+__device__ void softmax(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl* ctl,
                         uint32_t tmem, uint32_t rank) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3, group = (warp - 4) >> 2;
@@ -376,9 +382,7 @@ __device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
   const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
   const int col0 = group * 32;                     // of S: keys; of a half of O: dims
   float* const mine = &ctl->red[kh * 4 + group][row];
-  const long long n = w.end - w.begin;
-  int block = (int)(w.begin / w.tiles), first_tile = (int)(w.begin % w.tiles);
-  uint32_t tails = 0;                              // parity of each stage's tails so far
+  uint32_t tails = 0, g = 0;                       // parity of each stage's tails so far; tiles
   bool ok = true;                                  // warp-uniform
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     const bool got = ok && w_wait(bar, parity, ctl, a.status);
@@ -398,22 +402,21 @@ __device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
     for (int j = 0; j < 8; ++j) v += ctl->red[j][row];
     return v;
   };
-  long long g = 0;
-  while (g < n) {
-    const int nt = (int)min((long long)(w.tiles - first_tile), n - g);
+  WidePiece piece;
+  while (walk.next(piece)) {
     float m = -INFINITY, l = 0.f;                  // the row's max; this thread's share of its sum
-    for (int t = 0; t < nt; ++t, ++g) {
+    for (int t = 0; t < piece.count; ++t, ++g) {
       const int st = g & 1;
-      const uint32_t ph = (uint32_t)(g >> 1) & 1;
-      const int key0 = (first_tile + t) * kKeys;
-      const bool tail = key0 + kKeys > w.len;
+      const uint32_t ph = (g >> 1) & 1;
+      const int key0 = (piece.tile + t) * kKeys;
+      const bool tail = ragged(piece, t);
       wait(&ctl->s_full[st], ph);
       tc::fence_after_sync();
       uint32_t raw[32], hi[8], lo[8];
       tc::tmem_ld32(tmem + lanes + kSCol + st * 128 + col0, raw);
       tc::tmem_wait_ld();
       if (tail) {                                  // keys past the end
-        const int left = w.len - (key0 + kh * 128 + col0);
+        const int left = piece.len - (key0 + kh * 128 + col0);
 #pragma unroll
         for (int i = 0; i < 32; ++i)
           if (i >= left) raw[i] = 0xff800000u;     // -inf
@@ -439,7 +442,7 @@ __device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
         m = mn;
         l *= f;
         if (t > 0) {
-          wait(&ctl->pv_done[(g - 1) & 1], (uint32_t)((g - 1) >> 1) & 1);
+          wait(&ctl->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
           tc::fence_after_sync();
 #pragma unroll 1
           for (int d = 0; d < 2; ++d) {
@@ -461,7 +464,7 @@ __device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
       // P of these keys is free once PV of the previous tile is done with it.
       if (g > 0)
         wait(kh == 0 ? &ctl->pv_half[(g - 1) & 1] : &ctl->pv_done[(g - 1) & 1],
-             (uint32_t)((g - 1) >> 1) & 1);
+             ((g - 1) >> 1) & 1);
       // Rows of 128 bytes (128 keys) in 16-byte pieces, piece j of row r at j ^ (r & 7).
       uint8_t* p = smem + kOffP + kh * kPChunk + row * 128;
 #pragma unroll
@@ -478,15 +481,15 @@ __device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
         wait(&ctl->v_tail[st], (tails >> st) & 1);
         for (int z = threadIdx.x - 128; z < kKeys * 2; z += kSoft) {
           const int key = z >> 1, slot = (key >> 7) * 2 + (z & 1);
-          if (key0 + key >= w.len) {
+          if (key0 + key >= piece.len) {
             uint4* v = reinterpret_cast<uint4*>(smem + st * kStageBytes + slot * kChunkBytes +
                                                 (key & 127) * 128);
 #pragma unroll
             for (int u = 0; u < 8; ++u) v[u] = make_uint4(0, 0, 0, 0);
           }
         }
+        tails ^= 1u << st;
       }
-      if (first_tile + t == w.tiles - 1) tails ^= 1u << st;
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
       if (tail) soft_sync();                       // V is clear before any P of this CTA counts
@@ -497,10 +500,10 @@ __device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
     soft_sync();                                   // red[] is free
     const float z = row_sum(l);
     const float inv = z > 0.f ? 1.f / z : 0.f;
-    const size_t at = (size_t)(w.unit + block) * kRows + rank * 64 + row;
-    const bool live = (long long)block * kRows + rank * 64 + row < a.N;
+    const size_t at = piece.slot + rank * 64 + row;
+    const bool live = piece.row0 + rank * 64 + row < piece.row_end;
     if (live && kh == 0 && group == 0) a.part_lse[at] = z == 0.f ? -INFINITY : m + __log2f(z);
-    wait(&ctl->pv_done[(g - 1) & 1], (uint32_t)((g - 1) >> 1) & 1);
+    wait(&ctl->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
     tc::fence_after_sync();
 #pragma unroll 1
     for (int d = 0; d < 2; ++d) {
@@ -516,9 +519,7 @@ __device__ void softmax(const WideArgs& a, const WidePart& w, uint8_t* smem, Wid
       }
     }
     tc::fence_before_sync();
-    soft_sync();                                   // O is read before any P of the next block counts
-    ++block;
-    first_tile = 0;
+    soft_sync();                                   // O is read before any P of the next piece counts
   }
 }
 
@@ -566,20 +567,30 @@ wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
 
   grid_dep_wait();
   grid_dep_launch();
-  const WidePart w = wide_part(a, (int)(blockIdx.x >> 1), threadIdx.x == 0);
-  if (w.begin == w.end) {
-    // No tiles for this pair.
+  long long* plan = reinterpret_cast<long long*>(smem + kOffPlan);
+  for (int i = threadIdx.x; i <= a.R; i += kThreads) plan[i] = a.plan[i];
+  if (blockIdx.x == 0) {       // lengths past their tables are cut off (prefix.h)
+    for (int i = threadIdx.x; i <= a.R; i += kThreads) {
+      const int len = i < a.R ? a.seq_lens[i] : *a.prefix_len;
+      const int pages = i < a.R ? a.max_pages : a.prefix_pages;
+      if (len > (long long)pages * kPage && a.status) atomicOr(a.status, MLA_FAULT_PAGE_RANGE);
+    }
+  }
+  __syncthreads();
+  const WideWalk walk(a, plan, (int)(blockIdx.x >> 1));
+  if (walk.pos == walk.end) {
+    // Nothing for this pair.
   } else if (warp == 0) {
-    load_keys(a, w, smem, ctl, rank, &tm_kv, &tm_kvr, &tm_q, &tm_qr);
+    load_keys(a, walk, smem, ctl, rank, &tm_kv, &tm_kvr, &tm_q, &tm_qr);
   } else if (warp == 3) {
-    load_values(a, w, smem, ctl, rank, &tm_kv);
+    load_values(a, walk, smem, ctl, rank, &tm_kv);
   } else if (warp >= 4) {
-    softmax(a, w, smem, ctl, tmem, rank);
+    softmax(a, walk, smem, ctl, tmem, rank);
   } else if (rank == 0 && lane == 0) {
     if (warp == 1)
-      issue_s(a, w, smem, ctl, tmem);
+      issue_s(a, walk, smem, ctl, tmem);
     else
-      issue_pv(a, w, smem, ctl, tmem);
+      issue_pv(a, walk, smem, ctl, tmem);
   }
   tc::fence_before_sync();
   __syncthreads();
