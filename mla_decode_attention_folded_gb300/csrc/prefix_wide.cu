@@ -500,26 +500,37 @@ __device__ void softmax(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl
     soft_sync();                                   // red[] is free
     const float z = row_sum(l);
     const float inv = z > 0.f ? 1.f / z : 0.f;
-    const size_t at = piece.slot + rank * 64 + row;
-    const bool live = piece.row0 + rank * 64 + row < piece.row_end;
-    if (live && kh == 0 && group == 0) a.part_lse[at] = z == 0.f ? -INFINITY : m + __log2f(z);
+    const size_t first_row = piece.slot + rank * 64;
+    const int live = (int)min(64LL, piece.row_end - piece.row0 - rank * 64);
+    if (row < live && kh == 0 && group == 0)
+      a.part_lse[first_row + row] = z == 0.f ? -INFINITY : m + __log2f(z);
     wait(&ctl->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
     tc::fence_after_sync();
+    // Through P's place, 16 of each thread's 32 columns of a half at a time, so that
+    // a warp stores pieces of 64 bytes of one row; 16-byte pieces c of row r at
+    // c ^ (r & 7).
+    float4* const stage = reinterpret_cast<float4*>(smem + kOffP);
 #pragma unroll 1
-    for (int d = 0; d < 2; ++d) {
-      uint32_t o[32];
-      tc::tmem_ld32(tmem + lanes + d * 128 + col0, o);
+    for (int turn = 0; turn < 4; ++turn) {         // dims 128 (turn / 2) + 16 (turn % 2) ..
+      uint32_t o[16];
+      tc::tmem_ld16(tmem + lanes + (turn >> 1) * 128 + col0 + (turn & 1) * 16, o);
       tc::tmem_wait_ld();
-      if (live) {                                  // columns of half d: band d of CTA kh's dims
-        float4* dst = reinterpret_cast<float4*>(a.part_o + at * kDv + kh * 256 + d * 128 + col0);
 #pragma unroll
-        for (int i = 0; i < 32; i += 4)
-          dst[i / 4] = make_float4(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
-                                   __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
-      }
+      for (int j = 0; j < 4; ++j)
+        stage[row * 32 + ((kh * 16 + group * 4 + j) ^ (row & 7))] =
+            make_float4(__uint_as_float(o[4 * j]) * inv, __uint_as_float(o[4 * j + 1]) * inv,
+                        __uint_as_float(o[4 * j + 2]) * inv, __uint_as_float(o[4 * j + 3]) * inv);
+      soft_sync();
+      const int dim = (lane >> 4) * 256 + (turn >> 1) * 128 + ((lane >> 2) & 3) * 32 +
+                      (turn & 1) * 16 + (lane & 3) * 4;
+#pragma unroll
+      for (int r = warp - 4; r < 64; r += kSoft / 32)
+        if (r < live)
+          *reinterpret_cast<float4*>(a.part_o + (first_row + r) * kDv + dim) =
+              stage[r * 32 + (lane ^ (r & 7))];
+      soft_sync();                                 // the place, and after the last turn O, is free
     }
     tc::fence_before_sync();
-    soft_sync();                                   // O is read before any P of the next piece counts
   }
 }
 
