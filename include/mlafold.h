@@ -429,7 +429,9 @@ int32_t mla_query_absorb(const mla_query_shape *shape, const void *q, const void
 /* The decode of a batch whose requests all begin with one shared prefix, for
  * mla_shape with groups 0 or 1 (its policy, min_split_tokens and max_splits are
  * not used: the work is cut into equal parts, one per pair of CTAs, num_ctas / 2
- * pairs).
+ * pairs). Refused with MLA_ERR_SHAPE: a shape whose work has 2^31 or more places,
+ * ceil(N / 128) (prefix_pages / 4 + 2) + R ceil(M / 128) (max_pages / 4 + 2) at
+ * most, or as many workspace rows.
  *
  * mla_prefix_workspace_bytes -- bytes of workspace the decode needs. Writes the
  * size to *bytes. Host only.
@@ -437,7 +439,7 @@ int32_t mla_query_absorb(const mla_query_shape *shape, const void *q, const void
  * mla_prefix_plan -- once per step, reused by every layer: where each request's
  * own keys lie in the line of work (one CTA; integer arithmetic only).
  *   seq_lens  [R] int32, device: the requests' own keys (negative is read as 0).
- *   plan      [plan_len] int64, device, plan_len >= R + 1: words 0 .. R written.
+ *   plan      [plan_len] int32, device, plan_len >= R + 1: words 0 .. R written.
  *
  * mla_prefix_decode -- the prefix's keys are read and multiplied once for all
  * R*k*H rows; each request's own keys (none is fine) follow; one softmax over both:
@@ -465,12 +467,12 @@ int32_t mla_query_absorb(const mla_query_shape *shape, const void *q, const void
  * relative, down to 2^-13 where p is small) and that all partial results stay
  * FP32 until one rounding to BF16. */
 int32_t mla_prefix_workspace_bytes(const mla_shape *shape, size_t *bytes);
-int32_t mla_prefix_plan(const mla_shape *shape, const int32_t *seq_lens, int64_t *plan,
+int32_t mla_prefix_plan(const mla_shape *shape, const int32_t *seq_lens, int32_t *plan,
                         int32_t plan_len, mla_stream_t stream);
 int32_t mla_prefix_decode(const mla_shape *shape, int32_t prefix_pages, const void *q,
                           const void *kv, const int32_t *prefix_table, const int32_t *prefix_len,
                           const int32_t *block_table, const int32_t *seq_lens, float bmm1_scale,
-                          float bmm2_scale, const int64_t *plan, int32_t plan_len, void *workspace,
+                          float bmm2_scale, const int32_t *plan, int32_t plan_len, void *workspace,
                           size_t workspace_bytes, void *out, float *lse, int32_t *status,
                           mla_stream_t stream);
 

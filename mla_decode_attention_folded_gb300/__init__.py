@@ -493,7 +493,7 @@ def prefix_workspace_bytes(shape: MlaShape) -> int:
 
 
 def prefix_plan(shape: MlaShape, seq_lens, plan, stream=None) -> None:
-    """The line of work of the requests' own keys: plan [R + 1] int64 (see
+    """The line of work of the requests' own keys: plan [R + 1] int32 (see
     mla_prefix_plan in include/mlafold.h)."""
     _lib.check("mla_prefix_plan", _lib.load().mla_prefix_plan(
         ctypes.byref(shape), _ptr(seq_lens), _ptr(plan), plan.numel(), _stream(stream)))
@@ -528,7 +528,7 @@ class PrefixMla:
         self.max_pages, self.prefix_pages, self.num_pages = max_pages, prefix_pages, num_pages
         self.workspace = torch.empty(prefix_workspace_bytes(self.shape), dtype=torch.uint8,
                                      device=self.device)
-        self.places = torch.zeros(R + 1, dtype=torch.int64, device=self.device)
+        self.places = torch.zeros(R + 1, dtype=torch.int32, device=self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
 
     def plan(self, seq_lens, stream=None) -> None:

@@ -25,17 +25,16 @@ constexpr int kWarps = 8;                  // rows per CTA
 
 __global__ void __launch_bounds__(kMaxR)
 prefix_plan_kernel(const int32_t* __restrict__ seq_lens, int R, int max_pages, int own_blocks,
-                   long long* __restrict__ plan) {
-  __shared__ long long s_warp[32];
+                   int32_t* __restrict__ plan) {
+  __shared__ int s_warp[32];
   grid_dep_wait();
   grid_dep_launch();
   const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
-  const long long tiles = i < R ? cdiv(wide_len(seq_lens[i], max_pages), kWideKeys) : 0;
-  const long long mine = tiles > 0 ? own_blocks * (tiles + 1) : 0;
-  long long sum = mine;
+  const int tiles = i < R ? (int)cdiv(wide_len(seq_lens[i], max_pages), kWideKeys) : 0;
+  int sum = tiles > 0 ? own_blocks * (tiles + 1) : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long t = __shfl_up_sync(0xffffffffu, sum, o);
+    const int t = __shfl_up_sync(0xffffffffu, sum, o);
     if (lane >= o) sum += t;
   }
   if (lane == 31) s_warp[warp] = sum;
@@ -47,7 +46,7 @@ prefix_plan_kernel(const int32_t* __restrict__ seq_lens, int R, int max_pages, i
 
 struct MergeArgs {
   const int32_t* prefix_len;               // [1]
-  const long long* plan;                   // [R + 1]
+  const int32_t* plan;                     // [R + 1]
   const float* part_o;                     // [slots][128][512]
   const float* part_lse;                   // [slots][128]
   uint16_t* out;                           // [N][512]
@@ -63,25 +62,25 @@ __global__ void __launch_bounds__(kWarps * 32) prefix_merge_kernel(const MergeAr
   const int m = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (m >= a.M) return;
   const size_t row = (size_t)r * a.M + m;
-  const long long own = a.plan[r], own_next = a.plan[r + 1];
+  const int own = a.plan[r], own_next = a.plan[r + 1];
   const WideLine line(*a.prefix_len, a.plan[a.R], a.prefix_pages, a.blocks, a.units);
   // The pieces of this row's two segments, in consecutive slots each.
   int n_pre = 0, n_own = 0;
   size_t pre = 0, mine = 0;
-  auto pieces = [&](long long first, long long tiles, long long segment, int in_block, size_t& at) {
+  auto pieces = [&](int first, int tiles, int segment, int in_block, size_t& at) {
     const int u0 = line.unit_of(first), u1 = line.unit_of(first + tiles - 1);
     at = (size_t)(u0 + segment) * kWideRows + in_block;
     return u1 - u0 + 1;
   };
   if (line.prefix_tiles > 0) {
-    const long long b = (long long)(row / kWideRows);
+    const int b = (int)(row / kWideRows);
     n_pre = pieces(b * (line.prefix_tiles + 1), line.prefix_tiles, b, (int)(row % kWideRows), pre);
   }
-  const long long span = (own_next - own) / a.own_blocks;
+  const int span = (own_next - own) / a.own_blocks;
   if (span >= 2) {
     const int j = m / kWideRows;
     n_own = pieces(line.prefix_places + own + j * span, span - 1,
-                   a.blocks + (long long)r * a.own_blocks + j, m % kWideRows, mine);
+                   a.blocks + r * a.own_blocks + j, m % kWideRows, mine);
   }
   const int n = n_pre + n_own;
   auto at = [&](int s) {
@@ -149,10 +148,17 @@ size_t wide_rows(const mla_shape& s) {
 size_t wide_out_bytes(const mla_shape& s) { return align256(wide_rows(s) * kDv * 4); }
 size_t wide_bytes(const mla_shape& s) { return wide_out_bytes(s) + align256(wide_rows(s) * 4); }
 
+// Places on the line of work: 31 bits hold them.
+bool places_fit(const mla_shape& s, int prefix_pages) {
+  const long long own = (long long)s.R * wide_own_blocks(s) * (cdiv((long long)s.max_pages * kPage, kWideKeys) + 1);
+  return own + wide_blocks(s) * (cdiv((long long)prefix_pages * kPage, kWideKeys) + 1) < (1LL << 31) &&
+         wide_rows(s) < (1ull << 31);
+}
+
 int check_prefix_shape(const mla_shape* s) {
   const int st = check_shape(s);
   if (st != MLA_OK) return st;
-  return shape_groups(*s) == 1 ? MLA_OK : MLA_ERR_SHAPE;
+  return shape_groups(*s) == 1 && places_fit(*s, 1) ? MLA_OK : MLA_ERR_SHAPE;
 }
 
 }  // namespace
@@ -168,18 +174,18 @@ extern "C" int32_t mla_prefix_workspace_bytes(const mla_shape* shape, size_t* by
   return MLA_OK;
 }
 
-extern "C" int32_t mla_prefix_plan(const mla_shape* shape, const int32_t* seq_lens, int64_t* plan,
+extern "C" int32_t mla_prefix_plan(const mla_shape* shape, const int32_t* seq_lens, int32_t* plan,
                                    int32_t plan_len, mla_stream_t stream) {
   int st = check_prefix_shape(shape);
   if (st != MLA_OK) return st;
   if (!seq_lens || !plan) return MLA_ERR_NULL;
-  if (!aligned(seq_lens, 4) || !aligned(plan, 8)) return MLA_ERR_ALIGN;
+  if (!aligned(seq_lens, 4) || !aligned(plan, 4)) return MLA_ERR_ALIGN;
   if (plan_len < shape->R + 1) return MLA_ERR_LIST;
   if ((st = check_device()) != MLA_OK) return st;
   const cudaError_t e =
       launch(prefix_plan_kernel, dim3(1), (shape->R + 31) / 32 * 32,
              reinterpret_cast<cudaStream_t>(stream), seq_lens, shape->R, shape->max_pages,
-             wide_own_blocks(*shape), reinterpret_cast<long long*>(plan));
+             wide_own_blocks(*shape), plan);
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
@@ -187,18 +193,19 @@ extern "C" int32_t mla_prefix_decode(const mla_shape* shape, int32_t prefix_page
                                      const void* kv, const int32_t* prefix_table,
                                      const int32_t* prefix_len, const int32_t* block_table,
                                      const int32_t* seq_lens, float bmm1_scale, float bmm2_scale,
-                                     const int64_t* plan, int32_t plan_len, void* workspace,
+                                     const int32_t* plan, int32_t plan_len, void* workspace,
                                      size_t workspace_bytes_given, void* out, float* lse,
                                      int32_t* status, mla_stream_t stream) {
   int st = check_prefix_shape(shape);
   if (st != MLA_OK) return st;
-  if (prefix_pages < 1 || prefix_pages > (1 << 24)) return MLA_ERR_SHAPE;
+  if (prefix_pages < 1 || prefix_pages > (1 << 24) || !places_fit(*shape, prefix_pages))
+    return MLA_ERR_SHAPE;
   if (!q || !kv || !prefix_table || !prefix_len || !block_table || !seq_lens || !plan ||
       !workspace || !out)
     return MLA_ERR_NULL;
   if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
       !aligned(prefix_table, 4) || !aligned(prefix_len, 4) || !aligned(block_table, 4) ||
-      !aligned(seq_lens, 4) || !aligned(plan, 8) || !aligned(workspace, 256) || !aligned(status, 4))
+      !aligned(seq_lens, 4) || !aligned(plan, 4) || !aligned(workspace, 256) || !aligned(status, 4))
     return MLA_ERR_ALIGN;
   if (plan_len < shape->R + 1) return MLA_ERR_LIST;
   if (workspace_bytes_given < wide_bytes(*shape)) return MLA_ERR_WORKSPACE;
@@ -210,7 +217,7 @@ extern "C" int32_t mla_prefix_decode(const mla_shape* shape, int32_t prefix_page
   w.prefix_len = prefix_len;
   w.block_table = block_table;
   w.seq_lens = seq_lens;
-  w.plan = reinterpret_cast<const long long*>(plan);
+  w.plan = plan;
   w.part_o = static_cast<float*>(workspace);
   w.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + wide_out_bytes(*shape));
   w.status = status;

@@ -24,7 +24,7 @@ struct WideArgs {
   const int32_t* prefix_len;       // [1]
   const int32_t* block_table;      // [R][max_pages]
   const int32_t* seq_lens;         // [R]
-  const long long* plan;           // [R + 1]: first place of each request's segments
+  const int32_t* plan;             // [R + 1]: first place of each request's segments
   float* part_o;                   // [slots][128][512]
   float* part_lse;                 // [slots][128]
   int32_t* status;                 // may be null
@@ -39,86 +39,85 @@ __host__ __device__ __forceinline__ int wide_len(int len, int pages) {
   return len < 0 ? 0 : (int)(len < most ? len : most);
 }
 
-// The whole line, and how it is cut.
+// The whole line, and how it is cut. Places fit 31 bits (the host checks).
 struct WideLine {
-  int prefix_len, prefix_tiles;
-  long long prefix_places, places;
-  long long used;                  // parts: no more than there are places
-  __device__ __forceinline__ WideLine(int prefix_len_, long long own_places, int prefix_pages,
-                                      int blocks, int units) {
+  int prefix_len, prefix_tiles, prefix_places, places;
+  int used;                        // parts: no more than there are places
+  __device__ __forceinline__ WideLine(int prefix_len_, int own_places, int prefix_pages, int blocks,
+                                      int units) {
     prefix_len = wide_len(prefix_len_, prefix_pages);
     prefix_tiles = (int)cdiv(prefix_len, kWideKeys);
-    prefix_places = prefix_tiles > 0 ? (long long)blocks * (prefix_tiles + 1) : 0;
+    prefix_places = prefix_tiles > 0 ? blocks * (prefix_tiles + 1) : 0;
     places = prefix_places + own_places;
     used = places < units ? places : units;
   }
-  __device__ __forceinline__ long long part(long long unit) const {
-    return unit < used ? unit * places / used : places;
+  __device__ __forceinline__ int part(int unit) const {
+    return unit < used ? (int)((long long)unit * places / used) : places;
   }
-  __device__ __forceinline__ int unit_of(long long place) const {
-    return (int)(((place + 1) * used - 1) / places);
+  __device__ __forceinline__ int unit_of(int place) const {
+    return (int)(((place + 1LL) * used - 1) / places);
   }
 };
 
 // What one part does with one segment.
 struct WidePiece {
   const int32_t* table;
-  long long row0;                  // first row; rows from row_end on are others'
-  long long row_end;
-  size_t slot;
+  int row0, row_end;               // first row; rows from row_end on are others'
+  int slot;
   int len, tile, count;            // keys, first tile, tiles
 };
 
-// The pieces of part `unit`, in order. `plan` may lie in shared memory.
+// The pieces of part `unit`, in order, from the plan and the lengths ([R] each,
+// the plan with its end) as the caller holds them.
 struct WideWalk {
   const WideArgs& a;
-  const long long* plan;
-  const WideLine line;
-  long long pos, end;
-  int unit;
-  __device__ WideWalk(const WideArgs& a_, const long long* plan_, int unit_)
-      : a(a_), plan(plan_),
-        line(*a_.prefix_len, plan_[a_.R], a_.prefix_pages, a_.blocks, a_.units), unit(unit_) {
+  const int32_t* plan;
+  const int32_t* lens;
+  int prefix_len, prefix_tiles, prefix_places;
+  int pos, end, unit, r = 0;
+  __device__ WideWalk(const WideArgs& a_, const int32_t* plan_, const int32_t* lens_, int unit_)
+      : a(a_), plan(plan_), lens(lens_), unit(unit_) {
+    const WideLine line(*a_.prefix_len, plan_[a_.R], a_.prefix_pages, a_.blocks, a_.units);
+    prefix_len = line.prefix_len;
+    prefix_tiles = line.prefix_tiles;
+    prefix_places = line.prefix_places;
     pos = line.part(unit);
     end = line.part(unit + 1);
+    const int at = pos - prefix_places;
+    for (int step = 1 << 30; step; step >>= 1)       // the last request that begins at or before
+      if (r + step < a.R && plan[r + step] <= at) r += step;
   }
   __device__ bool next(WidePiece& p) {
     while (pos < end) {
-      long long first;             // the segment's first place
-      int tiles, segment;
-      if (pos < line.prefix_places) {
-        segment = (int)(pos / (line.prefix_tiles + 1));
-        tiles = line.prefix_tiles;
-        first = (long long)segment * (tiles + 1);
+      int first, tiles, segment;                     // first: the segment's first place
+      if (pos < prefix_places) {
+        tiles = prefix_tiles;
+        segment = (int)((unsigned)pos / (unsigned)(tiles + 1));
+        first = segment * (tiles + 1);
         p.table = a.prefix_table;
-        p.len = line.prefix_len;
-        p.row0 = (long long)segment * kWideRows;
-        p.row_end = a.N;
+        p.len = prefix_len;
+        p.row0 = segment * kWideRows;
+        p.row_end = (int)a.N;
       } else {
-        const long long at = pos - line.prefix_places;
-        int lo = 0, hi = a.R - 1;  // the last request that begins at or before it
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (plan[mid] <= at) lo = mid; else hi = mid - 1;
-        }
-        const long long span = (plan[lo + 1] - plan[lo]) / a.own_blocks;
-        if (span < 2) return false;                  // not a plan of this shape
-        const int j = (int)((at - plan[lo]) / span);
-        segment = a.blocks + lo * a.own_blocks + j;
-        tiles = (int)(span - 1);
-        first = line.prefix_places + plan[lo] + j * span;
-        p.table = a.block_table + (long long)lo * a.max_pages;
-        p.len = wide_len(a.seq_lens[lo], a.max_pages);
-        p.row0 = (long long)lo * a.M + (long long)j * kWideRows;
-        p.row_end = (long long)(lo + 1) * a.M;
+        const int at = pos - prefix_places;
+        while (r + 1 < a.R && plan[r + 1] <= at) ++r;
+        const unsigned span = (unsigned)(plan[r + 1] - plan[r]) / (unsigned)a.own_blocks;
+        if ((int)span < 2) return false;             // not a plan of this shape
+        const int j = (int)((unsigned)(at - plan[r]) / span);
+        tiles = (int)span - 1;
+        segment = a.blocks + r * a.own_blocks + j;
+        first = prefix_places + plan[r] + j * (int)span;
+        p.table = a.block_table + (long long)r * a.max_pages;
+        p.len = lens[r];
+        p.row0 = r * a.M + j * kWideRows;
+        p.row_end = (r + 1) * a.M;
       }
-      const long long last = first + tiles, stop = end < last ? end : last;
-      const long long from = pos;
+      const int last = first + tiles, stop = end < last ? end : last, from = pos;
       pos = stop < last ? stop : last + 1;
       if (from >= last) continue;                    // the place after the tiles
-      p.tile = (int)(from - first);
-      p.count = (int)(stop - from);
-      p.slot = (size_t)(unit + segment) * kWideRows;
+      p.tile = from - first;
+      p.count = stop - from;
+      p.slot = (unit + segment) * kWideRows;
       return true;
     }
     return false;

@@ -75,9 +75,9 @@ struct WideCtl {
   int abort_flag;
   alignas(16) float red[8][64];     // row values of the eight threads that share a row
 };
-// Behind the control block: the plan, R + 1 places.
+// Behind the control block: the plan (R + 1 places) and the lengths.
 constexpr int kOffPlan = kOffCtl + (int)((sizeof(WideCtl) + 15) / 16 * 16);
-constexpr int kSmemBytes = kOffPlan + (kMaxR + 1) * 8 + 1024;
+constexpr int kSmemBytes = kOffPlan + (2 * kMaxR + 1) * 4 + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ bool w_wait(uint64_t* bar, uint32_t parity, WideCtl* ctl,
@@ -174,7 +174,7 @@ __device__ void load_keys(const WideArgs& a, WideWalk walk, uint8_t* smem, WideC
           if (x > 0) ok = w_wait(&ctl->q_empty, (x - 1) & 1, ctl, a.status);
           if (ok) {
             uint8_t* q = smem + kOffQ;
-            const int row = (int)(piece.row0 + rank * 64);
+            const int row = piece.row0 + (int)rank * 64;
             tc::remote_arrive_expect_tx(q_bar, kQBytes);
             for (int c = 0; c < 4; ++c)
               tc::tma_load_2d_pair(q + c * kQChunk, tm_q, q_bar, c * 128, row);
@@ -500,36 +500,43 @@ __device__ void softmax(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl
     soft_sync();                                   // red[] is free
     const float z = row_sum(l);
     const float inv = z > 0.f ? 1.f / z : 0.f;
-    const size_t first_row = piece.slot + rank * 64;
-    const int live = (int)min(64LL, piece.row_end - piece.row0 - rank * 64);
+    const size_t first_row = (size_t)piece.slot + rank * 64;
+    const int live = min(64, piece.row_end - piece.row0 - (int)rank * 64);
     if (row < live && kh == 0 && group == 0)
       a.part_lse[first_row + row] = z == 0.f ? -INFINITY : m + __log2f(z);
     wait(&ctl->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
     tc::fence_after_sync();
-    // Through P's place, 16 of each thread's 32 columns of a half at a time, so that
-    // a warp stores pieces of 64 bytes of one row; 16-byte pieces c of row r at
-    // c ^ (r & 7).
-    float4* const stage = reinterpret_cast<float4*>(smem + kOffP);
+    // Through 2 KB of P's place per warp, 16 of its 32 columns of a half at a time:
+    // lane l then stores 16-byte piece l % 4 of rows l / 4, l / 4 + 8, ..., 64 bytes
+    // of a row per four lanes. Piece c of row r lies at c ^ ((r >> 1) & 3).
+    float4* const stage = reinterpret_cast<float4*>(smem + kOffP) + (warp - 4) * 128;
+    float* const dst = a.part_o + (first_row + (quarter & 1) * 32 + (lane >> 2)) * kDv + kh * 256 +
+                       col0 + (lane & 3) * 4;
+    const int rows = live - (quarter & 1) * 32 - (lane >> 2);      // of this lane, 8 apart
 #pragma unroll 1
-    for (int turn = 0; turn < 4; ++turn) {         // dims 128 (turn / 2) + 16 (turn % 2) ..
+    for (int turn = 0; turn < 4; ++turn) {         // columns 128 (turn / 2) + 16 (turn % 2) ..
       uint32_t o[16];
       tc::tmem_ld16(tmem + lanes + (turn >> 1) * 128 + col0 + (turn & 1) * 16, o);
       tc::tmem_wait_ld();
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        stage[row * 32 + ((kh * 16 + group * 4 + j) ^ (row & 7))] =
+        stage[lane * 4 + (j ^ ((lane >> 1) & 3))] =
             make_float4(__uint_as_float(o[4 * j]) * inv, __uint_as_float(o[4 * j + 1]) * inv,
                         __uint_as_float(o[4 * j + 2]) * inv, __uint_as_float(o[4 * j + 3]) * inv);
-      soft_sync();
-      const int dim = (lane >> 4) * 256 + (turn >> 1) * 128 + ((lane >> 2) & 3) * 32 +
-                      (turn & 1) * 16 + (lane & 3) * 4;
+      __syncwarp();
+      float4 v[4];
 #pragma unroll
-      for (int r = warp - 4; r < 64; r += kSoft / 32)
-        if (r < live)
-          *reinterpret_cast<float4*>(a.part_o + (first_row + r) * kDv + dim) =
-              stage[r * 32 + (lane ^ (r & 7))];
-      soft_sync();                                 // the place, and after the last turn O, is free
+      for (int u = 0; u < 4; ++u) {
+        const int r = (lane >> 2) + 8 * u;
+        v[u] = stage[r * 4 + ((lane & 3) ^ ((r >> 1) & 3))];
+      }
+      float* const at = dst + (turn >> 1) * 128 + (turn & 1) * 16;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (8 * u < rows) *reinterpret_cast<float4*>(at + u * 8 * kDv) = v[u];
+      __syncwarp();
     }
+    soft_sync();                                   // P's place and O are free
     tc::fence_before_sync();
   }
 }
@@ -578,18 +585,21 @@ wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
 
   grid_dep_wait();
   grid_dep_launch();
-  long long* plan = reinterpret_cast<long long*>(smem + kOffPlan);
-  for (int i = threadIdx.x; i <= a.R; i += kThreads) plan[i] = a.plan[i];
-  if (blockIdx.x == 0) {       // lengths past their tables are cut off (prefix.h)
-    for (int i = threadIdx.x; i <= a.R; i += kThreads) {
-      const int len = i < a.R ? a.seq_lens[i] : *a.prefix_len;
-      const int pages = i < a.R ? a.max_pages : a.prefix_pages;
-      if (len > (long long)pages * kPage && a.status) atomicOr(a.status, MLA_FAULT_PAGE_RANGE);
+  int32_t* plan = reinterpret_cast<int32_t*>(smem + kOffPlan);
+  int32_t* lens = plan + kMaxR + 1;
+  bool cut = blockIdx.x == 0 && threadIdx.x == 0 && *a.prefix_len > (long long)a.prefix_pages * kPage;
+  for (int i = threadIdx.x; i <= a.R; i += kThreads) {
+    plan[i] = a.plan[i];
+    if (i < a.R) {
+      const int len = a.seq_lens[i];
+      lens[i] = wide_len(len, a.max_pages);
+      cut |= blockIdx.x == 0 && len > lens[i] && len > 0;
     }
   }
+  if (cut && a.status) atomicOr(a.status, MLA_FAULT_PAGE_RANGE);
   __syncthreads();
-  const WideWalk walk(a, plan, (int)(blockIdx.x >> 1));
-  if (walk.pos == walk.end) {
+  const WideWalk walk(a, plan, lens, (int)(blockIdx.x >> 1));
+  if (walk.pos >= walk.end) {
     // Nothing for this pair.
   } else if (warp == 0) {
     load_keys(a, walk, smem, ctl, rank, &tm_kv, &tm_kvr, &tm_q, &tm_qr);
