@@ -31,7 +31,7 @@ prefix_plan_kernel(const int32_t* __restrict__ seq_lens, int R, int max_pages, i
   grid_dep_launch();
   const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
   const int tiles = i < R ? (int)cdiv(wide_len(seq_lens[i], max_pages), kWideKeys) : 0;
-  int sum = tiles > 0 ? own_blocks * (tiles + 1) : 0;
+  int sum = tiles > 0 ? own_blocks * (tiles + kWideCost) : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int t = __shfl_up_sync(0xffffffffu, sum, o);
@@ -74,12 +74,12 @@ __global__ void __launch_bounds__(kWarps * 32) prefix_merge_kernel(const MergeAr
   };
   if (line.prefix_tiles > 0) {
     const int b = (int)(row / kWideRows);
-    n_pre = pieces(b * (line.prefix_tiles + 1), line.prefix_tiles, b, (int)(row % kWideRows), pre);
+    n_pre = pieces(b * (line.prefix_tiles + kWideCost), line.prefix_tiles, b, (int)(row % kWideRows), pre);
   }
   const int span = (own_next - own) / a.own_blocks;
-  if (span >= 2) {
+  if (span > kWideCost) {
     const int j = m / kWideRows;
-    n_own = pieces(line.prefix_places + own + j * span, span - 1,
+    n_own = pieces(line.prefix_places + own + j * span, span - kWideCost,
                    a.blocks + r * a.own_blocks + j, m % kWideRows, mine);
   }
   const int n = n_pre + n_own;
@@ -150,8 +150,8 @@ size_t wide_bytes(const mla_shape& s) { return wide_out_bytes(s) + align256(wide
 
 // Places on the line of work: 31 bits hold them.
 bool places_fit(const mla_shape& s, int prefix_pages) {
-  const long long own = (long long)s.R * wide_own_blocks(s) * (cdiv((long long)s.max_pages * kPage, kWideKeys) + 1);
-  return own + wide_blocks(s) * (cdiv((long long)prefix_pages * kPage, kWideKeys) + 1) < (1LL << 31) &&
+  const long long own = (long long)s.R * wide_own_blocks(s) * (cdiv((long long)s.max_pages * kPage, kWideKeys) + kWideCost);
+  return own + wide_blocks(s) * (cdiv((long long)prefix_pages * kPage, kWideKeys) + kWideCost) < (1LL << 31) &&
          wide_rows(s) < (1ull << 31);
 }
 

@@ -4,8 +4,9 @@
 // A segment is a block of up to 128 rows with the keys it attends to: block b of
 // all N rows with the prefix's keys (segments 0 .. blocks - 1), then block j of
 // request r's M rows with the request's own keys (segment blocks + r * own_blocks
-// + j). A segment of t > 0 tiles takes t + 1 places of one line of places, one per
-// tile and one for what a segment costs besides; segments without keys take none.
+// + j). A segment of t > 0 tiles takes t + kWideCost places of one line of places,
+// one per tile, the others for what a piece costs besides (Q, new maxima, 256 KB of
+// partial rows out); segments without keys take none.
 // The line is cut into equal parts, part u from floor(u * places / used), one per
 // pair of CTAs. The piece of segment s that part u holds has partial slot u + s:
 // along the line one of the two grows with every piece, so no two share a slot and
@@ -18,6 +19,10 @@ namespace mlafold {
 
 constexpr int kWideRows = 128;     // query rows per block
 constexpr int kWideKeys = 256;     // keys per tile
+// A piece costs about two tiles' time. Measured with 1, 2, 3, 4, 6: 24 x 1 x 64
+// behind 64k 177, 142, 137, 137, 140 us; 128 x 7 x 64 behind 16k 1412, 1338, 1335,
+// 1368, 1387 us; 64 x 7 x 8 behind 16k 120, 113, 115, 118, 124 us.
+constexpr int kWideCost = 3;
 
 struct WideArgs {
   const int32_t* prefix_table;     // [prefix_pages]
@@ -47,7 +52,7 @@ struct WideLine {
                                       int units) {
     prefix_len = wide_len(prefix_len_, prefix_pages);
     prefix_tiles = (int)cdiv(prefix_len, kWideKeys);
-    prefix_places = prefix_tiles > 0 ? blocks * (prefix_tiles + 1) : 0;
+    prefix_places = prefix_tiles > 0 ? blocks * (prefix_tiles + kWideCost) : 0;
     places = prefix_places + own_places;
     used = places < units ? places : units;
   }
@@ -92,8 +97,8 @@ struct WideWalk {
       int first, tiles, segment;                     // first: the segment's first place
       if (pos < prefix_places) {
         tiles = prefix_tiles;
-        segment = (int)((unsigned)pos / (unsigned)(tiles + 1));
-        first = segment * (tiles + 1);
+        segment = (int)((unsigned)pos / (unsigned)(tiles + kWideCost));
+        first = segment * (tiles + kWideCost);
         p.table = a.prefix_table;
         p.len = prefix_len;
         p.row0 = segment * kWideRows;
@@ -102,9 +107,9 @@ struct WideWalk {
         const int at = pos - prefix_places;
         while (r + 1 < a.R && plan[r + 1] <= at) ++r;
         const unsigned span = (unsigned)(plan[r + 1] - plan[r]) / (unsigned)a.own_blocks;
-        if ((int)span < 2) return false;             // not a plan of this shape
+        if ((int)span <= kWideCost) return false;    // not a plan of this shape
         const int j = (int)((unsigned)(at - plan[r]) / span);
-        tiles = (int)span - 1;
+        tiles = (int)span - kWideCost;
         segment = a.blocks + r * a.own_blocks + j;
         first = prefix_places + plan[r] + j * (int)span;
         p.table = a.block_table + (long long)r * a.max_pages;
@@ -113,8 +118,8 @@ struct WideWalk {
         p.row_end = (r + 1) * a.M;
       }
       const int last = first + tiles, stop = end < last ? end : last, from = pos;
-      pos = stop < last ? stop : last + 1;
-      if (from >= last) continue;                    // the place after the tiles
+      pos = stop < last ? stop : last + kWideCost;
+      if (from >= last) continue;                    // the places after the tiles
       p.tile = from - first;
       p.count = stop - from;
       p.slot = (unit + segment) * kWideRows;

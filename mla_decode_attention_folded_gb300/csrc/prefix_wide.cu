@@ -27,7 +27,7 @@
 // e4m3(p16), lo = e5m2(p16 - hi). E5M2's range keeps the second term where hi
 // is subnormal (p < 2^-6, absolute step 2^-9), so hi + lo is p to 2^-7 relative
 // down to 2^-13 of absolute error. The running max is lazy as in decode_tc.cu
-// (moved when a score exceeds it by more than 8, to 2 below the new one); P is
+// (moved when a weight exceeds 2^8, to 2 below the tile's); P is
 // computed as if no row moved and once more where one did.
 #include "decode_common.cuh"
 #include "internal.h"
@@ -67,6 +67,7 @@ struct WideCtl {
   uint64_t s_full[2];      // MMA -> softmax, TMA: S of a tile done
   uint64_t p_full[2];      // rank 0: softmax of both CTAs -> PV: P of CTA h's keys written
   uint64_t pv_half[2];     // MMA -> softmax, TMA: O holds CTA 0's keys of the tile
+  uint64_t pv_most[2];     // MMA -> TMA: and the first dim half of CTA 1's
   uint64_t pv_done[2];     // MMA -> softmax, TMA: O holds the tile; P and the stage are free
   uint64_t q_full;         // rank 0: TMA of both CTAs -> S
   uint64_t q_empty;        // MMA -> TMA
@@ -139,8 +140,8 @@ struct Pages {
 };
 
 // Own keys (and Q at each piece's start). A stage's bands 0-1 hold V of CTA 0's
-// keys, which PV is done with first, bands 2-3 that of CTA 1's: it is refilled in
-// two parts.
+// keys, which PV is done with first, bands 2 and 3 that of CTA 1's: it is refilled
+// in three parts, so that little is left to load once PV is done.
 __device__ void load_keys(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl* ctl,
                           uint32_t rank, const CUtensorMap* tm_kv, const CUtensorMap* tm_kvr,
                           const CUtensorMap* tm_q, const CUtensorMap* tm_qr) {
@@ -162,13 +163,20 @@ __device__ void load_keys(const WideArgs& a, WideWalk walk, uint8_t* smem, WideC
         const uint32_t bar = tc::map_rank(&ctl->k_full[st], 0);
         uint8_t* stage = smem + st * kStageBytes;
         if (i >= 2) ok = w_wait(&ctl->pv_half[st], ph, ctl, a.status);
+        auto band = [&](int c) {
+          for (int h = 0; h < 2; ++h)
+            if ((h ? p1 : p0) >= 0)
+              tc::tma_load_2d_pair(stage + c * kChunkBytes + h * (kChunkBytes / 2), tm_kv, bar,
+                                   c * 128, (h ? p1 : p0) * kPage);
+        };
         if (ok) {
           tc::remote_arrive_expect_tx(bar, ((p0 >= 0) + (p1 >= 0)) * dec::kPageBytes);
+          band(0);
+          band(1);
           for (int h = 0; h < 2; ++h)
-            for (int c = 0; c < 2; ++c)
-              if ((h ? p1 : p0) >= 0)
-                tc::tma_load_2d_pair(stage + c * kChunkBytes + h * (kChunkBytes / 2), tm_kv, bar,
-                                     c * 128, (h ? p1 : p0) * kPage);
+            if ((h ? p1 : p0) >= 0)
+              tc::tma_load_2d_pair(stage + 4 * kChunkBytes + h * (kRopeBytes / 2), tm_kvr, bar, 512,
+                                   (h ? p1 : p0) * kPage);
         }
         if (ok && t == 0) {
           if (x > 0) ok = w_wait(&ctl->q_empty, (x - 1) & 1, ctl, a.status);
@@ -181,18 +189,10 @@ __device__ void load_keys(const WideArgs& a, WideWalk walk, uint8_t* smem, WideC
             tc::tma_load_2d_pair(q + 4 * kQChunk, tm_qr, q_bar, 512, row);
           }
         }
+        if (ok && i >= 2) ok = w_wait(&ctl->pv_most[st], ph, ctl, a.status);
+        if (ok) band(2);
         if (ok && i >= 2) ok = w_wait(&ctl->pv_done[st], ph, ctl, a.status);
-        if (ok) {
-          for (int h = 0; h < 2; ++h) {
-            const int id = h ? p1 : p0;
-            if (id < 0) continue;
-            for (int c = 2; c < 4; ++c)
-              tc::tma_load_2d_pair(stage + c * kChunkBytes + h * (kChunkBytes / 2), tm_kv, bar,
-                                   c * 128, id * kPage);
-            tc::tma_load_2d_pair(stage + 4 * kChunkBytes + h * (kRopeBytes / 2), tm_kvr, bar, 512,
-                                 id * kPage);
-          }
-        }
+        if (ok) band(3);
       }
       ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
     }
@@ -306,7 +306,7 @@ __device__ void issue_pv(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCt
         tc::fence_after_sync();
         const uint32_t kv = s_kv + st * kStageBytes;
 #pragma unroll
-        for (int d = 0; d < 2; ++d)
+        for (int d = 0; d < 2; ++d) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             const uint64_t v = tc::smem_desc(kv + (kh * 2 + d) * kChunkBytes + kk * 32 * 128,
@@ -317,6 +317,8 @@ __device__ void issue_pv(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCt
             tc::mma_f8_pair(tmem + d * 128, tc::smem_desc(p + 2 * kPChunk, 16, 1024, tc::kSw128), v,
                             kIdescLo, true);
           }
+          if (kh == 1 && d == 0) tc::mma_commit_pair(&ctl->pv_most[st]);
+        }
         tc::mma_commit_pair(kh == 0 ? &ctl->pv_half[st] : &ctl->pv_done[st]);
       }
     }
@@ -325,9 +327,10 @@ __device__ void issue_pv(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCt
 }
 
 // ---------------------------------------------------------------- softmax
-__device__ __forceinline__ float at_most_9(float d) {      // NaN stays
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(d), "f"(9.f));
+// The larger of two FP16 pairs, lane by lane; a NaN loses.
+__device__ __forceinline__ uint32_t f16x2_max(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 __device__ __forceinline__ uint16_t f16x2_to_e5m2x2(uint32_t h) {
@@ -335,30 +338,28 @@ __device__ __forceinline__ uint16_t f16x2_to_e5m2x2(uint32_t h) {
   asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
   return r;
 }
-// P of 32 keys of a row from their scores: the codes of both terms, the sum, and
-// the largest score above the row's max. More than 9 above it counts as 9: such
-// a tile is done again.
-__device__ __forceinline__ void weigh(const uint32_t (&raw)[32], float scale, float neg_max,
-                                      float& most, float& sum, uint32_t (&hi)[8],
-                                      uint32_t (&lo)[8]) {
+// P of 32 keys of a row from their scores: the codes of both terms and the sum.
+// Returns whether a weight exceeds 2^8 (as FP16): the tile is then done again.
+__device__ __forceinline__ bool weigh(const uint32_t (&raw)[32], float scale, float neg_max,
+                                      float& sum, uint32_t (&hi)[8], uint32_t (&lo)[8]) {
   const uint64_t scale2 = pack_f32x2(scale, scale), neg2 = pack_f32x2(neg_max, neg_max);
   uint64_t sums[2] = {0, 0};
-  most = -INFINITY;
+  uint32_t most = 0;
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
     uint64_t d01 = pack_f32x2(__uint_as_float(raw[i]), __uint_as_float(raw[i + 1]));
     uint64_t d23 = pack_f32x2(__uint_as_float(raw[i + 2]), __uint_as_float(raw[i + 3]));
     d01 = fma_f32x2(d01, scale2, neg2);
     d23 = fma_f32x2(d23, scale2, neg2);
-    float d[4], p[4];
-    unpack_f32x2(d01, d[0], d[1]);
-    unpack_f32x2(d23, d[2], d[3]);
-    most = fmaxf(most, fmaxf(fmaxf(d[0], d[1]), fmaxf(d[2], d[3])));
+    float p[4];
+    unpack_f32x2(d01, p[0], p[1]);
+    unpack_f32x2(d23, p[2], p[3]);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) p[u] = ex2(at_most_9(d[u]));
+    for (int u = 0; u < 4; ++u) p[u] = ex2(p[u]);
     sums[0] = add_f32x2(sums[0], pack_f32x2(p[0], p[1]));
     sums[1] = add_f32x2(sums[1], pack_f32x2(p[2], p[3]));
     const uint32_t h01 = dec::f32x2_to_f16x2(p[0], p[1]), h23 = dec::f32x2_to_f16x2(p[2], p[3]);
+    most = f16x2_max(most, f16x2_max(h01, h23));
     const uint16_t e01 = dec::f16x2_to_e4m3x2(h01), e23 = dec::f16x2_to_e4m3x2(h23);
     const uint16_t l01 = f16x2_to_e5m2x2(dec::f16x2_sub(h01, e4m3x2_to_f16x2(e01)));
     const uint16_t l23 = f16x2_to_e5m2x2(dec::f16x2_sub(h23, e4m3x2_to_f16x2(e23)));
@@ -368,6 +369,8 @@ __device__ __forceinline__ void weigh(const uint32_t (&raw)[32], float scale, fl
   float a, b;
   unpack_f32x2(add_f32x2(sums[0], sums[1]), a, b);
   sum = a + b;
+  constexpr uint32_t k256 = 0x5c00;                // 2^8; weights are >= 0: bits compare as values
+  return (most & 0xffff) > k256 || (most >> 16) > k256;
 }
 
 // Thread (row, 32 keys): TMEM lane l holds row l % 64, keys of CTA l / 64; the
@@ -421,11 +424,11 @@ __device__ void softmax(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl
         for (int i = 0; i < 32; ++i)
           if (i >= left) raw[i] = 0xff800000u;     // -inf
       }
-      float most, sum;
+      float sum;
       bool moved = t == 0;
       if (t > 0) {
-        weigh(raw, a.bmm1_log2, -m, most, sum, hi, lo);
-        if (soft_any(most > 8.f || !ok)) {
+        const bool over = weigh(raw, a.bmm1_log2, -m, sum, hi, lo);
+        if (soft_any(over || !ok)) {
           if (soft_any(!ok)) return;               // all of them
           moved = true;
         }
@@ -458,7 +461,7 @@ __device__ void softmax(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl
           tc::fence_before_sync();
         }
         soft_sync();                               // O is scaled before any P of this CTA counts
-        weigh(raw, a.bmm1_log2, m == -INFINITY ? 0.f : -m, most, sum, hi, lo);
+        weigh(raw, a.bmm1_log2, m == -INFINITY ? 0.f : -m, sum, hi, lo);
       }
       l += sum;
       // P of these keys is free once PV of the previous tile is done with it.
@@ -559,6 +562,7 @@ wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
       tc::mbar_init(&ctl->s_full[b], 1);
       tc::mbar_init(&ctl->p_full[b], 2 * kSoft / 64);   // the warps of one key half, both CTAs
       tc::mbar_init(&ctl->pv_half[b], 1);
+      tc::mbar_init(&ctl->pv_most[b], 1);
       tc::mbar_init(&ctl->pv_done[b], 1);
       tc::mbar_init(&ctl->drain[b], 1);
     }
