@@ -18,7 +18,8 @@
 // jobs: warp 0 loads by TMA (Q of a job into a ring of two, W bands into a ring
 // of four), warp 1 issues the MMAs into four TMEM accumulators, warps 2-9 turn
 // the rope dims while the first band is on its way, then read the accumulators
-// back and store each band by TMA from a ring of two staging tiles.
+// back and store it by TMA, each warp its 32 tokens x 64 dims on its own, from two
+// staging tiles.
 #include <cmath>
 
 #include "decode_common.cuh"
@@ -37,12 +38,12 @@ constexpr int kWStages = 4, kQStages = 2, kOutStages = 2, kAccs = 4;
 constexpr int kChunk = 128 * 128;               // 128 rows of 128 bytes
 constexpr int kQBytes = 2 * kChunk;             // 128 tokens x 128 BF16, two 64-dim chunks
 constexpr int kWBytes = 2 * kChunk;             // 128 nope rows x 128 BF16, two 64-latent chunks
-constexpr int kOutBytes = kTok * kBand;         // 128 tokens x 128 codes
+constexpr int kOutBytes = 32 * 64;              // of a read-back warp: 32 tokens x 64 codes
 constexpr int kOffW = 0;
 constexpr int kOffQ = kOffW + kWStages * kWBytes;
 constexpr int kOffOut = kOffQ + kQStages * kQBytes;
-constexpr int kOffCtl = kOffOut + kOutStages * kOutBytes;
 constexpr int kEpi = 256;                       // read-back threads
+constexpr int kOffCtl = kOffOut + kEpi / 32 * kOutStages * kOutBytes;
 constexpr int kThreads = 64 + kEpi;
 constexpr uint32_t kTmemCols = kAccs * kBand;   // 512
 // BF16 x BF16 -> FP32, A (queries) K-major, B (W_UK) MN-major.
@@ -86,19 +87,6 @@ __device__ __forceinline__ bool ab_wait(uint64_t* bar, uint32_t parity, AbsorbCt
     }
   }
 }
-// Barrier of the read-back threads that also tells whether any of them gave up
-// a wait: they then all leave together.
-__device__ __forceinline__ bool epi_all(bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
-      " bar.red.and.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
-      : "=r"(r)
-      : "r"((uint32_t)ok), "n"(kEpi)
-      : "memory");
-  return r != 0;
-}
-
 // The 64 rope dims of the 128 tokens of a job: two threads per token, 16
 // planes each, straight from and to global memory.
 __device__ __forceinline__ void turn_rope(const AbsorbArgs& a, int h, int tok0, int gt) {
@@ -301,7 +289,6 @@ absorb_kernel(const AbsorbArgs a, const __grid_constant__ CUtensorMap tm_q,
     grid_dep_wait();
     const int gt = threadIdx.x - 64;
     const int quarter = warp & 3, half = (warp - 2) >> 2;
-    const int row = quarter * 32 + lane;           // token of the tile = TMEM lane
     uint32_t u = 0;
     bool ok = true;
     for (int job = blockIdx.x; ok && job < a.jobs; job += gridDim.x) {
@@ -309,9 +296,8 @@ absorb_kernel(const AbsorbArgs a, const __grid_constant__ CUtensorMap tm_q,
       if (band_of(job) == 0) turn_rope(a, h, tok0, gt);
       for (int b = 0; ok && b < per; ++b, ++u) {
         const int ds = u % kAccs;
-        // The staging tile is free once the store of two units back has read it.
-        if (gt == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        if (!(ok = epi_all(ab_wait(&ctl->d_full[ds], (u / kAccs) & 1, ctl, a.status)))) break;
+        ok = __all_sync(0xffffffffu, ab_wait(&ctl->d_full[ds], (u / kAccs) & 1, ctl, a.status));
+        if (!ok) break;
         tc::fence_after_sync();
         uint32_t raw[2][32];
         const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + ds * kBand + half * 64;
@@ -320,8 +306,11 @@ absorb_kernel(const AbsorbArgs a, const __grid_constant__ CUtensorMap tm_q,
         tc::tmem_wait_ld();
         tc::fence_before_sync();
         tc::mbar_arrive(&ctl->d_empty[ds]);
-        uint8_t* stage = smem + kOffOut + (u % kOutStages) * kOutBytes;
-        uint4* dst = reinterpret_cast<uint4*>(stage + row * 128);
+        // The warp's staging tile is free once its store of two units back has read it.
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        __syncwarp();
+        uint8_t* stage = smem + kOffOut + ((warp - 2) * kOutStages + u % kOutStages) * kOutBytes;
+        uint4* dst = reinterpret_cast<uint4*>(stage + lane * 64);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint32_t w[4];
@@ -333,18 +322,18 @@ absorb_kernel(const AbsorbArgs a, const __grid_constant__ CUtensorMap tm_q,
                                    __uint_as_float(f[2]) * a.inv_scale,
                                    __uint_as_float(f[3]) * a.inv_scale);
           }
-          // 128-byte swizzle: 16-byte piece p of row r at piece p ^ (r & 7).
-          dst[(half * 4 + j) ^ (row & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
+          // 64-byte swizzle: 16-byte piece p of row r at piece p ^ ((r >> 1) & 3).
+          dst[j ^ ((lane >> 1) & 3)] = make_uint4(w[0], w[1], w[2], w[3]);
         }
         tc::fence_proxy_async_smem();
-        ok = epi_all(true);
-        if (gt == 0) {
-          tc::tma_store_3d(&tm_o, stage, (band_of(job) + b) * kBand, h, tok0);
-          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        }
+        __syncwarp();
+        const int tok = tok0 + quarter * 32;
+        if (lane == 0 && tok < a.T)
+          tc::tma_store_3d(&tm_o, stage, (band_of(job) + b) * kBand + half * 64, h, tok);
+        if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       }
     }
-    if (gt == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -388,10 +377,10 @@ extern "C" int32_t mla_query_absorb(const mla_query_shape* s, const void* q, con
   const cuuint64_t w_str[1] = {kDv * 2};
   const cuuint64_t o_dims[3] = {kDqk, (cuuint64_t)s->H, (cuuint64_t)T};
   const cuuint64_t o_str[2] = {kDqk, (cuuint64_t)s->H * kDqk};
-  const cuuint32_t box3[3] = {128, 1, kTok}, box2[2] = {128, kNope};
+  const cuuint32_t box3[3] = {128, 1, kTok}, box2[2] = {128, kNope}, box_o[3] = {64, 1, 32};
   if (!dec::encode(&tq, q, 3, q_dims, q_str, box3, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !dec::encode(&tw, w_uk, 2, w_dims, w_str, box2, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !dec::encode(&to, out, 3, o_dims, o_str, box3, CU_TENSOR_MAP_SWIZZLE_128B))
+      !dec::encode(&to, out, 3, o_dims, o_str, box_o, CU_TENSOR_MAP_SWIZZLE_64B))
     return MLA_ERR_CUDA;
   static bool attr_set[64] = {};
   if (dec::set_smem(absorb_kernel, kSmemBytes, attr_set) != cudaSuccess) return MLA_ERR_CUDA;
