@@ -16,10 +16,9 @@
 // that bound); 128 latent dims (one band) are its N, read MN-major from W_UK's
 // latent-contiguous rows. Persistent CTAs walk (head, 128 tokens, band set)
 // jobs: warp 0 loads by TMA (Q of a job into a ring of two, W bands into a ring
-// of four), warp 1 issues the MMAs into four TMEM accumulators, warps 2-9 turn
-// the rope dims while the first band is on its way, then read the accumulators
-// back and store it by TMA, each warp its 32 tokens x 64 dims on its own, from two
-// staging tiles.
+// of four), warp 1 issues the MMAs into four TMEM accumulators, warps 2-9 read them
+// back and store them by TMA, each warp its 32 tokens x 64 dims on its own, from
+// two staging tiles, and warps 10-17 turn the rope dims beside them.
 #include <cmath>
 
 #include "decode_common.cuh"
@@ -44,7 +43,8 @@ constexpr int kOffQ = kOffW + kWStages * kWBytes;
 constexpr int kOffOut = kOffQ + kQStages * kQBytes;
 constexpr int kEpi = 256;                       // read-back threads
 constexpr int kOffCtl = kOffOut + kEpi / 32 * kOutStages * kOutBytes;
-constexpr int kThreads = 64 + kEpi;
+constexpr int kTurn = 256;                      // rope threads: two per token
+constexpr int kThreads = 64 + kEpi + kTurn;
 constexpr uint32_t kTmemCols = kAccs * kBand;   // 512
 // BF16 x BF16 -> FP32, A (queries) K-major, B (W_UK) MN-major.
 constexpr uint32_t kIdesc = tc::idesc_bf16_f32(kTok, kBand) | (1u << 16);
@@ -285,15 +285,17 @@ absorb_kernel(const AbsorbArgs a, const __grid_constant__ CUtensorMap tm_q,
       while (!tc::mbar_try_wait(&ctl->drain, 0) && tc::globaltimer_ns() - t0 < kTimeoutNs) {
       }
     }
+  } else if (warp >= 2 + kEpi / 32) {
+    grid_dep_wait();
+    for (int job = blockIdx.x; job < a.jobs; job += gridDim.x)
+      if (band_of(job) == 0) turn_rope(a, head_of(job), tok_of(job), threadIdx.x - 64 - kEpi);
   } else {
     grid_dep_wait();
-    const int gt = threadIdx.x - 64;
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     uint32_t u = 0;
     bool ok = true;
     for (int job = blockIdx.x; ok && job < a.jobs; job += gridDim.x) {
       const int h = head_of(job), tok0 = tok_of(job);
-      if (band_of(job) == 0) turn_rope(a, h, tok0, gt);
       for (int b = 0; ok && b < per; ++b, ++u) {
         const int ds = u % kAccs;
         ok = __all_sync(0xffffffffu, ab_wait(&ctl->d_full[ds], (u / kAccs) & 1, ctl, a.status));

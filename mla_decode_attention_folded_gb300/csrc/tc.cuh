@@ -254,14 +254,8 @@ __device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
-__device__ __forceinline__ void remote_st(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ void fence_cluster() {
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
-}
 // Arrival on a barrier of the cluster. It orders this CTA's own shared memory
-// (CTA-scope release); data for another CTA's memory goes by remote_st_async.
+// (CTA-scope release), which is all that the pair's MMAs read here.
 __device__ __forceinline__ void remote_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -278,24 +272,6 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y)
-      : "memory");
-}
-// Stores into the memory of the CTA that also holds `bar`; the bytes count there
-// once they have landed.
-__device__ __forceinline__ void remote_st_async(uint32_t addr, uint32_t v, uint32_t bar) {
-  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(
-                   addr),
-               "r"(v), "r"(bar)
-               : "memory");
-}
-// `bytes` (a multiple of 16) of this CTA's shared memory into that of the CTA
-// that also holds `bar`; the bytes count there once they have landed.
-__device__ __forceinline__ void bulk_copy_to(uint32_t dst, const void* src, uint32_t bytes,
-                                             uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst),
-      "r"(smem_u32(src)), "r"(bytes), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {

@@ -95,3 +95,51 @@ def test_absorb_by_the_library(change, code):
     with pytest.raises(mla.MlaError) as e:
         _absorb(**change())
     assert e.value.code == code
+
+
+def _prefix(**change):
+    eng = mla.PrefixMla(2, 2, 3, 2, 4, 8, "cuda")
+    a = dict(q=torch.zeros(4, 3, 576, dtype=torch.uint8, device="cuda"),
+             kv=torch.zeros(8, 64, 576, dtype=torch.uint8, device="cuda"),
+             prefix_table=_i32(0, 1, 2, 3), prefix_len=_i32(5),
+             block_table=_i32(4, 5, 6, 7).view(2, 2), seq_lens=_i32(3, 9), bmm1_scale=1.0,
+             bmm2_scale=1.0)
+    a.update(change)
+    eng.plan(_i32(3, 9))
+    return eng.decode(**a)
+
+
+def test_prefix_accepts():
+    out, lse = _prefix()
+    assert out.shape == (2, 6, 512) and lse.shape == (2, 6)
+    assert _prefix(return_lse=False)[1] is None
+
+
+@pytest.mark.parametrize("change", [
+    lambda: dict(q=torch.zeros(4, 3, 576, device="cuda")),
+    lambda: dict(q=torch.zeros(4, 4, 576, dtype=torch.uint8, device="cuda")),
+    lambda: dict(kv=torch.zeros(7, 64, 576, dtype=torch.uint8, device="cuda")),
+    lambda: dict(kv=torch.zeros(8, 64, 576, dtype=torch.uint8)),
+    lambda: dict(prefix_table=_i32(0, 1, 2)),
+    lambda: dict(prefix_table=_i32(0, 1, 2, 3).long()),
+    lambda: dict(prefix_len=5),
+    lambda: dict(prefix_len=_i32(5, 5)),
+    lambda: dict(block_table=_i32(4, 5, 6, 7).view(2, 2).t()),
+    lambda: dict(seq_lens=_i32(3)),
+    lambda: dict(out=torch.zeros(2, 6, 512, device="cuda")),
+    lambda: dict(out=torch.zeros(4, 3, 512, dtype=torch.bfloat16, device="cuda")),
+    lambda: dict(lse=torch.zeros(2, 6, dtype=torch.bfloat16, device="cuda")),
+])
+def test_prefix(change):
+    with pytest.raises(ValueError):
+        _prefix(**change())
+
+
+def test_prefix_by_the_library():
+    with pytest.raises(mla.MlaError) as e:
+        _prefix(bmm1_scale=0.0)
+    assert e.value.code == -2
+    with pytest.raises(ValueError):
+        mla.PrefixMla(2, 2, 3, 2, 4, 8, "cuda").plan(torch.zeros(2, dtype=torch.int64, device="cuda"))
+    with pytest.raises(mla.MlaError):
+        mla.PrefixMla(2000, 2, 3, 2, 4, 8, "cuda")

@@ -112,6 +112,94 @@ def test_scores_far_apart():
         _check(*_decode(b, table, n), b, table, n, big)
 
 
+@pytest.mark.parametrize("k,H", [(4, 8), (1, 64), (7, 33)])
+def test_scores_that_grow_from_tile_to_tile(k, H):
+    """Every few pages the keys double: the running max moves in the middle of a
+    piece, again and again, and the sums follow."""
+    b, table, n = prefix_batch((700, 0, 1500), k, H, 3000, seed=21 + H)
+    kv = b.kv.view(torch.float8_e4m3fn).float() / 64
+    for row in [table] + list(b.block_table):
+        for i, page in enumerate(row.tolist()):
+            kv[page] = kv[page] * 2.0 ** min(6, i // 7)
+    b.kv = kv.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    for ctas in (None, 2, 7):
+        _check(*_decode(b, table, n, num_ctas=ctas), b, table, n, f"{ctas} CTAs")
+
+
+def test_a_row_of_nan_stays_alone():
+    b, table, n = prefix_batch((100, 300), 4, 8, 600, seed=22)
+    clean = b.q.clone()
+    b.q[2, 3] = 0x7F
+    out, lse = _decode(b, table, n)
+    bad = 2 * 8 + 3                              # row of request 0
+    assert out[0, bad].isnan().all() and not lse[0, bad].isfinite()
+    b.q = clean
+    good = torch.ones(b.R, b.M, dtype=torch.bool)
+    good[0, bad] = False
+    again, lse2 = _decode(b, table, n)
+    assert torch.equal(out.cpu()[good], again.cpu()[good]) and torch.equal(lse.cpu()[good], lse2.cpu()[good])
+
+
+def test_pages_past_2_31_bytes_of_cache():
+    b, table, n = prefix_batch((100, 300), 4, 8, 600, seed=23)
+    used, far = b.kv.shape[0], (1 << 31) // (64 * 576) + 7
+    d = to_device(b)
+    kv = torch.empty((far + used, 64, 576), dtype=torch.uint8, device="cuda")
+    kv[far:] = d["kv"]
+    bmm1, bmm2 = bmm_scales(b)
+    eng = mla.PrefixMla(b.R, b.k, b.H, d["bt"].shape[1], table.numel(), far + used, "cuda")
+    eng.plan(d["lens"])
+    plen = torch.tensor([n], dtype=torch.int32, device="cuda")
+    out, lse = eng.decode(d["q"], kv, table.cuda() + far, plen, d["bt"] + far, d["lens"], bmm1, bmm2)
+    assert int(eng.status.item()) == 0
+    _check(out, lse, b, table, n)
+
+
+def test_two_batches_on_two_streams():
+    """Two engines, each on its own stream, many times over: neither disturbs the other."""
+    jobs = []
+    for seed, (lens, prefix) in enumerate((((100, 700, 0), 900), ((64, 5), 2500))):
+        b, table, n = prefix_batch(lens, 4, 8, prefix, seed=24 + seed)
+        d = to_device(b)
+        eng = mla.PrefixMla(b.R, b.k, b.H, d["bt"].shape[1], table.numel(), d["kv"].shape[0], "cuda")
+        jobs.append((b, table, n, d, eng, table.cuda(), torch.tensor([n], dtype=torch.int32).cuda(),
+                     torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    results = []
+    for _ in range(20):
+        results = []
+        for b, table, n, d, eng, pt, plen, stream in jobs:
+            bmm1, bmm2 = bmm_scales(b)
+            eng.plan(d["lens"], stream)
+            results.append(eng.decode(d["q"], d["kv"], pt, plen, d["bt"], d["lens"], bmm1, bmm2,
+                                      stream=stream))
+    torch.cuda.synchronize()
+    for (b, table, n, _, eng, *_), (out, lse) in zip(jobs, results):
+        assert int(eng.status.item()) == 0
+        _check(out, lse, b, table, n)
+
+
+def test_many_short_requests():
+    """More segments than parts, pieces of one tile, requests without keys between."""
+    rng = np.random.default_rng(3)
+    lens = [int(v) if rng.random() < 0.7 else 0 for v in rng.integers(1, 70, 300)]
+    b, table, n = prefix_batch(lens, 1, 8, 100, seed=26)
+    _check(*_decode(b, table, n), b, table, n)
+
+
+def test_a_plan_of_other_lengths_stays_in_bounds():
+    """Keys beyond the plan are not attended to, planned keys that are gone are masked."""
+    b, table, n = prefix_batch((300, 40, 0), 4, 8, 200, seed=27)
+    d = to_device(b)
+    bmm1, bmm2 = bmm_scales(b)
+    eng = mla.PrefixMla(b.R, b.k, b.H, d["bt"].shape[1], table.numel(), d["kv"].shape[0], "cuda")
+    eng.plan(torch.tensor([320, 320, 320], dtype=torch.int32, device="cuda"))
+    plen = torch.tensor([n], dtype=torch.int32, device="cuda")
+    out, lse = eng.decode(d["q"], d["kv"], table.cuda(), plen, d["bt"], d["lens"], bmm1, bmm2)
+    assert int(eng.status.item()) == 0
+    _check(out, lse, b, table, n)
+
+
 def test_garbage_behind_the_last_keys_is_not_read():
     """NaN codes in the unused slots of the last pages, prefix and own."""
     b, table, n = prefix_batch((100, 37, 1), 4, 8, 333, seed=12)

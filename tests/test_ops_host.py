@@ -89,6 +89,67 @@ def test_absorb_scales_refused(scale):
     assert _absorb(scale=scale) == SHAPE
 
 
+def _shape(**fields):
+    s = mla.make_shape(4, 2, 8, 10, 100, 152)
+    for name, value in fields.items():
+        setattr(s, name, value)
+    return s
+
+
+def _prefix(shape=None, *, ptr=None, pages=3, bmm1=1.0, bmm2=1.0, plan_len=5, ws=1 << 40):
+    s = shape or _shape()
+    at = dict(q=P, kv=P, ptable=P, plen=P, table=P, lens=P, plan=P, ws=P, out=P, lse=None, status=None)
+    at.update(ptr or {})
+    return _lib.load().mla_prefix_decode(
+        ctypes.byref(s), pages, at["q"], at["kv"], at["ptable"], at["plen"], at["table"], at["lens"],
+        bmm1, bmm2, at["plan"], plan_len, at["ws"], ws, at["out"], at["lse"], at["status"], None)
+
+
+@pytest.mark.parametrize("fields,code", [
+    (dict(page_size=32), UNSUPPORTED), (dict(R=0), SHAPE), (dict(R=1025), SHAPE), (dict(H=5000), SHAPE),
+    (dict(groups=2), SHAPE), (dict(max_pages=0), SHAPE), (dict(num_pages=1 << 25), SHAPE),
+    (dict(num_ctas=0), SHAPE), (dict(R=1024, H=2048, max_pages=1 << 24), SHAPE)])
+def test_prefix_shapes_refused(fields, code):
+    assert _prefix(_shape(**fields)) == code
+    lib, s = _lib.load(), _shape(**fields)
+    size = ctypes.c_size_t(0)
+    assert lib.mla_prefix_workspace_bytes(ctypes.byref(s), ctypes.byref(size)) == code
+    assert lib.mla_prefix_plan(ctypes.byref(s), P, P, 2000, None) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(pages=0), SHAPE), (dict(pages=(1 << 24) + 1), SHAPE), (dict(bmm1=0.0), SHAPE),
+    (dict(bmm1=float("nan")), SHAPE), (dict(bmm2=float("inf")), SHAPE), (dict(plan_len=4), -4),
+    (dict(ws=1000), -3)])
+def test_prefix_arguments_refused(kw, code):
+    assert _prefix(**kw) == code
+
+
+@pytest.mark.parametrize("name", ["q", "kv", "ptable", "plen", "table", "lens", "plan", "ws", "out"])
+def test_prefix_pointers_refused(name):
+    assert _prefix(ptr={name: None}) == NULL
+    assert _prefix(ptr={name: ctypes.c_void_p((1 << 20) + 2)}) == ALIGN
+
+
+def test_prefix_plan_arguments_refused():
+    lib, s = _lib.load(), _shape()
+    assert lib.mla_prefix_plan(ctypes.byref(s), None, P, 5, None) == NULL
+    assert lib.mla_prefix_plan(ctypes.byref(s), P, None, 5, None) == NULL
+    assert lib.mla_prefix_plan(ctypes.byref(s), P, P, 4, None) == -4
+    assert lib.mla_prefix_plan(ctypes.byref(s), P, ctypes.c_void_p((1 << 20) + 2), 5, None) == ALIGN
+    assert lib.mla_prefix_workspace_bytes(ctypes.byref(s), None) == NULL
+
+
+@pytest.mark.parametrize("R,k,H,ctas", [(1, 1, 1, 1), (4, 2, 8, 152), (64, 7, 8, 152), (128, 7, 64, 152)])
+def test_prefix_workspace(R, k, H, ctas):
+    """One slot of 128 rows for every pair and segment but one: FP32 rows, then LSEs."""
+    N, M = R * k * H, k * H
+    slots = max(1, ctas // 2) + -(-N // 128) + R * -(-M // 128) - 1
+    align = lambda x: (x + 255) // 256 * 256  # noqa: E731
+    want = align(slots * 128 * 512 * 4) + align(slots * 128 * 4)
+    assert mla.prefix_workspace_bytes(mla.make_shape(R, k, H, 10, 100, ctas)) == want
+
+
 def test_binding_refuses_cpu_tensors():
     x = torch.zeros(2, 576, dtype=torch.bfloat16)
     kv = torch.zeros(1, 64, 576, dtype=torch.uint8)
