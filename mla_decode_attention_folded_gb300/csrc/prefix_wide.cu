@@ -61,7 +61,8 @@ constexpr uint32_t kIdescLo = kIdescHi | (1u << 7);       // A in E5M2
 static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms need 1 KB alignment");
 
 struct WideCtl {
-  uint64_t k_full[2];      // rank 0: TMA of both CTAs -> S: both CTAs' keys landed
+  uint64_t k_full[2];      // rank 0: TMA of both CTAs -> S: both CTAs' keys landed, but for
+  uint64_t k_last[2];      // band 3, which has its own
   uint64_t v_full[2];      // rank 0: TMA of both CTAs -> PV: V complete in both
   uint64_t v_tail[2];      // TMA -> softmax, TMA warp: V of a block's last tile landed here
   uint64_t s_full[2];      // MMA -> softmax, TMA: S of a tile done
@@ -161,16 +162,19 @@ __device__ void load_keys(const WideArgs& a, WideWalk walk, uint8_t* smem, WideC
       const int p1 = __shfl_sync(0xffffffffu, cur, 2 * rank + 1);
       if (lane == 0) {
         const uint32_t bar = tc::map_rank(&ctl->k_full[st], 0);
+        const uint32_t last = tc::map_rank(&ctl->k_last[st], 0);
+        const uint32_t live = (p0 >= 0) + (p1 >= 0);
         uint8_t* stage = smem + st * kStageBytes;
         if (i >= 2) ok = w_wait(&ctl->pv_half[st], ph, ctl, a.status);
         auto band = [&](int c) {
           for (int h = 0; h < 2; ++h)
             if ((h ? p1 : p0) >= 0)
-              tc::tma_load_2d_pair(stage + c * kChunkBytes + h * (kChunkBytes / 2), tm_kv, bar,
-                                   c * 128, (h ? p1 : p0) * kPage);
+              tc::tma_load_2d_pair(stage + c * kChunkBytes + h * (kChunkBytes / 2), tm_kv,
+                                   c == 3 ? last : bar, c * 128, (h ? p1 : p0) * kPage);
         };
         if (ok) {
-          tc::remote_arrive_expect_tx(bar, ((p0 >= 0) + (p1 >= 0)) * dec::kPageBytes);
+          tc::remote_arrive_expect_tx(bar, live * (kPage * (kDqk - 128)));
+          tc::remote_arrive_expect_tx(last, live * (kPage * 128));
           band(0);
           band(1);
           for (int h = 0; h < 2; ++h)
@@ -265,23 +269,30 @@ __device__ void issue_s(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl
     ++x;
     for (int t = 0; t < piece.count; ++t, ++i) {
       const int st = i & 1;
-      // The S buffer of tile i - 2 is free: its stage was refilled after its PV,
-      // whose P the softmax wrote after it had read that S.
+      // The S buffer of tile i - 2 is free: band 2 was refilled after PV had begun on
+      // CTA 1's keys (pv_most), whose P the softmax wrote after it had read that S.
+      // Band 3 comes last, when that PV is done; the other bands' MMAs cover its flight.
       if (!(ok = w_wait(&ctl->k_full[st], (i >> 1) & 1, ctl, a.status))) break;
       tc::fence_after_sync();
       const uint32_t kv = s_kv + st * kStageBytes, d = tmem + kSCol + st * 128;
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
+      auto band = [&](int c) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           tc::mma_f8_pair(d, tc::smem_desc(s_q + c * kQChunk + kk * 32, 16, 1024, tc::kSw128),
-                          tc::smem_desc(kv + c * kChunkBytes + kk * 32, 16, 1024, tc::kSw128), kIdescS,
-                          (c | kk) != 0);
+                          tc::smem_desc(kv + c * kChunkBytes + kk * 32, 16, 1024, tc::kSw128),
+                          kIdescS, (c | kk) != 0);
+      };
+      band(0);
+      band(1);
+      band(2);
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk)
         tc::mma_f8_pair(d, tc::smem_desc(s_q + 4 * kQChunk + kk * 32, 16, 512, tc::kSw64),
                         tc::smem_desc(kv + 4 * kChunkBytes + kk * 32, 16, 512, tc::kSw64), kIdescS,
                         true);
+      if (!(ok = w_wait(&ctl->k_last[st], (i >> 1) & 1, ctl, a.status))) break;
+      tc::fence_after_sync();
+      band(3);
       tc::mma_commit_pair(&ctl->s_full[st]);
     }
     if (ok) tc::mma_commit_pair(&ctl->q_empty);
@@ -557,6 +568,7 @@ wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&ctl->k_full[b], 2);
+      tc::mbar_init(&ctl->k_last[b], 2);
       tc::mbar_init(&ctl->v_full[b], 2);
       tc::mbar_init(&ctl->v_tail[b], 1);
       tc::mbar_init(&ctl->s_full[b], 1);
@@ -566,7 +578,7 @@ wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
       tc::mbar_init(&ctl->pv_done[b], 1);
       tc::mbar_init(&ctl->drain[b], 1);
     }
-        tc::mbar_init(&ctl->q_full, 2);
+    tc::mbar_init(&ctl->q_full, 2);
     tc::mbar_init(&ctl->q_empty, 1);
     ctl->abort_flag = 0;
     tc::fence_barrier_init();
