@@ -413,8 +413,6 @@ typedef struct {
  *   q            [R*k, H, 192] BF16 with the shape's strides, device, 16-byte
  *                aligned: 128 nope dims, then 64 rope dims.
  *   w_uk         [H, 128, 512] BF16, device, 16-byte aligned, latent-contiguous.
- *                May be read before the preceding call of this library on the
- *                stream has finished: none of them writes it.
  *   rope         the rope table, device, 16-byte aligned.
  *   rope_starts  [R] int32, device; negative: a padding request (rope dims 0).
  *   q_scale      finite, > 0, with a finite reciprocal.

@@ -213,12 +213,6 @@ absorb_kernel(const AbsorbArgs a, const __grid_constant__ CUtensorMap tm_q,
         tc::tma_load_2d(w, &tm_w, bar, xb, y);
         tc::tma_load_2d(w + kChunk, &tm_w, bar, xb + 128, y);
       };
-      // The first job's weights before the wait for the upstream kernel: none
-      // of the library's kernels writes them, and each lets its successor
-      // start only after its own wait, so what wrote them has finished.
-      uint32_t early = 0;
-      if ((int)blockIdx.x < a.jobs)
-        for (; early < (uint32_t)per; ++early) load_w(blockIdx.x, early, early);
       grid_dep_wait();
       grid_dep_launch();
       for (int job = blockIdx.x; ok && job < a.jobs; job += gridDim.x, ++x) {
@@ -232,7 +226,6 @@ absorb_kernel(const AbsorbArgs a, const __grid_constant__ CUtensorMap tm_q,
         tc::tma_load_3d(q + kChunk, &tm_q, &ctl->q_full[qs], 128, head_of(job), tok_of(job));
         uq = x + 1;
         for (int b = 0; b < per; ++b, ++u) {
-          if (u < early) continue;
           if (u >= kWStages &&
               !(ok = ab_wait(&ctl->w_empty[u % kWStages], (u / kWStages - 1) & 1, ctl, a.status)))
             break;
@@ -240,7 +233,6 @@ absorb_kernel(const AbsorbArgs a, const __grid_constant__ CUtensorMap tm_q,
         }
       }
       if (!ok) {                                   // never leave with copies in flight
-        if (u < early) u = early;
         const unsigned long long t0 = tc::globaltimer_ns();
         for (uint32_t i = u < kWStages ? 0 : u - kWStages; i < u; ++i)
           while (!tc::mbar_try_wait(&ctl->w_full[i % kWStages], (i / kWStages) & 1) &&
