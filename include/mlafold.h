@@ -428,8 +428,8 @@ int32_t mla_query_absorb(const mla_query_shape *shape, const void *q, const void
  * mla_shape with groups 0 or 1 (its policy, min_split_tokens and max_splits are
  * not used: the work is cut into equal parts, one per pair of CTAs, num_ctas / 2
  * pairs). Refused with MLA_ERR_SHAPE: a shape whose work has 2^31 or more places,
- * ceil(N / 128) (prefix_pages / 4 + 2) + R ceil(M / 128) (max_pages / 4 + 2) at
- * most, or as many workspace rows.
+ * ceil(N / 128) (ceil(prefix_pages / 4) + 3) + R ceil(M / 128) (ceil(max_pages / 4)
+ * + 3) at most, or as many workspace rows.
  *
  * mla_prefix_workspace_bytes -- bytes of workspace the decode needs. Writes the
  * size to *bytes. Host only.
@@ -451,7 +451,9 @@ int32_t mla_query_absorb(const mla_query_shape *shape, const void *q, const void
  *                MLA_FAULT_PAGE_RANGE and is cut off). May change between the
  *                decodes of one plan.
  *   seq_lens     the planned lengths.
- *   plan         of mla_prefix_plan for them.
+ *   plan         of mla_prefix_plan for them. One that is no plan of this shape
+ *                sets MLA_FAULT_WORK_ITEM; what the requests get is then
+ *                unspecified, but nothing else is read or written.
  *   workspace    >= mla_prefix_workspace_bytes(shape) bytes, device, 256-byte
  *                aligned; calls that share one must not overlap. Its contents
  *                need not be initialised.
@@ -459,7 +461,7 @@ int32_t mla_query_absorb(const mla_query_shape *shape, const void *q, const void
  *                written; lse [R, k*H] FP32 base-2 or NULL. A row with no keys
  *                at all gets out = 0, lse = -inf.
  *   status       as for mla_folded_decode: MLA_FAULT_PAGE_RANGE,
- *                MLA_FAULT_WAIT_TIMEOUT.
+ *                MLA_FAULT_WORK_ITEM, MLA_FAULT_WAIT_TIMEOUT.
  *   the others   as for mla_folded_decode.
  * Numerics as there, except that P's second term is E5M2 (hi + lo is p to 2^-7
  * relative, down to 2^-13 where p is small) and that all partial results stay
@@ -477,7 +479,8 @@ int32_t mla_prefix_decode(const mla_shape *shape, int32_t prefix_pages, const vo
 /* Bits the kernels OR into *status. */
 #define MLA_FAULT_WAIT_TIMEOUT 0x1 /* a pipeline wait gave up; the CTA stopped early */
 #define MLA_FAULT_PAGE_RANGE 0x2   /* a block-table entry was outside [0, num_pages) */
-#define MLA_FAULT_WORK_ITEM 0x4    /* a work item named a request or split out of range */
+#define MLA_FAULT_WORK_ITEM 0x4    /* a work item named a request or split out of range;
+                                      a prefix plan that is none of the shape */
 #define MLA_FAULT_ROPE_RANGE 0x8   /* a token's position was outside the rope table */
 
 #ifdef __cplusplus

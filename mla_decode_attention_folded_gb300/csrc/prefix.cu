@@ -52,7 +52,7 @@ struct MergeArgs {
   uint16_t* out;                           // [N][512]
   float* lse;                              // [N], may be null
   float bmm2;
-  int R, M, prefix_pages, units, blocks, own_blocks;
+  int R, M, prefix_pages, max_pages, units, blocks, own_blocks;
 };
 
 __global__ void __launch_bounds__(kWarps * 32) prefix_merge_kernel(const MergeArgs a) {
@@ -62,8 +62,9 @@ __global__ void __launch_bounds__(kWarps * 32) prefix_merge_kernel(const MergeAr
   const int m = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (m >= a.M) return;
   const size_t row = (size_t)r * a.M + m;
-  const int own = a.plan[r], own_next = a.plan[r + 1];
-  const WideLine line(*a.prefix_len, a.plan[a.R], a.prefix_pages, a.blocks, a.units);
+  const int own = a.plan[r], own_end = a.plan[r + 1];
+  const int own_places = wide_own_places(a.plan, a.R, a.own_blocks, a.max_pages);
+  const WideLine line(*a.prefix_len, own_places, a.prefix_pages, a.blocks, a.units);
   // The pieces of this row's two segments, in consecutive slots each.
   int n_pre = 0, n_own = 0;
   size_t pre = 0, mine = 0;
@@ -74,10 +75,11 @@ __global__ void __launch_bounds__(kWarps * 32) prefix_merge_kernel(const MergeAr
   };
   if (line.prefix_tiles > 0) {
     const int b = (int)(row / kWideRows);
-    n_pre = pieces(b * (line.prefix_tiles + kWideCost), line.prefix_tiles, b, (int)(row % kWideRows), pre);
+    n_pre = pieces(b * (line.prefix_tiles + kWideCost), line.prefix_tiles, b,
+                   (int)(row % kWideRows), pre);
   }
-  const int span = (own_next - own) / a.own_blocks;
-  if (span > kWideCost) {
+  const int span = wide_span(own, own_end, own_places, a.own_blocks, a.max_pages);
+  if (span > 0) {
     const int j = m / kWideRows;
     n_own = pieces(line.prefix_places + own + j * span, span - kWideCost,
                    a.blocks + r * a.own_blocks + j, m % kWideRows, mine);
@@ -150,8 +152,9 @@ size_t wide_bytes(const mla_shape& s) { return wide_out_bytes(s) + align256(wide
 
 // Places on the line of work: 31 bits hold them.
 bool places_fit(const mla_shape& s, int prefix_pages) {
-  const long long own = (long long)s.R * wide_own_blocks(s) * (cdiv((long long)s.max_pages * kPage, kWideKeys) + kWideCost);
-  return own + wide_blocks(s) * (cdiv((long long)prefix_pages * kPage, kWideKeys) + kWideCost) < (1LL << 31) &&
+  const long long prefix =
+      wide_blocks(s) * (cdiv((long long)prefix_pages * kPage, kWideKeys) + kWideCost);
+  return prefix + wide_own_most(s.R, wide_own_blocks(s), s.max_pages) < (1LL << 31) &&
          wide_rows(s) < (1ull << 31);
 }
 
@@ -245,6 +248,7 @@ extern "C" int32_t mla_prefix_decode(const mla_shape* shape, int32_t prefix_page
   m.R = w.R;
   m.M = w.M;
   m.prefix_pages = prefix_pages;
+  m.max_pages = w.max_pages;
   m.units = w.units;
   m.blocks = w.blocks;
   m.own_blocks = w.own_blocks;

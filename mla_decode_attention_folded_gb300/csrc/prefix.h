@@ -44,6 +44,30 @@ __host__ __device__ __forceinline__ int wide_len(int len, int pages) {
   return len < 0 ? 0 : (int)(len < most ? len : most);
 }
 
+// Places of the requests' own keys when every table row is full: no plan has more.
+__host__ __device__ __forceinline__ long long wide_own_most(int R, int own_blocks, int max_pages) {
+  return (long long)R * own_blocks * (cdiv((long long)max_pages * kPage, kWideKeys) + kWideCost);
+}
+// The requests' own places by a plan; none if its end cannot be one. A plan of other
+// lengths or of no lengths at all never leads out of the tables, rows and slots.
+__device__ __forceinline__ int wide_own_places(const int32_t* plan, int R, int own_blocks,
+                                               int max_pages) {
+  const int own = plan[R];
+  return own >= 0 && own <= wide_own_most(R, own_blocks, max_pages) ? own : 0;
+}
+// Places of each block of the request with places [first, end) of `own`: 0 if it has
+// no keys, -1 if that is no request of a plan.
+__device__ __forceinline__ int wide_span(int first, int end, int own, int own_blocks,
+                                         int max_pages) {
+  if (first < 0 || end < first || end > own) return -1;
+  const int span = (int)((unsigned)(end - first) / (unsigned)own_blocks);
+  if (span * own_blocks != end - first) return -1;
+  return span == 0 || (span > kWideCost &&
+                       span - kWideCost <= (int)cdiv((long long)max_pages * kPage, kWideKeys))
+             ? span
+             : -1;
+}
+
 // The whole line, and how it is cut. Places fit 31 bits (the host checks).
 struct WideLine {
   int prefix_len, prefix_tiles, prefix_places, places;
@@ -78,11 +102,12 @@ struct WideWalk {
   const WideArgs& a;
   const int32_t* plan;
   const int32_t* lens;
-  int prefix_len, prefix_tiles, prefix_places;
+  int prefix_len, prefix_tiles, prefix_places, own;
   int pos, end, unit, r = 0;
   __device__ WideWalk(const WideArgs& a_, const int32_t* plan_, const int32_t* lens_, int unit_)
       : a(a_), plan(plan_), lens(lens_), unit(unit_) {
-    const WideLine line(*a_.prefix_len, plan_[a_.R], a_.prefix_pages, a_.blocks, a_.units);
+    own = wide_own_places(plan_, a_.R, a_.own_blocks, a_.max_pages);
+    const WideLine line(*a_.prefix_len, own, a_.prefix_pages, a_.blocks, a_.units);
     prefix_len = line.prefix_len;
     prefix_tiles = line.prefix_tiles;
     prefix_places = line.prefix_places;
@@ -106,12 +131,12 @@ struct WideWalk {
       } else {
         const int at = pos - prefix_places;
         while (r + 1 < a.R && plan[r + 1] <= at) ++r;
-        const unsigned span = (unsigned)(plan[r + 1] - plan[r]) / (unsigned)a.own_blocks;
-        if ((int)span <= kWideCost) return false;    // not a plan of this shape
-        const int j = (int)((unsigned)(at - plan[r]) / span);
-        tiles = (int)span - kWideCost;
+        const int span = wide_span(plan[r], plan[r + 1], own, a.own_blocks, a.max_pages);
+        if (span <= 0 || plan[r] > at) return false;        // not a plan
+        const int j = (int)((unsigned)(at - plan[r]) / (unsigned)span);
+        tiles = span - kWideCost;
         segment = a.blocks + r * a.own_blocks + j;
-        first = prefix_places + plan[r] + j * (int)span;
+        first = prefix_places + plan[r] + j * span;
         p.table = a.block_table + (long long)r * a.max_pages;
         p.len = lens[r];
         p.row0 = r * a.M + j * kWideRows;

@@ -614,6 +614,13 @@ wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
   }
   if (cut && a.status) atomicOr(a.status, MLA_FAULT_PAGE_RANGE);
   __syncthreads();
+  if (blockIdx.x == 0 && a.status) {
+    const int own = wide_own_places(plan, a.R, a.own_blocks, a.max_pages);
+    bool bad = threadIdx.x == 0 && (plan[0] != 0 || plan[a.R] != own);
+    for (int i = threadIdx.x; i < a.R; i += kThreads)
+      bad |= wide_span(plan[i], plan[i + 1], own, a.own_blocks, a.max_pages) < 0;
+    if (bad) atomicOr(a.status, MLA_FAULT_WORK_ITEM);
+  }
   const WideWalk walk(a, plan, lens, (int)(blockIdx.x >> 1));
   if (walk.pos >= walk.end) {
     // Nothing for this pair.

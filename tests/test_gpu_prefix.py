@@ -200,6 +200,41 @@ def test_a_plan_of_other_lengths_stays_in_bounds():
     _check(out, lse, b, table, n)
 
 
+@pytest.mark.parametrize("plan,fault", [
+    ([0, 0, 0, 0], False),                        # a plan: nobody has keys
+    ([0, 4, 8, 8], False),                        # a plan of other lengths
+    ([-1, -1, -1, -1], True),
+    ([0, 5, 9, 1 << 30], True),
+    ([2147483647, -2147483648, 7, 12], True),
+    ([0, 2147483647, 4, 12], True),
+    ([4, 4, 9, 9], True),                         # does not begin at 0
+    ([0, 3, 7, 7], True),                         # three places: no tile
+    ([0, 7, 3, 12], True),                        # descends
+    ([0, 9, 9, 9], True),                         # more tiles than the table holds
+    ([0, 9, 13, 13], True),
+])
+def test_a_plan_that_is_none_is_reported_without_a_fault(plan, fault):
+    """Places that lead out of the line, its tables or its slots are not followed; the
+    canary behind the workspace and the outputs stays, and a true plan works after it."""
+    b, table, n = prefix_batch((300, 40, 0), 4, 8, 200, seed=27)
+    d = to_device(b)
+    bmm1, bmm2 = bmm_scales(b)
+    eng = mla.PrefixMla(b.R, b.k, b.H, d["bt"].shape[1], table.numel(), d["kv"].shape[0], "cuda")
+    assert d["bt"].shape[1] * 64 <= 512           # at most two tiles a request
+    size = eng.workspace.numel()
+    eng.workspace = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    plen = torch.tensor([n], dtype=torch.int32, device="cuda")
+    eng.places.copy_(torch.tensor(plan, dtype=torch.int32))
+    eng.decode(d["q"], d["kv"], table.cuda(), plen, d["bt"], d["lens"], bmm1, bmm2)
+    assert int(eng.status.item()) == (mla.FAULT_WORK_ITEM if fault else 0)
+    assert bool((eng.workspace[size:] == 0xA5).all())
+    eng.status.zero_()
+    eng.plan(d["lens"])
+    out, lse = eng.decode(d["q"], d["kv"], table.cuda(), plen, d["bt"], d["lens"], bmm1, bmm2)
+    assert int(eng.status.item()) == 0
+    _check(out, lse, b, table, n)
+
+
 def test_garbage_behind_the_last_keys_is_not_read():
     """NaN codes in the unused slots of the last pages, prefix and own."""
     b, table, n = prefix_batch((100, 37, 1), 4, 8, 333, seed=12)
