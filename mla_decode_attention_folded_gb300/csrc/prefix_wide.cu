@@ -61,13 +61,15 @@ constexpr uint32_t kIdescLo = kIdescHi | (1u << 7);       // A in E5M2
 static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms need 1 KB alignment");
 
 struct WideCtl {
-  uint64_t k_full[2];      // rank 0: TMA of both CTAs -> S: both CTAs' keys landed, but for
-  uint64_t k_last[2];      // band 3, which has its own
+  uint64_t k_full[2];      // rank 0: TMA of both CTAs -> S: bands 0, 1 and the rope of both
+                           // CTAs' keys landed
+  uint64_t k_band[2][2];   // rank 0: TMA of both CTAs -> S: bands 2 and 3, by stage and band
   uint64_t v_full[2];      // rank 0: TMA of both CTAs -> PV: V complete in both
   uint64_t v_tail[2];      // TMA -> softmax, TMA warp: V of a block's last tile landed here
   uint64_t s_full[2];      // MMA -> softmax, TMA: S of a tile done
   uint64_t p_full[2];      // rank 0: softmax of both CTAs -> PV: P of CTA h's keys written
-  uint64_t pv_half[2];     // MMA -> softmax, TMA: O holds CTA 0's keys of the tile
+  uint64_t pv_first[2];    // MMA -> TMA: O's first dim half holds CTA 0's keys of the tile
+  uint64_t pv_half[2];     // MMA -> softmax, TMA: all of O does, and all of P has been written
   uint64_t pv_most[2];     // MMA -> TMA: and the first dim half of CTA 1's
   uint64_t pv_done[2];     // MMA -> softmax, TMA: O holds the tile; P and the stage are free
   uint64_t q_full;         // rank 0: TMA of both CTAs -> S
@@ -140,9 +142,10 @@ struct Pages {
   }
 };
 
-// Own keys (and Q at each piece's start). A stage's bands 0-1 hold V of CTA 0's
-// keys, which PV is done with first, bands 2 and 3 that of CTA 1's: it is refilled
-// in three parts, so that little is left to load once PV is done.
+// Own keys (and Q at each piece's start). A stage's bands hold V in the order in
+// which PV is done with it (CTA 0's keys of the first dim half, of the second, CTA
+// 1's keys): each is refilled as it becomes free, so that little is left to load once
+// PV is done.
 __device__ void load_keys(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl* ctl,
                           uint32_t rank, const CUtensorMap* tm_kv, const CUtensorMap* tm_kvr,
                           const CUtensorMap* tm_q, const CUtensorMap* tm_qr) {
@@ -162,21 +165,22 @@ __device__ void load_keys(const WideArgs& a, WideWalk walk, uint8_t* smem, WideC
       const int p1 = __shfl_sync(0xffffffffu, cur, 2 * rank + 1);
       if (lane == 0) {
         const uint32_t bar = tc::map_rank(&ctl->k_full[st], 0);
-        const uint32_t last = tc::map_rank(&ctl->k_last[st], 0);
+        const uint32_t bar2 = tc::map_rank(&ctl->k_band[st][0], 0);
+        const uint32_t bar3 = tc::map_rank(&ctl->k_band[st][1], 0);
         const uint32_t live = (p0 >= 0) + (p1 >= 0);
         uint8_t* stage = smem + st * kStageBytes;
-        if (i >= 2) ok = w_wait(&ctl->pv_half[st], ph, ctl, a.status);
-        auto band = [&](int c) {
+        if (i >= 2) ok = w_wait(&ctl->pv_first[st], ph, ctl, a.status);
+        auto band = [&](int c, uint32_t to) {
           for (int h = 0; h < 2; ++h)
             if ((h ? p1 : p0) >= 0)
-              tc::tma_load_2d_pair(stage + c * kChunkBytes + h * (kChunkBytes / 2), tm_kv,
-                                   c == 3 ? last : bar, c * 128, (h ? p1 : p0) * kPage);
+              tc::tma_load_2d_pair(stage + c * kChunkBytes + h * (kChunkBytes / 2), tm_kv, to,
+                                   c * 128, (h ? p1 : p0) * kPage);
         };
         if (ok) {
-          tc::remote_arrive_expect_tx(bar, live * (kPage * (kDqk - 128)));
-          tc::remote_arrive_expect_tx(last, live * (kPage * 128));
-          band(0);
-          band(1);
+          tc::remote_arrive_expect_tx(bar, live * (kPage * (2 * 128 + 64)));
+          tc::remote_arrive_expect_tx(bar2, live * (kPage * 128));
+          tc::remote_arrive_expect_tx(bar3, live * (kPage * 128));
+          band(0, bar);
           for (int h = 0; h < 2; ++h)
             if ((h ? p1 : p0) >= 0)
               tc::tma_load_2d_pair(stage + 4 * kChunkBytes + h * (kRopeBytes / 2), tm_kvr, bar, 512,
@@ -193,10 +197,12 @@ __device__ void load_keys(const WideArgs& a, WideWalk walk, uint8_t* smem, WideC
             tc::tma_load_2d_pair(q + 4 * kQChunk, tm_qr, q_bar, 512, row);
           }
         }
+        if (ok && i >= 2) ok = w_wait(&ctl->pv_half[st], ph, ctl, a.status);
+        if (ok) band(1, bar);
         if (ok && i >= 2) ok = w_wait(&ctl->pv_most[st], ph, ctl, a.status);
-        if (ok) band(2);
+        if (ok) band(2, bar2);
         if (ok && i >= 2) ok = w_wait(&ctl->pv_done[st], ph, ctl, a.status);
-        if (ok) band(3);
+        if (ok) band(3, bar3);
       }
       ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
     }
@@ -269,9 +275,9 @@ __device__ void issue_s(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl
     ++x;
     for (int t = 0; t < piece.count; ++t, ++i) {
       const int st = i & 1;
-      // The S buffer of tile i - 2 is free: band 2 was refilled after PV had begun on
-      // CTA 1's keys (pv_most), whose P the softmax wrote after it had read that S.
-      // Band 3 comes last, when that PV is done; the other bands' MMAs cover its flight.
+      // The S buffer of tile i - 2 is free: band 1 was refilled after pv_half, when all
+      // of that tile's P had been written, after all of its S had been read. Bands 2
+      // and 3 follow as PV leaves them; the others' MMAs cover their flight.
       if (!(ok = w_wait(&ctl->k_full[st], (i >> 1) & 1, ctl, a.status))) break;
       tc::fence_after_sync();
       const uint32_t kv = s_kv + st * kStageBytes, d = tmem + kSCol + st * 128;
@@ -284,15 +290,17 @@ __device__ void issue_s(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl
       };
       band(0);
       band(1);
-      band(2);
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk)
         tc::mma_f8_pair(d, tc::smem_desc(s_q + 4 * kQChunk + kk * 32, 16, 512, tc::kSw64),
                         tc::smem_desc(kv + 4 * kChunkBytes + kk * 32, 16, 512, tc::kSw64), kIdescS,
                         true);
-      if (!(ok = w_wait(&ctl->k_last[st], (i >> 1) & 1, ctl, a.status))) break;
-      tc::fence_after_sync();
-      band(3);
+      for (int c = 2; c < 4 && ok; ++c) {
+        if (!(ok = w_wait(&ctl->k_band[st][c - 2], (i >> 1) & 1, ctl, a.status))) break;
+        tc::fence_after_sync();
+        band(c);
+      }
+      if (!ok) break;
       tc::mma_commit_pair(&ctl->s_full[st]);
     }
     if (ok) tc::mma_commit_pair(&ctl->q_empty);
@@ -309,29 +317,33 @@ __device__ void issue_pv(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCt
   while (ok && walk.next(piece)) {
     for (int t = 0; ok && t < piece.count; ++t, ++i) {
       const int st = i & 1;
-      ok = w_wait(&ctl->v_full[st], (i >> 1) & 1, ctl, a.status);
+      ok = w_wait(&ctl->v_full[st], (i >> 1) & 1, ctl, a.status) &&
+           w_wait(&ctl->p_full[0], i & 1, ctl, a.status);
+      if (!ok) break;
+      tc::fence_after_sync();
+      const uint32_t kv = s_kv + st * kStageBytes;
+      auto product = [&](int kh, int d) {            // CTA kh's keys, dim half d
 #pragma unroll
-      for (int kh = 0; kh < 2; ++kh) {               // CTA 0's keys, then CTA 1's
-        ok = ok && w_wait(&ctl->p_full[kh], i & 1, ctl, a.status);
-        if (!ok) break;
-        tc::fence_after_sync();
-        const uint32_t kv = s_kv + st * kStageBytes;
-#pragma unroll
-        for (int d = 0; d < 2; ++d) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t v = tc::smem_desc(kv + (kh * 2 + d) * kChunkBytes + kk * 32 * 128,
-                                             kChunkBytes, 1024, tc::kSw128);
-            const uint32_t p = s_p + kh * kPChunk + kk * 32;
-            tc::mma_f8_pair(tmem + d * 128, tc::smem_desc(p, 16, 1024, tc::kSw128), v, kIdescHi,
-                            !(t == 0 && kh == 0 && kk == 0));
-            tc::mma_f8_pair(tmem + d * 128, tc::smem_desc(p + 2 * kPChunk, 16, 1024, tc::kSw128), v,
-                            kIdescLo, true);
-          }
-          if (kh == 1 && d == 0) tc::mma_commit_pair(&ctl->pv_most[st]);
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t v = tc::smem_desc(kv + (kh * 2 + d) * kChunkBytes + kk * 32 * 128,
+                                           kChunkBytes, 1024, tc::kSw128);
+          const uint32_t p = s_p + kh * kPChunk + kk * 32;
+          tc::mma_f8_pair(tmem + d * 128, tc::smem_desc(p, 16, 1024, tc::kSw128), v, kIdescHi,
+                          !(t == 0 && kh == 0 && kk == 0));
+          tc::mma_f8_pair(tmem + d * 128, tc::smem_desc(p + 2 * kPChunk, 16, 1024, tc::kSw128), v,
+                          kIdescLo, true);
         }
-        tc::mma_commit_pair(kh == 0 ? &ctl->pv_half[st] : &ctl->pv_done[st]);
-      }
+      };
+      product(0, 0);
+      tc::mma_commit_pair(&ctl->pv_first[st]);
+      product(0, 1);
+      if (!(ok = w_wait(&ctl->p_full[1], i & 1, ctl, a.status))) break;
+      tc::fence_after_sync();
+      tc::mma_commit_pair(&ctl->pv_half[st]);
+      product(1, 0);
+      tc::mma_commit_pair(&ctl->pv_most[st]);
+      product(1, 1);
+      tc::mma_commit_pair(&ctl->pv_done[st]);
     }
   }
   mma_drain(&ctl->drain[1]);
@@ -568,11 +580,13 @@ wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&ctl->k_full[b], 2);
-      tc::mbar_init(&ctl->k_last[b], 2);
+      tc::mbar_init(&ctl->k_band[b][0], 2);
+      tc::mbar_init(&ctl->k_band[b][1], 2);
       tc::mbar_init(&ctl->v_full[b], 2);
       tc::mbar_init(&ctl->v_tail[b], 1);
       tc::mbar_init(&ctl->s_full[b], 1);
       tc::mbar_init(&ctl->p_full[b], 2 * kSoft / 64);   // the warps of one key half, both CTAs
+      tc::mbar_init(&ctl->pv_first[b], 1);
       tc::mbar_init(&ctl->pv_half[b], 1);
       tc::mbar_init(&ctl->pv_most[b], 1);
       tc::mbar_init(&ctl->pv_done[b], 1);
