@@ -23,12 +23,11 @@
 // own dims, so that V of (dim half i, keys of CTA h) lies in slot 2 h + i in both
 // CTAs, as the pair's MMA wants, and two stages fit.
 //
-// P enters the product as an E4M3 and an E5M2 term: p16 = fp16(p), hi =
-// e4m3(p16), lo = e5m2(p16 - hi). E5M2's range keeps the second term where hi
-// is subnormal (p < 2^-6, absolute step 2^-9), so hi + lo is p to 2^-7 relative
-// down to 2^-13 of absolute error. The running max is lazy as in decode_tc.cu
-// (moved when a weight exceeds 2^8, to 2 below the tile's); P is
-// computed as if no row moved and once more where one did.
+// P enters the product as an E4M3 and an E5M2 term: hi = e4m3(p), lo = e5m2(p - hi).
+// E5M2's range keeps the second term where hi is subnormal (p < 2^-6, absolute step
+// 2^-9), so hi + lo is p to 2^-7 relative down to 2^-13 of absolute error. The
+// running max is lazy (moved when 32 weights of a row sum to more than 2^8, to 2
+// below the tile's); P is computed as if no row moved and once more where one did.
 #include "decode_common.cuh"
 #include "internal.h"
 #include "prefix.h"
@@ -350,24 +349,23 @@ __device__ void issue_pv(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCt
 }
 
 // ---------------------------------------------------------------- softmax
-// The larger of two FP16 pairs, lane by lane; a NaN loses.
-__device__ __forceinline__ uint32_t f16x2_max(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+// p - h for an FP16 h, in FP32.
+__device__ __forceinline__ float less_f16(float p, uint16_t h) {
+  float r;
+  asm("fma.rn.f32.f16 %0, %1, %2, %3;" : "=f"(r) : "h"(h), "h"((uint16_t)0xbc00), "f"(p));
   return r;
 }
-__device__ __forceinline__ uint16_t f16x2_to_e5m2x2(uint32_t h) {
+__device__ __forceinline__ uint16_t f32x2_to_e5m2x2(float lo, float hi) {
   uint16_t r;
-  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
 // P of 32 keys of a row from their scores: the codes of both terms and the sum.
-// Returns whether a weight exceeds 2^8 (as FP16): the tile is then done again.
+// Returns whether they sum to more than 2^8: the tile is then done again.
 __device__ __forceinline__ bool weigh(const uint32_t (&raw)[32], float scale, float neg_max,
                                       float& sum, uint32_t (&hi)[8], uint32_t (&lo)[8]) {
   const uint64_t scale2 = pack_f32x2(scale, scale), neg2 = pack_f32x2(neg_max, neg_max);
   uint64_t sums[2] = {0, 0};
-  uint32_t most = 0;
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
     uint64_t d01 = pack_f32x2(__uint_as_float(raw[i]), __uint_as_float(raw[i + 1]));
@@ -381,19 +379,19 @@ __device__ __forceinline__ bool weigh(const uint32_t (&raw)[32], float scale, fl
     for (int u = 0; u < 4; ++u) p[u] = ex2(p[u]);
     sums[0] = add_f32x2(sums[0], pack_f32x2(p[0], p[1]));
     sums[1] = add_f32x2(sums[1], pack_f32x2(p[2], p[3]));
-    const uint32_t h01 = dec::f32x2_to_f16x2(p[0], p[1]), h23 = dec::f32x2_to_f16x2(p[2], p[3]);
-    most = f16x2_max(most, f16x2_max(h01, h23));
-    const uint16_t e01 = dec::f16x2_to_e4m3x2(h01), e23 = dec::f16x2_to_e4m3x2(h23);
-    const uint16_t l01 = f16x2_to_e5m2x2(dec::f16x2_sub(h01, e4m3x2_to_f16x2(e01)));
-    const uint16_t l23 = f16x2_to_e5m2x2(dec::f16x2_sub(h23, e4m3x2_to_f16x2(e23)));
+    const uint16_t e01 = f32x2_to_e4m3x2(p[0], p[1]), e23 = f32x2_to_e4m3x2(p[2], p[3]);
+    const uint32_t h01 = e4m3x2_to_f16x2(e01), h23 = e4m3x2_to_f16x2(e23);
+    const uint16_t l01 = f32x2_to_e5m2x2(less_f16(p[0], (uint16_t)h01),
+                                         less_f16(p[1], (uint16_t)(h01 >> 16)));
+    const uint16_t l23 = f32x2_to_e5m2x2(less_f16(p[2], (uint16_t)h23),
+                                         less_f16(p[3], (uint16_t)(h23 >> 16)));
     hi[i / 4] = (uint32_t)e01 | ((uint32_t)e23 << 16);
     lo[i / 4] = (uint32_t)l01 | ((uint32_t)l23 << 16);
   }
   float a, b;
   unpack_f32x2(add_f32x2(sums[0], sums[1]), a, b);
   sum = a + b;
-  constexpr uint32_t k256 = 0x5c00;                // 2^8; weights are >= 0: bits compare as values
-  return (most & 0xffff) > k256 || (most >> 16) > k256;
+  return sum > 256.f;
 }
 
 // Thread (row, 32 keys): TMEM lane l holds row l % 64, keys of CTA l / 64; the
@@ -450,20 +448,21 @@ __device__ void softmax(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl
       float sum;
       bool moved = t == 0;
       if (t > 0) {
-        const bool over = weigh(raw, a.bmm1_log2, -m, sum, hi, lo);
+        const bool over = weigh(raw, a.bmm1_log2, m == -INFINITY ? 0.f : -m, sum, hi, lo);
         if (soft_any(over || !ok)) {
           if (soft_any(!ok)) return;               // all of them
           moved = true;
         }
       }
       if (moved) {
-        // Rows whose max grew by more than 8 (or begin): the new max is 2 below
-        // the tile's; the sum and O follow.
+        // Rows whose max grew by more than 3 (or begin; 32 weights that sum to more
+        // than 2^8 hold one above 2^3): the new max is 2 below the tile's; the sum and
+        // O follow.
         float v = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 32; ++i) v = fmaxf(v, __uint_as_float(raw[i]) * a.bmm1_log2);
         const float tm = row_max(v);
-        const float mn = tm > m + 8.f ? tm - dec::kMaxLead : m;
+        const float mn = tm > m + 3.f ? tm - dec::kMaxLead : m;
         const float f = m == -INFINITY ? 0.f : ex2(m - mn);
         m = mn;
         l *= f;

@@ -126,6 +126,24 @@ def test_scores_that_grow_from_tile_to_tile(k, H):
         _check(*_decode(b, table, n, num_ctas=ctas), b, table, n, f"{ctas} CTAs")
 
 
+@pytest.mark.parametrize("spots", [(261,), (390,), (261, 390), (390, 520), (767, 768), (900, 130)])
+@pytest.mark.parametrize("k,H", [(4, 8), (3, 64)])
+def test_one_key_that_tops_all_before_it(spots, k, H):
+    """A key along some rows' queries, each later one longer, in the first or the second
+    128 keys of a tile: the maximum of a few rows moves there, in one half or in both."""
+    b, table, n = prefix_batch((700, 0, 300), k, H, 1000, seed=31)
+    kv = b.kv.view(torch.float8_e4m3fn).float() / 16
+    q = b.q.view(torch.float8_e4m3fn).float()
+    for i, j in enumerate(sorted(spots)):
+        kv[table[j // 64], j % 64] = q[i % q.shape[0], i % H] * 0.25 * 2 ** i
+        for r in range(3):
+            if j < int(b.seq_lens[r]):
+                kv[b.block_table[r, j // 64], j % 64] = q[k * r, i % H] * 0.25 * 2 ** i
+    b.kv = kv.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    for ctas in (None, 2):
+        _check(*_decode(b, table, n, num_ctas=ctas), b, table, n, f"{ctas} CTAs")
+
+
 def test_a_row_of_nan_stays_alone():
     b, table, n = prefix_batch((100, 300), 4, 8, 600, seed=22)
     clean = b.q.clone()
@@ -187,13 +205,16 @@ def test_many_short_requests():
     _check(*_decode(b, table, n), b, table, n)
 
 
-def test_a_plan_of_other_lengths_stays_in_bounds():
-    """Keys beyond the plan are not attended to, planned keys that are gone are masked."""
-    b, table, n = prefix_batch((300, 40, 0), 4, 8, 200, seed=27)
+@pytest.mark.parametrize("num_ctas", [None, 2])
+def test_a_plan_of_other_lengths_stays_in_bounds(num_ctas):
+    """Keys beyond the plan are not attended to, planned keys that are gone are masked,
+    whole pieces of several tiles without a key among them."""
+    b, table, n = prefix_batch((800, 40, 0), 4, 8, 200, seed=27)
     d = to_device(b)
     bmm1, bmm2 = bmm_scales(b)
-    eng = mla.PrefixMla(b.R, b.k, b.H, d["bt"].shape[1], table.numel(), d["kv"].shape[0], "cuda")
-    eng.plan(torch.tensor([320, 320, 320], dtype=torch.int32, device="cuda"))
+    eng = mla.PrefixMla(b.R, b.k, b.H, d["bt"].shape[1], table.numel(), d["kv"].shape[0], "cuda",
+                        num_ctas=num_ctas)
+    eng.plan(torch.tensor([820, 820, 820], dtype=torch.int32, device="cuda"))
     plen = torch.tensor([n], dtype=torch.int32, device="cuda")
     out, lse = eng.decode(d["q"], d["kv"], table.cuda(), plen, d["bt"], d["lens"], bmm1, bmm2)
     assert int(eng.status.item()) == 0
