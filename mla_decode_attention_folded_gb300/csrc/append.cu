@@ -108,15 +108,16 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendArgs a)
     for (int u = 0; u < 16; ++u) ss += f[u] * f[u];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float rs = rsqrtf(ss * (1.f / kDv) + a.eps);
+    const float rs = rsqrtf(ss * (1.f / kDv) + a.eps) * a.inv_scale;
     float w[16];
     bf16x8_to_f32(reinterpret_cast<const uint4*>(a.weight)[lane], w);
     bf16x8_to_f32(reinterpret_cast<const uint4*>(a.weight + 256)[lane], w + 8);
 #pragma unroll
     for (int u = 0; u < 16; ++u) f[u] = f[u] * rs * w[u];
-  }
+  } else {
 #pragma unroll
-  for (int u = 0; u < 16; ++u) f[u] *= a.inv_scale;
+    for (int u = 0; u < 16; ++u) f[u] *= a.inv_scale;
+  }
   uint8_t* dst = a.kv + ((size_t)page * kPage + (size_t)(j % kPage)) * kDqk;
   reinterpret_cast<uint2*>(dst)[lane] =
       make_uint2(f32x4_to_e4m3x4(f[0], f[1], f[2], f[3]), f32x4_to_e4m3x4(f[4], f[5], f[6], f[7]));
