@@ -13,7 +13,9 @@
 //
 // The merge is bound by memory: per row, its partials (2 KB each) in, 1 KB out.
 // One warp per row; the lanes hold the partials' LSEs and share weights by
-// shuffles, as the split reducer does.
+// shuffles, as the split reducer does. 128 x 7 x 64 behind 16k: 57 us for 271 MB of
+// partials and 59 MB out (5.8 TB/s); 64 x 7 x 8: 11 us from DRAM, where the loads'
+// latency counts.
 #include "internal.h"
 #include "prefix.h"
 #include "ptx.cuh"
