@@ -221,18 +221,18 @@ def test_a_plan_of_other_lengths_stays_in_bounds(num_ctas):
     _check(out, lse, b, table, n)
 
 
-@pytest.mark.parametrize("plan,fault", [
-    ([0, 0, 0, 0], False),                        # a plan: nobody has keys
-    ([0, 4, 8, 8], False),                        # a plan of other lengths
-    ([-1, -1, -1, -1], True),
-    ([0, 5, 9, 1 << 30], True),
-    ([2147483647, -2147483648, 7, 12], True),
-    ([0, 2147483647, 4, 12], True),
-    ([4, 4, 9, 9], True),                         # does not begin at 0
-    ([0, 3, 7, 7], True),                         # three places: no tile
-    ([0, 7, 3, 12], True),                        # descends
-    ([0, 9, 9, 9], True),                         # more tiles than the table holds
-    ([0, 9, 13, 13], True),
+@pytest.mark.parametrize("plan,fault", [          # one: the places of a request with one tile
+    (lambda one: [0, 0, 0, 0], False),            # a plan: nobody has keys
+    (lambda one: [0, one, 2 * one, 2 * one], False),             # a plan of other lengths
+    (lambda one: [-1, -1, -1, -1], True),
+    (lambda one: [0, one + 1, 2 * one + 1, 1 << 30], True),
+    (lambda one: [2147483647, -2147483648, 7, 3 * one], True),
+    (lambda one: [0, 2147483647, one, 3 * one], True),
+    (lambda one: [one, one, 2 * one, 2 * one], True),            # does not begin at 0
+    (lambda one: [0, one - 1, 2 * one - 1, 2 * one - 1], True),  # no tile
+    (lambda one: [0, one + 1, one - 1, 3 * one], True),          # descends
+    (lambda one: [0, one + 2, one + 2, one + 2], True),          # more tiles than the table holds
+    (lambda one: [0, one + 2, 2 * one + 2, 2 * one + 2], True),
 ])
 def test_a_plan_that_is_none_is_reported_without_a_fault(plan, fault):
     """Places that lead out of the line, its tables or its slots are not followed; the
@@ -245,7 +245,8 @@ def test_a_plan_that_is_none_is_reported_without_a_fault(plan, fault):
     size = eng.workspace.numel()
     eng.workspace = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
     plen = torch.tensor([n], dtype=torch.int32, device="cuda")
-    eng.places.copy_(torch.tensor(plan, dtype=torch.int32))
+    eng.plan(torch.tensor([1, 0, 0], dtype=torch.int32, device="cuda"))
+    eng.places.copy_(torch.tensor(plan(int(eng.places[-1])), dtype=torch.int32))
     eng.decode(d["q"], d["kv"], table.cuda(), plen, d["bt"], d["lens"], bmm1, bmm2)
     assert int(eng.status.item()) == (mla.FAULT_WORK_ITEM if fault else 0)
     assert bool((eng.workspace[size:] == 0xA5).all())
