@@ -24,7 +24,9 @@
 // per CTA).
 #include <cmath>
 
+#include "checks.h"
 #include "decode_common.cuh"
+#include "formats.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 #include "tc.cuh"
@@ -76,6 +78,15 @@ struct AbsorbArgs {
   int tiles, sets, jobs;         // token tiles, band sets per (head, tile), jobs
 };
 
+// A box of shared memory -> global; the issuing thread commits and waits for its bulk group.
+__device__ __forceinline__ void store_box(const CUtensorMap* m, const void* src, int x, int y,
+                                          int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(m)),
+      "r"(tc::smem_u32(src)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
 __device__ __forceinline__ bool ab_wait(uint64_t* bar, uint32_t parity, AbsorbCtl* ctl,
                                         int32_t* status) {
   if (tc::mbar_try_wait(bar, parity)) return true;
@@ -326,7 +337,7 @@ absorb_kernel(const AbsorbArgs a, const __grid_constant__ CUtensorMap tm_q,
         __syncwarp();
         const int tok = tok0 + quarter * 32;
         if (lane == 0 && tok < a.T)
-          tc::tma_store_3d(&tm_o, stage, (band_of(job) + b) * kBand + half * 64, h, tok);
+          store_box(&tm_o, stage, (band_of(job) + b) * kBand + half * 64, h, tok);
         if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       }
     }

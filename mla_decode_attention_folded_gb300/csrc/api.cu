@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "checks.h"
 #include "internal.h"
 
 using namespace mlafold;

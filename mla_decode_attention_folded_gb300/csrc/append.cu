@@ -17,6 +17,8 @@
 // decode reads.
 #include <cmath>
 
+#include "checks.h"
+#include "formats.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 

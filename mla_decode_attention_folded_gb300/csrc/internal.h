@@ -98,12 +98,6 @@ inline size_t workspace_bytes(const mla_shape& s) {
   return partial_out_bytes(slots, M) + align256(size_t(slots) * M * 4);
 }
 
-// Host checks shared by the entry points (api.cu): MLA_OK or an error.
-inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-int check_shape(const mla_shape* s);
-int check_device();
-bool scales_ok(float bmm1, float bmm2);   // bmm1 finite and positive, bmm2 finite
-
 struct DecodeArgs {
   const uint8_t* q;
   const uint8_t* kv;

@@ -8,6 +8,8 @@
 //   lse = max + log2 sum_s w_s; rows whose sources are all empty: 0 and -inf.
 // One warp per row; each lane owns 16 of the 512 dims; lanes hold 32 sources'
 // LSEs at a time and share weights by shuffles.
+#include "checks.h"
+#include "formats.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 

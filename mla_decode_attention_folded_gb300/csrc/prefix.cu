@@ -16,6 +16,7 @@
 // shuffles, as the split reducer does. 128 x 7 x 64 behind 16k: 57 us for 271 MB of
 // partials and 59 MB out (5.8 TB/s); 64 x 7 x 8: 11 us from DRAM, where the loads'
 // latency counts.
+#include "checks.h"
 #include "internal.h"
 #include "prefix.h"
 #include "ptx.cuh"

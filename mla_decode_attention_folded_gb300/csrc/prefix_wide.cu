@@ -38,7 +38,9 @@
 // slower: the softmax in two halves of warps, so that PV begins on the first (by CTA's
 // keys: only two of four schedulers work, 4,385 cycles; by 64 keys of each: 4,397).
 #include "decode_common.cuh"
+#include "formats.cuh"
 #include "internal.h"
+#include "pair.cuh"
 #include "prefix.h"
 #include "ptx.cuh"
 #include "tc.cuh"

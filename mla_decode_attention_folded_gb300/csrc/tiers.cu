@@ -13,6 +13,7 @@
 // Both are plain CUDA-core kernels: integer work and copies of a few MB.
 #include <cstdint>
 
+#include "checks.h"
 #include "internal.h"
 
 namespace mlafold {

@@ -172,3 +172,12 @@ def test_rope_table(base):
             # 64-bit angles: their error is below 2^-53 * 2^17 * a few steps, FP32 rounding 2^-25.
             assert abs(float(t[p, i]) - math.cos(a)) < 2.0 ** -24
             assert abs(float(t[p, 32 + i]) - math.sin(a)) < 2.0 ** -24
+
+
+def test_the_decode_profiles_are_of_this_source():
+    """The operators around the decode leave its sources, and so its measured DRAM
+    bytes, as they were."""
+    import bench
+    for name in ("R128_k7_H64_skewed128k", "R32_k4_H8_len1k-8k", "R64_k7_H8_lognormal2k",
+                 "R16_k4_H64_len16k-64k"):
+        assert bench.profiled_traffic(name) is not None
