@@ -58,7 +58,10 @@ struct MergeArgs {
   int R, M, prefix_pages, max_pages, units, blocks, own_blocks;
 };
 
-__global__ void __launch_bounds__(kWarps * 32) prefix_merge_kernel(const MergeArgs a) {
+// EARLY: the first two partials are asked for before any LSE is there, at 95 registers.
+template <bool EARLY>
+__global__ void __launch_bounds__(kWarps * 32, EARLY ? 2 : 4)
+prefix_merge_kernel(const MergeArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   const int r = blockIdx.y, lane = threadIdx.x & 31;
@@ -91,27 +94,43 @@ __global__ void __launch_bounds__(kWarps * 32) prefix_merge_kernel(const MergeAr
   auto at = [&](int s) {
     return s < n_pre ? pre + (size_t)s * kWideRows : mine + (size_t)(s - n_pre) * kWideRows;
   };
+  float4 early[2][4] = {};
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+    if (EARLY && s < n)
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        early[s][v] = reinterpret_cast<const float4*>(a.part_o + at(s) * kDv)[v * 32 + lane];
   float mx = -INFINITY;
   for (int s = lane; s < n; s += 32) mx = fmaxf(mx, a.part_lse[at(s)]);
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   float4 acc[4];
 #pragma unroll
   for (int v = 0; v < 4; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](int v, float w, const float4& o) {
+    acc[v].x += w * o.x; acc[v].y += w * o.y; acc[v].z += w * o.z; acc[v].w += w * o.w;
+  };
   float z = 0.f;
   for (int c0 = 0; c0 < n; c0 += 32) {
     const float lc = c0 + lane < n ? a.part_lse[at(c0 + lane)] : -INFINITY;
     const float wc = (mx == -INFINITY || lc == -INFINITY) ? 0.f : ex2(lc - mx);
     z += wc;
     const int cn = min(32, n - c0);
+    int s = 0;
+    if (EARLY && c0 == 0) {
+#pragma unroll
+      for (; s < 2; ++s) {
+        const float w = __shfl_sync(0xffffffffu, wc, s);       // 0 past the last partial
+#pragma unroll
+        for (int v = 0; v < 4; ++v) add(v, w, early[s][v]);
+      }
+    }
 #pragma unroll 2
-    for (int s = 0; s < cn; ++s) {
+    for (; s < cn; ++s) {
       const float w = __shfl_sync(0xffffffffu, wc, s);
       const float4* src = reinterpret_cast<const float4*>(a.part_o + at(c0 + s) * kDv);
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const float4 o = src[v * 32 + lane];
-        acc[v].x += w * o.x; acc[v].y += w * o.y; acc[v].z += w * o.z; acc[v].w += w * o.w;
-      }
+      for (int v = 0; v < 4; ++v) add(v, w, src[v * 32 + lane]);
     }
   }
   for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
@@ -255,7 +274,13 @@ extern "C" int32_t mla_prefix_decode(const mla_shape* shape, int32_t prefix_page
   m.units = w.units;
   m.blocks = w.blocks;
   m.own_blocks = w.own_blocks;
-  return launch(prefix_merge_kernel, dim3((unsigned)cdiv(w.M, kWarps), (unsigned)w.R), kWarps * 32,
+  // While all rows are resident at once, a row's chain of loads is what the merge takes:
+  // the early one (2 x 4 x 8 behind 300 17.8 against 20.0 us with plan and decode, 32 x 4 x 8
+  // behind 4k 27.4 against 30.7, 24 x 1 x 64 behind 64k 113 against 118). With more rows,
+  // warps in flight count (128 x 7 x 64 behind 16k 1205 against 1186).
+  const dim3 grid((unsigned)cdiv(w.M, kWarps), (unsigned)w.R);
+  const bool early = (long long)grid.x * grid.y <= 2LL * shape->num_ctas;
+  return launch(early ? prefix_merge_kernel<true> : prefix_merge_kernel<false>, grid, kWarps * 32,
                 cs, m) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;

@@ -99,17 +99,18 @@ struct WidePiece {
 };
 
 // The pieces of part `unit`, in order, from the plan and the lengths ([R] each,
-// the plan with its end) as the caller holds them.
+// the plan with its end) and the prefix's length as the caller holds them.
 struct WideWalk {
   const WideArgs& a;
   const int32_t* plan;
   const int32_t* lens;
   int prefix_len, prefix_tiles, prefix_places, own;
   int pos, end, unit, r = 0;
-  __device__ WideWalk(const WideArgs& a_, const int32_t* plan_, const int32_t* lens_, int unit_)
+  __device__ WideWalk(const WideArgs& a_, const int32_t* plan_, const int32_t* lens_,
+                      int prefix_len_, int unit_)
       : a(a_), plan(plan_), lens(lens_), unit(unit_) {
     own = wide_own_places(plan_, a_.R, a_.own_blocks, a_.max_pages);
-    const WideLine line(*a_.prefix_len, own, a_.prefix_pages, a_.blocks, a_.units);
+    const WideLine line(prefix_len_, own, a_.prefix_pages, a_.blocks, a_.units);
     prefix_len = line.prefix_len;
     prefix_tiles = line.prefix_tiles;
     prefix_places = line.prefix_places;

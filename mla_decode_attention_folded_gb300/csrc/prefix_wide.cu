@@ -167,6 +167,16 @@ __device__ void load_keys(const WideArgs& a, WideWalk walk, uint8_t* smem, WideC
   WidePiece piece;
   while (ok && walk.next(piece)) {
     pages.begin(piece);
+    auto load_q = [&] {
+      uint8_t* q = smem + kOffQ;
+      const int row = piece.row0 + (int)rank * 64;
+      tc::remote_arrive_expect_tx(q_bar, kQBytes);
+      for (int c = 0; c < 4; ++c)
+        tc::tma_load_2d_pair(q + c * kQChunk, tm_q, q_bar, c * 128, row);
+      tc::tma_load_2d_pair(q + 4 * kQChunk, tm_qr, q_bar, 512, row);
+    };
+    if (x == 0 && lane == 0) load_q();             // while the first page ids are under way
+    __syncwarp();
     for (int t = 0; ok && t < piece.count; ++t, ++i) {
       const int st = i & 1;
       const uint32_t ph = ((i >> 1) - 1) & 1;
@@ -196,16 +206,9 @@ __device__ void load_keys(const WideArgs& a, WideWalk walk, uint8_t* smem, WideC
               tc::tma_load_2d_pair(stage + 4 * kChunkBytes + h * (kRopeBytes / 2), tm_kvr, bar, 512,
                                    (h ? p1 : p0) * kPage);
         }
-        if (ok && t == 0) {
-          if (x > 0) ok = w_wait(&ctl->q_empty, (x - 1) & 1, ctl, a.status);
-          if (ok) {
-            uint8_t* q = smem + kOffQ;
-            const int row = piece.row0 + (int)rank * 64;
-            tc::remote_arrive_expect_tx(q_bar, kQBytes);
-            for (int c = 0; c < 4; ++c)
-              tc::tma_load_2d_pair(q + c * kQChunk, tm_q, q_bar, c * 128, row);
-            tc::tma_load_2d_pair(q + 4 * kQChunk, tm_qr, q_bar, 512, row);
-          }
+        if (ok && t == 0 && x > 0) {
+          ok = w_wait(&ctl->q_empty, (x - 1) & 1, ctl, a.status);
+          if (ok) load_q();
         }
         if (ok && i >= 2) ok = w_wait(&ctl->pv_half[st], ph, ctl, a.status);
         if (ok) band(1, bar);
@@ -550,7 +553,8 @@ __device__ void softmax(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl
                        col0 + (lane & 3) * 4;
     const int rows = live - (quarter & 1) * 32 - (lane >> 2);      // of this lane, 8 apart
 #pragma unroll 1
-    for (int turn = 0; turn < 4; ++turn) {         // columns 128 (turn / 2) + 16 (turn % 2) ..
+    for (int turn = (quarter & 1) * 32 < live ? 0 : 4; turn < 4; ++turn) {
+      // columns 128 (turn / 2) + 16 (turn % 2) ..; none for a warp without live rows
       uint32_t o[16];
       tc::tmem_ld16(tmem + lanes + (turn >> 1) * 128 + col0 + (turn & 1) * 16, o);
       tc::tmem_wait_ld();
@@ -627,7 +631,8 @@ wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
   grid_dep_launch();
   int32_t* plan = reinterpret_cast<int32_t*>(smem + kOffPlan);
   int32_t* lens = plan + kMaxR + 1;
-  bool cut = blockIdx.x == 0 && threadIdx.x == 0 && *a.prefix_len > (long long)a.prefix_pages * kPage;
+  const int prefix_len = *a.prefix_len;
+  bool cut = blockIdx.x == 0 && threadIdx.x == 0 && prefix_len > (long long)a.prefix_pages * kPage;
   for (int i = threadIdx.x; i <= a.R; i += kThreads) {
     plan[i] = a.plan[i];
     if (i < a.R) {
@@ -645,7 +650,7 @@ wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
       bad |= wide_span(plan[i], plan[i + 1], own, a.own_blocks, a.max_pages) < 0;
     if (bad) atomicOr(a.status, MLA_FAULT_WORK_ITEM);
   }
-  const WideWalk walk(a, plan, lens, (int)(blockIdx.x >> 1));
+  const WideWalk walk(a, plan, lens, prefix_len, (int)(blockIdx.x >> 1));
   if (walk.pos >= walk.end) {
     // Nothing for this pair.
   } else if (warp == 0) {
