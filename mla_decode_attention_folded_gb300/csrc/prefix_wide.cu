@@ -79,7 +79,7 @@ struct WideCtl {
   uint64_t s_full[2];      // MMA -> softmax, TMA: S of a tile done
   uint64_t p_full[2];      // rank 0: softmax of both CTAs -> PV: P of CTA h's keys written
   uint64_t pv_first[2];    // MMA -> TMA: O's first dim half holds CTA 0's keys of the tile
-  uint64_t pv_half[2];     // MMA -> softmax, TMA: all of O does, and all of P has been written
+  uint64_t pv_half[2];     // MMA -> softmax, TMA: all of O does
   uint64_t pv_most[2];     // MMA -> TMA: and the first dim half of CTA 1's
   uint64_t pv_done[2];     // MMA -> softmax, TMA: O holds the tile; P and the stage are free
   uint64_t q_full;         // rank 0: TMA of both CTAs -> S
@@ -288,9 +288,9 @@ __device__ void issue_s(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl
     ++x;
     for (int t = 0; t < piece.count; ++t, ++i) {
       const int st = i & 1;
-      // The S buffer of tile i - 2 is free: band 1 was refilled after pv_half, when all
-      // of that tile's P had been written, after all of its S had been read. Bands 2
-      // and 3 follow as PV leaves them; the others' MMAs cover their flight.
+      // The S buffer of tile i - 2 is free: the bands were refilled after PV had begun,
+      // and no P of a tile is written before every thread of its CTA has read its S (the
+      // vote). Bands 2 and 3 follow as PV leaves them; the others' MMAs cover their flight.
       if (!(ok = w_wait(&ctl->k_full[st], (i >> 1) & 1, ctl, a.status))) break;
       tc::fence_after_sync();
       const uint32_t kv = s_kv + st * kStageBytes, d = tmem + kSCol + st * 128;
@@ -350,9 +350,9 @@ __device__ void issue_pv(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCt
       product(0, 0);
       tc::mma_commit_pair(&ctl->pv_first[st]);
       product(0, 1);
+      tc::mma_commit_pair(&ctl->pv_half[st]);
       if (!(ok = w_wait(&ctl->p_full[1], i & 1, ctl, a.status))) break;
       tc::fence_after_sync();
-      tc::mma_commit_pair(&ctl->pv_half[st]);
       product(1, 0);
       tc::mma_commit_pair(&ctl->pv_most[st]);
       product(1, 1);
