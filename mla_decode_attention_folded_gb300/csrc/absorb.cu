@@ -19,9 +19,10 @@
 // of four), warp 1 issues the MMAs into four TMEM accumulators, warps 2-9 read them
 // back and store them by TMA, each warp its 32 tokens x 64 dims on its own, from
 // two staging tiles, and warps 10-17 turn the rope dims beside them. 128 x 7 x 64:
-// 12.8 us, 4.9 TB/s (0.74 of the copy rate; the read-back sets the pace, 2,250 cycles
-// a band); 16 x 4 x 64 4.4 us, 64 x 7 x 8 4.0 us, 2 x 4 x 8 3.4 us (latency: one band
-// per CTA).
+// 12.8 us, 5.0 TB/s (0.74 of the copy rate; a band takes 1,300 cycles, the time in which
+// shared memory, 128 B a cycle, takes in W, feeds A and B to the MMAs, 64 KB, and
+// passes the codes on); 16 x 4 x 64 4.4 us, 64 x 7 x 8 4.0 us, 2 x 4 x 8 3.4 us (one
+// band per CTA: latency).
 #include <cmath>
 
 #include "checks.h"

@@ -19,7 +19,8 @@ namespace mlafold {
 
 constexpr int kWideRows = 128;     // query rows per block
 constexpr int kWideKeys = 256;     // keys per tile
-// A piece costs about three tiles' time. Measured with 3, 4, 5, 6: 32 x 4 x 8 behind 4k
+// A piece costs about three tiles' time. Measured with 3, 4, 5, 6 (the merge's later gain
+// left out): 32 x 4 x 8 behind 4k
 // 29.9, 32.7, 33.0, 33.1 us; 64 x 7 x 8 behind 16k 102, 99, 104, 102 us; 24 x 1 x 64
 // behind 64k 116, 117, 119, 120 us; 128 x 7 x 64 behind 16k 1186, 1178, 1184, 1180 us.
 // A cost of its own for pieces of own keys (their last tile is cleared behind the last

@@ -29,14 +29,16 @@
 // running max is lazy (moved when 32 weights of a row sum to more than 2^8, to 2
 // below the tile's); P is computed as if no row moved and once more where one did.
 //
-// With plan and merge: 128 x 7 x 64 behind 16k 1.18 ms, 1.97 PFLOP/s (0.50 of twice
-// the BF16 rate); 24 x 1 x 64 behind 64k 114 us (0.49); 64 x 7 x 8 behind 16k 102 us
-// (0.36); 32 x 4 x 8 behind 4k 30 us; 2 x 4 x 8 behind 300 19.5 us. The second term of
+// With plan and merge: 128 x 7 x 64 behind 16k 1.17 ms, 1.98 PFLOP/s (0.51 of twice
+// the BF16 rate); 24 x 1 x 64 behind 64k 112 us (0.50); 64 x 7 x 8 behind 16k 102 us
+// (0.36); 32 x 4 x 8 behind 4k 27.5 us; 2 x 4 x 8 behind 300 18 us. The second term of
 // P makes the tensor pipe's work 1.47 times the algorithmic. A tile takes 4,080 cycles
 // against the MMAs' 3,300: from S to PV 2,570 (weights 1,090, vote 390, stores 380)
 // and from PV to the next S 1,300, with two stages to hide them behind. Tried and
 // slower: the softmax in two halves of warps, so that PV begins on the first (by CTA's
-// keys: only two of four schedulers work, 4,385 cycles; by 64 keys of each: 4,397).
+// keys: only two of four schedulers work, 4,385 cycles; by 64 keys of each: 4,397); P
+// written before the vote (112 -> 120 us); barriers per 32 rows (112 -> 116); V of CTA
+// 0's keys as soon as S leaves its bands (112 -> 114).
 #include "decode_common.cuh"
 #include "formats.cuh"
 #include "internal.h"
