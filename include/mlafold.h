@@ -428,8 +428,8 @@ int32_t mla_query_absorb(const mla_query_shape *shape, const void *q, const void
  * mla_shape with groups 0 or 1 (its policy, min_split_tokens and max_splits are
  * not used: the work is cut into equal parts, one per pair of CTAs, num_ctas / 2
  * pairs). Refused with MLA_ERR_SHAPE: a shape whose work has 2^31 or more places,
- * ceil(N / 128) (ceil(prefix_pages / 4) + 3) + R ceil(M / 128) (ceil(max_pages / 4)
- * + 3) at most, or as many workspace rows.
+ * ceil(N / 128) (ceil(prefix_pages / 4) + 3) + R ceil(M / 128) (9/8 ceil(max_pages
+ * / 4) + 3) at most, or as many workspace rows.
  *
  * mla_prefix_workspace_bytes -- bytes of workspace the decode needs. Writes the
  * size to *bytes. Host only.

@@ -34,7 +34,7 @@ prefix_plan_kernel(const int32_t* __restrict__ seq_lens, int R, int max_pages, i
   grid_dep_launch();
   const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
   const int tiles = i < R ? (int)cdiv(wide_len(seq_lens[i], max_pages), kWideKeys) : 0;
-  int sum = tiles > 0 ? own_blocks * (tiles + kWideCost) : 0;
+  int sum = tiles > 0 ? own_blocks * (int)wide_own_span(tiles) : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int t = __shfl_up_sync(0xffffffffu, sum, o);
@@ -87,7 +87,7 @@ prefix_merge_kernel(const MergeArgs a) {
   const int span = wide_span(own, own_end, own_places, a.own_blocks, a.max_pages);
   if (span > 0) {
     const int j = m / kWideRows;
-    n_own = pieces(line.prefix_places + own + j * span, span - kWideCost,
+    n_own = pieces(line.prefix_places + own + j * span, wide_own_tiles(span),
                    a.blocks + r * a.own_blocks + j, m % kWideRows, mine);
   }
   const int n = n_pre + n_own;

@@ -4,7 +4,7 @@
 // A segment is a block of up to 128 rows with the keys it attends to: block b of
 // all N rows with the prefix's keys (segments 0 .. blocks - 1), then block j of
 // request r's M rows with the request's own keys (segment blocks + r * own_blocks
-// + j). A segment of t > 0 tiles takes t + kWideCost places of one line of places,
+// + j). A segment of t > 0 tiles takes t places and a few more of one line of places,
 // one per tile, the others for what a piece costs besides (Q, new maxima, 256 KB of
 // partial rows out); segments without keys take none.
 // The line is cut into equal parts, part u from floor(u * places / used), one per
@@ -20,12 +20,16 @@ namespace mlafold {
 constexpr int kWideRows = 128;     // query rows per block
 constexpr int kWideKeys = 256;     // keys per tile
 // A piece costs about three tiles' time. Measured with 3, 4, 5, 6 (the merge's later gain
-// left out): 32 x 4 x 8 behind 4k
-// 29.9, 32.7, 33.0, 33.1 us; 64 x 7 x 8 behind 16k 102, 99, 104, 102 us; 24 x 1 x 64
-// behind 64k 116, 117, 119, 120 us; 128 x 7 x 64 behind 16k 1186, 1178, 1184, 1180 us.
-// A cost of its own for pieces of own keys (their last tile is cleared behind the last
-// key) gains 2-5 % there at 2 and 5, and loses 4 % over 21 shapes.
+// left out): 32 x 4 x 8 behind 4k 29.9, 32.7, 33.0, 33.1 us; 64 x 7 x 8 behind 16k 102,
+// 99, 104, 102 us; 24 x 1 x 64 behind 64k 116, 117, 119, 120 us; 128 x 7 x 64 behind 16k
+// 1186, 1178, 1184, 1180 us.
+// A cost of its own for pieces of own keys gains 2-5 % there at 2 and 5, and loses 4 %
+// over 21 shapes.
 constexpr int kWideCost = 3;
+// A tile of own keys takes about an eighth longer, since they come from HBM where the
+// prefix's come from L2: one place more for every 8. Without, and for every 8, 4: 64 x 7
+// x 8 behind 16k 104, 101, 99 us; 128 x 7 x 64 behind 16k 1164, 1148, 1168 us.
+constexpr int kOwnSlow = 8;
 
 struct WideArgs {
   const int32_t* prefix_table;     // [prefix_pages]
@@ -47,9 +51,16 @@ __host__ __device__ __forceinline__ int wide_len(int len, int pages) {
   return len < 0 ? 0 : (int)(len < most ? len : most);
 }
 
+// Places of a block with t > 0 tiles of own keys, and back.
+__host__ __device__ __forceinline__ long long wide_own_span(long long t) {
+  return t + t / kOwnSlow + kWideCost;
+}
+__host__ __device__ __forceinline__ int wide_own_tiles(int span) {
+  return span - kWideCost - (span - kWideCost) / (kOwnSlow + 1);
+}
 // Places of the requests' own keys when every table row is full: no plan has more.
 __host__ __device__ __forceinline__ long long wide_own_most(int R, int own_blocks, int max_pages) {
-  return (long long)R * own_blocks * (cdiv((long long)max_pages * kPage, kWideKeys) + kWideCost);
+  return R * own_blocks * wide_own_span(cdiv((long long)max_pages * kPage, kWideKeys));
 }
 // The requests' own places by a plan; none if its end cannot be one. A plan of other
 // lengths or of no lengths at all never leads out of the tables, rows and slots.
@@ -65,8 +76,9 @@ __device__ __forceinline__ int wide_span(int first, int end, int own, int own_bl
   if (first < 0 || end < first || end > own) return -1;
   const int span = (int)((unsigned)(end - first) / (unsigned)own_blocks);
   if (span * own_blocks != end - first) return -1;
-  return span == 0 || (span > kWideCost &&
-                       span - kWideCost <= (int)cdiv((long long)max_pages * kPage, kWideKeys))
+  if (span <= kWideCost) return span == 0 ? 0 : -1;
+  const int tiles = wide_own_tiles(span);
+  return wide_own_span(tiles) == span && tiles <= cdiv((long long)max_pages * kPage, kWideKeys)
              ? span
              : -1;
 }
@@ -123,9 +135,10 @@ struct WideWalk {
   }
   __device__ bool next(WidePiece& p) {
     while (pos < end) {
-      int first, tiles, segment;                     // first: the segment's first place
+      int first, tiles, after, segment;              // first place, tiles, places after them
       if (pos < prefix_places) {
         tiles = prefix_tiles;
+        after = kWideCost;
         segment = (int)((unsigned)pos / (unsigned)(tiles + kWideCost));
         first = segment * (tiles + kWideCost);
         p.table = a.prefix_table;
@@ -138,7 +151,8 @@ struct WideWalk {
         const int span = wide_span(plan[r], plan[r + 1], own, a.own_blocks, a.max_pages);
         if (span <= 0 || plan[r] > at) return false;        // not a plan
         const int j = (int)((unsigned)(at - plan[r]) / (unsigned)span);
-        tiles = span - kWideCost;
+        tiles = wide_own_tiles(span);
+        after = span - tiles;
         segment = a.blocks + r * a.own_blocks + j;
         first = prefix_places + plan[r] + j * span;
         p.table = a.block_table + (long long)r * a.max_pages;
@@ -147,7 +161,7 @@ struct WideWalk {
         p.row_end = (r + 1) * a.M;
       }
       const int last = first + tiles, stop = end < last ? end : last, from = pos;
-      pos = stop < last ? stop : last + kWideCost;
+      pos = stop < last ? stop : last + after;
       if (from >= last) continue;                    // the places after the tiles
       p.tile = from - first;
       p.count = stop - from;

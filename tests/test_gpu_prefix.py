@@ -62,10 +62,12 @@ def test_against_the_oracle(prefix, k, H):
     _check(out, lse, b, table, n)
 
 
-@pytest.mark.parametrize("lens", [(0, 0, 0), (0,), (1,), (700,), (5, 0, 1, 400, 64, 63, 65, 129)])
+@pytest.mark.parametrize("lens", [(0, 0, 0), (0,), (1,), (700,), (5, 0, 1, 400, 64, 63, 65, 129),
+                                  (5000, 2048, 0, 1793, 2304)])
 def test_own_keys_of_any_length(lens):
     b, table, n = prefix_batch(lens, 4, 8, 333, seed=sum(lens))
-    _check(*_decode(b, table, n), b, table, n)
+    for ctas in (None, 6):
+        _check(*_decode(b, table, n, num_ctas=ctas), b, table, n, f"{ctas} CTAs")
 
 
 def test_empty_prefix_and_rows_without_keys():
