@@ -60,7 +60,7 @@ __host__ __device__ __forceinline__ int wide_own_tiles(int span) {
 }
 // Places of the requests' own keys when every table row is full: no plan has more.
 __host__ __device__ __forceinline__ long long wide_own_most(int R, int own_blocks, int max_pages) {
-  return R * own_blocks * wide_own_span(cdiv((long long)max_pages * kPage, kWideKeys));
+  return (long long)R * own_blocks * wide_own_span(cdiv((long long)max_pages * kPage, kWideKeys));
 }
 // The requests' own places by a plan; none if its end cannot be one. A plan of other
 // lengths or of no lengths at all never leads out of the tables, rows and slots.

@@ -77,7 +77,7 @@ def test_empty_prefix_and_rows_without_keys():
     assert not out[0].any() and torch.isneginf(lse[0]).all() and torch.isneginf(lse[2]).all()
 
 
-@pytest.mark.parametrize("num_ctas", [1, 2, 3, 7, 20, 151, 152])
+@pytest.mark.parametrize("num_ctas", [1, 2, 3, 7, 20, 151, 152, 500])
 @pytest.mark.parametrize("R,k,H,prefix", [(3, 4, 8, 5000), (9, 7, 8, 2500), (5, 1, 64, 1500)])
 def test_any_number_of_ctas(R, k, H, prefix, num_ctas):
     rng = np.random.default_rng(num_ctas)
