@@ -547,36 +547,43 @@ __device__ void softmax(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl
       a.part_lse[first_row + row] = z == 0.f ? -INFINITY : m + __log2f(z);
     wait(&ctl->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
     tc::fence_after_sync();
-    // Through 2 KB of P's place per warp, 16 of its 32 columns of a half at a time:
-    // lane l then stores 16-byte piece l % 4 of rows l / 4, l / 4 + 8, ..., 64 bytes
-    // of a row per four lanes. Piece c of row r lies at c ^ ((r >> 1) & 3).
+    // Through 2 KB of P's place per warp, 16 of its rows of 128 bytes at a time: lane l
+    // then stores 16-byte piece l % 8 of rows l / 8, l / 8 + 4, ..., whole lines. Piece c
+    // of row r lies at c ^ (r & 7).
     float4* const stage = reinterpret_cast<float4*>(smem + kOffP) + (warp - 4) * 128;
-    float* const dst = a.part_o + (first_row + (quarter & 1) * 32 + (lane >> 2)) * kDv + kh * 256 +
-                       col0 + (lane & 3) * 4;
-    const int rows = live - (quarter & 1) * 32 - (lane >> 2);      // of this lane, 8 apart
+    float* const dst = a.part_o + (first_row + (quarter & 1) * 32 + (lane >> 3)) * kDv + kh * 256 +
+                       col0 + (lane & 7) * 4;
+    const int rows = live - (quarter & 1) * 32 - (lane >> 3);      // of this lane, 4 apart
+    if ((quarter & 1) * 32 < live) {               // else: a warp without live rows
 #pragma unroll 1
-    for (int turn = (quarter & 1) * 32 < live ? 0 : 4; turn < 4; ++turn) {
-      // columns 128 (turn / 2) + 16 (turn % 2) ..; none for a warp without live rows
-      uint32_t o[16];
-      tc::tmem_ld16(tmem + lanes + (turn >> 1) * 128 + col0 + (turn & 1) * 16, o);
-      tc::tmem_wait_ld();
+      for (int d = 0; d < 2; ++d) {
+        uint32_t o[32];
+        tc::tmem_ld32(tmem + lanes + d * 128 + col0, o);
+        tc::tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        stage[lane * 4 + (j ^ ((lane >> 1) & 3))] =
-            make_float4(__uint_as_float(o[4 * j]) * inv, __uint_as_float(o[4 * j + 1]) * inv,
-                        __uint_as_float(o[4 * j + 2]) * inv, __uint_as_float(o[4 * j + 3]) * inv);
-      __syncwarp();
-      float4 v[4];
+        for (int pass = 0; pass < 2; ++pass) {
+          if (lane >> 4 == pass) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int r = (lane >> 2) + 8 * u;
-        v[u] = stage[r * 4 + ((lane & 3) ^ ((r >> 1) & 3))];
+            for (int j = 0; j < 8; ++j)
+              stage[(lane & 15) * 8 + (j ^ (lane & 7))] =
+                  make_float4(__uint_as_float(o[4 * j]) * inv, __uint_as_float(o[4 * j + 1]) * inv,
+                              __uint_as_float(o[4 * j + 2]) * inv,
+                              __uint_as_float(o[4 * j + 3]) * inv);
+          }
+          __syncwarp();
+          float4 v[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int r = (lane >> 3) + 4 * u;
+            v[u] = stage[r * 8 + ((lane & 7) ^ (r & 7))];
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (pass * 16 + 4 * u < rows)
+              *reinterpret_cast<float4*>(dst + (pass * 16 + 4 * u) * kDv + d * 128) = v[u];
+          __syncwarp();
+        }
       }
-      float* const at = dst + (turn >> 1) * 128 + (turn & 1) * 16;
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (8 * u < rows) *reinterpret_cast<float4*>(at + u * 8 * kDv) = v[u];
-      __syncwarp();
     }
     soft_sync();                                   // P's place and O are free
     tc::fence_before_sync();
