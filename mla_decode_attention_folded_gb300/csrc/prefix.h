@@ -19,10 +19,10 @@ namespace mlafold {
 
 constexpr int kWideRows = 128;     // query rows per block
 constexpr int kWideKeys = 256;     // keys per tile
-// A piece costs about three tiles' time. Measured with 3, 4, 5, 6 (the merge's later gain
-// left out): 32 x 4 x 8 behind 4k 29.9, 32.7, 33.0, 33.1 us; 64 x 7 x 8 behind 16k 102,
-// 99, 104, 102 us; 24 x 1 x 64 behind 64k 116, 117, 119, 120 us; 128 x 7 x 64 behind 16k
-// 1186, 1178, 1184, 1180 us.
+// A piece costs about three tiles' time. Measured with 2, 3, 4: 32 x 4 x 8 behind 4k 27.8,
+// 29.2, 29.1 us; 64 x 7 x 8 behind 16k 102, 99, 99 us; 24 x 1 x 64 behind 64k 132, 115, 114
+// us; 128 x 7 x 64 behind 16k 1200, 1149, 1148 us; geometric mean over 21 shapes 40.2, 39.3,
+// 39.8 us.
 // A cost of its own for pieces of own keys gains 2-5 % there at 2 and 5, and loses 4 %
 // over 21 shapes.
 constexpr int kWideCost = 3;

@@ -29,9 +29,9 @@
 // running max is lazy (moved when 32 weights of a row sum to more than 2^8, to 2
 // below the tile's); P is computed as if no row moved and once more where one did.
 //
-// With plan and merge: 128 x 7 x 64 behind 16k 1.16 ms, 2.0 PFLOP/s (0.52 of twice
-// the BF16 rate); 24 x 1 x 64 behind 64k 112 us (0.50); 64 x 7 x 8 behind 16k 101 us
-// (0.37); 32 x 4 x 8 behind 4k 27.5 us; 2 x 4 x 8 behind 300 18 us. The second term of
+// With plan and merge: 128 x 7 x 64 behind 16k 1.15 ms, 2.0 PFLOP/s (0.52 of twice
+// the BF16 rate); 24 x 1 x 64 behind 64k 112 us (0.50); 64 x 7 x 8 behind 16k 99 us
+// (0.37); 32 x 4 x 8 behind 4k 29 us; 2 x 4 x 8 behind 300 18 us. The second term of
 // P makes the tensor pipe's work 1.47 times the algorithmic. A tile takes 4,080 cycles
 // against the MMAs' 3,300: from S to PV 2,570 (weights 1,090, vote 390, stores 380)
 // and from PV to the next S 1,300, with two stages to hide them behind. Tried and
