@@ -459,7 +459,8 @@ int32_t mla_query_absorb(const mla_query_shape *shape, const void *q, const void
  *                need not be initialised.
  *   out          [R, k*H, 512] BF16, device, 16-byte aligned: every row is
  *                written; lse [R, k*H] FP32 base-2 or NULL. A row with no keys
- *                at all gets out = 0, lse = -inf.
+ *                at all gets out = 0, lse = -inf; one that meets a NaN gets
+ *                NaN in both.
  *   status       as for mla_folded_decode: MLA_FAULT_PAGE_RANGE,
  *                MLA_FAULT_WORK_ITEM, MLA_FAULT_WAIT_TIMEOUT.
  *   the others   as for mla_folded_decode.

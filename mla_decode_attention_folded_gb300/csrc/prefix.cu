@@ -104,6 +104,9 @@ prefix_merge_kernel(const MergeArgs a) {
   float mx = -INFINITY;
   for (int s = lane; s < n; s += 32) mx = fmaxf(mx, a.part_lse[at(s)]);
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  // fmaxf passes over a NaN LSE: where all others are empty too, mx is still -inf. The
+  // weights then are 2^NaN, not 0: only empty partials weigh nothing.
+  const float base = mx == -INFINITY ? 0.f : mx;
   float4 acc[4];
 #pragma unroll
   for (int v = 0; v < 4; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -113,7 +116,7 @@ prefix_merge_kernel(const MergeArgs a) {
   float z = 0.f;
   for (int c0 = 0; c0 < n; c0 += 32) {
     const float lc = c0 + lane < n ? a.part_lse[at(c0 + lane)] : -INFINITY;
-    const float wc = (mx == -INFINITY || lc == -INFINITY) ? 0.f : ex2(lc - mx);
+    const float wc = lc == -INFINITY ? 0.f : ex2(lc - base);
     z += wc;
     const int cn = min(32, n - c0);
     int s = 0;
@@ -143,7 +146,7 @@ prefix_merge_kernel(const MergeArgs a) {
                        ((uint32_t)f32_to_bf16_bits(acc[v].y * scale) << 16),
                    (uint32_t)f32_to_bf16_bits(acc[v].z * scale) |
                        ((uint32_t)f32_to_bf16_bits(acc[v].w * scale) << 16));
-  if (a.lse && lane == 0) a.lse[row] = z == 0.f ? -INFINITY : mx + __log2f(z);
+  if (a.lse && lane == 0) a.lse[row] = z == 0.f ? -INFINITY : base + __log2f(z);
 }
 
 template <typename... P, typename... A>
