@@ -258,7 +258,8 @@ int32_t mla_uv_combine(const mla_shape *shape, const int32_t *counts, const int3
  * (drafter-attention page, `DraftDcp`: each head's rows are merged over the
  * DCP sources by exp2(lse - max) / sum in FP32 with one BF16 rounding):
  *   w_s = 2^(lse_s - max_s lse_s), out = sum_s w_s out_s / sum_s w_s,
- *   lse = max + log2 sum_s w_s; rows whose sources are all empty get 0, -inf.
+ *   lse = max + log2 sum_s w_s; rows whose sources are all empty get 0, -inf,
+ *   rows with a source whose LSE is NaN get NaN in both.
  *   parts_out [S, rows, 512] BF16, device, 16-byte aligned: each source's out.
  *   parts_lse [S, rows] FP32 base-2 LSE, device.
  *   out [rows, 512] BF16 (16-byte aligned), lse [rows] FP32, device, written

@@ -5,7 +5,8 @@
 // rounding). Here the S sources sit in one device buffer; moving them between
 // GPUs is the caller's transport.
 //   w_s = 2^(lse_s - max_s lse_s), out = sum_s w_s out_s / sum_s w_s,
-//   lse = max + log2 sum_s w_s; rows whose sources are all empty: 0 and -inf.
+//   lse = max + log2 sum_s w_s; rows whose sources are all empty: 0 and -inf; rows
+//   with a source whose LSE is NaN: NaN in both.
 // One warp per row; each lane owns 16 of the 512 dims; lanes hold 32 sources'
 // LSEs at a time and share weights by shuffles.
 #include "checks.h"
@@ -31,13 +32,15 @@ lse_merge_kernel(int S, int rows, const uint16_t* __restrict__ parts_out,
     for (int c0 = 0; c0 < S; c0 += 32)
       if (c0 + lane < S) mx = fmaxf(mx, parts_lse[(long long)(c0 + lane) * rows + row]);
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    // fmaxf passes over NaN: with no finite LSE beside one, mx is -inf.
+    const float base = mx == -INFINITY ? 0.f : mx;
     float acc[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.f;
     float z = 0.f;
     for (int c0 = 0; c0 < S; c0 += 32) {
       const float lc = c0 + lane < S ? parts_lse[(long long)(c0 + lane) * rows + row] : -INFINITY;
-      const float wc = (mx == -INFINITY || lc == -INFINITY) ? 0.f : ex2(lc - mx);
+      const float wc = lc == -INFINITY ? 0.f : ex2(lc - base);
       z += wc;
       const int cn = min(32, S - c0);
       for (int s = 0; s < cn; ++s) {
@@ -53,7 +56,7 @@ lse_merge_kernel(int S, int rows, const uint16_t* __restrict__ parts_out,
       }
     }
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    const float inv = z > 0.f ? 1.f / z : 0.f;
+    const float inv = z > 0.f ? 1.f / z : z;             // NaN stays
     uint32_t pk[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -62,7 +65,7 @@ lse_merge_kernel(int S, int rows, const uint16_t* __restrict__ parts_out,
     uint4* dst = reinterpret_cast<uint4*>(out + row * kDv + lane * 16);
     dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
     dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-    if (lse && lane == 0) lse[row] = z > 0.f ? mx + __log2f(z) : -INFINITY;
+    if (lse && lane == 0) lse[row] = z == 0.f ? -INFINITY : base + __log2f(z);
   }
 }
 
