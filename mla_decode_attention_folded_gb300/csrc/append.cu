@@ -79,12 +79,13 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendArgs a)
     p1 = (uint32_t)x[kDv + 32 + lane] << 16;
   }
 
-  int r, i;
+  int r;
+  long long i;                                        // offsets that are none may lie 2^31 below t
   if (a.cu) {
     r = ragged_request(a.cu, a.R, t, lane);
     const int first = a.cu[r];
     if (t < first || t >= a.cu[r + 1]) return;        // rows of no request
-    i = t - first;
+    i = (long long)t - first;
   } else {
     const int k = a.tokens / a.R;
     r = t / k;
@@ -92,8 +93,8 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendArgs a)
   }
   const int start = a.starts[r];
   if (start < 0) return;                              // a padding request
-  const long long j = (long long)start + i;
-  const long long pos = (a.rope_starts ? (long long)a.rope_starts[r] : start) + i;
+  const long long j = start + i;                      // >= 0, as both are
+  const long long pos = (a.rope_starts ? a.rope_starts[r] : start) + i;
   int page = -1;
   if (j < (long long)a.max_pages * kPage) page = a.block_table[(long long)r * a.max_pages + j / kPage];
   const bool page_ok = page >= 0 && page < a.num_pages, pos_ok = pos >= 0 && pos < a.rope_rows;

@@ -178,6 +178,41 @@ def test_ragged_offsets_out_of_order_stay_in_bounds():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("cu", [(5, 2, 9), (-4, 100, 3), (7, 7, 7), (0, 3, 1), (0, 4, 6), (2, 6, 6),
+                                (-(1 << 31), 6, 6), (2 - (1 << 31), 6, 6), (-(1 << 31), 1, 6),
+                                (0, -(1 << 31), 6), ((1 << 31) - 1, -(1 << 31), 6),
+                                (-1, (1 << 31) - 1, (1 << 31) - 1)])
+def test_ragged_offsets_change_only_their_own_rows(cu):
+    """Whatever the offsets: a token leaves nothing but the cache row of a request whose
+    offsets hold it, and the pages beside the cache's stay. Offsets far below 0 put a
+    token past every table: it is skipped and reported."""
+    starts = (0, 70)
+    x, _, table = _small()
+    around = torch.full((12, 64, 576), 9, dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    mla.kv_append(x, around[4:8], table, i32(starts), angle_table(200).cuda(), 0.05,
+                  cu_tokens=i32(cu), status=status)
+    torch.cuda.synchronize()
+    changed = {tuple(v) for v in (around != 9).any(-1).nonzero().tolist()}
+    may, faults = set(), 0
+    for t in range(6):
+        for r in range(2):
+            if cu[r] <= t < cu[r + 1]:
+                j = starts[r] + t - cu[r]
+                if j < 128:
+                    may.add((4 + 2 * r + j // 64, j % 64))
+                faults |= (mla.FAULT_PAGE_RANGE if j >= 128 else 0) | \
+                    (mla.FAULT_ROPE_RANGE if j >= 200 else 0)
+    assert changed <= may
+    if cu == (0, 4, 6):
+        assert changed == may and len(may) == 6
+    assert int(status.item()) & ~faults == 0
+    if cu[0] < -1000 and cu[1] == 6:              # past its block-table row and the angles
+        assert not changed
+        assert int(status.item()) == mla.FAULT_PAGE_RANGE | mla.FAULT_ROPE_RANGE
+
+
 def test_no_tokens_launch_nothing():
     x, kv, table = _small()
     mla.kv_append(x[:0], kv, table, torch.zeros(2, dtype=torch.int32, device="cuda"),
