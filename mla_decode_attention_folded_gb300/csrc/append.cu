@@ -59,7 +59,8 @@ __device__ __forceinline__ int ragged_request(const int32_t* cu, int R, int t, i
   return lo;
 }
 
-template <bool INTERLEAVED>
+// JOINS: the scale's reciprocal joins the norm's factor (16 products fewer).
+template <bool INTERLEAVED, bool JOINS>
 __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendArgs a) {
   grid_dep_wait();
   grid_dep_launch();
@@ -114,12 +115,16 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendArgs a)
     for (int u = 0; u < 16; ++u) ss += f[u] * f[u];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float rs = rsqrtf(ss * (1.f / kDv) + a.eps) * a.inv_scale;
+    const float n = rsqrtf(ss * (1.f / kDv) + a.eps);
     float w[16];
     bf16x8_to_f32(reinterpret_cast<const uint4*>(a.weight)[lane], w);
     bf16x8_to_f32(reinterpret_cast<const uint4*>(a.weight + 256)[lane], w + 8);
+    const float rs = JOINS ? n * a.inv_scale : n;
 #pragma unroll
     for (int u = 0; u < 16; ++u) f[u] = f[u] * rs * w[u];
+    if (!JOINS)
+#pragma unroll
+      for (int u = 0; u < 16; ++u) f[u] *= a.inv_scale;
   } else {
 #pragma unroll
     for (int u = 0; u < 16; ++u) f[u] *= a.inv_scale;
@@ -195,7 +200,11 @@ extern "C" int32_t mla_kv_append(const mla_append_shape* s, const void* kv_new,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = s->interleaved ? cudaLaunchKernelEx(&cfg, append_kernel<true>, a)
-                                 : cudaLaunchKernelEx(&cfg, append_kernel<false>, a);
+  // With a scale near FP32's ends the norm's factor times its reciprocal could overflow, and
+  // 0 times that be NaN: the products are then apart (24 prompts: 31.9 against 31.5 us).
+  const bool joins = a.inv_scale > 0x1p-40f && a.inv_scale < 0x1p40f;
+  auto* kernel = s->interleaved ? (joins ? append_kernel<true, true> : append_kernel<true, false>)
+                                : (joins ? append_kernel<false, true> : append_kernel<false, false>);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }

@@ -213,6 +213,31 @@ def test_ragged_offsets_change_only_their_own_rows(cu):
         assert int(status.item()) == mla.FAULT_PAGE_RANGE | mla.FAULT_ROPE_RANGE
 
 
+@pytest.mark.parametrize("scale,eps", [(1e-37, 1e-6), (3e-39, 1e-6), (1e-30, 0.0), (1e37, 1e-6)])
+def test_scales_at_the_ends_of_fp32(scale, eps):
+    """A scale whose reciprocal is near FP32's end, beside rows whose norm is far from 1:
+    zeros stay zeros, the rest saturates or vanishes as its exact value does."""
+    x = torch.zeros(3, 576, dtype=torch.bfloat16)
+    x[0, 0], x[0, 1], x[0, 2] = 1e-15, -1e-15, 1e-38
+    x[1, :2] = torch.tensor([1.0, -2e-37])
+    x[2, 512:514] = torch.tensor([3e-38, -1.0])
+    x[2, 0] = 1.0
+    w = torch.ones(512, dtype=torch.bfloat16)
+    w[5] = 0.0
+    kv = torch.full((1, 64, 576), 7, dtype=torch.uint8, device="cuda")
+    i32 = torch.zeros(1, dtype=torch.int32, device="cuda")
+    rope = torch.cat([torch.ones(4, 32), torch.zeros(4, 32)], 1).cuda()       # no turn
+    mla.kv_append(x.cuda(), kv, i32[None], i32, rope, scale, norm_weight=w.cuda(), norm_eps=eps)
+    got = kv[0, :3].cpu().numpy()
+    xs, ws = x.double().numpy(), w.double().numpy()
+    scale = float(np.float32(scale))
+    y = np.stack([st.cache_row(xs[t], ws, float(np.float32(eps)), 0, True, scale) for t in range(3)])
+    # As for the other rows, and the two products before the scale's, each within half of
+    # FP32's smallest step where they are that small.
+    assert_codes(got, y, 2.0 ** -18 * np.abs(y) + 2.0 ** -149 / scale)
+    assert not (got[:, 5] & 0x7F).any()
+
+
 def test_no_tokens_launch_nothing():
     x, kv, table = _small()
     mla.kv_append(x[:0], kv, table, torch.zeros(2, dtype=torch.int32, device="cuda"),
