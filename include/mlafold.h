@@ -462,7 +462,8 @@ int32_t mla_query_absorb(const mla_query_shape *shape, const void *q, const void
  *                written; lse [R, k*H] FP32 base-2 or NULL. A row with no keys
  *                at all gets out = 0, lse = -inf; one that meets a NaN gets
  *                NaN in both.
- *   status       as for mla_folded_decode: MLA_FAULT_PAGE_RANGE,
+ *   status       as for mla_folded_decode: MLA_FAULT_PAGE_RANGE (an entry
+ *                outside [0, num_pages) is read as a page of zeros),
  *                MLA_FAULT_WORK_ITEM, MLA_FAULT_WAIT_TIMEOUT.
  *   the others   as for mla_folded_decode.
  * Numerics as there, except that P's second term is E5M2 (hi + lo is p to 2^-7

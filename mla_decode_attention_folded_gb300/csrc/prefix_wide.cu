@@ -126,30 +126,32 @@ __device__ __forceinline__ bool soft_any(bool pred) {
 
 // ---------------------------------------------------------------- loads
 // The page ids of a piece's tiles, in lanes 0-3 of a warp: asked for a tile ahead,
-// checked when used.
+// checked when used. One outside the cache becomes the first page behind it, which a
+// copy fills with zeros: no stale keys take its place.
 struct Pages {
   const WideArgs& a;
   const int32_t* table = nullptr;
-  int page = 0, end = 0, next = -2, lane;          // page: this lane's of the next tile
+  int page = 0, end = 0, next = 0, lane;           // page: this lane's of the next tile
+  bool there = false;                              // it is one of the keys' pages
   __device__ explicit Pages(const WideArgs& a_) : a(a_), lane(threadIdx.x & 31) {}
-  __device__ int ask() {
-    const int p = page;
+  __device__ void ask() {
+    there = lane < kKeys / kPage && page < end;
+    if (there) next = table[page];
     page += kKeys / kPage;
-    return lane < kKeys / kPage && p < end ? table[p] : -2;      // -2: no such page
   }
   __device__ void begin(const WidePiece& p) {
     table = p.table;
     page = p.tile * (kKeys / kPage) + lane;
     end = (int)cdiv(p.len, kPage);
-    next = ask();
+    ask();
   }
-  __device__ int take(bool more, bool report) {
-    int cur = next;
-    next = more ? ask() : -2;
-    if (cur != -2 && (cur < 0 || cur >= a.num_pages)) {
+  __device__ int take(bool more, bool report) {    // -1: no such page
+    int cur = there ? next : -1;
+    if (there && (cur < 0 || cur >= a.num_pages)) {
       if (report && a.status) atomicOr(a.status, MLA_FAULT_PAGE_RANGE);
-      cur = -1;
+      cur = a.num_pages;
     }
+    if (more) ask();
     return cur;
   }
 };
