@@ -451,10 +451,14 @@ int32_t mla_query_absorb(const mla_query_shape *shape, const void *q, const void
  *                prefix_pages * 64, as more than max_pages * 64 own keys, sets
  *                MLA_FAULT_PAGE_RANGE and is cut off). May change between the
  *                decodes of one plan.
- *   seq_lens     the planned lengths.
- *   plan         of mla_prefix_plan for them. One that is no plan of this shape
- *                sets MLA_FAULT_WORK_ITEM; what the requests get is then
- *                unspecified, but nothing else is read or written.
+ *   seq_lens     [R] int32, device: the requests' own keys. All of them are
+ *                attended to, whatever lengths the plan was made for.
+ *   plan         of mla_prefix_plan, best for these lengths. With fewer tiles of
+ *                256 keys than some request has, the decode cuts its work by
+ *                the lengths itself, which takes longer; so it does with words
+ *                that are no plan of this shape, which set MLA_FAULT_WORK_ITEM.
+ *                Word 0 is where it notes that (-1, else 0): decodes that
+ *                share a plan may overlap if their seq_lens are the same.
  *   workspace    >= mla_prefix_workspace_bytes(shape) bytes, device, 256-byte
  *                aligned; calls that share one must not overlap. Its contents
  *                need not be initialised.
@@ -475,7 +479,7 @@ int32_t mla_prefix_plan(const mla_shape *shape, const int32_t *seq_lens, int32_t
 int32_t mla_prefix_decode(const mla_shape *shape, int32_t prefix_pages, const void *q,
                           const void *kv, const int32_t *prefix_table, const int32_t *prefix_len,
                           const int32_t *block_table, const int32_t *seq_lens, float bmm1_scale,
-                          float bmm2_scale, const int32_t *plan, int32_t plan_len, void *workspace,
+                          float bmm2_scale, int32_t *plan, int32_t plan_len, void *workspace,
                           size_t workspace_bytes, void *out, float *lse, int32_t *status,
                           mla_stream_t stream);
 

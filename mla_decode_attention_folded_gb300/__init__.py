@@ -503,7 +503,8 @@ def prefix_decode(shape: MlaShape, q, kv, prefix_table, prefix_len, block_table,
                   bmm1_scale: float, bmm2_scale: float, plan, workspace, out, lse, status=None,
                   stream=None) -> None:
     """The shared-prefix decode over the plan of prefix_plan for the requests'
-    own lengths (see mla_prefix_decode in include/mlafold.h)."""
+    own lengths; it notes in the plan's first word whether that serves them (see
+    mla_prefix_decode in include/mlafold.h)."""
     _lib.check("mla_prefix_decode", _lib.load().mla_prefix_decode(
         ctypes.byref(shape), prefix_table.numel(), _ptr(q), _ptr(kv), _ptr(prefix_table),
         _ptr(prefix_len), _ptr(block_table), _ptr(seq_lens), float(bmm1_scale), float(bmm2_scale),
@@ -545,7 +546,8 @@ class PrefixMla:
         """out [R, k*H, 512] BF16 and the base-2 lse [R, k*H] (None without
         return_lse) of queries q [R*k, H, 576] over the prefix (prefix_table
         [prefix_pages] and prefix_len [1], int32) and each request's own keys
-        (block_table [R, max_pages], seq_lens [R], the planned lengths)."""
+        (block_table [R, max_pages], seq_lens [R]). All keys of seq_lens are attended
+        to; lengths that need more tiles than the planned ones only take longer."""
         dev = self.places.get_device()
         if dev != torch.cuda.current_device():
             with torch.cuda.device(dev):

@@ -33,8 +33,7 @@ prefix_plan_kernel(const int32_t* __restrict__ seq_lens, int R, int max_pages, i
   grid_dep_wait();
   grid_dep_launch();
   const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
-  const int tiles = i < R ? (int)cdiv(wide_len(seq_lens[i], max_pages), kWideKeys) : 0;
-  int sum = tiles > 0 ? own_blocks * (int)wide_own_span(tiles) : 0;
+  int sum = i < R ? wide_places(wide_len(seq_lens[i], max_pages), own_blocks) : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int t = __shfl_up_sync(0xffffffffu, sum, o);
@@ -50,6 +49,7 @@ prefix_plan_kernel(const int32_t* __restrict__ seq_lens, int R, int max_pages, i
 struct MergeArgs {
   const int32_t* prefix_len;               // [1]
   const int32_t* plan;                     // [R + 1]
+  const int32_t* seq_lens;                 // [R]
   const float* part_o;                     // [slots][128][512]
   const float* part_lse;                   // [slots][128]
   uint16_t* out;                           // [N][512]
@@ -64,12 +64,31 @@ __global__ void __launch_bounds__(kWarps * 32, EARLY ? 2 : 4)
 prefix_merge_kernel(const MergeArgs a) {
   grid_dep_wait();
   grid_dep_launch();
+  __shared__ int s_before, s_all;
   const int r = blockIdx.y, lane = threadIdx.x & 31;
   const int m = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  // The places of the request, and of all: the plan's, unless wide_kernel made its own.
+  int own = r > 0 ? a.plan[r] : 0, own_end = a.plan[r + 1], own_places = a.plan[a.R];
+  if (a.plan[0] != 0) {
+    if (threadIdx.x == 0) s_before = s_all = 0;
+    __syncthreads();
+    const auto places = [&](int i) {
+      return wide_places(wide_len(a.seq_lens[i], a.max_pages), a.own_blocks);
+    };
+    int before = 0, all = 0;
+    for (int i = threadIdx.x; i < a.R; i += kWarps * 32) {
+      all += places(i);
+      if (i < r) before += places(i);
+    }
+    atomicAdd(&s_before, before);
+    atomicAdd(&s_all, all);
+    __syncthreads();
+    own = s_before;
+    own_end = own + places(r);
+    own_places = s_all;
+  }
   if (m >= a.M) return;
   const size_t row = (size_t)r * a.M + m;
-  const int own = a.plan[r], own_end = a.plan[r + 1];
-  const int own_places = wide_own_places(a.plan, a.R, a.own_blocks, a.max_pages);
   const WideLine line(*a.prefix_len, own_places, a.prefix_pages, a.blocks, a.units);
   // The pieces of this row's two segments, in consecutive slots each.
   int n_pre = 0, n_own = 0;
@@ -84,7 +103,7 @@ prefix_merge_kernel(const MergeArgs a) {
     n_pre = pieces(b * (line.prefix_tiles + kWideCost), line.prefix_tiles, b,
                    (int)(row % kWideRows), pre);
   }
-  const int span = wide_span(own, own_end, own_places, a.own_blocks, a.max_pages);
+  const int span = (int)((unsigned)(own_end - own) / (unsigned)a.own_blocks);
   if (span > 0) {
     const int j = m / kWideRows;
     n_own = pieces(line.prefix_places + own + j * span, wide_own_tiles(span),
@@ -221,7 +240,7 @@ extern "C" int32_t mla_prefix_decode(const mla_shape* shape, int32_t prefix_page
                                      const void* kv, const int32_t* prefix_table,
                                      const int32_t* prefix_len, const int32_t* block_table,
                                      const int32_t* seq_lens, float bmm1_scale, float bmm2_scale,
-                                     const int32_t* plan, int32_t plan_len, void* workspace,
+                                     int32_t* plan, int32_t plan_len, void* workspace,
                                      size_t workspace_bytes_given, void* out, float* lse,
                                      int32_t* status, mla_stream_t stream) {
   int st = check_prefix_shape(shape);
@@ -259,12 +278,15 @@ extern "C" int32_t mla_prefix_decode(const mla_shape* shape, int32_t prefix_page
   w.units = wide_units(*shape);
   w.blocks = wide_blocks(*shape);
   w.own_blocks = wide_own_blocks(*shape);
+  w.own_tiles = (int)cdiv((long long)w.max_pages * kPage, kWideKeys);
+  w.own_most = (int)wide_own_most(w.R, w.own_blocks, w.max_pages);
   if (launch_wide(w, static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(kv), cs) !=
       cudaSuccess)
     return MLA_ERR_CUDA;
   MergeArgs m;
   m.prefix_len = prefix_len;
   m.plan = w.plan;
+  m.seq_lens = seq_lens;
   m.part_o = w.part_o;
   m.part_lse = w.part_lse;
   m.out = static_cast<uint16_t*>(out);

@@ -36,13 +36,14 @@ struct WideArgs {
   const int32_t* prefix_len;       // [1]
   const int32_t* block_table;      // [R][max_pages]
   const int32_t* seq_lens;         // [R]
-  const int32_t* plan;             // [R + 1]: first place of each request's segments
+  int32_t* plan;                   // [R + 1]: first place of each request's segments
   float* part_o;                   // [slots][128][512]
   float* part_lse;                 // [slots][128]
   int32_t* status;                 // may be null
   float bmm1_log2;
   long long N;                     // query rows
   int R, M, prefix_pages, max_pages, num_pages, units, blocks, own_blocks;
+  int own_tiles, own_most;         // tiles of a full table row, places when all rows are full
 };
 
 // Keys of a table row of `pages` entries.
@@ -51,6 +52,10 @@ __host__ __device__ __forceinline__ int wide_len(int len, int pages) {
   return len < 0 ? 0 : (int)(len < most ? len : most);
 }
 
+// Tiles of `len` keys.
+__host__ __device__ __forceinline__ int wide_tiles(int len) {
+  return (int)(((unsigned)len + kWideKeys - 1) / kWideKeys);
+}
 // Places of a block with t > 0 tiles of own keys, and back.
 __host__ __device__ __forceinline__ long long wide_own_span(long long t) {
   return t + t / kOwnSlow + kWideCost;
@@ -58,29 +63,39 @@ __host__ __device__ __forceinline__ long long wide_own_span(long long t) {
 __host__ __device__ __forceinline__ int wide_own_tiles(int span) {
   return span - kWideCost - (span - kWideCost) / (kOwnSlow + 1);
 }
+// Places of a request with `len` keys.
+__host__ __device__ __forceinline__ int wide_places(int len, int own_blocks) {
+  const int t = wide_tiles(len);
+  return t > 0 ? own_blocks * (int)wide_own_span(t) : 0;
+}
 // Places of the requests' own keys when every table row is full: no plan has more.
 __host__ __device__ __forceinline__ long long wide_own_most(int R, int own_blocks, int max_pages) {
   return (long long)R * own_blocks * wide_own_span(cdiv((long long)max_pages * kPage, kWideKeys));
 }
-// The requests' own places by a plan; none if its end cannot be one. A plan of other
-// lengths or of no lengths at all never leads out of the tables, rows and slots.
-__device__ __forceinline__ int wide_own_places(const int32_t* plan, int R, int own_blocks,
-                                               int max_pages) {
-  const int own = plan[R];
-  return own >= 0 && own <= wide_own_most(R, own_blocks, max_pages) ? own : 0;
+
+// A plan serves when its words are places of the shape and hold every tile of the lengths at
+// hand: it may be one of other lengths. Each thread of wide_kernel looks at words of its
+// own; where any finds a flaw, the lengths are laid out anew (wide_places), so that no plan
+// loses keys or leads out of the tables, rows and slots. Word 0, the place where the line
+// begins, is 0 where the plan serves and kPlanAnew (or no place at all) where it does not: the
+// merge goes by it.
+enum : int { kPlanNone = 1, kPlanShort = 2 };       // no plan of the shape; too few tiles
+constexpr int kPlanAnew = -1;
+__device__ __forceinline__ int wide_ends_flaw(int begin, int end, int own_most) {
+  return (begin == 0 || begin == kPlanAnew) && end >= 0 && end <= own_most ? 0 : kPlanNone;
 }
-// Places of each block of the request with places [first, end) of `own`: 0 if it has
-// no keys, -1 if that is no request of a plan.
-__device__ __forceinline__ int wide_span(int first, int end, int own, int own_blocks,
-                                         int max_pages) {
-  if (first < 0 || end < first || end > own) return -1;
+// Of a request with `len` keys and places [first, end).
+__device__ __forceinline__ int wide_flaw(int first, int end, int len, int own_blocks,
+                                         int own_tiles) {
+  if ((unsigned)end - (unsigned)first == (unsigned)wide_places(len, own_blocks)) return 0;
+  if (first < 0 || end < first) return kPlanNone;
   const int span = (int)((unsigned)(end - first) / (unsigned)own_blocks);
-  if (span * own_blocks != end - first) return -1;
-  if (span <= kWideCost) return span == 0 ? 0 : -1;
+  if (span * own_blocks != end - first) return kPlanNone;
+  if (span == 0) return kPlanShort;
+  if (span <= kWideCost) return kPlanNone;
   const int tiles = wide_own_tiles(span);
-  return wide_own_span(tiles) == span && tiles <= cdiv((long long)max_pages * kPage, kWideKeys)
-             ? span
-             : -1;
+  if (wide_own_span(tiles) != span || tiles > own_tiles) return kPlanNone;
+  return tiles < wide_tiles(len) ? kPlanShort : 0;
 }
 
 // The whole line, and how it is cut. Places fit 31 bits (the host checks).
@@ -111,19 +126,18 @@ struct WidePiece {
   int len, tile, count;            // keys, first tile, tiles
 };
 
-// The pieces of part `unit`, in order, from the plan and the lengths ([R] each,
+// The pieces of part `unit`, in order, from a plan that serves (word 0 is 0) and the lengths ([R] each,
 // the plan with its end) and the prefix's length as the caller holds them.
 struct WideWalk {
   const WideArgs& a;
   const int32_t* plan;
   const int32_t* lens;
-  int prefix_len, prefix_tiles, prefix_places, own;
+  int prefix_len, prefix_tiles, prefix_places;
   int pos, end, unit, r = 0;
   __device__ WideWalk(const WideArgs& a_, const int32_t* plan_, const int32_t* lens_,
                       int prefix_len_, int unit_)
       : a(a_), plan(plan_), lens(lens_), unit(unit_) {
-    own = wide_own_places(plan_, a_.R, a_.own_blocks, a_.max_pages);
-    const WideLine line(prefix_len_, own, a_.prefix_pages, a_.blocks, a_.units);
+    const WideLine line(prefix_len_, plan_[a_.R], a_.prefix_pages, a_.blocks, a_.units);
     prefix_len = line.prefix_len;
     prefix_tiles = line.prefix_tiles;
     prefix_places = line.prefix_places;
@@ -148,8 +162,7 @@ struct WideWalk {
       } else {
         const int at = pos - prefix_places;
         while (r + 1 < a.R && plan[r + 1] <= at) ++r;
-        const int span = wide_span(plan[r], plan[r + 1], own, a.own_blocks, a.max_pages);
-        if (span <= 0 || plan[r] > at) return false;        // not a plan
+        const int span = (int)((unsigned)(plan[r + 1] - plan[r]) / (unsigned)a.own_blocks);
         const int j = (int)((unsigned)(at - plan[r]) / (unsigned)span);
         tiles = wide_own_tiles(span);
         after = span - tiles;

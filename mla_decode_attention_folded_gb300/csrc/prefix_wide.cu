@@ -644,22 +644,39 @@ wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
   int32_t* lens = plan + kMaxR + 1;
   const int prefix_len = *a.prefix_len;
   bool cut = blockIdx.x == 0 && threadIdx.x == 0 && prefix_len > (long long)a.prefix_pages * kPage;
-  for (int i = threadIdx.x; i <= a.R; i += kThreads) {
-    plan[i] = a.plan[i];
-    if (i < a.R) {
-      const int len = a.seq_lens[i];
-      lens[i] = wide_len(len, a.max_pages);
-      cut |= blockIdx.x == 0 && len > lens[i] && len > 0;
-    }
+  const int begin = a.plan[0];
+  int flaw = threadIdx.x == 0 ? wide_ends_flaw(begin, a.plan[a.R], a.own_most) : 0;
+  for (int i = threadIdx.x; i < a.R; i += kThreads) {
+    const int first = i > 0 ? a.plan[i] : 0, after = a.plan[i + 1], len = a.seq_lens[i];
+    plan[i + 1] = after;
+    lens[i] = wide_len(len, a.max_pages);
+    cut |= blockIdx.x == 0 && len > lens[i] && len > 0;
+    flaw |= wide_flaw(first, after, lens[i], a.own_blocks, a.own_tiles);
   }
+  if (threadIdx.x == 0) plan[0] = 0;
   if (cut && a.status) atomicOr(a.status, MLA_FAULT_PAGE_RANGE);
-  __syncthreads();
-  if (blockIdx.x == 0 && a.status) {
-    const int own = wide_own_places(plan, a.R, a.own_blocks, a.max_pages);
-    bool bad = threadIdx.x == 0 && (plan[0] != 0 || plan[a.R] != own);
-    for (int i = threadIdx.x; i < a.R; i += kThreads)
-      bad |= wide_span(plan[i], plan[i + 1], own, a.own_blocks, a.max_pages) < 0;
-    if (bad) atomicOr(a.status, MLA_FAULT_WORK_ITEM);
+  if ((flaw & kPlanNone) && blockIdx.x == 0 && a.status) atomicOr(a.status, MLA_FAULT_WORK_ITEM);
+  flaw = __syncthreads_or(flaw);
+  // Other CTAs may read the word before or after: 0 and kPlanAnew are one to them. A word
+  // that is neither stays, so that all of them see it.
+  if (blockIdx.x == 0 && threadIdx.x == 0 && begin == (flaw ? 0 : kPlanAnew))
+    a.plan[0] = flaw ? kPlanAnew : 0;
+  if (flaw) {                          // a scan that takes few registers: unrolled, the tiles' loops
+    if (warp == 0) {                   // of the whole kernel took 1 - 2 % longer
+      int sum = 0;
+#pragma unroll 1
+      for (int base = 0; base < a.R; base += 32) {
+        int v = base + lane < a.R ? wide_places(lens[base + lane], a.own_blocks) : 0;
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+          const int t = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += t;
+        }
+        if (base + lane < a.R) plan[base + lane + 1] = sum + v;
+        sum += __shfl_sync(0xffffffffu, v, 31);
+      }
+    }
+    __syncthreads();
   }
   const WideWalk walk(a, plan, lens, prefix_len, (int)(blockIdx.x >> 1));
   if (walk.pos >= walk.end) {
