@@ -516,8 +516,10 @@ class PrefixMla:
     """Decode of a batch of R requests that share a prefix of up to
     prefix_pages pages: plan and workspace of one shape, allocated here and
     reused by every call. ``plan(seq_lens)`` plans the requests' own keys once
-    per step; ``decode`` attends over the prefix and them. Calls on one object
-    share its buffers: they must run in stream order."""
+    per step (the first ``decode`` does so itself where none was planned);
+    ``decode`` attends over the prefix and them. Calls on one object share its
+    buffers: they must run in stream order (``status`` is cleared on the stream
+    that is current when the object is made)."""
 
     def __init__(self, R: int, k: int, H: int, max_pages: int, prefix_pages: int, num_pages: int,
                  device=None, num_ctas: int | None = None):
@@ -529,7 +531,9 @@ class PrefixMla:
         self.max_pages, self.prefix_pages, self.num_pages = max_pages, prefix_pages, num_pages
         self.workspace = torch.empty(prefix_workspace_bytes(self.shape), dtype=torch.uint8,
                                      device=self.device)
-        self.places = torch.zeros(R + 1, dtype=torch.int32, device=self.device)
+        # Not filled: a fill on this stream could come after a plan on another.
+        self.places = torch.empty(R + 1, dtype=torch.int32, device=self.device)
+        self.planned = False
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
 
     def plan(self, seq_lens, stream=None) -> None:
@@ -540,6 +544,7 @@ class PrefixMla:
                 return self.plan(seq_lens, stream)
         _check(dev, "seq_lens", seq_lens, _I32, (self.R,))
         prefix_plan(self.shape, seq_lens, self.places, stream)
+        self.planned = True
 
     def decode(self, q, kv, prefix_table, prefix_len, block_table, seq_lens, bmm1_scale: float,
                bmm2_scale: float, out=None, lse=None, stream=None, return_lse: bool = True):
@@ -570,6 +575,8 @@ class PrefixMla:
             lse = _empty((R, M), torch.float32, q.device, stream)
         else:
             _check(dev, "lse", lse, _F32, (R, M))
+        if not self.planned:
+            self.plan(seq_lens, stream)
         prefix_decode(self.shape, q, kv, prefix_table, prefix_len, block_table, seq_lens,
                       bmm1_scale, bmm2_scale, self.places, self.workspace, out, lse, self.status,
                       stream)

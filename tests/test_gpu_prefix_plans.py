@@ -100,3 +100,39 @@ def test_one_plan_for_a_graph_whose_lengths_grow():
             assert int(eng.status.item()) == 0
             b.seq_lens = torch.tensor(lens, dtype=torch.int32)
             _check(out, lse, b, table, n, str(lens))
+
+
+def test_decode_before_any_plan():
+    """The first decode plans its lengths itself, on its own stream."""
+    b, table, n = prefix_batch((300, 40, 0), 4, 8, 200, seed=65)
+    _decode(_engine(b, table), b, table, n)
+    d = to_device(b)
+    eng, side = _engine(b, table), torch.cuda.Stream()
+    eng.places.fill_(-7)                          # what an allocation may hold
+    plen, pt = torch.tensor([n], dtype=torch.int32, device="cuda"), table.cuda()
+    torch.cuda.synchronize()
+    out, lse = eng.decode(d["q"], d["kv"], pt, plen, d["bt"], d["lens"], *bmm_scales(b), stream=side)
+    side.synchronize()
+    assert int(eng.status.item()) == 0 and eng.planned
+    _check(out, lse, b, table, n)
+
+
+def test_a_new_engine_leaves_no_fill_behind():
+    """A plan on another stream is not overwritten by what the constructor put on its own:
+    that stream is kept busy until after the plan."""
+    b, table, n = prefix_batch((300, 40, 0), 4, 8, 200, seed=66)
+    d = to_device(b)
+    plen, pt = torch.tensor([n], dtype=torch.int32, device="cuda"), table.cuda()
+    side, x = torch.cuda.Stream(), torch.randn(4096, 4096, device="cuda")
+    _engine(b, table).plan(d["lens"], side)       # its memory is there to take afterwards
+    x @ x
+    torch.cuda.synchronize()
+    for _ in range(60):                           # some tens of ms on the current stream
+        x = x @ x * 1e-2
+    eng = _engine(b, table)
+    eng.plan(d["lens"], side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    places = eng.places.tolist()
+    assert places[0] == 0 and places[-1] > places[1] > 0
+    _decode(eng, b, table, n)
