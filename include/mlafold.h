@@ -425,6 +425,17 @@ int32_t mla_query_absorb(const mla_query_shape *shape, const void *q, const void
                          const float *rope, const int32_t *rope_starts, float q_scale, void *out,
                          int32_t *status, mla_stream_t stream);
 
+/* Failure detection, for tests: mla_query_absorb with every pipeline wait bounded
+ * by wait_limit_ns (1 ms .. 2 s; the regular call uses 2 s) and, where withhold
+ * is 1 (else 0), with CTA 0's first weights never loaded, so that a wait runs
+ * out. The CTA then ORs MLA_FAULT_WAIT_TIMEOUT into *status (required here),
+ * stops, lets its copies and MMAs in flight finish, frees its tensor memory and
+ * returns; what it had not written of `out` is unspecified. */
+int32_t mla_query_absorb_wait_test(const mla_query_shape *shape, const void *q, const void *w_uk,
+                                   const float *rope, const int32_t *rope_starts, float q_scale,
+                                   void *out, int32_t *status, int32_t withhold,
+                                   uint64_t wait_limit_ns, mla_stream_t stream);
+
 /* The decode of a batch whose requests all begin with one shared prefix, for
  * mla_shape with groups 0 or 1 (its policy, min_split_tokens and max_splits are
  * not used: the work is cut into equal parts, one per pair of CTAs, num_ctas / 2

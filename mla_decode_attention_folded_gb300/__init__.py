@@ -39,7 +39,7 @@ __all__ = ["MlaShape", "MlaError", "POLICY_BALANCED", "POLICY_UNIFORM", "make_sh
            "folded_decode_wait_test", "tier_plan", "row_copy", "balanced_tiers", "TIERS", "MOVE",
            "FoldedMla", "TieredMla", "fold_factor", "FAULT_WAIT_TIMEOUT", "FAULT_PAGE_RANGE",
            "FAULT_WORK_ITEM", "FAULT_ROPE_RANGE", "library_path", "rope_table", "kv_append",
-           "query_absorb", "prefix_workspace_bytes", "prefix_plan", "prefix_decode",
+           "query_absorb", "query_absorb_wait_test", "prefix_workspace_bytes", "prefix_plan", "prefix_decode",
            "PrefixMla"]
 
 PAGE = 64
@@ -483,6 +483,21 @@ def query_absorb(q, w_uk, rope, rope_starts, q_scale: float, out=None, interleav
         ctypes.byref(shape), _ptr(q), _ptr(w_uk), _ptr(rope), _ptr(rope_starts), float(q_scale),
         _ptr(out), _ptr(status), _stream(stream)))
     return out
+
+
+def query_absorb_wait_test(q, w_uk, rope, rope_starts, q_scale: float, out, status,
+                           wait_limit_ns: int, withhold: bool = True, interleaved: bool = True,
+                           stream=None) -> None:
+    """Failure-detection test hook: query_absorb with every pipeline wait bounded by
+    wait_limit_ns and, with `withhold`, CTA 0's first weights never loaded, so that a
+    wait runs out and MLA_FAULT_WAIT_TIMEOUT is set in `status` (see include/mlafold.h)."""
+    T, H, _ = q.shape
+    R = rope_starts.shape[0]
+    shape = QueryShape(R, T // R, H, rope.shape[0], 1 if interleaved else 0,
+                       q.stride(0) if T > 1 else H * 192, q.stride(1) if H > 1 else 192)
+    _lib.check("mla_query_absorb_wait_test", _lib.load().mla_query_absorb_wait_test(
+        ctypes.byref(shape), _ptr(q), _ptr(w_uk), _ptr(rope), _ptr(rope_starts), float(q_scale),
+        _ptr(out), _ptr(status), 1 if withhold else 0, int(wait_limit_ns), _stream(stream)))
 
 
 def prefix_workspace_bytes(shape: MlaShape) -> int:

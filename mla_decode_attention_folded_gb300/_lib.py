@@ -23,7 +23,8 @@ EXPORTS = ("mla_plan_list_len", "mla_workspace_bytes", "mla_plan_splits",
            "mla_folded_decode", "mla_split_combine", "mla_lse_merge",
            "mla_folded_decode_noalloc", "mla_uv_combine", "mla_folded_decode_wait_test",
            "mla_tier_plan", "mla_row_copy", "mla_kv_append", "mla_query_absorb",
-           "mla_prefix_workspace_bytes", "mla_prefix_plan", "mla_prefix_decode")
+           "mla_query_absorb_wait_test", "mla_prefix_workspace_bytes", "mla_prefix_plan",
+           "mla_prefix_decode")
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -94,6 +95,9 @@ def load() -> ctypes.CDLL:
     lib.mla_kv_append.restype = I32
     lib.mla_query_absorb.argtypes = [ctypes.POINTER(QueryShape), P, P, P, P, F, P, P, P]
     lib.mla_query_absorb.restype = I32
+    lib.mla_query_absorb_wait_test.argtypes = [ctypes.POINTER(QueryShape), P, P, P, P, F, P, P, I32,
+                                               ctypes.c_uint64, P]
+    lib.mla_query_absorb_wait_test.restype = I32
     lib.mla_prefix_workspace_bytes.argtypes = [SP, ctypes.POINTER(SZ)]
     lib.mla_prefix_workspace_bytes.restype = I32
     lib.mla_prefix_plan.argtypes = [SP, P, P, I32, P]

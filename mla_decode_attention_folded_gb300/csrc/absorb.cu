@@ -55,7 +55,6 @@ constexpr int kThreads = 64 + kEpi + kTurn;
 constexpr uint32_t kTmemCols = kAccs * kBand;   // 512
 // BF16 x BF16 -> FP32, A (queries) K-major, B (W_UK) MN-major.
 constexpr uint32_t kIdesc = tc::idesc_bf16_f32(kTok, kBand) | (1u << 16);
-constexpr unsigned long long kTimeoutNs = 2000000000ull;
 
 struct AbsorbCtl {
   uint64_t w_full[kWStages], w_empty[kWStages];   // TMA -> MMA, MMA -> TMA
@@ -78,6 +77,9 @@ struct AbsorbArgs {
   float inv_scale;
   int T, k, H, rope_rows, interleaved;
   int tiles, sets, jobs;         // token tiles, band sets per (head, tile), jobs
+  unsigned long long wait_limit_ns;   // bound of every pipeline wait
+  int withhold_first_copy;            // failure-detection test: CTA 0 never loads its first
+                                      // weights, so one wait must run out
 };
 
 // A box of shared memory -> global; the issuing thread commits and waits for its bulk group.
@@ -90,15 +92,15 @@ __device__ __forceinline__ void store_box(const CUtensorMap* m, const void* src,
       : "memory");
 }
 __device__ __forceinline__ bool ab_wait(uint64_t* bar, uint32_t parity, AbsorbCtl* ctl,
-                                        int32_t* status) {
+                                        const AbsorbArgs& a) {
   if (tc::mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = tc::globaltimer_ns();
   while (true) {
     if (tc::mbar_try_wait(bar, parity)) return true;
     if (*reinterpret_cast<volatile int*>(&ctl->abort_flag)) return false;
-    if (tc::globaltimer_ns() - t0 > kTimeoutNs) {
+    if (tc::globaltimer_ns() - t0 > a.wait_limit_ns) {
       *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
-      if (status) atomicOr(status, MLA_FAULT_WAIT_TIMEOUT);
+      if (a.status) atomicOr(a.status, MLA_FAULT_WAIT_TIMEOUT);
       return false;
     }
   }
@@ -221,10 +223,14 @@ absorb_kernel(const AbsorbArgs a, const __grid_constant__ CUtensorMap tm_q,
     if (lane == 0) {
       bool ok = true;
       uint32_t u = 0, x = 0, uq = 0;
+      auto withheld = [&](uint32_t at) {
+        return a.withhold_first_copy && blockIdx.x == 0 && at == 0;
+      };
       auto load_w = [&](int job, int b, uint32_t at) {
         uint64_t* bar = &ctl->w_full[at % kWStages];
         uint8_t* w = smem + kOffW + (at % kWStages) * kWBytes;
         const int y = head_of(job) * kNope, xb = (band_of(job) + b) * kBand * 2;
+        if (withheld(at)) return;
         tc::mbar_arrive_expect_tx(bar, kWBytes);
         tc::tma_load_2d(w, &tm_w, bar, xb, y);
         tc::tma_load_2d(w + kChunk, &tm_w, bar, xb + 128, y);
@@ -234,7 +240,7 @@ absorb_kernel(const AbsorbArgs a, const __grid_constant__ CUtensorMap tm_q,
       for (int job = blockIdx.x; ok && job < a.jobs; job += gridDim.x, ++x) {
         const int qs = x % kQStages;
         if (x >= kQStages &&
-            !(ok = ab_wait(&ctl->q_empty[qs], (x / kQStages - 1) & 1, ctl, a.status)))
+            !(ok = ab_wait(&ctl->q_empty[qs], (x / kQStages - 1) & 1, ctl, a)))
           break;
         uint8_t* q = smem + kOffQ + qs * kQBytes;
         tc::mbar_arrive_expect_tx(&ctl->q_full[qs], kQBytes);
@@ -243,22 +249,22 @@ absorb_kernel(const AbsorbArgs a, const __grid_constant__ CUtensorMap tm_q,
         uq = x + 1;
         for (int b = 0; b < per; ++b, ++u) {
           if (u >= kWStages &&
-              !(ok = ab_wait(&ctl->w_empty[u % kWStages], (u / kWStages - 1) & 1, ctl, a.status)))
+              !(ok = ab_wait(&ctl->w_empty[u % kWStages], (u / kWStages - 1) & 1, ctl, a)))
             break;
           load_w(job, b, u);
         }
       }
-      if (!ok) {                                   // never leave with copies in flight
-        const unsigned long long t0 = tc::globaltimer_ns();
-        for (uint32_t i = u < kWStages ? 0 : u - kWStages; i < u; ++i)
-          while (!tc::mbar_try_wait(&ctl->w_full[i % kWStages], (i / kWStages) & 1) &&
-                 tc::globaltimer_ns() - t0 < kTimeoutNs) {
-          }
-        for (uint32_t i = uq < kQStages ? 0 : uq - kQStages; i < uq; ++i)
-          while (!tc::mbar_try_wait(&ctl->q_full[i % kQStages], (i / kQStages) & 1) &&
-                 tc::globaltimer_ns() - t0 < kTimeoutNs) {
-          }
-      }
+      // Never leave with copies in flight: another role may have given up a wait, then or
+      // later, whether this one did or not.
+      const unsigned long long t0 = tc::globaltimer_ns();
+      for (uint32_t i = u < kWStages ? 0 : u - kWStages; i < u; ++i)
+        while (!withheld(i) && !tc::mbar_try_wait(&ctl->w_full[i % kWStages], (i / kWStages) & 1) &&
+               tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
+        }
+      for (uint32_t i = uq < kQStages ? 0 : uq - kQStages; i < uq; ++i)
+        while (!tc::mbar_try_wait(&ctl->q_full[i % kQStages], (i / kQStages) & 1) &&
+               tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
+        }
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -266,12 +272,12 @@ absorb_kernel(const AbsorbArgs a, const __grid_constant__ CUtensorMap tm_q,
       uint32_t u = 0, x = 0;
       for (int job = blockIdx.x; ok && job < a.jobs; job += gridDim.x, ++x) {
         const int qs = x % kQStages;
-        if (!(ok = ab_wait(&ctl->q_full[qs], (x / kQStages) & 1, ctl, a.status))) break;
+        if (!(ok = ab_wait(&ctl->q_full[qs], (x / kQStages) & 1, ctl, a))) break;
         const uint32_t q = tc::smem_u32(smem + kOffQ + qs * kQBytes);
         for (int b = 0; b < per; ++b, ++u) {
           const int ws = u % kWStages, ds = u % kAccs;
-          if (!(ok = ab_wait(&ctl->w_full[ws], (u / kWStages) & 1, ctl, a.status))) break;
-          if (u >= kAccs && !(ok = ab_wait(&ctl->d_empty[ds], (u / kAccs - 1) & 1, ctl, a.status)))
+          if (!(ok = ab_wait(&ctl->w_full[ws], (u / kWStages) & 1, ctl, a))) break;
+          if (u >= kAccs && !(ok = ab_wait(&ctl->d_empty[ds], (u / kAccs - 1) & 1, ctl, a)))
             break;
           tc::fence_after_sync();
           const uint32_t w = tc::smem_u32(smem + kOffW + ws * kWBytes);
@@ -290,7 +296,7 @@ absorb_kernel(const AbsorbArgs a, const __grid_constant__ CUtensorMap tm_q,
       }
       tc::mma_commit(&ctl->drain);                 // every MMA done before TMEM is released
       const unsigned long long t0 = tc::globaltimer_ns();
-      while (!tc::mbar_try_wait(&ctl->drain, 0) && tc::globaltimer_ns() - t0 < kTimeoutNs) {
+      while (!tc::mbar_try_wait(&ctl->drain, 0) && tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
       }
     }
   } else if (warp >= 2 + kEpi / 32) {
@@ -306,7 +312,7 @@ absorb_kernel(const AbsorbArgs a, const __grid_constant__ CUtensorMap tm_q,
       const int h = head_of(job), tok0 = tok_of(job);
       for (int b = 0; ok && b < per; ++b, ++u) {
         const int ds = u % kAccs;
-        ok = __all_sync(0xffffffffu, ab_wait(&ctl->d_full[ds], (u / kAccs) & 1, ctl, a.status));
+        ok = __all_sync(0xffffffffu, ab_wait(&ctl->d_full[ds], (u / kAccs) & 1, ctl, a));
         if (!ok) break;
         tc::fence_after_sync();
         uint32_t raw[2][32];
@@ -356,9 +362,13 @@ absorb_kernel(const AbsorbArgs a, const __grid_constant__ CUtensorMap tm_q,
 
 using namespace mlafold;
 
-extern "C" int32_t mla_query_absorb(const mla_query_shape* s, const void* q, const void* w_uk,
-                                    const float* rope, const int32_t* rope_starts, float q_scale,
-                                    void* out, int32_t* status, mla_stream_t stream) {
+namespace {
+
+constexpr unsigned long long kWaitLimitNs = 2000000000ull;   // 2 s
+
+int32_t absorb_impl(const mla_query_shape* s, const void* q, const void* w_uk, const float* rope,
+                    const int32_t* rope_starts, float q_scale, void* out, int32_t* status,
+                    mla_stream_t stream, unsigned long long wait_limit_ns, int withhold) {
   if (!s) return MLA_ERR_NULL;
   if (s->R < 1 || s->k < 1 || s->H < 1 || s->rope_rows < 1 ||
       (s->interleaved != 0 && s->interleaved != 1) || s->token_stride < kNope + kRope ||
@@ -422,6 +432,8 @@ extern "C" int32_t mla_query_absorb(const mla_query_shape* s, const void* q, con
     }
   }
   a.jobs = (int)(tiles * s->H * a.sets);
+  a.wait_limit_ns = wait_limit_ns;
+  a.withhold_first_copy = withhold;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.jobs < sms ? a.jobs : sms));
   cfg.blockDim = dim3(kThreads);
@@ -434,4 +446,24 @@ extern "C" int32_t mla_query_absorb(const mla_query_shape* s, const void* q, con
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, absorb_kernel, a, tq, tw, to);
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" int32_t mla_query_absorb(const mla_query_shape* s, const void* q, const void* w_uk,
+                                    const float* rope, const int32_t* rope_starts, float q_scale,
+                                    void* out, int32_t* status, mla_stream_t stream) {
+  return absorb_impl(s, q, w_uk, rope, rope_starts, q_scale, out, status, stream, kWaitLimitNs, 0);
+}
+
+extern "C" int32_t mla_query_absorb_wait_test(const mla_query_shape* s, const void* q,
+                                              const void* w_uk, const float* rope,
+                                              const int32_t* rope_starts, float q_scale, void* out,
+                                              int32_t* status, int32_t withhold,
+                                              uint64_t wait_limit_ns, mla_stream_t stream) {
+  if (!status) return MLA_ERR_NULL;
+  if (wait_limit_ns < 1000000ull || wait_limit_ns > kWaitLimitNs || (withhold != 0 && withhold != 1))
+    return MLA_ERR_SHAPE;
+  return absorb_impl(s, q, w_uk, rope, rope_starts, q_scale, out, status, stream, wait_limit_ns,
+                     withhold);
 }

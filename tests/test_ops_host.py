@@ -181,3 +181,13 @@ def test_the_decode_profiles_are_of_this_source():
     for name in ("R128_k7_H64_skewed128k", "R32_k4_H8_len1k-8k", "R64_k7_H8_lognormal2k",
                  "R16_k4_H64_len16k-64k"):
         assert bench.profiled_traffic(name) is not None
+
+
+@pytest.mark.parametrize("withhold,limit,status,code", [
+    (0, 999_999, P, SHAPE), (1, 0, P, SHAPE), (1, 2_000_000_001, P, SHAPE), (2, 2_000_000, P, SHAPE),
+    (-1, 2_000_000, P, SHAPE), (1, 2_000_000, None, NULL)])
+def test_absorb_wait_test_refuses(withhold, limit, status, code):
+    """Other pointers are NULL: a working check answers first, and nothing launches."""
+    s = _lib.QueryShape(2, 4, 8, 100, 1, 8 * 192, 192)
+    assert _lib.load().mla_query_absorb_wait_test(ctypes.byref(s), None, None, None, None, 0.1, None,
+                                                  status, withhold, limit, None) == code
