@@ -268,6 +268,7 @@ absorb_kernel(const AbsorbArgs a, const __grid_constant__ CUtensorMap tm_q,
     }
   } else if (warp == 1) {
     if (lane == 0) {
+      grid_dep_wait();       // its waits' limit counts from the end of the preceding kernel
       bool ok = true;
       uint32_t u = 0, x = 0;
       for (int job = blockIdx.x; ok && job < a.jobs; job += gridDim.x, ++x) {

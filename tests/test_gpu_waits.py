@@ -38,3 +38,38 @@ def test_absorb_wait_that_runs_out(R, k, H):
     status.zero_()
     again = mla.query_absorb(*args, status=status)
     assert int(status.item()) == 0 and torch.equal(again, want)
+
+
+def test_absorb_behind_a_kernel_that_outlasts_its_limit():
+    """A decode on one CTA lets its successor start at once and then runs for tens of ms;
+    the absorb's CTAs are on other SMs by then, with 2 ms for any of their waits."""
+    keys = 1 << 23
+    shape = mla.make_shape(1, 4, 8, keys // 64, 1, 1)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.zeros((4, 8, 576), dtype=torch.uint8, device="cuda")
+    kv = torch.zeros((1, 64, 576), dtype=torch.uint8, device="cuda")
+    table, lens = torch.zeros((1, keys // 64), **i32), torch.full((1,), keys, **i32)
+    counts, work = torch.zeros(1, **i32), torch.full((mla.plan_list_len(shape),), -1, **i32)
+    ws = torch.empty(max(mla.workspace_bytes(shape), 256), dtype=torch.uint8, device="cuda")
+    out = torch.empty((1, 32, 512), dtype=torch.bfloat16, device="cuda")
+    lse, status = torch.empty((1, 32), device="cuda"), torch.zeros(2, **i32)
+    args = _absorb_inputs(5, 3, 8)
+    want = mla.query_absorb(*args)
+    got = torch.empty_like(want)
+    mla.plan_splits(shape, lens, counts, work)
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+
+    def decode():
+        mla.folded_decode(shape, q, kv, table, lens, 0.1, 1.0, counts, work, ws, out, lse, status[:1])
+
+    decode()
+    begin.record()
+    decode()
+    end.record()
+    torch.cuda.synchronize()
+    assert begin.elapsed_time(end) > 20.0         # ms: ten times the limit below
+    decode()                                      # no event between the two
+    mla.query_absorb_wait_test(*args, got, status[1:], 2 * MS, withhold=False)
+    torch.cuda.synchronize()
+    assert status.tolist() == [0, 0]
+    assert torch.equal(got, want)
