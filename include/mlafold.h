@@ -494,6 +494,20 @@ int32_t mla_prefix_decode(const mla_shape *shape, int32_t prefix_pages, const vo
                           size_t workspace_bytes, void *out, float *lse, int32_t *status,
                           mla_stream_t stream);
 
+/* Failure detection, for tests: mla_prefix_decode with every pipeline wait bounded
+ * by wait_limit_ns (1 ms .. 2 s; the regular call uses 2 s) and with the first
+ * queries of CTA 0 never loaded, so that waits of its pair run out. The pair then
+ * ORs MLA_FAULT_WAIT_TIMEOUT into *status (required here), stops, lets its copies
+ * and MMAs in flight finish, frees its tensor memory and returns; the rows that
+ * it had a part in are unspecified. The plan and the workspace may be used again. */
+int32_t mla_prefix_decode_wait_test(const mla_shape *shape, int32_t prefix_pages, const void *q,
+                                    const void *kv, const int32_t *prefix_table,
+                                    const int32_t *prefix_len, const int32_t *block_table,
+                                    const int32_t *seq_lens, float bmm1_scale, float bmm2_scale,
+                                    int32_t *plan, int32_t plan_len, void *workspace,
+                                    size_t workspace_bytes, void *out, float *lse, int32_t *status,
+                                    uint64_t wait_limit_ns, mla_stream_t stream);
+
 /* Bits the kernels OR into *status. */
 #define MLA_FAULT_WAIT_TIMEOUT 0x1 /* a pipeline wait gave up; the CTA stopped early */
 #define MLA_FAULT_PAGE_RANGE 0x2   /* a block-table entry was outside [0, num_pages) */

@@ -40,7 +40,7 @@ __all__ = ["MlaShape", "MlaError", "POLICY_BALANCED", "POLICY_UNIFORM", "make_sh
            "FoldedMla", "TieredMla", "fold_factor", "FAULT_WAIT_TIMEOUT", "FAULT_PAGE_RANGE",
            "FAULT_WORK_ITEM", "FAULT_ROPE_RANGE", "library_path", "rope_table", "kv_append",
            "query_absorb", "query_absorb_wait_test", "prefix_workspace_bytes", "prefix_plan", "prefix_decode",
-           "PrefixMla"]
+           "prefix_decode_wait_test", "PrefixMla"]
 
 PAGE = 64
 
@@ -525,6 +525,19 @@ def prefix_decode(shape: MlaShape, q, kv, prefix_table, prefix_len, block_table,
         _ptr(prefix_len), _ptr(block_table), _ptr(seq_lens), float(bmm1_scale), float(bmm2_scale),
         _ptr(plan), plan.numel(), _ptr(workspace), workspace.numel() * workspace.element_size(),
         _ptr(out), _ptr(lse), _ptr(status), _stream(stream)))
+
+
+def prefix_decode_wait_test(shape: MlaShape, q, kv, prefix_table, prefix_len, block_table, seq_lens,
+                            bmm1_scale: float, bmm2_scale: float, plan, workspace, out, lse, status,
+                            wait_limit_ns: int, stream=None) -> None:
+    """Failure-detection test hook: the shared-prefix decode with every pipeline wait
+    bounded by wait_limit_ns and CTA 0's first queries withheld, so that a wait runs out
+    and MLA_FAULT_WAIT_TIMEOUT is set in `status` (see include/mlafold.h)."""
+    _lib.check("mla_prefix_decode_wait_test", _lib.load().mla_prefix_decode_wait_test(
+        ctypes.byref(shape), prefix_table.numel(), _ptr(q), _ptr(kv), _ptr(prefix_table),
+        _ptr(prefix_len), _ptr(block_table), _ptr(seq_lens), float(bmm1_scale), float(bmm2_scale),
+        _ptr(plan), plan.numel(), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _ptr(out), _ptr(lse), _ptr(status), int(wait_limit_ns), _stream(stream)))
 
 
 class PrefixMla:

@@ -24,7 +24,7 @@ EXPORTS = ("mla_plan_list_len", "mla_workspace_bytes", "mla_plan_splits",
            "mla_folded_decode_noalloc", "mla_uv_combine", "mla_folded_decode_wait_test",
            "mla_tier_plan", "mla_row_copy", "mla_kv_append", "mla_query_absorb",
            "mla_query_absorb_wait_test", "mla_prefix_workspace_bytes", "mla_prefix_plan",
-           "mla_prefix_decode")
+           "mla_prefix_decode", "mla_prefix_decode_wait_test")
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -104,6 +104,9 @@ def load() -> ctypes.CDLL:
     lib.mla_prefix_plan.restype = I32
     lib.mla_prefix_decode.argtypes = [SP, I32, P, P, P, P, P, P, F, F, P, I32, P, SZ, P, P, P, P]
     lib.mla_prefix_decode.restype = I32
+    lib.mla_prefix_decode_wait_test.argtypes = [SP, I32, P, P, P, P, P, P, F, F, P, I32, P, SZ, P, P,
+                                                P, ctypes.c_uint64, P]
+    lib.mla_prefix_decode_wait_test.restype = I32
     _lib = lib
     return lib
 

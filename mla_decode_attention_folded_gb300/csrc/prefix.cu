@@ -236,13 +236,15 @@ extern "C" int32_t mla_prefix_plan(const mla_shape* shape, const int32_t* seq_le
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
-extern "C" int32_t mla_prefix_decode(const mla_shape* shape, int32_t prefix_pages, const void* q,
-                                     const void* kv, const int32_t* prefix_table,
-                                     const int32_t* prefix_len, const int32_t* block_table,
-                                     const int32_t* seq_lens, float bmm1_scale, float bmm2_scale,
-                                     int32_t* plan, int32_t plan_len, void* workspace,
-                                     size_t workspace_bytes_given, void* out, float* lse,
-                                     int32_t* status, mla_stream_t stream) {
+namespace {
+
+// test_limit_ns: 0, or the failure-detection test's (WideArgs::wait_limit_ns).
+int32_t decode_impl(const mla_shape* shape, int32_t prefix_pages, const void* q, const void* kv,
+                    const int32_t* prefix_table, const int32_t* prefix_len,
+                    const int32_t* block_table, const int32_t* seq_lens, float bmm1_scale,
+                    float bmm2_scale, int32_t* plan, int32_t plan_len, void* workspace,
+                    size_t workspace_bytes_given, void* out, float* lse, int32_t* status,
+                    mla_stream_t stream, unsigned long long test_limit_ns) {
   int st = check_prefix_shape(shape);
   if (st != MLA_OK) return st;
   if (prefix_pages < 1 || prefix_pages > (1 << 24) || !places_fit(*shape, prefix_pages))
@@ -280,6 +282,7 @@ extern "C" int32_t mla_prefix_decode(const mla_shape* shape, int32_t prefix_page
   w.own_blocks = wide_own_blocks(*shape);
   w.own_tiles = (int)cdiv((long long)w.max_pages * kPage, kWideKeys);
   w.own_most = (int)wide_own_most(w.R, w.own_blocks, w.max_pages);
+  w.wait_limit_ns = test_limit_ns;
   if (launch_wide(w, static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(kv), cs) !=
       cudaSuccess)
     return MLA_ERR_CUDA;
@@ -309,4 +312,31 @@ extern "C" int32_t mla_prefix_decode(const mla_shape* shape, int32_t prefix_page
                 cs, m) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" int32_t mla_prefix_decode(const mla_shape* shape, int32_t prefix_pages, const void* q,
+                                     const void* kv, const int32_t* prefix_table,
+                                     const int32_t* prefix_len, const int32_t* block_table,
+                                     const int32_t* seq_lens, float bmm1_scale, float bmm2_scale,
+                                     int32_t* plan, int32_t plan_len, void* workspace,
+                                     size_t workspace_bytes_given, void* out, float* lse,
+                                     int32_t* status, mla_stream_t stream) {
+  return decode_impl(shape, prefix_pages, q, kv, prefix_table, prefix_len, block_table, seq_lens,
+                     bmm1_scale, bmm2_scale, plan, plan_len, workspace, workspace_bytes_given, out,
+                     lse, status, stream, 0);
+}
+
+extern "C" int32_t mla_prefix_decode_wait_test(
+    const mla_shape* shape, int32_t prefix_pages, const void* q, const void* kv,
+    const int32_t* prefix_table, const int32_t* prefix_len, const int32_t* block_table,
+    const int32_t* seq_lens, float bmm1_scale, float bmm2_scale, int32_t* plan, int32_t plan_len,
+    void* workspace, size_t workspace_bytes_given, void* out, float* lse, int32_t* status,
+    uint64_t wait_limit_ns, mla_stream_t stream) {
+  if (!status) return MLA_ERR_NULL;
+  if (wait_limit_ns < 1000000ull || wait_limit_ns > 2000000000ull) return MLA_ERR_SHAPE;
+  return decode_impl(shape, prefix_pages, q, kv, prefix_table, prefix_len, block_table, seq_lens,
+                     bmm1_scale, bmm2_scale, plan, plan_len, workspace, workspace_bytes_given, out,
+                     lse, status, stream, wait_limit_ns);
 }

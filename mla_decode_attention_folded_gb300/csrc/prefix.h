@@ -44,6 +44,9 @@ struct WideArgs {
   long long N;                     // query rows
   int R, M, prefix_pages, max_pages, num_pages, units, blocks, own_blocks;
   int own_tiles, own_most;         // tiles of a full table row, places when all rows are full
+  // Failure-detection test, where not 0: the bound of every pipeline wait; CTA 0 never loads its
+  // first queries, so that one must run out.
+  unsigned long long wait_limit_ns;
 };
 
 // Keys of a table row of `pages` entries.

@@ -66,7 +66,7 @@ constexpr int kOffP = kOffQ + kQBytes;        // hi of CTA 0's and CTA 1's keys,
 constexpr int kOffCtl = kOffP + 4 * kPChunk;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSCol = 256;                    // S buffers after O's two halves of 128 columns
-constexpr unsigned long long kTimeoutNs = 2000000000ull;
+constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 constexpr uint32_t kIdescS = tc::idesc_e4m3_f32(kRows, kKeys, false, false);
 constexpr uint32_t kIdescHi = tc::idesc_e4m3_f32(kRows, 256, false, true);
 constexpr uint32_t kIdescLo = kIdescHi | (1u << 7);       // A in E5M2
@@ -96,16 +96,23 @@ constexpr int kOffPlan = kOffCtl + (int)((sizeof(WideCtl) + 15) / 16 * 16);
 constexpr int kSmemBytes = kOffPlan + (2 * kMaxR + 1) * 4 + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
+// TEST, through the whole kernel: the instance of the failure-detection test, whose limit is an
+// argument (read in the regular instance, it cost the tiles' loops 1 - 2 %).
+template <bool TEST>
+__device__ __forceinline__ unsigned long long wait_limit(const WideArgs& a) {
+  return TEST ? a.wait_limit_ns : kWaitLimitNs;
+}
+template <bool TEST>
 __device__ __forceinline__ bool w_wait(uint64_t* bar, uint32_t parity, WideCtl* ctl,
-                                       int32_t* status) {
+                                       const WideArgs& a) {
   if (tc::mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = tc::globaltimer_ns();
   while (true) {
     if (tc::mbar_try_wait(bar, parity)) return true;
     if (*reinterpret_cast<volatile int*>(&ctl->abort_flag)) return false;
-    if (tc::globaltimer_ns() - t0 > kTimeoutNs) {
+    if (tc::globaltimer_ns() - t0 > wait_limit<TEST>(a)) {
       *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
-      if (status) atomicOr(status, MLA_FAULT_WAIT_TIMEOUT);
+      if (a.status) atomicOr(a.status, MLA_FAULT_WAIT_TIMEOUT);
       return false;
     }
   }
@@ -160,6 +167,7 @@ struct Pages {
 // which PV is done with it (CTA 0's keys of the first dim half, of the second, CTA
 // 1's keys): each is refilled as it becomes free, so that little is left to load once
 // PV is done.
+template <bool TEST>
 __device__ void load_keys(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl* ctl,
                           uint32_t rank, const CUtensorMap* tm_kv, const CUtensorMap* tm_kvr,
                           const CUtensorMap* tm_q, const CUtensorMap* tm_qr) {
@@ -179,7 +187,8 @@ __device__ void load_keys(const WideArgs& a, WideWalk walk, uint8_t* smem, WideC
         tc::tma_load_2d_pair(q + c * kQChunk, tm_q, q_bar, c * 128, row);
       tc::tma_load_2d_pair(q + 4 * kQChunk, tm_qr, q_bar, 512, row);
     };
-    if (x == 0 && lane == 0) load_q();             // while the first page ids are under way
+    // While the first page ids are under way. Failure-detection test: never, in CTA 0.
+    if (x == 0 && lane == 0 && !(TEST && blockIdx.x == 0)) load_q();
     __syncwarp();
     for (int t = 0; ok && t < piece.count; ++t, ++i) {
       const int st = i & 1;
@@ -193,7 +202,7 @@ __device__ void load_keys(const WideArgs& a, WideWalk walk, uint8_t* smem, WideC
         const uint32_t bar3 = tc::map_rank(&ctl->k_band[st][1], 0);
         const uint32_t live = (p0 >= 0) + (p1 >= 0);
         uint8_t* stage = smem + st * kStageBytes;
-        if (i >= 2) ok = w_wait(&ctl->pv_first[st], ph, ctl, a.status);
+        if (i >= 2) ok = w_wait<TEST>(&ctl->pv_first[st], ph, ctl, a);
         auto band = [&](int c, uint32_t to) {
           for (int h = 0; h < 2; ++h)
             if ((h ? p1 : p0) >= 0)
@@ -211,14 +220,14 @@ __device__ void load_keys(const WideArgs& a, WideWalk walk, uint8_t* smem, WideC
                                    (h ? p1 : p0) * kPage);
         }
         if (ok && t == 0 && x > 0) {
-          ok = w_wait(&ctl->q_empty, (x - 1) & 1, ctl, a.status);
+          ok = w_wait<TEST>(&ctl->q_empty, (x - 1) & 1, ctl, a);
           if (ok) load_q();
         }
-        if (ok && i >= 2) ok = w_wait(&ctl->pv_half[st], ph, ctl, a.status);
+        if (ok && i >= 2) ok = w_wait<TEST>(&ctl->pv_half[st], ph, ctl, a);
         if (ok) band(1, bar);
-        if (ok && i >= 2) ok = w_wait(&ctl->pv_most[st], ph, ctl, a.status);
+        if (ok && i >= 2) ok = w_wait<TEST>(&ctl->pv_most[st], ph, ctl, a);
         if (ok) band(2, bar2);
-        if (ok && i >= 2) ok = w_wait(&ctl->pv_done[st], ph, ctl, a.status);
+        if (ok && i >= 2) ok = w_wait<TEST>(&ctl->pv_done[st], ph, ctl, a);
         if (ok) band(3, bar3);
       }
       ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
@@ -235,6 +244,7 @@ __device__ __forceinline__ bool ragged(const WidePiece& p, int t) {
 // The other CTA's keys of the own value dims, over the bands S is done with. Where
 // the softmax clears V behind the last key, that must have landed here before
 // rank 0 hears of it.
+template <bool TEST>
 __device__ void load_values(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl* ctl,
                             uint32_t rank, const CUtensorMap* tm_kv) {
   const int lane = threadIdx.x & 31;
@@ -251,7 +261,7 @@ __device__ void load_values(const WideArgs& a, WideWalk walk, uint8_t* smem, Wid
       const int p0 = __shfl_sync(0xffffffffu, cur, 2 * other);
       const int p1 = __shfl_sync(0xffffffffu, cur, 2 * other + 1);
       const bool tail = ragged(piece, t);
-      if (lane == 0 && (ok = w_wait(&ctl->s_full[st], (i >> 1) & 1, ctl, a.status))) {
+      if (lane == 0 && (ok = w_wait<TEST>(&ctl->s_full[st], (i >> 1) & 1, ctl, a))) {
         uint8_t* stage = smem + st * kStageBytes;
         const uint32_t there = tc::map_rank(&ctl->v_full[st], 0);
         const uint32_t bar = tail ? tc::map_rank(&ctl->v_tail[st], rank) : there;
@@ -262,7 +272,7 @@ __device__ void load_values(const WideArgs& a, WideWalk walk, uint8_t* smem, Wid
               tc::tma_load_2d_pair(stage + (2 * other + d) * kChunkBytes + h * (kChunkBytes / 2),
                                    tm_kv, bar, (2 * rank + d) * 128, (h ? p1 : p0) * kPage);
         if (tail) {
-          ok = w_wait(&ctl->v_tail[st], (tails >> st) & 1, ctl, a.status);
+          ok = w_wait<TEST>(&ctl->v_tail[st], (tails >> st) & 1, ctl, a);
           tc::remote_arrive(there);
         }
       }
@@ -274,13 +284,15 @@ __device__ void load_values(const WideArgs& a, WideWalk walk, uint8_t* smem, Wid
 
 // ---------------------------------------------------------------- MMAs (rank 0)
 // S and PV are issued by a thread each: neither waits on the other's inputs.
-__device__ __forceinline__ void mma_drain(uint64_t* bar) {
+template <bool TEST>
+__device__ __forceinline__ void mma_drain(uint64_t* bar, const WideArgs& a) {
   tc::mma_commit_pair(bar);                        // every MMA done before TMEM is released
   const unsigned long long t0 = tc::globaltimer_ns();
-  while (!tc::mbar_try_wait(bar, 0) && tc::globaltimer_ns() - t0 < kTimeoutNs) {
+  while (!tc::mbar_try_wait(bar, 0) && tc::globaltimer_ns() - t0 < wait_limit<TEST>(a)) {
   }
 }
 
+template <bool TEST>
 __device__ void issue_s(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl* ctl,
                         uint32_t tmem) {
   const uint32_t s_kv = tc::smem_u32(smem), s_q = tc::smem_u32(smem + kOffQ);
@@ -288,14 +300,14 @@ __device__ void issue_s(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl
   bool ok = true;
   WidePiece piece;
   while (ok && walk.next(piece)) {
-    if (!(ok = w_wait(&ctl->q_full, x & 1, ctl, a.status))) break;     // Q in both CTAs
+    if (!(ok = w_wait<TEST>(&ctl->q_full, x & 1, ctl, a))) break;     // Q in both CTAs
     ++x;
     for (int t = 0; t < piece.count; ++t, ++i) {
       const int st = i & 1;
       // The S buffer of tile i - 2 is free: the bands were refilled after PV had begun,
       // and no P of a tile is written before every thread of its CTA has read its S (the
       // vote). Bands 2 and 3 follow as PV leaves them; the others' MMAs cover their flight.
-      if (!(ok = w_wait(&ctl->k_full[st], (i >> 1) & 1, ctl, a.status))) break;
+      if (!(ok = w_wait<TEST>(&ctl->k_full[st], (i >> 1) & 1, ctl, a))) break;
       tc::fence_after_sync();
       const uint32_t kv = s_kv + st * kStageBytes, d = tmem + kSCol + st * 128;
       auto band = [&](int c) {
@@ -313,7 +325,7 @@ __device__ void issue_s(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl
                         tc::smem_desc(kv + 4 * kChunkBytes + kk * 32, 16, 512, tc::kSw64), kIdescS,
                         true);
       for (int c = 2; c < 4 && ok; ++c) {
-        if (!(ok = w_wait(&ctl->k_band[st][c - 2], (i >> 1) & 1, ctl, a.status))) break;
+        if (!(ok = w_wait<TEST>(&ctl->k_band[st][c - 2], (i >> 1) & 1, ctl, a))) break;
         tc::fence_after_sync();
         band(c);
       }
@@ -322,9 +334,10 @@ __device__ void issue_s(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl
     }
     if (ok) tc::mma_commit_pair(&ctl->q_empty);
   }
-  mma_drain(&ctl->drain[0]);
+  mma_drain<TEST>(&ctl->drain[0], a);
 }
 
+template <bool TEST>
 __device__ void issue_pv(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl* ctl,
                          uint32_t tmem) {
   const uint32_t s_kv = tc::smem_u32(smem), s_p = tc::smem_u32(smem + kOffP);
@@ -334,8 +347,8 @@ __device__ void issue_pv(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCt
   while (ok && walk.next(piece)) {
     for (int t = 0; ok && t < piece.count; ++t, ++i) {
       const int st = i & 1;
-      ok = w_wait(&ctl->v_full[st], (i >> 1) & 1, ctl, a.status) &&
-           w_wait(&ctl->p_full[0], i & 1, ctl, a.status);
+      ok = w_wait<TEST>(&ctl->v_full[st], (i >> 1) & 1, ctl, a) &&
+           w_wait<TEST>(&ctl->p_full[0], i & 1, ctl, a);
       if (!ok) break;
       tc::fence_after_sync();
       const uint32_t kv = s_kv + st * kStageBytes;
@@ -355,7 +368,7 @@ __device__ void issue_pv(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCt
       tc::mma_commit_pair(&ctl->pv_first[st]);
       product(0, 1);
       tc::mma_commit_pair(&ctl->pv_half[st]);
-      if (!(ok = w_wait(&ctl->p_full[1], i & 1, ctl, a.status))) break;
+      if (!(ok = w_wait<TEST>(&ctl->p_full[1], i & 1, ctl, a))) break;
       tc::fence_after_sync();
       product(1, 0);
       tc::mma_commit_pair(&ctl->pv_most[st]);
@@ -363,7 +376,7 @@ __device__ void issue_pv(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCt
       tc::mma_commit_pair(&ctl->pv_done[st]);
     }
   }
-  mma_drain(&ctl->drain[1]);
+  mma_drain<TEST>(&ctl->drain[1], a);
 }
 
 // ---------------------------------------------------------------- softmax
@@ -416,6 +429,7 @@ __device__ __forceinline__ bool weigh(const uint32_t (&raw)[32], float scale, fl
 // four warps of a lane quarter take 32 of its columns each. A thread that gave up
 // a wait goes on through the barriers, so that every thread reaches each of
 // them, until the next vote has all of them leave.
+template <bool TEST>
 __device__ void softmax(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl* ctl,
                         uint32_t tmem, uint32_t rank) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -427,7 +441,7 @@ __device__ void softmax(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl
   uint32_t tails = 0, g = 0;                       // parity of each stage's tails so far; tiles
   bool ok = true;                                  // warp-uniform
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    const bool got = ok && w_wait(bar, parity, ctl, a.status);
+    const bool got = ok && w_wait<TEST>(bar, parity, ctl, a);
     ok = __all_sync(0xffffffffu, got);
   };
   // The eight threads' values of this row, joined.
@@ -592,6 +606,7 @@ __device__ void softmax(const WideArgs& a, WideWalk walk, uint8_t* smem, WideCtl
   }
 }
 
+template <bool TEST>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
             const __grid_constant__ CUtensorMap tm_kvr, const __grid_constant__ CUtensorMap tm_q,
@@ -682,16 +697,16 @@ wide_kernel(const WideArgs a, const __grid_constant__ CUtensorMap tm_kv,
   if (walk.pos >= walk.end) {
     // Nothing for this pair.
   } else if (warp == 0) {
-    load_keys(a, walk, smem, ctl, rank, &tm_kv, &tm_kvr, &tm_q, &tm_qr);
+    load_keys<TEST>(a, walk, smem, ctl, rank, &tm_kv, &tm_kvr, &tm_q, &tm_qr);
   } else if (warp == 3) {
-    load_values(a, walk, smem, ctl, rank, &tm_kv);
+    load_values<TEST>(a, walk, smem, ctl, rank, &tm_kv);
   } else if (warp >= 4) {
-    softmax(a, walk, smem, ctl, tmem, rank);
+    softmax<TEST>(a, walk, smem, ctl, tmem, rank);
   } else if (rank == 0 && lane == 0) {
     if (warp == 1)
-      issue_s(a, walk, smem, ctl, tmem);
+      issue_s<TEST>(a, walk, smem, ctl, tmem);
     else
-      issue_pv(a, walk, smem, ctl, tmem);
+      issue_pv<TEST>(a, walk, smem, ctl, tmem);
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -716,8 +731,10 @@ cudaError_t launch_wide(const WideArgs& a, const uint8_t* q, const uint8_t* kv, 
       !dec::encode(&tq, q, 2, q_dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !dec::encode(&tqr, q, 2, q_dims, str, boxr, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
-  static bool attr_set[64] = {};
-  cudaError_t e = dec::set_smem(wide_kernel, kSmemBytes, attr_set);
+  static bool attr_set[2][64] = {};
+  const bool test = a.wait_limit_ns != 0;
+  auto* kernel = test ? wide_kernel<true> : wide_kernel<false>;
+  cudaError_t e = dec::set_smem(kernel, kSmemBytes, attr_set[test]);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * a.units));
@@ -729,7 +746,7 @@ cudaError_t launch_wide(const WideArgs& a, const uint8_t* q, const uint8_t* kv, 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, wide_kernel, a, tkv, tkvr, tq, tqr);
+  return cudaLaunchKernelEx(&cfg, kernel, a, tkv, tkvr, tq, tqr);
 }
 
 }  // namespace mlafold

@@ -4,7 +4,9 @@ import pytest
 import torch
 
 import mla_decode_attention_folded_gb300 as mla
-from tests.step_util import angle_table
+from tests.gpu_util import bmm_scales, to_device
+from tests.step_util import angle_table, prefix_batch
+from tests.test_gpu_prefix import _check
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +75,32 @@ def test_absorb_behind_a_kernel_that_outlasts_its_limit():
     torch.cuda.synchronize()
     assert status.tolist() == [0, 0]
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("lens,k,H,prefix,num_ctas", [
+    ((100, 300), 4, 8, 600, None),                # a tile or two per pair, most pairs without any
+    ((100, 300), 4, 8, 600, 2),                   # all on the pair that stops
+    ((700, 0, 1500), 3, 64, 3000, 6),             # pieces of several tiles, in three pairs
+    ((5,) * 40, 1, 64, 0, 4),                     # own keys alone, many pieces of one tile
+])
+def test_prefix_wait_that_runs_out(lens, k, H, prefix, num_ctas):
+    """The pair without its first queries stops after 20 ms; the same plan and workspace serve
+    the next call."""
+    b, table, _ = prefix_batch(lens, k, H, max(prefix, 1), seed=72)
+    d = to_device(b)
+    eng = mla.PrefixMla(b.R, k, H, d["bt"].shape[1], table.numel(), d["kv"].shape[0], "cuda",
+                        num_ctas=num_ctas)
+    eng.plan(d["lens"])
+    pt, plen = table.cuda(), torch.tensor([prefix], dtype=torch.int32, device="cuda")
+    bmm1, bmm2 = bmm_scales(b)
+    out = torch.empty((b.R, b.M, 512), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((b.R, b.M), device="cuda")
+    mla.prefix_decode_wait_test(eng.shape, d["q"], d["kv"], pt, plen, d["bt"], d["lens"], bmm1, bmm2,
+                                eng.places, eng.workspace, out, lse, eng.status, 20 * MS)
+    torch.cuda.synchronize()
+    assert int(eng.status.item()) == mla.FAULT_WAIT_TIMEOUT
+    eng.status.zero_()
+    out, lse = eng.decode(d["q"], d["kv"], pt, plen, d["bt"], d["lens"], bmm1, bmm2)
+    torch.cuda.synchronize()
+    assert int(eng.status.item()) == 0
+    _check(out, lse, b, table, prefix)

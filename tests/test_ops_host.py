@@ -191,3 +191,12 @@ def test_absorb_wait_test_refuses(withhold, limit, status, code):
     s = _lib.QueryShape(2, 4, 8, 100, 1, 8 * 192, 192)
     assert _lib.load().mla_query_absorb_wait_test(ctypes.byref(s), None, None, None, None, 0.1, None,
                                                   status, withhold, limit, None) == code
+
+
+@pytest.mark.parametrize("limit,status,code", [(999_999, P, SHAPE), (0, P, SHAPE),
+                                               (2_000_000_001, P, SHAPE), (2_000_000, None, NULL)])
+def test_prefix_wait_test_refuses(limit, status, code):
+    s = _shape()
+    assert _lib.load().mla_prefix_decode_wait_test(
+        ctypes.byref(s), 3, None, None, None, None, None, None, 1.0, 1.0, None, 5, None, 0, None, None,
+        status, limit, None) == code
