@@ -481,9 +481,9 @@ int32_t mla_query_absorb_wait_test(const mla_query_shape *shape, const void *q, 
  *                outside [0, num_pages) is read as a page of zeros),
  *                MLA_FAULT_WORK_ITEM, MLA_FAULT_WAIT_TIMEOUT.
  *   the others   as for mla_folded_decode.
- * Numerics as there, except that P's second term is E5M2 (hi + lo is p to 2^-7
- * relative, down to 2^-13 where p is small) and that all partial results stay
- * FP32 until one rounding to BF16. */
+ * Numerics as there, except that P's second term is E5M2 (hi + lo is p to 2^-8
+ * relative or 2^-14 absolute, where two E4M3 terms give 2^-9 or 2^-10) and that
+ * all partial results stay FP32 until one rounding to BF16. */
 int32_t mla_prefix_workspace_bytes(const mla_shape *shape, size_t *bytes);
 int32_t mla_prefix_plan(const mla_shape *shape, const int32_t *seq_lens, int32_t *plan,
                         int32_t plan_len, mla_stream_t stream);

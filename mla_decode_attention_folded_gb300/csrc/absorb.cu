@@ -19,9 +19,9 @@
 // of four), warp 1 issues the MMAs into four TMEM accumulators, warps 2-9 read them
 // back and store them by TMA, each warp its 32 tokens x 64 dims on its own, from
 // two staging tiles, and warps 10-17 turn the rope dims beside them. 128 x 7 x 64:
-// 12.8 us, 5.0 TB/s (0.74 of the copy rate; a band takes 1,300 cycles, the time in which
+// 12.5 - 12.8 us, 5.0 TB/s (0.74 of the copy rate; a band takes 1,300 cycles, the time in which
 // shared memory, 128 B a cycle, takes in W, feeds A and B to the MMAs, 64 KB, and
-// passes the codes on); 16 x 4 x 64 4.4 us, 64 x 7 x 8 4.0 us, 2 x 4 x 8 3.4 us (one
+// passes the codes on); 16 x 4 x 64 4.2 - 4.4 us, 64 x 7 x 8 3.8 - 4.0 us, 2 x 4 x 8 3.2 - 3.4 us (one
 // band per CTA: latency). Pairs of CTAs (M = 256, N = 256) took 16.5 us, twice the
 // read-back warps 12.6 and more on the small ones.
 #include <cmath>

@@ -9,9 +9,9 @@
 // neighbouring requests share in L2, per token) and by launch latency for
 // decode steps. One warp per token: each lane holds 16 latent dims in
 // registers between the sum of squares (five shuffles) and the stores, so a
-// row is read once; lane p turns plane p. 24 ragged prompts, 101 k tokens: 31.7 us,
-// 5.6 TB/s (0.83 of the copy rate, 0.94 with the angles; issue slots 77 % busy);
-// 128 x 7 tokens 2.3 us, 2 x 4 2.0 us. Warps that step over several tokens with the
+// row is read once; lane p turns plane p. 24 ragged prompts, 101 k tokens: 31.1 - 31.8
+// us, 5.6 TB/s (0.82 of the copy rate, 0.95 with the angles; issue slots 75 % busy);
+// 128 x 7 tokens 2.1 - 2.3 us, 2 x 4 1.9 - 2.2 us. Warps that step over several tokens with the
 // norm's weights in registers were slower (32.7 us: 55 registers). Every value is FP32
 // from load to the one rounding to E4M3 (round to nearest even, saturating), the format
 // the decode reads.

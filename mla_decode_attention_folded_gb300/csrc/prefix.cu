@@ -9,7 +9,8 @@
 // of rows against the prefix's keys and against the requests' own, in equal
 // parts, into FP32 partials; the merge below joins all of a row's partials and
 // rounds once to BF16. The plan is the line of work of prefix.h: one CTA, one
-// thread per request, a scan.
+// thread per request, a scan. Where it does not serve the lengths at hand, wide_kernel
+// and the merge lay them out themselves.
 //
 // The merge is bound by memory: per row, its partials (2 KB each) in, 1 KB out.
 // One warp per row; the lanes hold the partials' LSEs and share weights by
@@ -58,7 +59,7 @@ struct MergeArgs {
   int R, M, prefix_pages, max_pages, units, blocks, own_blocks;
 };
 
-// EARLY: the first two partials are asked for before any LSE is there, at 95 registers.
+// EARLY: the first two partials are asked for before any LSE is there, at 99 registers.
 template <bool EARLY>
 __global__ void __launch_bounds__(kWarps * 32, EARLY ? 2 : 4)
 prefix_merge_kernel(const MergeArgs a) {

@@ -22,13 +22,20 @@ constexpr int kWideKeys = 256;     // keys per tile
 // A piece costs about three tiles' time. Measured with 2, 3, 4: 32 x 4 x 8 behind 4k 27.8,
 // 29.2, 29.1 us; 64 x 7 x 8 behind 16k 102, 99, 99 us; 24 x 1 x 64 behind 64k 132, 115, 114
 // us; 128 x 7 x 64 behind 16k 1200, 1149, 1148 us; geometric mean over 21 shapes 40.2, 39.3,
-// 39.8 us.
+// 39.8 us (the five listed by perf/operators.py and 16 drawn, random.Random(77)); over 35 others
+// (random.Random(101)) 2.2 % and 0.1 % above that for 3.
 // A cost of its own for pieces of own keys gains 2-5 % there at 2 and 5, and loses 4 %
 // over 21 shapes.
 constexpr int kWideCost = 3;
-// A tile of own keys takes about an eighth longer, since they come from HBM where the
-// prefix's come from L2: one place more for every 8. Without, and for every 8, 4: 64 x 7
-// x 8 behind 16k 104, 101, 99 us; 128 x 7 x 64 behind 16k 1164, 1148, 1168 us.
+// A tile of own keys takes about an eighth longer beside a long prefix, since they come from
+// HBM where the prefix's come from L2: one place more for every 8, behind a segment's tiles.
+// Without, and for every 16, 8, 4: 64 x 7 x 8 behind 16k 101, 100, 98, 97 us; 128 x 7 x 64
+// behind 16k 1134, 1123, 1102, 1113 us; 4 x 2 x 8 behind 20k, up to 9k own keys 35.5, 35.2,
+// 34.5, 34.1 us. It costs where nearly all keys are own ones, as the part at a segment's end
+// then has fewer tiles than the others: 44 x 2 x 16 behind 12, up to 10k own keys 58.5, 58.7,
+// 64.5, 65.8 us; 13 x 7 x 64 behind 8, up to 13k 63.6, 63.3, 68.4, 69.3 us. Over 35 shapes
+// drawn by perf/operators.py (random.Random(101)), most of them within 1 %, the geometric mean
+// is 1.1, 0.8, 0, 0.5 % below that for 8.
 constexpr int kOwnSlow = 8;
 
 struct WideArgs {

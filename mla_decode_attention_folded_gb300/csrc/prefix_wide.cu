@@ -25,16 +25,21 @@
 //
 // P enters the product as an E4M3 and an E5M2 term: hi = e4m3(p), lo = e5m2(p - hi).
 // E5M2's range keeps the second term where hi is subnormal (p < 2^-6, absolute step
-// 2^-9), so hi + lo is p to 2^-7 relative down to 2^-13 of absolute error. The
-// running max is lazy (moved when 32 weights of a row sum to more than 2^8, to 2
-// below the tile's); P is computed as if no row moved and once more where one did.
+// 2^-9), so hi + lo is p to 2^-8 relative or 2^-14 absolute. With a second E4M3 term, as in
+// the decode of every request on its own, it is 2^-9 or 2^-10: modelled over 4,096 keys
+// (tests/test_prefix_p_precision.py), outputs of broad rows (values of deviation 0.5) are off
+// by 9e-4 of theirs against 5e-4, those of peaked rows (deviation 1) by 7e-4 against 2 - 3e-3.
+// The running max is lazy (moved when 32 weights of a row sum to more than 2^8, to 2 below
+// the tile's); P is computed as if no row moved and once more where one did.
 //
-// With plan and merge: 128 x 7 x 64 behind 16k 1.15 ms, 2.0 PFLOP/s (0.52 of twice
-// the BF16 rate); 24 x 1 x 64 behind 64k 112 us (0.50); 64 x 7 x 8 behind 16k 99 us
-// (0.37); 32 x 4 x 8 behind 4k 29 us; 2 x 4 x 8 behind 300 18 us. The second term of
-// P makes the tensor pipe's work 1.47 times the algorithmic. A tile takes 4,080 cycles
-// against the MMAs' 3,300: from S to PV 2,570 (weights 1,090, vote 390, stores 380)
-// and from PV to the next S 1,300, with two stages to hide them behind. Tried and
+// With plan and merge: 128 x 7 x 64 behind 16k 1.13 - 1.18 ms from box to box, 2.0 PFLOP/s
+// (0.52 of twice the BF16 rate); 24 x 1 x 64 behind 64k 111 us (0.51); 64 x 7 x 8 behind 16k
+// 99 us (0.37); 32 x 4 x 8 behind 4k 27 - 30 us by its lengths; 2 x 4 x 8 behind 300 18 us. The
+// second term of P makes the tensor pipe's work 1.47 times the algorithmic. A tile takes
+// 4,110 cycles against the MMAs' 3,300: from S to PV 2,380 (weights 1,100, vote 280, wait
+// for P's place 320, stores 490) and from PV to the next band of keys 1,420, with two stages
+// to hide them behind. From a piece's last P to the next piece's first S it takes 11,000:
+// the last PV and the row sums 3,000 - 4,000, partial rows out 6,200. Tried and
 // slower: the softmax in two halves of warps, so that PV begins on the first (by CTA's
 // keys: only two of four schedulers work, 4,385 cycles; by 64 keys of each: 4,397); P
 // written before the vote (112 -> 120 us); barriers per 32 rows (112 -> 116); V of CTA
