@@ -136,8 +136,8 @@ struct WidePiece {
   int len, tile, count;            // keys, first tile, tiles
 };
 
-// The pieces of part `unit`, in order, from a plan that serves (word 0 is 0) and the lengths ([R] each,
-// the plan with its end) and the prefix's length as the caller holds them.
+// The pieces of part `unit`, in order, from a plan that serves (word 0 is 0) and the lengths
+// ([R] each, the plan with its end) and the prefix's length as the caller holds them.
 struct WideWalk {
   const WideArgs& a;
   const int32_t* plan;
