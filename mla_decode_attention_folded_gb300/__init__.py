@@ -39,8 +39,8 @@ __all__ = ["MlaShape", "MlaError", "POLICY_BALANCED", "POLICY_UNIFORM", "make_sh
            "folded_decode_wait_test", "tier_plan", "row_copy", "balanced_tiers", "TIERS", "MOVE",
            "FoldedMla", "TieredMla", "fold_factor", "FAULT_WAIT_TIMEOUT", "FAULT_PAGE_RANGE",
            "FAULT_WORK_ITEM", "FAULT_ROPE_RANGE", "library_path", "rope_table", "kv_append",
-           "query_absorb", "query_absorb_wait_test", "prefix_workspace_bytes", "prefix_plan", "prefix_decode",
-           "prefix_decode_wait_test", "PrefixMla"]
+           "query_absorb", "query_absorb_wait_test", "prefix_workspace_bytes", "prefix_plan",
+           "prefix_decode", "prefix_decode_wait_test", "PrefixMla"]
 
 PAGE = 64
 

@@ -32,7 +32,7 @@
 // The running max is lazy (moved when 32 weights of a row sum to more than 2^8, to 2 below
 // the tile's); P is computed as if no row moved and once more where one did.
 //
-// With plan and merge: 128 x 7 x 64 behind 16k 1.13 - 1.18 ms from box to box, 2.0 PFLOP/s
+// With plan and merge: 128 x 7 x 64 behind 16k 1.13 - 1.18 ms (power cap), 2.0 PFLOP/s
 // (0.52 of twice the BF16 rate); 24 x 1 x 64 behind 64k 111 us (0.51); 64 x 7 x 8 behind 16k
 // 99 us (0.37); 32 x 4 x 8 behind 4k 27 - 30 us by its lengths; 2 x 4 x 8 behind 300 18 us. The
 // second term of P makes the tensor pipe's work 1.47 times the algorithmic. A tile takes

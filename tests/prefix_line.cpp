@@ -27,7 +27,9 @@ int at_case = 0;
 int main(int argc, char** argv) {
   const int cases = argc > 1 ? std::atoi(argv[1]) : 1000;
   std::mt19937 g(1);
-  const auto rnd = [&](int lo, int hi) { return (int)(lo + (long long)(g() % (unsigned)(hi - lo + 1))); };
+  const auto rnd = [&](int lo, int hi) {
+    return (int)(lo + (long long)(g() % (unsigned)(hi - lo + 1)));
+  };
   long pieces = 0, served = 0, unserved = 0, longer = 0;
   for (int t = 1; t < 100000; ++t) CHECK(wide_own_tiles((int)wide_own_span(t)) == t);
   for (at_case = 0; at_case < cases; ++at_case) {
@@ -68,7 +70,8 @@ int main(int argc, char** argv) {
     if (mode >= 7) {                       // a plan of other lengths; 8: of longer ones
       std::vector<int> other(a.R);
       for (int r = 0; r < a.R; ++r)
-        other[r] = wide_len(mode == 8 ? lens[r] + rnd(0, 600) : rnd(0, a.max_pages * kPage), a.max_pages);
+        other[r] = wide_len(mode == 8 ? lens[r] + rnd(0, 600) : rnd(0, a.max_pages * kPage),
+                            a.max_pages);
       lay_out(other);
     }
 
@@ -142,14 +145,17 @@ int main(int argc, char** argv) {
       for (int u = u0; u <= u1; ++u, ++read) CHECK(used.count(u + segment));
     };
     if (line.prefix_tiles > 0)
-      for (int b = 0; b < a.blocks; ++b) take(b * (line.prefix_tiles + kWideCost), line.prefix_tiles, b);
+      for (int b = 0; b < a.blocks; ++b)
+        take(b * (line.prefix_tiles + kWideCost), line.prefix_tiles, b);
     for (int r = 0; r < a.R; ++r) {
       const int span = (plan[r + 1] - plan[r]) / a.own_blocks;
       for (int j = 0; span > 0 && j < a.own_blocks; ++j)
-        take(line.prefix_places + plan[r] + j * span, wide_own_tiles(span), a.blocks + r * a.own_blocks + j);
+        take(line.prefix_places + plan[r] + j * span, wide_own_tiles(span),
+             a.blocks + r * a.own_blocks + j);
     }
     CHECK(read == used.size());
   }
-  std::printf("pieces %ld served %ld of which longer %ld unserved %ld\n", pieces, served, longer, unserved);
+  std::printf("pieces %ld served %ld of which longer %ld unserved %ld\n", pieces, served, longer,
+              unserved);
   return 0;
 }
