@@ -508,6 +508,102 @@ int32_t mla_prefix_decode_wait_test(const mla_shape *shape, int32_t prefix_pages
                                     size_t workspace_bytes, void *out, float *lse, int32_t *status,
                                     uint64_t wait_limit_ns, mla_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Bounding the cache: the attention weight that every cached key got, and the
+ * keys of least weight dropped. Additions of this library.
+ *
+ * Books of a cache: `weights` and `positions`, [R, max_pages * 64], one entry per
+ * slot (key j of request r, in page block_table[r][j / 64], has entry j): the weight
+ * the key has been given so far and the position of its token. */
+
+/* Shape of mla_kv_weigh and mla_kv_evict. All fields are host values. */
+typedef struct {
+  int32_t R;            /* requests, 1 .. 1024                                          */
+  int32_t k;            /* query tokens per request, >= 1 (mla_kv_evict: not used)      */
+  int32_t H;            /* heads, >= 1; M = k*H <= 4096 (mla_kv_evict: not used)        */
+  int32_t page_size;    /* tokens per cache page; must be 64                            */
+  int32_t max_pages;    /* entries per block_table row (row pitch), 1 .. 2^20           */
+  int32_t num_pages;    /* pages in the cache, 1 .. 2^25 - 1                            */
+} mla_cache_shape;
+
+/* After a decode, what each cached key got from the step's M query rows:
+ *   w[r][j] = (j < starts[r] ? decay * w[r][j] : 0)
+ *             + sum_m 2^(bmm1_scale log2(e) q[r][m] . kv[page(r, j)][j % 64] - lse[r][m])
+ * for j < seq_lens[r]; other entries stay as they are. With the LSEs of the decode
+ * of the same queries and keys each row gives 1 in all. (Behind a shared prefix: the
+ * requests' own keys, with the LSEs over both.)
+ *   q            [R*k, H, 576] E4M3, device, 16-byte aligned, as the decode read it.
+ *   kv           [num_pages, 64, 576] E4M3, device, 16-byte aligned.
+ *   block_table  [R, max_pages] int32, device; read at the pages of seq_lens.
+ *   seq_lens     [R] int32, device (negative is read as 0, more than max_pages * 64
+ *                as that).
+ *   lse          [R, k*H] FP32 base-2, device. A row whose LSE is no finite number
+ *                adds nothing.
+ *   bmm1_scale   as for the decode: finite, > 0.
+ *   decay        finite, >= 0: what is left of earlier weights (1: all of them).
+ *   starts       [R] int32, device: slots from here on are new with this step, as in
+ *                mla_kv_append; negative: a padding request, skipped.
+ *   rope_starts  [R] int32, device: the position of the first new key; NULL: starts.
+ *   weights      [R, max_pages * 64] FP32, device, updated.
+ *   positions    [R, max_pages * 64] int32, device, or NULL: entries of new keys are
+ *                written, rope_starts[r] + j - starts[r].
+ *   status       optional int32 device word: MLA_FAULT_PAGE_RANGE (an entry outside
+ *                [0, num_pages) is read as a page of zeros), MLA_FAULT_WAIT_TIMEOUT.
+ * FP8 products, FP32 accumulation, weights and sums; rows are added in a fixed order, so
+ * the same inputs give the same bits. A score that is NaN adds nothing. */
+int32_t mla_kv_weigh(const mla_cache_shape *shape, const void *q, const void *kv,
+                     const int32_t *block_table, const int32_t *seq_lens, const float *lse,
+                     float bmm1_scale, float decay, const int32_t *starts,
+                     const int32_t *rope_starts, float *weights, int32_t *positions,
+                     int32_t *status, mla_stream_t stream);
+
+/* Failure detection, for tests: mla_kv_weigh with every pipeline wait bounded by
+ * wait_limit_ns (1 ms .. 2 s; the regular call uses 2 s) and with CTA 0's first tile of
+ * keys never loaded, so that a wait runs out. The CTA then ORs MLA_FAULT_WAIT_TIMEOUT
+ * into *status (required here), writes no more weights, lets its copies and MMAs in flight
+ * finish, frees its tensor memory and returns. */
+int32_t mla_kv_weigh_wait_test(const mla_cache_shape *shape, const void *q, const void *kv,
+                               const int32_t *block_table, const int32_t *seq_lens,
+                               const float *lse, float bmm1_scale, float decay,
+                               const int32_t *starts, const int32_t *rope_starts, float *weights,
+                               int32_t *positions, int32_t *status, uint64_t wait_limit_ns,
+                               mla_stream_t stream);
+
+/* Keep at most keep[r] keys of every request. First stay the keys held by their
+ * position (below `sinks`, or from the newest position back `recent` ones), then those
+ * of most weight; ties, and held keys beyond keep[r], go to the lower slot; a NaN weighs
+ * less than any number. The new length is min(seq_lens[r], keep[r]): kept keys in slots
+ * from there on move, in order, into the slots before it whose keys are dropped, with
+ * their rows of the cache, weights and positions. Attention does not depend on the
+ * order of keys, so the decode goes on with the new lengths; the pages behind them
+ * are free for others.
+ *   kv           [num_pages, 64, 576] E4M3, device, 16-byte aligned; only rows that
+ *                keys move into are written. No page may belong to two requests.
+ *   block_table  [R, max_pages] int32, device; read at the pages of moved keys.
+ *   seq_lens     [R] int32, device (negative is read as 0, more than max_pages * 64
+ *                as that, with MLA_FAULT_PAGE_RANGE).
+ *   weights      [R, max_pages * 64] FP32, device.
+ *   positions    [R, max_pages * 64] int32, device, or NULL: a key's position is its slot.
+ *                (Once keys have moved it no longer is.)
+ *   keep         [R] int32, device (negative is read as 0).
+ *   recent, sinks >= 0.
+ *   weights_out  [R, max_pages * 64] FP32, device: entries below the new length, and 0 from
+ *                there to the old one; entries behind that stay as they are. May be
+ *                `weights`, else must not overlap it.
+ *   positions_out [R, max_pages * 64] int32, device, in the same way (-1 for 0); NULL where
+ *                positions is. May be `positions`, else must not overlap it.
+ *   lens_out     [R] int32, device: the new lengths. May be seq_lens.
+ *   workspace    >= mla_kv_evict_workspace_bytes(shape) bytes, device, 256-byte aligned; calls
+ *                that share one must not overlap. Its contents need not be initialised.
+ *   status       optional int32 device word: MLA_FAULT_PAGE_RANGE (a moved key's page is
+ *                outside the cache: its row is not copied). */
+int32_t mla_kv_evict_workspace_bytes(const mla_cache_shape *shape, size_t *bytes);
+int32_t mla_kv_evict(const mla_cache_shape *shape, void *kv, const int32_t *block_table,
+                     const int32_t *seq_lens, const float *weights, const int32_t *positions,
+                     const int32_t *keep, int32_t recent, int32_t sinks, float *weights_out,
+                     int32_t *positions_out, int32_t *lens_out, void *workspace,
+                     size_t workspace_bytes, int32_t *status, mla_stream_t stream);
+
 /* Bits the kernels OR into *status. */
 #define MLA_FAULT_WAIT_TIMEOUT 0x1 /* a pipeline wait gave up; the CTA stopped early */
 #define MLA_FAULT_PAGE_RANGE 0x2   /* a block-table entry was outside [0, num_pages) */

@@ -21,6 +21,9 @@ tokens into the paged cache (RMS norm, rotation, E4M3), ``query_absorb(...)``
 makes the decode's queries (W_UK, rotation, E4M3), ``rope_table(rows)`` makes the
 table of angles both read; ``PrefixMla(...)`` decodes a batch whose requests
 share a prefix, reading the prefix's keys once for all of them.
+
+To bound the cache: ``kv_weigh(...)`` adds up the attention weight of every cached
+key after a decode, ``kv_evict(...)`` keeps the keys of most weight.
 """
 from __future__ import annotations
 
@@ -29,7 +32,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import (AppendShape, FAULT_PAGE_RANGE, FAULT_ROPE_RANGE, FAULT_WAIT_TIMEOUT,
+from ._lib import (AppendShape, CacheShape, FAULT_PAGE_RANGE, FAULT_ROPE_RANGE, FAULT_WAIT_TIMEOUT,
                    FAULT_WORK_ITEM, MlaError, MlaShape, POLICY_BALANCED, POLICY_UNIFORM,
                    QueryShape)
 
@@ -40,7 +43,8 @@ __all__ = ["MlaShape", "MlaError", "POLICY_BALANCED", "POLICY_UNIFORM", "make_sh
            "FoldedMla", "TieredMla", "fold_factor", "FAULT_WAIT_TIMEOUT", "FAULT_PAGE_RANGE",
            "FAULT_WORK_ITEM", "FAULT_ROPE_RANGE", "library_path", "rope_table", "kv_append",
            "query_absorb", "query_absorb_wait_test", "prefix_workspace_bytes", "prefix_plan",
-           "prefix_decode", "prefix_decode_wait_test", "PrefixMla"]
+           "prefix_decode", "prefix_decode_wait_test", "PrefixMla", "kv_weigh", "kv_weigh_wait_test",
+           "kv_evict", "kv_evict_workspace_bytes"]
 
 PAGE = 64
 
@@ -609,3 +613,138 @@ class PrefixMla:
                       bmm1_scale, bmm2_scale, self.places, self.workspace, out, lse, self.status,
                       stream)
         return out, lse
+
+
+# ---------------------------------------------------------------- bounding the cache
+def kv_weigh(q, kv, block_table, seq_lens, lse, bmm1_scale: float, weights, starts,
+             decay: float = 1.0, positions=None, rope_starts=None, status=None, stream=None) -> None:
+    """Add to weights [R, max_pages * 64] FP32 (in place) what every cached key got
+    from the k*H query rows of its request in a decode with these queries q
+    [R*k, H, 576], keys and base-2 lse [R, k*H]: earlier weights times decay, plus
+    the sum of 2^(score - lse). Keys at slots from starts[r] on are new: they begin
+    with this step's weight, and positions [R, max_pages * 64] int32 (or None) gets
+    theirs, counted from rope_starts[r] (None: starts). A request with a negative
+    start is skipped. See mla_kv_weigh in include/mlafold.h."""
+    dev = _device("kv", kv, 3)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return kv_weigh(q, kv, block_table, seq_lens, lse, bmm1_scale, weights, starts, decay,
+                            positions, rope_starts, status, stream)
+    shape = _weigh_shape(dev, q, kv, block_table, seq_lens, lse, weights, starts, positions,
+                         rope_starts, status)
+    _lib.check("mla_kv_weigh", _lib.load().mla_kv_weigh(
+        ctypes.byref(shape), _ptr(q), _ptr(kv), _ptr(block_table), _ptr(seq_lens), _ptr(lse),
+        float(bmm1_scale), float(decay), _ptr(starts), _ptr(rope_starts), _ptr(weights),
+        _ptr(positions), _ptr(status), _stream(stream)))
+
+
+def _weigh_shape(dev, q, kv, block_table, seq_lens, lse, weights, starts, positions, rope_starts,
+                 status) -> CacheShape:
+    _device("block_table", block_table, 2)
+    _device("q", q, 3)
+    (R, max_pages), (T, H, _), pages = block_table.shape, q.shape, kv.shape[0]
+    if R < 1 or T < R or T % R:
+        raise ValueError(f"{T} tokens are not a positive multiple of {R} requests")
+    k, slots = T // R, max_pages * PAGE
+    _check(dev, "q", q, _E4M3, (T, H, 576))
+    _check(dev, "kv", kv, _E4M3, (pages, PAGE, 576))
+    _check(dev, "block_table", block_table, _I32, (R, max_pages))
+    _check(dev, "seq_lens", seq_lens, _I32, (R,))
+    _check(dev, "lse", lse, _F32, (R, k * H))
+    _check(dev, "weights", weights, _F32, (R, slots))
+    _check(dev, "starts", starts, _I32, (R,))
+    if positions is not None:
+        _check(dev, "positions", positions, _I32, (R, slots))
+    if rope_starts is not None:
+        _check(dev, "rope_starts", rope_starts, _I32, (R,))
+    if status is not None:
+        _check(dev, "status", status, _I32, (1,))
+    return CacheShape(R, k, H, PAGE, max_pages, pages)
+
+
+def kv_weigh_wait_test(q, kv, block_table, seq_lens, lse, bmm1_scale: float, weights, starts, status,
+                       wait_limit_ns: int, decay: float = 1.0, positions=None, rope_starts=None,
+                       stream=None) -> None:
+    """Failure-detection test hook: kv_weigh with every pipeline wait bounded by
+    wait_limit_ns and CTA 0's first keys withheld, so that a wait runs out and
+    MLA_FAULT_WAIT_TIMEOUT is set in `status` (see include/mlafold.h)."""
+    shape = _weigh_shape(_device("kv", kv, 3), q, kv, block_table, seq_lens, lse, weights, starts,
+                         positions, rope_starts, status)
+    _lib.check("mla_kv_weigh_wait_test", _lib.load().mla_kv_weigh_wait_test(
+        ctypes.byref(shape), _ptr(q), _ptr(kv), _ptr(block_table), _ptr(seq_lens), _ptr(lse),
+        float(bmm1_scale), float(decay), _ptr(starts), _ptr(rope_starts), _ptr(weights),
+        _ptr(positions), _ptr(status), int(wait_limit_ns), _stream(stream)))
+
+
+def kv_evict_workspace_bytes(R: int, max_pages: int, num_pages: int = 1) -> int:
+    out = ctypes.c_size_t(0)
+    _lib.check("mla_kv_evict_workspace_bytes", _lib.load().mla_kv_evict_workspace_bytes(
+        ctypes.byref(CacheShape(R, 1, 1, PAGE, max_pages, num_pages)), ctypes.byref(out)))
+    return out.value
+
+
+def kv_evict(kv, block_table, seq_lens, weights, keep, positions=None, recent: int = 0,
+             sinks: int = 0, weights_out=None, positions_out=None, lens_out=None, workspace=None,
+             status=None, stream=None):
+    """Keep at most keep[r] keys of every request of the paged cache kv
+    [pages, 64, 576]: those of positions below `sinks`, the `recent` newest, then
+    those of most weight (ties: the lower slot). Kept keys behind the new length
+    move into slots of dropped ones, with their weights and positions
+    [R, max_pages * 64] (positions None: a key's position is its slot). Returns
+    the new lengths [R] int32. weights_out and positions_out may be the inputs, which
+    is the default; lens_out may be seq_lens. `workspace`: uint8, at least
+    kv_evict_workspace_bytes (None: allocated for the call). See mla_kv_evict in
+    include/mlafold.h."""
+    dev = _device("kv", kv, 3)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return kv_evict(kv, block_table, seq_lens, weights, keep, positions, recent, sinks,
+                            weights_out, positions_out, lens_out, workspace, status, stream)
+    _device("block_table", block_table, 2)
+    (R, max_pages), pages = block_table.shape, kv.shape[0]
+    slots = (R, max_pages * PAGE)
+    _check(dev, "kv", kv, _E4M3, (pages, PAGE, 576))
+    _check(dev, "block_table", block_table, _I32, (R, max_pages))
+    _check(dev, "seq_lens", seq_lens, _I32, (R,))
+    _check(dev, "weights", weights, _F32, slots)
+    _check(dev, "keep", keep, _I32, (R,))
+    if weights_out is None:
+        weights_out = weights
+    else:
+        _check(dev, "weights_out", weights_out, _F32, slots)
+        _apart("weights_out", weights_out, weights)
+    if positions is not None:
+        _check(dev, "positions", positions, _I32, slots)
+        if positions_out is None:
+            positions_out = positions
+        else:
+            _check(dev, "positions_out", positions_out, _I32, slots)
+            _apart("positions_out", positions_out, positions)
+    elif positions_out is not None:
+        raise ValueError("positions_out without positions")
+    if status is not None:
+        _check(dev, "status", status, _I32, (1,))
+    if lens_out is None:
+        lens_out = _empty((R,), torch.int32, kv.device, stream)
+    else:
+        _check(dev, "lens_out", lens_out, _I32, (R,))
+    shape = CacheShape(R, 1, 1, PAGE, max_pages, pages)
+    if workspace is None:
+        need = kv_evict_workspace_bytes(R, max_pages)
+        workspace = _empty((need,), torch.uint8, kv.device, stream)
+    else:
+        _check(dev, "workspace", workspace, (torch.uint8,), workspace.shape)
+    _lib.check("mla_kv_evict", _lib.load().mla_kv_evict(
+        ctypes.byref(shape), _ptr(kv), _ptr(block_table), _ptr(seq_lens), _ptr(weights),
+        _ptr(positions), _ptr(keep), int(recent), int(sinks), _ptr(weights_out),
+        _ptr(positions_out), _ptr(lens_out), _ptr(workspace), workspace.numel(), _ptr(status),
+        _stream(stream)))
+    return lens_out
+
+
+def _apart(name: str, t, other) -> None:
+    """`t` is `other` itself, or shares no memory with it (both contiguous)."""
+    a, b = t.data_ptr(), other.data_ptr()
+    if a != b and a < b + other.numel() * other.element_size() and \
+            b < a + t.numel() * t.element_size():
+        raise ValueError(f"{name} overlaps its input")

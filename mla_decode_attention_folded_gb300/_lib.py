@@ -24,7 +24,8 @@ EXPORTS = ("mla_plan_list_len", "mla_workspace_bytes", "mla_plan_splits",
            "mla_folded_decode_noalloc", "mla_uv_combine", "mla_folded_decode_wait_test",
            "mla_tier_plan", "mla_row_copy", "mla_kv_append", "mla_query_absorb",
            "mla_query_absorb_wait_test", "mla_prefix_workspace_bytes", "mla_prefix_plan",
-           "mla_prefix_decode", "mla_prefix_decode_wait_test")
+           "mla_prefix_decode", "mla_prefix_decode_wait_test", "mla_kv_weigh",
+           "mla_kv_weigh_wait_test", "mla_kv_evict_workspace_bytes", "mla_kv_evict")
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -47,6 +48,12 @@ class QueryShape(ctypes.Structure):
     _fields_ = [("R", ctypes.c_int32), ("k", ctypes.c_int32), ("H", ctypes.c_int32),
                 ("rope_rows", ctypes.c_int32), ("interleaved", ctypes.c_int32),
                 ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class CacheShape(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int32), ("k", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32)]
 
 
 class MlaError(RuntimeError):
@@ -107,6 +114,16 @@ def load() -> ctypes.CDLL:
     lib.mla_prefix_decode_wait_test.argtypes = [SP, I32, P, P, P, P, P, P, F, F, P, I32, P, SZ, P, P,
                                                 P, ctypes.c_uint64, P]
     lib.mla_prefix_decode_wait_test.restype = I32
+    CP = ctypes.POINTER(CacheShape)
+    lib.mla_kv_weigh.argtypes = [CP, P, P, P, P, P, F, F, P, P, P, P, P, P]
+    lib.mla_kv_weigh.restype = I32
+    lib.mla_kv_weigh_wait_test.argtypes = [CP, P, P, P, P, P, F, F, P, P, P, P, P, ctypes.c_uint64,
+                                           P]
+    lib.mla_kv_weigh_wait_test.restype = I32
+    lib.mla_kv_evict_workspace_bytes.argtypes = [CP, ctypes.POINTER(SZ)]
+    lib.mla_kv_evict_workspace_bytes.restype = I32
+    lib.mla_kv_evict.argtypes = [CP, P, P, P, P, P, P, I32, I32, P, P, P, P, SZ, P, P]
+    lib.mla_kv_evict.restype = I32
     _lib = lib
     return lib
 

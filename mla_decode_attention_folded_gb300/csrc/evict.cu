@@ -1,0 +1,442 @@
+// Eviction from the paged latent cache by accumulated attention weight.
+//
+// Of a request's n keys the `keep` first in this order stay: keys held by their
+// position (below `sinks`, or among the `recent` newest), then by weight from
+// the largest, ties to the lower slot; NaN counts as less than any weight. Attention
+// does not depend on the order of its keys, so the keys that stay behind slot
+// `keep` move into the slots of dropped ones, the i-th of them into the i-th such
+// slot, and nothing else moves: the fewest rows that can be read and written, every
+// source behind `keep` and every target before it, so no two copies touch the same row.
+//
+// Bound by HBM for large evictions (16 B per key, 1,152 B per moved key) and by latency for
+// a step's few keys. Two launches: a cluster per request orders its keys (32-bit codes
+// that sort as the rule does, held in shared memory; the keep-th largest by three digits
+// of histograms, joined over the cluster; places by ordered counts) and lists the moves;
+// then all SMs copy the listed rows, 9 threads a row.
+#include <climits>
+
+#include "checks.h"
+#include "internal.h"
+#include "pair.cuh"
+#include "ptx.cuh"
+
+namespace mlafold {
+namespace {
+
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kBins = 2048;                      // 11 + 11 + 10 bits
+constexpr int kMaxCluster = 16;
+constexpr int kCached = 40960;                   // keys a CTA holds in shared memory (160 KB)
+constexpr uint32_t kHeld = 0xFFFFFFFFu;          // above the code of any weight
+
+struct EvictArgs {
+  uint8_t* kv;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const float* weights;
+  const int32_t* positions;      // may be null: a key's position is its slot
+  const int32_t* keep;
+  float* weights_out;
+  int32_t* positions_out;        // null where positions is
+  int32_t* lens_out;
+  int32_t* moves;                // [R][cap][2]: from, to
+  int32_t* count;                // [R]
+  int32_t* status;
+  long long cap;
+  int R, max_pages, num_pages, recent, sinks, cluster, chunk;
+};
+
+// A code that sorts as the weights do (-0 as 0, NaN lowest), below kHeld.
+__device__ __forceinline__ uint32_t weight_code(float w) {
+  const uint32_t b = __float_as_uint(w + 0.f);
+  if ((b << 1) > 0xFF000000u) return 0u;
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+__device__ __forceinline__ uint32_t ld_rank(const void* p, int rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(tc::map_rank(p, rank)) : "memory");
+  return v;
+}
+
+struct Shared {
+  uint32_t hist[3][kBins];
+  unsigned long long sums[kWarps];
+  uint32_t found, rest;          // the digit that holds the wanted place, places left in it
+  int top;                       // newest position of this CTA's keys
+  uint32_t equal, holes, movers; // this CTA's counts
+};
+
+__device__ __forceinline__ void join(int cluster) {
+  if (cluster > 1) tc::cluster_sync();
+  else __syncthreads();
+}
+
+// Exclusive sum over the block's threads; `total` gets the whole.
+__device__ __forceinline__ unsigned long long scan(unsigned long long v, unsigned long long* sums,
+                                                   unsigned long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned long long s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long u = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += u;
+  }
+  if (lane == 31) sums[warp] = s;
+  __syncthreads();
+  if (warp == 0) {
+    unsigned long long w = sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long u = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += u;
+    }
+    sums[lane] = w;
+  }
+  __syncthreads();
+  total = sums[kWarps - 1];
+  const unsigned long long before = warp ? sums[warp - 1] : 0;
+  __syncthreads();
+  return before + s - v;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictArgs a) {
+  extern __shared__ uint32_t codes[];            // this CTA's codes, where they fit
+  __shared__ Shared sh;
+  const int rank = a.cluster > 1 ? (int)tc::cluster_rank() : 0;
+  const int r = blockIdx.x / a.cluster, tid = threadIdx.x;
+  for (int i = tid; i < 3 * kBins; i += kThreads) sh.hist[i / kBins][i % kBins] = 0;
+  if (tid == 0) {
+    sh.top = INT_MIN;
+    sh.equal = sh.holes = sh.movers = 0;
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+  long long n_ = a.seq_lens[r];
+  if (n_ > (long long)a.max_pages * kPage) {
+    n_ = (long long)a.max_pages * kPage;
+    if (a.status && tid == 0 && rank == 0) atomicOr(a.status, MLA_FAULT_PAGE_RANGE);
+  }
+  const int n = (int)(n_ > 0 ? n_ : 0), keep = max(a.keep[r], 0);
+  const size_t row = (size_t)r * a.max_pages * kPage;
+  const float* w = a.weights + row;
+  const int32_t* p = a.positions ? a.positions + row : nullptr;
+  float* wo = a.weights_out + row;
+  int32_t* po = a.positions ? a.positions_out + row : nullptr;
+  const bool copies_w = wo != w, copies_p = p && po != p;
+  // This CTA's slots, and this thread's among them: runs in order, of odd length, so that the
+  // threads' places in shared memory lie in different banks.
+  const int each = (int)cdiv(n, a.cluster);
+  const int first = min(rank * each, n), len = min(each, n - first);
+  const int run = (int)cdiv(len, kThreads) | 1;
+  const int b0 = min(tid * run, len), b1 = min(b0 + run, len);
+
+  join(a.cluster);                               // every CTA of the cluster has read seq_lens
+  if (rank == 0 && tid == 0) a.lens_out[r] = min(n, keep);
+  if (n <= keep) {                               // nothing to drop
+    for (int i = first + tid; i < first + len; i += kThreads) {
+      if (copies_w) wo[i] = w[i];
+      if (copies_p) po[i] = p[i];
+    }
+    if (rank == 0 && tid == 0) a.count[r] = 0;
+    return;
+  }
+
+  long long newest = LLONG_MAX;                  // positions from here on are held
+  if (a.recent > 0) {
+    int top = n - 1;
+    if (p) {
+      int mine = INT_MIN;
+      for (int i = first + tid; i < first + len; i += kThreads) mine = max(mine, p[i]);
+      mine = __reduce_max_sync(0xffffffffu, mine);
+      if ((tid & 31) == 0) atomicMax(&sh.top, mine);
+      join(a.cluster);
+      top = sh.top;
+      for (int c = 0; c < a.cluster && a.cluster > 1; ++c) top = max(top, (int)ld_rank(&sh.top, c));
+    }
+    newest = (long long)top + 1 - a.recent;
+  }
+  const bool cached = len <= a.chunk;
+  auto make = [&](int i) {                       // the code of this CTA's i-th slot
+    const int pos = p ? p[first + i] : first + i;
+    if (pos < a.sinks || pos >= newest) return kHeld;
+    return weight_code(w[first + i]);
+  };
+  auto code = [&](int i) { return cached ? codes[i] : make(i); };
+
+  // The keep-th largest code, digit by digit, and how many of its equals stay.
+  uint32_t want = keep, found = 0;
+  if (keep > 0) {
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+      for (int i = tid; i < len; i += kThreads) {
+        uint32_t c;
+        if (pass == 0) {
+          c = make(i);
+          if (cached) codes[i] = c;
+        } else {
+          c = code(i);
+          if (c >> (shift + bits) != found >> (shift + bits)) continue;
+        }
+        atomicAdd(&sh.hist[pass][(c >> shift) & ((1 << bits) - 1)], 1u);
+      }
+      join(a.cluster);
+      // Digits from the largest down, two to a thread.
+      const int hi = kBins - 1 - 2 * tid;
+      uint32_t h[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        h[u] = 0;
+        if (a.cluster == 1) h[u] = sh.hist[pass][hi - u];
+        else
+          for (int c = 0; c < a.cluster; ++c) h[u] += ld_rank(&sh.hist[pass][hi - u], c);
+      }
+      unsigned long long total;
+      const uint32_t above = (uint32_t)scan(h[0] + h[1], sh.sums, total);
+      if (above < want && want <= above + h[0] + h[1]) {
+        const bool second = above + h[0] < want;
+        sh.found = hi - (second ? 1 : 0);
+        sh.rest = want - above - (second ? h[0] : 0);
+      }
+      __syncthreads();
+      found |= sh.found << shift;
+      want = sh.rest;
+      __syncthreads();
+    }
+  } else {
+    found = kHeld;                               // no code is larger, and no equal stays
+  }
+
+  // Equals stay in the order of their slots.
+  uint32_t equal = 0;
+  for (int i = b0; i < b1; ++i) equal += (keep > 0 ? code(i) : make(i)) == found;
+  unsigned long long total;
+  uint32_t eq = (uint32_t)scan(equal, sh.sums, total);
+  if (tid == 0) sh.equal = (uint32_t)total;
+  join(a.cluster);
+  for (int c = 0; c < rank; ++c) eq += ld_rank(&sh.equal, c);
+  // A dropped key's slot before `keep` is a hole; a kept key behind it moves.
+  uint32_t holes = 0, movers = 0, e = eq;
+  for (int i = b0; i < b1; ++i) {
+    const uint32_t c = keep > 0 ? code(i) : make(i);
+    const bool stays = c > found || (c == found && e++ < want);
+    if (first + i < keep) holes += !stays;
+    else movers += stays;
+  }
+  const unsigned long long at = scan((unsigned long long)holes << 32 | movers, sh.sums, total);
+  if (tid == 0) {
+    sh.holes = (uint32_t)(total >> 32);
+    sh.movers = (uint32_t)total;
+  }
+  join(a.cluster);
+  uint32_t hole = (uint32_t)(at >> 32), mover = (uint32_t)at, all = (uint32_t)total;
+  if (a.cluster > 1) {
+    all = 0;
+    for (int c = 0; c < a.cluster; ++c) {
+      const uint32_t m = ld_rank(&sh.movers, c);
+      all += m;
+      if (c < rank) {
+        mover += m;
+        hole += ld_rank(&sh.holes, c);
+      }
+    }
+  }
+  int32_t* list = a.moves + (size_t)r * a.cap * 2;
+  for (int i = b0; i < b1; ++i) {
+    const uint32_t c = keep > 0 ? code(i) : make(i);
+    const bool stays = c > found || (c == found && eq++ < want);
+    const int slot = first + i;
+    if (slot < keep) {
+      if (!stays) list[2 * (size_t)hole++ + 1] = slot;
+      else {
+        if (copies_w) wo[slot] = w[slot];
+        if (copies_p) po[slot] = p[slot];
+      }
+    } else if (stays) {
+      list[2 * (size_t)mover++] = slot;
+    } else {
+      wo[slot] = 0.f;
+      if (p) po[slot] = -1;
+    }
+  }
+  if (rank == 0 && tid == 0) a.count[r] = (int)all;
+  if (a.cluster > 1) tc::cluster_sync();         // no CTA leaves while others read its counts
+}
+
+// The listed rows with their weights and positions: 9 threads a row, 64 bytes each.
+constexpr int kRowThreads = kDqk / 64, kRows = 28, kMoveThreads = 256;
+
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
+  __shared__ long long before[kMaxR + 1];
+  __shared__ long long sums[kMoveThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dep_wait();
+  grid_dep_launch();
+  long long base = 0;                            // the moves of the requests before each
+  for (int r0 = 0; r0 < a.R; r0 += kMoveThreads) {
+    const long long v = r0 + tid < a.R ? a.count[r0 + tid] : 0;
+    long long s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += u;
+    }
+    if (lane == 31) sums[warp] = s;
+    __syncthreads();
+    long long add = base;
+    for (int i = 0; i < warp; ++i) add += sums[i];
+    if (r0 + tid < a.R) before[r0 + tid] = add + s - v;
+    for (int i = 0; i < kMoveThreads / 32; ++i) base += sums[i];
+    __syncthreads();
+  }
+  if (tid == 0) before[a.R] = base;
+  __syncthreads();
+  const int group = tid / kRowThreads, part = tid % kRowThreads;
+  if (group >= kRows) return;
+  for (long long m = (long long)blockIdx.x * kRows + group; m < base; m += (long long)gridDim.x * kRows) {
+    int lo = 0, hi = a.R;                        // before[lo] <= m < before[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before[mid] <= m) lo = mid;
+      else hi = mid;
+    }
+    const int2 mv = reinterpret_cast<const int2*>(a.moves + (size_t)lo * a.cap * 2)[m - before[lo]];
+    const int32_t* table = a.block_table + (size_t)lo * a.max_pages;
+    const int pf = table[mv.x / kPage], pt = table[mv.y / kPage];
+    const bool ok = pf >= 0 && pf < a.num_pages && pt >= 0 && pt < a.num_pages;
+    if (ok) {
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.kv + ((size_t)pf * kPage + mv.x % kPage) * kDqk) + part;
+      uint4* dst = reinterpret_cast<uint4*>(
+          a.kv + ((size_t)pt * kPage + mv.y % kPage) * kDqk) + part;
+      uint4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = src[u * kRowThreads];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) dst[u * kRowThreads] = v[u];
+    }
+    if (part == 0) {
+      if (!ok && a.status) atomicOr(a.status, MLA_FAULT_PAGE_RANGE);
+      const size_t row = (size_t)lo * a.max_pages * kPage;
+      const float w = a.weights[row + mv.x];
+      a.weights_out[row + mv.y] = w;
+      a.weights_out[row + mv.x] = 0.f;
+      if (a.positions) {
+        const int32_t p = a.positions[row + mv.x];
+        a.positions_out[row + mv.y] = p;
+        a.positions_out[row + mv.x] = -1;
+      }
+    }
+  }
+}
+
+int check_evict(const mla_cache_shape* s) {
+  if (!s) return MLA_ERR_NULL;
+  if (s->page_size != kPage) return MLA_ERR_UNSUPPORTED;
+  if (s->R < 1 || s->R > kMaxR || s->max_pages < 1 || s->max_pages > (1 << 20) ||
+      s->num_pages < 1 || s->num_pages >= (1 << 25))
+    return MLA_ERR_SHAPE;
+  return MLA_OK;
+}
+size_t list_bytes(const mla_cache_shape* s) {
+  return align256((size_t)s->R * s->max_pages * (kPage / 2) * 8);
+}
+
+}  // namespace
+}  // namespace mlafold
+
+using namespace mlafold;
+
+extern "C" int32_t mla_kv_evict_workspace_bytes(const mla_cache_shape* s, size_t* bytes) {
+  const int st = check_evict(s);
+  if (st != MLA_OK) return st;
+  if (!bytes) return MLA_ERR_NULL;
+  *bytes = list_bytes(s) + align256((size_t)s->R * 4);
+  return MLA_OK;
+}
+
+extern "C" int32_t mla_kv_evict(const mla_cache_shape* s, void* kv, const int32_t* block_table,
+                                const int32_t* seq_lens, const float* weights,
+                                const int32_t* positions, const int32_t* keep, int32_t recent,
+                                int32_t sinks, float* weights_out, int32_t* positions_out,
+                                int32_t* lens_out, void* workspace, size_t workspace_bytes_given,
+                                int32_t* status, mla_stream_t stream) {
+  int st = check_evict(s);
+  if (st != MLA_OK) return st;
+  if (recent < 0 || sinks < 0) return MLA_ERR_SHAPE;
+  if (!kv || !block_table || !seq_lens || !weights || !keep || !weights_out || !lens_out ||
+      !workspace || (positions != nullptr) != (positions_out != nullptr))
+    return MLA_ERR_NULL;
+  if (!aligned(kv, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(weights, 4) ||
+      !aligned(positions, 4) || !aligned(keep, 4) || !aligned(weights_out, 4) ||
+      !aligned(positions_out, 4) || !aligned(lens_out, 4) || !aligned(workspace, 256) ||
+      !aligned(status, 4))
+    return MLA_ERR_ALIGN;
+  const size_t lists = list_bytes(s);
+  if (workspace_bytes_given < lists + align256((size_t)s->R * 4)) return MLA_ERR_WORKSPACE;
+  if ((st = check_device()) != MLA_OK) return st;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return MLA_ERR_CUDA;
+
+  EvictArgs a;
+  a.kv = static_cast<uint8_t*>(kv);
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.weights = weights;
+  a.positions = positions;
+  a.keep = keep;
+  a.weights_out = weights_out;
+  a.positions_out = positions_out;
+  a.lens_out = lens_out;
+  a.moves = static_cast<int32_t*>(workspace);
+  a.count = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + lists);
+  a.status = status;
+  a.cap = (long long)s->max_pages * (kPage / 2);
+  a.R = s->R;
+  a.max_pages = s->max_pages;
+  a.num_pages = s->num_pages;
+  a.recent = recent;
+  a.sinks = sinks;
+  // CTAs per request: as many as have 4,096 slots each, up to the cluster's limit and as
+  // long as the batch's CTAs fit on the SMs.
+  const long long slots = (long long)s->max_pages * kPage;
+  a.cluster = 1;
+  while (a.cluster < kMaxCluster && slots > 4096ll * a.cluster && s->R * a.cluster * 2 <= sms)
+    a.cluster *= 2;
+  const long long each = cdiv(slots, a.cluster);
+  a.chunk = (int)(each <= kCached ? each : 0);
+  static bool attr_set[64] = {};
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kCached * 4) != cudaSuccess ||
+        cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                             1) != cudaSuccess)
+      return MLA_ERR_CUDA;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(s->R * a.cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)a.chunk * 4;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)a.cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, evict_select_kernel, a) != cudaSuccess) return MLA_ERR_CUDA;
+  // At most half of a request's keys move.
+  const long long most = (long long)s->R * a.cap;
+  const long long grid = cdiv(most, kRows);
+  cfg.gridDim = dim3((unsigned)(grid < 8ll * sms ? grid : 8ll * sms));
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, evict_move_kernel, a) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}

@@ -1,0 +1,463 @@
+// Attention weight per cached key, summed over a decode step's query rows.
+//
+//   w[r][j] = decay w[r][j] + sum over the request's M rows of 2^(x[m][j] - lse[r][m]),
+//   x[m][j] = bmm1 log2(e) q[r][m] . kv[page(r, j)][j % 64]
+//
+// The LSEs come from the decode, so one pass over the keys is enough: a tile of 128 keys
+// is the MMA's M and up to 128 query rows its N, the 576 dims its K (18 FP8 MMAs), and
+// a thread that owns a key reads the key's scores from its TMEM lane, takes their
+// exponentials and adds them up in FP32 without a shuffle. Rows beyond 128 follow as further
+// blocks over the same tiles (from L2, eight tiles at a time), in order: no atomics, the
+// same sums every time.
+//
+// Bound by HBM up to some 100 rows (576 B a key), by the FP8 tensor pipe beyond. All
+// tiles of the batch are one line, cut into equal runs, one per CTA: keys need no
+// joining, so a cut costs nothing.
+#include <cmath>
+
+#include "checks.h"
+#include "decode_common.cuh"
+#include "formats.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+#include "tc.cuh"
+
+namespace mlafold {
+namespace {
+
+constexpr int kTile = 128;                       // keys per tile: the MMA's M
+constexpr int kMaxRows = 128;                    // rows per block: its N, a multiple of 32
+constexpr int kRun = 8;                          // tiles that a row block goes over
+constexpr int kStages = 2, kBufs = 4;            // tiles in flight, score buffers in TMEM
+constexpr int kChunk = kTile * 128, kStageBytes = kTile * kDqk;
+constexpr int kOffQ = kStages * kStageBytes;
+constexpr int kOffSums = kOffQ + kMaxRows * kDqk;
+constexpr int kSum = 256;                        // summing threads: two per key
+constexpr int kThreads = 64 + kSum;
+constexpr unsigned long long kWaitLimitNs = 2000000000ull;   // 2 s
+
+struct WeighCtl {
+  uint64_t kv_full[kStages], kv_empty[kStages];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[kBufs], s_empty[kBufs];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  int first_r, first_tile;                       // where this CTA's run begins
+  long long total;                               // tiles of the batch
+};
+constexpr int kOffNeg = kOffSums + kRun * 2 * kTile * 4;   // -lse of a block's rows, two buffers
+constexpr int kOffCtl = kOffNeg + 2 * kMaxRows * 4;
+constexpr int kSmemBytes = kOffCtl + (int)sizeof(WeighCtl) + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+struct WeighArgs {
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* starts;
+  const int32_t* rope_starts;    // may be null: starts
+  const float* lse;              // [R][M]
+  float* weights;                // [R][max_pages 64]
+  int32_t* positions;            // may be null
+  int32_t* status;
+  float scale_log2, decay;
+  int R, M, max_pages, num_pages;
+  int rows, blocks;              // rows per block, blocks per request
+  unsigned long long wait_limit_ns;
+  int withhold;                  // failure-detection test: CTA 0 never loads its first tile
+};
+
+__device__ __forceinline__ bool wg_wait(uint64_t* bar, uint32_t parity, WeighCtl* ctl,
+                                        const WeighArgs& a) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = tc::globaltimer_ns();
+  while (true) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    if (*reinterpret_cast<volatile int*>(&ctl->abort_flag)) return false;
+    if (tc::globaltimer_ns() - t0 > a.wait_limit_ns) {
+      *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
+      if (a.status) atomicOr(a.status, MLA_FAULT_WAIT_TIMEOUT);
+      return false;
+    }
+  }
+}
+// The keys of request r that are weighed.
+__device__ __forceinline__ int weigh_len(const WeighArgs& a, int r) {
+  const long long n = a.starts[r] < 0 ? 0 : a.seq_lens[r], most = (long long)a.max_pages * kPage;
+  return (int)(n < 0 ? 0 : n < most ? n : most);
+}
+// A CTA's tiles as groups: up to kRun tiles of one request.
+struct Walk {
+  int r, tile, tiles, len;       // request, its next tile, tiles of the group, its keys
+  long long left;                // tiles of the CTA's run from here on
+  __device__ __forceinline__ bool next(const WeighArgs& a) {
+    tile += tiles;
+    left -= tiles;
+    if (left <= 0) return false;
+    while (tile >= (int)cdiv(len, kTile)) {
+      tile = 0;
+      if (++r >= a.R) return false;
+      len = weigh_len(a, r);
+    }
+    const long long rest = cdiv(len, kTile) - tile;
+    tiles = (int)min(min(rest, left), (long long)kRun);
+    return true;
+  }
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+weigh_kernel(const WeighArgs a, const __grid_constant__ CUtensorMap tm_kv,
+             const __grid_constant__ CUtensorMap tm_kvr, const __grid_constant__ CUtensorMap tm_q,
+             const __grid_constant__ CUtensorMap tm_qr) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  WeighCtl* ctl = reinterpret_cast<WeighCtl*>(smem + kOffCtl);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      tc::mbar_init(&ctl->kv_full[i], 1);
+      tc::mbar_init(&ctl->kv_empty[i], 1);
+    }
+    tc::mbar_init(&ctl->q_full, 1);
+    tc::mbar_init(&ctl->q_empty, 1);
+    for (int i = 0; i < kBufs; ++i) {
+      tc::mbar_init(&ctl->s_full[i], 1);
+      tc::mbar_init(&ctl->s_empty[i], kSum);
+    }
+    tc::mbar_init(&ctl->drain, 1);
+    ctl->abort_flag = 0;
+    tc::fence_barrier_init();
+    tc::prefetch_tmap(&tm_kv);
+    tc::prefetch_tmap(&tm_kvr);
+    tc::prefetch_tmap(&tm_q);
+    tc::prefetch_tmap(&tm_qr);
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(&ctl->tmem_base, kBufs * kMaxRows);
+    tc::tmem_relinquish();
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+  // The line of tiles: warp 0 sums the requests' tiles, 32 at a time, and finds where the
+  // run of this CTA begins.
+  if (warp == 0) {
+    long long total = 0;
+    for (int r0 = 0; r0 < a.R; r0 += 32)
+      total += r0 + lane < a.R ? cdiv(weigh_len(a, r0 + lane), kTile) : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    const long long begin = cdiv(total * blockIdx.x, gridDim.x);
+    long long before = 0;
+    int fr = a.R, ft = 0;
+    for (int r0 = 0; r0 < a.R && fr == a.R; r0 += 32) {
+      const long long v = r0 + lane < a.R ? cdiv(weigh_len(a, r0 + lane), kTile) : 0;
+      long long s = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += u;
+      }
+      const unsigned m = __ballot_sync(0xffffffffu, before + s > begin);
+      if (m) {
+        const int l = __ffs(m) - 1;
+        fr = r0 + l;
+        ft = (int)(begin - before - __shfl_sync(0xffffffffu, s - v, l));
+      }
+      before += __shfl_sync(0xffffffffu, s, 31);
+    }
+    if (lane == 0) {
+      ctl->total = total;
+      ctl->first_r = fr;
+      ctl->first_tile = ft;
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = ctl->tmem_base;
+  Walk w;
+  w.r = ctl->first_r;
+  w.tile = ctl->first_tile;
+  w.tiles = 0;
+  w.left = cdiv(ctl->total * (blockIdx.x + 1), gridDim.x) - cdiv(ctl->total * blockIdx.x, gridDim.x);
+  w.len = w.r < a.R ? weigh_len(a, w.r) : 0;
+  const int qchunk = a.rows * 128;
+
+  if (warp == 0) {
+    // Copies: a block's queries, then the group's tiles, block after block.
+    uint32_t g = 0, x = 0;
+    bool ok = true;
+    auto wait0 = [&](uint64_t* bar, uint32_t parity) {
+      int v = 1;
+      if (lane == 0) v = wg_wait(bar, parity, ctl, a) ? 1 : 0;
+      return __shfl_sync(0xffffffffu, v, 0) != 0;
+    };
+    const bool withheld = a.withhold && blockIdx.x == 0;
+    while (ok && w.next(a)) {
+      // Page ids of the group: lane i has its i-th page; one outside the cache is read behind
+      // the cache's end, where the copy fills in zeros.
+      const int page = w.tile * (kTile / kPage) + lane;
+      int id = a.num_pages;
+      if (lane < 2 * w.tiles && page < (int)cdiv(w.len, kPage)) {
+        id = a.block_table[(size_t)w.r * a.max_pages + page];
+        if (id < 0 || id >= a.num_pages) {
+          if (a.status) atomicOr(a.status, MLA_FAULT_PAGE_RANGE);
+          id = a.num_pages;
+        }
+      }
+      for (int b = 0; ok && b < a.blocks; ++b, ++x) {
+        if (x > 0 && !(ok = wait0(&ctl->q_empty, (x - 1) & 1))) break;
+        if (lane == 0) {
+          uint8_t* q = smem + kOffQ;
+          const int row = w.r * a.M + b * a.rows;
+          tc::mbar_arrive_expect_tx(&ctl->q_full, a.rows * kDqk);
+          for (int c = 0; c < 4; ++c)
+            tc::tma_load_2d(q + c * qchunk, &tm_q, &ctl->q_full, c * 128, row);
+          tc::tma_load_2d(q + 4 * qchunk, &tm_qr, &ctl->q_full, kDv, row);
+        }
+        for (int t = 0; t < w.tiles; ++t, ++g) {
+          const int st = g % kStages;
+          if (g >= kStages && !(ok = wait0(&ctl->kv_empty[st], (g / kStages - 1) & 1))) break;
+          const int p0 = __shfl_sync(0xffffffffu, id, 2 * t), p1 = __shfl_sync(0xffffffffu, id, 2 * t + 1);
+          const int pages = (w.tile + t) * kTile + kPage < w.len ? 2 : 1;
+          if (lane == 0 && !(withheld && g == 0)) {
+            uint8_t* s = smem + st * kStageBytes;
+            tc::mbar_arrive_expect_tx(&ctl->kv_full[st], pages * kPage * kDqk);
+            for (int h = 0; h < pages; ++h) {
+              const int row = (h ? p1 : p0) * kPage;
+              for (int c = 0; c < 4; ++c)
+                tc::tma_load_2d(s + c * kChunk + h * (kChunk / 2), &tm_kv, &ctl->kv_full[st], c * 128,
+                                row);
+              tc::tma_load_2d(s + 4 * kChunk + h * kPage * 64, &tm_kvr, &ctl->kv_full[st], kDv, row);
+            }
+          }
+        }
+      }
+    }
+    // Never leave with copies in flight: another role may have given up a wait.
+    if (lane == 0) {
+      const unsigned long long t0 = tc::globaltimer_ns();
+      for (uint32_t i = g < kStages ? 0 : g - kStages; i < g; ++i)
+        while (!(withheld && i == 0) && !tc::mbar_try_wait(&ctl->kv_full[i % kStages], (i / kStages) & 1) &&
+               tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
+        }
+      while (x > 0 && !tc::mbar_try_wait(&ctl->q_full, (x - 1) & 1) &&
+             tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      bool ok = true;
+      uint32_t g = 0, x = 0;
+      const uint32_t idesc = tc::idesc_e4m3_f32(kTile, a.rows, false, false);
+      const uint32_t q = tc::smem_u32(smem + kOffQ);
+      while (ok && w.next(a)) {
+        for (int b = 0; ok && b < a.blocks; ++b, ++x) {
+          if (!(ok = wg_wait(&ctl->q_full, x & 1, ctl, a))) break;
+          for (int t = 0; t < w.tiles; ++t, ++g) {
+            const int st = g % kStages, bf = g % kBufs;
+            if (!(ok = wg_wait(&ctl->kv_full[st], (g / kStages) & 1, ctl, a))) break;
+            if (g >= kBufs && !(ok = wg_wait(&ctl->s_empty[bf], (g / kBufs - 1) & 1, ctl, a))) break;
+            tc::fence_after_sync();
+            const uint32_t s = tc::smem_u32(smem + st * kStageBytes), d = tmem + bf * kMaxRows;
+#pragma unroll
+            for (int kk = 0; kk < 16; ++kk)
+              tc::mma_e4m3(d, tc::smem_desc(s + (kk >> 2) * kChunk + (kk & 3) * 32, 16, 1024, tc::kSw128),
+                           tc::smem_desc(q + (kk >> 2) * qchunk + (kk & 3) * 32, 16, 1024, tc::kSw128),
+                           idesc, kk != 0);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+              tc::mma_e4m3(d, tc::smem_desc(s + 4 * kChunk + kk * 32, 16, 512, tc::kSw64),
+                           tc::smem_desc(q + 4 * qchunk + kk * 32, 16, 512, tc::kSw64), idesc, true);
+            tc::mma_commit(&ctl->kv_empty[st]);
+            if (t == w.tiles - 1) tc::mma_commit(&ctl->q_empty);
+            tc::mma_commit(&ctl->s_full[bf]);
+          }
+        }
+      }
+      tc::mma_commit(&ctl->drain);               // every MMA done before TMEM is released
+      const unsigned long long t0 = tc::globaltimer_ns();
+      while (!tc::mbar_try_wait(&ctl->drain, 0) && tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
+      }
+    }
+  } else {
+    // Sums: thread (quarter, lane) owns a key, the two groups the two halves of a block's rows.
+    // After a wait that ran out the threads go on without waiting, so that all meet at
+    // the group's barriers; they write nothing more.
+    const int quarter = warp & 3, half = (warp - 2) >> 2, st = tid - 64;
+    const int key = quarter * 32 + lane, cols = a.rows / 2;
+    float* sums = reinterpret_cast<float*>(smem + kOffSums);       // [tile][half][key]
+    float* neg = reinterpret_cast<float*>(smem + kOffNeg);         // [x & 1][row]
+    const uint64_t c2 = pack_f32x2(a.scale_log2, a.scale_log2);
+    uint32_t g = 0, x = 0;
+    bool ok = true;
+    // -lse of a block's row; rows that have none (behind the request's, or with an LSE that is
+    // no number) get -inf, so that their weights are 0.
+    auto row_neg = [&](int r, int b) {
+      const int m = b * a.rows + st;
+      if (st >= a.rows || m >= a.M || r >= a.R) return -INFINITY;
+      const float l = a.lse[(size_t)r * a.M + m];
+      return fabsf(l) < INFINITY ? -l : -INFINITY;
+    };
+    while (w.next(a)) {
+      float ahead = row_neg(w.r, 0);
+      const int new_at = a.starts[w.r];
+      for (int b = 0; b < a.blocks; ++b, ++x) {
+        if (st < kMaxRows) neg[(x & 1) * kMaxRows + st] = ahead;
+        if (b + 1 < a.blocks) ahead = row_neg(w.r, b + 1);
+        asm volatile("bar.sync 1, %0;" ::"r"(kSum) : "memory");
+        const float* ng = neg + (x & 1) * kMaxRows + half * cols;
+        for (int t = 0; t < w.tiles; ++t, ++g) {
+          const int bf = g % kBufs;
+          ok = __all_sync(0xffffffffu, wg_wait(&ctl->s_full[bf], (g / kBufs) & 1, ctl, a)) && ok;
+          tc::fence_after_sync();
+          const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + bf * kMaxRows + half * cols;
+          uint64_t acc[2] = {0, 0};
+          for (int c = 0; c < cols; c += 16) {
+            uint32_t raw[16];
+            tc::tmem_ld16(src + c, raw);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              const float4 n4 = *reinterpret_cast<const float4*>(ng + c + i);
+              float e[4];
+              unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(raw[i]), __uint_as_float(raw[i + 1])), c2,
+                                     pack_f32x2(n4.x, n4.y)), e[0], e[1]);
+              unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(raw[i + 2]), __uint_as_float(raw[i + 3])),
+                                     c2, pack_f32x2(n4.z, n4.w)), e[2], e[3]);
+              // fmaxf: a score that is NaN adds 0.
+#pragma unroll
+              for (int u = 0; u < 4; ++u) e[u] = fmaxf(ex2(e[u]), 0.f);
+              acc[0] = add_f32x2(acc[0], pack_f32x2(e[0], e[1]));
+              acc[1] = add_f32x2(acc[1], pack_f32x2(e[2], e[3]));
+            }
+          }
+          tc::fence_before_sync();
+          tc::mbar_arrive(&ctl->s_empty[bf]);
+          float s0, s1;
+          unpack_f32x2(add_f32x2(acc[0], acc[1]), s0, s1);
+          float* at = sums + (t * 2 + half) * kTile + key;
+          *at = (b ? *at : 0.f) + s0 + s1;
+        }
+      }
+      asm volatile("bar.sync 1, %0;" ::"r"(kSum) : "memory");
+      for (int i = st; i < w.tiles * kTile; i += kSum) {
+        const int slot = w.tile * kTile + i;
+        const float* at = sums + (i / kTile) * 2 * kTile + i % kTile;
+        if (slot < w.len && ok) {
+          const size_t o = (size_t)w.r * a.max_pages * kPage + slot;
+          const float s = at[0] + at[kTile];
+          if (slot < new_at) {
+            a.weights[o] = a.weights[o] * a.decay + s;
+          } else {
+            a.weights[o] = s;
+            if (a.positions)
+              a.positions[o] = (a.rope_starts ? a.rope_starts[w.r] : new_at) + (slot - new_at);
+          }
+        }
+      }
+      asm volatile("bar.sync 1, %0;" ::"r"(kSum) : "memory");
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 1) tc::tmem_dealloc(tmem, kBufs * kMaxRows);
+}
+
+int32_t weigh_impl(const mla_cache_shape* s, const void* q, const void* kv,
+                   const int32_t* block_table, const int32_t* seq_lens, const float* lse,
+                   float bmm1_scale, float decay, const int32_t* starts, const int32_t* rope_starts,
+                   float* weights, int32_t* positions, int32_t* status, mla_stream_t stream,
+                   unsigned long long wait_limit_ns, int withhold) {
+  if (!s) return MLA_ERR_NULL;
+  if (s->page_size != kPage) return MLA_ERR_UNSUPPORTED;
+  if (s->R < 1 || s->R > kMaxR || s->k < 1 || s->H < 1 || (long long)s->k * s->H > kMaxM ||
+      s->max_pages < 1 || s->max_pages > (1 << 20) || s->num_pages < 1 ||
+      s->num_pages >= (1 << 25))
+    return MLA_ERR_SHAPE;
+  if (!scales_ok(bmm1_scale, 0.f) || !std::isfinite(decay) || decay < 0.f) return MLA_ERR_SHAPE;
+  if (!q || !kv || !block_table || !seq_lens || !lse || !starts || !weights) return MLA_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(lse, 4) || !aligned(starts, 4) || !aligned(rope_starts, 4) || !aligned(weights, 4) ||
+      !aligned(positions, 4) || !aligned(status, 4))
+    return MLA_ERR_ALIGN;
+  int st = check_device();
+  if (st != MLA_OK) return st;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  WeighArgs a;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.starts = starts;
+  a.rope_starts = rope_starts;
+  a.lse = lse;
+  a.weights = weights;
+  a.positions = positions;
+  a.status = status;
+  a.scale_log2 = (float)((double)bmm1_scale * 1.4426950408889634);
+  a.decay = decay;
+  a.R = s->R;
+  a.M = s->k * s->H;
+  a.max_pages = s->max_pages;
+  a.num_pages = s->num_pages;
+  // Blocks of equal size, as few as hold the rows.
+  a.blocks = (int)cdiv(a.M, kMaxRows);
+  a.rows = (int)cdiv(cdiv(a.M, a.blocks), 32) * 32;
+  a.wait_limit_ns = wait_limit_ns;
+  a.withhold = withhold;
+  CUtensorMap tkv, tkvr, tq, tqr;
+  const cuuint64_t kv_dims[2] = {kDqk, (cuuint64_t)s->num_pages * kPage}, str[1] = {kDqk};
+  const cuuint64_t q_dims[2] = {kDqk, (cuuint64_t)s->R * a.M};
+  const cuuint32_t box[2] = {128, kPage}, box_r[2] = {64, kPage};
+  const cuuint32_t qbox[2] = {128, (cuuint32_t)a.rows}, qbox_r[2] = {64, (cuuint32_t)a.rows};
+  if (!dec::encode(&tkv, kv, 2, kv_dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !dec::encode(&tkvr, kv, 2, kv_dims, str, box_r, CU_TENSOR_MAP_SWIZZLE_64B) ||
+      !dec::encode(&tq, q, 2, q_dims, str, qbox, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !dec::encode(&tqr, q, 2, q_dims, str, qbox_r, CU_TENSOR_MAP_SWIZZLE_64B))
+    return MLA_ERR_CUDA;
+  static bool attr_set[64] = {};
+  if (dec::set_smem(weigh_kernel, kSmemBytes, attr_set) != cudaSuccess) return MLA_ERR_CUDA;
+  const long long most = (long long)s->R * cdiv((long long)s->max_pages * kPage, kTile);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, weigh_kernel, a, tkv, tkvr, tq, tqr);
+  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace mlafold
+
+using namespace mlafold;
+
+extern "C" int32_t mla_kv_weigh(const mla_cache_shape* s, const void* q, const void* kv,
+                                const int32_t* block_table, const int32_t* seq_lens,
+                                const float* lse, float bmm1_scale, float decay,
+                                const int32_t* starts, const int32_t* rope_starts, float* weights,
+                                int32_t* positions, int32_t* status, mla_stream_t stream) {
+  return weigh_impl(s, q, kv, block_table, seq_lens, lse, bmm1_scale, decay, starts, rope_starts,
+                    weights, positions, status, stream, kWaitLimitNs, 0);
+}
+
+extern "C" int32_t mla_kv_weigh_wait_test(const mla_cache_shape* s, const void* q, const void* kv,
+                                          const int32_t* block_table, const int32_t* seq_lens,
+                                          const float* lse, float bmm1_scale, float decay,
+                                          const int32_t* starts, const int32_t* rope_starts,
+                                          float* weights, int32_t* positions, int32_t* status,
+                                          uint64_t wait_limit_ns, mla_stream_t stream) {
+  if (!status) return MLA_ERR_NULL;
+  if (wait_limit_ns < 1000000ull || wait_limit_ns > kWaitLimitNs) return MLA_ERR_SHAPE;
+  return weigh_impl(s, q, kv, block_table, seq_lens, lse, bmm1_scale, decay, starts, rope_starts,
+                    weights, positions, status, stream, wait_limit_ns, 1);
+}
