@@ -604,6 +604,74 @@ int32_t mla_kv_evict(const mla_cache_shape *shape, void *kv, const int32_t *bloc
                      int32_t *positions_out, int32_t *lens_out, void *workspace,
                      size_t workspace_bytes, int32_t *status, mla_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The prompt: attention over whole prompts before anything is cached (or over a
+ * chunk of one), in the expanded form. An addition of this library. */
+
+/* Shape of mla_prompt_attention. All fields are host values; strides in elements, multiples
+ * of 8, at least the width of what they step over. */
+typedef struct {
+  int32_t R;               /* requests, 1 .. 1024                                        */
+  int32_t tokens;          /* rows of q, 0 .. 2^24 (0 launches nothing)                  */
+  int32_t keys;            /* rows of k_nope, k_rope and v, 0 .. 2^24                    */
+  int32_t H;               /* query heads, 1 .. 4096                                     */
+  int32_t kv_heads;        /* heads of k_nope and v, dividing H: head h reads head
+                              h / (H / kv_heads)                                         */
+  int32_t causal;          /* 1 or 0                                                     */
+  int32_t num_ctas;        /* persistent CTAs, 1 .. 2048; normally the device's SM count */
+  int64_t q_token_stride, q_head_stride;       /* >= 192 */
+  int64_t k_token_stride, k_head_stride;       /* >= 128 */
+  int64_t v_token_stride, v_head_stride;       /* >= 128 */
+  int64_t rope_stride;                         /* >= 64  */
+} mla_prompt_shape;
+
+/* Attention of packed prompts: for token i of request r's n and its keys j < m,
+ *   s[i][h][j] = sm_scale (q[i][h][0:128] . k_nope[j][h'] + q[i][h][128:192] . k_rope[j]),
+ *   out[i][h]  = softmax_j(s[i][h]) v[j][h'],   lse[i][h] = log2 sum_j e^s[i][h][j]
+ * with h' = h / (H / kv_heads). causal = 1: token i sees keys j <= i + m - n (its own
+ * place, counted from the end: a chunk whose earlier keys are there too has m > n);
+ * causal = 0: all m.
+ *   q          [tokens, H, 192] BF16, device, 16-byte aligned: 128 nope dims, then 64 rope
+ *              dims, rotated.
+ *   k_nope, v  [keys, kv_heads, 128] BF16, device, 16-byte aligned (so may be the two halves
+ *              of one projection's [keys, kv_heads, 256]).
+ *   k_rope     [keys, 64] BF16, device, 16-byte aligned: the rotated rope dims, one vector
+ *              for all heads.
+ *   cu_tokens  [R + 1] int32, device: request r's rows of q are cu_tokens[r] ..
+ *              cu_tokens[r + 1] - 1, ascending; rows that belong to no request keep
+ *              their out and lse as they are.
+ *   cu_keys    [R + 1] int32, device: the same for its keys; NULL: cu_tokens.
+ *   sm_scale   finite, > 0.
+ *   workspace  >= mla_prompt_workspace_bytes(shape) bytes, device, 256-byte aligned; calls
+ *              that share one must not overlap. Its contents need not be initialised.
+ *   out        [tokens, H, 128] BF16, device, 16-byte aligned; lse [tokens, H] FP32 base-2 or
+ *              NULL. A token that sees no key gets out = 0, lse = -inf.
+ *   status     optional int32 device word: MLA_FAULT_WORK_ITEM (offsets that descend or
+ *              leave the rows: that request is skipped), MLA_FAULT_WAIT_TIMEOUT.
+ * What lies between and behind the requests' rows and keys reaches no result, whatever its
+ * bits. Within a request a NaN or infinity in k or q reaches the rows that see it; one in v
+ * may also reach rows up to 127 places before them (0 times it, in the same tile of keys).
+ * BF16 products, FP32 scores, sums and accumulation; the weights are rounded to BF16 for
+ * their product with v. */
+int32_t mla_prompt_workspace_bytes(const mla_prompt_shape *shape, size_t *bytes);
+int32_t mla_prompt_attention(const mla_prompt_shape *shape, const void *q, const void *k_nope,
+                             const void *k_rope, const void *v, const int32_t *cu_tokens,
+                             const int32_t *cu_keys, float sm_scale, void *workspace,
+                             size_t workspace_bytes, void *out, float *lse, int32_t *status,
+                             mla_stream_t stream);
+
+/* Failure detection, for tests: mla_prompt_attention with every pipeline wait bounded by
+ * wait_limit_ns (1 ms .. 2 s; the regular call uses 2 s) and with CTA 0's first keys never
+ * loaded, so that a wait runs out. The CTA then ORs MLA_FAULT_WAIT_TIMEOUT into *status
+ * (required here), stops, lets its copies and MMAs in flight finish, frees its tensor memory
+ * and returns; what it had a part in is unspecified. The workspace may be used again. */
+int32_t mla_prompt_attention_wait_test(const mla_prompt_shape *shape, const void *q,
+                                       const void *k_nope, const void *k_rope, const void *v,
+                                       const int32_t *cu_tokens, const int32_t *cu_keys,
+                                       float sm_scale, void *workspace, size_t workspace_bytes,
+                                       void *out, float *lse, int32_t *status,
+                                       uint64_t wait_limit_ns, mla_stream_t stream);
+
 /* Bits the kernels OR into *status. */
 #define MLA_FAULT_WAIT_TIMEOUT 0x1 /* a pipeline wait gave up; the CTA stopped early */
 #define MLA_FAULT_PAGE_RANGE 0x2   /* a block-table entry was outside [0, num_pages) */

@@ -22,7 +22,8 @@ makes the decode's queries (W_UK, rotation, E4M3), ``rope_table(rows)`` makes th
 table of angles both read; ``PrefixMla(...)`` decodes a batch whose requests
 share a prefix, reading the prefix's keys once for all of them.
 
-To bound the cache: ``kv_weigh(...)`` adds up the attention weight of every cached
+Before the cache: ``prompt_attention(...)`` over whole packed prompts, or chunks of
+them, in the expanded form. To bound the cache: ``kv_weigh(...)`` adds up the attention weight of every cached
 key after a decode, ``kv_evict(...)`` keeps the keys of most weight.
 """
 from __future__ import annotations
@@ -34,7 +35,7 @@ import torch
 from . import _lib
 from ._lib import (AppendShape, CacheShape, FAULT_PAGE_RANGE, FAULT_ROPE_RANGE, FAULT_WAIT_TIMEOUT,
                    FAULT_WORK_ITEM, MlaError, MlaShape, POLICY_BALANCED, POLICY_UNIFORM,
-                   QueryShape)
+                   PromptShape, QueryShape)
 
 __all__ = ["MlaShape", "MlaError", "POLICY_BALANCED", "POLICY_UNIFORM", "make_shape",
            "plan_list_len", "workspace_bytes", "plan_splits", "folded_decode",
@@ -44,7 +45,8 @@ __all__ = ["MlaShape", "MlaError", "POLICY_BALANCED", "POLICY_UNIFORM", "make_sh
            "FAULT_WORK_ITEM", "FAULT_ROPE_RANGE", "library_path", "rope_table", "kv_append",
            "query_absorb", "query_absorb_wait_test", "prefix_workspace_bytes", "prefix_plan",
            "prefix_decode", "prefix_decode_wait_test", "PrefixMla", "kv_weigh", "kv_weigh_wait_test",
-           "kv_evict", "kv_evict_workspace_bytes"]
+           "kv_evict", "kv_evict_workspace_bytes", "prompt_attention", "prompt_attention_wait_test",
+           "prompt_workspace_bytes"]
 
 PAGE = 64
 
@@ -748,3 +750,105 @@ def _apart(name: str, t, other) -> None:
     if a != b and a < b + other.numel() * other.element_size() and \
             b < a + t.numel() * t.element_size():
         raise ValueError(f"{name} overlaps its input")
+
+
+# ---------------------------------------------------------------- the prompt
+def prompt_workspace_bytes(R: int, num_ctas: int | None = None, device=None) -> int:
+    """Bytes of the workspace of prompt_attention for R requests (num_ctas None: the
+    device's SM count, as the call takes it)."""
+    if num_ctas is None:
+        num_ctas = torch.cuda.get_device_properties(
+            torch.device("cuda" if device is None else device)).multi_processor_count
+    shape = PromptShape(R, 1, 1, 1, 1, 1, num_ctas, 192, 192, 128, 128, 128, 128, 64)
+    out = ctypes.c_size_t(0)
+    _lib.check("mla_prompt_workspace_bytes", _lib.load().mla_prompt_workspace_bytes(
+        ctypes.byref(shape), ctypes.byref(out)))
+    return out.value
+
+
+def prompt_attention(q, k_nope, k_rope, v, cu_tokens, sm_scale: float, cu_keys=None,
+                     causal: bool = True, out=None, lse=None, return_lse: bool = True,
+                     workspace=None, status=None, stream=None):
+    """Attention over packed prompts: out [tokens, H, 128] BF16 and the base-2 lse
+    [tokens, H] (None without return_lse) of q [tokens, H, 192] BF16 (128 nope, 64
+    rotated rope dims) over k_nope and v [keys, kv_heads, 128] and k_rope [keys, 64]
+    (rotated, one vector for all heads), BF16; tokens and heads of all may be strided.
+    Request r has rows cu_tokens[r] .. cu_tokens[r + 1] of q and cu_keys[r] .. of the keys
+    (None: the same). Causal: token i of n sees keys j <= i + m - n of m. Rows that
+    belong to no request are not written. `workspace`: uint8, at least
+    prompt_workspace_bytes (None: allocated for the call). See mla_prompt_attention in
+    include/mlafold.h."""
+    dev = _device("q", q, 3)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return prompt_attention(q, k_nope, k_rope, v, cu_tokens, sm_scale, cu_keys, causal, out,
+                                    lse, return_lse, workspace, status, stream)
+    shape = _prompt_shape(dev, q, k_nope, k_rope, v, cu_tokens, cu_keys, causal, status)
+    T, H = shape.tokens, shape.H
+    if out is None:
+        out = _empty((T, H, 128), torch.bfloat16, q.device, stream)
+    else:
+        _check(dev, "out", out, _BF16, (T, H, 128))
+    if not return_lse:
+        lse = None
+    elif lse is None:
+        lse = _empty((T, H), torch.float32, q.device, stream)
+    else:
+        _check(dev, "lse", lse, _F32, (T, H))
+    if workspace is None:
+        need = ctypes.c_size_t(0)
+        _lib.check("mla_prompt_workspace_bytes", _lib.load().mla_prompt_workspace_bytes(
+            ctypes.byref(shape), ctypes.byref(need)))
+        workspace = _empty((need.value,), torch.uint8, q.device, stream)
+    else:
+        _check(dev, "workspace", workspace, (torch.uint8,), workspace.shape)
+    _lib.check("mla_prompt_attention", _lib.load().mla_prompt_attention(
+        ctypes.byref(shape), _ptr(q), _ptr(k_nope), _ptr(k_rope), _ptr(v), _ptr(cu_tokens),
+        _ptr(cu_keys), float(sm_scale), _ptr(workspace), workspace.numel(), _ptr(out), _ptr(lse),
+        _ptr(status), _stream(stream)))
+    return out, lse
+
+
+def _prompt_shape(dev, q, k_nope, k_rope, v, cu_tokens, cu_keys, causal, status) -> PromptShape:
+    def rows(name, t, dims, width):
+        if _device(name, t, dims) != dev or t.shape[-1] != width or t.dtype != torch.bfloat16 or \
+                t.stride(-1) != 1:
+            raise ValueError(f"{name} is not [..., {width}] BF16 with contiguous dims on q's device")
+
+    rows("q", q, 3, 192)
+    rows("k_nope", k_nope, 3, 128)
+    rows("k_rope", k_rope, 2, 64)
+    rows("v", v, 3, 128)
+    (T, H, _), (Tk, Hkv, _) = q.shape, k_nope.shape
+    if v.shape != (Tk, Hkv, 128) or k_rope.shape[0] != Tk:
+        raise ValueError(f"v {tuple(v.shape)} and k_rope {tuple(k_rope.shape)} do not go with k_nope "
+                         f"{tuple(k_nope.shape)}")
+    if _device("cu_tokens", cu_tokens, 1) != dev or cu_tokens.shape[0] < 2:
+        raise ValueError("cu_tokens is not [R + 1] int32 on q's device")
+    R = cu_tokens.shape[0] - 1
+    _check(dev, "cu_tokens", cu_tokens, _I32, (R + 1,))
+    if cu_keys is not None:
+        _check(dev, "cu_keys", cu_keys, _I32, (R + 1,))
+    elif Tk != T:
+        raise ValueError(f"{Tk} keys for {T} tokens without cu_keys")
+    if status is not None:
+        _check(dev, "status", status, _I32, (1,))
+    # The stride over a dim of one element is never used: any that the library takes will do.
+    step = lambda t, d, width: t.stride(d) if t.shape[d] > 1 else width  # noqa: E731
+    sms = torch.cuda.get_device_properties(dev).multi_processor_count
+    return PromptShape(R, T, Tk, H, Hkv, 1 if causal else 0, sms, step(q, 0, H * 192), step(q, 1, 192),
+                       step(k_nope, 0, Hkv * 128), step(k_nope, 1, 128), step(v, 0, Hkv * 128),
+                       step(v, 1, 128), step(k_rope, 0, 64))
+
+
+def prompt_attention_wait_test(q, k_nope, k_rope, v, cu_tokens, sm_scale: float, out, lse, workspace,
+                               status, wait_limit_ns: int, cu_keys=None, causal: bool = True,
+                               stream=None) -> None:
+    """Failure-detection test hook: prompt_attention with every pipeline wait bounded
+    by wait_limit_ns and CTA 0's first keys withheld, so that a wait runs out and
+    MLA_FAULT_WAIT_TIMEOUT is set in `status` (see include/mlafold.h)."""
+    shape = _prompt_shape(_device("q", q, 3), q, k_nope, k_rope, v, cu_tokens, cu_keys, causal, status)
+    _lib.check("mla_prompt_attention_wait_test", _lib.load().mla_prompt_attention_wait_test(
+        ctypes.byref(shape), _ptr(q), _ptr(k_nope), _ptr(k_rope), _ptr(v), _ptr(cu_tokens),
+        _ptr(cu_keys), float(sm_scale), _ptr(workspace), workspace.numel(), _ptr(out), _ptr(lse),
+        _ptr(status), int(wait_limit_ns), _stream(stream)))

@@ -25,7 +25,8 @@ EXPORTS = ("mla_plan_list_len", "mla_workspace_bytes", "mla_plan_splits",
            "mla_tier_plan", "mla_row_copy", "mla_kv_append", "mla_query_absorb",
            "mla_query_absorb_wait_test", "mla_prefix_workspace_bytes", "mla_prefix_plan",
            "mla_prefix_decode", "mla_prefix_decode_wait_test", "mla_kv_weigh",
-           "mla_kv_weigh_wait_test", "mla_kv_evict_workspace_bytes", "mla_kv_evict")
+           "mla_kv_weigh_wait_test", "mla_kv_evict_workspace_bytes", "mla_kv_evict",
+           "mla_prompt_workspace_bytes", "mla_prompt_attention", "mla_prompt_attention_wait_test")
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -54,6 +55,15 @@ class CacheShape(ctypes.Structure):
     _fields_ = [("R", ctypes.c_int32), ("k", ctypes.c_int32), ("H", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
                 ("num_pages", ctypes.c_int32)]
+
+
+class PromptShape(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int32), ("tokens", ctypes.c_int32), ("keys", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("num_ctas", ctypes.c_int32), ("q_token_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64), ("k_token_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64), ("v_token_stride", ctypes.c_int64),
+                ("v_head_stride", ctypes.c_int64), ("rope_stride", ctypes.c_int64)]
 
 
 class MlaError(RuntimeError):
@@ -124,6 +134,14 @@ def load() -> ctypes.CDLL:
     lib.mla_kv_evict_workspace_bytes.restype = I32
     lib.mla_kv_evict.argtypes = [CP, P, P, P, P, P, P, I32, I32, P, P, P, P, SZ, P, P]
     lib.mla_kv_evict.restype = I32
+    PP = ctypes.POINTER(PromptShape)
+    lib.mla_prompt_workspace_bytes.argtypes = [PP, ctypes.POINTER(SZ)]
+    lib.mla_prompt_workspace_bytes.restype = I32
+    lib.mla_prompt_attention.argtypes = [PP, P, P, P, P, P, P, F, P, SZ, P, P, P, P]
+    lib.mla_prompt_attention.restype = I32
+    lib.mla_prompt_attention_wait_test.argtypes = [PP, P, P, P, P, P, P, F, P, SZ, P, P, P,
+                                                   ctypes.c_uint64, P]
+    lib.mla_prompt_attention_wait_test.restype = I32
     _lib = lib
     return lib
 

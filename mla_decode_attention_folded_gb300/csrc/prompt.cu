@@ -1,0 +1,818 @@
+// Attention over whole prompts, packed: the expanded form of the latent attention.
+//
+//   s[i][h][j] = sm_scale (q[i][h][0:128] . k_nope[j][h / G] + q[i][h][128:192] . k_rope[j])
+//   out[i][h]  = softmax_j(s[i][h]) v[j][h / G],   lse[i][h] = log2 sum_j 2^(s log2 e)
+//
+// over the keys j of token i's request that it sees (causal: up to its own place, counted
+// from the end). The rope dims of a key are one vector for all heads.
+//
+// Bound by the BF16 tensor pipe: 640 FLOP per (query, key, head) against 644 bytes per (query,
+// head). A CTA takes 256 query rows of one head as two halves of 128, each the M of its MMAs:
+// while the softmax of one half runs, the tensor pipe multiplies for the other.
+//   S[128, 128 keys] = Q K^T, 12 MMAs;  O[128, 128] += P V, 8 MMAs, P from TMEM.
+// TMEM holds both halves' S and O (4 x 128 columns); P (BF16) takes the place of the S it was
+// made from. Warp 0 loads by TMA (Q, and K and V in a ring of 16 KB blocks), warp 1
+// issues the MMAs, warps 4-7 and 8-11 are the softmax of the halves: a thread owns a row, so
+// that no maximum or sum crosses threads. The maximum that P is relative to moves only when
+// a score exceeds it by 2^8 (O and the sum are then rescaled); P is rounded to BF16 (2^-8,
+// as the inputs are), its sum is of the FP32 values.
+//
+// How the work is shared out is in prompt.h. The order of a CTA's MMAs is PV(t) before S(t + 1)
+// of the same half, so that S may overwrite P and its completion tells that O is final.
+#include <cmath>
+
+#include "checks.h"
+#include "decode_common.cuh"
+#include "formats.cuh"
+#include "internal.h"
+#include "prompt.h"
+#include "ptx.cuh"
+#include "tc.cuh"
+
+namespace mlafold {
+namespace {
+
+using namespace prompt;
+
+constexpr int kNope = 128, kRope = 64, kV = 128;
+constexpr int kBlock = 128 * 128;                // bytes: 128 rows of 64 BF16
+constexpr int kQBlocks = 3;                      // 192 dims
+// K's nope dims and V, two blocks each, take turns in a ring of three pairs; K's rope dims have
+// two blocks of their own. A tile's K goes where V was two tiles before, whose last reader
+// came after that tile's S: its rope block is free too, without a barrier of its own.
+constexpr int kRing = 3;
+constexpr int kOffRing = 2 * kQBlocks * kBlock;
+constexpr int kOffRope = kOffRing + kRing * 2 * kBlock;
+constexpr int kOffCtl = kOffRope + 2 * kBlock;
+constexpr int kThreads = 128 + 2 * kHalf;        // warps 2 and 3 only give their registers
+// Registers a thread at the launch (384 x 168 = 64,512), and after the split: 128 x 80 + 256 x 208.
+constexpr int kRegsFew = 80, kRegsMany = 208;
+constexpr uint32_t kTmemCols = 512, kColO = 256;
+constexpr unsigned long long kWaitLimitNs = 2000000000ull;   // 2 s
+constexpr uint32_t kIdescS = tc::idesc_bf16_f32(kHalf, kKeys);
+constexpr uint32_t kIdescO = tc::idesc_bf16_f32(kHalf, kV) | (1u << 16);   // V is MN-major
+constexpr float kLazy = 8.f;
+
+// A run of tiles of one item.
+struct Piece {
+  int row0, rows;                // first query row (of all), rows of the item
+  int head, key0, m;             // head, first key (of all), keys of the request
+  int lim0;                      // keys that row 0 would see, before it is cut to 0 .. m
+  int t0, t1;                    // tiles, t1 <= what the last row sees
+  int slot;                      // of its FP32 rows; -1: the whole item, straight to out
+  int causal;
+};
+__device__ __forceinline__ int row_limit(const Piece& p, int j) {
+  const int e = p.causal ? p.lim0 + j : p.m;
+  return e < 0 ? 0 : e < p.m ? e : p.m;
+}
+// Tiles of the piece that half h multiplies.
+__device__ __forceinline__ int half_tiles(const Piece& p, int h) {
+  const int rows = min(p.rows - h * kHalf, kHalf);
+  if (rows <= 0) return 0;
+  const int last = tiles_of(row_limit(p, h * kHalf + rows - 1));
+  return max(min(p.t1, last) - p.t0, 0);
+}
+
+struct PromptCtl {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t full[kRing], empty[kRing];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t job_full[2], job_empty[2];
+  uint64_t drain;
+  Piece job[2];
+  uint32_t tmem_base;
+  int abort_flag;
+};
+constexpr int kSmemBytes = kOffCtl + (int)sizeof(PromptCtl) + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+struct PromptArgs {
+  const int32_t* cu;             // [R + 1]
+  const int32_t* cu_keys;        // [R + 1], or null: cu
+  uint16_t* out;                 // [T][H][128]
+  float* lse;                    // [T][H], or null
+  Plan* plan;
+  long long* first_place;        // [R + 1]
+  long long* first_item;         // [R + 1]
+  long long* part_place;         // [parts + 1]
+  float* part_o;                 // [slots][32][256][4]
+  float* part_lse;               // [slots][256]
+  int32_t* status;
+  float scale_log2;
+  int R, T, Tk, H, group, causal, ctas;
+  unsigned long long wait_limit_ns;
+  int withhold;                  // failure-detection test: CTA 0 never loads its first keys
+};
+
+// Rows [first, first + count) of request r; offsets that are none give no rows.
+__device__ __forceinline__ bool span(const int32_t* cu, int r, int most, int& first, int& count) {
+  const int a = cu[r], b = cu[r + 1];
+  const bool ok = a >= 0 && b >= a && b <= most;
+  first = ok ? a : 0;
+  count = ok ? b - a : 0;
+  return ok;
+}
+__device__ __forceinline__ Request request(const PromptArgs& a, int r, int& row0, int& key0, bool& ok) {
+  Request q;
+  ok = span(a.cu, r, a.T, row0, q.n);
+  ok = span(a.cu_keys ? a.cu_keys : a.cu, r, a.Tk, key0, q.m) && ok;
+  if (!ok) q.n = q.m = 0;
+  q.causal = a.causal;
+  return q;
+}
+
+// ---------------------------------------------------------------- plan
+constexpr int kPlanThreads = kMaxR;
+
+__global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptArgs a) {
+  __shared__ long long sums[2][32];
+  __shared__ int most[32];
+  const int r = threadIdx.x, lane = r & 31, warp = r >> 5;
+  grid_dep_wait();
+  grid_dep_launch();
+  int row0, key0, longest = 0;
+  long long w = 0, it = 0;
+  if (r < a.R) {
+    bool ok;
+    const Request q = request(a, r, row0, key0, ok);
+    if (!ok && a.status) atomicOr(a.status, MLA_FAULT_WORK_ITEM);
+    const int I = items(q);
+    w = places(q) * a.H;
+    it = (long long)I * a.H;
+    if (I) longest = max(item_tiles(q, I - 1), I > 1 ? item_tiles(q, I - 2) : 0);
+  }
+  long long sw = w, si = it;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, sw, o), v = __shfl_up_sync(0xffffffffu, si, o);
+    if (lane >= o) sw += u, si += v;
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) sums[0][warp] = sw, sums[1][warp] = si;
+  if (lane == 0) most[warp] = longest;
+  __syncthreads();
+  long long bw = 0, bi = 0, tw = 0, ti = 0;
+  for (int i = 0; i < (int)(blockDim.x >> 5); ++i) {
+    if (i < warp) bw += sums[0][i], bi += sums[1][i];
+    tw += sums[0][i], ti += sums[1][i];
+    longest = max(longest, most[i]);
+  }
+  if (r < a.R) {
+    a.first_place[r] = bw + sw - w;
+    a.first_item[r] = bi + si - it;
+  }
+  if (r == 0) {
+    a.first_place[a.R] = tw;
+    a.first_item[a.R] = ti;
+    a.plan->total = tw;
+    a.plan->all_items = ti;
+    a.plan->parts = parts_of(tw, longest, a.ctas);
+    a.plan->claimed = 0;
+  }
+  const int parts = parts_of(tw, longest, a.ctas);
+  for (int p = r; parts > 0 && p <= parts; p += blockDim.x) a.part_place[p] = part_at(tw, parts, p);
+}
+
+// The last r with first[r] <= x, by a warp.
+__device__ __forceinline__ int find_request(const long long* first, int R, long long x, int lane) {
+  int lo = 0, n = R;
+  while (n > 1) {
+    const int step = (n + 31) >> 5;
+    const bool le = lane * step < n && first[lo + lane * step] <= x;
+    const unsigned m = __ballot_sync(0xffffffffu, le);
+    const int hit = m ? 31 - __clz(m) : 0, end = lo + n;
+    lo += hit * step;
+    n = min(step, end - lo);
+  }
+  return lo;
+}
+
+// ---------------------------------------------------------------- attention
+__device__ __forceinline__ bool pr_wait(uint64_t* bar, uint32_t parity, PromptCtl* ctl,
+                                        const PromptArgs& a) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = tc::globaltimer_ns();
+  while (true) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    if (*reinterpret_cast<volatile int*>(&ctl->abort_flag)) return false;
+    if (tc::globaltimer_ns() - t0 > a.wait_limit_ns) {
+      *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
+      if (a.status) atomicOr(a.status, MLA_FAULT_WAIT_TIMEOUT);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool take(PromptCtl* ctl, uint32_t seq, const PromptArgs& a, Piece& p) {
+  const int b = seq & 1;
+  if (!pr_wait(&ctl->job_full[b], (seq >> 1) & 1, ctl, a)) return false;
+  const volatile Piece* s = &ctl->job[b];
+  p.row0 = s->row0;
+  p.rows = s->rows;
+  p.head = s->head;
+  p.key0 = s->key0;
+  p.m = s->m;
+  p.lim0 = s->lim0;
+  p.t0 = s->t0;
+  p.t1 = s->t1;
+  p.slot = s->slot;
+  p.causal = s->causal;
+  tc::mbar_arrive(&ctl->job_empty[b]);
+  return p.rows > 0;
+}
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// 1 / x to 2^-23 (the exact division is a call, which setmaxnreg does not allow).
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
+              const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_r,
+              const __grid_constant__ CUtensorMap tm_v) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  PromptCtl* ctl = reinterpret_cast<PromptCtl*>(smem + kOffCtl);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&ctl->q_full[i], 1);
+      tc::mbar_init(&ctl->q_empty[i], 1);
+      tc::mbar_init(&ctl->s_full[i], 1);
+      tc::mbar_init(&ctl->p_full[i], kHalf);
+      tc::mbar_init(&ctl->o_full[i], 1);
+      tc::mbar_init(&ctl->job_full[i], 1);
+      tc::mbar_init(&ctl->job_empty[i], 1 + 2 * kHalf);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      tc::mbar_init(&ctl->full[i], 1);
+      tc::mbar_init(&ctl->empty[i], 1);
+    }
+    tc::mbar_init(&ctl->drain, 1);
+    ctl->abort_flag = 0;
+    tc::fence_barrier_init();
+    tc::prefetch_tmap(&tm_q);
+    tc::prefetch_tmap(&tm_k);
+    tc::prefetch_tmap(&tm_r);
+    tc::prefetch_tmap(&tm_v);
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(&ctl->tmem_base, kTmemCols);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = ctl->tmem_base;
+  grid_dep_wait();               // the waits' limit counts from the end of the kernel before
+  grid_dep_launch();
+
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
+  if (warp == 0) {
+    // ------------------------------------------------------------ pieces and copies
+    uint32_t seq = 0, slot = 0, xq0 = 0, xq1 = 0;  // places of the ring, queries loaded per half
+    bool ok = true;
+    auto wait0 = [&](uint64_t* bar, uint32_t parity) {
+      int v = 1;
+      if (lane == 0) v = pr_wait(bar, parity, ctl, a) ? 1 : 0;
+      return __shfl_sync(0xffffffffu, v, 0) != 0;
+    };
+    const bool withheld = a.withhold && blockIdx.x == 0;
+    const int parts = a.plan->parts;
+    const long long all = a.plan->all_items;
+    // Whole items: the first by the CTA's index, then claimed. Parts: places [at, end).
+    long long at = blockIdx.x, end = 0;
+    if (parts > 0) {
+      at = (int)blockIdx.x < parts ? a.part_place[blockIdx.x] : 0;
+      end = (int)blockIdx.x < parts ? a.part_place[blockIdx.x + 1] : 0;
+    }
+    while (ok) {
+      Piece p;
+      p.rows = 0;
+      if (parts > 0 ? at < end : at < all) {
+        const long long* first = parts > 0 ? a.first_place : a.first_item;
+        const int r = find_request(first, a.R, at, lane);
+        int row0, key0;
+        bool good;
+        const Request q = request(a, r, row0, key0, good);
+        const long long x = at - first[r], per = parts > 0 ? places(q) : items(q);
+        p.head = head_at(x, per, a.H);
+        const long long rest = x - p.head * per;
+        const int u = parts > 0 ? item_at(q, rest) : items(q) - 1 - (int)rest;
+        const int tiles = item_tiles(q, u);
+        p.row0 = row0 + u * kRows;
+        p.rows = min(q.n - u * kRows, kRows);
+        p.key0 = key0;
+        p.m = q.m;
+        p.causal = q.causal;
+        p.lim0 = u * kRows + 1 + q.m - q.n;
+        p.t0 = 0;
+        p.t1 = tiles;
+        p.slot = -1;
+        if (parts > 0) {
+          p.t0 = (int)(rest - before(q, u));
+          p.t1 = (int)min((long long)tiles, p.t0 + (end - at));
+          if (p.t0 > 0) p.slot = 2 * blockIdx.x;
+          else if (p.t1 < tiles) p.slot = 2 * blockIdx.x + 1;
+          at += p.t1 - p.t0;
+        }
+      }
+      // Hand it on, or an empty one at the end.
+      if (seq >= 2 && !(ok = wait0(&ctl->job_empty[seq & 1], ((seq >> 1) - 1) & 1))) break;
+      if (lane == 0) {
+        volatile Piece* s = &ctl->job[seq & 1];
+        s->row0 = p.row0;
+        s->rows = p.rows;
+        s->head = p.head;
+        s->key0 = p.key0;
+        s->m = p.m;
+        s->lim0 = p.lim0;
+        s->t0 = p.t0;
+        s->t1 = p.t1;
+        s->slot = p.slot;
+        s->causal = p.causal;
+        tc::mbar_arrive(&ctl->job_full[seq & 1]);
+      }
+      ++seq;
+      if (p.rows == 0) break;
+      if (parts == 0) {
+        int k = 0;
+        if (lane == 0) k = atomicAdd(&a.plan->claimed, 1);
+        at = (long long)gridDim.x + __shfl_sync(0xffffffffu, k, 0);
+      }
+      const int c0 = half_tiles(p, 0), c1 = half_tiles(p, 1), nt = max(c0, c1), kvh = p.head / a.group;
+#pragma unroll 1
+      for (int i = 0; i < 2 * nt; ++i, ++slot) {               // K, V of every tile
+        const int b = slot % kRing, key = p.key0 + (p.t0 + (i >> 1)) * kKeys, is_v = i & 1;
+        if (slot >= kRing && !(ok = wait0(&ctl->empty[b], (slot / kRing - 1) & 1))) break;
+        if (lane == 0 && !(withheld && slot == 0)) {
+          uint8_t* dst = smem + kOffRing + b * 2 * kBlock;
+          const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
+          tc::mbar_arrive_expect_tx(&ctl->full[b], (is_v ? 2 : 3) * kBlock);
+          tc::tma_load_3d(dst, tm, &ctl->full[b], 0, kvh, key);
+          tc::tma_load_3d(dst + kBlock, tm, &ctl->full[b], 128, kvh, key);
+          if (!is_v) tc::tma_load_2d(smem + kOffRope + (slot / 2 & 1) * kBlock, &tm_r, &ctl->full[b], 0, key);
+        }
+        if (i == 0) {
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            if (!(h ? c1 : c0)) continue;
+            const uint32_t x = h ? xq1++ : xq0++;
+            if (x > 0 && !(ok = wait0(&ctl->q_empty[h], (x - 1) & 1))) {
+              --(h ? xq1 : xq0);                               // not loaded
+              break;
+            }
+            if (lane == 0) {
+              tc::mbar_arrive_expect_tx(&ctl->q_full[h], kQBlocks * kBlock);
+              for (int e = 0; e < kQBlocks; ++e)
+                tc::tma_load_3d(smem + (h * kQBlocks + e) * kBlock, &tm_q, &ctl->q_full[h], e * 128, p.head,
+                                p.row0 + h * kHalf);
+            }
+          }
+          if (!ok) {
+            ++slot;                                            // loaded above
+            break;
+          }
+        }
+      }
+    }
+    // Never leave with copies in flight: another role may have given up a wait.
+    if (lane == 0) {
+      const unsigned long long t0 = tc::globaltimer_ns();
+      for (uint32_t i = slot < kRing ? 0 : slot - kRing; i < slot; ++i)
+        while (!(withheld && i == 0) && !tc::mbar_try_wait(&ctl->full[i % kRing], (i / kRing) & 1) &&
+               tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
+        }
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t x = h ? xq1 : xq0;
+        while (x > 0 && !tc::mbar_try_wait(&ctl->q_full[h], (x - 1) & 1) &&
+               tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMAs
+    if (lane == 0) {
+      uint32_t slot = 0, xq = 0, xp = 0;         // bit h: the phase of half h's barrier
+      const uint32_t s_q = tc::smem_u32(smem), s_ring = tc::smem_u32(smem + kOffRing);
+      const uint32_t s_rope = tc::smem_u32(smem + kOffRope);
+      Piece p;
+      bool ok = true;
+      for (uint32_t seq = 0; ok && take(ctl, seq, a, p); ++seq) {
+        const int c0 = half_tiles(p, 0), c1 = half_tiles(p, 1), nt = max(c0, c1);
+        // PV of tile t, then S of tile t + 1, half by half.
+#pragma unroll 1
+        for (int step = 0; step < 2 * (nt + 1); ++step) {
+          const int h = step & 1, t = (step >> 1) - 1, c = h ? c1 : c0;
+          // The half that reads a tile last gives its place in the ring back.
+          if (t >= 0 && t < c) {
+            const uint32_t at = slot + 2 * t + 1;
+            if (!(ok = pr_wait(&ctl->p_full[h], xp >> h & 1, ctl, a) &&
+                       pr_wait(&ctl->full[at % kRing], (at / kRing) & 1, ctl, a)))
+              break;
+            xp ^= 1u << h;
+            tc::fence_after_sync();
+            const uint32_t vb = s_ring + at % kRing * 2 * kBlock;
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              mma_bf16_ts(tmem + kColO + h * kV, tmem + h * kKeys + kk * 8,
+                          tc::smem_desc(vb + kk * 16 * 128, kBlock, 1024, tc::kSw128), kIdescO,
+                          t + kk != 0);
+            if (h == 1 || t >= c1) tc::mma_commit(&ctl->empty[at % kRing]);
+            if (t == c - 1) tc::mma_commit(&ctl->o_full[h]);
+          }
+          if (t + 1 < c) {
+            const uint32_t at = slot + 2 * (t + 1);
+            if (!(ok = pr_wait(&ctl->full[at % kRing], (at / kRing) & 1, ctl, a))) break;
+            if (t < 0) {
+              if (!(ok = pr_wait(&ctl->q_full[h], xq >> h & 1, ctl, a))) break;
+              xq ^= 1u << h;
+            }
+            tc::fence_after_sync();
+            const uint32_t kb = s_ring + at % kRing * 2 * kBlock, rb = s_rope + (at / 2 & 1) * kBlock;
+            const uint32_t qb = s_q + h * kQBlocks * kBlock;
+#pragma unroll
+            for (int kk = 0; kk < 12; ++kk)
+              tc::mma_bf16(tmem + h * kKeys,
+                           tc::smem_desc(qb + (kk >> 2) * kBlock + (kk & 3) * 32, 16, 1024, tc::kSw128),
+                           tc::smem_desc((kk < 8 ? kb + (kk >> 2) * kBlock : rb) + (kk & 3) * 32, 16, 1024,
+                                         tc::kSw128),
+                           kIdescS, kk != 0);
+            if (h == 1 || t + 1 >= c1) tc::mma_commit(&ctl->empty[at % kRing]);
+            if (t + 1 == c - 1) tc::mma_commit(&ctl->q_empty[h]);
+            tc::mma_commit(&ctl->s_full[h]);
+          }
+        }
+        slot += 2 * nt;
+      }
+      tc::mma_commit(&ctl->drain);               // every MMA done before TMEM is released
+      const unsigned long long t0 = tc::globaltimer_ns();
+      while (!tc::mbar_try_wait(&ctl->drain, 0) && tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
+      }
+    }
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
+    // ------------------------------------------------------------ softmax and output
+    const int h = (warp - 4) >> 2, quarter = warp & 3, j = h * kHalf + quarter * 32 + lane;
+    const uint32_t col_s = tmem + ((uint32_t)(quarter * 32) << 16) + h * kKeys;
+    const uint32_t col_o = tmem + ((uint32_t)(quarter * 32) << 16) + kColO + h * kV;
+    uint32_t slot = 0, xs = 0, xo = 0;
+    Piece p;
+    auto all_wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, pr_wait(bar, parity, ctl, a));
+    };
+    for (uint32_t seq = 0; __all_sync(0xffffffffu, take(ctl, seq, a, p)); ++seq) {
+      const int c = half_tiles(p, h), nt = max(c, half_tiles(p, h ^ 1));
+      const bool valid = j < p.rows;
+      const int lim = valid ? row_limit(p, j) : INT_MAX;
+      const int lowest = __reduce_min_sync(0xffffffffu, lim);
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int t = 0; t < c; ++t) {
+        if (!(ok = all_wait(&ctl->s_full[h], xs++ & 1))) break;
+        tc::fence_after_sync();
+        uint32_t raw[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tc::tmem_ld32(col_s + 32 * i, raw[i]);
+        tc::tmem_wait_ld();
+        const int key = (p.t0 + t) * kKeys;
+        if (key + kKeys > lowest) {              // keys that some row of the warp does not see
+#pragma unroll
+          for (int i = 0; i < kKeys; ++i)
+            if (key + i >= lim) raw[i >> 5][i & 31] = 0xFF800000u;
+        }
+        float mx[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          mx[i] = __uint_as_float(raw[i][0]);
+#pragma unroll
+          for (int e = 1; e < 32; ++e) mx[i] = fmaxf(mx[i], __uint_as_float(raw[i][e]));
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+        // The first tile sets the maximum; later ones move it only when they exceed it by 2^8.
+        const bool moves = top > m + kLazy;
+        const float f = moves ? ex2(m - top) : 1.f;
+        if (moves) m = top;
+        if (t > 0 && __any_sync(0xffffffffu, moves)) {
+          l *= f;
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            uint32_t o[32];
+            tc::tmem_ld32(col_o + 32 * i, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tc::tmem_st32(col_o + 32 * i, o);
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : -m;
+        const uint64_t c2 = pack_f32x2(a.scale_log2, a.scale_log2), b2 = pack_f32x2(base, base);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int at = 64 * i + 2 * e;
+            float x, y;
+            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(raw[at >> 5][at & 31]),
+                                              __uint_as_float(raw[at >> 5][(at & 31) + 1])), c2, b2), x, y);
+            x = ex2(x);
+            y = ex2(y);
+            sum[e & 1] = add_f32x2(sum[e & 1], pack_f32x2(x, y));
+            pk[e] = f32x2_to_bf16x2(x, y);
+          }
+          tc::tmem_st32(col_s + 32 * i, pk);
+        }
+        float s0, s1;
+        unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
+        // Values behind the request's last key are another's, or nothing's: their weights are 0,
+        // and they are cleared so that 0 times them is 0.
+        if (key + kKeys > p.m) {
+          const uint32_t at = slot + 2 * t + 1;
+          ok = all_wait(&ctl->full[at % kRing], (at / kRing) & 1);
+          const int row = quarter * 32 + lane;
+          if (ok && key + row >= p.m)
+            for (int i = 0; i < 16; ++i)
+              *reinterpret_cast<uint4*>(smem + kOffRing + (at % kRing * 2 + (i >> 3)) * kBlock + row * 128 +
+                                        (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+          tc::fence_proxy_async_smem();
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        tc::mbar_arrive(&ctl->p_full[h]);
+        if (!ok) break;
+      }
+      if (!ok) break;
+      slot += 2 * nt;
+      if (c > 0 && !all_wait(&ctl->o_full[h], xo++ & 1)) break;
+      tc::fence_after_sync();
+      const float inv = l > 0.f ? rcp(l) : l;    // NaN stays
+      const float lse = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
+      const size_t row = (size_t)(p.row0 + j) * a.H + p.head;
+      if (p.slot < 0) {
+        if (valid && a.lse) a.lse[row] = lse;
+        uint4* dst = reinterpret_cast<uint4*>(a.out + row * kV);
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          uint32_t o[32];
+          if (c > 0) {
+            tc::tmem_ld32(col_o + 32 * i, o);
+            tc::tmem_wait_ld();
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = l == 0.f ? 0u
+                              : f32x2_to_bf16x2(__uint_as_float(o[8 * u + 2 * e]) * inv,
+                                                __uint_as_float(o[8 * u + 2 * e + 1]) * inv);
+            if (valid) dst[4 * i + u] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      } else {
+        a.part_lse[(size_t)p.slot * kRows + j] = lse;
+        float4* dst = reinterpret_cast<float4*>(a.part_o) + (size_t)p.slot * 32 * kRows + j;
+        if (c > 0) {
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            uint32_t o[32];
+            tc::tmem_ld32(col_o + 32 * i, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              dst[(size_t)(8 * i + u) * kRows] =
+                  make_float4(__uint_as_float(o[4 * u]) * inv, __uint_as_float(o[4 * u + 1]) * inv,
+                              __uint_as_float(o[4 * u + 2]) * inv, __uint_as_float(o[4 * u + 3]) * inv);
+          }
+        }
+      }
+      tc::fence_before_sync();
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 1) tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+// ---------------------------------------------------------------- joining the pieces
+// An item that a cut runs through: CTA (c - 1, s) of the first cut c within it joins 32 of its rows.
+constexpr int kSlices = kRows / 32;
+
+__global__ void __launch_bounds__(256) prompt_join_kernel(const PromptArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int parts = a.plan->parts, cut = blockIdx.x + 1;
+  const long long* place = a.part_place;
+  if (cut >= parts) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long x0 = place[cut];
+  const int r = find_request(a.first_place, a.R, x0, lane);
+  int row0, key0;
+  bool good;
+  const Request q = request(a, r, row0, key0, good);
+  const long long x = x0 - a.first_place[r], per = places(q);
+  const int head = head_at(x, per, a.H);
+  const long long rest = x - head * per;
+  const int u = item_at(q, rest);
+  const long long start = x0 - (rest - before(q, u)), end = start + item_tiles(q, u);
+  if (start == x0 || place[cut - 1] > start) return;
+  const int j = blockIdx.y * 32 + lane, rows = min(q.n - u * kRows, kRows);
+  if (j >= rows) return;
+  // Pieces: the tail of part cut - 1, then the heads of the parts from `cut` on.
+  int last = cut;
+  while (last + 1 < parts && place[last + 1] < end) ++last;
+  float top = -INFINITY;
+  for (int p = cut - 1; p <= last; ++p)
+    top = fmaxf(top, a.part_lse[(size_t)(p < cut ? 2 * p + 1 : 2 * p) * kRows + j]);
+  const float base = top == -INFINITY ? 0.f : top;
+  float acc[16], z = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+  for (int p = cut - 1; p <= last; ++p) {
+    const int slot = p < cut ? 2 * p + 1 : 2 * p;
+    const float w = ex2(a.part_lse[(size_t)slot * kRows + j] - base);
+    if (w == 0.f) continue;                      // nothing there: its rows may not be written
+    z += w;
+    const float4* src = reinterpret_cast<const float4*>(a.part_o) + ((size_t)slot * 32 + warp * 4) * kRows + j;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = src[(size_t)i * kRows];
+      acc[4 * i] += w * v.x;
+      acc[4 * i + 1] += w * v.y;
+      acc[4 * i + 2] += w * v.z;
+      acc[4 * i + 3] += w * v.w;
+    }
+  }
+  const float inv = z > 0.f ? 1.f / z : z;       // NaN stays
+  const size_t row = (size_t)(row0 + u * kRows + j) * a.H + head;
+  if (a.lse && warp == 0) a.lse[row] = z > 0.f ? base + log2f(z) : z == 0.f ? -INFINITY : z;
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = f32x2_to_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+  uint4* dst = reinterpret_cast<uint4*>(a.out + row * kV + warp * 16);
+  dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+int check_prompt(const mla_prompt_shape* s) {
+  if (!s) return MLA_ERR_NULL;
+  if (s->R < 1 || s->R > kMaxR || s->tokens < 0 || s->tokens > (1 << 24) || s->keys < 0 ||
+      s->keys > (1 << 24) || s->H < 1 || s->H > (1 << 12) || s->kv_heads < 1 ||
+      s->H % s->kv_heads != 0 || (s->causal != 0 && s->causal != 1) || s->num_ctas < 1 ||
+      s->num_ctas > 2048)
+    return MLA_ERR_SHAPE;
+  return MLA_OK;
+}
+size_t prompt_bytes(const mla_prompt_shape* s) {
+  return plan_bytes(s->R, s->num_ctas) + lse_bytes(s->num_ctas) + 2 * (size_t)s->num_ctas * kSlotBytes;
+}
+
+int32_t prompt_impl(const mla_prompt_shape* s, const void* q, const void* k_nope, const void* k_rope,
+                    const void* v, const int32_t* cu_tokens, const int32_t* cu_keys, float sm_scale,
+                    void* workspace, size_t workspace_bytes_given, void* out, float* lse,
+                    int32_t* status, mla_stream_t stream, unsigned long long wait_limit_ns,
+                    int withhold) {
+  int st = check_prompt(s);
+  if (st != MLA_OK) return st;
+  if (s->q_token_stride < kNope + kRope || s->q_head_stride < kNope + kRope ||
+      s->k_token_stride < kNope || s->k_head_stride < kNope || s->v_token_stride < kV ||
+      s->v_head_stride < kV || s->rope_stride < kRope)
+    return MLA_ERR_SHAPE;
+  if (!std::isfinite(sm_scale) || !(sm_scale > 0.f)) return MLA_ERR_SHAPE;
+  if (s->tokens == 0) return MLA_OK;
+  if (!q || !cu_tokens || !out || !workspace || (s->keys > 0 && (!k_nope || !k_rope || !v)))
+    return MLA_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(k_nope, 16) || !aligned(k_rope, 16) || !aligned(v, 16) ||
+      !aligned(out, 16) || !aligned(lse, 4) || !aligned(cu_tokens, 4) || !aligned(cu_keys, 4) ||
+      !aligned(workspace, 256) || !aligned(status, 4) || s->q_token_stride % 8 || s->q_head_stride % 8 ||
+      s->k_token_stride % 8 || s->k_head_stride % 8 || s->v_token_stride % 8 || s->v_head_stride % 8 ||
+      s->rope_stride % 8)
+    return MLA_ERR_ALIGN;
+  if (workspace_bytes_given < prompt_bytes(s)) return MLA_ERR_WORKSPACE;
+  if ((st = check_device()) != MLA_OK) return st;
+
+  PromptArgs a;
+  char* ws = static_cast<char*>(workspace);
+  a.cu = cu_tokens;
+  a.cu_keys = cu_keys;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.plan = reinterpret_cast<Plan*>(ws);
+  a.first_place = reinterpret_cast<long long*>(ws + sizeof(Plan));
+  a.first_item = a.first_place + s->R + 1;
+  a.part_place = a.first_item + s->R + 1;
+  a.part_lse = reinterpret_cast<float*>(ws + plan_bytes(s->R, s->num_ctas));
+  a.part_o = reinterpret_cast<float*>(ws + plan_bytes(s->R, s->num_ctas) + lse_bytes(s->num_ctas));
+  a.status = status;
+  a.scale_log2 = (float)((double)sm_scale * 1.4426950408889634);
+  a.R = s->R;
+  a.T = s->tokens;
+  a.Tk = s->keys;
+  a.H = s->H;
+  a.group = s->H / s->kv_heads;
+  a.causal = s->causal;
+  a.ctas = s->num_ctas;
+  a.wait_limit_ns = wait_limit_ns;
+  a.withhold = withhold;
+  // Without keys the maps of K and V stand on the queries; nothing is read through them.
+  CUtensorMap tq, tk, tr, tv;
+  const void* kn = s->keys ? k_nope : q;
+  const void* kr = s->keys ? k_rope : q;
+  const void* kv = s->keys ? v : q;
+  const cuuint64_t T = (cuuint64_t)s->tokens, Tk = s->keys ? (cuuint64_t)s->keys : 1;
+  const cuuint64_t q_dims[3] = {(kNope + kRope) * 2, (cuuint64_t)s->H, T};
+  const cuuint64_t q_str[2] = {(cuuint64_t)s->q_head_stride * 2, (cuuint64_t)s->q_token_stride * 2};
+  const cuuint64_t k_dims[3] = {kNope * 2, s->keys ? (cuuint64_t)s->kv_heads : 1, Tk};
+  const cuuint64_t k_str[2] = {(cuuint64_t)s->k_head_stride * 2, (cuuint64_t)s->k_token_stride * 2};
+  const cuuint64_t v_dims[3] = {kV * 2, s->keys ? (cuuint64_t)s->kv_heads : 1, Tk};
+  const cuuint64_t v_str[2] = {(cuuint64_t)s->v_head_stride * 2, (cuuint64_t)s->v_token_stride * 2};
+  const cuuint64_t r_dims[2] = {kRope * 2, Tk}, r_str[1] = {(cuuint64_t)s->rope_stride * 2};
+  const cuuint32_t box3[3] = {128, 1, 128}, box2[2] = {128, 128};
+  if (!dec::encode(&tq, q, 3, q_dims, q_str, box3, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !dec::encode(&tk, kn, 3, k_dims, k_str, box3, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !dec::encode(&tv, kv, 3, v_dims, v_str, box3, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !dec::encode(&tr, kr, 2, r_dims, r_str, box2, CU_TENSOR_MAP_SWIZZLE_128B))
+    return MLA_ERR_CUDA;
+  static bool attr_set[64] = {};
+  if (dec::set_smem(prompt_kernel, kSmemBytes, attr_set) != cudaSuccess) return MLA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3((unsigned)(cdiv(s->R, 32) * 32));
+  if (cudaLaunchKernelEx(&cfg, prompt_plan_kernel, a) != cudaSuccess) return MLA_ERR_CUDA;
+  // No more CTAs than the batch can have places.
+  const long long items_most = (long long)s->H * (cdiv(s->tokens, kRows) + s->R);
+  const long long places_most = items_most * (1 + cdiv(s->keys, kKeys));
+  cfg.gridDim = dim3((unsigned)(places_most < s->num_ctas ? places_most : s->num_ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  if (cudaLaunchKernelEx(&cfg, prompt_kernel, a, tq, tk, tr, tv) != cudaSuccess) return MLA_ERR_CUDA;
+  // Requests of so few keys that no item can be cut leave nothing to join.
+  if (cdiv(s->keys, kKeys) <= kUncut || s->num_ctas < 2) return MLA_OK;
+  cfg.gridDim = dim3((unsigned)(s->num_ctas - 1), kSlices);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, prompt_join_kernel, a) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace mlafold
+
+using namespace mlafold;
+
+extern "C" int32_t mla_prompt_workspace_bytes(const mla_prompt_shape* s, size_t* bytes) {
+  const int st = check_prompt(s);
+  if (st != MLA_OK) return st;
+  if (!bytes) return MLA_ERR_NULL;
+  *bytes = prompt_bytes(s);
+  return MLA_OK;
+}
+
+extern "C" int32_t mla_prompt_attention(const mla_prompt_shape* s, const void* q, const void* k_nope,
+                                        const void* k_rope, const void* v, const int32_t* cu_tokens,
+                                        const int32_t* cu_keys, float sm_scale, void* workspace,
+                                        size_t workspace_bytes, void* out, float* lse,
+                                        int32_t* status, mla_stream_t stream) {
+  return prompt_impl(s, q, k_nope, k_rope, v, cu_tokens, cu_keys, sm_scale, workspace, workspace_bytes,
+                     out, lse, status, stream, kWaitLimitNs, 0);
+}
+
+extern "C" int32_t mla_prompt_attention_wait_test(const mla_prompt_shape* s, const void* q,
+                                                  const void* k_nope, const void* k_rope,
+                                                  const void* v, const int32_t* cu_tokens,
+                                                  const int32_t* cu_keys, float sm_scale,
+                                                  void* workspace, size_t workspace_bytes, void* out,
+                                                  float* lse, int32_t* status,
+                                                  uint64_t wait_limit_ns, mla_stream_t stream) {
+  if (!status) return MLA_ERR_NULL;
+  if (wait_limit_ns < 1000000ull || wait_limit_ns > kWaitLimitNs) return MLA_ERR_SHAPE;
+  return prompt_impl(s, q, k_nope, k_rope, v, cu_tokens, cu_keys, sm_scale, workspace, workspace_bytes,
+                     out, lse, status, stream, wait_limit_ns, 1);
+}

@@ -1,0 +1,107 @@
+// The work of a batch of prompts: items of 256 query rows of one head, each with the
+// tiles of 128 keys that its rows see, and how all items lie on one line of places (a
+// place is a tile). Host and device code include this.
+#pragma once
+
+#include "internal.h"
+
+namespace mlafold {
+namespace prompt {
+
+constexpr int kRows = 256;       // query rows of an item: two halves of 128
+constexpr int kHalf = 128;
+constexpr int kKeys = 128;       // keys of a tile
+constexpr int kUncut = 4;        // items of no more tiles are never cut
+constexpr int kMinPart = 3;      // tiles of a part, at least
+constexpr int kWhole = 4;        // items stay whole where a CTA has so many of the longest's tiles
+
+// A request of n query tokens and m keys; causal: query i sees keys j <= i + m - n.
+struct Request {
+  int n, m;
+  bool causal;
+};
+
+// ceil(x / 128) for any x.
+__host__ __device__ inline int tiles_of(int x) { return x >= 0 ? (x + 127) >> 7 : -((-x) >> 7); }
+
+__host__ __device__ inline int items(const Request& q) { return (q.n + kRows - 1) / kRows; }
+// Keys that query row i sees.
+__host__ __device__ inline int limit(const Request& q, int i) {
+  if (!q.causal) return q.m;
+  const int e = i + 1 + (q.m - q.n);
+  return e < 0 ? 0 : e < q.m ? e : q.m;
+}
+// Places of item u: the tiles that its last row sees, one where there are none.
+__host__ __device__ inline int item_tiles(const Request& q, int u) {
+  const int last = (u + 1) * kRows < q.n ? (u + 1) * kRows : q.n;
+  const int t = tiles_of(limit(q, last - 1));
+  return t < 1 ? 1 : t;
+}
+// Places of the items before item u, 0 <= u <= items. All items but the last have 256 rows,
+// so item v of them sees 256 (v + 1) + m - n keys: max(1, 2 (v + 1) + ceil((m - n) / 128))
+// tiles, of which the first z are ones.
+__host__ __device__ inline long long before(const Request& q, int u) {
+  const int I = items(q);
+  if (I == 0) return 0;
+  const long long v = u < I ? u : I - 1, last = u < I ? 0 : item_tiles(q, I - 1);
+  if (!q.causal) {
+    const int t = tiles_of(q.m);
+    return v * (t < 1 ? 1 : t) + last;
+  }
+  const long long c = tiles_of(q.m - q.n);
+  long long z = c < 0 ? (-c) >> 1 : 0;
+  if (z > v) z = v;
+  return z + (v * (v + 1) - z * (z + 1)) + (v - z) * c + last;
+}
+__host__ __device__ inline long long places(const Request& q) { return before(q, items(q)); }
+// x = head * per + rest, 0 <= rest < per, without a division (the kernel that splits its registers
+// among its warps may call no function).
+__host__ __device__ inline int head_at(long long x, long long per, int H) {
+  int lo = 0, hi = H;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (mid * per <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+// The item that holds place x of its head, 0 <= x < places.
+__host__ __device__ inline int item_at(const Request& q, long long x) {
+  int lo = 0, hi = items(q);
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (before(q, mid) <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// The plan in the workspace: words, then the requests' first places and items (R + 1 each), then
+// where the parts begin (parts + 1).
+struct Plan {
+  long long total, all_items;    // places and items of the batch
+  int parts;                     // > 0: the line is cut into so many; 0: whole items, claimed
+  int claimed;                   // items claimed beyond the first of each CTA
+};
+// Where part p begins.
+__host__ __device__ inline long long part_at(long long total, int parts, int p) {
+  return cdiv(total * p, parts);
+}
+// How a batch is shared out among `ctas` CTAs, by its places and its longest item: whole items
+// where a CTA's share is worth several of them (they are claimed longest first within each head,
+// so that little is left over at the end and the CTAs work on few heads at a time, whose keys
+// stay in L2), else equal parts of the line.
+__host__ __device__ inline int parts_of(long long total, int longest, int ctas) {
+  if (longest <= kUncut || total >= (long long)kWhole * longest * ctas) return 0;
+  const long long p = cdiv(total, kMinPart);
+  return (int)(p < ctas ? p : ctas);
+}
+
+constexpr size_t kSlotBytes = (size_t)kRows * 128 * 4;     // a piece's FP32 rows
+inline size_t plan_bytes(int R, int ctas) {
+  return align256(sizeof(Plan) + (2 * (size_t)(R + 1) + ctas + 1) * 8);
+}
+inline size_t lse_bytes(int ctas) { return align256((size_t)2 * ctas * kRows * 4); }
+
+}  // namespace prompt
+}  // namespace mlafold
