@@ -11,8 +11,8 @@
 // while the softmax of one half runs, the tensor pipe multiplies for the other.
 //   S[128, 128 keys] = Q K^T, 12 MMAs;  O[128, 128] += P V, 8 MMAs, P from TMEM.
 // TMEM holds both halves' S and O (4 x 128 columns); P (BF16) takes the place of the S it was
-// made from. Warp 0 loads by TMA (Q, and K and V in a ring of 16 KB blocks), warp 1
-// issues the MMAs, warps 4-7 and 8-11 are the softmax of the halves: a thread owns a row, so
+// made from. Warp 0 loads by TMA (Q, and K and V in a ring of 16 KB blocks), warps
+// 1 and 2 issue the halves' MMAs, warps 4-7 and 8-11 are the softmax of the halves: a thread owns a row, so
 // that no maximum or sum crosses threads. The maximum that P is relative to moves only when
 // a score exceeds it by 2^8 (O and the sum are then rescaled); P is rounded to BF16 (2^-8,
 // as the inputs are), its sum is of the FP32 values.
@@ -44,7 +44,7 @@ constexpr int kRing = 3;
 constexpr int kOffRing = 2 * kQBlocks * kBlock;
 constexpr int kOffRope = kOffRing + kRing * 2 * kBlock;
 constexpr int kOffCtl = kOffRope + 2 * kBlock;
-constexpr int kThreads = 128 + 2 * kHalf;        // warps 2 and 3 only give their registers
+constexpr int kThreads = 128 + 2 * kHalf;        // warp 3 only gives its registers
 // Registers a thread at the launch (384 x 168 = 64,512), and after the split: 128 x 80 + 256 x 208.
 constexpr int kRegsFew = 80, kRegsMany = 208;
 constexpr uint32_t kTmemCols = 512, kColO = 256;
@@ -79,7 +79,7 @@ struct PromptCtl {
   uint64_t full[kRing], empty[kRing];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t job_full[2], job_empty[2];
-  uint64_t drain;
+  uint64_t drain[2];
   Piece job[2];
   uint32_t tmem_base;
   int abort_flag;
@@ -258,13 +258,13 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
       tc::mbar_init(&ctl->p_full[i], kHalf);
       tc::mbar_init(&ctl->o_full[i], 1);
       tc::mbar_init(&ctl->job_full[i], 1);
-      tc::mbar_init(&ctl->job_empty[i], 1 + 2 * kHalf);
+      tc::mbar_init(&ctl->job_empty[i], 2 + 2 * kHalf);
+      tc::mbar_init(&ctl->drain[i], 1);
     }
     for (int i = 0; i < kRing; ++i) {
       tc::mbar_init(&ctl->full[i], 1);
-      tc::mbar_init(&ctl->empty[i], 1);
+      tc::mbar_init(&ctl->empty[i], 2);
     }
-    tc::mbar_init(&ctl->drain, 1);
     ctl->abort_flag = 0;
     tc::fence_barrier_init();
     tc::prefetch_tmap(&tm_q);
@@ -407,64 +407,67 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
         }
       }
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMAs
+  } else if (warp <= 2) {
+    // ------------------------------------------------------------ MMAs of half h
     if (lane == 0) {
-      uint32_t slot = 0, xq = 0, xp = 0;         // bit h: the phase of half h's barrier
-      const uint32_t s_q = tc::smem_u32(smem), s_ring = tc::smem_u32(smem + kOffRing);
-      const uint32_t s_rope = tc::smem_u32(smem + kOffRope);
+      const int h = warp - 1;
+      uint32_t slot = 0, xq = 0, xp = 0;
+      const uint32_t q = tc::smem_u32(smem) + h * kQBlocks * kBlock;
+      const uint32_t s_ring = tc::smem_u32(smem + kOffRing), s_rope = tc::smem_u32(smem + kOffRope);
+      const uint32_t col_s = tmem + h * kKeys, col_o = tmem + kColO + h * kV;
       Piece p;
       bool ok = true;
+      auto landed = [&](uint32_t at) {
+        return pr_wait(&ctl->full[at % kRing], (at / kRing) & 1, ctl, a);
+      };
       for (uint32_t seq = 0; ok && take(ctl, seq, a, p); ++seq) {
-        const int c0 = half_tiles(p, 0), c1 = half_tiles(p, 1), nt = max(c0, c1);
-        // PV of tile t, then S of tile t + 1, half by half.
+        const int c = half_tiles(p, h), nt = max(c, half_tiles(p, h ^ 1));
+        // PV of tile t, then S of tile t + 1. A tile that only the other half multiplies is given back
+        // as it lands.
 #pragma unroll 1
-        for (int step = 0; step < 2 * (nt + 1); ++step) {
-          const int h = step & 1, t = (step >> 1) - 1, c = h ? c1 : c0;
-          // The half that reads a tile last gives its place in the ring back.
-          if (t >= 0 && t < c) {
+        for (int t = -1; t < nt; ++t) {
+          if (t >= 0) {
             const uint32_t at = slot + 2 * t + 1;
-            if (!(ok = pr_wait(&ctl->p_full[h], xp >> h & 1, ctl, a) &&
-                       pr_wait(&ctl->full[at % kRing], (at / kRing) & 1, ctl, a)))
-              break;
-            xp ^= 1u << h;
-            tc::fence_after_sync();
-            const uint32_t vb = s_ring + at % kRing * 2 * kBlock;
+            if (!(ok = (t >= c || pr_wait(&ctl->p_full[h], xp++ & 1, ctl, a)) && landed(at))) break;
+            if (t < c) {
+              tc::fence_after_sync();
+              const uint32_t vb = s_ring + at % kRing * 2 * kBlock;
 #pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-              mma_bf16_ts(tmem + kColO + h * kV, tmem + h * kKeys + kk * 8,
-                          tc::smem_desc(vb + kk * 16 * 128, kBlock, 1024, tc::kSw128), kIdescO,
-                          t + kk != 0);
-            if (h == 1 || t >= c1) tc::mma_commit(&ctl->empty[at % kRing]);
-            if (t == c - 1) tc::mma_commit(&ctl->o_full[h]);
-          }
-          if (t + 1 < c) {
-            const uint32_t at = slot + 2 * (t + 1);
-            if (!(ok = pr_wait(&ctl->full[at % kRing], (at / kRing) & 1, ctl, a))) break;
-            if (t < 0) {
-              if (!(ok = pr_wait(&ctl->q_full[h], xq >> h & 1, ctl, a))) break;
-              xq ^= 1u << h;
+              for (int kk = 0; kk < kKeys / 16; ++kk)
+                mma_bf16_ts(col_o, col_s + kk * 8, tc::smem_desc(vb + kk * 16 * 128, kBlock, 1024, tc::kSw128),
+                            kIdescO, t + kk != 0);
+              tc::mma_commit(&ctl->empty[at % kRing]);
+              if (t == c - 1) tc::mma_commit(&ctl->o_full[h]);
+            } else {
+              tc::mbar_arrive(&ctl->empty[at % kRing]);
             }
-            tc::fence_after_sync();
-            const uint32_t kb = s_ring + at % kRing * 2 * kBlock, rb = s_rope + (at / 2 & 1) * kBlock;
-            const uint32_t qb = s_q + h * kQBlocks * kBlock;
+          }
+          if (t + 1 < nt) {
+            const uint32_t at = slot + 2 * (t + 1);
+            if (!(ok = landed(at))) break;
+            if (t + 1 < c) {
+              if (t < 0 && !(ok = pr_wait(&ctl->q_full[h], xq++ & 1, ctl, a))) break;
+              tc::fence_after_sync();
+              const uint32_t kb = s_ring + at % kRing * 2 * kBlock, rb = s_rope + (at / 2 & 1) * kBlock;
 #pragma unroll
-            for (int kk = 0; kk < 12; ++kk)
-              tc::mma_bf16(tmem + h * kKeys,
-                           tc::smem_desc(qb + (kk >> 2) * kBlock + (kk & 3) * 32, 16, 1024, tc::kSw128),
-                           tc::smem_desc((kk < 8 ? kb + (kk >> 2) * kBlock : rb) + (kk & 3) * 32, 16, 1024,
-                                         tc::kSw128),
-                           kIdescS, kk != 0);
-            if (h == 1 || t + 1 >= c1) tc::mma_commit(&ctl->empty[at % kRing]);
-            if (t + 1 == c - 1) tc::mma_commit(&ctl->q_empty[h]);
-            tc::mma_commit(&ctl->s_full[h]);
+              for (int kk = 0; kk < 12; ++kk)
+                tc::mma_bf16(col_s, tc::smem_desc(q + (kk >> 2) * kBlock + (kk & 3) * 32, 16, 1024, tc::kSw128),
+                             tc::smem_desc((kk < 8 ? kb + (kk >> 2) * kBlock : rb) + (kk & 3) * 32, 16, 1024,
+                                           tc::kSw128),
+                             kIdescS, kk != 0);
+              tc::mma_commit(&ctl->s_full[h]);
+              tc::mma_commit(&ctl->empty[at % kRing]);
+              if (t + 1 == c - 1) tc::mma_commit(&ctl->q_empty[h]);
+            } else {
+              tc::mbar_arrive(&ctl->empty[at % kRing]);
+            }
           }
         }
         slot += 2 * nt;
       }
-      tc::mma_commit(&ctl->drain);               // every MMA done before TMEM is released
+      tc::mma_commit(&ctl->drain[h]);            // every MMA done before TMEM is released
       const unsigned long long t0 = tc::globaltimer_ns();
-      while (!tc::mbar_try_wait(&ctl->drain, 0) && tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
+      while (!tc::mbar_try_wait(&ctl->drain[h], 0) && tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
       }
     }
   }
