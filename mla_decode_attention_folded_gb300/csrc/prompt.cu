@@ -12,10 +12,11 @@
 //   S[128, 128 keys] = Q K^T, 12 MMAs;  O[128, 128] += P V, 8 MMAs, P from TMEM.
 // TMEM holds both halves' S and O (4 x 128 columns); P (BF16) takes the place of the S it was
 // made from. Warp 0 loads by TMA (Q, and K and V in a ring of 16 KB blocks), warps
-// 1 and 2 issue the halves' MMAs, warps 4-7 and 8-11 are the softmax of the halves: a thread owns a row, so
-// that no maximum or sum crosses threads. The maximum that P is relative to moves only when
-// a score exceeds it by 2^8 (O and the sum are then rescaled); P is rounded to BF16 (2^-8,
-// as the inputs are), its sum is of the FP32 values.
+// 1 and 2 issue the halves' MMAs, eight warps each are the softmax of the halves: two threads
+// to a row, 64 keys each. The maximum that P is relative to moves only when a score exceeds it by
+// 2^8 (O and the sum are then rescaled), so that the two threads need no more than a
+// barrier's vote in most tiles; P is rounded to BF16 (2^-8, as the inputs are), its sum is of the
+// FP32 values.
 //
 // How the work is shared out is in prompt.h. The order of a CTA's MMAs is PV(t) before S(t + 1)
 // of the same half, so that S may overwrite P and its completion tells that O is final.
@@ -38,15 +39,17 @@ constexpr int kNope = 128, kRope = 64, kV = 128;
 constexpr int kBlock = 128 * 128;                // bytes: 128 rows of 64 BF16
 constexpr int kQBlocks = 3;                      // 192 dims
 // K's nope dims and V, two blocks each, take turns in a ring of three pairs; K's rope dims have
-// two blocks of their own. A tile's K goes where V was two tiles before, whose last reader
-// came after that tile's S: its rope block is free too, without a barrier of its own.
+// two blocks of their own. V goes where K was one tile before: once that is read, the rope block
+// of the tile after next is free too, and is loaded then. K, which comes where V was two tiles
+// before, is the late one: S begins with the rope dims and goes on block by block as they land.
 constexpr int kRing = 3;
 constexpr int kOffRing = 2 * kQBlocks * kBlock;
 constexpr int kOffRope = kOffRing + kRing * 2 * kBlock;
 constexpr int kOffCtl = kOffRope + 2 * kBlock;
-constexpr int kThreads = 128 + 2 * kHalf;        // warp 3 only gives its registers
-// Registers a thread at the launch (384 x 168 = 64,512), and after the split: 128 x 80 + 256 x 208.
-constexpr int kRegsFew = 80, kRegsMany = 208;
+constexpr int kSoft = 2 * kHalf;                 // softmax threads of a half: two to a row
+constexpr int kThreads = 128 + 2 * kSoft;        // warp 3 only gives its registers
+// Registers a thread at the launch (640 x 96 = 61,440), and after the split: 128 x 64 + 512 x 104.
+constexpr int kRegsFew = 64, kRegsMany = 104;
 constexpr uint32_t kTmemCols = 512, kColO = 256;
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;   // 2 s
 constexpr uint32_t kIdescS = tc::idesc_bf16_f32(kHalf, kKeys);
@@ -76,11 +79,13 @@ __device__ __forceinline__ int half_tiles(const Piece& p, int h) {
 
 struct PromptCtl {
   uint64_t q_full[2], q_empty[2];
-  uint64_t full[kRing], empty[kRing];
+  uint64_t full[kRing], empty[kRing];   // K's first block, or V
+  uint64_t full2[kRing], rope_full[2];  // K's second block, its rope block
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t job_full[2], job_empty[2];
   uint64_t drain[2];
   Piece job[2];
+  float row[2][kHalf];           // [half][row]: what the two threads of a row tell one another
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -191,7 +196,10 @@ __device__ __forceinline__ int find_request(const long long* first, int R, long 
 // ---------------------------------------------------------------- attention
 __device__ __forceinline__ bool pr_wait(uint64_t* bar, uint32_t parity, PromptCtl* ctl,
                                         const PromptArgs& a) {
-  if (tc::mbar_try_wait(bar, parity)) return true;
+  // Reading the timer takes longer than most waits: not before the barrier was tried for a while.
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (tc::mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = tc::globaltimer_ns();
   while (true) {
     if (tc::mbar_try_wait(bar, parity)) return true;
@@ -203,9 +211,10 @@ __device__ __forceinline__ bool pr_wait(uint64_t* bar, uint32_t parity, PromptCt
     }
   }
 }
-__device__ __forceinline__ bool take(PromptCtl* ctl, uint32_t seq, const PromptArgs& a, Piece& p) {
+// The next piece, for a whole warp; false at the end, or where the wait ran out.
+__device__ __forceinline__ bool take(PromptCtl* ctl, uint32_t seq, const PromptArgs& a, Piece& p, bool read) {
   const int b = seq & 1;
-  if (!pr_wait(&ctl->job_full[b], (seq >> 1) & 1, ctl, a)) return false;
+  if (!__all_sync(0xffffffffu, pr_wait(&ctl->job_full[b], (seq >> 1) & 1, ctl, a))) return false;
   const volatile Piece* s = &ctl->job[b];
   p.row0 = s->row0;
   p.rows = s->rows;
@@ -217,8 +226,15 @@ __device__ __forceinline__ bool take(PromptCtl* ctl, uint32_t seq, const PromptA
   p.t1 = s->t1;
   p.slot = s->slot;
   p.causal = s->causal;
-  tc::mbar_arrive(&ctl->job_empty[b]);
+  __syncwarp();
+  if (read) tc::mbar_arrive(&ctl->job_empty[b]);
   return p.rows > 0;
+}
+// One lane of a whole warp, always the same.
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
 }
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                             uint32_t idesc, bool accumulate) {
@@ -227,6 +243,22 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// A barrier of a half's softmax threads; whether any of them, or all, say so.
+__device__ __forceinline__ bool half_any(int h, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
+      " barrier.cta.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(1 + h), "n"(kSoft)
+      : "memory");
+  return r != 0;
 }
 __device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
   uint32_t r;
@@ -255,14 +287,16 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
       tc::mbar_init(&ctl->q_full[i], 1);
       tc::mbar_init(&ctl->q_empty[i], 1);
       tc::mbar_init(&ctl->s_full[i], 1);
-      tc::mbar_init(&ctl->p_full[i], kHalf);
+      tc::mbar_init(&ctl->p_full[i], kSoft / 32);
       tc::mbar_init(&ctl->o_full[i], 1);
       tc::mbar_init(&ctl->job_full[i], 1);
-      tc::mbar_init(&ctl->job_empty[i], 2 + 2 * kHalf);
+      tc::mbar_init(&ctl->job_empty[i], 2 + 2 * kSoft / 32);
       tc::mbar_init(&ctl->drain[i], 1);
+      tc::mbar_init(&ctl->rope_full[i], 1);
     }
     for (int i = 0; i < kRing; ++i) {
       tc::mbar_init(&ctl->full[i], 1);
+      tc::mbar_init(&ctl->full2[i], 1);
       tc::mbar_init(&ctl->empty[i], 2);
     }
     ctl->abort_flag = 0;
@@ -287,7 +321,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
   if (warp == 0) {
     // ------------------------------------------------------------ pieces and copies
-    uint32_t seq = 0, slot = 0, xq0 = 0, xq1 = 0;  // places of the ring, queries loaded per half
+    uint32_t seq = 0, slot = 0, ropes = 0, xq0 = 0, xq1 = 0;   // slot: K and V tiles loaded
     bool ok = true;
     auto wait0 = [&](uint64_t* bar, uint32_t parity) {
       int v = 1;
@@ -362,13 +396,28 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
       for (int i = 0; i < 2 * nt; ++i, ++slot) {               // K, V of every tile
         const int b = slot % kRing, key = p.key0 + (p.t0 + (i >> 1)) * kKeys, is_v = i & 1;
         if (slot >= kRing && !(ok = wait0(&ctl->empty[b], (slot / kRing - 1) & 1))) break;
-        if (lane == 0 && !(withheld && slot == 0)) {
+        auto load_rope = [&](int tile, int at) {
+          uint64_t* bar = &ctl->rope_full[tile & 1];
+          tc::mbar_arrive_expect_tx(bar, kBlock);
+          tc::tma_load_2d(smem + kOffRope + (tile & 1) * kBlock, &tm_r, bar, 0, at);
+        };
+        if (i == 0 || (is_v && i + 1 < 2 * nt)) ropes = slot / 2 + 1 + is_v;
+        if (lane == 0) {
           uint8_t* dst = smem + kOffRing + b * 2 * kBlock;
-          const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
-          tc::mbar_arrive_expect_tx(&ctl->full[b], (is_v ? 2 : 3) * kBlock);
-          tc::tma_load_3d(dst, tm, &ctl->full[b], 0, kvh, key);
-          tc::tma_load_3d(dst + kBlock, tm, &ctl->full[b], 128, kvh, key);
-          if (!is_v) tc::tma_load_2d(smem + kOffRope + (slot / 2 & 1) * kBlock, &tm_r, &ctl->full[b], 0, key);
+          if (is_v) {
+            tc::mbar_arrive_expect_tx(&ctl->full[b], 2 * kBlock);
+            tc::tma_load_3d(dst, &tm_v, &ctl->full[b], 0, kvh, key);
+            tc::tma_load_3d(dst + kBlock, &tm_v, &ctl->full[b], 128, kvh, key);
+            if (i + 1 < 2 * nt) load_rope(slot / 2 + 1, key + kKeys);
+          } else {
+            if (i == 0) load_rope(slot / 2, key);
+            if (!(withheld && slot == 0)) {
+              tc::mbar_arrive_expect_tx(&ctl->full[b], kBlock);
+              tc::tma_load_3d(dst, &tm_k, &ctl->full[b], 0, kvh, key);
+            }
+            tc::mbar_arrive_expect_tx(&ctl->full2[b], kBlock);
+            tc::tma_load_3d(dst + kBlock, &tm_k, &ctl->full2[b], 128, kvh, key);
+          }
         }
         if (i == 0) {
 #pragma unroll 1
@@ -400,6 +449,14 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
         while (!(withheld && i == 0) && !tc::mbar_try_wait(&ctl->full[i % kRing], (i / kRing) & 1) &&
                tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
         }
+      for (uint32_t i = slot < kRing ? 0 : slot - kRing; i < slot; ++i)
+        while (!(i & 1) && !tc::mbar_try_wait(&ctl->full2[i % kRing], (i / (2 * kRing)) & 1) &&
+               tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
+        }
+      for (uint32_t i = ropes < 2 ? 0 : ropes - 2; i < ropes; ++i)
+        while (!tc::mbar_try_wait(&ctl->rope_full[i & 1], (i >> 1) & 1) &&
+               tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
+        }
       for (int h = 0; h < 2; ++h) {
         const uint32_t x = h ? xq1 : xq0;
         while (x > 0 && !tc::mbar_try_wait(&ctl->q_full[h], (x - 1) & 1) &&
@@ -409,62 +466,81 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
     }
   } else if (warp <= 2) {
     // ------------------------------------------------------------ MMAs of half h
-    if (lane == 0) {
-      const int h = warp - 1;
-      uint32_t slot = 0, xq = 0, xp = 0;
-      const uint32_t q = tc::smem_u32(smem) + h * kQBlocks * kBlock;
-      const uint32_t s_ring = tc::smem_u32(smem + kOffRing), s_rope = tc::smem_u32(smem + kOffRope);
-      const uint32_t col_s = tmem + h * kKeys, col_o = tmem + kColO + h * kV;
+    // The whole warp goes through the waits, so that what the MMAs are given is the same in all
+    // lanes and stays in uniform registers; one lane issues.
+    const int h = __shfl_sync(0xffffffffu, warp, 0) - 1;
+    const bool one = elect();
+    uint32_t slot = 0, xq = 0, xp = 0;
+    const uint32_t q = tc::smem_u32(smem) + h * kQBlocks * kBlock;
+    const uint32_t s_ring = tc::smem_u32(smem + kOffRing), s_rope = tc::smem_u32(smem + kOffRope);
+    const uint32_t col_s = tmem + h * kKeys, col_o = tmem + kColO + h * kV;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return ok = __all_sync(0xffffffffu, pr_wait(bar, parity, ctl, a));
+    };
+    for (uint32_t seq = 0; ok; ++seq) {
       Piece p;
-      bool ok = true;
-      auto landed = [&](uint32_t at) {
-        return pr_wait(&ctl->full[at % kRing], (at / kRing) & 1, ctl, a);
-      };
-      for (uint32_t seq = 0; ok && take(ctl, seq, a, p); ++seq) {
-        const int c = half_tiles(p, h), nt = max(c, half_tiles(p, h ^ 1));
-        // PV of tile t, then S of tile t + 1. A tile that only the other half multiplies is given back
-        // as it lands.
+      if (!take(ctl, seq, a, p, one)) break;
+      const int c = __shfl_sync(0xffffffffu, half_tiles(p, h), 0);
+      const int nt = max(c, __shfl_sync(0xffffffffu, half_tiles(p, h ^ 1), 0));
+      // PV of tile t, then S of tile t + 1. A tile that only the other half multiplies is given back
+      // as it lands.
 #pragma unroll 1
-        for (int t = -1; t < nt; ++t) {
-          if (t >= 0) {
-            const uint32_t at = slot + 2 * t + 1;
-            if (!(ok = (t >= c || pr_wait(&ctl->p_full[h], xp++ & 1, ctl, a)) && landed(at))) break;
-            if (t < c) {
-              tc::fence_after_sync();
-              const uint32_t vb = s_ring + at % kRing * 2 * kBlock;
+      for (int t = -1; t < nt; ++t) {
+        if (t >= 0) {
+          const uint32_t at = slot + 2 * t + 1, b = at % kRing;
+          if (t < c && !wait(&ctl->p_full[h], xp++ & 1)) break;
+          if (!wait(&ctl->full[b], (at / kRing) & 1)) break;
+          if (t < c) {
+            tc::fence_after_sync();
+            const uint64_t v = tc::smem_desc(s_ring + b * 2 * kBlock, kBlock, 1024, tc::kSw128);
+            if (one) {
 #pragma unroll
               for (int kk = 0; kk < kKeys / 16; ++kk)
-                mma_bf16_ts(col_o, col_s + kk * 8, tc::smem_desc(vb + kk * 16 * 128, kBlock, 1024, tc::kSw128),
-                            kIdescO, t + kk != 0);
-              tc::mma_commit(&ctl->empty[at % kRing]);
+                mma_bf16_ts(col_o, col_s + kk * 8, v + (kk * 16 * 128 >> 4), kIdescO, t + kk != 0);
+              tc::mma_commit(&ctl->empty[b]);
               if (t == c - 1) tc::mma_commit(&ctl->o_full[h]);
-            } else {
-              tc::mbar_arrive(&ctl->empty[at % kRing]);
             }
-          }
-          if (t + 1 < nt) {
-            const uint32_t at = slot + 2 * (t + 1);
-            if (!(ok = landed(at))) break;
-            if (t + 1 < c) {
-              if (t < 0 && !(ok = pr_wait(&ctl->q_full[h], xq++ & 1, ctl, a))) break;
-              tc::fence_after_sync();
-              const uint32_t kb = s_ring + at % kRing * 2 * kBlock, rb = s_rope + (at / 2 & 1) * kBlock;
-#pragma unroll
-              for (int kk = 0; kk < 12; ++kk)
-                tc::mma_bf16(col_s, tc::smem_desc(q + (kk >> 2) * kBlock + (kk & 3) * 32, 16, 1024, tc::kSw128),
-                             tc::smem_desc((kk < 8 ? kb + (kk >> 2) * kBlock : rb) + (kk & 3) * 32, 16, 1024,
-                                           tc::kSw128),
-                             kIdescS, kk != 0);
-              tc::mma_commit(&ctl->s_full[h]);
-              tc::mma_commit(&ctl->empty[at % kRing]);
-              if (t + 1 == c - 1) tc::mma_commit(&ctl->q_empty[h]);
-            } else {
-              tc::mbar_arrive(&ctl->empty[at % kRing]);
-            }
+          } else if (one) {
+            tc::mbar_arrive(&ctl->empty[b]);
           }
         }
-        slot += 2 * nt;
+        if (t + 1 < nt) {
+          const uint32_t at = slot + 2 * (t + 1), b = at % kRing, n = at / 2;
+          if (t < 0 && c > 0 && !wait(&ctl->q_full[h], xq++ & 1)) break;
+          if (!wait(&ctl->rope_full[n & 1], (n >> 1) & 1)) break;
+          const uint64_t k = tc::smem_desc(s_ring + b * 2 * kBlock, 16, 1024, tc::kSw128);
+          const uint64_t r = tc::smem_desc(s_rope + (n & 1) * kBlock, 16, 1024, tc::kSw128);
+          const uint64_t qd = tc::smem_desc(q, 16, 1024, tc::kSw128);
+          const bool mine = t + 1 < c;
+          tc::fence_after_sync();
+          if (mine && one)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc::mma_bf16(col_s, qd + ((2 * kBlock + kk * 32) >> 4), r + (kk * 32 >> 4), kIdescS, kk != 0);
+          if (!wait(&ctl->full[b], (at / kRing) & 1)) break;
+          tc::fence_after_sync();
+          if (mine && one)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc::mma_bf16(col_s, qd + (kk * 32 >> 4), k + (kk * 32 >> 4), kIdescS, true);
+          if (!wait(&ctl->full2[b], (at / (2 * kRing)) & 1)) break;
+          tc::fence_after_sync();
+          if (mine && one) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc::mma_bf16(col_s, qd + ((kBlock + kk * 32) >> 4), k + ((kBlock + kk * 32) >> 4), kIdescS, true);
+            tc::mma_commit(&ctl->s_full[h]);
+            tc::mma_commit(&ctl->empty[b]);
+            if (t + 1 == c - 1) tc::mma_commit(&ctl->q_empty[h]);
+          } else if (one) {
+            tc::mbar_arrive(&ctl->empty[b]);
+          }
+        }
       }
+      slot += 2 * nt;
+    }
+    if (one) {
       tc::mma_commit(&ctl->drain[h]);            // every MMA done before TMEM is released
       const unsigned long long t0 = tc::globaltimer_ns();
       while (!tc::mbar_try_wait(&ctl->drain[h], 0) && tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
@@ -474,56 +550,69 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
     // ------------------------------------------------------------ softmax and output
-    const int h = (warp - 4) >> 2, quarter = warp & 3, j = h * kHalf + quarter * 32 + lane;
-    const uint32_t col_s = tmem + ((uint32_t)(quarter * 32) << 16) + h * kKeys;
-    const uint32_t col_o = tmem + ((uint32_t)(quarter * 32) << 16) + kColO + h * kV;
+    // Thread (h, side, row): keys 64 side .. of its row of S, dims 64 side .. of its row of O. After a
+    // wait that ran out a half's threads go on to the end of the piece without waiting, so that
+    // all meet at its barriers, and leave together.
+    const int h = (warp - 4) >> 3, side = (warp - 4) >> 2 & 1, quarter = warp & 3, row = quarter * 32 + lane;
+    const int j = h * kHalf + row;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t col_s = lanes + h * kKeys + side * 64, col_p = lanes + h * kKeys + side * 32;
+    const uint32_t col_o = lanes + kColO + h * kV + side * 64;
     uint32_t slot = 0, xs = 0, xo = 0;
     Piece p;
+    bool ok = true;
     auto all_wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, pr_wait(bar, parity, ctl, a));
     };
-    for (uint32_t seq = 0; __all_sync(0xffffffffu, take(ctl, seq, a, p)); ++seq) {
+    for (uint32_t seq = 0; !half_any(h, !(ok && take(ctl, seq, a, p, lane == 0))); ++seq) {
       const int c = half_tiles(p, h), nt = max(c, half_tiles(p, h ^ 1));
       const bool valid = j < p.rows;
       const int lim = valid ? row_limit(p, j) : INT_MAX;
       const int lowest = __reduce_min_sync(0xffffffffu, lim);
       float m = -INFINITY, l = 0.f;
-      bool ok = true;
-      for (int t = 0; t < c; ++t) {
-        if (!(ok = all_wait(&ctl->s_full[h], xs++ & 1))) break;
-        tc::fence_after_sync();
-        uint32_t raw[4][32];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tc::tmem_ld32(col_s + 32 * i, raw[i]);
-        tc::tmem_wait_ld();
-        const int key = (p.t0 + t) * kKeys;
-        if (key + kKeys > lowest) {              // keys that some row of the warp does not see
-#pragma unroll
-          for (int i = 0; i < kKeys; ++i)
-            if (key + i >= lim) raw[i >> 5][i & 31] = 0xFF800000u;
-        }
-        float mx[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          mx[i] = __uint_as_float(raw[i][0]);
-#pragma unroll
-          for (int e = 1; e < 32; ++e) mx[i] = fmaxf(mx[i], __uint_as_float(raw[i][e]));
-        }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-        // The first tile sets the maximum; later ones move it only when they exceed it by 2^8.
-        const bool moves = top > m + kLazy;
-        const float f = moves ? ex2(m - top) : 1.f;
-        if (moves) m = top;
-        if (t > 0 && __any_sync(0xffffffffu, moves)) {
-          l *= f;
 #pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            uint32_t o[32];
-            tc::tmem_ld32(col_o + 32 * i, o);
-            tc::tmem_wait_ld();
+      for (int t = 0; t < c; ++t) {
+        ok = all_wait(&ctl->s_full[h], xs++ & 1) && ok;
+        tc::fence_after_sync();
+        uint32_t raw[2][32];
+        tc::tmem_ld32(col_s, raw[0]);
+        tc::tmem_ld32(col_s + 32, raw[1]);
+        tc::tmem_wait_ld();
+        const int key = (p.t0 + t) * kKeys, mine = key + side * 64;
+        if (mine + 64 > lowest) {                // keys that some row of the warp does not see
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tc::tmem_st32(col_o + 32 * i, o);
+          for (int i = 0; i < 64; ++i)
+            if (mine + i >= lim) raw[i >> 5][i & 31] = 0xFF800000u;
+        }
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            mx[i] = max3(mx[i], __uint_as_float(raw[i][e]), __uint_as_float(raw[i][e + 1]));
+        float top = fmaxf(mx[0], mx[1]) * a.scale_log2;
+        // The first tile sets the maximum; later ones move it only when they exceed it by 2^8. The
+        // barrier also tells that S is read, which P may now overwrite.
+        if (half_any(h, top > m + kLazy)) {
+          if (side) ctl->row[h][row] = top;
+          half_any(h, false);
+          if (!side) ctl->row[h][row] = top = fmaxf(top, ctl->row[h][row]);
+          half_any(h, false);
+          if (side) top = ctl->row[h][row];
+          const bool moves = top > m + kLazy;
+          const float f = moves ? ex2(m - top) : 1.f;
+          if (moves) m = top;
+          l *= f;
+          if (t > 0 && __any_sync(0xffffffffu, moves)) {
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              uint32_t o[16];
+              tc::tmem_ld16(col_o + 16 * i, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tc::tmem_st16(col_o + 16 * i, o);
+            }
           }
         }
         const float base = m == -INFINITY ? 0.f : -m;
@@ -531,19 +620,18 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
         uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          uint32_t pk[32];
+          uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int at = 64 * i + 2 * e;
+          for (int e = 0; e < 16; ++e) {
             float x, y;
-            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(raw[at >> 5][at & 31]),
-                                              __uint_as_float(raw[at >> 5][(at & 31) + 1])), c2, b2), x, y);
+            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(raw[i][2 * e]), __uint_as_float(raw[i][2 * e + 1])),
+                                   c2, b2), x, y);
             x = ex2(x);
             y = ex2(y);
             sum[e & 1] = add_f32x2(sum[e & 1], pack_f32x2(x, y));
             pk[e] = f32x2_to_bf16x2(x, y);
           }
-          tc::tmem_st32(col_s + 32 * i, pk);
+          tc::tmem_st16(col_p + 16 * i, pk);
         }
         float s0, s1;
         unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
@@ -552,62 +640,63 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
         // and they are cleared so that 0 times them is 0.
         if (key + kKeys > p.m) {
           const uint32_t at = slot + 2 * t + 1;
-          ok = all_wait(&ctl->full[at % kRing], (at / kRing) & 1);
-          const int row = quarter * 32 + lane;
-          if (ok && key + row >= p.m)
-            for (int i = 0; i < 16; ++i)
-              *reinterpret_cast<uint4*>(smem + kOffRing + (at % kRing * 2 + (i >> 3)) * kBlock + row * 128 +
-                                        (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+          const bool landed = all_wait(&ctl->full[at % kRing], (at / kRing) & 1);
+          ok = ok && landed;
+          if (landed && key + row >= p.m)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(smem + kOffRing + (at % kRing * 2 + side) * kBlock + row * 128 + i * 16) =
+                  make_uint4(0, 0, 0, 0);
           tc::fence_proxy_async_smem();
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
-        tc::mbar_arrive(&ctl->p_full[h]);
-        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ctl->p_full[h]);
       }
-      if (!ok) break;
       slot += 2 * nt;
-      if (c > 0 && !all_wait(&ctl->o_full[h], xo++ & 1)) break;
+      // The rows' sums, of both threads.
+      if (side) ctl->row[h][row] = l;
+      half_any(h, false);
+      if (!side) ctl->row[h][row] = l += ctl->row[h][row];
+      if (c > 0) ok = all_wait(&ctl->o_full[h], xo++ & 1) && ok;
+      half_any(h, false);
+      if (side) l = ctl->row[h][row];
       tc::fence_after_sync();
       const float inv = l > 0.f ? rcp(l) : l;    // NaN stays
       const float lse = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
-      const size_t row = (size_t)(p.row0 + j) * a.H + p.head;
+      const size_t at = (size_t)(p.row0 + j) * a.H + p.head;
       if (p.slot < 0) {
-        if (valid && a.lse) a.lse[row] = lse;
-        uint4* dst = reinterpret_cast<uint4*>(a.out + row * kV);
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          uint32_t o[32];
-          if (c > 0) {
-            tc::tmem_ld32(col_o + 32 * i, o);
-            tc::tmem_wait_ld();
-          }
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = l == 0.f ? 0u
-                              : f32x2_to_bf16x2(__uint_as_float(o[8 * u + 2 * e]) * inv,
-                                                __uint_as_float(o[8 * u + 2 * e + 1]) * inv);
-            if (valid) dst[4 * i + u] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-      } else {
+        if (valid && a.lse && side == 0) a.lse[at] = lse;
+      } else if (side == 0) {
         a.part_lse[(size_t)p.slot * kRows + j] = lse;
-        float4* dst = reinterpret_cast<float4*>(a.part_o) + (size_t)p.slot * 32 * kRows + j;
-        if (c > 0) {
+      }
+      uint4* whole = reinterpret_cast<uint4*>(a.out + at * kV + side * 64);
+      float4* part = reinterpret_cast<float4*>(a.part_o) + ((size_t)p.slot * 32 + side * 16) * kRows + j;
 #pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            uint32_t o[32];
-            tc::tmem_ld32(col_o + 32 * i, o);
-            tc::tmem_wait_ld();
+      for (int i = 0; i < 4; ++i) {
+        uint32_t o[16];
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-              dst[(size_t)(8 * i + u) * kRows] =
-                  make_float4(__uint_as_float(o[4 * u]) * inv, __uint_as_float(o[4 * u + 1]) * inv,
-                              __uint_as_float(o[4 * u + 2]) * inv, __uint_as_float(o[4 * u + 3]) * inv);
-          }
+        for (int e = 0; e < 16; ++e) o[e] = 0;
+        if (c > 0) {
+          tc::tmem_ld16(col_o + 16 * i, o);
+          tc::tmem_wait_ld();
+        }
+        float f[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) f[e] = l == 0.f ? 0.f : __uint_as_float(o[e]) * inv;
+        if (p.slot < 0) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            if (valid && ok)
+              whole[2 * i + u] = make_uint4(f32x2_to_bf16x2(f[8 * u], f[8 * u + 1]),
+                                            f32x2_to_bf16x2(f[8 * u + 2], f[8 * u + 3]),
+                                            f32x2_to_bf16x2(f[8 * u + 4], f[8 * u + 5]),
+                                            f32x2_to_bf16x2(f[8 * u + 6], f[8 * u + 7]));
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            part[(size_t)(4 * i + u) * kRows] = make_float4(f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
         }
       }
       tc::fence_before_sync();
