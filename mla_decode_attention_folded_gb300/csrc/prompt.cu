@@ -83,6 +83,7 @@ struct PromptCtl {
   uint64_t full2[kRing], rope_full[2];  // K's second block, its rope block
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t job_full[2], job_empty[2];
+  uint64_t turn[2];              // the other half's MMAs of the step are issued
   uint64_t drain[2];
   Piece job[2];
   float row[2][kHalf];           // [half][row]: what the two threads of a row tell one another
@@ -291,6 +292,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
       tc::mbar_init(&ctl->o_full[i], 1);
       tc::mbar_init(&ctl->job_full[i], 1);
       tc::mbar_init(&ctl->job_empty[i], 2 + 2 * kSoft / 32);
+      tc::mbar_init(&ctl->turn[i], 1);
       tc::mbar_init(&ctl->drain[i], 1);
       tc::mbar_init(&ctl->rope_full[i], 1);
     }
@@ -470,7 +472,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
     // lanes and stays in uniform registers; one lane issues.
     const int h = __shfl_sync(0xffffffffu, warp, 0) - 1;
     const bool one = elect();
-    uint32_t slot = 0, xq = 0, xp = 0;
+    uint32_t slot = 0, xq = 0, xp = 0, turn = h ^ 1;   // half 0 begins
     const uint32_t q = tc::smem_u32(smem) + h * kQBlocks * kBlock;
     const uint32_t s_ring = tc::smem_u32(smem + kOffRing), s_rope = tc::smem_u32(smem + kOffRope);
     const uint32_t col_s = tmem + h * kKeys, col_o = tmem + kColO + h * kV;
@@ -483,60 +485,70 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
       if (!take(ctl, seq, a, p, one)) break;
       const int c = __shfl_sync(0xffffffffu, half_tiles(p, h), 0);
       const int nt = max(c, __shfl_sync(0xffffffffu, half_tiles(p, h ^ 1), 0));
-      // PV of tile t, then S of tile t + 1. A tile that only the other half multiplies is given back
-      // as it lands.
+      // PV of tile t, then S of tile t + 1, the halves in turn: issued as they come, the halves' MMAs
+      // would mingle, both finish late, and both softmaxes then run while the tensor pipe
+      // waits. A tile that only the other half multiplies is given back
+      // as it lands. What the copies bring is waited for before P, where it is there by then, so
+      // that nothing stands between P and the MMAs.
 #pragma unroll 1
       for (int t = -1; t < nt; ++t) {
+        const uint32_t av = slot + 2 * t + 1, bv = av % kRing;        // V of tile t
+        const uint32_t ak = av + 1, bk = ak % kRing, n = ak >> 1;     // K of tile t + 1
+        const bool has_k = t + 1 < nt, mine = t + 1 < c;
+        if (t < 0 && c > 0 && !wait(&ctl->q_full[h], xq++ & 1)) break;
+        if (t >= 0 && !wait(&ctl->full[bv], (av / kRing) & 1)) break;
+        const bool early = has_k && tc::mbar_test_wait(&ctl->rope_full[n & 1], (n >> 1) & 1) &&
+                           tc::mbar_test_wait(&ctl->full[bk], (ak / kRing) & 1) &&
+                           tc::mbar_test_wait(&ctl->full2[bk], (ak / (2 * kRing)) & 1);
+        const bool landed = __all_sync(0xffffffffu, early);
+        if (t >= 0 && t < c && !wait(&ctl->p_full[h], xp++ & 1)) break;
+        if (!wait(&ctl->turn[h], turn++ & 1)) break;
         if (t >= 0) {
-          const uint32_t at = slot + 2 * t + 1, b = at % kRing;
-          if (t < c && !wait(&ctl->p_full[h], xp++ & 1)) break;
-          if (!wait(&ctl->full[b], (at / kRing) & 1)) break;
-          if (t < c) {
-            tc::fence_after_sync();
-            const uint64_t v = tc::smem_desc(s_ring + b * 2 * kBlock, kBlock, 1024, tc::kSw128);
-            if (one) {
+          tc::fence_after_sync();
+          const uint64_t v = tc::smem_desc(s_ring + bv * 2 * kBlock, kBlock, 1024, tc::kSw128);
+          if (t < c && one) {
 #pragma unroll
-              for (int kk = 0; kk < kKeys / 16; ++kk)
-                mma_bf16_ts(col_o, col_s + kk * 8, v + (kk * 16 * 128 >> 4), kIdescO, t + kk != 0);
-              tc::mma_commit(&ctl->empty[b]);
-              if (t == c - 1) tc::mma_commit(&ctl->o_full[h]);
-            }
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              mma_bf16_ts(col_o, col_s + kk * 8, v + (kk * 16 * 128 >> 4), kIdescO, t + kk != 0);
+            tc::mma_commit(&ctl->empty[bv]);
+            if (t == c - 1) tc::mma_commit(&ctl->o_full[h]);
           } else if (one) {
-            tc::mbar_arrive(&ctl->empty[b]);
+            tc::mbar_arrive(&ctl->empty[bv]);
           }
         }
-        if (t + 1 < nt) {
-          const uint32_t at = slot + 2 * (t + 1), b = at % kRing, n = at / 2;
-          if (t < 0 && c > 0 && !wait(&ctl->q_full[h], xq++ & 1)) break;
-          if (!wait(&ctl->rope_full[n & 1], (n >> 1) & 1)) break;
-          const uint64_t k = tc::smem_desc(s_ring + b * 2 * kBlock, 16, 1024, tc::kSw128);
+        if (has_k) {
+          const uint64_t k = tc::smem_desc(s_ring + bk * 2 * kBlock, 16, 1024, tc::kSw128);
           const uint64_t r = tc::smem_desc(s_rope + (n & 1) * kBlock, 16, 1024, tc::kSw128);
           const uint64_t qd = tc::smem_desc(q, 16, 1024, tc::kSw128);
-          const bool mine = t + 1 < c;
+          if (!landed && !wait(&ctl->rope_full[n & 1], (n >> 1) & 1)) break;
           tc::fence_after_sync();
           if (mine && one)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               tc::mma_bf16(col_s, qd + ((2 * kBlock + kk * 32) >> 4), r + (kk * 32 >> 4), kIdescS, kk != 0);
-          if (!wait(&ctl->full[b], (at / kRing) & 1)) break;
+          if (!landed && !wait(&ctl->full[bk], (ak / kRing) & 1)) break;
           tc::fence_after_sync();
           if (mine && one)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               tc::mma_bf16(col_s, qd + (kk * 32 >> 4), k + (kk * 32 >> 4), kIdescS, true);
-          if (!wait(&ctl->full2[b], (at / (2 * kRing)) & 1)) break;
+          if (!landed && !wait(&ctl->full2[bk], (ak / (2 * kRing)) & 1)) break;
           tc::fence_after_sync();
-          if (mine && one) {
+          if (mine && one)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               tc::mma_bf16(col_s, qd + ((kBlock + kk * 32) >> 4), k + ((kBlock + kk * 32) >> 4), kIdescS, true);
+        }
+        if (has_k && one) {
+          if (mine) {
             tc::mma_commit(&ctl->s_full[h]);
-            tc::mma_commit(&ctl->empty[b]);
+            tc::mma_commit(&ctl->empty[bk]);
             if (t + 1 == c - 1) tc::mma_commit(&ctl->q_empty[h]);
-          } else if (one) {
-            tc::mbar_arrive(&ctl->empty[b]);
+          } else {
+            tc::mbar_arrive(&ctl->empty[bk]);
           }
         }
+        if (one) tc::mbar_arrive(&ctl->turn[h ^ 1]);
       }
       slot += 2 * nt;
     }
