@@ -644,13 +644,13 @@ typedef struct {
  *   sm_scale   finite, > 0.
  *   workspace  >= mla_prompt_workspace_bytes(shape) bytes, device, 256-byte aligned; calls
  *              that share one must not overlap. Its contents need not be initialised.
- *   out        [tokens, H, 128] BF16, device, 16-byte aligned; lse [tokens, H] FP32 base-2 or
+ *   out        [tokens, H, 128] BF16, device, 32-byte aligned; lse [tokens, H] FP32 base-2 or
  *              NULL. A token that sees no key gets out = 0, lse = -inf.
  *   status     optional int32 device word: MLA_FAULT_WORK_ITEM (offsets that descend or
  *              leave the rows: that request is skipped), MLA_FAULT_WAIT_TIMEOUT.
  * What lies between and behind the requests' rows and keys reaches no result, whatever its
- * bits. Within a request a NaN or infinity in k or q reaches the rows that see it; one in v
- * may also reach rows up to 127 places before them (0 times it, in the same tile of keys).
+ * bits. Within a request a NaN or infinity reaches the rows that see it and no others; one in v
+ * its own dim alone (as NaN, or as the infinity).
  * BF16 products, FP32 scores, sums and accumulation; the weights are rounded to BF16 for
  * their product with v. */
 int32_t mla_prompt_workspace_bytes(const mla_prompt_shape *shape, size_t *bytes);

@@ -7,25 +7,29 @@
 // from the end). The rope dims of a key are one vector for all heads.
 //
 // Bound by the BF16 tensor pipe: 640 FLOP per (query, key, head) against 644 bytes per (query,
-// head). A CTA takes 256 query rows of one head as two halves of 128, each the M of its MMAs:
-// while the softmax of one half runs, the tensor pipe multiplies for the other.
-//   S[128, 128 keys] = Q K^T, 12 MMAs;  O[128, 128] += P V, 8 MMAs, P from TMEM.
-// TMEM holds both halves' S and O (4 x 128 columns); P (BF16) takes the place of the S it was
-// made from. Warp 0 loads by TMA (Q, and K and V in a ring of 16 KB blocks), warps
-// 1 and 2 issue the halves' MMAs, eight warps each are the softmax of the halves: two threads
-// to a row, 64 keys each. The maximum that P is relative to moves only when a score exceeds it by
-// 2^8 (O and the sum are then rescaled), so that the two threads need no more than a
-// barrier's vote in most tiles; P is rounded to BF16 (2^-8, as the inputs are), its sum is of the
-// FP32 values.
+// head). A pair of CTAs takes 512 query rows of one head as two halves of 256, each the M of
+// its MMAs (cta_group::2: 128 rows in each CTA): while the softmax of one half runs, the tensor
+// pipe multiplies for the other.
+//   S[256, 128 keys] = Q K^T, 12 MMAs;  O[256, 128] += P V, 8 MMAs, P from TMEM.
+// Each CTA loads half of a tile of K (64 keys) and of V (64 dims), 40 KB: three tiles are in
+// flight where a CTA on its own has room for little more than one, and waits for it. TMEM
+// holds both halves' S and O (4 x 128 columns); P (BF16) takes the place of the S it was made from.
+// Warp 0 loads by TMA; warps 1 and 2 of the first CTA issue the halves' MMAs; warp 3 tells
+// them that V is there, and clears what lies behind a request's last key; eight warps each are
+// the softmax of the halves: two threads to a row, 64 keys each. The maximum that P is relative
+// to moves only when a score exceeds it by 2^8 (O and the sum are then rescaled), so that the
+// two threads need no more than a barrier's vote in most tiles; P is rounded to BF16 (2^-8, as
+// the inputs are), its sum is of the FP32 values.
 //
-// How the work is shared out is in prompt.h. The order of a CTA's MMAs is PV(t) before S(t + 1)
-// of the same half, so that S may overwrite P and its completion tells that O is final.
+// How the work is shared out is in prompt.h. The order of a half's MMAs is PV(t) before S(t + 1),
+// so that S may overwrite P and its completion tells that O is final.
 #include <cmath>
 
 #include "checks.h"
 #include "decode_common.cuh"
 #include "formats.cuh"
 #include "internal.h"
+#include "pair.cuh"
 #include "prompt.h"
 #include "ptx.cuh"
 #include "tc.cuh"
@@ -38,21 +42,20 @@ using namespace prompt;
 constexpr int kNope = 128, kRope = 64, kV = 128;
 constexpr int kBlock = 128 * 128;                // bytes: 128 rows of 64 BF16
 constexpr int kQBlocks = 3;                      // 192 dims
-// K's nope dims and V, two blocks each, take turns in a ring of three pairs; K's rope dims have
-// two blocks of their own. V goes where K was one tile before: once that is read, the rope block
-// of the tile after next is free too, and is loaded then. K, which comes where V was two tiles
-// before, is the late one: S begins with the rope dims and goes on block by block as they land.
-constexpr int kRing = 3;
-constexpr int kOffRing = 2 * kQBlocks * kBlock;
-constexpr int kOffRope = kOffRing + kRing * 2 * kBlock;
-constexpr int kOffCtl = kOffRope + 2 * kBlock;
-constexpr int kSoft = 2 * kHalf;                 // softmax threads of a half: two to a row
-constexpr int kThreads = 128 + 2 * kSoft;        // warp 3 only gives its registers
+constexpr int kMine = 128;                       // a CTA's rows of a half
+constexpr int kStages = 3;                       // tiles of K and of V in flight
+constexpr int kKBlock = 64 * 128, kKBytes = 3 * kKBlock;   // 64 keys of 64 dims; 192 dims
+constexpr int kVBytes = kBlock;                  // 128 keys of 64 dims
+constexpr int kOffK = 2 * kQBlocks * kBlock;
+constexpr int kOffV = kOffK + kStages * kKBytes;
+constexpr int kOffCtl = kOffV + kStages * kVBytes;
+constexpr int kSoft = 256;                       // softmax threads of a half: two to a row
+constexpr int kThreads = 128 + 2 * kSoft;
 // Registers a thread at the launch (640 x 96 = 61,440), and after the split: 128 x 64 + 512 x 104.
 constexpr int kRegsFew = 64, kRegsMany = 104;
 constexpr uint32_t kTmemCols = 512, kColO = 256;
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;   // 2 s
-constexpr uint32_t kIdescS = tc::idesc_bf16_f32(kHalf, kKeys);
+constexpr uint32_t kIdescS = tc::idesc_bf16_f32(kHalf, kKeys);   // M = 256 over the pair
 constexpr uint32_t kIdescO = tc::idesc_bf16_f32(kHalf, kV) | (1u << 16);   // V is MN-major
 constexpr float kLazy = 8.f;
 
@@ -77,16 +80,25 @@ __device__ __forceinline__ int half_tiles(const Piece& p, int h) {
   return max(min(p.t1, last) - p.t0, 0);
 }
 
+// The pair's barriers: those that MMAs wait for count on the first CTA, those that MMAs arrive on
+// in both.
 struct PromptCtl {
   uint64_t q_full[2], q_empty[2];
-  uint64_t full[kRing], empty[kRing];   // K's first block, or V
-  uint64_t full2[kRing], rope_full[2];  // K's second block, its rope block
+  uint64_t k_full[kStages], k_empty[kStages];
+  uint64_t v_land[kStages];      // this CTA's copies of V
+  uint64_t v_full[kStages], v_empty[kStages];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t job_full[2], job_empty[2];
+  uint64_t claim_full[2], claim_empty[2];   // first CTA -> second: claimed items; and back
   uint64_t turn[2];              // the other half's MMAs of the step are issued
   uint64_t drain[2];
   Piece job[2];
-  float row[2][kHalf];           // [half][row]: what the two threads of a row tell one another
+  long long claim[2];
+  float row[2][kMine];           // [half][row]: what the two threads of a row tell one another
+  // Values that are no numbers (below): by piece and dim, (piece + 1, ~ the first such key). Four
+  // pieces' worth: no CTA's softmax is further behind the other's copies.
+  unsigned long long bad[4][kV];
+  uint32_t bad_piece[4];         // piece + 1, where there are any
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -102,11 +114,11 @@ struct PromptArgs {
   long long* first_place;        // [R + 1]
   long long* first_item;         // [R + 1]
   long long* part_place;         // [parts + 1]
-  float* part_o;                 // [slots][32][256][4]
-  float* part_lse;               // [slots][256]
+  float* part_o;                 // [slots][32][512][4]
+  float* part_lse;               // [slots][512]
   int32_t* status;
   float scale_log2;
-  int R, T, Tk, H, group, causal, ctas;
+  int R, T, Tk, H, group, causal, pairs;
   unsigned long long wait_limit_ns;
   int withhold;                  // failure-detection test: CTA 0 never loads its first keys
 };
@@ -173,10 +185,10 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptA
     a.first_item[a.R] = ti;
     a.plan->total = tw;
     a.plan->all_items = ti;
-    a.plan->parts = parts_of(tw, longest, a.ctas);
+    a.plan->parts = parts_of(tw, longest, a.pairs);
     a.plan->claimed = 0;
   }
-  const int parts = parts_of(tw, longest, a.ctas);
+  const int parts = parts_of(tw, longest, a.pairs);
   for (int p = r; parts > 0 && p <= parts; p += blockDim.x) a.part_place[p] = part_at(tw, parts, p);
 }
 
@@ -212,6 +224,28 @@ __device__ __forceinline__ bool pr_wait(uint64_t* bar, uint32_t parity, PromptCt
     }
   }
 }
+// The same for what the other CTA's threads wrote.
+__device__ __forceinline__ bool pr_wait_pair(uint64_t* bar, uint32_t parity, PromptCtl* ctl,
+                                             const PromptArgs& a) {
+  const unsigned long long t0 = tc::globaltimer_ns();
+  while (true) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (*reinterpret_cast<volatile int*>(&ctl->abort_flag)) return false;
+    if (tc::globaltimer_ns() - t0 > a.wait_limit_ns) {
+      *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
+      if (a.status) atomicOr(a.status, MLA_FAULT_WAIT_TIMEOUT);
+      return false;
+    }
+  }
+}
 // The next piece, for a whole warp; false at the end, or where the wait ran out.
 __device__ __forceinline__ bool take(PromptCtl* ctl, uint32_t seq, const PromptArgs& a, Piece& p, bool read) {
   const int b = seq & 1;
@@ -237,12 +271,28 @@ __device__ __forceinline__ bool elect() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
   return r != 0;
 }
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                            uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, bool accumulate) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_bf16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                 uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m, uint32_t bar, int x,
+                                                 int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(tc::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -261,6 +311,12 @@ __device__ __forceinline__ bool half_any(int h, bool v) {
       : "memory");
   return r != 0;
 }
+// 32 bytes, a sector of its own, at a 32-byte boundary.
+__device__ __forceinline__ void st_32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 __device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -274,7 +330,7 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
               const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_r,
               const __grid_constant__ CUtensorMap tm_v) {
@@ -283,37 +339,43 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
                                              ~uintptr_t(1023));
   PromptCtl* ctl = reinterpret_cast<PromptCtl*>(smem + kOffCtl);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = tc::cluster_rank();
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&ctl->q_full[i], 1);
+      tc::mbar_init(&ctl->q_full[i], 2);
       tc::mbar_init(&ctl->q_empty[i], 1);
       tc::mbar_init(&ctl->s_full[i], 1);
-      tc::mbar_init(&ctl->p_full[i], kSoft / 32);
+      tc::mbar_init(&ctl->p_full[i], 2 * kSoft / 32);
       tc::mbar_init(&ctl->o_full[i], 1);
       tc::mbar_init(&ctl->job_full[i], 1);
-      tc::mbar_init(&ctl->job_empty[i], 2 + 2 * kSoft / 32);
+      tc::mbar_init(&ctl->job_empty[i], (rank ? 1 : 3) + 2 * kSoft / 32);
+      tc::mbar_init(&ctl->claim_full[i], 1);
+      tc::mbar_init(&ctl->claim_empty[i], 1);
       tc::mbar_init(&ctl->turn[i], 1);
       tc::mbar_init(&ctl->drain[i], 1);
-      tc::mbar_init(&ctl->rope_full[i], 1);
     }
-    for (int i = 0; i < kRing; ++i) {
-      tc::mbar_init(&ctl->full[i], 1);
-      tc::mbar_init(&ctl->full2[i], 1);
-      tc::mbar_init(&ctl->empty[i], 2);
+    for (int i = 0; i < kStages; ++i) {
+      tc::mbar_init(&ctl->k_full[i], 2);
+      tc::mbar_init(&ctl->k_empty[i], 2);
+      tc::mbar_init(&ctl->v_land[i], 1);
+      tc::mbar_init(&ctl->v_full[i], 2);
+      tc::mbar_init(&ctl->v_empty[i], 2);
     }
     ctl->abort_flag = 0;
+    for (int i = 0; i < 4; ++i) ctl->bad_piece[i] = 0;
     tc::fence_barrier_init();
     tc::prefetch_tmap(&tm_q);
     tc::prefetch_tmap(&tm_k);
     tc::prefetch_tmap(&tm_r);
     tc::prefetch_tmap(&tm_v);
   }
+  if (threadIdx.x < 4 * kV) ctl->bad[threadIdx.x / kV][threadIdx.x % kV] = 0;
   if (warp == 1) {
-    tc::tmem_alloc(&ctl->tmem_base, kTmemCols);
-    tc::tmem_relinquish();
+    tc::tmem_alloc_pair(&ctl->tmem_base, kTmemCols);
+    tc::tmem_relinquish_pair();
   }
   tc::fence_before_sync();
-  __syncthreads();
+  tc::cluster_sync();            // both CTAs' barriers and TMEM are there
   tc::fence_after_sync();
   const uint32_t tmem = ctl->tmem_base;
   grid_dep_wait();               // the waits' limit counts from the end of the kernel before
@@ -323,21 +385,22 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
   if (warp == 0) {
     // ------------------------------------------------------------ pieces and copies
-    uint32_t seq = 0, slot = 0, ropes = 0, xq0 = 0, xq1 = 0;   // slot: K and V tiles loaded
+    uint32_t seq = 0, n = 0, xq0 = 0, xq1 = 0;   // pieces, tiles and queries of the halves so far
     bool ok = true;
     auto wait0 = [&](uint64_t* bar, uint32_t parity) {
       int v = 1;
       if (lane == 0) v = pr_wait(bar, parity, ctl, a) ? 1 : 0;
       return __shfl_sync(0xffffffffu, v, 0) != 0;
     };
+    const int pair = blockIdx.x >> 1;
     const bool withheld = a.withhold && blockIdx.x == 0;
     const int parts = a.plan->parts;
     const long long all = a.plan->all_items;
-    // Whole items: the first by the CTA's index, then claimed. Parts: places [at, end).
-    long long at = blockIdx.x, end = 0;
+    // Whole items: the first by the pair's index, then claimed. Parts: places [at, end).
+    long long at = pair, end = 0;
     if (parts > 0) {
-      at = (int)blockIdx.x < parts ? a.part_place[blockIdx.x] : 0;
-      end = (int)blockIdx.x < parts ? a.part_place[blockIdx.x + 1] : 0;
+      at = pair < parts ? a.part_place[pair] : 0;
+      end = pair < parts ? a.part_place[pair + 1] : 0;
     }
     while (ok) {
       Piece p;
@@ -365,8 +428,8 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
         if (parts > 0) {
           p.t0 = (int)(rest - before(q, u));
           p.t1 = (int)min((long long)tiles, p.t0 + (end - at));
-          if (p.t0 > 0) p.slot = 2 * blockIdx.x;
-          else if (p.t1 < tiles) p.slot = 2 * blockIdx.x + 1;
+          if (p.t0 > 0) p.slot = 2 * pair;
+          else if (p.t1 < tiles) p.slot = 2 * pair + 1;
           at += p.t1 - p.t0;
         }
       }
@@ -386,80 +449,89 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
         s->causal = p.causal;
         tc::mbar_arrive(&ctl->job_full[seq & 1]);
       }
-      ++seq;
       if (p.rows == 0) break;
       if (parts == 0) {
-        int k = 0;
-        if (lane == 0) k = atomicAdd(&a.plan->claimed, 1);
-        at = (long long)gridDim.x + __shfl_sync(0xffffffffu, k, 0);
-      }
-      const int c0 = half_tiles(p, 0), c1 = half_tiles(p, 1), nt = max(c0, c1), kvh = p.head / a.group;
-#pragma unroll 1
-      for (int i = 0; i < 2 * nt; ++i, ++slot) {               // K, V of every tile
-        const int b = slot % kRing, key = p.key0 + (p.t0 + (i >> 1)) * kKeys, is_v = i & 1;
-        if (slot >= kRing && !(ok = wait0(&ctl->empty[b], (slot / kRing - 1) & 1))) break;
-        auto load_rope = [&](int tile, int at) {
-          uint64_t* bar = &ctl->rope_full[tile & 1];
-          tc::mbar_arrive_expect_tx(bar, kBlock);
-          tc::tma_load_2d(smem + kOffRope + (tile & 1) * kBlock, &tm_r, bar, 0, at);
-        };
-        if (i == 0 || (is_v && i + 1 < 2 * nt)) ropes = slot / 2 + 1 + is_v;
+        // The first CTA claims the next item and tells the second.
+        int got = 1;
         if (lane == 0) {
-          uint8_t* dst = smem + kOffRing + b * 2 * kBlock;
-          if (is_v) {
-            tc::mbar_arrive_expect_tx(&ctl->full[b], 2 * kBlock);
-            tc::tma_load_3d(dst, &tm_v, &ctl->full[b], 0, kvh, key);
-            tc::tma_load_3d(dst + kBlock, &tm_v, &ctl->full[b], 128, kvh, key);
-            if (i + 1 < 2 * nt) load_rope(slot / 2 + 1, key + kKeys);
-          } else {
-            if (i == 0) load_rope(slot / 2, key);
-            if (!(withheld && slot == 0)) {
-              tc::mbar_arrive_expect_tx(&ctl->full[b], kBlock);
-              tc::tma_load_3d(dst, &tm_k, &ctl->full[b], 0, kvh, key);
+          const int i = seq & 1;
+          const uint32_t phase = seq >> 1 & 1;
+          if (rank == 0) {
+            at = (long long)(gridDim.x >> 1) + atomicAdd(&a.plan->claimed, 1);
+            got = seq < 2 || pr_wait_pair(&ctl->claim_empty[i], phase ^ 1, ctl, a);
+            if (got) {
+              asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(tc::map_rank(&ctl->claim[i], 1)), "l"(at)
+                           : "memory");
+              asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                               tc::map_rank(&ctl->claim_full[i], 1))
+                           : "memory");
             }
-            tc::mbar_arrive_expect_tx(&ctl->full2[b], kBlock);
-            tc::tma_load_3d(dst + kBlock, &tm_k, &ctl->full2[b], 128, kvh, key);
+          } else {
+            got = pr_wait_pair(&ctl->claim_full[i], phase, ctl, a);
+            if (got) {
+              at = *reinterpret_cast<volatile long long*>(&ctl->claim[i]);
+              asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                               tc::map_rank(&ctl->claim_empty[i], 0))
+                           : "memory");
+            }
           }
         }
-        if (i == 0) {
+        at = __shfl_sync(0xffffffffu, at, 0);
+        if (!(ok = __shfl_sync(0xffffffffu, got, 0) != 0)) break;
+      }
+      ++seq;
+      const int c0 = half_tiles(p, 0), c1 = half_tiles(p, 1), nt = max(c0, c1), kvh = p.head / a.group;
+#pragma unroll 1
+      for (int t = 0; t < nt; ++t, ++n) {
+        const int st = n % kStages, key = p.key0 + (p.t0 + t) * kKeys;
+        if (n >= kStages && !(ok = wait0(&ctl->k_empty[st], (n / kStages - 1) & 1))) break;
+        if (lane == 0 && !(withheld && n == 0)) {
+          const uint32_t bar = tc::map_rank(&ctl->k_full[st], 0);
+          uint8_t* dst = smem + kOffK + st * kKBytes;
+          const int mine = key + (int)rank * 64;
+          tc::remote_arrive_expect_tx(bar, kKBytes);
+          tma_load_3d_pair(dst, &tm_k, bar, 0, kvh, mine);
+          tma_load_3d_pair(dst + kKBlock, &tm_k, bar, 128, kvh, mine);
+          tc::tma_load_2d_pair(dst + 2 * kKBlock, &tm_r, bar, 0, mine);
+        }
+        if (t == 0) {
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             if (!(h ? c1 : c0)) continue;
-            const uint32_t x = h ? xq1++ : xq0++;
-            if (x > 0 && !(ok = wait0(&ctl->q_empty[h], (x - 1) & 1))) {
-              --(h ? xq1 : xq0);                               // not loaded
-              break;
-            }
+            const uint32_t x = h ? xq1 : xq0;
+            if (x > 0 && !(ok = wait0(&ctl->q_empty[h], (x - 1) & 1))) break;
+            ++(h ? xq1 : xq0);
             if (lane == 0) {
-              tc::mbar_arrive_expect_tx(&ctl->q_full[h], kQBlocks * kBlock);
+              const uint32_t bar = tc::map_rank(&ctl->q_full[h], 0);
+              tc::remote_arrive_expect_tx(bar, kQBlocks * kBlock);
               for (int e = 0; e < kQBlocks; ++e)
-                tc::tma_load_3d(smem + (h * kQBlocks + e) * kBlock, &tm_q, &ctl->q_full[h], e * 128, p.head,
-                                p.row0 + h * kHalf);
+                tma_load_3d_pair(smem + (h * kQBlocks + e) * kBlock, &tm_q, bar, e * 128, p.head,
+                                 p.row0 + h * kHalf + (int)rank * kMine);
             }
           }
-          if (!ok) {
-            ++slot;                                            // loaded above
-            break;
-          }
+          if (!ok) break;
+        }
+        if (n >= kStages && !(ok = wait0(&ctl->v_empty[st], (n / kStages - 1) & 1))) break;
+        if (lane == 0) {
+          tc::mbar_arrive_expect_tx(&ctl->v_land[st], kVBytes);
+          tc::tma_load_3d(smem + kOffV + st * kVBytes, &tm_v, &ctl->v_land[st], (int)rank * 128, kvh, key);
         }
       }
     }
-    // Never leave with copies in flight: another role may have given up a wait.
+    // Never leave with copies in flight: another role may have given up a wait. V counts here, the
+    // pair's K and queries on the first CTA; the CTAs leave together.
     if (lane == 0) {
       const unsigned long long t0 = tc::globaltimer_ns();
-      for (uint32_t i = slot < kRing ? 0 : slot - kRing; i < slot; ++i)
-        while (!(withheld && i == 0) && !tc::mbar_try_wait(&ctl->full[i % kRing], (i / kRing) & 1) &&
+      const uint32_t last = ok ? n : n + 1;      // a tile begun when a wait ran out
+      for (uint32_t i = n < kStages ? 0 : n - kStages; i < n; ++i)
+        while (!tc::mbar_try_wait(&ctl->v_land[i % kStages], (i / kStages) & 1) &&
                tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
         }
-      for (uint32_t i = slot < kRing ? 0 : slot - kRing; i < slot; ++i)
-        while (!(i & 1) && !tc::mbar_try_wait(&ctl->full2[i % kRing], (i / (2 * kRing)) & 1) &&
+      for (uint32_t i = last < kStages ? 0 : last - kStages; rank == 0 && i < last; ++i)
+        while (!tc::mbar_try_wait(&ctl->k_full[i % kStages], (i / kStages) & 1) &&
                tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
         }
-      for (uint32_t i = ropes < 2 ? 0 : ropes - 2; i < ropes; ++i)
-        while (!tc::mbar_try_wait(&ctl->rope_full[i & 1], (i >> 1) & 1) &&
-               tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
-        }
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; rank == 0 && h < 2; ++h) {
         const uint32_t x = h ? xq1 : xq0;
         while (x > 0 && !tc::mbar_try_wait(&ctl->q_full[h], (x - 1) & 1) &&
                tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
@@ -467,18 +539,23 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
       }
     }
   } else if (warp <= 2) {
-    // ------------------------------------------------------------ MMAs of half h
+    // ------------------------------------------------------------ MMAs of half h, for both CTAs
     // The whole warp goes through the waits, so that what the MMAs are given is the same in all
     // lanes and stays in uniform registers; one lane issues.
+    if (rank == 0) {
     const int h = __shfl_sync(0xffffffffu, warp, 0) - 1;
     const bool one = elect();
-    uint32_t slot = 0, xq = 0, xp = 0, turn = h ^ 1;   // half 0 begins
-    const uint32_t q = tc::smem_u32(smem) + h * kQBlocks * kBlock;
-    const uint32_t s_ring = tc::smem_u32(smem + kOffRing), s_rope = tc::smem_u32(smem + kOffRope);
+    uint32_t n0 = 0, xq = 0, xp = 0, turn = h ^ 1;   // half 0 begins
+    const uint32_t s_k = tc::smem_u32(smem + kOffK), s_v = tc::smem_u32(smem + kOffV);
     const uint32_t col_s = tmem + h * kKeys, col_o = tmem + kColO + h * kV;
+    const uint64_t qd = tc::smem_desc(tc::smem_u32(smem) + h * kQBlocks * kBlock, 16, 1024, tc::kSw128);
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return ok = __all_sync(0xffffffffu, pr_wait(bar, parity, ctl, a));
+    };
+    auto give_back = [&](uint64_t* bar) {        // what this half does not multiply
+      tc::remote_arrive(tc::map_rank(bar, 0));
+      tc::remote_arrive(tc::map_rank(bar, 1));
     };
     for (uint32_t seq = 0; ok; ++seq) {
       Piece p;
@@ -487,75 +564,117 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
       const int nt = max(c, __shfl_sync(0xffffffffu, half_tiles(p, h ^ 1), 0));
       // PV of tile t, then S of tile t + 1, the halves in turn: issued as they come, the halves' MMAs
       // would mingle, both finish late, and both softmaxes then run while the tensor pipe
-      // waits. A tile that only the other half multiplies is given back
-      // as it lands. What the copies bring is waited for before P, where it is there by then, so
-      // that nothing stands between P and the MMAs.
+      // waits. A tile that only the other half multiplies is given back as it lands. What the
+      // copies bring is waited for before P, where it is there by then, so that nothing stands
+      // between P and the MMAs.
 #pragma unroll 1
       for (int t = -1; t < nt; ++t) {
-        const uint32_t av = slot + 2 * t + 1, bv = av % kRing;        // V of tile t
-        const uint32_t ak = av + 1, bk = ak % kRing, n = ak >> 1;     // K of tile t + 1
+        const uint32_t nv = n0 + t, sv = nv % kStages;          // V of tile t
+        const uint32_t nk = nv + 1, sk = nk % kStages;          // K of tile t + 1
         const bool has_k = t + 1 < nt, mine = t + 1 < c;
         if (t < 0 && c > 0 && !wait(&ctl->q_full[h], xq++ & 1)) break;
-        if (t >= 0 && !wait(&ctl->full[bv], (av / kRing) & 1)) break;
-        const bool early = has_k && tc::mbar_test_wait(&ctl->rope_full[n & 1], (n >> 1) & 1) &&
-                           tc::mbar_test_wait(&ctl->full[bk], (ak / kRing) & 1) &&
-                           tc::mbar_test_wait(&ctl->full2[bk], (ak / (2 * kRing)) & 1);
-        const bool landed = __all_sync(0xffffffffu, early);
+        if (t >= 0 && !wait(&ctl->v_full[sv], (nv / kStages) & 1)) break;
+        const bool landed = __all_sync(0xffffffffu, has_k && tc::mbar_test_wait(&ctl->k_full[sk], (nk / kStages) & 1));
         if (t >= 0 && t < c && !wait(&ctl->p_full[h], xp++ & 1)) break;
         if (!wait(&ctl->turn[h], turn++ & 1)) break;
-        if (t >= 0) {
-          tc::fence_after_sync();
-          const uint64_t v = tc::smem_desc(s_ring + bv * 2 * kBlock, kBlock, 1024, tc::kSw128);
-          if (t < c && one) {
+        tc::fence_after_sync();
+        if (t >= 0 && one) {
+          if (t < c) {
+            const uint64_t v = tc::smem_desc(s_v + sv * kVBytes, kBlock, 1024, tc::kSw128);
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
-              mma_bf16_ts(col_o, col_s + kk * 8, v + (kk * 16 * 128 >> 4), kIdescO, t + kk != 0);
-            tc::mma_commit(&ctl->empty[bv]);
-            if (t == c - 1) tc::mma_commit(&ctl->o_full[h]);
-          } else if (one) {
-            tc::mbar_arrive(&ctl->empty[bv]);
+              mma_bf16_ts_pair(col_o, col_s + kk * 8, v + (kk * 16 * 128 >> 4), kIdescO, t + kk != 0);
+            tc::mma_commit_pair(&ctl->v_empty[sv]);
+            if (t == c - 1) tc::mma_commit_pair(&ctl->o_full[h]);
+          } else {
+            give_back(&ctl->v_empty[sv]);
           }
         }
+        __syncwarp();
         if (has_k) {
-          const uint64_t k = tc::smem_desc(s_ring + bk * 2 * kBlock, 16, 1024, tc::kSw128);
-          const uint64_t r = tc::smem_desc(s_rope + (n & 1) * kBlock, 16, 1024, tc::kSw128);
-          const uint64_t qd = tc::smem_desc(q, 16, 1024, tc::kSw128);
-          if (!landed && !wait(&ctl->rope_full[n & 1], (n >> 1) & 1)) break;
+          if (!landed && !wait(&ctl->k_full[sk], (nk / kStages) & 1)) break;
           tc::fence_after_sync();
-          if (mine && one)
+          if (mine && one) {
+            const uint64_t k = tc::smem_desc(s_k + sk * kKBytes, 16, 1024, tc::kSw128);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc::mma_bf16(col_s, qd + ((2 * kBlock + kk * 32) >> 4), r + (kk * 32 >> 4), kIdescS, kk != 0);
-          if (!landed && !wait(&ctl->full[bk], (ak / kRing) & 1)) break;
-          tc::fence_after_sync();
-          if (mine && one)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc::mma_bf16(col_s, qd + (kk * 32 >> 4), k + (kk * 32 >> 4), kIdescS, true);
-          if (!landed && !wait(&ctl->full2[bk], (ak / (2 * kRing)) & 1)) break;
-          tc::fence_after_sync();
-          if (mine && one)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc::mma_bf16(col_s, qd + ((kBlock + kk * 32) >> 4), k + ((kBlock + kk * 32) >> 4), kIdescS, true);
-        }
-        if (has_k && one) {
-          if (mine) {
-            tc::mma_commit(&ctl->s_full[h]);
-            tc::mma_commit(&ctl->empty[bk]);
-            if (t + 1 == c - 1) tc::mma_commit(&ctl->q_empty[h]);
-          } else {
-            tc::mbar_arrive(&ctl->empty[bk]);
+            for (int kk = 0; kk < 12; ++kk)
+              mma_bf16_pair(col_s, qd + (((kk >> 2) * kBlock + (kk & 3) * 32) >> 4),
+                            k + (((kk >> 2) * kKBlock + (kk & 3) * 32) >> 4), kIdescS, kk != 0);
+            tc::mma_commit_pair(&ctl->s_full[h]);
+            tc::mma_commit_pair(&ctl->k_empty[sk]);
+            if (t + 1 == c - 1) tc::mma_commit_pair(&ctl->q_empty[h]);
+          } else if (one) {
+            give_back(&ctl->k_empty[sk]);
           }
         }
         if (one) tc::mbar_arrive(&ctl->turn[h ^ 1]);
+        __syncwarp();
       }
-      slot += 2 * nt;
+      n0 += nt;
     }
     if (one) {
-      tc::mma_commit(&ctl->drain[h]);            // every MMA done before TMEM is released
+      tc::mma_commit_pair(&ctl->drain[h]);       // every MMA done before the CTAs leave
       const unsigned long long t0 = tc::globaltimer_ns();
       while (!tc::mbar_try_wait(&ctl->drain[h], 0) && tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
+      }
+    }
+    }
+  } else {
+    // ------------------------------------------------------------ V, made fit for the MMAs
+    // Weights of keys that a row does not see are 0, and 0 times a value has to be 0. Values behind
+    // the request's last key are another's, or nothing's: they are cleared. In tiles that some
+    // row sees in part, values that are no numbers are cleared too, and noted by dim, so that the
+    // rows that see them get NaN there at the end.
+    uint32_t n = 0;
+    bool ok = true;
+    for (uint32_t seq = 0; ok; ++seq) {
+      Piece p;
+      if (!take(ctl, seq, a, p, lane == 0)) break;
+      const int c0 = half_tiles(p, 0), nt = max(c0, half_tiles(p, 1));
+#pragma unroll 1
+      for (int t = 0; t < nt; ++t, ++n) {
+        const int st = n % kStages, key = (p.t0 + t) * kKeys, there = min(p.m - key, kKeys);
+        uint4* v = reinterpret_cast<uint4*>(smem + kOffV + st * kVBytes);
+        if (!(ok = __all_sync(0xffffffffu, pr_wait(&ctl->v_land[st], (n / kStages) & 1, ctl, a)))) break;
+        if (there < kKeys) {
+          for (int i = there * 8 + lane; i < kKeys * 8; i += 32) v[i] = make_uint4(0, 0, 0, 0);
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (row_limit(p, t < c0 ? 0 : kHalf) < key + there) {
+          uint32_t odd = 0;                      // bit 15 of a half: an exponent of ones
+#pragma unroll 4
+          for (int i = lane; i < kKeys * 8; i += 32) {
+            const uint4 x = v[i];
+            odd |= ((x.x & 0x7F807F80u) + 0x00800080u) | ((x.y & 0x7F807F80u) + 0x00800080u) |
+                   ((x.z & 0x7F807F80u) + 0x00800080u) | ((x.w & 0x7F807F80u) + 0x00800080u);
+          }
+          if (__any_sync(0xffffffffu, (odd & 0x80008000u) != 0)) {
+            const int b = seq & 3;
+            for (int i = lane; i < kKeys * 64; i += 32) {
+              uint16_t* x = reinterpret_cast<uint16_t*>(v) + i;
+              if ((*x & 0x7F80u) != 0x7F80u) continue;
+              *x = 0;
+              // Row i / 64; its 16-byte pieces lie exchanged by the row's place among eight.
+              const int key_row = i >> 6, piece = (i >> 3 & 7) ^ (key_row & 7);
+              const int dim = (int)rank * 64 + piece * 8 + (i & 7);
+              const unsigned long long note = (unsigned long long)(seq + 1) << 32 | ~(uint32_t)(key + key_row);
+              for (int c = 0; c < 2; ++c) {
+                asm volatile("red.relaxed.cluster.shared::cluster.max.u64 [%0], %1;" ::"r"(
+                                 tc::map_rank(&ctl->bad[b][dim], c)),
+                             "l"(note)
+                             : "memory");
+                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(tc::map_rank(&ctl->bad_piece[b], c)),
+                             "r"(seq + 1)
+                             : "memory");
+              }
+            }
+            asm volatile("fence.acq_rel.cluster;" ::: "memory");
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        if (lane == 0) tc::remote_arrive(tc::map_rank(&ctl->v_full[st], 0));
       }
     }
   }
@@ -566,18 +685,19 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
     // wait that ran out a half's threads go on to the end of the piece without waiting, so that
     // all meet at its barriers, and leave together.
     const int h = (warp - 4) >> 3, side = (warp - 4) >> 2 & 1, quarter = warp & 3, row = quarter * 32 + lane;
-    const int j = h * kHalf + row;
+    const int j = h * kHalf + (int)rank * kMine + row;
+    const uint32_t p_full = tc::map_rank(&ctl->p_full[h], 0);
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t col_s = lanes + h * kKeys + side * 64, col_p = lanes + h * kKeys + side * 32;
     const uint32_t col_o = lanes + kColO + h * kV + side * 64;
-    uint32_t slot = 0, xs = 0, xo = 0;
+    uint32_t xs = 0, xo = 0;
     Piece p;
     bool ok = true;
     auto all_wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, pr_wait(bar, parity, ctl, a));
     };
     for (uint32_t seq = 0; !half_any(h, !(ok && take(ctl, seq, a, p, lane == 0))); ++seq) {
-      const int c = half_tiles(p, h), nt = max(c, half_tiles(p, h ^ 1));
+      const int c = half_tiles(p, h);
       const bool valid = j < p.rows;
       const int lim = valid ? row_limit(p, j) : INT_MAX;
       const int lowest = __reduce_min_sync(0xffffffffu, lim);
@@ -648,25 +768,11 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
         float s0, s1;
         unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
-        // Values behind the request's last key are another's, or nothing's: their weights are 0,
-        // and they are cleared so that 0 times them is 0.
-        if (key + kKeys > p.m) {
-          const uint32_t at = slot + 2 * t + 1;
-          const bool landed = all_wait(&ctl->full[at % kRing], (at / kRing) & 1);
-          ok = ok && landed;
-          if (landed && key + row >= p.m)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<uint4*>(smem + kOffRing + (at % kRing * 2 + side) * kBlock + row * 128 + i * 16) =
-                  make_uint4(0, 0, 0, 0);
-          tc::fence_proxy_async_smem();
-        }
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&ctl->p_full[h]);
+        if (lane == 0) tc::remote_arrive(p_full);
       }
-      slot += 2 * nt;
       // The rows' sums, of both threads.
       if (side) ctl->row[h][row] = l;
       half_any(h, false);
@@ -683,9 +789,9 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
       } else if (side == 0) {
         a.part_lse[(size_t)p.slot * kRows + j] = lse;
       }
-      uint4* whole = reinterpret_cast<uint4*>(a.out + at * kV + side * 64);
-      float4* part = reinterpret_cast<float4*>(a.part_o) + ((size_t)p.slot * 32 + side * 16) * kRows + j;
-#pragma unroll 1
+      const volatile unsigned long long* bad = ctl->bad[seq & 3] + side * 64;
+      const bool noted = *reinterpret_cast<volatile uint32_t*>(&ctl->bad_piece[seq & 3]) == seq + 1;
+#pragma unroll 4
       for (int i = 0; i < 4; ++i) {
         uint32_t o[16];
 #pragma unroll
@@ -694,30 +800,34 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
           tc::tmem_ld16(col_o + 16 * i, o);
           tc::tmem_wait_ld();
         }
-        float f[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) f[e] = l == 0.f ? 0.f : __uint_as_float(o[e]) * inv;
+        for (int e = 0; e < 16; ++e) o[e] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
+        if (noted) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const unsigned long long note = bad[16 * i + e];
+            if ((uint32_t)(note >> 32) == seq + 1 && (uint32_t)lim > ~(uint32_t)note) o[e] = 0x7FC00000u;
+          }
+        }
         if (p.slot < 0) {
+          uint32_t w[8];
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
-            if (valid && ok)
-              whole[2 * i + u] = make_uint4(f32x2_to_bf16x2(f[8 * u], f[8 * u + 1]),
-                                            f32x2_to_bf16x2(f[8 * u + 2], f[8 * u + 3]),
-                                            f32x2_to_bf16x2(f[8 * u + 4], f[8 * u + 5]),
-                                            f32x2_to_bf16x2(f[8 * u + 6], f[8 * u + 7]));
-        } else {
+          for (int e = 0; e < 8; ++e)
+            w[e] = f32x2_to_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+          if (valid && ok) st_32(a.out + at * kV + side * 64 + 16 * i, w);
+        } else if (c > 0) {
+          uint4* dst = reinterpret_cast<uint4*>(a.part_o) + ((size_t)p.slot * 32 + side * 16 + 4 * i) * kRows + j;
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            part[(size_t)(4 * i + u) * kRows] = make_float4(f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
+          for (int e = 0; e < 4; ++e) dst[e * kRows] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       }
       tc::fence_before_sync();
     }
   }
   tc::fence_before_sync();
-  __syncthreads();
+  tc::cluster_sync();            // no CTA leaves while the other's MMAs or arrivals may reach it
   tc::fence_after_sync();
-  if (warp == 1) tc::tmem_dealloc(tmem, kTmemCols);
+  if (warp == 1) tc::tmem_dealloc_pair(tmem, kTmemCols);
 }
 
 // ---------------------------------------------------------------- joining the pieces
@@ -790,7 +900,7 @@ int check_prompt(const mla_prompt_shape* s) {
   return MLA_OK;
 }
 size_t prompt_bytes(const mla_prompt_shape* s) {
-  return plan_bytes(s->R, s->num_ctas) + lse_bytes(s->num_ctas) + 2 * (size_t)s->num_ctas * kSlotBytes;
+  return plan_bytes(s->R, pairs_of(s->num_ctas)) + lse_bytes(pairs_of(s->num_ctas)) + 2 * (size_t)pairs_of(s->num_ctas) * kSlotBytes;
 }
 
 int32_t prompt_impl(const mla_prompt_shape* s, const void* q, const void* k_nope, const void* k_rope,
@@ -809,7 +919,7 @@ int32_t prompt_impl(const mla_prompt_shape* s, const void* q, const void* k_nope
   if (!q || !cu_tokens || !out || !workspace || (s->keys > 0 && (!k_nope || !k_rope || !v)))
     return MLA_ERR_NULL;
   if (!aligned(q, 16) || !aligned(k_nope, 16) || !aligned(k_rope, 16) || !aligned(v, 16) ||
-      !aligned(out, 16) || !aligned(lse, 4) || !aligned(cu_tokens, 4) || !aligned(cu_keys, 4) ||
+      !aligned(out, 32) || !aligned(lse, 4) || !aligned(cu_tokens, 4) || !aligned(cu_keys, 4) ||
       !aligned(workspace, 256) || !aligned(status, 4) || s->q_token_stride % 8 || s->q_head_stride % 8 ||
       s->k_token_stride % 8 || s->k_head_stride % 8 || s->v_token_stride % 8 || s->v_head_stride % 8 ||
       s->rope_stride % 8)
@@ -827,8 +937,8 @@ int32_t prompt_impl(const mla_prompt_shape* s, const void* q, const void* k_nope
   a.first_place = reinterpret_cast<long long*>(ws + sizeof(Plan));
   a.first_item = a.first_place + s->R + 1;
   a.part_place = a.first_item + s->R + 1;
-  a.part_lse = reinterpret_cast<float*>(ws + plan_bytes(s->R, s->num_ctas));
-  a.part_o = reinterpret_cast<float*>(ws + plan_bytes(s->R, s->num_ctas) + lse_bytes(s->num_ctas));
+  a.part_lse = reinterpret_cast<float*>(ws + plan_bytes(s->R, pairs_of(s->num_ctas)));
+  a.part_o = reinterpret_cast<float*>(ws + plan_bytes(s->R, pairs_of(s->num_ctas)) + lse_bytes(pairs_of(s->num_ctas)));
   a.status = status;
   a.scale_log2 = (float)((double)sm_scale * 1.4426950408889634);
   a.R = s->R;
@@ -837,7 +947,7 @@ int32_t prompt_impl(const mla_prompt_shape* s, const void* q, const void* k_nope
   a.H = s->H;
   a.group = s->H / s->kv_heads;
   a.causal = s->causal;
-  a.ctas = s->num_ctas;
+  a.pairs = pairs_of(s->num_ctas);
   a.wait_limit_ns = wait_limit_ns;
   a.withhold = withhold;
   // Without keys the maps of K and V stand on the queries; nothing is read through them.
@@ -853,11 +963,11 @@ int32_t prompt_impl(const mla_prompt_shape* s, const void* q, const void* k_nope
   const cuuint64_t v_dims[3] = {kV * 2, s->keys ? (cuuint64_t)s->kv_heads : 1, Tk};
   const cuuint64_t v_str[2] = {(cuuint64_t)s->v_head_stride * 2, (cuuint64_t)s->v_token_stride * 2};
   const cuuint64_t r_dims[2] = {kRope * 2, Tk}, r_str[1] = {(cuuint64_t)s->rope_stride * 2};
-  const cuuint32_t box3[3] = {128, 1, 128}, box2[2] = {128, 128};
+  const cuuint32_t box3[3] = {128, 1, 128}, box_k[3] = {128, 1, 64}, box_r[2] = {128, 64};
   if (!dec::encode(&tq, q, 3, q_dims, q_str, box3, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !dec::encode(&tk, kn, 3, k_dims, k_str, box3, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !dec::encode(&tk, kn, 3, k_dims, k_str, box_k, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !dec::encode(&tv, kv, 3, v_dims, v_str, box3, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !dec::encode(&tr, kr, 2, r_dims, r_str, box2, CU_TENSOR_MAP_SWIZZLE_128B))
+      !dec::encode(&tr, kr, 2, r_dims, r_str, box_r, CU_TENSOR_MAP_SWIZZLE_128B))
     return MLA_ERR_CUDA;
   static bool attr_set[64] = {};
   if (dec::set_smem(prompt_kernel, kSmemBytes, attr_set) != cudaSuccess) return MLA_ERR_CUDA;
@@ -871,16 +981,16 @@ int32_t prompt_impl(const mla_prompt_shape* s, const void* q, const void* k_nope
   cfg.gridDim = dim3(1);
   cfg.blockDim = dim3((unsigned)(cdiv(s->R, 32) * 32));
   if (cudaLaunchKernelEx(&cfg, prompt_plan_kernel, a) != cudaSuccess) return MLA_ERR_CUDA;
-  // No more CTAs than the batch can have places.
+  // No more pairs than the batch can have places.
   const long long items_most = (long long)s->H * (cdiv(s->tokens, kRows) + s->R);
   const long long places_most = items_most * (1 + cdiv(s->keys, kKeys));
-  cfg.gridDim = dim3((unsigned)(places_most < s->num_ctas ? places_most : s->num_ctas));
+  cfg.gridDim = dim3(2 * (unsigned)(places_most < a.pairs ? places_most : a.pairs));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   if (cudaLaunchKernelEx(&cfg, prompt_kernel, a, tq, tk, tr, tv) != cudaSuccess) return MLA_ERR_CUDA;
   // Requests of so few keys that no item can be cut leave nothing to join.
-  if (cdiv(s->keys, kKeys) <= kUncut || s->num_ctas < 2) return MLA_OK;
-  cfg.gridDim = dim3((unsigned)(s->num_ctas - 1), kSlices);
+  if (cdiv(s->keys, kKeys) <= kUncut || a.pairs < 2) return MLA_OK;
+  cfg.gridDim = dim3((unsigned)(a.pairs - 1), kSlices);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, prompt_join_kernel, a) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;

@@ -1,6 +1,7 @@
-// The work of a batch of prompts: items of 256 query rows of one head, each with the
+// The work of a batch of prompts: items of 512 query rows of one head, each with the
 // tiles of 128 keys that its rows see, and how all items lie on one line of places (a
-// place is a tile). Host and device code include this.
+// place is a tile). A pair of CTAs takes an item, as two halves of 256 rows. Host and
+// device code include this.
 #pragma once
 
 #include "internal.h"
@@ -8,12 +9,13 @@
 namespace mlafold {
 namespace prompt {
 
-constexpr int kRows = 256;       // query rows of an item: two halves of 128
-constexpr int kHalf = 128;
+constexpr int kRows = 512;       // query rows of an item
+constexpr int kHalf = 256;       // of its half
 constexpr int kKeys = 128;       // keys of a tile
+constexpr int kStep = kRows / kKeys;
 constexpr int kUncut = 4;        // items of no more tiles are never cut
 constexpr int kMinPart = 3;      // tiles of a part, at least
-constexpr int kWhole = 4;        // items stay whole where a CTA has so many of the longest's tiles
+constexpr int kWhole = 4;        // items stay whole where a pair has so many of the longest's tiles
 
 // A request of n query tokens and m keys; causal: query i sees keys j <= i + m - n.
 struct Request {
@@ -37,8 +39,8 @@ __host__ __device__ inline int item_tiles(const Request& q, int u) {
   const int t = tiles_of(limit(q, last - 1));
   return t < 1 ? 1 : t;
 }
-// Places of the items before item u, 0 <= u <= items. All items but the last have 256 rows,
-// so item v of them sees 256 (v + 1) + m - n keys: max(1, 2 (v + 1) + ceil((m - n) / 128))
+// Places of the items before item u, 0 <= u <= items. All items but the last have 512 rows,
+// so item v of them sees 512 (v + 1) + m - n keys: max(1, 4 (v + 1) + ceil((m - n) / 128))
 // tiles, of which the first z are ones.
 __host__ __device__ inline long long before(const Request& q, int u) {
   const int I = items(q);
@@ -49,9 +51,9 @@ __host__ __device__ inline long long before(const Request& q, int u) {
     return v * (t < 1 ? 1 : t) + last;
   }
   const long long c = tiles_of(q.m - q.n);
-  long long z = c < 0 ? (-c) >> 1 : 0;
+  long long z = c < 0 ? -c / kStep : 0;
   if (z > v) z = v;
-  return z + (v * (v + 1) - z * (z + 1)) + (v - z) * c + last;
+  return z + kStep / 2 * (v * (v + 1) - z * (z + 1)) + (v - z) * c + last;
 }
 __host__ __device__ inline long long places(const Request& q) { return before(q, items(q)); }
 // x = head * per + rest, 0 <= rest < per, without a division (the kernel that splits its registers
@@ -81,27 +83,28 @@ __host__ __device__ inline int item_at(const Request& q, long long x) {
 struct Plan {
   long long total, all_items;    // places and items of the batch
   int parts;                     // > 0: the line is cut into so many; 0: whole items, claimed
-  int claimed;                   // items claimed beyond the first of each CTA
+  int claimed;                   // items claimed beyond the first of each pair
 };
 // Where part p begins.
 __host__ __device__ inline long long part_at(long long total, int parts, int p) {
   return cdiv(total * p, parts);
 }
-// How a batch is shared out among `ctas` CTAs, by its places and its longest item: whole items
-// where a CTA's share is worth several of them (they are claimed longest first within each head,
-// so that little is left over at the end and the CTAs work on few heads at a time, whose keys
-// stay in L2), else equal parts of the line.
-__host__ __device__ inline int parts_of(long long total, int longest, int ctas) {
-  if (longest <= kUncut || total >= (long long)kWhole * longest * ctas) return 0;
+// How a batch is shared out among the pairs of CTAs, by its places and its longest item: whole
+// items where a pair's share is worth several of them (they are claimed longest first within each
+// head, so that little is left over at the end and the pairs work on few heads at a time, whose
+// keys stay in L2), else equal parts of the line.
+__host__ __device__ inline int parts_of(long long total, int longest, int pairs) {
+  if (longest <= kUncut || total >= (long long)kWhole * longest * pairs) return 0;
   const long long p = cdiv(total, kMinPart);
-  return (int)(p < ctas ? p : ctas);
+  return (int)(p < pairs ? p : pairs);
 }
 
 constexpr size_t kSlotBytes = (size_t)kRows * 128 * 4;     // a piece's FP32 rows
-inline size_t plan_bytes(int R, int ctas) {
-  return align256(sizeof(Plan) + (2 * (size_t)(R + 1) + ctas + 1) * 8);
+inline int pairs_of(int ctas) { return ctas < 2 ? 1 : ctas / 2; }
+inline size_t plan_bytes(int R, int pairs) {
+  return align256(sizeof(Plan) + (2 * (size_t)(R + 1) + pairs + 1) * 8);
 }
-inline size_t lse_bytes(int ctas) { return align256((size_t)2 * ctas * kRows * 4); }
+inline size_t lse_bytes(int pairs) { return align256((size_t)2 * pairs * kRows * 4); }
 
 }  // namespace prompt
 }  // namespace mlafold

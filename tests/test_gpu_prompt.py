@@ -160,6 +160,25 @@ def test_nan_and_infinities_stay_in_their_request():
     assert same(out[465:465 + 128], want[465:465 + 128]) and torch.isnan(out[615:]).all()
 
 
+@pytest.mark.parametrize("n,m,H", [(700, 700, 2), (300, 900, 1), (1500, 1500, 1), (2048, 2048, 4)])
+def test_values_that_are_no_numbers_reach_only_rows_that_see_them(n, m, H):
+    """Other rows, and other dims of the rows that do, keep their bits; cut items too."""
+    q, kn, kr, v = _inputs([0, n], [0, m], H, H, 21)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    want, want_l = mla.prompt_attention(q, kn, kr, v, i32(0, n), SCALE, cu_keys=i32(0, m))
+    spots = [(m - n + i, d, x) for i, d, x in
+             [(0, 3, math.nan), (5, 64, math.inf), (127, 127, -math.inf), (128, 0, math.nan), (n - 1, 63, math.nan),
+              (n // 2, 77, math.inf), (n // 2 + 1, 77, -math.inf)]]
+    for j, d, x in spots:
+        v[j, H - 1, d] = x
+    out, lse = mla.prompt_attention(q, kn, kr, v, i32(0, n), SCALE, cu_keys=i32(0, m))
+    assert torch.equal(lse, want_l)
+    hit = torch.zeros(n, H, 128, dtype=torch.bool, device="cuda")
+    for j, d, _ in spots:
+        hit[max(0, j - (m - n)):, H - 1, d] = True
+    assert torch.equal(out[~hit], want[~hit]) and not torch.isfinite(out[hit]).any()
+
+
 def test_a_row_of_nan_queries_stays_alone():
     q, kn, kr, v = _inputs([0, 300], [0, 300], 2, 2, 10)
     cu = torch.tensor([0, 300], dtype=torch.int32, device="cuda")
