@@ -90,7 +90,6 @@ struct PromptCtl {
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t job_full[2], job_empty[2];
   uint64_t claim_full[2], claim_empty[2];   // first CTA -> second: claimed items; and back
-  uint64_t turn[2];              // the other half's MMAs of the step are issued
   uint64_t drain[2];
   Piece job[2];
   long long claim[2];
@@ -100,6 +99,7 @@ struct PromptCtl {
   unsigned long long bad[4][kV];
   uint32_t bad_piece[4];         // piece + 1, where there are any
   uint32_t tmem_base;
+  uint32_t lock;                 // held by the half whose MMAs are being issued
   int abort_flag;
 };
 constexpr int kSmemBytes = kOffCtl + (int)sizeof(PromptCtl) + 1024;
@@ -265,6 +265,23 @@ __device__ __forceinline__ bool take(PromptCtl* ctl, uint32_t seq, const PromptA
   if (read) tc::mbar_arrive(&ctl->job_empty[b]);
   return p.rows > 0;
 }
+// One half's MMAs at a time.
+__device__ __forceinline__ bool lock(PromptCtl* ctl, const PromptArgs& a) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (atomicCAS(&ctl->lock, 0u, 1u) == 0) return true;
+  const unsigned long long t0 = tc::globaltimer_ns();
+  while (atomicCAS(&ctl->lock, 0u, 1u) != 0) {
+    if (*reinterpret_cast<volatile int*>(&ctl->abort_flag)) return false;
+    if (tc::globaltimer_ns() - t0 > a.wait_limit_ns) {
+      *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
+      if (a.status) atomicOr(a.status, MLA_FAULT_WAIT_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ void unlock(PromptCtl* ctl) { atomicExch(&ctl->lock, 0u); }
 // One lane of a whole warp, always the same.
 __device__ __forceinline__ bool elect() {
   uint32_t r;
@@ -351,7 +368,6 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
       tc::mbar_init(&ctl->job_empty[i], (rank ? 1 : 3) + 2 * kSoft / 32);
       tc::mbar_init(&ctl->claim_full[i], 1);
       tc::mbar_init(&ctl->claim_empty[i], 1);
-      tc::mbar_init(&ctl->turn[i], 1);
       tc::mbar_init(&ctl->drain[i], 1);
     }
     for (int i = 0; i < kStages; ++i) {
@@ -362,6 +378,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
       tc::mbar_init(&ctl->v_empty[i], 2);
     }
     ctl->abort_flag = 0;
+    ctl->lock = 0;
     for (int i = 0; i < 4; ++i) ctl->bad_piece[i] = 0;
     tc::fence_barrier_init();
     tc::prefetch_tmap(&tm_q);
@@ -385,7 +402,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
   if (warp == 0) {
     // ------------------------------------------------------------ pieces and copies
-    uint32_t seq = 0, n = 0, xq0 = 0, xq1 = 0;   // pieces, tiles and queries of the halves so far
+    uint32_t seq = 0, n = 0, xq0 = 0, xq1 = 0, claims = 0;   // pieces, tiles, queries of the halves so far
     bool ok = true;
     auto wait0 = [&](uint64_t* bar, uint32_t parity) {
       int v = 1;
@@ -402,39 +419,126 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
       at = pair < parts ? a.part_place[pair] : 0;
       end = pair < parts ? a.part_place[pair + 1] : 0;
     }
-    while (ok) {
-      Piece p;
+    // The piece at `at`, none (no rows) at the end; moves `at` on.
+    auto next = [&](Piece& p) {
       p.rows = 0;
-      if (parts > 0 ? at < end : at < all) {
-        const long long* first = parts > 0 ? a.first_place : a.first_item;
+      const long long* first = parts > 0 ? a.first_place : a.first_item;
+      while (parts > 0 ? at < end : at < all) {
         const int r = find_request(first, a.R, at, lane);
-        int row0, key0;
+        int row0, u;
         bool good;
-        const Request q = request(a, r, row0, key0, good);
-        const long long x = at - first[r], per = parts > 0 ? places(q) : items(q);
-        p.head = head_at(x, per, a.H);
-        const long long rest = x - p.head * per;
-        const int u = parts > 0 ? item_at(q, rest) : items(q) - 1 - (int)rest;
-        const int tiles = item_tiles(q, u);
-        p.row0 = row0 + u * kRows;
-        p.rows = min(q.n - u * kRows, kRows);
-        p.key0 = key0;
-        p.m = q.m;
-        p.causal = q.causal;
-        p.lim0 = u * kRows + 1 + q.m - q.n;
+        const Request q = request(a, r, row0, p.key0, good);
+        const long long x = at - first[r];
         p.t0 = 0;
+        if (parts > 0) {
+          const long long per = places(q);
+          p.head = head_at(x, per, a.H);
+          const long long rest = x - p.head * per;
+          u = item_at(q, rest);
+          p.t0 = (int)(rest - before(q, u));
+        } else {
+          claimed_item(q, a.H, 3 * (int)(gridDim.x >> 1), (int)x, p.head, u);
+        }
+        const int tiles = item_tiles(q, u);
         p.t1 = tiles;
         p.slot = -1;
         if (parts > 0) {
-          p.t0 = (int)(rest - before(q, u));
-          p.t1 = (int)min((long long)tiles, p.t0 + (end - at));
+          const long long left = min(end - at, (long long)(tiles + kExtra - p.t0));
+          at += left;
+          if (p.t0 >= tiles) continue;           // what an item costs besides its tiles
+          p.t1 = (int)min((long long)tiles, p.t0 + left);
           if (p.t0 > 0) p.slot = 2 * pair;
           else if (p.t1 < tiles) p.slot = 2 * pair + 1;
-          at += p.t1 - p.t0;
+        }
+        p.row0 = row0 + u * kRows;
+        p.rows = min(q.n - u * kRows, kRows);
+        p.m = q.m;
+        p.causal = q.causal;
+        p.lim0 = u * kRows + 1 + q.m - q.n;
+        break;
+      }
+      if (parts > 0 || p.rows == 0) return;
+      // The first CTA claims the item after this and tells the second.
+      int got = 1;
+      if (lane == 0) {
+        const int i = claims & 1;
+        const uint32_t phase = claims >> 1 & 1;
+        if (rank == 0) {
+          at = (long long)(gridDim.x >> 1) + atomicAdd(&a.plan->claimed, 1);
+          got = claims < 2 || pr_wait_pair(&ctl->claim_empty[i], phase ^ 1, ctl, a);
+          if (got) {
+            asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(tc::map_rank(&ctl->claim[i], 1)), "l"(at)
+                         : "memory");
+            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                             tc::map_rank(&ctl->claim_full[i], 1))
+                         : "memory");
+          }
+        } else {
+          got = pr_wait_pair(&ctl->claim_full[i], phase, ctl, a);
+          if (got) {
+            at = *reinterpret_cast<volatile long long*>(&ctl->claim[i]);
+            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                             tc::map_rank(&ctl->claim_empty[i], 0))
+                         : "memory");
+          }
         }
       }
+      ++claims;
+      at = __shfl_sync(0xffffffffu, at, 0);
+      ok = __shfl_sync(0xffffffffu, got, 0) != 0;
+    };
+    // Queries are loaded as soon as their half's last S of the piece before is done, whatever else
+    // the warp waits for: q[h] tells what is next for half h, this piece's or the next one's. All
+    // that is lane 0's.
+    struct Load {
+      int head, row, due;
+    } q0 = {0, 0, 0}, q1 = {0, 0, 0}, n0 = {0, 0, 0}, n1 = {0, 0, 0};
+    auto load_q = [&](int h, Load& q, uint32_t& x) {
+      if (!q.due || (x > 0 && !tc::mbar_test_wait(&ctl->q_empty[h], (x - 1) & 1))) return;
+      const uint32_t bar = tc::map_rank(&ctl->q_full[h], 0);
+      tc::remote_arrive_expect_tx(bar, kQBlocks * kBlock);
+#pragma unroll 1
+      for (int e = 0; e < kQBlocks; ++e)
+        tma_load_3d_pair(smem + (h * kQBlocks + e) * kBlock, &tm_q, bar, e * 128, q.head, q.row + h * kHalf);
+      q.due = 0;
+      ++x;
+    };
+    auto load_queries = [&] {
+      if (q0.due) load_q(0, q0, xq0);
+      else load_q(0, n0, xq0);
+      if (q1.due) load_q(1, q1, xq1);
+      else load_q(1, n1, xq1);
+    };
+    // Waits for a place in a ring (bar null: for this piece's queries to be asked for).
+    auto wait_ring = [&](uint64_t* bar, uint32_t parity) {
+      int v = 1;
+      if (lane == 0) {
+        unsigned long long t0 = 0;
+        for (int i = 0;; ++i) {
+          if (q0.due | q1.due | n0.due | n1.due) load_queries();
+          if (bar ? tc::mbar_try_wait(bar, parity) : !(q0.due | q1.due)) break;
+          if (i < 32) continue;
+          if (!t0) t0 = tc::globaltimer_ns();
+          if (*reinterpret_cast<volatile int*>(&ctl->abort_flag) || tc::globaltimer_ns() - t0 > a.wait_limit_ns) {
+            if (atomicExch(&ctl->abort_flag, 1) == 0 && a.status) atomicOr(a.status, MLA_FAULT_WAIT_TIMEOUT);
+            v = 0;
+            break;
+          }
+        }
+      }
+      return __shfl_sync(0xffffffffu, v, 0) != 0;
+    };
+    auto queries = [&](const Piece& p, Load& a0, Load& a1) {
+      const int row = p.row0 + (int)rank * kMine;
+      a0 = {p.head, row, p.rows > 0 && half_tiles(p, 0) > 0};
+      a1 = {p.head, row, p.rows > 0 && half_tiles(p, 1) > 0};
+    };
+    Piece p;
+    next(p);
+    queries(p, q0, q1);
+    while (ok) {
       // Hand it on, or an empty one at the end.
-      if (seq >= 2 && !(ok = wait0(&ctl->job_empty[seq & 1], ((seq >> 1) - 1) & 1))) break;
+      if (seq >= 2 && !(ok = wait_ring(&ctl->job_empty[seq & 1], ((seq >> 1) - 1) & 1))) break;
       if (lane == 0) {
         volatile Piece* s = &ctl->job[seq & 1];
         s->row0 = p.row0;
@@ -450,41 +554,14 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
         tc::mbar_arrive(&ctl->job_full[seq & 1]);
       }
       if (p.rows == 0) break;
-      if (parts == 0) {
-        // The first CTA claims the next item and tells the second.
-        int got = 1;
-        if (lane == 0) {
-          const int i = seq & 1;
-          const uint32_t phase = seq >> 1 & 1;
-          if (rank == 0) {
-            at = (long long)(gridDim.x >> 1) + atomicAdd(&a.plan->claimed, 1);
-            got = seq < 2 || pr_wait_pair(&ctl->claim_empty[i], phase ^ 1, ctl, a);
-            if (got) {
-              asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(tc::map_rank(&ctl->claim[i], 1)), "l"(at)
-                           : "memory");
-              asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                               tc::map_rank(&ctl->claim_full[i], 1))
-                           : "memory");
-            }
-          } else {
-            got = pr_wait_pair(&ctl->claim_full[i], phase, ctl, a);
-            if (got) {
-              at = *reinterpret_cast<volatile long long*>(&ctl->claim[i]);
-              asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                               tc::map_rank(&ctl->claim_empty[i], 0))
-                           : "memory");
-            }
-          }
-        }
-        at = __shfl_sync(0xffffffffu, at, 0);
-        if (!(ok = __shfl_sync(0xffffffffu, got, 0) != 0)) break;
-      }
       ++seq;
-      const int c0 = half_tiles(p, 0), c1 = half_tiles(p, 1), nt = max(c0, c1), kvh = p.head / a.group;
+      const int nt = max(half_tiles(p, 0), half_tiles(p, 1)), kvh = p.head / a.group;
+      const int key0 = p.key0 + p.t0 * kKeys;
+      bool ahead = false;
 #pragma unroll 1
       for (int t = 0; t < nt; ++t, ++n) {
-        const int st = n % kStages, key = p.key0 + (p.t0 + t) * kKeys;
-        if (n >= kStages && !(ok = wait0(&ctl->k_empty[st], (n / kStages - 1) & 1))) break;
+        const int st = n % kStages, key = key0 + t * kKeys;
+        if (n >= kStages && !(ok = wait_ring(&ctl->k_empty[st], (n / kStages - 1) & 1))) break;
         if (lane == 0 && !(withheld && n == 0)) {
           const uint32_t bar = tc::map_rank(&ctl->k_full[st], 0);
           uint8_t* dst = smem + kOffK + st * kKBytes;
@@ -494,29 +571,31 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
           tma_load_3d_pair(dst + kKBlock, &tm_k, bar, 128, kvh, mine);
           tc::tma_load_2d_pair(dst + 2 * kKBlock, &tm_r, bar, 0, mine);
         }
-        if (t == 0) {
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            if (!(h ? c1 : c0)) continue;
-            const uint32_t x = h ? xq1 : xq0;
-            if (x > 0 && !(ok = wait0(&ctl->q_empty[h], (x - 1) & 1))) break;
-            ++(h ? xq1 : xq0);
-            if (lane == 0) {
-              const uint32_t bar = tc::map_rank(&ctl->q_full[h], 0);
-              tc::remote_arrive_expect_tx(bar, kQBlocks * kBlock);
-              for (int e = 0; e < kQBlocks; ++e)
-                tma_load_3d_pair(smem + (h * kQBlocks + e) * kBlock, &tm_q, bar, e * 128, p.head,
-                                 p.row0 + h * kHalf + (int)rank * kMine);
-            }
-          }
-          if (!ok) break;
-        }
-        if (n >= kStages && !(ok = wait0(&ctl->v_empty[st], (n / kStages - 1) & 1))) break;
+        if (lane == 0) load_queries();
+        if (n >= kStages && !(ok = wait_ring(&ctl->v_empty[st], (n / kStages - 1) & 1))) break;
         if (lane == 0) {
           tc::mbar_arrive_expect_tx(&ctl->v_land[st], kVBytes);
           tc::tma_load_3d(smem + kOffV + st * kVBytes, &tm_v, &ctl->v_land[st], (int)rank * 128, kvh, key);
         }
+        // The next piece is looked up while this one's tiles are multiplied.
+        if (t == kStages - 1) {
+          next(p);
+          queries(p, n0, n1);
+          ahead = true;
+          if (!ok) {
+            ++n;                                 // loaded
+            break;
+          }
+        }
       }
+      if (ok && !ahead) {
+        next(p);
+        queries(p, n0, n1);
+      }
+      if (!ok || !(ok = wait_ring(nullptr, 0))) break;
+      q0 = n0;
+      q1 = n1;
+      n0.due = n1.due = 0;
     }
     // Never leave with copies in flight: another role may have given up a wait. V counts here, the
     // pair's K and queries on the first CTA; the CTAs leave together.
@@ -545,7 +624,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
     if (rank == 0) {
     const int h = __shfl_sync(0xffffffffu, warp, 0) - 1;
     const bool one = elect();
-    uint32_t n0 = 0, xq = 0, xp = 0, turn = h ^ 1;   // half 0 begins
+    uint32_t n0 = 0, xq = 0, xp = 0;
     const uint32_t s_k = tc::smem_u32(smem + kOffK), s_v = tc::smem_u32(smem + kOffV);
     const uint32_t col_s = tmem + h * kKeys, col_o = tmem + kColO + h * kV;
     const uint64_t qd = tc::smem_desc(tc::smem_u32(smem) + h * kQBlocks * kBlock, 16, 1024, tc::kSw128);
@@ -562,39 +641,38 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
       if (!take(ctl, seq, a, p, one)) break;
       const int c = __shfl_sync(0xffffffffu, half_tiles(p, h), 0);
       const int nt = max(c, __shfl_sync(0xffffffffu, half_tiles(p, h ^ 1), 0));
-      // PV of tile t, then S of tile t + 1, the halves in turn: issued as they come, the halves' MMAs
-      // would mingle, both finish late, and both softmaxes then run while the tensor pipe
-      // waits. A tile that only the other half multiplies is given back as it lands. What the
-      // copies bring is waited for before P, where it is there by then, so that nothing stands
-      // between P and the MMAs.
+      // PV of tile t, then S of tile t + 1, under a lock: issued as they come, the halves' MMAs would
+      // mingle, both finish late, and both softmaxes then run while the tensor pipe waits. What
+      // the copies bring is waited for before P, where it is there by then, so that nothing
+      // stands between P and the MMAs.
 #pragma unroll 1
-      for (int t = -1; t < nt; ++t) {
+      for (int t = -1; t < c; ++t) {
         const uint32_t nv = n0 + t, sv = nv % kStages;          // V of tile t
         const uint32_t nk = nv + 1, sk = nk % kStages;          // K of tile t + 1
-        const bool has_k = t + 1 < nt, mine = t + 1 < c;
+        const bool has_k = t + 1 < c;
         if (t < 0 && c > 0 && !wait(&ctl->q_full[h], xq++ & 1)) break;
         if (t >= 0 && !wait(&ctl->v_full[sv], (nv / kStages) & 1)) break;
         const bool landed = __all_sync(0xffffffffu, has_k && tc::mbar_test_wait(&ctl->k_full[sk], (nk / kStages) & 1));
-        if (t >= 0 && t < c && !wait(&ctl->p_full[h], xp++ & 1)) break;
-        if (!wait(&ctl->turn[h], turn++ & 1)) break;
-        tc::fence_after_sync();
-        if (t >= 0 && one) {
-          if (t < c) {
+        if (t >= 0) {
+          if (!wait(&ctl->p_full[h], xp++ & 1)) break;
+          if (!(ok = __all_sync(0xffffffffu, !one || lock(ctl, a)))) break;
+          tc::fence_after_sync();
+          if (one) {
             const uint64_t v = tc::smem_desc(s_v + sv * kVBytes, kBlock, 1024, tc::kSw128);
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
               mma_bf16_ts_pair(col_o, col_s + kk * 8, v + (kk * 16 * 128 >> 4), kIdescO, t + kk != 0);
             tc::mma_commit_pair(&ctl->v_empty[sv]);
             if (t == c - 1) tc::mma_commit_pair(&ctl->o_full[h]);
-          } else {
-            give_back(&ctl->v_empty[sv]);
+            if (!landed) unlock(ctl);
           }
+          __syncwarp();
         }
-        __syncwarp();
         if (has_k) {
           if (!landed && !wait(&ctl->k_full[sk], (nk / kStages) & 1)) break;
+          if ((t < 0 || !landed) && !(ok = __all_sync(0xffffffffu, !one || lock(ctl, a)))) break;
           tc::fence_after_sync();
-          if (mine && one) {
+          if (one) {
             const uint64_t k = tc::smem_desc(s_k + sk * kKBytes, 16, 1024, tc::kSw128);
 #pragma unroll
             for (int kk = 0; kk < 12; ++kk)
@@ -603,12 +681,19 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
             tc::mma_commit_pair(&ctl->s_full[h]);
             tc::mma_commit_pair(&ctl->k_empty[sk]);
             if (t + 1 == c - 1) tc::mma_commit_pair(&ctl->q_empty[h]);
-          } else if (one) {
-            give_back(&ctl->k_empty[sk]);
+            unlock(ctl);
           }
+          __syncwarp();
         }
-        if (one) tc::mbar_arrive(&ctl->turn[h ^ 1]);
-        __syncwarp();
+      }
+      // Tiles that only the other half multiplies are given back as they land; this half goes on to
+      // its next piece while the other finishes.
+      for (int t = c; ok && t < nt; ++t) {
+        const uint32_t n = n0 + t, st = n % kStages;
+        if (!wait(&ctl->k_full[st], (n / kStages) & 1)) break;
+        if (one) give_back(&ctl->k_empty[st]);
+        if (!wait(&ctl->v_full[st], (n / kStages) & 1)) break;
+        if (one) give_back(&ctl->v_empty[st]);
       }
       n0 += nt;
     }
@@ -850,8 +935,9 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptArgs a) {
   const int head = head_at(x, per, a.H);
   const long long rest = x - head * per;
   const int u = item_at(q, rest);
+  // A cut among an item's extra places is none.
   const long long start = x0 - (rest - before(q, u)), end = start + item_tiles(q, u);
-  if (start == x0 || place[cut - 1] > start) return;
+  if (start == x0 || x0 >= end || place[cut - 1] > start) return;
   const int j = blockIdx.y * 32 + lane, rows = min(q.n - u * kRows, kRows);
   if (j >= rows) return;
   // Pieces: the tail of part cut - 1, then the heads of the parts from `cut` on.

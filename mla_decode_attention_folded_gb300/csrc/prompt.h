@@ -1,7 +1,7 @@
 // The work of a batch of prompts: items of 512 query rows of one head, each with the
-// tiles of 128 keys that its rows see, and how all items lie on one line of places (a
-// place is a tile). A pair of CTAs takes an item, as two halves of 256 rows. Host and
-// device code include this.
+// tiles of 128 keys that its rows see, and how all items lie on one line of places: a
+// place for each tile, then kExtra for what an item costs besides. A pair of CTAs takes an
+// item, as two halves of 256 rows. Host and device code include this.
 #pragma once
 
 #include "internal.h"
@@ -14,7 +14,8 @@ constexpr int kHalf = 256;       // of its half
 constexpr int kKeys = 128;       // keys of a tile
 constexpr int kStep = kRows / kKeys;
 constexpr int kUncut = 4;        // items of no more tiles are never cut
-constexpr int kMinPart = 3;      // tiles of a part, at least
+constexpr int kMinPart = 3;      // places of a part, at least
+constexpr int kExtra = 1;        // of an item: its first softmax, its output
 constexpr int kWhole = 4;        // items stay whole where a pair has so many of the longest's tiles
 
 // A request of n query tokens and m keys; causal: query i sees keys j <= i + m - n.
@@ -33,16 +34,16 @@ __host__ __device__ inline int limit(const Request& q, int i) {
   const int e = i + 1 + (q.m - q.n);
   return e < 0 ? 0 : e < q.m ? e : q.m;
 }
-// Places of item u: the tiles that its last row sees, one where there are none.
+// Tiles of item u: those that its last row sees, one where there are none.
 __host__ __device__ inline int item_tiles(const Request& q, int u) {
   const int last = (u + 1) * kRows < q.n ? (u + 1) * kRows : q.n;
   const int t = tiles_of(limit(q, last - 1));
   return t < 1 ? 1 : t;
 }
-// Places of the items before item u, 0 <= u <= items. All items but the last have 512 rows,
+// Tiles of the items before item u, 0 <= u <= items. All items but the last have 512 rows,
 // so item v of them sees 512 (v + 1) + m - n keys: max(1, 4 (v + 1) + ceil((m - n) / 128))
 // tiles, of which the first z are ones.
-__host__ __device__ inline long long before(const Request& q, int u) {
+__host__ __device__ inline long long tiles_before(const Request& q, int u) {
   const int I = items(q);
   if (I == 0) return 0;
   const long long v = u < I ? u : I - 1, last = u < I ? 0 : item_tiles(q, I - 1);
@@ -54,6 +55,10 @@ __host__ __device__ inline long long before(const Request& q, int u) {
   long long z = c < 0 ? -c / kStep : 0;
   if (z > v) z = v;
   return z + kStep / 2 * (v * (v + 1) - z * (z + 1)) + (v - z) * c + last;
+}
+// Places of the items before item u.
+__host__ __device__ inline long long before(const Request& q, int u) {
+  return tiles_before(q, u) + (long long)kExtra * u;
 }
 __host__ __device__ inline long long places(const Request& q) { return before(q, items(q)); }
 // x = head * per + rest, 0 <= rest < per, without a division (the kernel that splits its registers
@@ -78,6 +83,17 @@ __host__ __device__ inline int item_at(const Request& q, long long x) {
   return lo;
 }
 
+// Items in the order in which they are claimed: heads in groups, within a group the longest
+// first, so that the last ones are short and few heads' keys are in use at a time. A group has about
+// `wide` items. x = item of the request -> its head and place in it.
+__host__ __device__ inline void claimed_item(const Request& q, int H, int wide, int x, int& head, int& u) {
+  const int I = items(q), most = (wide + I - 1) / I, heads = most < 1 ? 1 : most < H ? most : H;
+  const int g = x / (heads * I), y = x - g * heads * I;
+  const int here = H - g * heads < heads ? H - g * heads : heads;
+  u = I - 1 - y / here;
+  head = g * heads + y % here;
+}
+
 // The plan in the workspace: words, then the requests' first places and items (R + 1 each), then
 // where the parts begin (parts + 1).
 struct Plan {
@@ -90,9 +106,8 @@ __host__ __device__ inline long long part_at(long long total, int parts, int p) 
   return cdiv(total * p, parts);
 }
 // How a batch is shared out among the pairs of CTAs, by its places and its longest item: whole
-// items where a pair's share is worth several of them (they are claimed longest first within each
-// head, so that little is left over at the end and the pairs work on few heads at a time, whose
-// keys stay in L2), else equal parts of the line.
+// items where a pair's share is worth several of them, claimed one by one, else equal parts of
+// the line.
 __host__ __device__ inline int parts_of(long long total, int longest, int pairs) {
   if (longest <= kUncut || total >= (long long)kWhole * longest * pairs) return 0;
   const long long p = cdiv(total, kMinPart);

@@ -49,9 +49,9 @@ int main(int argc, char** argv) {
           most = std::max(most, (int)cdiv(lim, 128));
         }
         CHECK(item_tiles(q[r], u) == std::max(most, 1));
-        CHECK(item_at(q[r], at) == u && item_at(q[r], at + item_tiles(q[r], u) - 1) == u);
+        CHECK(item_at(q[r], at) == u && item_at(q[r], at + item_tiles(q[r], u) + kExtra - 1) == u);
         longest = std::max(longest, item_tiles(q[r], u));
-        at += item_tiles(q[r], u);
+        at += item_tiles(q[r], u) + kExtra;
       }
       CHECK(places(q[r]) == at);
       const int I = items(q[r]);
@@ -68,6 +68,16 @@ int main(int argc, char** argv) {
     CHECK(parts >= 0 && parts <= ctas);
     if (!parts) {
       ++whole_batches;
+      // Every item is claimed once, the longest first within a group of heads.
+      for (int r = 0; r < R; ++r) {
+        std::set<std::pair<int, int>> seen;
+        const int I = items(q[r]), wide = pick(1, 500);
+        for (int x = 0; x < I * H; ++x) {
+          int head, u;
+          claimed_item(q[r], H, wide, x, head, u);
+          CHECK(head >= 0 && head < H && u >= 0 && u < I && seen.insert({head, u}).second);
+        }
+      }
       continue;
     }
     ++cut_batches;
@@ -90,8 +100,10 @@ int main(int argc, char** argv) {
         const long long rest = x - head * per;
         const int u = item_at(q[r], rest), tiles = item_tiles(q[r], u);
         const int t0 = (int)(rest - before(q[r], u));
-        const int t1 = (int)std::min((long long)tiles, t0 + (end - at));
-        const long long start = at - t0;
+        const long long left = std::min(end - at, (long long)(tiles + kExtra - t0)), start = at - t0;
+        at += left;
+        if (t0 >= tiles) continue;
+        const int t1 = (int)std::min((long long)tiles, t0 + left);
         CHECK(t1 > t0 && done[start] == t0);
         done[start] = t1;
         int slot = -1;
@@ -104,7 +116,6 @@ int main(int argc, char** argv) {
         } else {
           whole.insert(start);
         }
-        at += t1 - t0;
       }
     }
     std::set<int> read;
@@ -114,7 +125,7 @@ int main(int argc, char** argv) {
       const long long x = x0 - first[r], per = places(q[r]), rest = x - head_at(x, per, H) * per;
       const int u = item_at(q[r], rest);
       const long long start = x0 - (rest - before(q[r], u)), end = start + item_tiles(q[r], u);
-      if (start == x0 || part_at(total, parts, cut - 1) > start) continue;
+      if (start == x0 || x0 >= end || part_at(total, parts, cut - 1) > start) continue;
       ++joins;
       int last = cut, tiles = 0;
       while (last + 1 < parts && part_at(total, parts, last + 1) < end) ++last;
