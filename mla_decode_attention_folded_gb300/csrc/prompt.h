@@ -16,7 +16,7 @@ constexpr int kStep = kRows / kKeys;
 constexpr int kUncut = 4;        // items of no more tiles are never cut
 constexpr int kMinPart = 3;      // places of a part, at least
 constexpr int kExtra = 1;        // of an item: its first softmax, its output
-constexpr int kWhole = 4;        // items stay whole where a pair has so many of the longest's tiles
+constexpr int kWhole = 6;        // items stay whole where a pair has so many of the longest's tiles
 
 // A request of n query tokens and m keys; causal: query i sees keys j <= i + m - n.
 struct Request {
@@ -84,10 +84,11 @@ __host__ __device__ inline int item_at(const Request& q, long long x) {
 }
 
 // Items in the order in which they are claimed: heads in groups, within a group the longest
-// first, so that the last ones are short and few heads' keys are in use at a time. A group has about
-// `wide` items. x = item of the request -> its head and place in it.
+// first, so that the last ones are short and few heads' keys are in use at a time. Groups of equal
+// size, of about `wide` items. x = item of the request -> its head and place in it.
 __host__ __device__ inline void claimed_item(const Request& q, int H, int wide, int x, int& head, int& u) {
-  const int I = items(q), most = (wide + I - 1) / I, heads = most < 1 ? 1 : most < H ? most : H;
+  const int I = items(q), most = (wide + I - 1) / I, groups = most < H ? H / most : 1;
+  const int heads = (H + groups - 1) / groups;
   const int g = x / (heads * I), y = x - g * heads * I;
   const int here = H - g * heads < heads ? H - g * heads : heads;
   u = I - 1 - y / here;
