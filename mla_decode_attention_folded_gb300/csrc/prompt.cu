@@ -629,9 +629,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
     const uint32_t col_s = tmem + h * kKeys, col_o = tmem + kColO + h * kV;
     const uint64_t qd = tc::smem_desc(tc::smem_u32(smem) + h * kQBlocks * kBlock, 16, 1024, tc::kSw128);
     bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      return ok = __all_sync(0xffffffffu, pr_wait(bar, parity, ctl, a));
-    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = pr_wait(bar, parity, ctl, a); };
     auto give_back = [&](uint64_t* bar) {        // what this half does not multiply
       tc::remote_arrive(tc::map_rank(bar, 0));
       tc::remote_arrive(tc::map_rank(bar, 1));
@@ -652,27 +650,26 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
         const bool has_k = t + 1 < c;
         if (t < 0 && c > 0 && !wait(&ctl->q_full[h], xq++ & 1)) break;
         if (t >= 0 && !wait(&ctl->v_full[sv], (nv / kStages) & 1)) break;
-        const bool landed = __all_sync(0xffffffffu, has_k && tc::mbar_test_wait(&ctl->k_full[sk], (nk / kStages) & 1));
+        const bool landed = has_k && tc::mbar_test_wait(&ctl->k_full[sk], (nk / kStages) & 1);
         if (t >= 0) {
           if (!wait(&ctl->p_full[h], xp++ & 1)) break;
-          if (!(ok = __all_sync(0xffffffffu, !one || lock(ctl, a)))) break;
-          tc::fence_after_sync();
           if (one) {
+            if (!(ok = lock(ctl, a))) break;
+            tc::fence_after_sync();
             const uint64_t v = tc::smem_desc(s_v + sv * kVBytes, kBlock, 1024, tc::kSw128);
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
-              mma_bf16_ts_pair(col_o, col_s + kk * 8, v + (kk * 16 * 128 >> 4), kIdescO, t + kk != 0);
+              mma_bf16_ts_pair(col_o, col_s + (kk >> 2) * 64 + (kk & 3) * 8, v + (kk * 16 * 128 >> 4), kIdescO, t + kk != 0);
             tc::mma_commit_pair(&ctl->v_empty[sv]);
             if (t == c - 1) tc::mma_commit_pair(&ctl->o_full[h]);
             if (!landed) unlock(ctl);
           }
-          __syncwarp();
         }
         if (has_k) {
           if (!landed && !wait(&ctl->k_full[sk], (nk / kStages) & 1)) break;
-          if ((t < 0 || !landed) && !(ok = __all_sync(0xffffffffu, !one || lock(ctl, a)))) break;
-          tc::fence_after_sync();
           if (one) {
+            if ((t < 0 || !landed) && !(ok = lock(ctl, a))) break;
+            tc::fence_after_sync();
             const uint64_t k = tc::smem_desc(s_k + sk * kKBytes, 16, 1024, tc::kSw128);
 #pragma unroll
             for (int kk = 0; kk < 12; ++kk)
@@ -683,9 +680,9 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
             if (t + 1 == c - 1) tc::mma_commit_pair(&ctl->q_empty[h]);
             unlock(ctl);
           }
-          __syncwarp();
         }
       }
+      ok = __all_sync(0xffffffffu, ok);
       // Tiles that only the other half multiplies are given back as they land; this half goes on to
       // its next piece while the other finishes.
       for (int t = c; ok && t < nt; ++t) {
@@ -695,6 +692,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
         if (!wait(&ctl->v_full[st], (n / kStages) & 1)) break;
         if (one) give_back(&ctl->v_empty[st]);
       }
+      ok = __all_sync(0xffffffffu, ok);
       n0 += nt;
     }
     if (one) {
@@ -773,7 +771,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
     const int j = h * kHalf + (int)rank * kMine + row;
     const uint32_t p_full = tc::map_rank(&ctl->p_full[h], 0);
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t col_s = lanes + h * kKeys + side * 64, col_p = lanes + h * kKeys + side * 32;
+    const uint32_t col_s = lanes + h * kKeys + side * 64;
     const uint32_t col_o = lanes + kColO + h * kV + side * 64;
     uint32_t xs = 0, xo = 0;
     Piece p;
@@ -848,7 +846,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
             sum[e & 1] = add_f32x2(sum[e & 1], pack_f32x2(x, y));
             pk[e] = f32x2_to_bf16x2(x, y);
           }
-          tc::tmem_st16(col_p + 16 * i, pk);
+          tc::tmem_st16(col_s + 16 * i, pk);
         }
         float s0, s1;
         unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
