@@ -113,12 +113,13 @@ struct PromptArgs {
   Plan* plan;
   long long* first_place;        // [R + 1]
   long long* first_item;         // [R + 1]
-  long long* part_place;         // [parts + 1]
+  Join* joins;                   // [pairs]
   float* part_o;                 // [slots][32][512][4]
   float* part_lse;               // [slots][512]
   int32_t* status;
   float scale_log2;
   int R, T, Tk, H, group, causal, pairs;
+  int planned;                   // the plan kernel has run; else every CTA plans for itself (R <= 32)
   unsigned long long wait_limit_ns;
   int withhold;                  // failure-detection test: CTA 0 never loads its first keys
 };
@@ -185,11 +186,12 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptA
     a.first_item[a.R] = ti;
     a.plan->total = tw;
     a.plan->all_items = ti;
-    a.plan->parts = parts_of(tw, longest, a.pairs);
+    const bool whole = whole_items(tw, longest, a.pairs);
+    const long long len = whole ? 0 : cdiv(tw, parts_of(tw, a.pairs));
+    a.plan->len = len;
+    a.plan->parts = whole ? 0 : (int)cdiv(tw, len);
     a.plan->claimed = 0;
   }
-  const int parts = parts_of(tw, longest, a.pairs);
-  for (int p = r; parts > 0 && p <= parts; p += blockDim.x) a.part_place[p] = part_at(tw, parts, p);
 }
 
 // The last r with first[r] <= x, by a warp.
@@ -411,24 +413,78 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
     };
     const int pair = blockIdx.x >> 1;
     const bool withheld = a.withhold && blockIdx.x == 0;
-    const int parts = a.plan->parts;
-    const long long all = a.plan->all_items;
-    // Whole items: the first by the pair's index, then claimed. Parts: places [at, end).
+    if (rank == 0 && lane == 0) a.joins[pair].rows = 0;
+    // The plan: read, or made here with a request to a lane (by 32-bit divisions: longer ones are
+    // calls).
+    Request mine = {0, 0, false};
+    int my_row0 = 0, my_key0 = 0, parts;
+    long long my_place = 0, my_item = 0, total, all, len;
+    if (a.planned) {
+      total = a.plan->total;
+      all = a.plan->all_items;
+      parts = a.plan->parts;
+      len = a.plan->len;
+    } else {
+      int longest = 0;
+      if (lane < a.R) {
+        bool good;
+        mine = request(a, lane, my_row0, my_key0, good);
+        if (!good && a.status && blockIdx.x == 0) atomicOr(a.status, MLA_FAULT_WORK_ITEM);
+        const int I = items(mine);
+        my_place = places(mine) * a.H;
+        my_item = (long long)I * a.H;
+        if (I) longest = max(item_tiles(mine, I - 1), I > 1 ? item_tiles(mine, I - 2) : 0);
+      }
+      longest = __reduce_max_sync(0xffffffffu, longest);
+      const long long w = my_place, it = my_item;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, my_place, o), v = __shfl_up_sync(0xffffffffu, my_item, o);
+        if (lane >= o) my_place += u, my_item += v;
+      }
+      total = __shfl_sync(0xffffffffu, my_place, 31);
+      all = __shfl_sync(0xffffffffu, my_item, 31);
+      my_place -= w;
+      my_item -= it;
+      const uint32_t t = (uint32_t)total;
+      parts = 0;
+      len = 0;
+      if (t > 0 && !whole_items(total, longest, a.pairs)) {
+        const uint32_t aim = min((t + kMinPart - 1) / kMinPart, (uint32_t)a.pairs), l = (t + aim - 1) / aim;
+        len = l;
+        parts = (int)((t + l - 1) / l);
+      }
+    }
+    // Whole items: the first by the pair's index, then claimed, or by turns where each CTA plans for
+    // itself. Parts: places [at, end).
     long long at = pair, end = 0;
     if (parts > 0) {
-      at = pair < parts ? a.part_place[pair] : 0;
-      end = pair < parts ? a.part_place[pair + 1] : 0;
+      at = pair < parts ? part_at(total, len, pair) : 0;
+      end = pair < parts ? part_at(total, len, pair + 1) : 0;
     }
     // The piece at `at`, none (no rows) at the end; moves `at` on.
     auto next = [&](Piece& p) {
       p.rows = 0;
-      const long long* first = parts > 0 ? a.first_place : a.first_item;
       while (parts > 0 ? at < end : at < all) {
-        const int r = find_request(first, a.R, at, lane);
         int row0, u;
-        bool good;
-        const Request q = request(a, r, row0, p.key0, good);
-        const long long x = at - first[r];
+        long long x;
+        Request q;
+        if (a.planned) {
+          const long long* first = parts > 0 ? a.first_place : a.first_item;
+          const int r = find_request(first, a.R, at, lane);
+          bool good;
+          q = request(a, r, row0, p.key0, good);
+          x = at - first[r];
+        } else {
+          const long long first = parts > 0 ? my_place : my_item;
+          const int r = 31 - __clz(__ballot_sync(0xffffffffu, lane < a.R && first <= at) | 1);
+          q.n = __shfl_sync(0xffffffffu, mine.n, r);
+          q.m = __shfl_sync(0xffffffffu, mine.m, r);
+          q.causal = a.causal;
+          row0 = __shfl_sync(0xffffffffu, my_row0, r);
+          p.key0 = __shfl_sync(0xffffffffu, my_key0, r);
+          x = at - __shfl_sync(0xffffffffu, first, r);
+        }
         p.t0 = 0;
         if (parts > 0) {
           const long long per = places(q);
@@ -442,22 +498,35 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
         const int tiles = item_tiles(q, u);
         p.t1 = tiles;
         p.slot = -1;
-        if (parts > 0) {
-          const long long left = min(end - at, (long long)(tiles + kExtra - p.t0));
-          at += left;
-          if (p.t0 >= tiles) continue;           // what an item costs besides its tiles
-          p.t1 = (int)min((long long)tiles, p.t0 + left);
-          if (p.t0 > 0) p.slot = 2 * pair;
-          else if (p.t1 < tiles) p.slot = 2 * pair + 1;
-        }
         p.row0 = row0 + u * kRows;
         p.rows = min(q.n - u * kRows, kRows);
+        if (parts > 0) {
+          const long long left = min(end - at, (long long)(tiles + kExtra - p.t0)), stop = at - p.t0 + tiles;
+          at += left;
+          if (p.t0 >= tiles) {                   // what an item costs besides its tiles
+            p.rows = 0;
+            continue;
+          }
+          p.t1 = (int)min((long long)tiles, p.t0 + left);
+          if (p.t0 > 0) {
+            p.slot = 2 * pair;
+          } else if (p.t1 < tiles) {
+            p.slot = 2 * pair + 1;
+            int last = pair + 1;
+            while (last + 1 < parts && part_at(total, len, last + 1) < stop) ++last;
+            if (rank == 0 && lane == 0) a.joins[pair] = {p.row0, p.rows, p.head, last};
+          }
+        }
         p.m = q.m;
         p.causal = q.causal;
         p.lim0 = u * kRows + 1 + q.m - q.n;
         break;
       }
       if (parts > 0 || p.rows == 0) return;
+      if (!a.planned) {
+        at += gridDim.x >> 1;
+        return;
+      }
       // The first CTA claims the item after this and tells the second.
       int got = 1;
       if (lane == 0) {
@@ -914,64 +983,47 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
 }
 
 // ---------------------------------------------------------------- joining the pieces
-// An item that a cut runs through: CTA (c - 1, s) of the first cut c within it joins 32 of its rows.
-constexpr int kSlices = kRows / 32;
+// An item that a cut runs through: CTA (p, s) joins 16 rows of the one that begins in part p. A warp
+// has 16 rows x 2 quads of dims, 256 bytes in a row; a thread two quads of a row.
+constexpr int kJoinRows = 16, kSlices = kRows / kJoinRows;
 
 __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptArgs a) {
   grid_dep_wait();
   grid_dep_launch();
-  const int parts = a.plan->parts, cut = blockIdx.x + 1;
-  const long long* place = a.part_place;
-  if (cut >= parts) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long x0 = place[cut];
-  const int r = find_request(a.first_place, a.R, x0, lane);
-  int row0, key0;
-  bool good;
-  const Request q = request(a, r, row0, key0, good);
-  const long long x = x0 - a.first_place[r], per = places(q);
-  const int head = head_at(x, per, a.H);
-  const long long rest = x - head * per;
-  const int u = item_at(q, rest);
-  // A cut among an item's extra places is none.
-  const long long start = x0 - (rest - before(q, u)), end = start + item_tiles(q, u);
-  if (start == x0 || x0 >= end || place[cut - 1] > start) return;
-  const int j = blockIdx.y * 32 + lane, rows = min(q.n - u * kRows, kRows);
+  const int4 jn = *reinterpret_cast<const int4*>(a.joins + blockIdx.y);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = blockIdx.x * kJoinRows + (lane & 15);
+  const int rows = jn.y, part = blockIdx.y, last = jn.w;
   if (j >= rows) return;
-  // Pieces: the tail of part cut - 1, then the heads of the parts from `cut` on.
-  int last = cut;
-  while (last + 1 < parts && place[last + 1] < end) ++last;
+  // Pieces: the last of part `part`, then the first of the parts up to `last`.
+  auto slot = [&](int p) { return (size_t)(p == part ? 2 * p + 1 : 2 * p); };
   float top = -INFINITY;
-  for (int p = cut - 1; p <= last; ++p)
-    top = fmaxf(top, a.part_lse[(size_t)(p < cut ? 2 * p + 1 : 2 * p) * kRows + j]);
+#pragma unroll 8
+  for (int p = part; p <= last; ++p) top = fmaxf(top, a.part_lse[slot(p) * kRows + j]);
   const float base = top == -INFINITY ? 0.f : top;
-  float acc[16], z = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  for (int p = cut - 1; p <= last; ++p) {
-    const int slot = p < cut ? 2 * p + 1 : 2 * p;
-    const float w = ex2(a.part_lse[(size_t)slot * kRows + j] - base);
-    if (w == 0.f) continue;                      // nothing there: its rows may not be written
+  const int quad = (lane >> 4) + 2 * warp;                   // and quad + 16
+  float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0}, z = 0.f;
+#pragma unroll 4
+  for (int p = part; p <= last; ++p) {
+    const float w = ex2(a.part_lse[slot(p) * kRows + j] - base);
+    const float4* src = reinterpret_cast<const float4*>(a.part_o) + (slot(p) * 32 + quad) * kRows + j;
+    float4 v[2] = {src[0], src[16 * kRows]};
     z += w;
-    const float4* src = reinterpret_cast<const float4*>(a.part_o) + ((size_t)slot * 32 + warp * 4) * kRows + j;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = src[(size_t)i * kRows];
-      acc[4 * i] += w * v.x;
-      acc[4 * i + 1] += w * v.y;
-      acc[4 * i + 2] += w * v.z;
-      acc[4 * i + 3] += w * v.w;
-    }
+    if (w == 0.f) v[0] = v[1] = make_float4(0, 0, 0, 0);     // nothing there: perhaps not written
+    acc[0] += w * v[0].x;
+    acc[1] += w * v[0].y;
+    acc[2] += w * v[0].z;
+    acc[3] += w * v[0].w;
+    acc[4] += w * v[1].x;
+    acc[5] += w * v[1].y;
+    acc[6] += w * v[1].z;
+    acc[7] += w * v[1].w;
   }
   const float inv = z > 0.f ? 1.f / z : z;       // NaN stays
-  const size_t row = (size_t)(row0 + u * kRows + j) * a.H + head;
-  if (a.lse && warp == 0) a.lse[row] = z > 0.f ? base + log2f(z) : z == 0.f ? -INFINITY : z;
-  uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = f32x2_to_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-  uint4* dst = reinterpret_cast<uint4*>(a.out + row * kV + warp * 16);
-  dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  const size_t row = (size_t)(jn.x + j) * a.H + jn.z;
+  if (a.lse && threadIdx.x < 16) a.lse[row] = z > 0.f ? base + log2f(z) : z == 0.f ? -INFINITY : z;
+  uint2* dst = reinterpret_cast<uint2*>(a.out + row * kV) + quad;
+  dst[0] = make_uint2(f32x2_to_bf16x2(acc[0] * inv, acc[1] * inv), f32x2_to_bf16x2(acc[2] * inv, acc[3] * inv));
+  dst[16] = make_uint2(f32x2_to_bf16x2(acc[4] * inv, acc[5] * inv), f32x2_to_bf16x2(acc[6] * inv, acc[7] * inv));
 }
 
 int check_prompt(const mla_prompt_shape* s) {
@@ -1020,7 +1072,7 @@ int32_t prompt_impl(const mla_prompt_shape* s, const void* q, const void* k_nope
   a.plan = reinterpret_cast<Plan*>(ws);
   a.first_place = reinterpret_cast<long long*>(ws + sizeof(Plan));
   a.first_item = a.first_place + s->R + 1;
-  a.part_place = a.first_item + s->R + 1;
+  a.joins = reinterpret_cast<Join*>(a.first_item + s->R + 1);
   a.part_lse = reinterpret_cast<float*>(ws + plan_bytes(s->R, pairs_of(s->num_ctas)));
   a.part_o = reinterpret_cast<float*>(ws + plan_bytes(s->R, pairs_of(s->num_ctas)) + lse_bytes(pairs_of(s->num_ctas)));
   a.status = status;
@@ -1062,19 +1114,26 @@ int32_t prompt_impl(const mla_prompt_shape* s, const void* q, const void* k_nope
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3((unsigned)(cdiv(s->R, 32) * 32));
-  if (cudaLaunchKernelEx(&cfg, prompt_plan_kernel, a) != cudaSuccess) return MLA_ERR_CUDA;
+  // A batch of few requests and items has no plan kernel before it: 24 prompts up to 2k, 132 ->
+  // TODO us. Others gain by claimed items, which need one.
+  const long long items_least = (long long)s->H * cdiv(s->tokens, kRows);
+  const long long items_most = items_least + (long long)s->H * s->R;
+  const long long places_most = items_most * (1 + kExtra + cdiv(s->keys, kKeys));
+  a.planned = s->R > 32 || items_least >= (long long)kWhole * a.pairs || places_most >= (1ll << 31);
+  if (a.planned) {
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3((unsigned)(cdiv(s->R, 32) * 32));
+    if (cudaLaunchKernelEx(&cfg, prompt_plan_kernel, a) != cudaSuccess) return MLA_ERR_CUDA;
+  }
   // No more pairs than the batch can have places.
-  const long long items_most = (long long)s->H * (cdiv(s->tokens, kRows) + s->R);
-  const long long places_most = items_most * (1 + cdiv(s->keys, kKeys));
-  cfg.gridDim = dim3(2 * (unsigned)(places_most < a.pairs ? places_most : a.pairs));
+  const int pairs = (int)(places_most < a.pairs ? places_most : a.pairs);
+  cfg.gridDim = dim3(2 * (unsigned)pairs);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   if (cudaLaunchKernelEx(&cfg, prompt_kernel, a, tq, tk, tr, tv) != cudaSuccess) return MLA_ERR_CUDA;
   // Requests of so few keys that no item can be cut leave nothing to join.
-  if (cdiv(s->keys, kKeys) <= kUncut || a.pairs < 2) return MLA_OK;
-  cfg.gridDim = dim3((unsigned)(a.pairs - 1), kSlices);
+  if (cdiv(s->keys, kKeys) <= kUncut || pairs < 2) return MLA_OK;
+  cfg.gridDim = dim3(kSlices, (unsigned)(pairs - 1));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, prompt_join_kernel, a) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;

@@ -95,22 +95,31 @@ __host__ __device__ inline void claimed_item(const Request& q, int H, int wide, 
   head = g * heads + y % here;
 }
 
-// The plan in the workspace: words, then the requests' first places and items (R + 1 each), then
-// where the parts begin (parts + 1).
+// The plan in the workspace: this, then the requests' first places and items (R + 1 each), then a
+// Join for each pair.
 struct Plan {
   long long total, all_items;    // places and items of the batch
+  long long len;                 // places of a part
   int parts;                     // > 0: the line is cut into so many; 0: whole items, claimed
   int claimed;                   // items claimed beyond the first of each pair
 };
+// An item that a cut runs through, by the pair whose part it begins in (rows 0: none): its pieces
+// are that part's last and the first ones of the parts up to `last`.
+struct Join {
+  int row0, rows, head, last;
+};
 // Where part p begins.
-__host__ __device__ inline long long part_at(long long total, int parts, int p) {
-  return cdiv(total * p, parts);
+__host__ __device__ inline long long part_at(long long total, long long len, int p) {
+  return len * p < total ? len * p : total;
 }
 // How a batch is shared out among the pairs of CTAs, by its places and its longest item: whole
 // items where a pair's share is worth several of them, claimed one by one, else equal parts of
 // the line.
-__host__ __device__ inline int parts_of(long long total, int longest, int pairs) {
-  if (longest <= kUncut || total >= (long long)kWhole * longest * pairs) return 0;
+__host__ __device__ inline bool whole_items(long long total, int longest, int pairs) {
+  return longest <= kUncut || total >= (long long)kWhole * longest * pairs;
+}
+// Parts aimed at; their length is total over them, rounded up, which may leave fewer.
+__host__ __device__ inline int parts_of(long long total, int pairs) {
   const long long p = cdiv(total, kMinPart);
   return (int)(p < pairs ? p : pairs);
 }
@@ -118,7 +127,7 @@ __host__ __device__ inline int parts_of(long long total, int longest, int pairs)
 constexpr size_t kSlotBytes = (size_t)kRows * 128 * 4;     // a piece's FP32 rows
 inline int pairs_of(int ctas) { return ctas < 2 ? 1 : ctas / 2; }
 inline size_t plan_bytes(int R, int pairs) {
-  return align256(sizeof(Plan) + (2 * (size_t)(R + 1) + pairs + 1) * 8);
+  return align256(sizeof(Plan) + 2 * (size_t)(R + 1) * 8 + (size_t)pairs * sizeof(Join));
 }
 inline size_t lse_bytes(int pairs) { return align256((size_t)2 * pairs * kRows * 4); }
 

@@ -64,7 +64,9 @@ int main(int argc, char** argv) {
       }
     }
     const long long total = first[R];
-    const int parts = parts_of(total, longest, ctas);
+    const bool whole_batch = whole_items(total, longest, ctas);
+    const long long len = whole_batch ? 0 : cdiv(total, parts_of(total, ctas));
+    const int parts = whole_batch ? 0 : (int)cdiv(total, len);
     CHECK(parts >= 0 && parts <= ctas);
     if (!parts) {
       ++whole_batches;
@@ -81,7 +83,7 @@ int main(int argc, char** argv) {
       continue;
     }
     ++cut_batches;
-    CHECK(part_at(total, parts, 0) == 0 && part_at(total, parts, parts) == total);
+    CHECK(part_at(total, len, 0) == 0 && part_at(total, len, parts) == total);
     auto find = [&](long long x) {
       int r = 0;
       while (first[r + 1] <= x) ++r;
@@ -90,9 +92,11 @@ int main(int argc, char** argv) {
     std::map<int, std::tuple<long long, int, int>> slots;    // slot -> item's first place, tiles
     std::map<long long, int> done;                           // item's first place -> tiles done
     std::set<long long> whole;
+    std::map<int, std::pair<int, long long>> noted;          // part -> last part, item's first place
+    std::map<long long, int> size_of;
     for (int p = 0; p < parts; ++p) {
-      long long at = part_at(total, parts, p);
-      const long long end = part_at(total, parts, p + 1);
+      long long at = part_at(total, len, p);
+      const long long end = part_at(total, len, p + 1);
       CHECK(end > at);
       while (at < end) {
         const int r = find(at);
@@ -108,7 +112,14 @@ int main(int argc, char** argv) {
         done[start] = t1;
         int slot = -1;
         if (t0 > 0) slot = 2 * p;
-        else if (t1 < tiles) slot = 2 * p + 1;
+        else if (t1 < tiles) {
+          slot = 2 * p + 1;
+          int last = p + 1;
+          while (last + 1 < parts && part_at(total, len, last + 1) < start + tiles) ++last;
+          CHECK(!noted.count(p));
+          noted[p] = {last, start};
+          size_of[start] = tiles;
+        }
         if (slot >= 0) {
           CHECK(!slots.count(slot) && slot < 2 * ctas);
           slots[slot] = std::make_tuple(start, t0, t1);
@@ -119,23 +130,18 @@ int main(int argc, char** argv) {
       }
     }
     std::set<int> read;
-    for (int cut = 1; cut < parts; ++cut) {
-      const long long x0 = part_at(total, parts, cut);
-      const int r = find(x0);
-      const long long x = x0 - first[r], per = places(q[r]), rest = x - head_at(x, per, H) * per;
-      const int u = item_at(q[r], rest);
-      const long long start = x0 - (rest - before(q[r], u)), end = start + item_tiles(q[r], u);
-      if (start == x0 || x0 >= end || part_at(total, parts, cut - 1) > start) continue;
+    for (const auto& jn : noted) {
+      const int part = jn.first, last = jn.second.first;
+      const long long start = jn.second.second;
+      int tiles = 0;
       ++joins;
-      int last = cut, tiles = 0;
-      while (last + 1 < parts && part_at(total, parts, last + 1) < end) ++last;
-      for (int p = cut - 1; p <= last; ++p) {
-        const int slot = p < cut ? 2 * p + 1 : 2 * p;
+      for (int p = part; p <= last; ++p) {
+        const int slot = p == part ? 2 * p + 1 : 2 * p;
         CHECK(slots.count(slot) && std::get<0>(slots[slot]) == start && read.insert(slot).second);
         CHECK(std::get<1>(slots[slot]) == tiles);
         tiles = std::get<2>(slots[slot]);
       }
-      CHECK(tiles == end - start && !whole.count(start));
+      CHECK(tiles == size_of[start] && !whole.count(start));
     }
     CHECK(read.size() == slots.size());
   }
