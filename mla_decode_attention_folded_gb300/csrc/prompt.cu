@@ -51,8 +51,6 @@ constexpr int kOffV = kOffK + kStages * kKBytes;
 constexpr int kOffCtl = kOffV + kStages * kVBytes;
 constexpr int kSoft = 256;                       // softmax threads of a half: two to a row
 constexpr int kThreads = 128 + 2 * kSoft;
-// Registers a thread at the launch (640 x 96 = 61,440), and after the split: 128 x 64 + 512 x 104.
-constexpr int kRegsFew = 64, kRegsMany = 104;
 constexpr uint32_t kTmemCols = 512, kColO = 256;
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;   // 2 s
 constexpr uint32_t kIdescS = tc::idesc_bf16_f32(kHalf, kKeys);   // M = 256 over the pair
@@ -401,7 +399,6 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
   grid_dep_launch();
 
   if (warp < 4) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
   if (warp == 0) {
     // ------------------------------------------------------------ pieces and copies
     uint32_t seq = 0, n = 0, xq0 = 0, xq1 = 0, claims = 0;   // pieces, tiles, queries of the halves so far
@@ -831,7 +828,6 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
     }
   }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
     // ------------------------------------------------------------ softmax and output
     // Thread (h, side, row): keys 64 side .. of its row of S, dims 64 side .. of its row of O. After a
     // wait that ran out a half's threads go on to the end of the piece without waiting, so that
