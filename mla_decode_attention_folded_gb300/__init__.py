@@ -29,6 +29,7 @@ key after a decode, ``kv_evict(...)`` keeps the keys of most weight.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -635,9 +636,9 @@ def kv_weigh(q, kv, block_table, seq_lens, lse, bmm1_scale: float, weights, star
     shape = _weigh_shape(dev, q, kv, block_table, seq_lens, lse, weights, starts, positions,
                          rope_starts, status)
     _lib.check("mla_kv_weigh", _lib.load().mla_kv_weigh(
-        ctypes.byref(shape), _ptr(q), _ptr(kv), _ptr(block_table), _ptr(seq_lens), _ptr(lse),
-        float(bmm1_scale), float(decay), _ptr(starts), _ptr(rope_starts), _ptr(weights),
-        _ptr(positions), _ptr(status), _stream(stream)))
+        ctypes.byref(shape), q.data_ptr(), kv.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+        lse.data_ptr(), bmm1_scale, decay, starts.data_ptr(), _ptr(rope_starts), weights.data_ptr(),
+        _ptr(positions), _ptr(status), _stream_on(dev, stream)))
 
 
 def _weigh_shape(dev, q, kv, block_table, seq_lens, lse, weights, starts, positions, rope_starts,
@@ -678,6 +679,7 @@ def kv_weigh_wait_test(q, kv, block_table, seq_lens, lse, bmm1_scale: float, wei
         _ptr(positions), _ptr(status), int(wait_limit_ns), _stream(stream)))
 
 
+@functools.lru_cache(maxsize=64)
 def kv_evict_workspace_bytes(R: int, max_pages: int, num_pages: int = 1) -> int:
     out = ctypes.c_size_t(0)
     _lib.check("mla_kv_evict_workspace_bytes", _lib.load().mla_kv_evict_workspace_bytes(
@@ -730,18 +732,22 @@ def kv_evict(kv, block_table, seq_lens, weights, keep, positions=None, recent: i
         lens_out = _empty((R,), torch.int32, kv.device, stream)
     else:
         _check(dev, "lens_out", lens_out, _I32, (R,))
-    shape = CacheShape(R, 1, 1, PAGE, max_pages, pages)
     if workspace is None:
-        need = kv_evict_workspace_bytes(R, max_pages)
-        workspace = _empty((need,), torch.uint8, kv.device, stream)
+        workspace = _empty((kv_evict_workspace_bytes(R, max_pages),), torch.uint8, kv.device, stream)
     else:
         _check(dev, "workspace", workspace, (torch.uint8,), workspace.shape)
     _lib.check("mla_kv_evict", _lib.load().mla_kv_evict(
-        ctypes.byref(shape), _ptr(kv), _ptr(block_table), _ptr(seq_lens), _ptr(weights),
-        _ptr(positions), _ptr(keep), int(recent), int(sinks), _ptr(weights_out),
-        _ptr(positions_out), _ptr(lens_out), _ptr(workspace), workspace.numel(), _ptr(status),
-        _stream(stream)))
+        ctypes.byref(CacheShape(R, 1, 1, PAGE, max_pages, pages)), kv.data_ptr(),
+        block_table.data_ptr(), seq_lens.data_ptr(), weights.data_ptr(), _ptr(positions),
+        keep.data_ptr(), recent, sinks, weights_out.data_ptr(), _ptr(positions_out),
+        lens_out.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(status),
+        _stream_on(dev, stream)))
     return lens_out
+
+
+def _stream_on(dev: int, stream) -> int:
+    """The stream's handle; None: the current one of device `dev`."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _apart(name: str, t, other) -> None:
@@ -759,6 +765,11 @@ def prompt_workspace_bytes(R: int, num_ctas: int | None = None, device=None) -> 
     if num_ctas is None:
         num_ctas = torch.cuda.get_device_properties(
             torch.device("cuda" if device is None else device)).multi_processor_count
+    return _prompt_bytes(R, num_ctas)
+
+
+@functools.lru_cache(maxsize=64)
+def _prompt_bytes(R: int, num_ctas: int) -> int:
     shape = PromptShape(R, 1, 1, 1, 1, 1, num_ctas, 192, 192, 128, 128, 128, 128, 64)
     out = ctypes.c_size_t(0)
     _lib.check("mla_prompt_workspace_bytes", _lib.load().mla_prompt_workspace_bytes(
@@ -784,7 +795,7 @@ def prompt_attention(q, k_nope, k_rope, v, cu_tokens, sm_scale: float, cu_keys=N
             return prompt_attention(q, k_nope, k_rope, v, cu_tokens, sm_scale, cu_keys, causal, out,
                                     lse, return_lse, workspace, status, stream)
     shape = _prompt_shape(dev, q, k_nope, k_rope, v, cu_tokens, cu_keys, causal, status)
-    T, H = shape.tokens, shape.H
+    T, H = q.shape[:2]
     if out is None:
         out = _empty((T, H, 128), torch.bfloat16, q.device, stream)
     else:
@@ -796,49 +807,58 @@ def prompt_attention(q, k_nope, k_rope, v, cu_tokens, sm_scale: float, cu_keys=N
     else:
         _check(dev, "lse", lse, _F32, (T, H))
     if workspace is None:
-        need = ctypes.c_size_t(0)
-        _lib.check("mla_prompt_workspace_bytes", _lib.load().mla_prompt_workspace_bytes(
-            ctypes.byref(shape), ctypes.byref(need)))
-        workspace = _empty((need.value,), torch.uint8, q.device, stream)
+        workspace = _empty((_prompt_bytes(shape.R, shape.num_ctas),), torch.uint8, q.device, stream)
     else:
         _check(dev, "workspace", workspace, (torch.uint8,), workspace.shape)
     _lib.check("mla_prompt_attention", _lib.load().mla_prompt_attention(
-        ctypes.byref(shape), _ptr(q), _ptr(k_nope), _ptr(k_rope), _ptr(v), _ptr(cu_tokens),
-        _ptr(cu_keys), float(sm_scale), _ptr(workspace), workspace.numel(), _ptr(out), _ptr(lse),
-        _ptr(status), _stream(stream)))
+        ctypes.byref(shape), q.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(), v.data_ptr(),
+        cu_tokens.data_ptr(), _ptr(cu_keys), sm_scale, workspace.data_ptr(), workspace.numel(),
+        out.data_ptr(), _ptr(lse), _ptr(status), _stream_on(dev, stream)))
     return out, lse
 
 
-def _prompt_shape(dev, q, k_nope, k_rope, v, cu_tokens, cu_keys, causal, status) -> PromptShape:
-    def rows(name, t, dims, width):
-        if _device(name, t, dims) != dev or t.shape[-1] != width or t.dtype != torch.bfloat16 or \
-                t.stride(-1) != 1:
-            raise ValueError(f"{name} is not [..., {width}] BF16 with contiguous dims on q's device")
+@functools.lru_cache(maxsize=None)
+def _sms(dev: int) -> int:
+    return torch.cuda.get_device_properties(dev).multi_processor_count
 
-    rows("q", q, 3, 192)
-    rows("k_nope", k_nope, 3, 128)
-    rows("k_rope", k_rope, 2, 64)
-    rows("v", v, 3, 128)
+
+def _prompt_shape(dev, q, k_nope, k_rope, v, cu_tokens, cu_keys, causal, status) -> PromptShape:
+    bf16 = torch.bfloat16
+    for name, t, dims, width in (("q", q, 3, 192), ("k_nope", k_nope, 3, 128), ("k_rope", k_rope, 2, 64),
+                                 ("v", v, 3, 128)):
+        if not isinstance(t, torch.Tensor) or t.dim() != dims or t.get_device() != dev or \
+                t.dtype is not bf16 or t.shape[-1] != width or t.stride(-1) != 1:
+            raise ValueError(f"{name} is not a tensor of {dims} dims, the last {width} BF16 elements in a "
+                             f"row, on cuda:{dev}")
     (T, H, _), (Tk, Hkv, _) = q.shape, k_nope.shape
-    if v.shape != (Tk, Hkv, 128) or k_rope.shape[0] != Tk:
+    if v.shape != k_nope.shape or k_rope.shape[0] != Tk:
         raise ValueError(f"v {tuple(v.shape)} and k_rope {tuple(k_rope.shape)} do not go with k_nope "
                          f"{tuple(k_nope.shape)}")
-    if _device("cu_tokens", cu_tokens, 1) != dev or cu_tokens.shape[0] < 2:
-        raise ValueError("cu_tokens is not [R + 1] int32 on q's device")
-    R = cu_tokens.shape[0] - 1
-    _check(dev, "cu_tokens", cu_tokens, _I32, (R + 1,))
+    if not isinstance(cu_tokens, torch.Tensor) or cu_tokens.dim() != 1 or cu_tokens.shape[0] < 2:
+        raise ValueError("cu_tokens is not [R + 1] int32")
+    R1 = cu_tokens.shape[0]
+    _check(dev, "cu_tokens", cu_tokens, _I32, (R1,))
     if cu_keys is not None:
-        _check(dev, "cu_keys", cu_keys, _I32, (R + 1,))
+        _check(dev, "cu_keys", cu_keys, _I32, (R1,))
     elif Tk != T:
         raise ValueError(f"{Tk} keys for {T} tokens without cu_keys")
     if status is not None:
         _check(dev, "status", status, _I32, (1,))
     # The stride over a dim of one element is never used: any that the library takes will do.
-    step = lambda t, d, width: t.stride(d) if t.shape[d] > 1 else width  # noqa: E731
-    sms = torch.cuda.get_device_properties(dev).multi_processor_count
-    return PromptShape(R, T, Tk, H, Hkv, 1 if causal else 0, sms, step(q, 0, H * 192), step(q, 1, 192),
-                       step(k_nope, 0, Hkv * 128), step(k_nope, 1, 128), step(v, 0, Hkv * 128),
-                       step(v, 1, 128), step(k_rope, 0, 64))
+    q0, q1, _ = q.stride()
+    k0, k1, _ = k_nope.stride()
+    v0, v1, _ = v.stride()
+    if T < 2:
+        q0 = H * 192
+    if H < 2:
+        q1 = 192
+    r0 = k_rope.stride(0)
+    if Tk < 2:
+        k0 = v0 = Hkv * 128
+        r0 = 64
+    if Hkv < 2:
+        k1 = v1 = 128
+    return PromptShape(R1 - 1, T, Tk, H, Hkv, 1 if causal else 0, _sms(dev), q0, q1, k0, k1, v0, v1, r0)
 
 
 def prompt_attention_wait_test(q, k_nope, k_rope, v, cu_tokens, sm_scale: float, out, lse, workspace,
