@@ -9,10 +9,10 @@
 // source behind `keep` and every target before it, so no two copies touch the same row.
 //
 // Bound by HBM for large evictions (16 B per key, 1,152 B per moved key) and by latency for
-// a step's few keys. Two launches: a cluster per request orders its keys (32-bit codes
-// that sort as the rule does, held in shared memory; the keep-th largest by three digits
-// of histograms, joined over the cluster; places by ordered counts) and lists the moves;
-// then all SMs copy the listed rows, 9 threads a row.
+// a step's few keys. A cluster per request orders its keys: 32-bit codes that sort as the
+// rule does, held in shared memory; the keep-th largest by three digits of histograms, summed
+// in the first CTA; places by ordered counts. It lists the moves and makes them, 9 threads a
+// row; where the clusters of a batch leave most SMs idle, a second launch makes them on all.
 #include <climits>
 
 #include "checks.h"
@@ -29,6 +29,8 @@ constexpr int kMaxCluster = 16;
 constexpr int kCached = 40960;                   // keys a CTA holds in shared memory (160 KB)
 constexpr uint32_t kHeld = 0xFFFFFFFFu;          // above the code of any weight
 
+constexpr int kRowThreads = kDqk / 64;           // threads that copy a row, 64 bytes each
+
 struct EvictArgs {
   uint8_t* kv;
   const int32_t* block_table;
@@ -44,7 +46,43 @@ struct EvictArgs {
   int32_t* status;
   long long cap;
   int R, max_pages, num_pages, recent, sinks, cluster, chunk;
+  int apart;                     // a second launch makes the moves
 };
+
+// One of the 9 threads that move a key: its row, and with part 0 its weight and position.
+struct Move {
+  int from, to, page_from, page_to;
+};
+__device__ __forceinline__ Move read_move(const EvictArgs& a, int r, long long m) {
+  const int2 mv = reinterpret_cast<const int2*>(a.moves + (size_t)r * a.cap * 2)[m];
+  const int32_t* table = a.block_table + (size_t)r * a.max_pages;
+  return {mv.x, mv.y, table[mv.x / kPage], table[mv.y / kPage]};
+}
+__device__ __forceinline__ void make_move(const EvictArgs& a, int r, const Move& mv, int part) {
+  const bool ok = mv.page_from >= 0 && mv.page_from < a.num_pages && mv.page_to >= 0 && mv.page_to < a.num_pages;
+  if (ok) {
+    const uint4* src =
+        reinterpret_cast<const uint4*>(a.kv + ((size_t)mv.page_from * kPage + mv.from % kPage) * kDqk) + part;
+    uint4* dst = reinterpret_cast<uint4*>(a.kv + ((size_t)mv.page_to * kPage + mv.to % kPage) * kDqk) + part;
+    uint4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = src[u * kRowThreads];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) dst[u * kRowThreads] = v[u];
+  }
+  if (part == 0) {
+    if (!ok && a.status) atomicOr(a.status, MLA_FAULT_PAGE_RANGE);
+    const size_t row = (size_t)r * a.max_pages * kPage;
+    const float w = a.weights[row + mv.from];
+    a.weights_out[row + mv.to] = w;
+    a.weights_out[row + mv.from] = 0.f;
+    if (a.positions) {
+      const int32_t p = a.positions[row + mv.from];
+      a.positions_out[row + mv.to] = p;
+      a.positions_out[row + mv.from] = -1;
+    }
+  }
+}
 
 // A code that sorts as the weights do (-0 as 0, NaN lowest), below kHeld.
 __device__ __forceinline__ uint32_t weight_code(float w) {
@@ -60,9 +98,9 @@ __device__ __forceinline__ uint32_t ld_rank(const void* p, int rank) {
 }
 
 struct Shared {
-  uint32_t hist[3][kBins];
+  uint32_t hist[3][kBins];       // the first CTA's: of the cluster
   unsigned long long sums[kWarps];
-  uint32_t found, rest;          // the digit that holds the wanted place, places left in it
+  uint32_t found, rest, same;    // the digit that holds the wanted place, places left in it, its codes
   int top;                       // newest position of this CTA's keys
   uint32_t equal, holes, movers; // this CTA's counts
 };
@@ -112,13 +150,10 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictAr
   }
   grid_dep_wait();
   grid_dep_launch();
-  long long n_ = a.seq_lens[r];
-  if (n_ > (long long)a.max_pages * kPage) {
-    n_ = (long long)a.max_pages * kPage;
-    if (a.status && tid == 0 && rank == 0) atomicOr(a.status, MLA_FAULT_PAGE_RANGE);
-  }
-  const int n = (int)(n_ > 0 ? n_ : 0), keep = max(a.keep[r], 0);
-  const size_t row = (size_t)r * a.max_pages * kPage;
+  const int most = a.max_pages * kPage, given = a.seq_lens[r], keep = max(a.keep[r], 0);
+  const int n = min(max(given, 0), most);
+  if (given > most && a.status && tid == 0 && rank == 0) atomicOr(a.status, MLA_FAULT_PAGE_RANGE);
+  const size_t row = (size_t)r * most;
   const float* w = a.weights + row;
   const int32_t* p = a.positions ? a.positions + row : nullptr;
   float* wo = a.weights_out + row;
@@ -131,49 +166,61 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictAr
   const int run = (int)cdiv(len, kThreads) | 1;
   const int b0 = min(tid * run, len), b1 = min(b0 + run, len);
 
-  join(a.cluster);                               // every CTA of the cluster has read seq_lens
-  if (rank == 0 && tid == 0) a.lens_out[r] = min(n, keep);
   if (n <= keep) {                               // nothing to drop
+#pragma unroll 4
     for (int i = first + tid; i < first + len; i += kThreads) {
       if (copies_w) wo[i] = w[i];
       if (copies_p) po[i] = p[i];
     }
-    if (rank == 0 && tid == 0) a.count[r] = 0;
+    // seq_lens may be lens_out: what others of the cluster then read instead comes to the same.
+    if (rank == 0 && tid == 0) {
+      a.count[r] = 0;
+      a.lens_out[r] = n;
+    }
     return;
   }
 
+  const bool cached = len <= a.chunk;
   long long newest = LLONG_MAX;                  // positions from here on are held
+  join(a.cluster);                               // the histograms are cleared, in the first CTA too
   if (a.recent > 0) {
     int top = n - 1;
     if (p) {
       int mine = INT_MIN;
-      for (int i = first + tid; i < first + len; i += kThreads) mine = max(mine, p[i]);
+#pragma unroll 4
+      for (int i = tid; i < len; i += kThreads) {
+        const int pos = p[first + i];
+        if (cached) codes[i] = (uint32_t)pos;
+        mine = max(mine, pos);
+      }
       mine = __reduce_max_sync(0xffffffffu, mine);
       if ((tid & 31) == 0) atomicMax(&sh.top, mine);
       join(a.cluster);
       top = sh.top;
-      for (int c = 0; c < a.cluster && a.cluster > 1; ++c) top = max(top, (int)ld_rank(&sh.top, c));
+      if (a.cluster > 1) {
+        int other = INT_MIN;
+        if ((tid & 31) < a.cluster) other = (int)ld_rank(&sh.top, tid & 31);
+        top = __reduce_max_sync(0xffffffffu, other);
+      }
     }
     newest = (long long)top + 1 - a.recent;
   }
-  const bool cached = len <= a.chunk;
-  auto make = [&](int i) {                       // the code of this CTA's i-th slot
-    const int pos = p ? p[first + i] : first + i;
-    if (pos < a.sinks || pos >= newest) return kHeld;
-    return weight_code(w[first + i]);
+  auto make = [&](int i, int pos) {              // the code of this CTA's i-th slot
+    return pos < a.sinks || pos >= newest ? kHeld : weight_code(w[first + i]);
   };
-  auto code = [&](int i) { return cached ? codes[i] : make(i); };
+  auto code = [&](int i) { return cached ? codes[i] : make(i, p ? p[first + i] : first + i); };
 
   // The keep-th largest code, digit by digit, and how many of its equals stay.
-  uint32_t want = keep, found = 0;
+  uint32_t want = keep, found = 0, same = 0;
   if (keep > 0) {
 #pragma unroll
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+#pragma unroll 4
       for (int i = tid; i < len; i += kThreads) {
         uint32_t c;
         if (pass == 0) {
-          c = make(i);
+          c = make(i, !p ? first + i : cached && a.recent > 0 ? (int)codes[i] : p[first + i]);
           if (cached) codes[i] = c;
         } else {
           c = code(i);
@@ -181,91 +228,133 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictAr
         }
         atomicAdd(&sh.hist[pass][(c >> shift) & ((1 << bits) - 1)], 1u);
       }
-      join(a.cluster);
       // Digits from the largest down, two to a thread.
-      const int hi = kBins - 1 - 2 * tid;
-      uint32_t h[2];
+      const int hi = kBins - 2 - 2 * tid;        // and hi + 1
+      if (a.cluster > 1) {
+        __syncthreads();
+        if (rank > 0) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        h[u] = 0;
-        if (a.cluster == 1) h[u] = sh.hist[pass][hi - u];
-        else
-          for (int c = 0; c < a.cluster; ++c) h[u] += ld_rank(&sh.hist[pass][hi - u], c);
+          for (int u = 0; u < 2; ++u)
+            if (const uint32_t v = sh.hist[pass][hi + u])
+              asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(
+                               tc::map_rank(&sh.hist[pass][hi + u], 0)),
+                           "r"(v)
+                           : "memory");
+        }
+      }
+      join(a.cluster);
+      uint32_t h0, h1;
+      if (a.cluster > 1) {
+        asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(h1), "=r"(h0)
+                     : "r"(tc::map_rank(&sh.hist[pass][hi], 0)) : "memory");
+      } else {
+        h1 = sh.hist[pass][hi];
+        h0 = sh.hist[pass][hi + 1];
       }
       unsigned long long total;
-      const uint32_t above = (uint32_t)scan(h[0] + h[1], sh.sums, total);
-      if (above < want && want <= above + h[0] + h[1]) {
-        const bool second = above + h[0] < want;
-        sh.found = hi - (second ? 1 : 0);
-        sh.rest = want - above - (second ? h[0] : 0);
+      const uint32_t above = (uint32_t)scan(h0 + h1, sh.sums, total);
+      if (above < want && want <= above + h0 + h1) {
+        const bool second = above + h0 < want;
+        sh.found = hi + (second ? 0 : 1);
+        sh.rest = want - above - (second ? h0 : 0);
+        sh.same = second ? h1 : h0;
       }
       __syncthreads();
       found |= sh.found << shift;
       want = sh.rest;
+      same = sh.same;
       __syncthreads();
     }
   } else {
     found = kHeld;                               // no code is larger, and no equal stays
   }
 
-  // Equals stay in the order of their slots.
-  uint32_t equal = 0;
-  for (int i = b0; i < b1; ++i) equal += (keep > 0 ? code(i) : make(i)) == found;
+  // Equals stay in the order of their slots; mostly all do.
   unsigned long long total;
-  uint32_t eq = (uint32_t)scan(equal, sh.sums, total);
-  if (tid == 0) sh.equal = (uint32_t)total;
-  join(a.cluster);
-  for (int c = 0; c < rank; ++c) eq += ld_rank(&sh.equal, c);
+  uint32_t eq = 0;
+  if (same != want) {
+    uint32_t equal = 0;
+    for (int i = b0; i < b1; ++i) equal += code(i) == found;
+    eq = (uint32_t)scan(equal, sh.sums, total);
+    if (tid == 0) sh.equal = (uint32_t)total;
+    join(a.cluster);
+    for (int c = 0; c < rank; ++c) eq += ld_rank(&sh.equal, c);
+  }
   // A dropped key's slot before `keep` is a hole; a kept key behind it moves.
-  uint32_t holes = 0, movers = 0, e = eq;
-  for (int i = b0; i < b1; ++i) {
-    const uint32_t c = keep > 0 ? code(i) : make(i);
-    const bool stays = c > found || (c == found && e++ < want);
+  auto walk = [&](auto&& each_slot) {
+    uint32_t e = eq;
+    for (int i = b0; i < b1; ++i) {
+      const uint32_t c = keep > 0 ? code(i) : 0u;
+      each_slot(i, c > found || (c == found && e++ < want));
+    }
+  };
+  uint32_t holes = 0, movers = 0;
+  walk([&](int i, bool stays) {
     if (first + i < keep) holes += !stays;
     else movers += stays;
-  }
+  });
   const unsigned long long at = scan((unsigned long long)holes << 32 | movers, sh.sums, total);
-  if (tid == 0) {
-    sh.holes = (uint32_t)(total >> 32);
-    sh.movers = (uint32_t)total;
-  }
-  join(a.cluster);
   uint32_t hole = (uint32_t)(at >> 32), mover = (uint32_t)at, all = (uint32_t)total;
   if (a.cluster > 1) {
-    all = 0;
-    for (int c = 0; c < a.cluster; ++c) {
-      const uint32_t m = ld_rank(&sh.movers, c);
-      all += m;
-      if (c < rank) {
-        mover += m;
-        hole += ld_rank(&sh.holes, c);
-      }
+    if (tid == 0) {
+      sh.holes = (uint32_t)(total >> 32);
+      sh.movers = (uint32_t)total;
     }
+    tc::cluster_sync();
+    uint32_t m = 0, h = 0;                       // lane c: CTA c's
+    if ((tid & 31) < a.cluster) {
+      m = ld_rank(&sh.movers, tid & 31);
+      h = ld_rank(&sh.holes, tid & 31);
+    }
+    all = __reduce_add_sync(0xffffffffu, m);
+    mover += __reduce_add_sync(0xffffffffu, (tid & 31) < rank ? m : 0u);
+    hole += __reduce_add_sync(0xffffffffu, (tid & 31) < rank ? h : 0u);
   }
-  int32_t* list = a.moves + (size_t)r * a.cap * 2;
-  for (int i = b0; i < b1; ++i) {
-    const uint32_t c = keep > 0 ? code(i) : make(i);
-    const bool stays = c > found || (c == found && eq++ < want);
-    const int slot = first + i;
-    if (slot < keep) {
-      if (!stays) list[2 * (size_t)hole++ + 1] = slot;
-      else {
-        if (copies_w) wo[slot] = w[slot];
-        if (copies_p) po[slot] = p[slot];
-      }
-    } else if (stays) {
-      list[2 * (size_t)mover++] = slot;
-    } else {
+  auto settle = [&](int slot, bool stays) {      // the books of a key that does not move
+    if (stays) {
+      if (slot >= keep) return;
+      if (copies_w) wo[slot] = w[slot];
+      if (copies_p) po[slot] = p[slot];
+    } else if (slot >= keep) {
       wo[slot] = 0.f;
       if (p) po[slot] = -1;
     }
+  };
+  int32_t* list = a.moves + (size_t)r * a.cap * 2;
+  walk([&](int i, bool stays) {
+    const int slot = first + i;
+    if (slot < keep && !stays) list[2 * (size_t)hole++ + 1] = slot;
+    if (slot >= keep && stays) list[2 * (size_t)mover++] = slot;
+    if (cached) codes[i] = stays;
+    else settle(slot, stays);
+  });
+  __syncthreads();
+  if (cached)
+#pragma unroll 4
+    for (int i = tid; i < len; i += kThreads) settle(first + i, codes[i] != 0);
+  if (rank == 0 && tid == 0) {
+    a.count[r] = (int)all;
+    a.lens_out[r] = keep;
   }
-  if (rank == 0 && tid == 0) a.count[r] = (int)all;
-  if (a.cluster > 1) tc::cluster_sync();         // no CTA leaves while others read its counts
+  if (a.cluster > 1) tc::cluster_sync();         // the lists are whole; no CTA reads others' any more
+  if (a.apart) return;
+  const int group = tid / kRowThreads, part = tid % kRowThreads;
+  const uint32_t groups = kThreads / kRowThreads * a.cluster;
+  uint32_t m = rank * (kThreads / kRowThreads) + group;
+  if (group >= kThreads / kRowThreads || m >= all) return;
+  Move mv = read_move(a, r, m);
+  while (true) {
+    const bool more = m + groups < all;
+    Move next = mv;
+    if (more) next = read_move(a, r, m += groups);
+    make_move(a, r, mv, part);
+    if (!more) break;
+    mv = next;
+  }
 }
 
-// The listed rows with their weights and positions: 9 threads a row, 64 bytes each.
-constexpr int kRowThreads = kDqk / 64, kRows = 28, kMoveThreads = 256;
+// The listed moves of all requests on all SMs.
+constexpr int kRows = 28, kMoveThreads = 256;
 
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
   __shared__ long long before[kMaxR + 1];
@@ -301,33 +390,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
       if (before[mid] <= m) lo = mid;
       else hi = mid;
     }
-    const int2 mv = reinterpret_cast<const int2*>(a.moves + (size_t)lo * a.cap * 2)[m - before[lo]];
-    const int32_t* table = a.block_table + (size_t)lo * a.max_pages;
-    const int pf = table[mv.x / kPage], pt = table[mv.y / kPage];
-    const bool ok = pf >= 0 && pf < a.num_pages && pt >= 0 && pt < a.num_pages;
-    if (ok) {
-      const uint4* src = reinterpret_cast<const uint4*>(
-          a.kv + ((size_t)pf * kPage + mv.x % kPage) * kDqk) + part;
-      uint4* dst = reinterpret_cast<uint4*>(
-          a.kv + ((size_t)pt * kPage + mv.y % kPage) * kDqk) + part;
-      uint4 v[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) v[u] = src[u * kRowThreads];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) dst[u * kRowThreads] = v[u];
-    }
-    if (part == 0) {
-      if (!ok && a.status) atomicOr(a.status, MLA_FAULT_PAGE_RANGE);
-      const size_t row = (size_t)lo * a.max_pages * kPage;
-      const float w = a.weights[row + mv.x];
-      a.weights_out[row + mv.y] = w;
-      a.weights_out[row + mv.x] = 0.f;
-      if (a.positions) {
-        const int32_t p = a.positions[row + mv.x];
-        a.positions_out[row + mv.y] = p;
-        a.positions_out[row + mv.x] = -1;
-      }
-    }
+    make_move(a, lo, read_move(a, lo, m - before[lo]), part);
   }
 }
 
@@ -429,8 +492,12 @@ extern "C" int32_t mla_kv_evict(const mla_cache_shape* s, void* kv, const int32_
   attr[1].val.clusterDim.x = (unsigned)a.cluster;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+  // The clusters make the moves themselves where they are a third of the SMs or more, or the
+  // requests are short.
+  a.apart = (long long)s->R * a.cluster * 3 < sms && slots > 2048ll * a.cluster;
   if (cudaLaunchKernelEx(&cfg, evict_select_kernel, a) != cudaSuccess) return MLA_ERR_CUDA;
+  if (!a.apart) return MLA_OK;
   // At most half of a request's keys move.
   const long long most = (long long)s->R * a.cap;
   const long long grid = cdiv(most, kRows);
