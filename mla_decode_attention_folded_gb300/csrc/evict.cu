@@ -91,18 +91,16 @@ __device__ __forceinline__ uint32_t weight_code(float w) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-__device__ __forceinline__ uint32_t ld_rank(const void* p, int rank) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(tc::map_rank(p, rank)) : "memory");
-  return v;
+__device__ __forceinline__ void st_rank(void* p, int rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(tc::map_rank(p, rank)), "r"(v) : "memory");
 }
 
 struct Shared {
   uint32_t hist[3][kBins];       // the first CTA's: of the cluster
   unsigned long long sums[kWarps];
-  uint32_t found, rest, same;    // the digit that holds the wanted place, places left in it, its codes
+  uint32_t digit[3];             // what holds the wanted place, the places left in it, its codes
   int top;                       // newest position of this CTA's keys
-  uint32_t equal, holes, movers; // this CTA's counts
+  uint32_t told[3][kMaxCluster]; // what the cluster's CTAs tell all: newest positions or equals, holes, movers
 };
 
 __device__ __forceinline__ void join(int cluster) {
@@ -110,6 +108,10 @@ __device__ __forceinline__ void join(int cluster) {
   else __syncthreads();
 }
 
+// A value of each of the cluster's CTAs, told to all: thread c tells CTA c. The join is the caller's.
+__device__ __forceinline__ void tell(Shared& sh, int what, int rank, int cluster, uint32_t v) {
+  if ((int)threadIdx.x < cluster) st_rank(&sh.told[what][rank], threadIdx.x, v);
+}
 // Exclusive sum over the block's threads; `total` gets the whole.
 __device__ __forceinline__ unsigned long long scan(unsigned long long v, unsigned long long* sums,
                                                    unsigned long long& total) {
@@ -146,7 +148,6 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictAr
   for (int i = tid; i < 3 * kBins; i += kThreads) sh.hist[i / kBins][i % kBins] = 0;
   if (tid == 0) {
     sh.top = INT_MIN;
-    sh.equal = sh.holes = sh.movers = 0;
   }
   grid_dep_wait();
   grid_dep_launch();
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictAr
     int top = n - 1;
     if (p) {
       int mine = INT_MIN;
-#pragma unroll 4
+#pragma unroll 8
       for (int i = tid; i < len; i += kThreads) {
         const int pos = p[first + i];
         if (cached) codes[i] = (uint32_t)pos;
@@ -195,12 +196,12 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictAr
       }
       mine = __reduce_max_sync(0xffffffffu, mine);
       if ((tid & 31) == 0) atomicMax(&sh.top, mine);
-      join(a.cluster);
+      __syncthreads();
       top = sh.top;
       if (a.cluster > 1) {
-        int other = INT_MIN;
-        if ((tid & 31) < a.cluster) other = (int)ld_rank(&sh.top, tid & 31);
-        top = __reduce_max_sync(0xffffffffu, other);
+        tell(sh, 0, rank, a.cluster, (uint32_t)top);
+        tc::cluster_sync();
+        for (int c = 0; c < a.cluster; ++c) top = max(top, (int)sh.told[0][c]);
       }
     }
     newest = (long long)top + 1 - a.recent;
@@ -216,20 +217,39 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictAr
 #pragma unroll
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-#pragma unroll 4
-      for (int i = tid; i < len; i += kThreads) {
-        uint32_t c;
-        if (pass == 0) {
-          c = make(i, !p ? first + i : cached && a.recent > 0 ? (int)codes[i] : p[first + i]);
-          if (cached) codes[i] = c;
-        } else {
-          c = code(i);
-          if (c >> (shift + bits) != found >> (shift + bits)) continue;
+      if (pass == 0) {
+        // Four slots' loads at a time.
+        const bool have = cached && p && a.recent > 0;
+        for (int i0 = tid; i0 < len; i0 += 4 * kThreads) {
+          float x[4];
+          int pos[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * kThreads;
+            if (i < len) {
+              x[u] = w[first + i];
+              pos[u] = !p ? first + i : have ? (int)codes[i] : p[first + i];
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * kThreads;
+            if (i < len) {
+              const uint32_t c = pos[u] < a.sinks || pos[u] >= newest ? kHeld : weight_code(x[u]);
+              if (cached) codes[i] = c;
+              atomicAdd(&sh.hist[0][c >> 21], 1u);
+            }
+          }
         }
-        atomicAdd(&sh.hist[pass][(c >> shift) & ((1 << bits) - 1)], 1u);
+      } else {
+#pragma unroll 4
+        for (int i = tid; i < len; i += kThreads) {
+          const uint32_t c = code(i);
+          if (c >> (shift + bits) == found >> (shift + bits))
+            atomicAdd(&sh.hist[pass][(c >> shift) & ((1 << bits) - 1)], 1u);
+        }
       }
-      // Digits from the largest down, two to a thread.
-      const int hi = kBins - 2 - 2 * tid;        // and hi + 1
+      const int hi = kBins - 2 - 2 * tid;        // this thread's two digits: this and the next
       if (a.cluster > 1) {
         __syncthreads();
         if (rank > 0) {
@@ -243,27 +263,27 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictAr
         }
       }
       join(a.cluster);
-      uint32_t h0, h1;
-      if (a.cluster > 1) {
-        asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(h1), "=r"(h0)
-                     : "r"(tc::map_rank(&sh.hist[pass][hi], 0)) : "memory");
-      } else {
-        h1 = sh.hist[pass][hi];
-        h0 = sh.hist[pass][hi + 1];
+      // Digits from the largest down; the first CTA finds the one and tells the others.
+      if (rank == 0) {
+        const uint32_t h0 = sh.hist[pass][hi + 1], h1 = sh.hist[pass][hi];
+        unsigned long long total;
+        const uint32_t above = (uint32_t)scan(h0 + h1, sh.sums, total);
+        if (above < want && want <= above + h0 + h1) {
+          const bool second = above + h0 < want;
+          const uint32_t at[3] = {(uint32_t)(hi + (second ? 0 : 1)), want - above - (second ? h0 : 0),
+                                  second ? h1 : h0};
+#pragma unroll
+          for (int u = 0; u < 3; ++u) {
+            sh.digit[u] = at[u];
+            for (int c = 1; c < a.cluster; ++c) st_rank(&sh.digit[u], c, at[u]);
+          }
+        }
       }
-      unsigned long long total;
-      const uint32_t above = (uint32_t)scan(h0 + h1, sh.sums, total);
-      if (above < want && want <= above + h0 + h1) {
-        const bool second = above + h0 < want;
-        sh.found = hi + (second ? 0 : 1);
-        sh.rest = want - above - (second ? h0 : 0);
-        sh.same = second ? h1 : h0;
-      }
-      __syncthreads();
-      found |= sh.found << shift;
-      want = sh.rest;
-      same = sh.same;
-      __syncthreads();
+      join(a.cluster);
+      found |= sh.digit[0] << shift;
+      want = sh.digit[1];
+      same = sh.digit[2];
+      // (The next digit is told after the next join.)
     }
   } else {
     found = kHeld;                               // no code is larger, and no equal stays
@@ -276,9 +296,11 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictAr
     uint32_t equal = 0;
     for (int i = b0; i < b1; ++i) equal += code(i) == found;
     eq = (uint32_t)scan(equal, sh.sums, total);
-    if (tid == 0) sh.equal = (uint32_t)total;
-    join(a.cluster);
-    for (int c = 0; c < rank; ++c) eq += ld_rank(&sh.equal, c);
+    if (a.cluster > 1) {
+      tell(sh, 0, rank, a.cluster, (uint32_t)total);
+      tc::cluster_sync();
+      for (int c = 0; c < rank; ++c) eq += sh.told[0][c];
+    }
   }
   // A dropped key's slot before `keep` is a hole; a kept key behind it moves.
   auto walk = [&](auto&& each_slot) {
@@ -296,19 +318,17 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictAr
   const unsigned long long at = scan((unsigned long long)holes << 32 | movers, sh.sums, total);
   uint32_t hole = (uint32_t)(at >> 32), mover = (uint32_t)at, all = (uint32_t)total;
   if (a.cluster > 1) {
-    if (tid == 0) {
-      sh.holes = (uint32_t)(total >> 32);
-      sh.movers = (uint32_t)total;
-    }
+    tell(sh, 1, rank, a.cluster, (uint32_t)(total >> 32));
+    tell(sh, 2, rank, a.cluster, (uint32_t)total);
     tc::cluster_sync();
-    uint32_t m = 0, h = 0;                       // lane c: CTA c's
-    if ((tid & 31) < a.cluster) {
-      m = ld_rank(&sh.movers, tid & 31);
-      h = ld_rank(&sh.holes, tid & 31);
+    all = 0;
+    for (int c = 0; c < a.cluster; ++c) {
+      if (c < rank) {
+        hole += sh.told[1][c];
+        mover += sh.told[2][c];
+      }
+      all += sh.told[2][c];
     }
-    all = __reduce_add_sync(0xffffffffu, m);
-    mover += __reduce_add_sync(0xffffffffu, (tid & 31) < rank ? m : 0u);
-    hole += __reduce_add_sync(0xffffffffu, (tid & 31) < rank ? h : 0u);
   }
   auto settle = [&](int slot, bool stays) {      // the books of a key that does not move
     if (stays) {
@@ -330,8 +350,29 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictAr
   });
   __syncthreads();
   if (cached)
-#pragma unroll 4
-    for (int i = tid; i < len; i += kThreads) settle(first + i, codes[i] != 0);
+    for (int i0 = tid; i0 < len; i0 += 4 * kThreads) {   // as settle(), four slots' loads at a time
+      float x[4];
+      int pos[4];
+      bool copies[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * kThreads;
+        copies[u] = i < len && codes[i] && first + i < keep;
+        if (copies[u] && copies_w) x[u] = w[first + i];
+        if (copies[u] && copies_p) pos[u] = p[first + i];
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * kThreads, slot = first + i;
+        if (copies[u]) {
+          if (copies_w) wo[slot] = x[u];
+          if (copies_p) po[slot] = pos[u];
+        } else if (i < len && !codes[i] && slot >= keep) {
+          wo[slot] = 0.f;
+          if (p) po[slot] = -1;
+        }
+      }
+    }
   if (rank == 0 && tid == 0) {
     a.count[r] = (int)all;
     a.lens_out[r] = keep;
@@ -342,13 +383,17 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictAr
   const uint32_t groups = kThreads / kRowThreads * a.cluster;
   uint32_t m = rank * (kThreads / kRowThreads) + group;
   if (group >= kThreads / kRowThreads || m >= all) return;
-  Move mv = read_move(a, r, m);
-  while (true) {
-    const bool more = m + groups < all;
-    Move next = mv;
-    if (more) next = read_move(a, r, m += groups);
+  // Three moves at a time: one's row, the next one's pages, the list entry of the one after.
+  const int2* entry = reinterpret_cast<const int2*>(list);
+  const int32_t* table = a.block_table + (size_t)r * a.max_pages;
+  auto pages = [&](int2 mv) { return Move{mv.x, mv.y, table[mv.x / kPage], table[mv.y / kPage]}; };
+  Move mv = pages(entry[m]);
+  int2 after = m + groups < all ? entry[m + groups] : make_int2(0, 0);
+  for (; m < all; m += groups) {
+    const uint32_t m1 = m + groups, m2 = m1 + groups;
+    const Move next = m1 < all ? pages(after) : mv;
+    if (m2 < all) after = entry[m2];
     make_move(a, r, mv, part);
-    if (!more) break;
     mv = next;
   }
 }
