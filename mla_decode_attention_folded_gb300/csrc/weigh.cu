@@ -69,7 +69,10 @@ struct WeighArgs {
 
 __device__ __forceinline__ bool wg_wait(uint64_t* bar, uint32_t parity, WeighCtl* ctl,
                                         const WeighArgs& a) {
-  if (tc::mbar_try_wait(bar, parity)) return true;
+  // Reading the timer takes longer than most waits: not before the barrier was tried for a while.
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (tc::mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = tc::globaltimer_ns();
   while (true) {
     if (tc::mbar_try_wait(bar, parity)) return true;
@@ -80,6 +83,12 @@ __device__ __forceinline__ bool wg_wait(uint64_t* bar, uint32_t parity, WeighCtl
       return false;
     }
   }
+}
+// One lane of a whole warp, always the same.
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
 }
 // The keys of request r that are weighed.
 __device__ __forceinline__ int weigh_len(const WeighArgs& a, int r) {
@@ -123,7 +132,7 @@ weigh_kernel(const WeighArgs a, const __grid_constant__ CUtensorMap tm_kv,
     tc::mbar_init(&ctl->q_empty, 1);
     for (int i = 0; i < kBufs; ++i) {
       tc::mbar_init(&ctl->s_full[i], 1);
-      tc::mbar_init(&ctl->s_empty[i], kSum);
+      tc::mbar_init(&ctl->s_empty[i], kSum / 32);
     }
     tc::mbar_init(&ctl->drain, 1);
     ctl->abort_flag = 0;
@@ -247,35 +256,46 @@ weigh_kernel(const WeighArgs a, const __grid_constant__ CUtensorMap tm_kv,
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      bool ok = true;
-      uint32_t g = 0, x = 0;
-      const uint32_t idesc = tc::idesc_e4m3_f32(kTile, a.rows, false, false);
-      const uint32_t q = tc::smem_u32(smem + kOffQ);
-      while (ok && w.next(a)) {
-        for (int b = 0; ok && b < a.blocks; ++b, ++x) {
-          if (!(ok = wg_wait(&ctl->q_full, x & 1, ctl, a))) break;
-          for (int t = 0; t < w.tiles; ++t, ++g) {
-            const int st = g % kStages, bf = g % kBufs;
-            if (!(ok = wg_wait(&ctl->kv_full[st], (g / kStages) & 1, ctl, a))) break;
-            if (g >= kBufs && !(ok = wg_wait(&ctl->s_empty[bf], (g / kBufs - 1) & 1, ctl, a))) break;
-            tc::fence_after_sync();
-            const uint32_t s = tc::smem_u32(smem + st * kStageBytes), d = tmem + bf * kMaxRows;
+    // The whole warp waits, so that what the MMAs are given stays in uniform registers; one lane
+    // issues.
+    const bool one = elect();
+    bool ok = true;
+    uint32_t g = 0, x = 0;
+    const uint32_t idesc = tc::idesc_e4m3_f32(kTile, a.rows, false, false);
+    const uint64_t q = tc::smem_desc(tc::smem_u32(smem + kOffQ), 16, 1024, tc::kSw128);
+    const uint64_t qr = tc::smem_desc(tc::smem_u32(smem + kOffQ) + 4 * qchunk, 16, 512, tc::kSw64);
+    const uint32_t s0 = tc::smem_u32(smem);
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = wg_wait(bar, parity, ctl, a); };
+    while (ok && w.next(a)) {
+      for (int b = 0; ok && b < a.blocks; ++b, ++x) {
+        if (!wait(&ctl->q_full, x & 1)) break;
+        for (int t = 0; t < w.tiles; ++t, ++g) {
+          const int st = g % kStages, bf = g % kBufs;
+          if (!wait(&ctl->kv_full[st], (g / kStages) & 1)) break;
+          if (g >= kBufs && !wait(&ctl->s_empty[bf], (g / kBufs - 1) & 1)) break;
+          tc::fence_after_sync();
+          const uint64_t k = tc::smem_desc(s0 + st * kStageBytes, 16, 1024, tc::kSw128);
+          const uint64_t kr = tc::smem_desc(s0 + st * kStageBytes + 4 * kChunk, 16, 512, tc::kSw64);
+          const uint32_t d = tmem + bf * kMaxRows;
+          if (one) {
 #pragma unroll
-            for (int kk = 0; kk < 16; ++kk)
-              tc::mma_e4m3(d, tc::smem_desc(s + (kk >> 2) * kChunk + (kk & 3) * 32, 16, 1024, tc::kSw128),
-                           tc::smem_desc(q + (kk >> 2) * qchunk + (kk & 3) * 32, 16, 1024, tc::kSw128),
-                           idesc, kk != 0);
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                tc::mma_e4m3(d, k + ((c * kChunk + kk * 32) >> 4), q + ((c * qchunk + kk * 32) >> 4), idesc,
+                             c + kk != 0);
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
-              tc::mma_e4m3(d, tc::smem_desc(s + 4 * kChunk + kk * 32, 16, 512, tc::kSw64),
-                           tc::smem_desc(q + 4 * qchunk + kk * 32, 16, 512, tc::kSw64), idesc, true);
+              tc::mma_e4m3(d, kr + (kk * 32 >> 4), qr + (kk * 32 >> 4), idesc, true);
+            tc::mma_commit(&ctl->s_full[bf]);
             tc::mma_commit(&ctl->kv_empty[st]);
             if (t == w.tiles - 1) tc::mma_commit(&ctl->q_empty);
-            tc::mma_commit(&ctl->s_full[bf]);
           }
         }
       }
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (one) {
       tc::mma_commit(&ctl->drain);               // every MMA done before TMEM is released
       const unsigned long long t0 = tc::globaltimer_ns();
       while (!tc::mbar_try_wait(&ctl->drain, 0) && tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
@@ -314,17 +334,25 @@ weigh_kernel(const WeighArgs a, const __grid_constant__ CUtensorMap tm_kv,
           tc::fence_after_sync();
           const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + bf * kMaxRows + half * cols;
           uint64_t acc[2] = {0, 0};
-          for (int c = 0; c < cols; c += 16) {
-            uint32_t raw[16];
-            tc::tmem_ld16(src + c, raw);
-            tc::tmem_wait_ld();
+          // The half's columns in one go (16, 32, 48 or 64 of them), then read no more.
+          uint32_t raw[4][16];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (16 * c < cols) tc::tmem_ld16(src + 16 * c, raw[c]);
+          tc::tmem_wait_ld();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&ctl->s_empty[bf]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (16 * c >= cols) break;
 #pragma unroll
             for (int i = 0; i < 16; i += 4) {
-              const float4 n4 = *reinterpret_cast<const float4*>(ng + c + i);
+              const float4 n4 = *reinterpret_cast<const float4*>(ng + 16 * c + i);
               float e[4];
-              unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(raw[i]), __uint_as_float(raw[i + 1])), c2,
+              unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(raw[c][i]), __uint_as_float(raw[c][i + 1])), c2,
                                      pack_f32x2(n4.x, n4.y)), e[0], e[1]);
-              unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(raw[i + 2]), __uint_as_float(raw[i + 3])),
+              unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(raw[c][i + 2]), __uint_as_float(raw[c][i + 3])),
                                      c2, pack_f32x2(n4.z, n4.w)), e[2], e[3]);
               // fmaxf: a score that is NaN adds 0.
 #pragma unroll
@@ -333,8 +361,6 @@ weigh_kernel(const WeighArgs a, const __grid_constant__ CUtensorMap tm_kv,
               acc[1] = add_f32x2(acc[1], pack_f32x2(e[2], e[3]));
             }
           }
-          tc::fence_before_sync();
-          tc::mbar_arrive(&ctl->s_empty[bf]);
           float s0, s1;
           unpack_f32x2(add_f32x2(acc[0], acc[1]), s0, s1);
           float* at = sums + (t * 2 + half) * kTile + key;
