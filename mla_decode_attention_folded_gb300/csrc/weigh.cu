@@ -32,7 +32,7 @@ constexpr int kMine = 128;                       // rows in a CTA's shared memor
 constexpr int kStages = 2;                       // tiles in flight
 constexpr int kChunk = kTile * 128, kStageBytes = kTile * kDqk;
 constexpr int kOffQ = kStages * kStageBytes;
-constexpr int kOffSums = kOffQ + kMine * kDqk;
+constexpr int kMostRun = 16;                     // ... at most: their page ids are a lane's each
 constexpr int kSum = 256;                        // summing threads: two per key
 constexpr int kThreads = 64 + kSum;
 constexpr uint32_t kTmemCols = 512;
@@ -43,7 +43,7 @@ struct Cfg {
   static constexpr int kCtas = PAIR ? 2 : 1;
   static constexpr int kMaxRows = kCtas * kMine;     // rows of a block: the MMA's N
   static constexpr int kBufs = kTmemCols / kMaxRows; // score buffers in TMEM
-  static constexpr int kRun = PAIR ? 6 : 8;          // tiles that a row block goes over
+  static constexpr int kRun = PAIR ? 6 : 8;          // tiles that a row block goes over, at least
 };
 // MMAs wait on the first CTA's barriers of a pair, and arrive on both CTAs'.
 struct WeighCtl {
@@ -56,8 +56,10 @@ struct WeighCtl {
   int first_r, first_tile;                       // where this unit's run begins
   long long total;                               // tiles of the batch
 };
+// Behind the tiles: the queries, then the sums of a group's tiles (what the queries leave of
+// their place is the sums'), -lse of a block's rows in two buffers, the barriers.
 template <bool PAIR>
-constexpr int off_neg() { return kOffSums + Cfg<PAIR>::kRun * 2 * kTile * 4; }
+constexpr int off_neg() { return kOffQ + kMine * kDqk + Cfg<PAIR>::kRun * 2 * kTile * 4; }
 template <bool PAIR>
 constexpr int off_ctl() { return off_neg<PAIR>() + 2 * Cfg<PAIR>::kMaxRows * 4; }
 template <bool PAIR>
@@ -76,6 +78,7 @@ struct WeighArgs {
   float scale_log2, decay;
   int R, M, max_pages, num_pages;
   int rows, blocks;              // rows per block, blocks per request
+  int run;                       // tiles of a group, at most
   unsigned long long wait_limit_ns;
   int withhold;                  // failure-detection test: CTA 0 never loads its first tile
 };
@@ -108,24 +111,35 @@ __device__ __forceinline__ int weigh_len(const WeighArgs& a, int r) {
   const long long n = a.starts[r] < 0 ? 0 : a.seq_lens[r], most = (long long)a.max_pages * kPage;
   return (int)(n < 0 ? 0 : n < most ? n : most);
 }
-// A unit's tiles (of KEYS keys) as groups: up to RUN tiles of one request.
-template <int KEYS, int RUN>
+// A unit's tiles (of KEYS keys) as groups: up to a.run tiles of one request. The row blocks go
+// over a group's tiles in turn, forwards and backwards, so that the last block of a group is
+// the first of the next and its queries stay.
+template <int KEYS>
 struct Walk {
   int r, tile, tiles, len;       // request, its next tile, tiles of the group, its keys
   long long left;                // tiles of the unit's run from here on
+  bool before, after, back;      // the request has a group before, after; blocks go backwards
   __device__ __forceinline__ bool next(const WeighArgs& a) {
     tile += tiles;
     left -= tiles;
     if (left <= 0) return false;
+    before = tiles > 0;
+    back = before && !back;
     while (tile >= (int)cdiv(len, KEYS)) {
       tile = 0;
+      before = back = false;
       if (++r >= a.R) return false;
       len = weigh_len(a, r);
     }
     const long long rest = cdiv(len, KEYS) - tile;
-    tiles = (int)min(min(rest, left), (long long)RUN);
+    tiles = (int)min(min(rest, left), (long long)a.run);
+    after = tiles < rest && tiles < left;
     return true;
   }
+  __device__ __forceinline__ int block(const WeighArgs& a, int i) const { return back ? a.blocks - 1 - i : i; }
+  // Whether the i-th block's queries are there already, and whether they stay.
+  __device__ __forceinline__ bool has_q(int i) const { return i == 0 && before; }
+  __device__ __forceinline__ bool keeps_q(const WeighArgs& a, int i) const { return i == a.blocks - 1 && after; }
 };
 
 template <bool PAIR>
@@ -211,10 +225,11 @@ weigh_kernel(const WeighArgs a, const __grid_constant__ CUtensorMap tm_kv,
   else __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = ctl->tmem_base;
-  Walk<kKeys, C::kRun> w;
+  Walk<kKeys> w;
   w.r = ctl->first_r;
   w.tile = ctl->first_tile;
   w.tiles = 0;
+  w.back = false;
   w.left = cdiv(ctl->total * (unit + 1), units) - cdiv(ctl->total * unit, units);
   w.len = w.r < a.R ? weigh_len(a, w.r) : 0;
   const int held = a.rows / C::kCtas, qchunk = held * 128;   // rows in this CTA's shared memory
@@ -249,14 +264,17 @@ weigh_kernel(const WeighArgs a, const __grid_constant__ CUtensorMap tm_kv,
           id = a.num_pages;
         }
       }
-      for (int b = 0; ok && b < a.blocks; ++b, ++x) {
-        if (x > 0 && !(ok = wait0(&ctl->q_empty, (x - 1) & 1))) break;
-        if (lane == 0) {
-          uint8_t* q = smem + kOffQ;
-          const int row = w.r * a.M + b * a.rows + rank * held;
-          expect(&ctl->q_full, held * kDqk);
-          for (int c = 0; c < 4; ++c) load(q + c * qchunk, &tm_q, &ctl->q_full, c * 128, row);
-          load(q + 4 * qchunk, &tm_qr, &ctl->q_full, kDv, row);
+      for (int i = 0; ok && i < a.blocks; ++i) {
+        if (!w.has_q(i)) {
+          if (x > 0 && !(ok = wait0(&ctl->q_empty, (x - 1) & 1))) break;
+          if (lane == 0) {
+            uint8_t* q = smem + kOffQ;
+            const int row = w.r * a.M + w.block(a, i) * a.rows + rank * held;
+            expect(&ctl->q_full, held * kDqk);
+            for (int c = 0; c < 4; ++c) load(q + c * qchunk, &tm_q, &ctl->q_full, c * 128, row);
+            load(q + 4 * qchunk, &tm_qr, &ctl->q_full, kDv, row);
+          }
+          ++x;
         }
         for (int t = 0; t < w.tiles; ++t, ++g) {
           const int st = g % kStages;
@@ -310,8 +328,8 @@ weigh_kernel(const WeighArgs a, const __grid_constant__ CUtensorMap tm_kv,
       else tc::mma_commit(bar);
     };
     while (ok && w.next(a)) {
-      for (int b = 0; ok && b < a.blocks; ++b, ++x) {
-        if (!wait(&ctl->q_full, x & 1)) break;
+      for (int i = 0; ok && i < a.blocks; ++i) {
+        if (!w.has_q(i) && !wait(&ctl->q_full, x++ & 1)) break;
         for (int t = 0; t < w.tiles; ++t, ++g) {
           const int st = g % kStages, bf = g % C::kBufs;
           if (!wait(&ctl->kv_full[st], (g / kStages) & 1)) break;
@@ -330,7 +348,7 @@ weigh_kernel(const WeighArgs a, const __grid_constant__ CUtensorMap tm_kv,
             for (int kk = 0; kk < 2; ++kk) mma(d, kr + (kk * 32 >> 4), qr + (kk * 32 >> 4), true);
             commit(&ctl->s_full[bf]);
             commit(&ctl->kv_empty[st]);
-            if (t == w.tiles - 1) commit(&ctl->q_empty);
+            if (t == w.tiles - 1 && !w.keeps_q(a, i)) commit(&ctl->q_empty);
           }
         }
       }
@@ -349,8 +367,8 @@ weigh_kernel(const WeighArgs a, const __grid_constant__ CUtensorMap tm_kv,
     // the group's barriers; they write nothing more.
     const int quarter = warp & 3, half = (warp - 2) >> 2, st = tid - 64;
     const int key = quarter * 32 + lane, cols = a.rows / 2;
-    float* sums = reinterpret_cast<float*>(smem + kOffSums);           // [tile][half][key]
     float* neg = reinterpret_cast<float*>(smem + off_neg<PAIR>());     // [x & 1][row]
+    float* sums = neg - a.run * 2 * kTile;                             // [tile][half][key]
     const uint64_t c2 = pack_f32x2(a.scale_log2, a.scale_log2);
     uint32_t g = 0, x = 0;
     bool ok = true;
@@ -363,9 +381,9 @@ weigh_kernel(const WeighArgs a, const __grid_constant__ CUtensorMap tm_kv,
       return fabsf(l) < INFINITY ? -l : -INFINITY;
     };
     auto slot_of = [&](int i) { return (w.tile + i / kTile) * kKeys + rank * kTile + i % kTile; };
-    constexpr int kOwn = C::kRun * kTile / kSum;   // slots of a group that a thread writes
+    constexpr int kOwn = kMostRun * kTile / kSum;  // slots of a group that a thread writes
     while (w.next(a)) {
-      float ahead = row_neg(w.r, 0);
+      float ahead = row_neg(w.r, w.block(a, 0));
       const int new_at = a.starts[w.r];
       float* weights = a.weights + (size_t)w.r * a.max_pages * kPage;
       float old[kOwn];                             // earlier weights, asked for while S is made
@@ -374,9 +392,9 @@ weigh_kernel(const WeighArgs a, const __grid_constant__ CUtensorMap tm_kv,
         const int i = st + u * kSum, slot = slot_of(i);
         old[u] = i < w.tiles * kTile && slot < w.len && slot < new_at ? weights[slot] : 0.f;
       }
-      for (int b = 0; b < a.blocks; ++b, ++x) {
+      for (int b = 0; b < a.blocks; ++b, ++x) {    // the b-th of the group
         if (st < C::kMaxRows) neg[(x & 1) * C::kMaxRows + st] = ahead;
-        if (b + 1 < a.blocks) ahead = row_neg(w.r, b + 1);
+        if (b + 1 < a.blocks) ahead = row_neg(w.r, w.block(a, b + 1));
         asm volatile("bar.sync 1, %0;" ::"r"(kSum) : "memory");
         const float* ng = neg + (x & 1) * C::kMaxRows + half * cols;
         for (int t = 0; t < w.tiles; ++t, ++g) {
@@ -494,6 +512,9 @@ int32_t weigh_impl(const mla_cache_shape* s, const void* q, const void* kv,
   const int most_rows = pair ? 2 * kMine : kMine;
   a.blocks = (int)cdiv(a.M, most_rows);
   a.rows = (int)cdiv(cdiv(a.M, a.blocks), 32) * 32;
+  const int spare = (kMine - a.rows / (pair ? 2 : 1)) * kDqk / (2 * kTile * 4);
+  a.run = (pair ? Cfg<true>::kRun : Cfg<false>::kRun) + spare;
+  if (a.run > kMostRun) a.run = kMostRun;
   a.wait_limit_ns = wait_limit_ns;
   a.withhold = withhold;
   CUtensorMap tkv, tkvr, tq, tqr;
