@@ -265,17 +265,6 @@ weigh_kernel(const WeighArgs a, const __grid_constant__ CUtensorMap tm_kv,
         }
       }
       for (int i = 0; ok && i < a.blocks; ++i) {
-        if (!w.has_q(i)) {
-          if (x > 0 && !(ok = wait0(&ctl->q_empty, (x - 1) & 1))) break;
-          if (lane == 0) {
-            uint8_t* q = smem + kOffQ;
-            const int row = w.r * a.M + w.block(a, i) * a.rows + rank * held;
-            expect(&ctl->q_full, held * kDqk);
-            for (int c = 0; c < 4; ++c) load(q + c * qchunk, &tm_q, &ctl->q_full, c * 128, row);
-            load(q + 4 * qchunk, &tm_qr, &ctl->q_full, kDv, row);
-          }
-          ++x;
-        }
         for (int t = 0; t < w.tiles; ++t, ++g) {
           const int st = g % kStages;
           if (g >= kStages && !(ok = wait0(&ctl->kv_empty[st], (g / kStages - 1) & 1))) break;
@@ -291,6 +280,21 @@ weigh_kernel(const WeighArgs a, const __grid_constant__ CUtensorMap tm_kv,
                 load(s + c * kChunk + h * (kChunk / 2), &tm_kv, &ctl->kv_full[st], c * 128, row);
               load(s + 4 * kChunk + h * kPage * 64, &tm_kvr, &ctl->kv_full[st], kDv, row);
             }
+          }
+          // The queries after the first tile's keys, whose place is free before theirs.
+          if (t == 0 && !w.has_q(i)) {
+            if (x > 0 && !(ok = wait0(&ctl->q_empty, (x - 1) & 1))) {
+              ++g;                               // loaded
+              break;
+            }
+            if (lane == 0) {
+              uint8_t* q = smem + kOffQ;
+              const int row = w.r * a.M + w.block(a, i) * a.rows + rank * held;
+              expect(&ctl->q_full, held * kDqk);
+              for (int c = 0; c < 4; ++c) load(q + c * qchunk, &tm_q, &ctl->q_full, c * 128, row);
+              load(q + 4 * qchunk, &tm_qr, &ctl->q_full, kDv, row);
+            }
+            ++x;
           }
         }
       }
