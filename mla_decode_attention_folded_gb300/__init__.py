@@ -637,7 +637,7 @@ def kv_weigh(q, kv, block_table, seq_lens, lse, bmm1_scale: float, weights, star
                          rope_starts, status)
     _lib.check("mla_kv_weigh", _lib.load().mla_kv_weigh(
         ctypes.byref(shape), q.data_ptr(), kv.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
-        lse.data_ptr(), bmm1_scale, decay, starts.data_ptr(), _ptr(rope_starts), weights.data_ptr(),
+        lse.data_ptr(), float(bmm1_scale), float(decay), starts.data_ptr(), _ptr(rope_starts), weights.data_ptr(),
         _ptr(positions), _ptr(status), _stream_on(dev, stream)))
 
 
@@ -739,7 +739,7 @@ def kv_evict(kv, block_table, seq_lens, weights, keep, positions=None, recent: i
     _lib.check("mla_kv_evict", _lib.load().mla_kv_evict(
         ctypes.byref(CacheShape(R, 1, 1, PAGE, max_pages, pages)), kv.data_ptr(),
         block_table.data_ptr(), seq_lens.data_ptr(), weights.data_ptr(), _ptr(positions),
-        keep.data_ptr(), recent, sinks, weights_out.data_ptr(), _ptr(positions_out),
+        keep.data_ptr(), int(recent), int(sinks), weights_out.data_ptr(), _ptr(positions_out),
         lens_out.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(status),
         _stream_on(dev, stream)))
     return lens_out
@@ -812,7 +812,7 @@ def prompt_attention(q, k_nope, k_rope, v, cu_tokens, sm_scale: float, cu_keys=N
         _check(dev, "workspace", workspace, (torch.uint8,), workspace.shape)
     _lib.check("mla_prompt_attention", _lib.load().mla_prompt_attention(
         ctypes.byref(shape), q.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(), v.data_ptr(),
-        cu_tokens.data_ptr(), _ptr(cu_keys), sm_scale, workspace.data_ptr(), workspace.numel(),
+        cu_tokens.data_ptr(), _ptr(cu_keys), float(sm_scale), workspace.data_ptr(), workspace.numel(),
         out.data_ptr(), _ptr(lse), _ptr(status), _stream_on(dev, stream)))
     return out, lse
 

@@ -509,13 +509,15 @@ extern "C" int32_t mla_kv_evict(const mla_cache_shape* s, void* kv, const int32_
   a.recent = recent;
   a.sinks = sinks;
   // CTAs per request: as many as have 4,096 slots each, up to the cluster's limit and as
-  // long as the batch's CTAs fit on the SMs.
+  // long as the batch's CTAs fit on half of the SMs; more where the codes of a table's width would
+  // not fit into shared memory.
   const long long slots = (long long)s->max_pages * kPage;
   a.cluster = 1;
-  while (a.cluster < kMaxCluster && slots > 4096ll * a.cluster && s->R * a.cluster * 2 <= sms)
+  while (a.cluster < kMaxCluster && ((slots > 4096ll * a.cluster && s->R * a.cluster * 2 <= sms) ||
+                                     slots > (long long)kCached * a.cluster))
     a.cluster *= 2;
   const long long each = cdiv(slots, a.cluster);
-  a.chunk = (int)(each <= kCached ? each : 0);
+  a.chunk = (int)(each < kCached ? each : kCached);
   static bool attr_set[64] = {};
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
     if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

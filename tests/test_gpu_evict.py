@@ -130,6 +130,13 @@ def test_long_requests_on_clusters(n):
     _run([n], [n // 2], kind="ties", seed=n + 1, in_place=True)
 
 
+@pytest.mark.parametrize("R,width", [(3, 2048), (100, 700), (5, 12000)])
+def test_short_requests_in_wide_tables(R, width):
+    rng = np.random.default_rng(width)
+    lens = [int(v) for v in rng.integers(0, 300, R)]
+    _run(lens, [v // 2 for v in lens], recent=9, sinks=1, kind="ties", seed=R, width=width, mixed=True)
+
+
 def test_clusters_of_every_size():
     for R, width in ((80, 130), (70, 70), (38, 130), (19, 300), (9, 600), (4, 1100)):
         rng = np.random.default_rng(R)

@@ -111,6 +111,15 @@ def test_whole_items_claimed_by_the_ctas():
     _run((640, 700, 650, 900, 1100), H=64, Hkv=8, seed=4)
 
 
+@pytest.mark.parametrize("R", [31, 32, 33, 70])
+def test_one_long_prompt_among_short_ones(R):
+    """Up to 32 requests the CTAs plan for themselves, beyond a kernel does; the long one is cut."""
+    n = [(7 * i) % 50 for i in range(R)]
+    n[R // 2] = 3500
+    _run(n, H=2, seed=R, behind=3)
+    _run([1] * R, [40 + i if i != 5 else 5000 for i in range(R)], H=2, Hkv=1, seed=R + 1)
+
+
 def test_many_requests():
     g = torch.Generator().manual_seed(5)
     n = torch.randint(0, 40, (1024,), generator=g).tolist()
