@@ -61,8 +61,7 @@ __host__ __device__ inline long long before(const Request& q, int u) {
   return tiles_before(q, u) + (long long)kExtra * u;
 }
 __host__ __device__ inline long long places(const Request& q) { return before(q, items(q)); }
-// x = head * per + rest, 0 <= rest < per, without a division (the kernel that splits its registers
-// among its warps may call no function).
+// x = head * per + rest, 0 <= rest < per, without a division of 64 bits.
 __host__ __device__ inline int head_at(long long x, long long per, int H) {
   int lo = 0, hi = H;
   while (hi - lo > 1) {
