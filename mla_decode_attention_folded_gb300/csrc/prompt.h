@@ -15,7 +15,7 @@ constexpr int kKeys = 128;       // keys of a tile
 constexpr int kStep = kRows / kKeys;
 constexpr int kUncut = 4;        // items of no more tiles are never cut
 constexpr int kMinPart = 3;      // places of a part, at least
-constexpr int kExtra = 1;        // of an item: its first softmax, its output
+constexpr int kExtra = 2;        // of an item: its first softmax, its output
 constexpr int kWhole = 6;        // items stay whole where a pair has so many of the longest's tiles
 
 // A request of n query tokens and m keys; causal: query i sees keys j <= i + m - n.
