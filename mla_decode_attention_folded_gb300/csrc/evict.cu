@@ -508,13 +508,15 @@ extern "C" int32_t mla_kv_evict(const mla_cache_shape* s, void* kv, const int32_
   a.num_pages = s->num_pages;
   a.recent = recent;
   a.sinks = sinks;
-  // CTAs per request: as many as have 4,096 slots each, up to the cluster's limit and as
-  // long as the batch's CTAs fit on half of the SMs; more where the codes of a table's width would
-  // not fit into shared memory.
+  // CTAs per request: doubled while each has more than 4,096 slots (1 x 8k: 17.8 us on 2, 17.0 on 1;
+  // 4 x 32k: 22.6 on 8, 30.7 on 2) and the batch's fit on the SMs, clusters of 8 or 16 on two thirds of
+  // them: more of those do not run at a time (16 x 32k: 31.5 us on clusters of 4, 47 on 8; 10 x
+  // 20k: 27.8 and 25.6). More where the codes of a table's width would not fit into shared memory.
   const long long slots = (long long)s->max_pages * kPage;
   a.cluster = 1;
-  while (a.cluster < kMaxCluster && ((slots > 4096ll * a.cluster && s->R * a.cluster * 2 <= sms) ||
-                                     slots > (long long)kCached * a.cluster))
+  while (a.cluster < kMaxCluster &&
+         ((slots > 4096ll * a.cluster && s->R * a.cluster * 2 <= (a.cluster < 4 ? sms : sms * 2 / 3)) ||
+          slots > (long long)kCached * a.cluster))
     a.cluster *= 2;
   const long long each = cdiv(slots, a.cluster);
   a.chunk = (int)(each < kCached ? each : kCached);
@@ -540,9 +542,10 @@ extern "C" int32_t mla_kv_evict(const mla_cache_shape* s, void* kv, const int32_
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.cluster > 1 ? 2 : 1;
-  // The clusters make the moves themselves where they are a third of the SMs or more, or the
-  // requests are short.
-  a.apart = (long long)s->R * a.cluster * 3 < sms && slots > 2048ll * a.cluster;
+  // A second launch makes the moves on all SMs where the clusters leave a third of them idle (128k to
+  // 64k: 31 us with it, 60 without; 10 x 20k to 10k: 25.6 and 29.0; on more SMs it only costs: 32 x 16k
+  // to 2k 28.1 and 26.3) and the requests may have many (64 x 2,112 slots: 12.9 and 10.4 us).
+  a.apart = (long long)s->R * a.cluster * 3 <= sms * 2ll && slots > 2304ll * a.cluster;
   if (cudaLaunchKernelEx(&cfg, evict_select_kernel, a) != cudaSuccess) return MLA_ERR_CUDA;
   if (!a.apart) return MLA_OK;
   // At most half of a request's keys move.
