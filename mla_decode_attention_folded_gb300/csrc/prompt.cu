@@ -11,19 +11,34 @@
 // its MMAs (cta_group::2: 128 rows in each CTA): while the softmax of one half runs, the tensor
 // pipe multiplies for the other.
 //   S[256, 128 keys] = Q K^T, 12 MMAs;  O[256, 128] += P V, 8 MMAs, P from TMEM.
+// Requests of up to 256 rows would leave a half empty: theirs are the rows of two heads, on the same
+// keys (grouped heads) or on tiles of K and V that come by turns, one for each half.
+//
 // Each CTA loads half of a tile of K (64 keys) and of V (64 dims), 40 KB: three tiles are in
-// flight where a CTA on its own has room for little more than one, and waits for it. TMEM
-// holds both halves' S and O (4 x 128 columns); P (BF16) takes the place of the S it was made from.
-// Warp 0 loads by TMA; warps 1 and 2 of the first CTA issue the halves' MMAs; warp 3 tells
-// them that V is there, and clears what lies behind a request's last key; eight warps each are
-// the softmax of the halves: two threads to a row, 64 keys each. The maximum that P is relative
-// to moves only when a score exceeds it by 2^8 (O and the sum are then rescaled), so that the
-// two threads need no more than a barrier's vote in most tiles; P is rounded to BF16 (2^-8, as
-// the inputs are), its sum is of the FP32 values.
+// flight where a CTA on its own has room for little more than one, and waits for it (64 heads of
+// 8k tokens: 1130 us by single CTAs, 942 by pairs). TMEM holds both halves' S and O (4 x 128
+// columns); P (BF16) takes the place of the S it was made from.
+// Warp 0 loads by TMA; warps 1 and 2 of the first CTA issue the halves' MMAs (one warp for both:
+// 1320 us, 1172 with two); warp 3 tells them that V is there, and clears what lies behind a
+// request's last key; eight warps each are the softmax of the halves: two threads to a row, 64 keys
+// each (1172 -> 1130 us). The maximum that P is relative to moves only when a score exceeds it by
+// 2^8 (O and the sum are then rescaled), so that the two threads need no more than a barrier's vote
+// in most tiles; P is rounded to BF16 (2^-9, as the inputs are), its sum is of the FP32 values.
+// Registers are what the softmax is short of (96 a thread): what it spills costs more than anything
+// else here, so it keeps little of a piece and rescales O eight columns at a time.
 //
 // How the work is shared out is in prompt.h. The order of a half's MMAs is PV(t) before S(t + 1),
 // so that S may overwrite P and its completion tells that O is final.
+//
+// Measured (graph replays): 64 heads of 8,192 tokens 930 us, 1,480 TFLOP/s (the pipe's peak in a
+// burst is 1,874, and 1,690 under the power cap); 4 x 32 heads of 900 to 1,500 tokens, grouped,
+// without a mask 118 us, 1,030 TFLOP/s; 24 prompts of up to 2,048 tokens and 8 heads 123 us, 715;
+// 512 tokens on 16k keys, 8 heads 45 us, 940; two short prompts 8.5 us.
+// Dropped: V given back after S (1130 -> 1258 us); the MMAs' lock before the wait for P (912 -> 963);
+// weights made while the vote on the maximum runs (935 -> 1016); masks per 32 columns (spills, 916
+// -> 1173); registers moved from the four first warps to the softmax (24 prompts 128 -> 136 us).
 #include <cmath>
+#include <type_traits>
 
 #include "checks.h"
 #include "decode_common.cuh"
@@ -65,16 +80,19 @@ struct Piece {
   int t0, t1;                    // tiles, t1 <= what the last row sees
   int slot;                      // of its FP32 rows; -1: the whole item, straight to out
   int causal;
+  int twin;                      // 1: the halves are the rows of head and head + 1; 2: which have a K and V each
 };
+// First of the item's rows in half h.
+__device__ __forceinline__ int half_row(const Piece& p, int h) { return p.twin ? 0 : h * kHalf; }
 __device__ __forceinline__ int row_limit(const Piece& p, int j) {
   const int e = p.causal ? p.lim0 + j : p.m;
   return e < 0 ? 0 : e < p.m ? e : p.m;
 }
 // Tiles of the piece that half h multiplies.
 __device__ __forceinline__ int half_tiles(const Piece& p, int h) {
-  const int rows = min(p.rows - h * kHalf, kHalf);
+  const int row = half_row(p, h), rows = min(p.rows - row, kHalf);
   if (rows <= 0) return 0;
-  const int last = tiles_of(row_limit(p, h * kHalf + rows - 1));
+  const int last = tiles_of(row_limit(p, row + rows - 1));
   return max(min(p.t1, last) - p.t0, 0);
 }
 
@@ -94,7 +112,7 @@ struct PromptCtl {
   float row[2][kMine];           // [half][row]: what the two threads of a row tell one another
   // Values that are no numbers (below): by piece and dim, (piece + 1, ~ the first such key). Four
   // pieces' worth: no CTA's softmax is further behind the other's copies.
-  unsigned long long bad[4][kV];
+  unsigned long long bad[4][2][kV];   // [][half]
   uint32_t bad_piece[4];         // piece + 1, where there are any
   uint32_t tmem_base;
   uint32_t lock;                 // held by the half whose MMAs are being issued
@@ -117,6 +135,7 @@ struct PromptArgs {
   int32_t* status;
   float scale_log2;
   int R, T, Tk, H, group, causal, pairs;
+  int twins;                     // short requests have two heads to an item
   int planned;                   // the plan kernel has run; else every CTA plans for itself (R <= 32)
   unsigned long long wait_limit_ns;
   int withhold;                  // failure-detection test: CTA 0 never loads its first keys
@@ -155,8 +174,8 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptA
     const Request q = request(a, r, row0, key0, ok);
     if (!ok && a.status) atomicOr(a.status, MLA_FAULT_WORK_ITEM);
     const int I = items(q);
-    w = places(q) * a.H;
-    it = (long long)I * a.H;
+    w = places(q) * units(q, a.H, a.twins);
+    it = (long long)I * units(q, a.H, a.twins);
     if (I) longest = max(item_tiles(q, I - 1), I > 1 ? item_tiles(q, I - 2) : 0);
   }
   long long sw = w, si = it;
@@ -261,6 +280,7 @@ __device__ __forceinline__ bool take(PromptCtl* ctl, uint32_t seq, const PromptA
   p.t1 = s->t1;
   p.slot = s->slot;
   p.causal = s->causal;
+  p.twin = s->twin;
   __syncwarp();
   if (read) tc::mbar_arrive(&ctl->job_empty[b]);
   return p.rows > 0;
@@ -342,6 +362,16 @@ __device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
 
 // 1 / x to 2^-23, beside the 2^-9 of the BF16 that it scales: the exact division is a call, for which
 // the softmax threads would have to spare registers.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+               : "memory");
+}
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -387,7 +417,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
     tc::prefetch_tmap(&tm_r);
     tc::prefetch_tmap(&tm_v);
   }
-  if (threadIdx.x < 4 * kV) ctl->bad[threadIdx.x / kV][threadIdx.x % kV] = 0;
+  for (int i = threadIdx.x; i < 4 * 2 * kV; i += kThreads) (&ctl->bad[0][0][0])[i] = 0;
   if (warp == 1) {
     tc::tmem_alloc_pair(&ctl->tmem_base, kTmemCols);
     tc::tmem_relinquish_pair();
@@ -428,13 +458,13 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
           mine = request(a, lane, my_row0, my_key0, good);
           if (!good && a.status && blockIdx.x == 0) atomicOr(a.status, MLA_FAULT_WORK_ITEM);
           const int I = items(mine);
-          my_place = places(mine) * a.H;
-          my_item = (long long)I * a.H;
+          my_place = places(mine) * units(mine, a.H, a.twins);
+          my_item = (long long)I * units(mine, a.H, a.twins);
           if (I) longest = max(item_tiles(mine, I - 1), I > 1 ? item_tiles(mine, I - 2) : 0);
         }
         longest = __reduce_max_sync(0xffffffffu, longest);
         const long long w = my_place, it = my_item;
-  #pragma unroll
+#pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const long long u = __shfl_up_sync(0xffffffffu, my_place, o), v = __shfl_up_sync(0xffffffffu, my_item, o);
           if (lane >= o) my_place += u, my_item += v;
@@ -485,12 +515,17 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
           p.t0 = 0;
           if (parts > 0) {
             const long long per = places(q);
-            p.head = head_at(x, per, a.H);
+            p.head = head_at(x, per, units(q, a.H, a.twins));
             const long long rest = x - p.head * per;
             u = item_at(q, rest);
             p.t0 = (int)(rest - before(q, u));
           } else {
-            claimed_item(q, a.H, 3 * (int)(gridDim.x >> 1), (int)x, p.head, u);
+            claimed_item(q, units(q, a.H, a.twins), 3 * (int)(gridDim.x >> 1), (int)x, p.head, u);
+          }
+          p.twin = 0;
+          if (twins(q, a.twins)) {
+            p.head *= 2;
+            if (p.head + 1 < a.H) p.twin = p.head / a.group == (p.head + 1) / a.group ? 1 : 2;
           }
           const int tiles = item_tiles(q, u);
           p.t1 = tiles;
@@ -511,7 +546,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
               p.slot = 2 * pair + 1;
               int last = pair + 1;
               while (last + 1 < parts && part_at(total, len, last + 1) < stop) ++last;
-              if (rank == 0 && lane == 0) a.joins[pair] = {p.row0, p.rows, p.head, last};
+              if (rank == 0 && lane == 0) a.joins[pair] = {p.row0, p.rows, p.head, last << 1 | (p.twin > 0)};
             }
           }
           p.m = q.m;
@@ -554,26 +589,30 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
         ok = __shfl_sync(0xffffffffu, got, 0) != 0;
       };
       // Queries are loaded as soon as their half's last S of the piece before is done, whatever else
-      // the warp waits for: q[h] tells what is next for half h, this piece's or the next one's. All
-      // that is lane 0's.
+      // the warp waits for: this piece's, then the next one's. All that is lane 0's.
       struct Load {
-        int head, row, due;
-      } q0 = {0, 0, 0}, q1 = {0, 0, 0}, n0 = {0, 0, 0}, n1 = {0, 0, 0};
-      auto load_q = [&](int h, Load& q, uint32_t& x) {
-        if (!q.due || (x > 0 && !tc::mbar_test_wait(&ctl->q_empty[h], (x - 1) & 1))) return;
+        int head, row, due;                      // due: bit h: half h's; bit 2: a head for each half
+      } cur = {0, 0, 0}, nxt = {0, 0, 0};
+      auto load_q = [&](int h, uint32_t& x) {
+        const bool now = cur.due >> h & 1;
+        if ((!now && !(nxt.due >> h & 1)) || (x > 0 && !tc::mbar_test_wait(&ctl->q_empty[h], (x - 1) & 1))) return;
+        int head = now ? cur.head : nxt.head, row = now ? cur.row : nxt.row;
+        if (h) {
+          if ((now ? cur.due : nxt.due) & 4) ++head;
+          else row += kHalf;
+        }
         const uint32_t bar = tc::map_rank(&ctl->q_full[h], 0);
         tc::remote_arrive_expect_tx(bar, kQBlocks * kBlock);
-  #pragma unroll 1
+#pragma unroll 1
         for (int e = 0; e < kQBlocks; ++e)
-          tma_load_3d_pair(smem + (h * kQBlocks + e) * kBlock, &tm_q, bar, e * 128, q.head, q.row + h * kHalf);
-        q.due = 0;
+          tma_load_3d_pair(smem + (h * kQBlocks + e) * kBlock, &tm_q, bar, e * 128, head, row);
+        if (now) cur.due &= ~(1 << h);
+        else nxt.due &= ~(1 << h);
         ++x;
       };
       auto load_queries = [&] {
-        if (q0.due) load_q(0, q0, xq0);
-        else load_q(0, n0, xq0);
-        if (q1.due) load_q(1, q1, xq1);
-        else load_q(1, n1, xq1);
+        load_q(0, xq0);
+        load_q(1, xq1);
       };
       // Waits for a place in a ring (bar null: for this piece's queries to be asked for).
       auto wait_ring = [&](uint64_t* bar, uint32_t parity) {
@@ -581,8 +620,8 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
         if (lane == 0) {
           unsigned long long t0 = 0;
           for (int i = 0;; ++i) {
-            if (q0.due | q1.due | n0.due | n1.due) load_queries();
-            if (bar ? tc::mbar_try_wait(bar, parity) : !(q0.due | q1.due)) break;
+            if ((cur.due | nxt.due) & 3) load_queries();
+            if (bar ? tc::mbar_try_wait(bar, parity) : !(cur.due & 3)) break;
             if (i < 32) continue;
             if (!t0) t0 = tc::globaltimer_ns();
             if (*reinterpret_cast<volatile int*>(&ctl->abort_flag) || tc::globaltimer_ns() - t0 > a.wait_limit_ns) {
@@ -594,14 +633,13 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
         }
         return __shfl_sync(0xffffffffu, v, 0) != 0;
       };
-      auto queries = [&](const Piece& p, Load& a0, Load& a1) {
-        const int row = p.row0 + (int)rank * kMine;
-        a0 = {p.head, row, p.rows > 0 && half_tiles(p, 0) > 0};
-        a1 = {p.head, row, p.rows > 0 && half_tiles(p, 1) > 0};
+      auto queries = [&](const Piece& p, Load& l) {
+        l = {p.head, p.row0 + (int)rank * kMine, 0};
+        if (p.rows > 0) l.due = (half_tiles(p, 0) > 0) | (half_tiles(p, 1) > 0) << 1 | (p.twin > 0) << 2;
       };
       Piece p;
       next(p);
-      queries(p, q0, q1);
+      queries(p, cur);
       while (ok) {
         // Hand it on, or an empty one at the end.
         if (seq >= 2 && !(ok = wait_ring(&ctl->job_empty[seq & 1], ((seq >> 1) - 1) & 1))) break;
@@ -617,16 +655,19 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
           s->t1 = p.t1;
           s->slot = p.slot;
           s->causal = p.causal;
+          s->twin = p.twin;
           tc::mbar_arrive(&ctl->job_full[seq & 1]);
         }
         if (p.rows == 0) break;
         ++seq;
-        const int nt = max(half_tiles(p, 0), half_tiles(p, 1)), kvh = p.head / a.group;
+        // Places of the rings: a tile each, or one for each half.
+        const int two = p.twin == 2, nt = max(half_tiles(p, 0), half_tiles(p, 1)) << two;
+        const int kvh0 = p.head / a.group, kvh1 = two ? (p.head + 1) / a.group : kvh0;
         const int key0 = p.key0 + p.t0 * kKeys;
         bool ahead = false;
-  #pragma unroll 1
+#pragma unroll 1
         for (int t = 0; t < nt; ++t, ++n) {
-          const int st = n % kStages, key = key0 + t * kKeys;
+          const int st = n % kStages, key = key0 + (t >> two) * kKeys, kvh = t & two ? kvh1 : kvh0;
           if (n >= kStages && !(ok = wait_ring(&ctl->k_empty[st], (n / kStages - 1) & 1))) break;
           if (lane == 0 && !(withheld && n == 0)) {
             const uint32_t bar = tc::map_rank(&ctl->k_full[st], 0);
@@ -646,7 +687,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
           // The next piece is looked up while this one's tiles are multiplied.
           if (t == kStages - 1) {
             next(p);
-            queries(p, n0, n1);
+            queries(p, nxt);
             ahead = true;
             if (!ok) {
               ++n;                                 // loaded
@@ -656,12 +697,11 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
         }
         if (ok && !ahead) {
           next(p);
-          queries(p, n0, n1);
+          queries(p, nxt);
         }
         if (!ok || !(ok = wait_ring(nullptr, 0))) break;
-        q0 = n0;
-        q1 = n1;
-        n0.due = n1.due = 0;
+        cur = nxt;
+        nxt.due = 0;
       }
       // Never leave with copies in flight: another role may have given up a wait. V counts here, the
       // pair's K and queries on the first CTA; the CTAs leave together.
@@ -696,68 +736,78 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
         const uint64_t qd = tc::smem_desc(tc::smem_u32(smem) + h * kQBlocks * kBlock, 16, 1024, tc::kSw128);
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = pr_wait(bar, parity, ctl, a); };
-        auto give_back = [&](uint64_t* bar) {        // what this half does not multiply
-          tc::remote_arrive(tc::map_rank(bar, 0));
-          tc::remote_arrive(tc::map_rank(bar, 1));
+        // What this half does not multiply is given back as it lands: place i of a ring.
+        auto give = [&](uint64_t* full, uint64_t* empty, uint32_t i) {
+          const uint32_t st = i % kStages;
+          if (!wait(full + st, (i / kStages) & 1)) return false;
+          if (one) {
+            tc::remote_arrive(tc::map_rank(empty + st, 0));
+            tc::remote_arrive(tc::map_rank(empty + st, 1));
+          }
+          return true;
         };
         for (uint32_t seq = 0; ok; ++seq) {
           Piece p;
           if (!take(ctl, seq, a, p, one)) break;
           const int c = __shfl_sync(0xffffffffu, half_tiles(p, h), 0);
-          const int nt = max(c, __shfl_sync(0xffffffffu, half_tiles(p, h ^ 1), 0));
+          const int two = __shfl_sync(0xffffffffu, p.twin == 2, 0);
+          const uint32_t nt = max(c, __shfl_sync(0xffffffffu, half_tiles(p, h ^ 1), 0)) << two;
           // PV of tile t, then S of tile t + 1, under a lock: issued as they come, the halves' MMAs would
           // mingle, both finish late, and both softmaxes then run while the tensor pipe waits. What
           // the copies bring is waited for before P, where it is there by then, so that nothing
           // stands between P and the MMAs.
-    #pragma unroll 1
-          for (int t = -1; t < c; ++t) {
-            const uint32_t nv = n0 + t, sv = nv % kStages;          // V of tile t
-            const uint32_t nk = nv + 1, sk = nk % kStages;          // K of tile t + 1
-            const bool has_k = t + 1 < c;
-            if (t < 0 && c > 0 && !wait(&ctl->q_full[h], xq++ & 1)) break;
-            if (t >= 0 && !wait(&ctl->v_full[sv], (nv / kStages) & 1)) break;
-            const bool landed = has_k && tc::mbar_test_wait(&ctl->k_full[sk], (nk / kStages) & 1);
-            if (t >= 0) {
-              if (!wait(&ctl->p_full[h], xp++ & 1)) break;
-              if (one) {
-                if (!(ok = lock(ctl, a))) break;
-                tc::fence_after_sync();
-                const uint64_t v = tc::smem_desc(s_v + sv * kVBytes, kBlock, 1024, tc::kSw128);
-    #pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk)
-                  mma_bf16_ts_pair(col_o, col_s + (kk >> 2) * 64 + (kk & 3) * 8, v + (kk * 16 * 128 >> 4), kIdescO, t + kk != 0);
-                tc::mma_commit_pair(&ctl->v_empty[sv]);
-                if (t == c - 1) tc::mma_commit_pair(&ctl->o_full[h]);
-                if (!landed) unlock(ctl);
+          auto multiply = [&](auto by_turns) {
+            constexpr bool two = decltype(by_turns)::value;
+#pragma unroll 1
+            for (int t = -1; t < c; ++t) {
+              const uint32_t nv = two ? n0 + 2 * t + h : n0 + t, sv = nv % kStages;   // V of tile t
+              const uint32_t nk = nv + (two ? 2 : 1), sk = nk % kStages;              // K of tile t + 1
+              const bool has_k = t + 1 < c;
+              if (t < 0 && c > 0 && !wait(&ctl->q_full[h], xq++ & 1)) break;
+              // (Of two tiles by turns this half's comes first, or second.)
+              if (two && t >= 1 - h && !give(ctl->v_full, ctl->v_empty, nv - 1)) break;
+              if (t >= 0 && !wait(&ctl->v_full[sv], (nv / kStages) & 1)) break;
+              if (two && has_k && t + 1 >= 1 - h && !give(ctl->k_full, ctl->k_empty, nk - 1)) break;
+              const bool landed = has_k && tc::mbar_test_wait(&ctl->k_full[sk], (nk / kStages) & 1);
+              if (t >= 0) {
+                if (!wait(&ctl->p_full[h], xp++ & 1)) break;
+                if (one) {
+                  if (!(ok = lock(ctl, a))) break;
+                  tc::fence_after_sync();
+                  const uint64_t v = tc::smem_desc(s_v + sv * kVBytes, kBlock, 1024, tc::kSw128);
+#pragma unroll
+                  for (int kk = 0; kk < kKeys / 16; ++kk)
+                    mma_bf16_ts_pair(col_o, col_s + (kk >> 2) * 64 + (kk & 3) * 8, v + (kk * 16 * 128 >> 4), kIdescO, t + kk != 0);
+                  tc::mma_commit_pair(&ctl->v_empty[sv]);
+                  if (t == c - 1) tc::mma_commit_pair(&ctl->o_full[h]);
+                  if (!landed) unlock(ctl);
+                }
+              }
+              if (has_k) {
+                if (!landed && !wait(&ctl->k_full[sk], (nk / kStages) & 1)) break;
+                if (one) {
+                  if ((t < 0 || !landed) && !(ok = lock(ctl, a))) break;
+                  tc::fence_after_sync();
+                  const uint64_t k = tc::smem_desc(s_k + sk * kKBytes, 16, 1024, tc::kSw128);
+#pragma unroll
+                  for (int kk = 0; kk < 12; ++kk)
+                    mma_bf16_pair(col_s, qd + (((kk >> 2) * kBlock + (kk & 3) * 32) >> 4),
+                                  k + (((kk >> 2) * kKBlock + (kk & 3) * 32) >> 4), kIdescS, kk != 0);
+                  tc::mma_commit_pair(&ctl->s_full[h]);
+                  tc::mma_commit_pair(&ctl->k_empty[sk]);
+                  if (t + 1 == c - 1) tc::mma_commit_pair(&ctl->q_empty[h]);
+                  unlock(ctl);
+                }
               }
             }
-            if (has_k) {
-              if (!landed && !wait(&ctl->k_full[sk], (nk / kStages) & 1)) break;
-              if (one) {
-                if ((t < 0 || !landed) && !(ok = lock(ctl, a))) break;
-                tc::fence_after_sync();
-                const uint64_t k = tc::smem_desc(s_k + sk * kKBytes, 16, 1024, tc::kSw128);
-    #pragma unroll
-                for (int kk = 0; kk < 12; ++kk)
-                  mma_bf16_pair(col_s, qd + (((kk >> 2) * kBlock + (kk & 3) * 32) >> 4),
-                                k + (((kk >> 2) * kKBlock + (kk & 3) * 32) >> 4), kIdescS, kk != 0);
-                tc::mma_commit_pair(&ctl->s_full[h]);
-                tc::mma_commit_pair(&ctl->k_empty[sk]);
-                if (t + 1 == c - 1) tc::mma_commit_pair(&ctl->q_empty[h]);
-                unlock(ctl);
-              }
-            }
-          }
+          };
+          if (two) multiply(std::true_type{});
+          else multiply(std::false_type{});
           ok = __all_sync(0xffffffffu, ok);
-          // Tiles that only the other half multiplies are given back as they land; this half goes on to
-          // its next piece while the other finishes.
-          for (int t = c; ok && t < nt; ++t) {
-            const uint32_t n = n0 + t, st = n % kStages;
-            if (!wait(&ctl->k_full[st], (n / kStages) & 1)) break;
-            if (one) give_back(&ctl->k_empty[st]);
-            if (!wait(&ctl->v_full[st], (n / kStages) & 1)) break;
-            if (one) give_back(&ctl->v_empty[st]);
-          }
+          // The rest of the other half's, while it finishes: this half goes on to its next piece.
+          const uint32_t done = two && c > 0 ? (h ? nt : nt - 1) : c;
+          for (uint32_t i = done; ok && i < nt; ++i)
+            if (!give(ctl->k_full, ctl->k_empty, n0 + i) || !give(ctl->v_full, ctl->v_empty, n0 + i)) break;
           ok = __all_sync(0xffffffffu, ok);
           n0 += nt;
         }
@@ -779,10 +829,10 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
       for (uint32_t seq = 0; ok; ++seq) {
         Piece p;
         if (!take(ctl, seq, a, p, lane == 0)) break;
-        const int c0 = half_tiles(p, 0), nt = max(c0, half_tiles(p, 1));
-  #pragma unroll 1
+        const int two = p.twin == 2, c0 = half_tiles(p, 0), nt = max(c0, half_tiles(p, 1)) << two;
+#pragma unroll 1
         for (int t = 0; t < nt; ++t, ++n) {
-          const int st = n % kStages, key = (p.t0 + t) * kKeys, there = min(p.m - key, kKeys);
+          const int st = n % kStages, tile = t >> two, key = (p.t0 + tile) * kKeys, there = min(p.m - key, kKeys);
           uint4* v = reinterpret_cast<uint4*>(smem + kOffV + st * kVBytes);
           if (!(ok = __all_sync(0xffffffffu, pr_wait(&ctl->v_land[st], (n / kStages) & 1, ctl, a)))) break;
           if (there < kKeys) {
@@ -790,9 +840,9 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
             tc::fence_proxy_async_smem();
             __syncwarp();
           }
-          if (row_limit(p, t < c0 ? 0 : kHalf) < key + there) {
+          if (row_limit(p, tile < c0 ? 0 : half_row(p, 1)) < key + there) {
             uint32_t odd = 0;                      // bit 15 of a half: an exponent of ones
-  #pragma unroll 4
+#pragma unroll 4
             for (int i = lane; i < kKeys * 8; i += 32) {
               const uint4 x = v[i];
               odd |= ((x.x & 0x7F807F80u) + 0x00800080u) | ((x.y & 0x7F807F80u) + 0x00800080u) |
@@ -809,10 +859,11 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
                 const int dim = (int)rank * 64 + piece * 8 + (i & 7);
                 const unsigned long long note = (unsigned long long)(seq + 1) << 32 | ~(uint32_t)(key + key_row);
                 for (int c = 0; c < 2; ++c) {
-                  asm volatile("red.relaxed.cluster.shared::cluster.max.u64 [%0], %1;" ::"r"(
-                                   tc::map_rank(&ctl->bad[b][dim], c)),
-                               "l"(note)
-                               : "memory");
+                  for (int h = two ? t & 1 : 0; h < (two ? (t & 1) + 1 : 2); ++h)
+                    asm volatile("red.relaxed.cluster.shared::cluster.max.u64 [%0], %1;" ::"r"(
+                                     tc::map_rank(&ctl->bad[b][h][dim], c)),
+                                 "l"(note)
+                                 : "memory");
                   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(tc::map_rank(&ctl->bad_piece[b], c)),
                                "r"(seq + 1)
                                : "memory");
@@ -833,11 +884,11 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
     // wait that ran out a half's threads go on to the end of the piece without waiting, so that
     // all meet at its barriers, and leave together.
     const int h = (warp - 4) >> 3, side = (warp - 4) >> 2 & 1, quarter = warp & 3, row = quarter * 32 + lane;
-    const int j = h * kHalf + (int)rank * kMine + row;
+    const int in_half = (int)rank * kMine + row, j = h * kHalf + in_half;   // j: row of a slot
     const uint32_t p_full = tc::map_rank(&ctl->p_full[h], 0);
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t col_s = lanes + h * kKeys + side * 64;
-    const uint32_t col_o = lanes + kColO + h * kV + side * 64;
+    const uint32_t col_o = col_s + kColO;
     uint32_t xs = 0, xo = 0;
     Piece p;
     bool ok = true;
@@ -846,9 +897,12 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
     };
     for (uint32_t seq = 0; !half_any(h, !(ok && take(ctl, seq, a, p, lane == 0))); ++seq) {
       const int c = half_tiles(p, h);
-      const bool valid = j < p.rows;
-      const int lim = valid ? row_limit(p, j) : INT_MAX;
+      const int i_row = half_row(p, h) + in_half;
+      const int lim = i_row < p.rows ? row_limit(p, i_row) : INT_MAX;
+      p.row0 += i_row;                           // this thread's own
+      p.head += p.twin && h;
       const int lowest = __reduce_min_sync(0xffffffffu, lim);
+      int mine = p.t0 * kKeys + side * 64;       // this thread's first key of the tile
       float m = -INFINITY, l = 0.f;
 #pragma unroll 1
       for (int t = 0; t < c; ++t) {
@@ -858,12 +912,12 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
         tc::tmem_ld32(col_s, raw[0]);
         tc::tmem_ld32(col_s + 32, raw[1]);
         tc::tmem_wait_ld();
-        const int key = (p.t0 + t) * kKeys, mine = key + side * 64;
         if (mine + 64 > lowest) {                // keys that some row of the warp does not see
 #pragma unroll
           for (int i = 0; i < 64; ++i)
             if (mine + i >= lim) raw[i >> 5][i & 31] = 0xFF800000u;
         }
+        mine += kKeys;
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int e = 0; e < 32; e += 2)
@@ -885,13 +939,13 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
           l *= f;
           if (t > 0 && __any_sync(0xffffffffu, moves)) {
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-              uint32_t o[16];
-              tc::tmem_ld16(col_o + 16 * i, o);
+            for (int i = 0; i < 8; ++i) {
+              uint32_t o[8];
+              tmem_ld8(col_o + 8 * i, o);
               tc::tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tc::tmem_st16(col_o + 16 * i, o);
+              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st8(col_o + 8 * i, o);
             }
           }
         }
@@ -931,13 +985,14 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
       tc::fence_after_sync();
       const float inv = l > 0.f ? rcp(l) : l;    // NaN stays
       const float lse = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
-      const size_t at = (size_t)(p.row0 + j) * a.H + p.head;
+      const bool valid = lim != INT_MAX;
+      const size_t at = (size_t)p.row0 * a.H + p.head;
       if (p.slot < 0) {
         if (valid && a.lse && side == 0) a.lse[at] = lse;
       } else if (side == 0) {
         a.part_lse[(size_t)p.slot * kRows + j] = lse;
       }
-      const volatile unsigned long long* bad = ctl->bad[seq & 3] + side * 64;
+      const volatile unsigned long long* bad = ctl->bad[seq & 3][h] + side * 64;
       const bool noted = *reinterpret_cast<volatile uint32_t*>(&ctl->bad_piece[seq & 3]) == seq + 1;
 #pragma unroll 4
       for (int i = 0; i < 4; ++i) {
@@ -988,8 +1043,9 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptArgs a) {
   grid_dep_launch();
   const int4 jn = *reinterpret_cast<const int4*>(a.joins + blockIdx.y);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = blockIdx.x * kJoinRows + (lane & 15);
-  const int rows = jn.y, part = blockIdx.y, last = jn.w;
-  if (j >= rows) return;
+  // Row j of the slots: of the item, or in half j / 256 a row of that head of two.
+  const int part = blockIdx.y, last = jn.w >> 1, twin = jn.w & 1, row_of = twin ? j % kHalf : j;
+  if (row_of >= jn.y) return;
   // Pieces: the last of part `part`, then the first of the parts up to `last`.
   auto slot = [&](int p) { return (size_t)(p == part ? 2 * p + 1 : 2 * p); };
   float top = -INFINITY;
@@ -1015,7 +1071,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptArgs a) {
     acc[7] += w * v[1].w;
   }
   const float inv = z > 0.f ? 1.f / z : z;       // NaN stays
-  const size_t row = (size_t)(jn.x + j) * a.H + jn.z;
+  const size_t row = (size_t)(jn.x + row_of) * a.H + jn.z + (twin ? j / kHalf : 0);
   if (a.lse && threadIdx.x < 16) a.lse[row] = z > 0.f ? base + log2f(z) : z == 0.f ? -INFINITY : z;
   uint2* dst = reinterpret_cast<uint2*>(a.out + row * kV) + quad;
   dst[0] = make_uint2(f32x2_to_bf16x2(acc[0] * inv, acc[1] * inv), f32x2_to_bf16x2(acc[2] * inv, acc[3] * inv));
@@ -1113,6 +1169,8 @@ int32_t prompt_impl(const mla_prompt_shape* s, const void* q, const void* k_nope
   // A batch of few requests and items has no plan kernel before it: 2 short prompts 11.3 -> 8.8 us,
   // 512 tokens on 16k keys 51.4 -> 48.1, 24 prompts up to 2k the same. Others gain by claimed items,
   // which need one. Offsets that are none may let requests overlap: each may have all rows.
+  // Two heads to an item of a short request, unless a head for each pair of CTAs is quicker.
+  a.twins = s->keys > kUncut * kKeys || (long long)s->R * s->H > a.pairs;
   const long long items_least = (long long)s->H * cdiv(s->tokens, kRows);
   const long long places_most = items_least * s->R * (1 + kExtra + cdiv(s->keys, kKeys));
   a.planned = s->R > 32 || items_least >= (long long)kWhole * a.pairs || places_most >= (1ll << 31);

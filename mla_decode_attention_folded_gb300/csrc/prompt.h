@@ -1,7 +1,7 @@
-// The work of a batch of prompts: items of 512 query rows of one head, each with the
-// tiles of 128 keys that its rows see, and how all items lie on one line of places: a
-// place for each tile, then kExtra for what an item costs besides. A pair of CTAs takes an
-// item, as two halves of 256 rows. Host and device code include this.
+// The work of a batch of prompts: items of 512 query rows of one head (or of two heads' rows, where
+// a request has 256 at most), each with the tiles of 128 keys that its rows see, and how all items
+// lie on one line of places: a place for each tile, then kExtra for what an item costs besides. A
+// pair of CTAs takes an item, as two halves of 256 rows. Host and device code include this.
 #pragma once
 
 #include "internal.h"
@@ -13,10 +13,21 @@ constexpr int kRows = 512;       // query rows of an item
 constexpr int kHalf = 256;       // of its half
 constexpr int kKeys = 128;       // keys of a tile
 constexpr int kStep = kRows / kKeys;
-constexpr int kUncut = 4;        // items of no more tiles are never cut
-constexpr int kMinPart = 3;      // places of a part, at least
-constexpr int kExtra = 2;        // of an item: its first softmax, its output
-constexpr int kWhole = 6;        // items stay whole where a pair has so many of the longest's tiles
+// Requests of no more rows than a half have two heads to an item, a half each (up to 148 rows, 27
+// requests of 64 heads: 196 -> 135 us; 95 rows on 1,700 keys, four heads to a K and V: 656 -> 381 us;
+// 9 rows on 800 keys each: 494 -> 379 us).
+constexpr int kAlone = 256;
+// Items of no more tiles are never cut, so that batches of up to 512 keys need no launch that joins
+// pieces. (2, 4 and 8 measured the same.)
+constexpr int kUncut = 4;
+// Places of a part, at least (64 heads of 8k: 924 us with 1, 917 with 3 and 6).
+constexpr int kMinPart = 3;
+// What an item costs besides its tiles: its first softmax, its output (24 prompts up to 2k: 141 us with 0,
+// 128 with 1, 125 with 2; 512 rows on 16k keys 49.5, 47.7, 46.5; with 3 and 4 some gain, some lose).
+constexpr int kExtra = 2;
+// Items stay whole where a pair has so many of the longest's tiles (3: 24 prompts up to 2k 136 us, 128
+// with 6; 20, and 64 heads of 8k are cut: 934 us, 917 with 6).
+constexpr int kWhole = 6;
 
 // A request of n query tokens and m keys; causal: query i sees keys j <= i + m - n.
 struct Request {
@@ -33,6 +44,12 @@ __host__ __device__ inline int limit(const Request& q, int i) {
   if (!q.causal) return q.m;
   const int e = i + 1 + (q.m - q.n);
   return e < 0 ? 0 : e < q.m ? e : q.m;
+}
+// Whether a request has two heads to an item.
+__host__ __device__ inline bool twins(const Request& q, bool allowed) { return allowed && q.n <= kAlone; }
+// Heads, or pairs of heads, that have items of their own.
+__host__ __device__ inline int units(const Request& q, int H, bool allowed) {
+  return twins(q, allowed) ? (H + 1) / 2 : H;
 }
 // Tiles of item u: those that its last row sees, one where there are none.
 __host__ __device__ inline int item_tiles(const Request& q, int u) {
@@ -61,7 +78,7 @@ __host__ __device__ inline long long before(const Request& q, int u) {
   return tiles_before(q, u) + (long long)kExtra * u;
 }
 __host__ __device__ inline long long places(const Request& q) { return before(q, items(q)); }
-// x = head * per + rest, 0 <= rest < per, without a division of 64 bits.
+// x = unit * per + rest, 0 <= rest < per, without a division of 64 bits.
 __host__ __device__ inline int head_at(long long x, long long per, int H) {
   int lo = 0, hi = H;
   while (hi - lo > 1) {
@@ -105,7 +122,7 @@ struct Plan {
 // An item that a cut runs through, by the pair whose part it begins in (rows 0: none): its pieces
 // are that part's last and the first ones of the parts up to `last`.
 struct Join {
-  int row0, rows, head, last;
+  int row0, rows, head, last;    // last: with a bit below it, whether the item has two heads
 };
 // Where part p begins.
 __host__ __device__ inline long long part_at(long long total, long long len, int p) {

@@ -33,6 +33,8 @@ int main(int argc, char** argv) {
     const int R = pick(1, pick(0, 2) ? 6 : 30), H = pick(1, 9), ctas = pick(0, 1) ? 152 : pick(1, 200);
     std::vector<Request> q(R);
     std::vector<long long> first(R + 1, 0);
+    std::vector<int> of(R);                        // heads, or pairs of heads, of a request
+    const bool allowed = pick(0, 1);
     int longest = 0;
     for (int r = 0; r < R; ++r) {
       q[r].n = size();
@@ -57,10 +59,13 @@ int main(int argc, char** argv) {
       const int I = items(q[r]);
       CHECK(!I || std::max(item_tiles(q[r], I - 1), I > 1 ? item_tiles(q[r], I - 2) : 0) >=
                       item_tiles(q[r], 0));
-      first[r + 1] = first[r] + at * H;
+      of[r] = units(q[r], H, allowed);
+      CHECK(twins(q[r], allowed) == (allowed && q[r].n <= kHalf));
+      CHECK(twins(q[r], allowed) ? 2 * of[r] - H >= 0 && 2 * of[r] - H < 2 : of[r] == H);
+      first[r + 1] = first[r] + at * of[r];
       if (at) {
-        const long long x = std::uniform_int_distribution<long long>(0, at * H - 1)(g);
-        CHECK(head_at(x, at, H) == x / at);
+        const long long x = std::uniform_int_distribution<long long>(0, at * of[r] - 1)(g);
+        CHECK(head_at(x, at, of[r]) == x / at);
       }
     }
     const long long total = first[R];
@@ -74,10 +79,10 @@ int main(int argc, char** argv) {
       for (int r = 0; r < R; ++r) {
         std::set<std::pair<int, int>> seen;
         const int I = items(q[r]), wide = pick(1, 500);
-        for (int x = 0; x < I * H; ++x) {
+        for (int x = 0; x < I * of[r]; ++x) {
           int head, u;
-          claimed_item(q[r], H, wide, x, head, u);
-          CHECK(head >= 0 && head < H && u >= 0 && u < I && seen.insert({head, u}).second);
+          claimed_item(q[r], of[r], wide, x, head, u);
+          CHECK(head >= 0 && head < of[r] && u >= 0 && u < I && seen.insert({head, u}).second);
         }
       }
       continue;
@@ -100,7 +105,7 @@ int main(int argc, char** argv) {
       CHECK(end > at);
       while (at < end) {
         const int r = find(at);
-        const long long x = at - first[r], per = places(q[r]), head = head_at(x, per, H);
+        const long long x = at - first[r], per = places(q[r]), head = head_at(x, per, of[r]);
         const long long rest = x - head * per;
         const int u = item_at(q[r], rest), tiles = item_tiles(q[r], u);
         const int t0 = (int)(rest - before(q[r], u));

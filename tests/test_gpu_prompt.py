@@ -120,6 +120,23 @@ def test_one_long_prompt_among_short_ones(R):
     _run([1] * R, [40 + i if i != 5 else 5000 for i in range(R)], H=2, Hkv=1, seed=R + 1)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("H,Hkv", [(2, 2), (3, 3), (5, 1), (9, 3), (15, 5), (8, 2), (7, 7)])
+def test_two_heads_to_an_item(H, Hkv, causal):
+    """Requests of up to 256 rows have a head in each half of an item: on the same keys or each on its
+    own, an odd head left over, whole and cut, beside requests that are longer."""
+    _run((1, 256, 0, 100, 257, 200), (900, 256, 20, 1500, 300, 0), H=H, Hkv=Hkv, causal=causal, seed=H, behind=2)
+    _run((5,), (9000,), H=H, Hkv=Hkv, causal=causal, seed=H + 1)
+    _run((130, 20), (3000, 2500), H=H, Hkv=Hkv, causal=causal, seed=H + 2, start=4)
+
+
+@pytest.mark.parametrize("R,H,Hkv,n,m", [(30, 32, 32, 9, 10), (30, 32, 8, 40, 700), (40, 21, 3, 33, 650),
+                                         (40, 64, 64, 2, 300)])
+def test_many_short_items(R, H, Hkv, n, m):
+    """More items than pairs of CTAs, by turns and claimed, two heads each."""
+    _run([n + i % 7 for i in range(R)], [m + 5 * i for i in range(R)], H=H, Hkv=Hkv, seed=R)
+
+
 def test_many_requests():
     g = torch.Generator().manual_seed(5)
     n = torch.randint(0, 40, (1024,), generator=g).tolist()
@@ -169,7 +186,8 @@ def test_nan_and_infinities_stay_in_their_request():
     assert same(out[465:465 + 128], want[465:465 + 128]) and torch.isnan(out[615:]).all()
 
 
-@pytest.mark.parametrize("n,m,H", [(700, 700, 2), (300, 900, 1), (1500, 1500, 1), (2048, 2048, 4)])
+@pytest.mark.parametrize("n,m,H", [(700, 700, 2), (300, 900, 1), (1500, 1500, 1), (2048, 2048, 4),
+                                   (256, 900, 2), (200, 700, 3), (150, 6000, 4), (129, 129, 96)])
 def test_values_that_are_no_numbers_reach_only_rows_that_see_them(n, m, H):
     """Other rows, and other dims of the rows that do, keep their bits; cut items too."""
     q, kn, kr, v = _inputs([0, n], [0, m], H, H, 21)
