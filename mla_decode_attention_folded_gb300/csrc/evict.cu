@@ -11,8 +11,13 @@
 // Bound by HBM for large evictions (16 B per key, 1,152 B per moved key) and by latency for
 // a step's few keys. A cluster per request orders its keys: 32-bit codes that sort as the
 // rule does, held in shared memory; the keep-th largest by three digits of histograms, summed
-// in the first CTA; places by ordered counts. It lists the moves and makes them, 9 threads a
-// row; where the clusters of a batch leave most SMs idle, a second launch makes them on all.
+// in the first CTA (12.5 -> 10.2 us against every CTA reading all); places by ordered counts. It
+// lists the moves and makes them, 9 threads a row; where the clusters of a batch leave enough SMs
+// idle, a second launch makes them on all.
+//
+// Measured (graph replays): 128 requests drop 7 of 2,055 keys in 10.5 us, nearly all of it the
+// select's chain of dependent steps; 8 x 20k to 32k keys to 4k in 25 us (1.4 TB/s of what has to
+// move), 128k keys to 64k in 31 us (1.3 TB/s): the walks over the keys and the scattered rows.
 #include <climits>
 
 #include "checks.h"
@@ -59,7 +64,8 @@ __device__ __forceinline__ Move read_move(const EvictArgs& a, int r, long long m
   return {mv.x, mv.y, table[mv.x / kPage], table[mv.y / kPage]};
 }
 __device__ __forceinline__ void make_move(const EvictArgs& a, int r, const Move& mv, int part) {
-  const bool ok = mv.page_from >= 0 && mv.page_from < a.num_pages && mv.page_to >= 0 && mv.page_to < a.num_pages;
+  const bool ok = mv.page_from >= 0 && mv.page_from < a.num_pages && mv.page_to >= 0 &&
+                  mv.page_to < a.num_pages;
   if (ok) {
     const uint4* src =
         reinterpret_cast<const uint4*>(a.kv + ((size_t)mv.page_from * kPage + mv.from % kPage) * kDqk) + part;
@@ -100,7 +106,8 @@ struct Shared {
   unsigned long long sums[kWarps];
   uint32_t digit[3];             // what holds the wanted place, the places left in it, its codes
   int top;                       // newest position of this CTA's keys
-  uint32_t told[3][kMaxCluster]; // what the cluster's CTAs tell all: newest positions or equals, holes, movers
+  // What the cluster's CTAs tell all: newest positions or equals, holes, movers.
+  uint32_t told[3][kMaxCluster];
 };
 
 __device__ __forceinline__ void join(int cluster) {
@@ -146,9 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictAr
   const int rank = a.cluster > 1 ? (int)tc::cluster_rank() : 0;
   const int r = blockIdx.x / a.cluster, tid = threadIdx.x;
   for (int i = tid; i < 3 * kBins; i += kThreads) sh.hist[i / kBins][i % kBins] = 0;
-  if (tid == 0) {
-    sh.top = INT_MIN;
-  }
+  if (tid == 0) sh.top = INT_MIN;
   grid_dep_wait();
   grid_dep_launch();
   const int most = a.max_pages * kPage, given = a.seq_lens[r], keep = max(a.keep[r], 0);

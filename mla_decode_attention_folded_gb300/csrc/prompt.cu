@@ -23,7 +23,7 @@
 // request's last key; eight warps each are the softmax of the halves: two threads to a row, 64 keys
 // each (1172 -> 1130 us). The maximum that P is relative to moves only when a score exceeds it by
 // 2^8 (O and the sum are then rescaled), so that the two threads need no more than a barrier's vote
-// in most tiles; P is rounded to BF16 (2^-9, as the inputs are), its sum is of the FP32 values.
+// in most tiles; P is rounded to BF16 (2^-8, as the inputs are), its sum is of the FP32 values.
 // Registers are what the softmax is short of (96 a thread): what it spills costs more than anything
 // else here, so it keeps little of a piece and rescales O eight columns at a time.
 //
@@ -80,7 +80,7 @@ struct Piece {
   int t0, t1;                    // tiles, t1 <= what the last row sees
   int slot;                      // of its FP32 rows; -1: the whole item, straight to out
   int causal;
-  int twin;                      // 1: the halves are the rows of head and head + 1; 2: which have a K and V each
+  int twin;                      // 1: the halves are the rows of head and head + 1; 2: of K and V each
 };
 // First of the item's rows in half h.
 __device__ __forceinline__ int half_row(const Piece& p, int h) { return p.twin ? 0 : h * kHalf; }
@@ -360,7 +360,7 @@ __device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
   return r;
 }
 
-// 1 / x to 2^-23, beside the 2^-9 of the BF16 that it scales: the exact division is a call, for which
+// 1 / x to 2^-23, beside the 2^-8 of the BF16 that it scales: the exact division is a call, for which
 // the softmax threads would have to spare registers.
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -432,7 +432,8 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
   if (warp < 4) {
     if (warp == 0) {
       // ------------------------------------------------------------ pieces and copies
-      uint32_t seq = 0, n = 0, xq0 = 0, xq1 = 0, claims = 0;   // pieces, tiles, queries of the halves so far
+      // So far: pieces, tiles, queries of the halves, claims.
+      uint32_t seq = 0, n = 0, xq0 = 0, xq1 = 0, claims = 0;
       bool ok = true;
       auto wait0 = [&](uint64_t* bar, uint32_t parity) {
         int v = 1;
@@ -466,7 +467,8 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
         const long long w = my_place, it = my_item;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const long long u = __shfl_up_sync(0xffffffffu, my_place, o), v = __shfl_up_sync(0xffffffffu, my_item, o);
+          const long long u = __shfl_up_sync(0xffffffffu, my_place, o);
+          const long long v = __shfl_up_sync(0xffffffffu, my_item, o);
           if (lane >= o) my_place += u, my_item += v;
         }
         total = __shfl_sync(0xffffffffu, my_place, 31);
@@ -595,7 +597,8 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
       } cur = {0, 0, 0}, nxt = {0, 0, 0};
       auto load_q = [&](int h, uint32_t& x) {
         const bool now = cur.due >> h & 1;
-        if ((!now && !(nxt.due >> h & 1)) || (x > 0 && !tc::mbar_test_wait(&ctl->q_empty[h], (x - 1) & 1))) return;
+        if (!now && !(nxt.due >> h & 1)) return;
+        if (x > 0 && !tc::mbar_test_wait(&ctl->q_empty[h], (x - 1) & 1)) return;
         int head = now ? cur.head : nxt.head, row = now ? cur.row : nxt.row;
         if (h) {
           if ((now ? cur.due : nxt.due) & 4) ++head;
@@ -624,7 +627,8 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
             if (bar ? tc::mbar_try_wait(bar, parity) : !(cur.due & 3)) break;
             if (i < 32) continue;
             if (!t0) t0 = tc::globaltimer_ns();
-            if (*reinterpret_cast<volatile int*>(&ctl->abort_flag) || tc::globaltimer_ns() - t0 > a.wait_limit_ns) {
+            if (*reinterpret_cast<volatile int*>(&ctl->abort_flag) ||
+                tc::globaltimer_ns() - t0 > a.wait_limit_ns) {
               if (atomicExch(&ctl->abort_flag, 1) == 0 && a.status) atomicOr(a.status, MLA_FAULT_WAIT_TIMEOUT);
               v = 0;
               break;
@@ -777,7 +781,8 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
                   const uint64_t v = tc::smem_desc(s_v + sv * kVBytes, kBlock, 1024, tc::kSw128);
 #pragma unroll
                   for (int kk = 0; kk < kKeys / 16; ++kk)
-                    mma_bf16_ts_pair(col_o, col_s + (kk >> 2) * 64 + (kk & 3) * 8, v + (kk * 16 * 128 >> 4), kIdescO, t + kk != 0);
+                    mma_bf16_ts_pair(col_o, col_s + (kk >> 2) * 64 + (kk & 3) * 8, v + (kk * 16 * 128 >> 4),
+                                     kIdescO, t + kk != 0);
                   tc::mma_commit_pair(&ctl->v_empty[sv]);
                   if (t == c - 1) tc::mma_commit_pair(&ctl->o_full[h]);
                   if (!landed) unlock(ctl);
@@ -1019,9 +1024,11 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
             w[e] = f32x2_to_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
           if (valid && ok) st_32(a.out + at * kV + side * 64 + 16 * i, w);
         } else if (c > 0) {
-          uint4* dst = reinterpret_cast<uint4*>(a.part_o) + ((size_t)p.slot * 32 + side * 16 + 4 * i) * kRows + j;
+          uint4* dst =
+              reinterpret_cast<uint4*>(a.part_o) + ((size_t)p.slot * 32 + side * 16 + 4 * i) * kRows + j;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) dst[e * kRows] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          for (int e = 0; e < 4; ++e)
+            dst[e * kRows] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       }
       tc::fence_before_sync();
@@ -1088,7 +1095,8 @@ int check_prompt(const mla_prompt_shape* s) {
   return MLA_OK;
 }
 size_t prompt_bytes(const mla_prompt_shape* s) {
-  return plan_bytes(s->R, pairs_of(s->num_ctas)) + lse_bytes(pairs_of(s->num_ctas)) + 2 * (size_t)pairs_of(s->num_ctas) * kSlotBytes;
+  const int pairs = pairs_of(s->num_ctas);
+  return plan_bytes(s->R, pairs) + lse_bytes(pairs) + 2 * (size_t)pairs * kSlotBytes;
 }
 
 int32_t prompt_impl(const mla_prompt_shape* s, const void* q, const void* k_nope, const void* k_rope,
@@ -1125,8 +1133,9 @@ int32_t prompt_impl(const mla_prompt_shape* s, const void* q, const void* k_nope
   a.first_place = reinterpret_cast<long long*>(ws + sizeof(Plan));
   a.first_item = a.first_place + s->R + 1;
   a.joins = reinterpret_cast<Join*>(a.first_item + s->R + 1);
-  a.part_lse = reinterpret_cast<float*>(ws + plan_bytes(s->R, pairs_of(s->num_ctas)));
-  a.part_o = reinterpret_cast<float*>(ws + plan_bytes(s->R, pairs_of(s->num_ctas)) + lse_bytes(pairs_of(s->num_ctas)));
+  a.pairs = pairs_of(s->num_ctas);
+  a.part_lse = reinterpret_cast<float*>(ws + plan_bytes(s->R, a.pairs));
+  a.part_o = reinterpret_cast<float*>(ws + plan_bytes(s->R, a.pairs) + lse_bytes(a.pairs));
   a.status = status;
   a.scale_log2 = (float)((double)sm_scale * 1.4426950408889634);
   a.R = s->R;
@@ -1135,7 +1144,6 @@ int32_t prompt_impl(const mla_prompt_shape* s, const void* q, const void* k_nope
   a.H = s->H;
   a.group = s->H / s->kv_heads;
   a.causal = s->causal;
-  a.pairs = pairs_of(s->num_ctas);
   a.wait_limit_ns = wait_limit_ns;
   a.withhold = withhold;
   // Without keys the maps of K and V stand on the queries; nothing is read through them.

@@ -14,6 +14,13 @@
 // bring them: a pair of CTAs (cta_group::2) takes 256 keys, 128 in each, and blocks of up to 256 rows,
 // half of them in each CTA's shared memory. All tiles of the batch are one line, cut into equal
 // runs, one per CTA or pair: keys need no joining, so a cut costs nothing.
+//
+// Measured (graph replays): 64 requests of up to 8k keys, 56 rows, 30.7 us, 5.2 TB/s; 16 of 16k to
+// 64k, 256 rows, 74 us, 5.2 TB/s and 2,610 TFLOP/s; 128 of up to 4k, 448 rows, 68.7 us, 2,210
+// TFLOP/s of FP8; two short ones 5.5 us. What is left at many rows is the pipe's wait for keys and
+// queries at the change of a block: shared memory has room for two tiles beside the queries.
+// Dropped: tiles in bands of 128 dims, refilled as they are multiplied (69.6 -> 76.7 us), the queries
+// in bands (68.7 -> 67.7, but two short requests 5.7 -> 5.9).
 #include <cmath>
 
 #include "checks.h"
@@ -43,7 +50,8 @@ struct Cfg {
   static constexpr int kCtas = PAIR ? 2 : 1;
   static constexpr int kMaxRows = kCtas * kMine;     // rows of a block: the MMA's N
   static constexpr int kBufs = kTmemCols / kMaxRows; // score buffers in TMEM
-  static constexpr int kRun = PAIR ? 6 : 8;          // tiles that a row block goes over, at least
+  // Tiles that a row block goes over, at least (groups of 2: 256 rows 78 us, of 6 and more 74).
+  static constexpr int kRun = PAIR ? 6 : 8;
 };
 // MMAs wait on the first CTA's barriers of a pair, and arrive on both CTAs'.
 struct WeighCtl {
@@ -313,57 +321,57 @@ weigh_kernel(const WeighArgs a, const __grid_constant__ CUtensorMap tm_kv,
     }
   } else if (warp == 1) {
     if (rank == 0) {
-    // The whole warp waits, so that what the MMAs are given stays in uniform registers; one lane
-    // issues.
-    const bool one = elect();
-    bool ok = true;
-    uint32_t g = 0, x = 0;
-    const uint32_t idesc = tc::idesc_e4m3_f32(kKeys, a.rows, false, false);
-    const uint64_t q = tc::smem_desc(tc::smem_u32(smem + kOffQ), 16, 1024, tc::kSw128);
-    const uint64_t qr = tc::smem_desc(tc::smem_u32(smem + kOffQ) + 4 * qchunk, 16, 512, tc::kSw64);
-    const uint32_t s0 = tc::smem_u32(smem);
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = wg_wait(bar, parity, ctl, a); };
-    auto mma = [&](uint32_t d, uint64_t k, uint64_t n, bool accumulate) {
-      if (PAIR) tc::mma_f8_pair(d, k, n, idesc, accumulate);
-      else tc::mma_e4m3(d, k, n, idesc, accumulate);
-    };
-    auto commit = [&](uint64_t* bar) {
-      if (PAIR) tc::mma_commit_pair(bar);
-      else tc::mma_commit(bar);
-    };
-    while (ok && w.next(a)) {
-      for (int i = 0; ok && i < a.blocks; ++i) {
-        if (!w.has_q(i) && !wait(&ctl->q_full, x++ & 1)) break;
-        for (int t = 0; t < w.tiles; ++t, ++g) {
-          const int st = g % kStages, bf = g % C::kBufs;
-          if (!wait(&ctl->kv_full[st], (g / kStages) & 1)) break;
-          if (g >= C::kBufs && !wait(&ctl->s_empty[bf], (g / C::kBufs - 1) & 1)) break;
-          tc::fence_after_sync();
-          const uint64_t k = tc::smem_desc(s0 + st * kStageBytes, 16, 1024, tc::kSw128);
-          const uint64_t kr = tc::smem_desc(s0 + st * kStageBytes + 4 * kChunk, 16, 512, tc::kSw64);
-          const uint32_t d = tmem + bf * C::kMaxRows;
-          if (one) {
+      // The whole warp waits, so that what the MMAs are given stays in uniform registers; one lane
+      // issues.
+      const bool one = elect();
+      bool ok = true;
+      uint32_t g = 0, x = 0;
+      const uint32_t idesc = tc::idesc_e4m3_f32(kKeys, a.rows, false, false);
+      const uint64_t q = tc::smem_desc(tc::smem_u32(smem + kOffQ), 16, 1024, tc::kSw128);
+      const uint64_t qr = tc::smem_desc(tc::smem_u32(smem + kOffQ) + 4 * qchunk, 16, 512, tc::kSw64);
+      const uint32_t s0 = tc::smem_u32(smem);
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = wg_wait(bar, parity, ctl, a); };
+      auto mma = [&](uint32_t d, uint64_t k, uint64_t n, bool accumulate) {
+        if (PAIR) tc::mma_f8_pair(d, k, n, idesc, accumulate);
+        else tc::mma_e4m3(d, k, n, idesc, accumulate);
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (PAIR) tc::mma_commit_pair(bar);
+        else tc::mma_commit(bar);
+      };
+      while (ok && w.next(a)) {
+        for (int i = 0; ok && i < a.blocks; ++i) {
+          if (!w.has_q(i) && !wait(&ctl->q_full, x++ & 1)) break;
+          for (int t = 0; t < w.tiles; ++t, ++g) {
+            const int st = g % kStages, bf = g % C::kBufs;
+            if (!wait(&ctl->kv_full[st], (g / kStages) & 1)) break;
+            if (g >= C::kBufs && !wait(&ctl->s_empty[bf], (g / C::kBufs - 1) & 1)) break;
+            tc::fence_after_sync();
+            const uint64_t k = tc::smem_desc(s0 + st * kStageBytes, 16, 1024, tc::kSw128);
+            const uint64_t kr = tc::smem_desc(s0 + st * kStageBytes + 4 * kChunk, 16, 512, tc::kSw64);
+            const uint32_t d = tmem + bf * C::kMaxRows;
+            if (one) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+              for (int c = 0; c < 4; ++c)
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma(d, k + ((c * kChunk + kk * 32) >> 4), q + ((c * qchunk + kk * 32) >> 4), c + kk != 0);
+                for (int kk = 0; kk < 4; ++kk)
+                  mma(d, k + ((c * kChunk + kk * 32) >> 4), q + ((c * qchunk + kk * 32) >> 4), c + kk != 0);
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) mma(d, kr + (kk * 32 >> 4), qr + (kk * 32 >> 4), true);
-            commit(&ctl->s_full[bf]);
-            commit(&ctl->kv_empty[st]);
-            if (t == w.tiles - 1 && !w.keeps_q(a, i)) commit(&ctl->q_empty);
+              for (int kk = 0; kk < 2; ++kk) mma(d, kr + (kk * 32 >> 4), qr + (kk * 32 >> 4), true);
+              commit(&ctl->s_full[bf]);
+              commit(&ctl->kv_empty[st]);
+              if (t == w.tiles - 1 && !w.keeps_q(a, i)) commit(&ctl->q_empty);
+            }
           }
         }
+        ok = __all_sync(0xffffffffu, ok);
       }
-      ok = __all_sync(0xffffffffu, ok);
-    }
-    if (one) {
-      commit(&ctl->drain);                       // every MMA done before TMEM is released
-      const unsigned long long t0 = tc::globaltimer_ns();
-      while (!tc::mbar_try_wait(&ctl->drain, 0) && tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
+      if (one) {
+        commit(&ctl->drain);                       // every MMA done before TMEM is released
+        const unsigned long long t0 = tc::globaltimer_ns();
+        while (!tc::mbar_try_wait(&ctl->drain, 0) && tc::globaltimer_ns() - t0 < a.wait_limit_ns) {
+        }
       }
-    }
     }
   } else {
     // Sums: thread (quarter, lane) owns a key, the two groups the two halves of a block's rows.
@@ -511,7 +519,8 @@ int32_t weigh_impl(const mla_cache_shape* s, const void* q, const void* kv,
   a.M = s->k * s->H;
   a.max_pages = s->max_pages;
   a.num_pages = s->num_pages;
-  // Pairs of CTAs beyond 128 rows. Blocks of equal size, as few as hold the rows.
+  // Pairs of CTAs beyond 128 rows (448: 94 us by single CTAs, 69 by pairs; 256: 103 and 74; but 56 rows
+  // 30.7 us by single ones, 31.5 by pairs). Blocks of equal size, as few as hold the rows.
   const bool pair = a.M > kMine && sms >= 2;
   const int most_rows = pair ? 2 * kMine : kMine;
   a.blocks = (int)cdiv(a.M, most_rows);
