@@ -23,8 +23,9 @@ table of angles both read; ``PrefixMla(...)`` decodes a batch whose requests
 share a prefix, reading the prefix's keys once for all of them.
 
 Before the cache: ``prompt_attention(...)`` over whole packed prompts, or chunks of
-them, in the expanded form. To bound the cache: ``kv_weigh(...)`` adds up the attention weight of every cached
-key after a decode, ``kv_evict(...)`` keeps the keys of most weight.
+them, in the expanded form. To bound the cache: ``kv_weigh(...)`` adds up the attention
+weight of every cached key after a decode, ``kv_evict(...)`` keeps the keys of most
+weight.
 """
 from __future__ import annotations
 

@@ -16,7 +16,7 @@
 // runs, one per CTA or pair: keys need no joining, so a cut costs nothing.
 //
 // Measured (graph replays): 64 requests of up to 8k keys, 56 rows, 30.7 us, 5.2 TB/s; 16 of 16k to
-// 64k, 256 rows, 74 us, 5.2 TB/s and 2,610 TFLOP/s; 128 of up to 4k, 448 rows, 68.7 us, 2,210
+// 64k, 256 rows, 74 us, 5.2 TB/s and 2,610 TFLOP/s; 128 of up to 4k, 448 rows, 67 us, 2,270
 // TFLOP/s of FP8; two short ones 5.5 us. What is left at many rows is the pipe's wait for keys and
 // queries at the change of a block: shared memory has room for two tiles beside the queries.
 // Dropped: tiles in bands of 128 dims, refilled as they are multiplied (69.6 -> 76.7 us), the queries
@@ -50,7 +50,7 @@ struct Cfg {
   static constexpr int kCtas = PAIR ? 2 : 1;
   static constexpr int kMaxRows = kCtas * kMine;     // rows of a block: the MMA's N
   static constexpr int kBufs = kTmemCols / kMaxRows; // score buffers in TMEM
-  // Tiles that a row block goes over, at least (groups of 2: 256 rows 78 us, of 6 and more 74).
+  // Tiles that a row block goes over, single CTAs': at least (256 rows: groups of 2 78 us, of 6 74).
   static constexpr int kRun = PAIR ? 6 : 8;
 };
 // MMAs wait on the first CTA's barriers of a pair, and arrive on both CTAs'.
@@ -519,15 +519,17 @@ int32_t weigh_impl(const mla_cache_shape* s, const void* q, const void* kv,
   a.M = s->k * s->H;
   a.max_pages = s->max_pages;
   a.num_pages = s->num_pages;
-  // Pairs of CTAs beyond 128 rows (448: 94 us by single CTAs, 69 by pairs; 256: 103 and 74; but 56 rows
+  // Pairs of CTAs beyond 128 rows (448: 94 us by single CTAs, 67 by pairs; 256: 103 and 74; but 56 rows
   // 30.7 us by single ones, 31.5 by pairs). Blocks of equal size, as few as hold the rows.
   const bool pair = a.M > kMine && sms >= 2;
   const int most_rows = pair ? 2 * kMine : kMine;
   a.blocks = (int)cdiv(a.M, most_rows);
   a.rows = (int)cdiv(cdiv(a.M, a.blocks), 32) * 32;
-  const int spare = (kMine - a.rows / (pair ? 2 : 1)) * kDqk / (2 * kTile * 4);
-  a.run = (pair ? Cfg<true>::kRun : Cfg<false>::kRun) + spare;
-  if (a.run > kMostRun) a.run = kMostRun;
+  // Groups of tiles: without a second block as long as there is room for their sums. With one no longer
+  // than L2 keeps for it (76 pairs' groups of 6 are 67 MB; 32 x 7 x 64 on 16k keys: 78.9 us, of 10 83.3,
+  // of 3 81.6).
+  const int spare = (kMine - a.rows) * kDqk / (2 * kTile * 4), room = Cfg<false>::kRun + spare;
+  a.run = pair ? Cfg<true>::kRun : room < kMostRun ? room : kMostRun;
   a.wait_limit_ns = wait_limit_ns;
   a.withhold = withhold;
   CUtensorMap tkv, tkvr, tq, tqr;
