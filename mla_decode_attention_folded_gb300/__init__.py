@@ -638,8 +638,8 @@ def kv_weigh(q, kv, block_table, seq_lens, lse, bmm1_scale: float, weights, star
                          rope_starts, status)
     _lib.check("mla_kv_weigh", _lib.load().mla_kv_weigh(
         ctypes.byref(shape), q.data_ptr(), kv.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
-        lse.data_ptr(), float(bmm1_scale), float(decay), starts.data_ptr(), _ptr(rope_starts), weights.data_ptr(),
-        _ptr(positions), _ptr(status), _stream_on(dev, stream)))
+        lse.data_ptr(), float(bmm1_scale), float(decay), starts.data_ptr(), _ptr(rope_starts),
+        weights.data_ptr(), _ptr(positions), _ptr(status), _stream_on(dev, stream)))
 
 
 def _weigh_shape(dev, q, kv, block_table, seq_lens, lse, weights, starts, positions, rope_starts,

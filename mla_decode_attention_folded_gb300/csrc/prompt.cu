@@ -108,6 +108,7 @@ struct PromptCtl {
   uint64_t claim_full[2], claim_empty[2];   // first CTA -> second: claimed items; and back
   uint64_t drain[2];
   Piece job[2];
+  Piece staged;                  // the loading warp's: the next one
   long long claim[2];
   float row[2][kMine];           // [half][row]: what the two threads of a row tell one another
   // Values that are no numbers (below): by piece and dim, (piece + 1, ~ the first such key). Four
@@ -269,18 +270,7 @@ __device__ __forceinline__ bool pr_wait_pair(uint64_t* bar, uint32_t parity, Pro
 __device__ __forceinline__ bool take(PromptCtl* ctl, uint32_t seq, const PromptArgs& a, Piece& p, bool read) {
   const int b = seq & 1;
   if (!__all_sync(0xffffffffu, pr_wait(&ctl->job_full[b], (seq >> 1) & 1, ctl, a))) return false;
-  const volatile Piece* s = &ctl->job[b];
-  p.row0 = s->row0;
-  p.rows = s->rows;
-  p.head = s->head;
-  p.key0 = s->key0;
-  p.m = s->m;
-  p.lim0 = s->lim0;
-  p.t0 = s->t0;
-  p.t1 = s->t1;
-  p.slot = s->slot;
-  p.causal = s->causal;
-  p.twin = s->twin;
+  p = ctl->job[b];
   __syncwarp();
   if (read) tc::mbar_arrive(&ctl->job_empty[b]);
   return p.rows > 0;
@@ -435,46 +425,54 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
       // So far: pieces, tiles, queries of the halves, claims.
       uint32_t seq = 0, n = 0, xq0 = 0, xq1 = 0, claims = 0;
       bool ok = true;
-      auto wait0 = [&](uint64_t* bar, uint32_t parity) {
-        int v = 1;
-        if (lane == 0) v = pr_wait(bar, parity, ctl, a) ? 1 : 0;
-        return __shfl_sync(0xffffffffu, v, 0) != 0;
-      };
       const int pair = blockIdx.x >> 1;
       const bool withheld = a.withhold && blockIdx.x == 0;
       if (rank == 0 && lane == 0) a.joins[pair].rows = 0;
-      // The plan: read, or made here with a request to a lane.
-      Request mine = {0, 0, false};
-      int my_row0 = 0, my_key0 = 0, parts;
-      long long my_place = 0, my_item = 0, total, all, len;
+      // The plan: read, or made here with a request to a lane (and made again for each piece, so that
+      // it takes no registers meanwhile).
+      struct Lane {
+        Request q;
+        int row0, key0;
+        long long place, item, total, all;       // before this lane's; of all
+      };
+      auto lanes_plan = [&](Lane& l, bool report) {
+        l.q = {0, 0, false};
+        l.row0 = l.key0 = 0;
+        l.place = l.item = 0;
+        if (lane < a.R) {
+          bool good;
+          l.q = request(a, lane, l.row0, l.key0, good);
+          if (report && !good && a.status && blockIdx.x == 0) atomicOr(a.status, MLA_FAULT_WORK_ITEM);
+          l.place = places(l.q) * units(l.q, a.H, a.twins);
+          l.item = (long long)items(l.q) * units(l.q, a.H, a.twins);
+        }
+        const long long w = l.place, it = l.item;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long u = __shfl_up_sync(0xffffffffu, l.place, o);
+          const long long v = __shfl_up_sync(0xffffffffu, l.item, o);
+          if (lane >= o) l.place += u, l.item += v;
+        }
+        l.total = __shfl_sync(0xffffffffu, l.place, 31);
+        l.all = __shfl_sync(0xffffffffu, l.item, 31);
+        l.place -= w;
+        l.item -= it;
+      };
+      Lane plan;
+      int parts;
+      long long total, all, len;
       if (a.planned) {
         total = a.plan->total;
         all = a.plan->all_items;
         parts = a.plan->parts;
         len = a.plan->len;
       } else {
-        int longest = 0;
-        if (lane < a.R) {
-          bool good;
-          mine = request(a, lane, my_row0, my_key0, good);
-          if (!good && a.status && blockIdx.x == 0) atomicOr(a.status, MLA_FAULT_WORK_ITEM);
-          const int I = items(mine);
-          my_place = places(mine) * units(mine, a.H, a.twins);
-          my_item = (long long)I * units(mine, a.H, a.twins);
-          if (I) longest = max(item_tiles(mine, I - 1), I > 1 ? item_tiles(mine, I - 2) : 0);
-        }
-        longest = __reduce_max_sync(0xffffffffu, longest);
-        const long long w = my_place, it = my_item;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long u = __shfl_up_sync(0xffffffffu, my_place, o);
-          const long long v = __shfl_up_sync(0xffffffffu, my_item, o);
-          if (lane >= o) my_place += u, my_item += v;
-        }
-        total = __shfl_sync(0xffffffffu, my_place, 31);
-        all = __shfl_sync(0xffffffffu, my_item, 31);
-        my_place -= w;
-        my_item -= it;
+        lanes_plan(plan, true);
+        const int I = items(plan.q);
+        const int longest = __reduce_max_sync(
+            0xffffffffu, I ? max(item_tiles(plan.q, I - 1), I > 1 ? item_tiles(plan.q, I - 2) : 0) : 0);
+        total = plan.total;
+        all = plan.all;
         const uint32_t t = (uint32_t)total;
         parts = 0;
         len = 0;
@@ -491,8 +489,14 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
         at = pair < parts ? part_at(total, len, pair) : 0;
         end = pair < parts ? part_at(total, len, pair + 1) : 0;
       }
+      // Queries are loaded as soon as their half's last S of the piece before is done, whatever else
+      // the warp waits for: this piece's, then the next one's. All that is lane 0's.
+      struct Load {
+        int head, row, due;                      // due: bit h: half h's; bit 2: a head for each half
+      } cur = {0, 0, 0}, nxt = {0, 0, 0};
       // The piece at `at`, none (no rows) at the end; moves `at` on.
-      auto next = [&](Piece& p) {
+      auto next = [&](auto first_one) {
+        Piece p;
         p.rows = 0;
         while (parts > 0 ? at < end : at < all) {
           int row0, u;
@@ -505,13 +509,14 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
             q = request(a, r, row0, p.key0, good);
             x = at - first[r];
           } else {
-            const long long first = parts > 0 ? my_place : my_item;
+            if (!decltype(first_one)::value) lanes_plan(plan, false);
+            const long long first = parts > 0 ? plan.place : plan.item;
             const int r = 31 - __clz(__ballot_sync(0xffffffffu, lane < a.R && first <= at) | 1);
-            q.n = __shfl_sync(0xffffffffu, mine.n, r);
-            q.m = __shfl_sync(0xffffffffu, mine.m, r);
+            q.n = __shfl_sync(0xffffffffu, plan.q.n, r);
+            q.m = __shfl_sync(0xffffffffu, plan.q.m, r);
             q.causal = a.causal;
-            row0 = __shfl_sync(0xffffffffu, my_row0, r);
-            p.key0 = __shfl_sync(0xffffffffu, my_key0, r);
+            row0 = __shfl_sync(0xffffffffu, plan.row0, r);
+            p.key0 = __shfl_sync(0xffffffffu, plan.key0, r);
             x = at - __shfl_sync(0xffffffffu, first, r);
           }
           p.t0 = 0;
@@ -556,6 +561,13 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
           p.lim0 = u * kRows + 1 + q.m - q.n;
           break;
         }
+        // It waits in shared memory; what its queries need is kept at hand.
+        if (lane == 0) ctl->staged = p;
+        Load l = {p.head, p.row0 + (int)rank * kMine, 0};
+        if (p.rows > 0) l.due = (half_tiles(p, 0) > 0) | (half_tiles(p, 1) > 0) << 1 | (p.twin > 0) << 2;
+        if (decltype(first_one)::value) cur = l;
+        else nxt = l;
+        __syncwarp();
         if (parts > 0 || p.rows == 0) return;
         if (!a.planned) {
           at += gridDim.x >> 1;
@@ -590,11 +602,6 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
         at = __shfl_sync(0xffffffffu, at, 0);
         ok = __shfl_sync(0xffffffffu, got, 0) != 0;
       };
-      // Queries are loaded as soon as their half's last S of the piece before is done, whatever else
-      // the warp waits for: this piece's, then the next one's. All that is lane 0's.
-      struct Load {
-        int head, row, due;                      // due: bit h: half h's; bit 2: a head for each half
-      } cur = {0, 0, 0}, nxt = {0, 0, 0};
       auto load_q = [&](int h, uint32_t& x) {
         const bool now = cur.due >> h & 1;
         if (!now && !(nxt.due >> h & 1)) return;
@@ -637,29 +644,14 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
         }
         return __shfl_sync(0xffffffffu, v, 0) != 0;
       };
-      auto queries = [&](const Piece& p, Load& l) {
-        l = {p.head, p.row0 + (int)rank * kMine, 0};
-        if (p.rows > 0) l.due = (half_tiles(p, 0) > 0) | (half_tiles(p, 1) > 0) << 1 | (p.twin > 0) << 2;
-      };
-      Piece p;
-      next(p);
-      queries(p, cur);
+      next(std::true_type{});
       while (ok) {
         // Hand it on, or an empty one at the end.
         if (seq >= 2 && !(ok = wait_ring(&ctl->job_empty[seq & 1], ((seq >> 1) - 1) & 1))) break;
+        const Piece p = ctl->staged;
+        __syncwarp();
         if (lane == 0) {
-          volatile Piece* s = &ctl->job[seq & 1];
-          s->row0 = p.row0;
-          s->rows = p.rows;
-          s->head = p.head;
-          s->key0 = p.key0;
-          s->m = p.m;
-          s->lim0 = p.lim0;
-          s->t0 = p.t0;
-          s->t1 = p.t1;
-          s->slot = p.slot;
-          s->causal = p.causal;
-          s->twin = p.twin;
+          ctl->job[seq & 1] = p;
           tc::mbar_arrive(&ctl->job_full[seq & 1]);
         }
         if (p.rows == 0) break;
@@ -668,40 +660,33 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
         const int two = p.twin == 2, nt = max(half_tiles(p, 0), half_tiles(p, 1)) << two;
         const int kvh0 = p.head / a.group, kvh1 = two ? (p.head + 1) / a.group : kvh0;
         const int key0 = p.key0 + p.t0 * kKeys;
-        bool ahead = false;
 #pragma unroll 1
-        for (int t = 0; t < nt; ++t, ++n) {
-          const int st = n % kStages, key = key0 + (t >> two) * kKeys, kvh = t & two ? kvh1 : kvh0;
-          if (n >= kStages && !(ok = wait_ring(&ctl->k_empty[st], (n / kStages - 1) & 1))) break;
-          if (lane == 0 && !(withheld && n == 0)) {
-            const uint32_t bar = tc::map_rank(&ctl->k_full[st], 0);
-            uint8_t* dst = smem + kOffK + st * kKBytes;
-            const int mine = key + (int)rank * 64;
-            tc::remote_arrive_expect_tx(bar, kKBytes);
-            tma_load_3d_pair(dst, &tm_k, bar, 0, kvh, mine);
-            tma_load_3d_pair(dst + kKBlock, &tm_k, bar, 128, kvh, mine);
-            tc::tma_load_2d_pair(dst + 2 * kKBlock, &tm_r, bar, 0, mine);
-          }
-          if (lane == 0) load_queries();
-          if (n >= kStages && !(ok = wait_ring(&ctl->v_empty[st], (n / kStages - 1) & 1))) break;
-          if (lane == 0) {
-            tc::mbar_arrive_expect_tx(&ctl->v_land[st], kVBytes);
-            tc::tma_load_3d(smem + kOffV + st * kVBytes, &tm_v, &ctl->v_land[st], (int)rank * 128, kvh, key);
+        for (int t = 0; t < nt || t < kStages; ++t) {
+          if (t < nt) {
+            const int st = n % kStages, key = key0 + (t >> two) * kKeys, kvh = t & two ? kvh1 : kvh0;
+            if (n >= kStages && !(ok = wait_ring(&ctl->k_empty[st], (n / kStages - 1) & 1))) break;
+            if (lane == 0 && !(withheld && n == 0)) {
+              const uint32_t bar = tc::map_rank(&ctl->k_full[st], 0);
+              uint8_t* dst = smem + kOffK + st * kKBytes;
+              const int mine = key + (int)rank * 64;
+              tc::remote_arrive_expect_tx(bar, kKBytes);
+              tma_load_3d_pair(dst, &tm_k, bar, 0, kvh, mine);
+              tma_load_3d_pair(dst + kKBlock, &tm_k, bar, 128, kvh, mine);
+              tc::tma_load_2d_pair(dst + 2 * kKBlock, &tm_r, bar, 0, mine);
+            }
+            if (lane == 0) load_queries();
+            if (n >= kStages && !(ok = wait_ring(&ctl->v_empty[st], (n / kStages - 1) & 1))) break;
+            if (lane == 0) {
+              tc::mbar_arrive_expect_tx(&ctl->v_land[st], kVBytes);
+              tc::tma_load_3d(smem + kOffV + st * kVBytes, &tm_v, &ctl->v_land[st], (int)rank * 128, kvh, key);
+            }
+            ++n;
           }
           // The next piece is looked up while this one's tiles are multiplied.
           if (t == kStages - 1) {
-            next(p);
-            queries(p, nxt);
-            ahead = true;
-            if (!ok) {
-              ++n;                                 // loaded
-              break;
-            }
+            next(std::false_type{});
+            if (!ok) break;
           }
-        }
-        if (ok && !ahead) {
-          next(p);
-          queries(p, nxt);
         }
         if (!ok || !(ok = wait_ring(nullptr, 0))) break;
         cur = nxt;
