@@ -24,19 +24,21 @@
 // each (1172 -> 1130 us). The maximum that P is relative to moves only when a score exceeds it by
 // 2^8 (O and the sum are then rescaled), so that the two threads need no more than a barrier's vote
 // in most tiles; P is rounded to BF16 (2^-8, as the inputs are), its sum is of the FP32 values.
-// Registers are what the softmax is short of (96 a thread): what it spills costs more than anything
-// else here, so it keeps little of a piece and rescales O eight columns at a time.
+// Registers are short (96 a thread): a few words that the loading warp or a softmax thread spills cost 1
+// to 5 %. So the loading warp makes its plan again for each piece and leaves the next one in shared
+// memory, the softmax keeps little of a piece and rescales O eight columns at a time.
 //
 // How the work is shared out is in prompt.h. The order of a half's MMAs is PV(t) before S(t + 1),
 // so that S may overwrite P and its completion tells that O is final.
 //
-// Measured (graph replays): 64 heads of 8,192 tokens 930 us, 1,480 TFLOP/s (the pipe's peak in a
+// Measured (graph replays): 64 heads of 8,192 tokens 923 us, 1,490 TFLOP/s (the pipe's peak in a
 // burst is 1,874, and 1,690 under the power cap); 4 x 32 heads of 900 to 1,500 tokens, grouped,
-// without a mask 118 us, 1,030 TFLOP/s; 24 prompts of up to 2,048 tokens and 8 heads 123 us, 715;
-// 512 tokens on 16k keys, 8 heads 45 us, 940; two short prompts 8.5 us.
+// without a mask 117 us, 1,040 TFLOP/s; 24 prompts of up to 2,048 tokens and 8 heads 122.5 us, 715;
+// 512 tokens on 16k keys, 8 heads 43.5 us, 970; two short prompts 8.5 us.
 // Dropped: V given back after S (1130 -> 1258 us); the MMAs' lock before the wait for P (912 -> 963);
 // weights made while the vote on the maximum runs (935 -> 1016); masks per 32 columns (spills, 916
-// -> 1173); registers moved from the four first warps to the softmax (24 prompts 128 -> 136 us).
+// -> 1173); registers moved from the four first warps to the softmax (24 prompts 128 -> 136 us, again
+// 122 -> 135 at the end); votes by the two warps that share rows instead of a half's eight (equal).
 #include <cmath>
 #include <type_traits>
 
