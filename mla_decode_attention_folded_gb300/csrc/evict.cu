@@ -16,8 +16,8 @@
 // idle, a second launch makes them on all.
 //
 // Measured (graph replays): 128 requests drop 7 of 2,055 keys in 10.5 us, nearly all of it the
-// select's chain of dependent steps; 8 x 20k to 32k keys to 4k in 25 us (1.4 TB/s of what has to
-// move), 128k keys to 64k in 31 us (1.3 TB/s): the walks over the keys and the scattered rows.
+// select's chain of dependent steps; 8 x 20k to 32k keys to 4k in 23.8 us (1.5 TB/s of what has to
+// move), 128k keys to 64k in 29.5 us (1.35 TB/s): the walks over the keys and the scattered rows.
 #include <climits>
 
 #include "checks.h"
@@ -102,7 +102,7 @@ __device__ __forceinline__ void st_rank(void* p, int rank, uint32_t v) {
 }
 
 struct Shared {
-  uint32_t hist[3][kBins];       // the first CTA's: of the cluster
+  alignas(8) uint32_t hist[3][kBins];       // the first CTA's: of the cluster
   unsigned long long sums[kWarps];
   uint32_t digit[3];             // what holds the wanted place, the places left in it, its codes
   int top;                       // newest position of this CTA's keys
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictAr
   extern __shared__ uint32_t codes[];            // this CTA's codes, where they fit
   __shared__ Shared sh;
   const int rank = a.cluster > 1 ? (int)tc::cluster_rank() : 0;
-  const int r = blockIdx.x / a.cluster, tid = threadIdx.x;
+  const int r = blockIdx.x / a.cluster, tid = threadIdx.x, lane = tid & 31;
   for (int i = tid; i < 3 * kBins; i += kThreads) sh.hist[i / kBins][i % kBins] = 0;
   if (tid == 0) sh.top = INT_MIN;
   grid_dep_wait();
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictAr
         mine = max(mine, pos);
       }
       mine = __reduce_max_sync(0xffffffffu, mine);
-      if ((tid & 31) == 0) atomicMax(&sh.top, mine);
+      if (lane == 0) atomicMax(&sh.top, mine);
       __syncthreads();
       top = sh.top;
       if (a.cluster > 1) {
@@ -257,15 +257,13 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictAr
       const int hi = kBins - 2 - 2 * tid;        // this thread's two digits: this and the next
       if (a.cluster > 1) {
         __syncthreads();
-        if (rank > 0) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-            if (const uint32_t v = sh.hist[pass][hi + u])
-              asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(
-                               tc::map_rank(&sh.hist[pass][hi + u], 0)),
-                           "r"(v)
-                           : "memory");
-        }
+        // Both digits in one addition: no count reaches 2^32.
+        if (rank > 0)
+          if (const unsigned long long v = *reinterpret_cast<const unsigned long long*>(&sh.hist[pass][hi]))
+            asm volatile("red.relaxed.cluster.shared::cluster.add.u64 [%0], %1;" ::"r"(
+                             tc::map_rank(&sh.hist[pass][hi], 0)),
+                         "l"(v)
+                         : "memory");
       }
       join(a.cluster);
       // Digits from the largest down; the first CTA finds the one and tells the others.
@@ -273,14 +271,21 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictAr
         const uint32_t h0 = sh.hist[pass][hi + 1], h1 = sh.hist[pass][hi];
         unsigned long long total;
         const uint32_t above = (uint32_t)scan(h0 + h1, sh.sums, total);
-        if (above < want && want <= above + h0 + h1) {
-          const bool second = above + h0 < want;
-          const uint32_t at[3] = {(uint32_t)(hi + (second ? 0 : 1)), want - above - (second ? h0 : 0),
-                                  second ? h1 : h0};
+        const bool here = above < want && want <= above + h0 + h1, second = above + h0 < want;
+        const uint32_t at[3] = {(uint32_t)(hi + (second ? 0 : 1)), want - above - (second ? h0 : 0),
+                                second ? h1 : h0};
+        if (a.cluster == 1) {
+          if (here) {
+#pragma unroll
+            for (int u = 0; u < 3; ++u) sh.digit[u] = at[u];
+          }
+        } else if (const unsigned m = __ballot_sync(0xffffffffu, here)) {
+          // Its warp tells the cluster, a CTA each lane (128k keys: 31.0 us by its thread alone, 29.5).
 #pragma unroll
           for (int u = 0; u < 3; ++u) {
-            sh.digit[u] = at[u];
-            for (int c = 1; c < a.cluster; ++c) st_rank(&sh.digit[u], c, at[u]);
+            const uint32_t v = __shfl_sync(0xffffffffu, at[u], __ffs(m) - 1);
+            if (lane == 0) sh.digit[u] = v;
+            else if (lane < a.cluster) st_rank(&sh.digit[u], lane, v);
           }
         }
       }
