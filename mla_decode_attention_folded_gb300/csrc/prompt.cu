@@ -23,7 +23,8 @@
 // request's last key; eight warps each are the softmax of the halves: two threads to a row, 64 keys
 // each (1172 -> 1130 us). The maximum that P is relative to moves only when a score exceeds it by
 // 2^8 (O and the sum are then rescaled), so that the two threads need no more than a barrier's vote
-// in most tiles; P is rounded to BF16 (2^-8, as the inputs are), its sum is of the FP32 values.
+// in most tiles; P leaves in two halves, the first multiplied while the second is made (117 -> 112 us for
+// the grouped prompts below); P is rounded to BF16 (2^-8, as the inputs are), its sum is of the FP32 values.
 // Registers are short (96 a thread): a few words that the loading warp or a softmax thread spills cost 1
 // to 5 %. So the loading warp makes its plan again for each piece and leaves the next one in shared
 // memory, the softmax keeps little of a piece and rescales O eight columns at a time.
@@ -31,10 +32,10 @@
 // How the work is shared out is in prompt.h. The order of a half's MMAs is PV(t) before S(t + 1),
 // so that S may overwrite P and its completion tells that O is final.
 //
-// Measured (graph replays): 64 heads of 8,192 tokens 923 us, 1,490 TFLOP/s (the pipe's peak in a
+// Measured (graph replays): 64 heads of 8,192 tokens 905 us, 1,520 TFLOP/s (the pipe's peak in a
 // burst is 1,874, and 1,690 under the power cap); 4 x 32 heads of 900 to 1,500 tokens, grouped,
-// without a mask 117 us, 1,040 TFLOP/s; 24 prompts of up to 2,048 tokens and 8 heads 122.5 us, 715;
-// 512 tokens on 16k keys, 8 heads 43.5 us, 970; two short prompts 8.5 us.
+// without a mask 112 us, 1,090 TFLOP/s; 24 prompts of up to 2,048 tokens and 8 heads 122 us, 720;
+// 512 tokens on 16k keys, 8 heads 42.2 us, 1,000; two short prompts 8.5 us.
 // Dropped: V given back after S (1130 -> 1258 us); the MMAs' lock before the wait for P (912 -> 963);
 // weights made while the vote on the maximum runs (935 -> 1016); masks per 32 columns (spills, 916
 // -> 1173); registers moved from the four first warps to the softmax (24 prompts 128 -> 136 us, again
@@ -105,7 +106,7 @@ struct PromptCtl {
   uint64_t k_full[kStages], k_empty[kStages];
   uint64_t v_land[kStages];      // this CTA's copies of V
   uint64_t v_full[kStages], v_empty[kStages];
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], p_half[2], p_full[2], o_full[2];
   uint64_t job_full[2], job_empty[2];
   uint64_t claim_full[2], claim_empty[2];   // first CTA -> second: claimed items; and back
   uint64_t drain[2];
@@ -385,6 +386,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
       tc::mbar_init(&ctl->q_full[i], 2);
       tc::mbar_init(&ctl->q_empty[i], 1);
       tc::mbar_init(&ctl->s_full[i], 1);
+      tc::mbar_init(&ctl->p_half[i], 2 * kSoft / 32);
       tc::mbar_init(&ctl->p_full[i], 2 * kSoft / 32);
       tc::mbar_init(&ctl->o_full[i], 1);
       tc::mbar_init(&ctl->job_full[i], 1);
@@ -743,6 +745,8 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
           const int c = __shfl_sync(0xffffffffu, half_tiles(p, h), 0);
           const int two = __shfl_sync(0xffffffffu, p.twin == 2, 0);
           const uint32_t nt = max(c, __shfl_sync(0xffffffffu, half_tiles(p, h ^ 1), 0)) << two;
+          // No lane leaves the loop from where only one works, and none waits for the others in it: where a
+          // wait runs out they meet behind it.
           // PV of tile t, then S of tile t + 1, under a lock: issued as they come, the halves' MMAs would
           // mingle, both finish late, and both softmaxes then run while the tensor pipe waits. What
           // the copies bring is waited for before P, where it is there by then, so that nothing
@@ -761,15 +765,25 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
               if (two && has_k && t + 1 >= 1 - h && !give(ctl->k_full, ctl->k_empty, nk - 1)) break;
               const bool landed = has_k && tc::mbar_test_wait(&ctl->k_full[sk], (nk / kStages) & 1);
               if (t >= 0) {
+                // P in two halves of each side's keys: the first is multiplied while the second is made.
+                const uint64_t v = tc::smem_desc(s_v + sv * kVBytes, kBlock, 1024, tc::kSw128);
+                auto pv = [&](int part) {
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const int kk = (i >> 1) * 4 + part * 2 + (i & 1);
+                    mma_bf16_ts_pair(col_o, col_s + (kk >> 2) * 64 + (kk & 3) * 8, v + (kk * 16 * 128 >> 4),
+                                     kIdescO, t + part + i != 0);
+                  }
+                };
+                if (!wait(&ctl->p_half[h], xp & 1)) break;
+                if (one && (ok = lock(ctl, a))) {
+                  tc::fence_after_sync();
+                  pv(0);
+                }
                 if (!wait(&ctl->p_full[h], xp++ & 1)) break;
                 if (one) {
-                  if (!(ok = lock(ctl, a))) break;
                   tc::fence_after_sync();
-                  const uint64_t v = tc::smem_desc(s_v + sv * kVBytes, kBlock, 1024, tc::kSw128);
-#pragma unroll
-                  for (int kk = 0; kk < kKeys / 16; ++kk)
-                    mma_bf16_ts_pair(col_o, col_s + (kk >> 2) * 64 + (kk & 3) * 8, v + (kk * 16 * 128 >> 4),
-                                     kIdescO, t + kk != 0);
+                  pv(1);
                   tc::mma_commit_pair(&ctl->v_empty[sv]);
                   if (t == c - 1) tc::mma_commit_pair(&ctl->o_full[h]);
                   if (!landed) unlock(ctl);
@@ -777,8 +791,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
               }
               if (has_k) {
                 if (!landed && !wait(&ctl->k_full[sk], (nk / kStages) & 1)) break;
-                if (one) {
-                  if ((t < 0 || !landed) && !(ok = lock(ctl, a))) break;
+                if (one && ((t >= 0 && landed) || (ok = lock(ctl, a)))) {
                   tc::fence_after_sync();
                   const uint64_t k = tc::smem_desc(s_k + sk * kKBytes, 16, 1024, tc::kSw128);
 #pragma unroll
@@ -877,7 +890,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
     // all meet at its barriers, and leave together.
     const int h = (warp - 4) >> 3, side = (warp - 4) >> 2 & 1, quarter = warp & 3, row = quarter * 32 + lane;
     const int in_half = (int)rank * kMine + row, j = h * kHalf + in_half;   // j: row of a slot
-    const uint32_t p_full = tc::map_rank(&ctl->p_full[h], 0);
+    const uint32_t p_half = tc::map_rank(&ctl->p_half[h], 0), p_full = tc::map_rank(&ctl->p_full[h], 0);
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t col_s = lanes + h * kKeys + side * 64;
     const uint32_t col_o = col_s + kColO;
@@ -958,14 +971,15 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
             pk[e] = f32x2_to_bf16x2(x, y);
           }
           tc::tmem_st16(col_s + 16 * i, pk);
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::remote_arrive(i ? p_full : p_half);
+          __syncwarp();                          // the next store to TMEM is the whole warp's
         }
         float s0, s1;
         unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::remote_arrive(p_full);
       }
       // The rows' sums, of both threads.
       if (side) ctl->row[h][row] = l;
@@ -992,6 +1006,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[e] = 0;
         if (c > 0) {
+          __syncwarp();                          // rows that are none have stored nothing
           tc::tmem_ld16(col_o + 16 * i, o);
           tc::tmem_wait_ld();
         }
