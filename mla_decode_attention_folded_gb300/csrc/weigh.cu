@@ -407,7 +407,8 @@ weigh_kernel(const WeighArgs a, const __grid_constant__ CUtensorMap tm_kv,
       for (int b = 0; b < a.blocks; ++b, ++x) {    // the b-th of the group
         if (st < C::kMaxRows) neg[(x & 1) * C::kMaxRows + st] = ahead;
         if (b + 1 < a.blocks) ahead = row_neg(w.r, w.block(a, b + 1));
-        asm volatile("bar.sync 1, %0;" ::"r"(kSum) : "memory");
+        // (Not bar.sync, which a warp's threads have to reach together.)
+        asm volatile("barrier.sync 1, %0;" ::"r"(kSum) : "memory");
         const float* ng = neg + (x & 1) * C::kMaxRows + half * cols;
         for (int t = 0; t < w.tiles; ++t, ++g) {
           const int bf = g % C::kBufs;
@@ -468,7 +469,7 @@ weigh_kernel(const WeighArgs a, const __grid_constant__ CUtensorMap tm_kv,
           a.positions[(size_t)w.r * a.max_pages * kPage + slot] =
               (a.rope_starts ? a.rope_starts[w.r] : new_at) + (slot - new_at);
       }
-      asm volatile("bar.sync 1, %0;" ::"r"(kSum) : "memory");
+      asm volatile("barrier.sync 1, %0;" ::"r"(kSum) : "memory");
     }
   }
   tc::fence_before_sync();
