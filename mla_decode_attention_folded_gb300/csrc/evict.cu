@@ -102,7 +102,7 @@ __device__ __forceinline__ void st_rank(void* p, int rank, uint32_t v) {
 }
 
 struct Shared {
-  alignas(8) uint32_t hist[3][kBins];       // the first CTA's: of the cluster
+  uint32_t hist[3][kBins];       // the first CTA's: of the cluster
   unsigned long long sums[kWarps];
   uint32_t digit[3];             // what holds the wanted place, the places left in it, its codes
   int top;                       // newest position of this CTA's keys
@@ -257,13 +257,17 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictAr
       const int hi = kBins - 2 - 2 * tid;        // this thread's two digits: this and the next
       if (a.cluster > 1) {
         __syncthreads();
-        // Both digits in one addition: no count reaches 2^32.
-        if (rank > 0)
-          if (const unsigned long long v = *reinterpret_cast<const unsigned long long*>(&sh.hist[pass][hi]))
-            asm volatile("red.relaxed.cluster.shared::cluster.add.u64 [%0], %1;" ::"r"(
-                             tc::map_rank(&sh.hist[pass][hi], 0)),
-                         "l"(v)
-                         : "memory");
+        // Added in 32 bits, as the first CTA adds its own codes meanwhile: additions of two widths to the
+        // same words are not atomic to one another.
+        if (rank > 0) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            if (const uint32_t v = sh.hist[pass][hi + u])
+              asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(
+                               tc::map_rank(&sh.hist[pass][hi + u], 0)),
+                           "r"(v)
+                           : "memory");
+        }
       }
       join(a.cluster);
       // Digits from the largest down; the first CTA finds the one and tells the others.
