@@ -514,7 +514,11 @@ int32_t mla_prefix_decode_wait_test(const mla_shape *shape, int32_t prefix_pages
  *
  * Books of a cache: `weights` and `positions`, [R, max_pages * 64], one entry per
  * slot (key j of request r, in page block_table[r][j / 64], has entry j): the weight
- * the key has been given so far and the position of its token. */
+ * the key has been given so far and the position of its token. mla_kv_weigh fills in the
+ * keys that are new with a step. For keys that something else brought (a prompt appended
+ * to the cache) the caller sets both before the first mla_kv_evict: the tokens' positions,
+ * and a weight, 0 or what mla_kv_weigh gives them later. Left at 0, all such positions would
+ * be held as sinks, the lowest slots first. */
 
 /* Shape of mla_kv_weigh and mla_kv_evict. All fields are host values. */
 typedef struct {

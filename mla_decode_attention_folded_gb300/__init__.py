@@ -695,7 +695,8 @@ def kv_evict(kv, block_table, seq_lens, weights, keep, positions=None, recent: i
     [pages, 64, 576]: those of positions below `sinks`, the `recent` newest, then
     those of most weight (ties: the lower slot). Kept keys behind the new length
     move into slots of dropped ones, with their weights and positions
-    [R, max_pages * 64] (positions None: a key's position is its slot). Returns
+    [R, max_pages * 64] (positions None: a key's position is its slot; else the caller
+    has set those of keys that no kv_weigh call counted as new, a prompt's). Returns
     the new lengths [R] int32. weights_out and positions_out may be the inputs, which
     is the default; lens_out may be seq_lens. `workspace`: uint8, at least
     kv_evict_workspace_bytes (None: allocated for the call). See mla_kv_evict in
