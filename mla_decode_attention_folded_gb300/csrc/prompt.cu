@@ -1065,11 +1065,13 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptArgs a) {
   float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0}, z = 0.f;
 #pragma unroll 4
   for (int p = part; p <= last; ++p) {
-    const float w = ex2(a.part_lse[slot(p) * kRows + j] - base);
+    const float l = a.part_lse[slot(p) * kRows + j], w = ex2(l - base);
     const float4* src = reinterpret_cast<const float4*>(a.part_o) + (slot(p) * 32 + quad) * kRows + j;
     float4 v[2] = {src[0], src[16 * kRows]};
     z += w;
-    if (w == 0.f) v[0] = v[1] = make_float4(0, 0, 0, 0);     // nothing there: perhaps not written
+    // A piece of which the row sees nothing is perhaps not written. (One whose weight is too small for
+    // FP32 is, and its NaN counts.)
+    if (l == -INFINITY) v[0] = v[1] = make_float4(0, 0, 0, 0);
     acc[0] += w * v[0].x;
     acc[1] += w * v[0].y;
     acc[2] += w * v[0].z;
