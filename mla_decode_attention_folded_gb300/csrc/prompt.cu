@@ -115,9 +115,10 @@ struct PromptCtl {
   long long claim[2];
   float row[2][kMine];           // [half][row]: what the two threads of a row tell one another
   // Values that are no numbers (below): by piece and dim, (piece + 1, ~ the first such key). Four
-  // pieces' worth: no CTA's softmax is further behind the other's copies.
+  // pieces' worth: who notes them waits until both CTAs' softmaxes have done with the fourth before.
   unsigned long long bad[4][2][kV];   // [][half]
   uint32_t bad_piece[4];         // piece + 1, where there are any
+  uint32_t v_piece;              // the other CTA's: pieces that its V warp has taken
   uint32_t tmem_base;
   uint32_t lock;                 // held by the half whose MMAs are being issued
   int abort_flag;
@@ -269,6 +270,24 @@ __device__ __forceinline__ bool pr_wait_pair(uint64_t* bar, uint32_t parity, Pro
     }
   }
 }
+// Until the other CTA's V warp has taken `pieces` of them.
+__device__ __forceinline__ bool wait_v_piece(PromptCtl* ctl, uint32_t pieces, const PromptArgs& a) {
+  const unsigned long long t0 = tc::globaltimer_ns();
+  while (true) {
+    uint32_t v;
+    asm volatile("ld.acquire.cluster.shared::cta.u32 %0, [%1];"
+                 : "=r"(v)
+                 : "r"(tc::smem_u32(&ctl->v_piece))
+                 : "memory");
+    if (v >= pieces) return true;
+    if (*reinterpret_cast<volatile int*>(&ctl->abort_flag)) return false;
+    if (tc::globaltimer_ns() - t0 > a.wait_limit_ns) {
+      *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
+      if (a.status) atomicOr(a.status, MLA_FAULT_WAIT_TIMEOUT);
+      return false;
+    }
+  }
+}
 // The next piece, for a whole warp; false at the end, or where the wait ran out.
 __device__ __forceinline__ bool take(PromptCtl* ctl, uint32_t seq, const PromptArgs& a, Piece& p, bool read) {
   const int b = seq & 1;
@@ -405,6 +424,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
     ctl->abort_flag = 0;
     ctl->lock = 0;
     for (int i = 0; i < 4; ++i) ctl->bad_piece[i] = 0;
+    ctl->v_piece = 0;
     tc::fence_barrier_init();
     tc::prefetch_tmap(&tm_q);
     tc::prefetch_tmap(&tm_k);
@@ -834,6 +854,13 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
       for (uint32_t seq = 0; ok; ++seq) {
         Piece p;
         if (!take(ctl, seq, a, p, lane == 0)) break;
+        // A piece is handed on once this CTA's softmaxes have taken the one two before it, and so have done
+        // with the one three before it: what the other CTA has to know before it notes anything.
+        if (lane == 0)
+          asm volatile("st.release.cluster.shared::cluster.u32 [%0], %1;" ::"r"(tc::map_rank(&ctl->v_piece, rank ^ 1)),
+                       "r"(seq + 1)
+                       : "memory");
+        __syncwarp();
         const int two = p.twin == 2, c0 = half_tiles(p, 0), nt = max(c0, half_tiles(p, 1)) << two;
 #pragma unroll 1
         for (int t = 0; t < nt; ++t, ++n) {
@@ -854,6 +881,10 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
                      ((x.z & 0x7F807F80u) + 0x00800080u) | ((x.w & 0x7F807F80u) + 0x00800080u);
             }
             if (__any_sync(0xffffffffu, (odd & 0x80008000u) != 0)) {
+              // The notes' place was that of piece seq - 4. This CTA's softmaxes have done with it, as have the
+              // other's once its piece seq - 1 is handed on. (A half without tiles waits for nothing of
+              // the other CTA's, so that one may be pieces behind.)
+              if (!(ok = __all_sync(0xffffffffu, wait_v_piece(ctl, seq, a)))) break;
               const int b = seq & 3;
               for (int i = lane; i < kKeys * 64; i += 32) {
                 uint16_t* x = reinterpret_cast<uint16_t*>(v) + i;
