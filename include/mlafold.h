@@ -596,7 +596,8 @@ int32_t mla_kv_weigh_wait_test(const mla_cache_shape *shape, const void *q, cons
  *                `weights`, else must not overlap it.
  *   positions_out [R, max_pages * 64] int32, device, in the same way (-1 for 0); NULL where
  *                positions is. May be `positions`, else must not overlap it.
- *   lens_out     [R] int32, device: the new lengths. May be seq_lens.
+ *   lens_out     [R] int32, device: the new lengths. May be seq_lens, else must not overlap
+ *                it; must not overlap `keep`. (Requests read theirs in no order.)
  *   workspace    >= mla_kv_evict_workspace_bytes(shape) bytes, device, 256-byte aligned; calls
  *                that share one must not overlap. Its contents need not be initialised.
  *   status       optional int32 device word: MLA_FAULT_PAGE_RANGE (a moved key's page is

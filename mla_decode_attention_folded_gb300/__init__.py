@@ -698,7 +698,8 @@ def kv_evict(kv, block_table, seq_lens, weights, keep, positions=None, recent: i
     [R, max_pages * 64] (positions None: a key's position is its slot; else the caller
     has set those of keys that no kv_weigh call counted as new, a prompt's). Returns
     the new lengths [R] int32. weights_out and positions_out may be the inputs, which
-    is the default; lens_out may be seq_lens. `workspace`: uint8, at least
+    is the default; lens_out may be seq_lens; other overlaps of an output with what it is
+    made from are refused, and any of lens_out with keep. `workspace`: uint8, at least
     kv_evict_workspace_bytes (None: allocated for the call). See mla_kv_evict in
     include/mlafold.h."""
     dev = _device("kv", kv, 3)
@@ -734,6 +735,8 @@ def kv_evict(kv, block_table, seq_lens, weights, keep, positions=None, recent: i
         lens_out = _empty((R,), torch.int32, kv.device, stream)
     else:
         _check(dev, "lens_out", lens_out, _I32, (R,))
+        _apart("lens_out", lens_out, seq_lens)
+        _apart("lens_out", lens_out, keep, same=False)
     if workspace is None:
         workspace = _empty((kv_evict_workspace_bytes(R, max_pages),), torch.uint8, kv.device, stream)
     else:
@@ -752,10 +755,10 @@ def _stream_on(dev: int, stream) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
-def _apart(name: str, t, other) -> None:
-    """`t` is `other` itself, or shares no memory with it (both contiguous)."""
+def _apart(name: str, t, other, same: bool = True) -> None:
+    """`t` is `other` itself (where `same`), or shares no memory with it (both contiguous)."""
     a, b = t.data_ptr(), other.data_ptr()
-    if a != b and a < b + other.numel() * other.element_size() and \
+    if not (same and a == b) and a < b + other.numel() * other.element_size() and \
             b < a + t.numel() * t.element_size():
         raise ValueError(f"{name} overlaps its input")
 
