@@ -731,6 +731,9 @@ def kv_evict(kv, block_table, seq_lens, weights, keep, positions=None, recent: i
         raise ValueError("positions_out without positions")
     if status is not None:
         _check(dev, "status", status, _I32, (1,))
+    recent, sinks = int(recent), int(sinks)
+    if not (-2 ** 31 <= recent < 2 ** 31 and -2 ** 31 <= sinks < 2 ** 31):
+        raise ValueError(f"recent {recent} or sinks {sinks} is no int32")
     if lens_out is None:
         lens_out = _empty((R,), torch.int32, kv.device, stream)
     else:
@@ -744,7 +747,7 @@ def kv_evict(kv, block_table, seq_lens, weights, keep, positions=None, recent: i
     _lib.check("mla_kv_evict", _lib.load().mla_kv_evict(
         ctypes.byref(CacheShape(R, 1, 1, PAGE, max_pages, pages)), kv.data_ptr(),
         block_table.data_ptr(), seq_lens.data_ptr(), weights.data_ptr(), _ptr(positions),
-        keep.data_ptr(), int(recent), int(sinks), weights_out.data_ptr(), _ptr(positions_out),
+        keep.data_ptr(), recent, sinks, weights_out.data_ptr(), _ptr(positions_out),
         lens_out.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(status),
         _stream_on(dev, stream)))
     return lens_out

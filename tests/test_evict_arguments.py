@@ -47,3 +47,13 @@ def test_lens_out(evict):
             evict(keep=flat[a:a + 2], lens_out=flat[b:b + 2])
     with pytest.raises(ValueError, match="lens_out"):
         evict(keep=flat[:2], lens_out=flat[:2])
+
+
+@pytest.mark.parametrize("value", [2 ** 31, 2 ** 32, 2 ** 32 + 5, -2 ** 31 - 1, -2 ** 32 + 5, 2 ** 63])
+def test_counts_beyond_32_bits(evict, value):
+    """They would reach the library as other numbers: 2^32 + 5 as 5."""
+    for name in ("recent", "sinks"):
+        with pytest.raises(ValueError, match=name):
+            evict(**{name: value})
+        with pytest.raises(Launched):
+            evict(**{name: 2 ** 31 - 1})
