@@ -655,7 +655,8 @@ typedef struct {
  *              leave the rows: that request is skipped), MLA_FAULT_WAIT_TIMEOUT.
  * What lies between and behind the requests' rows and keys reaches no result, whatever its
  * bits. Within a request a NaN or infinity reaches the rows that see it and no others; one in v
- * its own dim alone (as NaN, or as the infinity).
+ * its own dim alone (as NaN, or as the infinity). A token whose every score is -infinity
+ * gets out = NaN, lse = -inf.
  * BF16 products, FP32 scores, sums and accumulation; the weights are rounded to BF16 for
  * their product with v. */
 int32_t mla_prompt_workspace_bytes(const mla_prompt_shape *shape, size_t *bytes);

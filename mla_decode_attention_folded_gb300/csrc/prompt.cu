@@ -40,6 +40,7 @@
 // weights made while the vote on the maximum runs (935 -> 1016); masks per 32 columns (spills, 916
 // -> 1173); registers moved from the four first warps to the softmax (24 prompts 128 -> 136 us, again
 // 122 -> 135 at the end); votes by the two warps that share rows instead of a half's eight (equal).
+#include <cfloat>
 #include <cmath>
 #include <type_traits>
 
@@ -74,6 +75,7 @@ constexpr unsigned long long kWaitLimitNs = 2000000000ull;   // 2 s
 constexpr uint32_t kIdescS = tc::idesc_bf16_f32(kHalf, kKeys);   // M = 256 over the pair
 constexpr uint32_t kIdescO = tc::idesc_bf16_f32(kHalf, kV) | (1u << 16);   // V is MN-major
 constexpr float kLazy = 8.f;
+constexpr float kLowest = -FLT_MAX;               // a piece's LSE: keys seen, all scores -infinity
 
 // A run of tiles of one item.
 struct Piece {
@@ -1020,8 +1022,14 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
       half_any(h, false);
       if (side) l = ctl->row[h][row];
       tc::fence_after_sync();
+      float lse = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
+      // A row that sees keys and has a sum of 0: all scores are -infinity, the formula 0 / 0. In a piece the
+      // others may still have weight: it keeps its O of zeros, and an LSE that tells.
+      if (l == 0.f && c > 0 && lim > 0) {
+        l = p.slot < 0 ? NAN : 1.f;
+        if (p.slot >= 0) lse = kLowest;
+      }
       const float inv = l > 0.f ? rcp(l) : l;    // NaN stays
-      const float lse = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
       const bool valid = lim != INT_MAX;
       const size_t at = (size_t)p.row0 * a.H + p.head;
       if (p.slot < 0) {
@@ -1112,9 +1120,11 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptArgs a) {
     acc[6] += w * v[1].z;
     acc[7] += w * v[1].w;
   }
-  const float inv = z > 0.f ? 1.f / z : z;       // NaN stays
+  const bool lowest = base == kLowest;           // keys seen, and no score above -infinity
+  const float inv = lowest ? NAN : z > 0.f ? 1.f / z : z;    // NaN stays
   const size_t row = (size_t)(jn.x + row_of) * a.H + jn.z + (twin ? j / kHalf : 0);
-  if (a.lse && threadIdx.x < 16) a.lse[row] = z > 0.f ? base + log2f(z) : z == 0.f ? -INFINITY : z;
+  if (a.lse && threadIdx.x < 16)
+    a.lse[row] = z > 0.f && !lowest ? base + log2f(z) : z >= 0.f ? -INFINITY : z;
   uint2* dst = reinterpret_cast<uint2*>(a.out + row * kV) + quad;
   dst[0] = make_uint2(f32x2_to_bf16x2(acc[0] * inv, acc[1] * inv), f32x2_to_bf16x2(acc[2] * inv, acc[3] * inv));
   dst[16] = make_uint2(f32x2_to_bf16x2(acc[4] * inv, acc[5] * inv), f32x2_to_bf16x2(acc[6] * inv, acc[7] * inv));

@@ -41,3 +41,42 @@ def test_a_piece_of_no_weight_keeps_its_nan(n, m, H, Hkv, causal, bad):
     else:
         assert torch.isnan(out[hit]).all()
     assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse, want_l)
+
+
+@pytest.mark.parametrize("n,m,H,Hkv", [(5, 100, 2, 2), (300, 900, 1, 1), (64, 5000, 2, 2), (200, 6000, 3, 1),
+                                       (1000, 1000, 1, 1)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_rows_whose_scores_are_all_minus_infinity(n, m, H, Hkv, causal):
+    """0 / 0: NaN, not the zeros of a row without keys. Some rows by their query, and by the first keys all
+    rows that see no others; the rest are as if those keys were not there."""
+    g = torch.Generator(device="cuda").manual_seed(m)
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    q, kn, kr, v = rand(n, H, 192), rand(m, Hkv, 128), rand(m, 64), rand(m, Hkv, 128)
+    low = m // 4
+    q[:, :, 0], q[:, :, 1], kn[:, :, 0], kn[:, :, 1] = 1, 1, 0, 1
+    kn[:low, :, 0] = -math.inf
+    mine = torch.arange(1, n, 7, device="cuda")
+    q[mine, H - 1, 1] = -math.inf
+    status = _i32(0)
+    out, lse = mla.prompt_attention(q, kn, kr, v, _i32(0, n), SCALE, _i32(0, m), causal, status=status)
+    alone = torch.zeros(n, H, dtype=torch.bool, device="cuda")
+    alone[mine, H - 1] = True
+    if causal:
+        alone[:max(0, low - (m - n))] = True
+    assert torch.isnan(out[alone]).all() and (lse[alone] == -math.inf).all()
+    q[mine, H - 1, 1] = 1
+    ref = reference(q, kn[low:], kr[low:], v[low:], [0, n], [0, m - low], SCALE, causal)
+    check(out[~alone], lse[~alone], [x[~alone] for x in ref])
+    assert int(status.item()) == 0
+
+
+def test_minus_infinity_beside_nan_scores():
+    """Pieces of a cut item that have NaN, and others with -infinity alone."""
+    n, m = 40, 6000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    q, kn, kr, v = rand(n, 1, 192), rand(m, 1, 128), rand(m, 64), rand(m, 1, 128)
+    q[:, :, 0], kn[:, :, 0] = 1, -math.inf
+    kn[m // 2, 0, 5] = math.nan
+    out, lse = mla.prompt_attention(q, kn, kr, v, _i32(0, n), SCALE, _i32(0, m))
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
