@@ -15,9 +15,10 @@
 // lists the moves and makes them, 9 threads a row; where the clusters of a batch leave enough SMs
 // idle, a second launch makes them on all.
 //
-// Measured (graph replays): 128 requests drop 7 of 2,055 keys in 10.5 us, nearly all of it the
-// select's chain of dependent steps; 8 x 20k to 32k keys to 4k in 23.8 us (1.5 TB/s of what has to
-// move), 128k keys to 64k in 29.5 us (1.35 TB/s): the walks over the keys and the scattered rows.
+// Measured (graph replays; in brackets with L2 flushed before each call): 128 requests drop 7 of 2,055
+// keys in 10.3 us (13.4), nearly all of it the select's chain of dependent steps; 8 x 20k to 32k keys to 4k
+// in 23.8 us (28.8), 1.5 TB/s of what has to move; 128k keys to 64k in 29.8 us (35.0), 1.35 TB/s: the walks
+// over the keys and the scattered rows.
 #include <climits>
 
 #include "checks.h"
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictAr
       if (a.cluster > 1) {
         __syncthreads();
         // Added in 32 bits, as the first CTA adds its own codes meanwhile: additions of two widths to the
-        // same words are not atomic to one another.
+        // same words are not atomic to one another. (In 64, to a second histogram, the times are the same.)
         if (rank > 0) {
 #pragma unroll
           for (int u = 0; u < 2; ++u)

@@ -32,10 +32,11 @@
 // How the work is shared out is in prompt.h. The order of a half's MMAs is PV(t) before S(t + 1),
 // so that S may overwrite P and its completion tells that O is final.
 //
-// Measured (graph replays): 64 heads of 8,192 tokens 905 us, 1,520 TFLOP/s (the pipe's peak in a
-// burst is 1,874, and 1,690 under the power cap); 4 x 32 heads of 900 to 1,500 tokens, grouped,
-// without a mask 112 us, 1,090 TFLOP/s; 24 prompts of up to 2,048 tokens and 8 heads 122 us, 720;
-// 512 tokens on 16k keys, 8 heads 42.2 us, 1,000; two short prompts 8.5 us.
+// Measured (graph replays; in brackets with L2 flushed before each call): 64 heads of 8,192 tokens 867 to
+// 926 us (885), 1,485 to 1,585 TFLOP/s (the pipe's peak in a burst is 1,874, and 1,690 under the power
+// cap); 4 x 32 heads of 900 to 1,500 tokens, grouped, without a mask 112 us (116), 1,088 TFLOP/s; 24
+// prompts of up to 2,048 tokens and 8 heads 122 us (125), 720; 512 tokens on 16k keys, 8 heads 42.6 to
+// 43.6 us (46.7), 990; two short prompts 8.5 us (10.6).
 // Dropped: V given back after S (1130 -> 1258 us); the MMAs' lock before the wait for P (912 -> 963);
 // weights made while the vote on the maximum runs (935 -> 1016); masks per 32 columns (spills, 916
 // -> 1173); registers moved from the four first warps to the softmax (24 prompts 128 -> 136 us, again
@@ -373,9 +374,6 @@ __device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-
-// 1 / x to 2^-23, beside the 2^-8 of the BF16 that it scales: the exact division is a call, for which
-// the softmax threads would have to spare registers.
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -386,6 +384,8 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
                : "memory");
 }
+// 1 / x to 2^-23, beside the 2^-8 of the BF16 that it scales: the exact division is a call, for which
+// the softmax threads would have to spare registers.
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -15,9 +15,9 @@
 // half of them in each CTA's shared memory. All tiles of the batch are one line, cut into equal
 // runs, one per CTA or pair: keys need no joining, so a cut costs nothing.
 //
-// Measured (graph replays): 64 requests of up to 8k keys, 56 rows, 30.7 us, 5.2 TB/s; 16 of 16k to
-// 64k, 256 rows, 74 us, 5.2 TB/s and 2,610 TFLOP/s; 128 of up to 4k, 448 rows, 67 us, 2,270
-// TFLOP/s of FP8; two short ones 5.5 us. What is left at many rows is the pipe's wait for keys and
+// Measured (graph replays; in brackets with L2 flushed before each call): 64 requests of up to 8k keys, 56
+// rows, 30.8 us (39.7), 5.2 TB/s; 16 of 16k to 64k, 256 rows, 73 us (82), 5.2 TB/s and 2,610 TFLOP/s; 128 of
+// up to 4k, 448 rows, 67 us (75), 2,270 TFLOP/s of FP8; two short ones 5.3 us (6.6). What is left at many rows is the pipe's wait for keys and
 // queries at the change of a block: shared memory has room for two tiles beside the queries.
 // Dropped: tiles in bands of 128 dims, refilled as they are multiplied (69.6 -> 76.7 us), the queries
 // in bands (68.7 -> 67.7, but two short requests 5.7 -> 5.9).
