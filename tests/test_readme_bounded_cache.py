@@ -1,4 +1,4 @@
-"""README's recipe of a bounded cache, run as it stands with the calls' contracts in place of the
+"""The documented recipe of a bounded cache, run as it stands with the calls' contracts in place of the
 kernels: after a prompt, the first and the newest tokens and the keys of most weight stay."""
 import os
 import re
